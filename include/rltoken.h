@@ -1,0 +1,105 @@
+/*
+ * rltoken.h — C ABI of the token log-probability and distillation operators
+ * that stand beside the fused policy loss (rlloss.h; GB300, sm_103a).
+ *
+ * The policy loss consumes log-probabilities of sampled tokens (the rollout
+ * buffer of the RL.cu article, ainews.cool, section "技术深度解析", bullet
+ * "滚动缓冲区", holds them) and returns one fixed objective's gradient.  The
+ * calls below give the pieces around it for logits that are in memory: the
+ * log-probabilities of any given tokens with the entropy and the top
+ * alternatives of each row, their gradient, and the loss and gradient of
+ * distillation from a teacher's top log-probabilities.  The source pages have
+ * no formula for them; each declaration states the definition it computes.
+ *
+ * Conventions are rlloss.h's: every array is DEVICE memory owned by the
+ * caller on the current device, nothing is allocated, calls are stream-ordered
+ * and capturable, argument errors are found on the host before anything is
+ * launched, device-detected errors set RL_DEVERR_* bits, make the affected
+ * outputs NaN and never trap.
+ *
+ * Common arguments:
+ *   logits      : [R, ld] of `dtype` (RL_F32, RL_BF16, RL_F16), row-major,
+ *                 16-byte aligned, ld * sizeof(dtype) a multiple of 16,
+ *                 ld >= V; the columns V .. ld-1 are ignored.
+ *   mask        : uint8[R], nonzero = valid row; NULL = every row is valid.
+ *                 The logits, ids and teacher of a masked row are not read.
+ *   temperature : z = logits / temperature enters every formula;
+ *                 0.01 <= temperature <= 100.
+ *   status_dev  : one unsigned int or NULL; RL_DEVERR_* bits are ORed into it.
+ * A logit of -inf is a token that cannot occur (probability 0, log-probability
+ * -inf, nothing in the entropy).  A valid row whose logits are all -inf has no
+ * distribution: its log-probabilities and entropy are NaN.  NaN or +inf in a
+ * valid row makes that row's results NaN.
+ */
+#ifndef RLTOKEN_H
+#define RLTOKEN_H
+
+#include "rlloss.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Most alternatives, given ids or teacher entries a row may have. */
+#define RL_TOKEN_MAX_K 128
+
+/* (device) the same teacher id twice in one row (rl_topk_distill_fwd_bwd). */
+#define RL_DEVERR_ID_REPEAT 4u
+
+/*
+ * Log-probabilities of given tokens, with entropy and top alternatives.
+ * For each valid row r, with z = logits[r] / temperature:
+ *   lse_out[r]        = log sum_v exp z_v
+ *   logp_out[r, j]    = z[ids[r, j]] - lse_out[r]            j < n_ids
+ *   entropy_out[r]    = -sum_v p_v log p_v,  p = softmax(z)
+ *   topk_ids[r, i]    = the i-th most likely token, ties to the lower id (a
+ *                       NaN logit comes before every number)   i < k
+ *   topk_logp[r, i]   = its log-probability
+ * Masked rows get logp, entropy, lse and topk_logp 0 and topk_ids -1.
+ *   ids      : int64 [R, n_ids] contiguous; an id outside [0, V) makes its
+ *              logp NaN and sets RL_DEVERR_ID_RANGE.  NULL iff n_ids = 0.
+ *   logp_out : float [R, n_ids]; NULL iff n_ids = 0.
+ *   entropy_out, lse_out : float [R], each may be NULL.
+ *   topk_ids, topk_logp  : int64 and float [R, k], both NULL iff k = 0.
+ *   0 <= n_ids, k <= RL_TOKEN_MAX_K, k <= V, 1 <= V <= 2^30; with k > 0 a row
+ *   may have at most 512 KB (2^18 16-bit or 2^17 fp32 logits).
+ * fp32 arithmetic on the exact differences to the row's maximum; the maximum
+ * itself stays out of the running sum, so that a log-probability next to 0
+ * keeps its relative precision.  Deterministic.  One launch.
+ * Errors: RL_ERR_DTYPE, RL_ERR_SHAPE (R < 0, R >= 2^31, V or ld out of range,
+ * k > V, a row too long for k > 0), RL_ERR_ARG (n_ids or k out of range,
+ * temperature), RL_ERR_NULL, RL_ERR_ALIGN, RL_ERR_CUDA.  R = 0 launches
+ * nothing.
+ */
+rl_status rl_token_logprobs(const void* logits, rl_dtype dtype, long long R, long long V, long long ld,
+                            const long long* ids, int n_ids, const unsigned char* mask, float temperature,
+                            int k, float* logp_out, float* entropy_out, float* lse_out,
+                            long long* topk_ids, float* topk_logp, unsigned int* status_dev, void* stream);
+
+/*
+ * Gradient of the log-probabilities and the entropy of rl_token_logprobs with
+ * respect to the logits.  For each valid row, with p_v = exp(z_v - lse):
+ *   dlogits_v = (1 / temperature) [ sum_j dlogp_j ([v = ids_j] - p_v)
+ *                                   - dentropy p_v (z_v - lse + entropy) ]
+ * rounded once to `dtype`; masked rows get an all-zero row.
+ *   lse      : float [R], as rl_token_logprobs wrote it.
+ *   dlogp    : float [R, n_ids]; NULL iff n_ids = 0.  An id that a row names
+ *              several times collects the sum of its gradients; an id outside
+ *              [0, V) makes the row NaN and sets RL_DEVERR_ID_RANGE.
+ *   entropy, dentropy : float [R] each, or both NULL (no entropy gradient).
+ *   dlogits  : [R, ld] of `dtype`, written (columns >= V untouched); may be
+ *              the same pointer as logits, any other overlap is RL_ERR_ALIAS.
+ * One launch.  Errors as rl_token_logprobs, and RL_ERR_NULL when neither
+ * dlogp nor dentropy is given.
+ */
+rl_status rl_token_logprobs_bwd(const void* logits, rl_dtype dtype, long long R, long long V, long long ld,
+                                const long long* ids, int n_ids, const unsigned char* mask,
+                                float temperature, const float* lse, const float* entropy,
+                                const float* dlogp, const float* dentropy, void* dlogits,
+                                unsigned int* status_dev, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* RLTOKEN_H */

@@ -536,3 +536,65 @@ def lmhead_policy_loss(hidden, weight, dtype, ids, mask, adv_row, logp_old=None,
     Wm = decode(np.ascontiguousarray(weight), dtype)
     out.update(z=z, dz=dz, dhidden=dz @ Wm, dweight=dz.T @ Hm)
     return out
+
+
+# --------------------------------------------------------------------------- token log-probabilities
+def token_logprobs(logits, dtype, V, ids=None, mask=None, k=0, temperature=1.0):
+    """Log-probabilities of given tokens, entropy, log-sum-exp and the k most
+    likely tokens of each row (ties to the lower id, NaN before every number),
+    from the definition in fp64.  ``logits`` is [R, >= V] storage; ``ids`` is
+    [R, n] or None.  Masked rows: 0, and alternatives of id -1."""
+    x = decode(logits[:, :V], dtype)
+    R = x.shape[0]
+    on = np.ones(R, bool) if mask is None else np.asarray(mask).astype(bool)
+    out = dict(lse=np.zeros(R), entropy=np.zeros(R), topk_ids=np.full((R, k), -1, np.int64),
+               topk_logp=np.zeros((R, k)), logp=None if ids is None else np.zeros(np.shape(ids)))
+    for r in np.nonzero(on)[0]:
+        z = x[r] / temperature
+        with np.errstate(invalid="ignore", over="ignore", divide="ignore"):
+            m = z.max()
+            e = np.exp(z - m) if np.isfinite(m) else np.full(V, np.nan)
+            first = int(np.argmax(z)) if np.isfinite(m) else 0
+            rest = e.sum() - e[first] if e[first] != 1.0 else np.delete(e, first).sum()
+            log_s = math.log1p(rest) if rest >= 0 else math.nan
+            lp = (z - m) - log_s
+            out["lse"][r] = -math.inf if m == -math.inf else m + log_s
+            out["entropy"][r] = -np.where(e > 0, e * lp, 0.0).sum() / (1.0 + rest) if rest >= 0 else math.nan
+        if ids is not None:
+            ok = (ids[r] >= 0) & (ids[r] < V)
+            out["logp"][r] = np.where(ok, lp[np.where(ok, ids[r], 0)], math.nan)
+        if k:
+            key = np.where(np.isnan(x[r]), math.inf, x[r] + 0.0)
+            order = np.lexsort((np.arange(V), -key, ~np.isnan(x[r])))[:k]
+            out["topk_ids"][r] = order
+            out["topk_logp"][r] = lp[order]
+    return out
+
+
+def token_logprobs_bwd(logits, dtype, V, ids, dlogp, lse, entropy=None, dentropy=None, mask=None, temperature=1.0):
+    """Gradient of the above in fp64 (not rounded): [R, V].  ``lse`` and
+    ``entropy`` are the forward pass's, taken as they are.  Also returns, per
+    element, the size of what it is the sum of (for rounding bounds)."""
+    x = decode(logits[:, :V], dtype)
+    R = x.shape[0]
+    lp = x / temperature - np.asarray(lse, np.float64)[:, None]
+    p = np.exp(lp)
+    g = np.zeros(R) if dlogp is None else np.asarray(dlogp, np.float64).sum(1)
+    with np.errstate(invalid="ignore"):
+        d = -p * g[:, None]
+        size = p * (0.0 if dlogp is None else np.abs(dlogp).astype(np.float64).sum(1))[:, None] \
+            if dlogp is not None else np.zeros_like(p)
+        if dentropy is not None:
+            h = np.asarray(dentropy, np.float64)[:, None]
+            H = np.asarray(entropy, np.float64)[:, None]
+            d -= h * np.where(p > 0, p * (lp + H), 0.0)
+            size = size + np.abs(h) * np.where(p > 0, p * (np.abs(lp) + np.abs(H)), 0.0)
+    if dlogp is not None:
+        for j in range(ids.shape[1]):
+            np.add.at(d, (np.arange(R), ids[:, j]), np.asarray(dlogp, np.float64)[:, j])
+            np.add.at(size, (np.arange(R), ids[:, j]), np.abs(np.asarray(dlogp, np.float64)[:, j]))
+    if mask is not None:
+        off = ~np.asarray(mask).astype(bool)
+        d[off] = 0.0
+        size[off] = 0.0
+    return d / temperature, size / temperature, lp

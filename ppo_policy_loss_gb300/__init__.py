@@ -1,7 +1,7 @@
 """Python binding of librlloss, the GB300-native fused RL policy-loss library.
 
 Argument marshalling only: every function forwards to the C entry point of
-the same name declared in include/rlloss.h, with the same arguments in the
+the same name declared in include/rlloss.h or include/rltoken.h, with the same arguments in the
 same order.  Array arguments may be torch CUDA tensors (their data_ptr() is
 passed), plain integer device addresses, or None for NULL.  ``stream`` may be
 a torch.cuda.Stream, an integer cudaStream_t, or None for torch's current
@@ -25,7 +25,8 @@ RL_AGG_TOKEN_MEAN, RL_AGG_SEQ_MEAN_TOKEN_MEAN, RL_AGG_SEQ_MEAN_TOKEN_SUM, RL_AGG
     0, 1, 2, 3
 AGGREGATIONS = {"token_mean": 0, "seq_mean_token_mean": 1, "seq_mean_token_sum": 2,
                 "token_sum_norm": 3}
-RL_DEVERR_ID_RANGE, RL_DEVERR_TIMEOUT = 1, 2
+RL_DEVERR_ID_RANGE, RL_DEVERR_TIMEOUT, RL_DEVERR_ID_REPEAT = 1, 2, 4
+RL_TOKEN_MAX_K = 128
 
 DTYPES = {"f32": RL_F32, "bf16": RL_BF16, "f16": RL_F16}
 
@@ -36,6 +37,7 @@ __all__ = [
     "rl_read_device_status", "rl_masked_whiten", "rl_count_tokens", "rl_value_loss_fwd_bwd",
     "rl_value_stats", "value_stats_from_bytes", "rl_lmhead_logprobs",
     "rl_lmhead_workspace_size", "rl_lmhead_plan", "rl_selftest_wait_timeout",
+    "rl_token_logprobs", "rl_token_logprobs_bwd",
     "rl_status_string", "rl_loss_stats", "RlLossError", "build", "load", "stats_from_bytes",
 ]
 
@@ -120,6 +122,10 @@ def load(path: str | None = None):
     lib.rl_lmhead_dlogits.argtypes = [P, LL, P, LL, I, LL, LL, LL, P, P, P, LL, P, P]
     lib.rl_lmhead_dhidden.argtypes = [P, LL, P, LL, I, LL, LL, LL, P, LL, P, P]
     lib.rl_lmhead_dweight.argtypes = [P, LL, P, LL, I, LL, LL, LL, P, LL, I, P, P]
+    lib.rl_token_logprobs.argtypes = [P, I, LL, LL, LL, P, I, P, F, I, P, P, P, P, P, P, P]
+    lib.rl_token_logprobs_bwd.argtypes = [P, I, LL, LL, LL, P, I, P, F, P, P, P, P, P, P, P]
+    for fn in ("rl_token_logprobs", "rl_token_logprobs_bwd"):
+        getattr(lib, fn).restype = I
     for fn in ("rl_lmhead_row_partials", "rl_lmhead_dlogits", "rl_lmhead_dhidden",
                "rl_lmhead_dweight"):
         getattr(lib, fn).restype = I
@@ -297,6 +303,22 @@ def rl_lmhead_plan(R, D, V, workspace_bytes, sm_count=0):
                                  ctypes.byref(grid), ctypes.byref(grp), ctypes.byref(need)),
            "rl_lmhead_plan")
     return ns.value, grid.value, grp.value, need.value
+
+
+def rl_token_logprobs(logits, dtype, R, V, ld, ids, n_ids, mask, temperature, k, logp_out, entropy_out,
+                      lse_out, topk_ids, topk_logp, status_dev=None, stream=None):
+    _check(load().rl_token_logprobs(_ptr(logits), _dtype(dtype), R, V, ld, _ptr(ids), n_ids, _ptr(mask),
+                                    temperature, k, _ptr(logp_out), _ptr(entropy_out), _ptr(lse_out),
+                                    _ptr(topk_ids), _ptr(topk_logp), _ptr(status_dev), _stream(stream)),
+           "rl_token_logprobs")
+
+
+def rl_token_logprobs_bwd(logits, dtype, R, V, ld, ids, n_ids, mask, temperature, lse, entropy, dlogp,
+                          dentropy, dlogits, status_dev=None, stream=None):
+    _check(load().rl_token_logprobs_bwd(_ptr(logits), _dtype(dtype), R, V, ld, _ptr(ids), n_ids,
+                                        _ptr(mask), temperature, _ptr(lse), _ptr(entropy), _ptr(dlogp),
+                                        _ptr(dentropy), _ptr(dlogits), _ptr(status_dev), _stream(stream)),
+           "rl_token_logprobs_bwd")
 
 
 def rl_policy_loss_launch_shape(dtype, V, n_rows):

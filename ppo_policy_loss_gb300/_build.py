@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "librlloss.so")
-SOURCES = ["policy_loss.cu", "advantages.cu", "critic.cu", "status.cu", "lmhead.cu", "lmhead_grad.cu"]
+SOURCES = ["policy_loss.cu", "advantages.cu", "critic.cu", "status.cu", "lmhead.cu", "lmhead_grad.cu",
+           "token_logprobs.cu"]
 # (object, source, extra flags): policy_loss.cu builds a second time with the
 # short-row configuration of the loss kernel.
 UNITS = [(src.replace(".cu", ".o"), src, []) for src in SOURCES] + [
@@ -39,7 +40,7 @@ def _nvcc() -> str:
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "rlloss.h"))
+    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     files.append(os.path.abspath(__file__))
     return files
 

@@ -1,0 +1,327 @@
+// token_rows.cuh — building blocks of the token log-probability and
+// distillation kernels (sm_103a): the 64-byte piece of a logits row that one
+// thread takes at a time, its element formats, and the online softmax
+// statistics whose sum leaves the maximum out.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "rl_device.cuh"
+#include "rltoken.h"
+
+namespace rl {
+namespace {
+
+// A piece: 64 consecutive bytes of a row, four 16-byte vectors.  Lanes of a
+// warp take consecutive pieces, so that a piece's maximum is one key of the
+// top-k search; from shared memory lane l takes its vectors in the order
+// (j + l / 2) mod 4, which touches every bank once per 8 lanes.
+constexpr int kPieceBytes = 64;
+constexpr int kRowThreads = 256;  // threads that work on a row
+
+// Every logit counts as at least the format's floor when it enters a sum, so
+// that -inf gives 2^x = 0 and 0 * x = 0 instead of NaN.  That is exact while
+// the row's maximum is far above the floor; a row whose maximum is at most
+// kExact (all -inf, or masked with the type's lowest value) is taken again
+// without the floor (exact_row).  With temperature <= 100 the floor's term
+// of any other row is 2^-x, x >= (65504 - 32768) log2(e) / 100 > 470: 0.
+constexpr float kRowFloor = -0x1p100f;
+constexpr float kMinTemperature = 0.01f, kMaxTemperature = 100.f;
+
+__device__ __forceinline__ uint32_t pmax_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pmax_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Order keys: unsigned integers that compare as the values do, with -0 = +0,
+// every NaN above +inf, and 0 below every value (an empty place).
+__device__ __forceinline__ uint32_t order16(uint32_t b, uint32_t inf) {
+  if ((b & 0x7fffu) > inf) return 0xffffu;
+  if (b == 0x8000u) b = 0u;
+  return (b & 0x8000u) ? (b ^ 0xffffu) : (b | 0x8000u);
+}
+__device__ __forceinline__ uint32_t unorder16(uint32_t k) { return (k & 0x8000u) ? (k & 0x7fffu) : (k ^ 0xffffu); }
+__device__ __forceinline__ uint32_t order32(uint32_t b) {
+  if ((b & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
+  if (b == 0x80000000u) b = 0u;
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float unorder32(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// Per format: elements per piece, the piece's raw maximum as a key and as a
+// float, clamping at the floor, widening, and single elements.
+template <int DT>
+struct Fmt;
+
+template <>
+struct Fmt<RL_F32> {
+  using Key = uint32_t;
+  static constexpr int kBytes = 4, kPiece = 16, kVec = 4;
+  static constexpr float kFloor = kRowFloor, kExact = -0x1p99f;
+  static constexpr uint32_t kNegInf2 = 0xff800000u;
+  __device__ static uint32_t raw_max(const uint32_t (&w)[16]) {
+    float m = __uint_as_float(w[0]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) m = max_nan(m, __uint_as_float(w[i]));
+    return __float_as_uint(m);
+  }
+  __device__ static float raw_value(uint32_t r) { return __uint_as_float(r); }
+  __device__ static Key raw_key(uint32_t r) { return order32(r); }
+  __device__ static uint32_t clamp(uint32_t w) { return __float_as_uint(max_nan(__uint_as_float(w), kFloor)); }
+  // elements e .. 15 of the piece become -inf
+  __device__ static void cut(uint32_t (&w)[16], int e) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i >= e) w[i] = kNegInf2;
+  }
+  __device__ static void pair(const uint32_t (&w)[16], int i, float& a, float& b) {
+    a = __uint_as_float(w[2 * i]);
+    b = __uint_as_float(w[2 * i + 1]);
+  }
+  __device__ static float load(const unsigned char* row, long long i) { return reinterpret_cast<const float*>(row)[i]; }
+  __device__ static Key load_key(const unsigned char* row, long long i) {
+    return order32(reinterpret_cast<const uint32_t*>(row)[i]);
+  }
+  __device__ static float key_value(Key k) { return unorder32(k); }
+  __device__ static void store(unsigned char* row, long long i, float v) { reinterpret_cast<float*>(row)[i] = v; }
+  __device__ static void unpack(const uint4& w, float (&z)[kVec]) {
+    z[0] = __uint_as_float(w.x);
+    z[1] = __uint_as_float(w.y);
+    z[2] = __uint_as_float(w.z);
+    z[3] = __uint_as_float(w.w);
+  }
+  __device__ static uint4 pack(const float (&z)[kVec]) {
+    return make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]), __float_as_uint(z[3]));
+  }
+};
+
+template <>
+struct Fmt<RL_BF16> {
+  using Key = uint16_t;
+  static constexpr int kBytes = 2, kPiece = 32, kVec = 8;
+  static constexpr float kFloor = kRowFloor, kExact = -0x1p99f;
+  static constexpr uint32_t kFloor2 = 0xF180F180u, kNegInf2 = 0xFF80FF80u;
+  __device__ static uint32_t raw_max(const uint32_t (&w)[16]) {
+    uint32_t m = w[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) m = pmax_bf16x2(m, w[i]);
+    return pmax_bf16x2(m, (m >> 16) | (m << 16)) & 0xffffu;
+  }
+  __device__ static float raw_value(uint32_t r) { return __uint_as_float(r << 16); }
+  __device__ static Key raw_key(uint32_t r) { return static_cast<Key>(order16(r, 0x7f80u)); }
+  __device__ static uint32_t clamp(uint32_t w) { return pmax_bf16x2(w, kFloor2); }
+  __device__ static void cut(uint32_t (&w)[16], int e) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (2 * i >= e)
+        w[i] = kNegInf2;
+      else if (2 * i + 1 >= e)
+        w[i] = (w[i] & 0xffffu) | (kNegInf2 & 0xffff0000u);
+    }
+  }
+  __device__ static void pair(const uint32_t (&w)[16], int i, float& a, float& b) {
+    a = __uint_as_float(w[i] << 16);
+    b = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  __device__ static float load(const unsigned char* row, long long i) {
+    return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[i]) << 16);
+  }
+  __device__ static Key load_key(const unsigned char* row, long long i) {
+    return static_cast<Key>(order16(reinterpret_cast<const uint16_t*>(row)[i], 0x7f80u));
+  }
+  __device__ static float key_value(Key k) { return __uint_as_float(unorder16(k) << 16); }
+  __device__ static void store(unsigned char* row, long long i, float v) {
+    reinterpret_cast<__nv_bfloat16*>(row)[i] = __float2bfloat16_rn(v);
+  }
+  __device__ static void unpack(const uint4& w, float (&z)[kVec]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      z[2 * k] = __uint_as_float(u[k] << 16);
+      z[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+    }
+  }
+  __device__ static uint4 pack(const float (&z)[kVec]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      __nv_bfloat162 h = __floats2bfloat162_rn(z[2 * k], z[2 * k + 1]);
+      u[k] = *reinterpret_cast<uint32_t*>(&h);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+
+template <>
+struct Fmt<RL_F16> {
+  using Key = uint16_t;
+  static constexpr int kBytes = 2, kPiece = 32, kVec = 8;
+  static constexpr float kFloor = -65504.f, kExact = -32768.f;
+  static constexpr uint32_t kFloor2 = 0xFBFFFBFFu, kNegInf2 = 0xFC00FC00u;
+  __device__ static uint32_t raw_max(const uint32_t (&w)[16]) {
+    uint32_t m = w[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) m = pmax_f16x2(m, w[i]);
+    return pmax_f16x2(m, (m >> 16) | (m << 16)) & 0xffffu;
+  }
+  __device__ static float half_bits(uint32_t r) { return __half2float(__ushort_as_half(static_cast<unsigned short>(r))); }
+  __device__ static float raw_value(uint32_t r) { return half_bits(r); }
+  __device__ static Key raw_key(uint32_t r) { return static_cast<Key>(order16(r, 0x7c00u)); }
+  __device__ static uint32_t clamp(uint32_t w) { return pmax_f16x2(w, kFloor2); }
+  __device__ static void cut(uint32_t (&w)[16], int e) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (2 * i >= e)
+        w[i] = kNegInf2;
+      else if (2 * i + 1 >= e)
+        w[i] = (w[i] & 0xffffu) | (kNegInf2 & 0xffff0000u);
+    }
+  }
+  __device__ static void pair(const uint32_t (&w)[16], int i, float& a, float& b) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    a = f.x;
+    b = f.y;
+  }
+  __device__ static float load(const unsigned char* row, long long i) {
+    return half_bits(reinterpret_cast<const uint16_t*>(row)[i]);
+  }
+  __device__ static Key load_key(const unsigned char* row, long long i) {
+    return static_cast<Key>(order16(reinterpret_cast<const uint16_t*>(row)[i], 0x7c00u));
+  }
+  __device__ static float key_value(Key k) { return half_bits(unorder16(k)); }
+  __device__ static void store(unsigned char* row, long long i, float v) {
+    reinterpret_cast<__half*>(row)[i] = __float2half_rn(v);
+  }
+  __device__ static void unpack(const uint4& w, float (&z)[kVec]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
+      z[2 * k] = f.x;
+      z[2 * k + 1] = f.y;
+    }
+  }
+  __device__ static uint4 pack(const float (&z)[kVec]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      __half2 h = __floats2half2_rn(z[2 * k], z[2 * k + 1]);
+      u[k] = *reinterpret_cast<uint32_t*>(&h);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+
+// ------------------------------------------------------------------ statistics
+// Over a set of logits with maximum m: r = sum 2^x - 1 and t = sum 2^x x,
+// x = (z - m) c with c = log2(e) / temperature.  Then
+//   lse = m / temperature + log1p(r),   H = log1p(r) - ln 2 t / (1 + r).
+// One of the maxima (its term is exactly 1) is left out of the sum, so r is a
+// sum of small terms where one token holds nearly all the mass and log1p(r)
+// keeps its relative precision.  An empty set is m = floor, r = -1, t = 0.
+struct RowStats {
+  float m, r, t;
+};
+
+__device__ __forceinline__ RowStats merge_row(RowStats a, RowStats b, float c) {
+  if (b.m > a.m) {
+    const RowStats x = a;
+    a = b;
+    b = x;
+  }
+  const float s = 1.f + b.r;
+  if (s == 0.f) return a;  // empty (a NaN goes on and poisons)
+  const float d = (a.m - b.m) * c;
+  const float f = ex2_approx(-d);
+  a.r = fmaf(f, s, a.r);
+  a.t = fmaf(f, fmaf(-d, s, b.t), a.t);
+  return a;
+}
+
+// A warp's running statistics: m is the warp's, r and t are spread over its
+// lanes (their sums are the warp's r and t).
+struct WarpStats {
+  float m;
+  float2 r, t;
+};
+
+__device__ __forceinline__ void warp_stats_init(WarpStats& a, float floor, int lane) {
+  a.m = floor;
+  a.r = make_float2(lane == 0 ? -1.f : 0.f, 0.f);
+  a.t = make_float2(0.f, 0.f);
+}
+
+// This lane's piece, raw and clamped as warp-wide call: `pm` is the clamped
+// maximum of the lane's piece.  A piece of nothing (all -inf) adds 0.
+template <class F, bool kEntropy>
+__device__ __forceinline__ void add_piece(WarpStats& a, uint32_t (&w)[16], float pm, float c, int lane) {
+  float wm;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(wm) : "f"(pm));
+  const float2 c2 = make_float2(c, c);
+  if (wm > a.m) {  // the warp's maximum rises: rescale, and leave one new maximum out
+    const float d = (wm - a.m) * c;
+    const float f = ex2_approx(-d);
+    const float one = lane == 0 ? 1.f : 0.f;
+    const float s = a.r.x + a.r.y + one;  // lane 0 takes the old maximum back in
+    if (kEntropy) a.t = make_float2(f * fmaf(-d, s, a.t.x + a.t.y), 0.f);
+    a.r = make_float2(f * s, 0.f);
+    a.m = wm;
+    const uint32_t holders = __ballot_sync(0xffffffffu, pm == wm);
+    bool out = lane == __ffs(holders) - 1;
+    const float2 nm = make_float2(-wm, -wm);
+#pragma unroll
+    for (int i = 0; i < F::kPiece / 2; ++i) {
+      float2 z;
+      F::pair(w, i, z.x, z.y);
+      const float2 x = __fmul2_rn(__fadd2_rn(z, nm), c2);
+      float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+      if (out && z.x == wm) {
+        e.x = 0.f;
+        out = false;
+      }
+      if (out && z.y == wm) {
+        e.y = 0.f;
+        out = false;
+      }
+      a.r = __fadd2_rn(a.r, e);
+      if (kEntropy) a.t = __ffma2_rn(e, x, a.t);
+    }
+  } else {
+    const float2 nm = make_float2(-a.m, -a.m);
+#pragma unroll
+    for (int i = 0; i < F::kPiece / 2; ++i) {
+      float2 z;
+      F::pair(w, i, z.x, z.y);
+      const float2 x = __fmul2_rn(__fadd2_rn(z, nm), c2);
+      const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+      a.r = __fadd2_rn(a.r, e);
+      if (kEntropy) a.t = __ffma2_rn(e, x, a.t);
+    }
+  }
+}
+
+__device__ __forceinline__ RowStats warp_stats_sum(const WarpStats& a) {
+  float r = a.r.x + a.r.y, t = a.t.x + a.t.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    r += __shfl_xor_sync(0xffffffffu, r, o);
+    t += __shfl_xor_sync(0xffffffffu, t, o);
+  }
+  return RowStats{a.m, r, t};
+}
+
+}  // namespace
+}  // namespace rl

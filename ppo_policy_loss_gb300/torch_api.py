@@ -256,3 +256,8 @@ def lmhead_logprobs(hidden: torch.Tensor, weight: torch.Tensor, ids: torch.Tenso
                        lse, status, workspace, workspace.numel() if workspace is not None else 0,
                        stream)
     return dict(logp=logp, entropy=ent, lse=lse, workspace=workspace)
+
+
+# The token log-probability operators are part of this layer; they live in a
+# module of their own.
+from .token_ops import TokenLogprobs, token_logprobs, token_logprobs_backward  # noqa: E402,F401
