@@ -98,6 +98,92 @@ rl_status rl_token_logprobs_bwd(const void* logits, rl_dtype dtype, long long R,
                                 const float* dlogp, const float* dentropy, void* dlogits,
                                 unsigned int* status_dev, void* stream);
 
+/* Where the teacher's mass outside its given entries goes. */
+typedef enum {
+  RL_DISTILL_TAIL_BUCKET = 0,   /* one more outcome: any token that is not given */
+  RL_DISTILL_TAIL_RENORM = 1    /* nowhere: the given entries are normalised to 1 */
+} rl_distill_tail;
+
+/* Scalar results of rl_topk_distill_fwd_bwd (device memory, written at the
+ * end): the loss, and means over the N valid rows of the two divergences and
+ * of the tail's probability under the teacher and the student (RENORM: only
+ * the forward divergence; the others are 0). */
+typedef struct {
+  double loss;
+  double forward_kl;
+  double reverse_kl;
+  double teacher_tail;
+  double student_tail;
+  long long n_rows;      /* N */
+  int device_error;      /* RL_DEVERR_* bits seen during this call */
+  int reserved;
+} rl_distill_stats;
+
+/*
+ * Distillation from a teacher's top log-probabilities: the loss and its
+ * gradient with respect to the student's logits, in one launch.  On-policy
+ * distillation puts this objective in the place of, or beside, the policy
+ * loss on the same [R, V] logits; the teacher's side is what rl_token_logprobs
+ * returns (topk_ids, topk_logp).
+ *
+ * For each valid row, the teacher gives K entries (id_j, l_j); an id of -1 is
+ * an empty entry.  p = softmax(logits / temperature).
+ *   BUCKET: q_j = exp(l_j); the tokens that are not given form one outcome
+ *     with q_t = max(1 - sum_j q_j, 2^-24) and p_t = max(sum of their p,
+ *     2^-126) (no such outcome when all V tokens are given).
+ *   RENORM: q = softmax over the row's l_j (they may be logits then); there is
+ *     no further outcome, and reverse must be 0.
+ *   F = sum_b q_b (ln q_b - ln p_b)     G = sum_b p_b (ln p_b - max(ln q_b, ln 2^-126))
+ *   L_r = weight_r [ (1 - reverse) F + reverse G ]
+ *   loss = (1/N) sum_r L_r,  N = norm if norm > 0, else the number of valid rows
+ * and, with Q = sum_b q_b and s = grad_scale weight_r / (N temperature),
+ *   dlogits_v = s [ (1 - reverse) (p_v Q - q_v) + reverse p_v (ln p_v - ln q_v - G) ]   v given
+ *   dlogits_v = s p_v [ (1 - reverse) (Q - q_t/p_t) + reverse (ln p_t - ln q_t - G) ]   v not given
+ * rounded once to `dtype`.  Masked rows get loss 0 and an all-zero gradient;
+ * so does a RENORM row with no entry.  The tail's mass is summed by itself,
+ * never taken as 1 - sum p_j.
+ * An id outside [-1, V) or named twice in a row sets RL_DEVERR_ID_RANGE or
+ * RL_DEVERR_ID_REPEAT and makes the row's loss and gradient NaN.
+ * Deterministic: fixed-order fp64 reductions.
+ */
+typedef struct {
+  const void* logits;
+  rl_dtype dtype;
+  long long R, V, ld;
+  const long long* teacher_ids;   /* int64 [R, K] */
+  const float* teacher_logp;      /* float [R, K] */
+  int K;                          /* 1 .. RL_TOKEN_MAX_K */
+  const unsigned char* mask;      /* nullable: every row is valid */
+  const float* weight;            /* nullable: float [R], 1 */
+  rl_distill_tail tail;           /* default RL_DISTILL_TAIL_BUCKET */
+  float reverse;                  /* default 0; in [0, 1] */
+  float temperature;              /* default 1 */
+  float grad_scale;               /* default 1 */
+  double norm;                    /* default 0 (= the number of valid rows) */
+  void* dlogits;                  /* nullable: forward only; may be logits itself */
+  float* row_loss_out;            /* nullable: float [R], L_r */
+  float* loss_out;                /* nullable: float [1], the loss */
+  rl_distill_stats* stats_dev;
+  void* workspace;                /* rl_topk_distill_workspace_size(); zero-filled once, left ready */
+  size_t workspace_bytes;
+} rl_topk_distill_desc;
+
+/* Fill *desc with the defaults above (all pointers NULL, sizes 0). */
+void rl_topk_distill_desc_init(rl_topk_distill_desc* desc);
+
+/* Bytes of device workspace rl_topk_distill_fwd_bwd needs (zero-filled before
+ * its first use; every call leaves it ready for the next; one call at a time). */
+size_t rl_topk_distill_workspace_size(void);
+
+/*
+ * Errors: RL_ERR_NULL (desc, stats_dev, logits or teacher), RL_ERR_DTYPE
+ * (dtype, tail), RL_ERR_SHAPE, RL_ERR_ARG (K, reverse, temperature,
+ * grad_scale, norm out of range; reverse != 0 with RENORM), RL_ERR_ALIGN,
+ * RL_ERR_ALIAS (dlogits partially overlaps logits), RL_ERR_WORKSPACE,
+ * RL_ERR_CUDA.
+ */
+rl_status rl_topk_distill_fwd_bwd(const rl_topk_distill_desc* desc, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

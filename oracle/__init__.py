@@ -598,3 +598,78 @@ def token_logprobs_bwd(logits, dtype, V, ids, dlogp, lse, entropy=None, dentropy
         d[off] = 0.0
         size[off] = 0.0
     return d / temperature, size / temperature, lp
+
+
+def topk_distill(logits, dtype, V, teacher_ids, teacher_logp, mask=None, weight=None, tail="bucket", reverse=0.0,
+                 temperature=1.0, grad_scale=1.0, norm=0.0):
+    """Distillation from a teacher's top entries in fp64, one row at a time
+    from the definition: the outcomes are the given tokens and (bucket) all
+    others together.  Returns the loss, its means, the rows' losses, the
+    gradient (not rounded), and for rounding bounds the sizes of what losses and
+    gradients are sums of."""
+    x = decode(logits[:, :V], dtype) / temperature
+    R, K = np.shape(teacher_ids)
+    on = np.ones(R, bool) if mask is None else np.asarray(mask).astype(bool)
+    w = np.ones(R) if weight is None else np.asarray(weight, np.float64)
+    N = int(on.sum())
+    div = norm if norm > 0 else N
+    row, d = np.zeros(R), np.zeros((R, V))
+    size_row, size = np.zeros(R), np.zeros((R, V))
+    lps, slope = np.zeros((R, V)), np.zeros(R)
+    means = np.zeros(4)
+    ln_tiny = math.log(2.0 ** -126)
+    for r in np.nonzero(on)[0]:
+        m = x[r].max()
+        # differences to the maximum first: at the type's lowest value m + log(sum) is m
+        log_sum = math.log(np.exp(x[r] - m).sum())
+        lp_all = (x[r] - m) - log_sum
+        p_all = np.exp(lp_all)
+        lps[r] = lp_all
+        use = np.asarray(teacher_ids[r]) >= 0
+        ids, lq = np.asarray(teacher_ids[r])[use], np.asarray(teacher_logp[r], np.float64)[use]
+        rest = np.ones(V, bool)
+        rest[ids] = False
+        if tail == "bucket":
+            q = np.exp(lq)
+        else:
+            if ids.size == 0:
+                continue
+            lq = lq - (lq.max() + math.log(np.exp(lq - lq.max()).sum()))
+            q = np.exp(lq)
+        lp, p = lp_all[ids], p_all[ids]
+        has_tail = tail == "bucket" and rest.any()
+        if has_tail:
+            qt = max(1.0 - q.sum(), 2.0 ** -24)
+            xr = x[r][rest]
+            mr = xr.max()
+            # the tail's own log-sum: no difference of near numbers
+            lpt = max((mr - m) + math.log(np.exp(xr - mr).sum()) - log_sum, ln_tiny) if mr > -math.inf else ln_tiny
+            pt, lqt = math.exp(lpt), math.log(qt)
+        else:
+            qt = pt = lqt = lpt = 0.0
+        Q = q.sum() + qt
+        gap = lp - np.maximum(lq, ln_tiny)
+        with np.errstate(invalid="ignore", divide="ignore"):
+            F = np.where(q > 0, q * (lq - lp), 0.0).sum() + qt * (lqt - lpt)
+            sF = np.where(q > 0, q * (1 + np.abs(lq) + np.abs(lp)), 0.0).sum() + qt * (1 + abs(lqt) + abs(lpt))
+            G = np.where(p > 0, p * gap, 0.0).sum() + pt * (lpt - lqt)
+            sG = np.where(p > 0, p * (1 + np.abs(gap)) * (1 + np.abs(lp)), 0.0).sum() + pt * (1 + abs(lpt) + abs(lqt)) * (1 + abs(lpt))
+        if tail != "bucket":
+            G = sG = 0.0
+        v, u = reverse, 1.0 - reverse
+        # a divergence of weight 0 does not count, infinite or not
+        row[r] = w[r] * ((u * F if u else 0.0) + (v * G if v else 0.0))
+        size_row[r] = abs(w[r]) * ((u * sF if u else 0.0) + v * sG)
+        means += (F, G, qt, pt)
+        s = grad_scale * w[r] / (div * temperature)
+        ct = u * (Q - (qt / pt if has_tail else 0.0)) + v * (lpt - lqt - G)
+        st = u * (Q + (qt / pt if has_tail else 0.0)) + v * (1 + abs(lpt) + abs(lqt) + sG)
+        d[r] = s * p_all * ct
+        slope[r] = abs(s) * st
+        size[r] = slope[r] * p_all
+        with np.errstate(invalid="ignore"):
+            d[r, ids] = s * (u * (p * Q - q) + v * np.where(p > 0, p * (gap - G), 0.0))
+            size[r, ids] = abs(s) * (u * (p * Q + q) + v * np.where(p > 0, p * (1 + np.abs(gap) + sG), 0.0))
+    mean = means / max(N, 1)
+    return dict(loss=row.sum() / div if div > 0 else 0.0, forward_kl=mean[0], reverse_kl=mean[1], teacher_tail=mean[2],
+                student_tail=mean[3], n_rows=N, row_loss=row, dlogits=d, size_row=size_row, size=size, slope=slope, lp=lps)

@@ -27,6 +27,8 @@ AGGREGATIONS = {"token_mean": 0, "seq_mean_token_mean": 1, "seq_mean_token_sum":
                 "token_sum_norm": 3}
 RL_DEVERR_ID_RANGE, RL_DEVERR_TIMEOUT, RL_DEVERR_ID_REPEAT = 1, 2, 4
 RL_TOKEN_MAX_K = 128
+RL_DISTILL_TAIL_BUCKET, RL_DISTILL_TAIL_RENORM = 0, 1
+DISTILL_TAILS = {"bucket": 0, "renormalise": 1}
 
 DTYPES = {"f32": RL_F32, "bf16": RL_BF16, "f16": RL_F16}
 
@@ -37,7 +39,9 @@ __all__ = [
     "rl_read_device_status", "rl_masked_whiten", "rl_count_tokens", "rl_value_loss_fwd_bwd",
     "rl_value_stats", "value_stats_from_bytes", "rl_lmhead_logprobs",
     "rl_lmhead_workspace_size", "rl_lmhead_plan", "rl_selftest_wait_timeout",
-    "rl_token_logprobs", "rl_token_logprobs_bwd",
+    "rl_token_logprobs", "rl_token_logprobs_bwd", "rl_topk_distill_fwd_bwd",
+    "rl_topk_distill_desc", "rl_topk_distill_desc_init", "rl_topk_distill_workspace_size",
+    "rl_distill_stats", "distill_stats_from_bytes",
     "rl_status_string", "rl_loss_stats", "RlLossError", "build", "load", "stats_from_bytes",
 ]
 
@@ -79,7 +83,27 @@ class rl_value_stats(ctypes.Structure):
                 ("n_clipped", ctypes.c_longlong)]
 
 
+class rl_distill_stats(ctypes.Structure):
+    _fields_ = [("loss", ctypes.c_double), ("forward_kl", ctypes.c_double),
+                ("reverse_kl", ctypes.c_double), ("teacher_tail", ctypes.c_double),
+                ("student_tail", ctypes.c_double), ("n_rows", ctypes.c_longlong),
+                ("device_error", ctypes.c_int), ("reserved", ctypes.c_int)]
+
+
+class rl_topk_distill_desc(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("R", ctypes.c_longlong), ("V", ctypes.c_longlong), ("ld", ctypes.c_longlong),
+                ("teacher_ids", ctypes.c_void_p), ("teacher_logp", ctypes.c_void_p),
+                ("K", ctypes.c_int), ("mask", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("tail", ctypes.c_int), ("reverse", ctypes.c_float), ("temperature", ctypes.c_float),
+                ("grad_scale", ctypes.c_float), ("norm", ctypes.c_double), ("dlogits", ctypes.c_void_p),
+                ("row_loss_out", ctypes.c_void_p), ("loss_out", ctypes.c_void_p),
+                ("stats_dev", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 STATS_BYTES = ctypes.sizeof(rl_loss_stats)
+DISTILL_STATS_BYTES = ctypes.sizeof(rl_distill_stats)
 VALUE_STATS_BYTES = ctypes.sizeof(rl_value_stats)
 _lib = None
 
@@ -124,7 +148,12 @@ def load(path: str | None = None):
     lib.rl_lmhead_dweight.argtypes = [P, LL, P, LL, I, LL, LL, LL, P, LL, I, P, P]
     lib.rl_token_logprobs.argtypes = [P, I, LL, LL, LL, P, I, P, F, I, P, P, P, P, P, P, P]
     lib.rl_token_logprobs_bwd.argtypes = [P, I, LL, LL, LL, P, I, P, F, P, P, P, P, P, P, P]
-    for fn in ("rl_token_logprobs", "rl_token_logprobs_bwd"):
+    lib.rl_topk_distill_desc_init.argtypes = [ctypes.POINTER(rl_topk_distill_desc)]
+    lib.rl_topk_distill_desc_init.restype = None
+    lib.rl_topk_distill_workspace_size.argtypes = []
+    lib.rl_topk_distill_workspace_size.restype = SZ
+    lib.rl_topk_distill_fwd_bwd.argtypes = [ctypes.POINTER(rl_topk_distill_desc), P]
+    for fn in ("rl_token_logprobs", "rl_token_logprobs_bwd", "rl_topk_distill_fwd_bwd"):
         getattr(lib, fn).restype = I
     for fn in ("rl_lmhead_row_partials", "rl_lmhead_dlogits", "rl_lmhead_dhidden",
                "rl_lmhead_dweight"):
@@ -319,6 +348,27 @@ def rl_token_logprobs_bwd(logits, dtype, R, V, ld, ids, n_ids, mask, temperature
                                         _ptr(mask), temperature, _ptr(lse), _ptr(entropy), _ptr(dlogp),
                                         _ptr(dentropy), _ptr(dlogits), _ptr(status_dev), _stream(stream)),
            "rl_token_logprobs_bwd")
+
+
+def rl_topk_distill_desc_init() -> rl_topk_distill_desc:
+    """A descriptor holding the library's defaults (see rl_topk_distill_desc_init)."""
+    d = rl_topk_distill_desc()
+    load().rl_topk_distill_desc_init(ctypes.byref(d))
+    return d
+
+
+def rl_topk_distill_workspace_size() -> int:
+    return int(load().rl_topk_distill_workspace_size())
+
+
+def rl_topk_distill_fwd_bwd(desc: rl_topk_distill_desc, stream=None):
+    _check(load().rl_topk_distill_fwd_bwd(ctypes.byref(desc), _stream(stream)), "rl_topk_distill_fwd_bwd")
+
+
+def distill_stats_from_bytes(raw: bytes) -> dict:
+    """Decode a host copy of one rl_distill_stats record."""
+    st = rl_distill_stats.from_buffer_copy(bytes(raw))
+    return {name: getattr(st, name) for name, _ in rl_distill_stats._fields_}
 
 
 def rl_policy_loss_launch_shape(dtype, V, n_rows):

@@ -87,6 +87,12 @@ struct Fmt<RL_F32> {
     for (int i = 0; i < 16; ++i)
       if (i >= e) w[i] = kNegInf2;
   }
+  // element e becomes -inf
+  __device__ static void drop(uint32_t (&w)[16], int e) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i == e) w[i] = kNegInf2;
+  }
   __device__ static void pair(const uint32_t (&w)[16], int i, float& a, float& b) {
     a = __uint_as_float(w[2 * i]);
     b = __uint_as_float(w[2 * i + 1]);
@@ -130,6 +136,13 @@ struct Fmt<RL_BF16> {
         w[i] = kNegInf2;
       else if (2 * i + 1 >= e)
         w[i] = (w[i] & 0xffffu) | (kNegInf2 & 0xffff0000u);
+    }
+  }
+  __device__ static void drop(uint32_t (&w)[16], int e) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (2 * i == e) w[i] = (w[i] & 0xffff0000u) | (kNegInf2 & 0xffffu);
+      if (2 * i + 1 == e) w[i] = (w[i] & 0xffffu) | (kNegInf2 & 0xffff0000u);
     }
   }
   __device__ static void pair(const uint32_t (&w)[16], int i, float& a, float& b) {
@@ -188,6 +201,13 @@ struct Fmt<RL_F16> {
         w[i] = kNegInf2;
       else if (2 * i + 1 >= e)
         w[i] = (w[i] & 0xffffu) | (kNegInf2 & 0xffff0000u);
+    }
+  }
+  __device__ static void drop(uint32_t (&w)[16], int e) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (2 * i == e) w[i] = (w[i] & 0xffff0000u) | (kNegInf2 & 0xffffu);
+      if (2 * i + 1 == e) w[i] = (w[i] & 0xffffu) | (kNegInf2 & 0xffff0000u);
     }
   }
   __device__ static void pair(const uint32_t (&w)[16], int i, float& a, float& b) {

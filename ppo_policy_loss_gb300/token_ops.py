@@ -1,8 +1,9 @@
-"""Token log-probabilities over torch CUDA tensors: the log-probabilities of
-given tokens with entropy and top alternatives, their gradient, and the
-autograd wrapper around both (rl_token_logprobs, rl_token_logprobs_bwd of
-include/rltoken.h; the rollout buffer of the ainews.cool RL.cu article,
-section "技术深度解析", holds such log-probabilities).
+"""Token log-probabilities and distillation over torch CUDA tensors: the
+log-probabilities of given tokens with entropy and top alternatives, their
+gradient, the loss and gradient of distillation from a teacher's top
+log-probabilities, and the autograd wrappers around them (include/rltoken.h;
+the rollout buffer of the ainews.cool RL.cu article, section "技术深度解析",
+holds such log-probabilities).
 
 Outputs are allocated with torch, everything is computed by librlloss's
 kernels.  Inputs are checked and never copied: a tensor of another type,
@@ -16,7 +17,9 @@ import contextlib
 
 import torch
 
-from . import DTYPES, rl_token_logprobs, rl_token_logprobs_bwd
+from . import (DISTILL_STATS_BYTES, DISTILL_TAILS, DTYPES, distill_stats_from_bytes, rl_token_logprobs,
+               rl_token_logprobs_bwd, rl_topk_distill_desc_init, rl_topk_distill_fwd_bwd,
+               rl_topk_distill_workspace_size)
 
 _DT = {torch.float32: DTYPES["f32"], torch.bfloat16: DTYPES["bf16"], torch.float16: DTYPES["f16"]}
 _HERE = contextlib.nullcontext()
@@ -167,3 +170,98 @@ class TokenLogprobs(torch.autograd.Function):
             entropy=ent if dent is not None else None,
             dentropy=dent.float().contiguous() if dent is not None else None, mask=mask,
             temperature=ctx.temperature), None, None, None
+
+
+def new_distill_workspace(device) -> torch.Tensor:
+    """Zero-filled workspace for topk_distill (every call leaves it ready for the next)."""
+    return torch.zeros(rl_topk_distill_workspace_size(), dtype=torch.uint8, device=device)
+
+
+def read_distill_stats(stats: torch.Tensor) -> dict:
+    return distill_stats_from_bytes(stats.cpu().numpy().tobytes())
+
+
+def topk_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logp: torch.Tensor,
+                 mask: torch.Tensor | None = None, weight: torch.Tensor | None = None, tail: str = "bucket",
+                 reverse: float = 0.0, temperature: float = 1.0, grad_scale: float = 1.0, norm: float = 0.0,
+                 dlogits="new", row_loss="new", workspace: torch.Tensor | None = None,
+                 stats: torch.Tensor | None = None, stream=None) -> dict:
+    """Distillation of the student's ``logits`` [R, V] from a teacher's top
+    entries, loss and gradient in one launch (rl_topk_distill_fwd_bwd).
+
+    ``teacher_ids`` int64 and ``teacher_logp`` float32 [R, K]: what
+    token_logprobs gives as topk_ids and topk_logp (an id of -1 is an empty
+    entry).  ``tail``: "bucket" keeps the rest of the vocabulary as one more
+    outcome, "renormalise" normalises the teacher over its entries.
+    ``reverse``: the weight of KL(student || teacher) beside KL(teacher ||
+    student).  ``mask`` uint8 or bool [R]; ``weight`` float32 [R]; ``norm``: what
+    the sum over rows is divided by (0: the number of valid rows).
+    ``dlogits`` / ``row_loss``: "new" allocates, None skips, a tensor is written
+    (``dlogits=logits`` overwrites the logits).
+
+    Returns dict(loss: float32 scalar, row_loss: [R], dlogits, stats: the device
+    record for read_distill_stats, workspace)."""
+    dt, R, V, ld = _logits(logits)
+    dev = logits.device
+    if teacher_ids.dim() != 2:
+        raise ValueError("teacher_ids must be of shape [R, K]")
+    K = teacher_ids.shape[1]
+    _given("teacher_ids", teacher_ids, torch.int64, (R, K), dev)
+    _given("teacher_logp", teacher_logp, torch.float32, (R, K), dev)
+    mask = _mask(mask, R, dev)
+    if weight is not None:
+        _given("weight", weight, torch.float32, (R,), dev)
+    if tail not in DISTILL_TAILS:
+        raise ValueError(f"tail must be one of {sorted(DISTILL_TAILS)}")
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous and on the logits' device")
+    if stats is not None and (stats.dtype != torch.uint8 or stats.device != dev or stats.numel() < DISTILL_STATS_BYTES):
+        raise ValueError(f"stats must be a uint8 tensor of {DISTILL_STATS_BYTES} bytes on the logits' device")
+    with _on(dev, stream):
+        if dlogits is not None:
+            dlogits = _dlogits_like(logits, dlogits, ld)
+        if isinstance(row_loss, str):
+            row_loss = torch.empty(R, dtype=torch.float32, device=dev)
+        elif row_loss is not None:
+            _given("row_loss", row_loss, torch.float32, (R,), dev)
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+        workspace = new_distill_workspace(dev) if workspace is None else workspace
+        stats = torch.empty(DISTILL_STATS_BYTES, dtype=torch.uint8, device=dev) if stats is None else stats
+        d = rl_topk_distill_desc_init()
+        p = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+        d.logits, d.dtype, d.R, d.V, d.ld = p(logits), dt, R, V, ld
+        d.teacher_ids, d.teacher_logp, d.K = p(teacher_ids), p(teacher_logp), K
+        d.mask, d.weight, d.tail = p(mask), p(weight), DISTILL_TAILS[tail]
+        d.reverse, d.temperature, d.grad_scale, d.norm = reverse, temperature, grad_scale, norm
+        d.dlogits, d.row_loss_out, d.loss_out = p(dlogits), p(row_loss), p(loss)
+        d.stats_dev, d.workspace = p(stats), p(workspace)
+        d.workspace_bytes = workspace.numel() * workspace.element_size()
+        rl_topk_distill_fwd_bwd(d)
+    return dict(loss=loss, row_loss=row_loss, dlogits=dlogits, stats=stats, workspace=workspace)
+
+
+class FusedTopkDistill(torch.autograd.Function):
+    """Autograd wrapper: loss = FusedTopkDistill.apply(logits, teacher_ids,
+    teacher_logp, mask, options), ``options`` a dict of topk_distill's keyword
+    arguments.
+
+    The forward pass runs the fused kernel and keeps its gradient; the backward
+    pass hands it back times the incoming gradient.  That product is skipped
+    where the incoming gradient is 1, which is read on the host, except while
+    a CUDA graph is being captured, where nothing is read and the product is
+    always taken."""
+
+    @staticmethod
+    def forward(ctx, logits, teacher_ids, teacher_logp, mask=None, options=None):
+        out = topk_distill(logits.detach(), teacher_ids, teacher_logp, mask=mask, **dict(options or {}))
+        ctx.save_for_backward(out["dlogits"])
+        return out["loss"]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        (dlogits,) = ctx.saved_tensors
+        if torch.cuda.is_current_stream_capturing() or float(grad) != 1.0:
+            # the product in fp32: a loss scale may not fit the gradient's type
+            dlogits = (dlogits.float() * grad).to(dlogits.dtype)
+        return dlogits, None, None, None, None

@@ -258,6 +258,7 @@ def lmhead_logprobs(hidden: torch.Tensor, weight: torch.Tensor, ids: torch.Tenso
     return dict(logp=logp, entropy=ent, lse=lse, workspace=workspace)
 
 
-# The token log-probability operators are part of this layer; they live in a
-# module of their own.
-from .token_ops import TokenLogprobs, token_logprobs, token_logprobs_backward  # noqa: E402,F401
+# The token log-probability and distillation operators are part of this layer;
+# they live in a module of their own.
+from .token_ops import (FusedTopkDistill, TokenLogprobs, new_distill_workspace,  # noqa: E402,F401
+                        read_distill_stats, token_logprobs, token_logprobs_backward, topk_distill)
