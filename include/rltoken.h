@@ -21,6 +21,7 @@
  *   logits      : [R, ld] of `dtype` (RL_F32, RL_BF16, RL_F16), row-major,
  *                 16-byte aligned, ld * sizeof(dtype) a multiple of 16,
  *                 ld >= V; the columns V .. ld-1 are ignored.
+ *   V           : 1 <= V <= 2^26.
  *   mask        : uint8[R], nonzero = valid row; NULL = every row is valid.
  *                 The logits, ids and teacher of a masked row are not read.
  *   temperature : z = logits / temperature enters every formula;
@@ -61,8 +62,8 @@ extern "C" {
  *   logp_out : float [R, n_ids]; NULL iff n_ids = 0.
  *   entropy_out, lse_out : float [R], each may be NULL.
  *   topk_ids, topk_logp  : int64 and float [R, k], both NULL iff k = 0.
- *   0 <= n_ids, k <= RL_TOKEN_MAX_K, k <= V, 1 <= V <= 2^30; with k > 0 a row
- *   may have at most 512 KB (2^18 16-bit or 2^17 fp32 logits).
+ *   0 <= n_ids, k <= RL_TOKEN_MAX_K, k <= V, with k > 0 a row may have at
+ *   most 4 MB (2^21 16-bit or 2^20 fp32 logits).
  * fp32 arithmetic on the exact differences to the row's maximum; the maximum
  * itself stays out of the running sum, so that a log-probability next to 0
  * keeps its relative precision.  Deterministic.  One launch.

@@ -11,68 +11,114 @@
 namespace rl {
 namespace {
 
+constexpr int kRowThreads = 128;  // threads that work on a row
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kMaxPieces = 8192;  // pieces of a row one CTA can search for alternatives
 constexpr int kMaxK = RL_TOKEN_MAX_K;
 constexpr int kList = 256;        // survivors a search ranks directly
 
 // ------------------------------------------------------------------ top-k search
-// The K largest of n unique keys by one group of kRowThreads threads, sorted.
-// Each thread takes the maximum of its keys (i * kRowThreads + tid); the K-th
-// largest of nb >= 2 K bucket maxima is a bound that at least K keys reach
-// and few others do; those that reach it are listed and ranked by counting.
-// If more than kList reach it (keys in an order that puts the large ones on
-// one thread), the bound is raised by bisection until exactly K do.
+// The k largest of n unique keys (0 = none) by kRowThreads threads, sorted.
+// Each thread takes the maxima of the even and the odd blocks of its keys; the
+// k-th largest of nb >= 2 k bucket maxima is a bound that at least k keys
+// reach and few others do; those that reach it are listed and ranked by
+// counting.  If more than kList reach it (an order of the keys that puts the
+// large ones on few threads), the bound is raised by bisection until exactly k
+// do.
 template <class K>
 struct SelSmem {
-  alignas(16) K a[kList];
-  alignas(16) K b[kList];
+  alignas(16) K a[2 * kRowThreads];
+  alignas(16) K b[kList + 4];
   K bound;
   int count;
   int sums[2];
 };
 
-template <class K>
-__device__ __forceinline__ int rank_of(const K* list, int n, K key) {
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
+__device__ __forceinline__ void row_barrier() { named_barrier(1, kRowThreads); }
+
+// Keys of list[0 .. n-1] above `key`; n up to a multiple of 16 bytes is read,
+// the places past n hold 0.
+__device__ __forceinline__ int rank_of(const uint32_t* list, int n, uint32_t key) {
   int r = 0;
-  for (int j = 0; j < n; ++j) r += list[j] > key;
+#pragma unroll 4
+  for (int j = 0; j < n; j += 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(list + j);
+    r += (v.x > key) + (v.y > key) + (v.z > key) + (v.w > key);
+  }
+  return r;
+}
+__device__ __forceinline__ int rank_of(const unsigned long long* list, int n, unsigned long long key) {
+  int r = 0;
+#pragma unroll 4
+  for (int j = 0; j < n; j += 2) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(list + j);
+    r += (v.x > key) + (v.y > key);
+  }
   return r;
 }
 
-// get(i): key i (0 = none), i < n.  out[0 .. K-1]: the keys, largest first, 0
-// where there are fewer.  All kRowThreads threads; ends with a barrier.
+// f(key) for this thread's keys get(tid), get(tid + kRowThreads), ... below n,
+// eight loads at a time; f also gets the block's parity.
+template <class K, class Get, class Fn>
+__device__ __forceinline__ void each_key(Get get, int n, int tid, Fn f) {
+  for (int base = tid; base < n; base += 8 * kRowThreads) {
+    K v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = base + j * kRowThreads < n ? get(base + j * kRowThreads) : 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f(v[j], j & 1);
+  }
+}
+
+// get(i): key i, i < n.  out[0 .. k-1]: the largest first, 0 where there are
+// fewer.  All kRowThreads threads, after a barrier; ends with a barrier.
 template <class K, class Get>
 __device__ __forceinline__ void block_select(Get get, int n, int k, K* out, SelSmem<K>& s, int tid) {
-  K best = 0;
-  for (int i = tid; i < n; i += kRowThreads) {
-    const K v = get(i);
-    best = v > best ? v : best;
-  }
+  K best[2] = {0, 0};
+  each_key<K>(get, n, tid, [&](K v, int odd) { best[odd] = v > best[odd] ? v : best[odd]; });
   const int nb = k <= 16 ? 32 : k <= 32 ? 64 : k <= 64 ? 128 : 256;
-  const int per = kRowThreads / nb;  // neighbouring lanes that share a bucket
-  for (int o = 1; o < per; o <<= 1) {
-    const K v = __shfl_xor_sync(0xffffffffu, best, o);
-    best = v > best ? v : best;
+  const K most = best[0] > best[1] ? best[0] : best[1];
+  if (nb == 2 * kRowThreads) {
+    s.a[2 * tid] = best[0];
+    s.a[2 * tid + 1] = best[1];
+  } else {
+    const int per = kRowThreads / nb;  // neighbouring lanes that share a bucket
+    K top = most;
+    for (int o = 1; o < per; o <<= 1) {
+      const K v = __shfl_xor_sync(0xffffffffu, top, o);
+      top = v > top ? v : top;
+    }
+    if (tid % per == 0) s.a[tid / per] = top;
   }
-  if (tid % per == 0) s.a[tid / per] = best;
   if (tid == 0) {
     s.bound = 1;
     s.count = 0;
     s.sums[0] = s.sums[1] = 0;
   }
   if (tid < k) out[tid] = 0;
-  __syncthreads();
-  if (tid < nb && s.a[tid] != 0 && rank_of(s.a, nb, s.a[tid]) == k - 1) s.bound = s.a[tid];
-  __syncthreads();
-  K bound = s.bound;
-  for (int i = tid; i < n; i += kRowThreads) {
-    const K v = get(i);
-    if (v >= bound) {
-      const int p = atomicAdd(&s.count, 1);
-      if (p < kList) s.b[p] = v;
-    }
+  row_barrier();
+  for (int q = tid; q < nb; q += kRowThreads) {
+    const K v = s.a[q];
+    if (v != 0 && rank_of(s.a, nb, v) == k - 1) s.bound = v;
   }
-  __syncthreads();
+  row_barrier();
+  const K bound = s.bound;
+  if (most >= bound)
+    each_key<K>(get, n, tid, [&](K v, int) {
+      if (v >= bound) {
+        const int p = atomicAdd(&s.count, 1);
+        if (p < kList) s.b[p] = v;
+      }
+    });
+  row_barrier();
   int cnt = s.count;
   if (cnt > kList) {
     // bisection over the key's bits: the largest bound that k keys still reach
@@ -80,33 +126,34 @@ __device__ __forceinline__ void block_select(Get get, int n, int k, K* out, SelS
     for (int round = 0; lo < hi; ++round) {
       const K mid = lo + (hi - lo) / 2 + 1;
       int c = 0;
-      for (int i = tid; i < n; i += kRowThreads) c += get(i) >= mid;
+      if (most >= mid) each_key<K>(get, n, tid, [&](K v, int) { c += v >= mid; });
       c = __reduce_add_sync(0xffffffffu, c);
       if ((tid & 31) == 0 && c) atomicAdd(&s.sums[round & 1], c);
-      __syncthreads();
+      row_barrier();
       const int total = s.sums[round & 1];
       if (tid == 0) s.sums[(round + 1) & 1] = 0;
-      __syncthreads();
+      row_barrier();
       if (total >= k)
         lo = mid;
       else
         hi = mid - 1;
     }
     if (tid == 0) s.count = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += kRowThreads) {
-      const K v = get(i);
+    row_barrier();
+    each_key<K>(get, n, tid, [&](K v, int) {
       if (v >= lo) s.b[atomicAdd(&s.count, 1)] = v;  // keys are unique: exactly k reach it
-    }
-    __syncthreads();
+    });
+    row_barrier();
     cnt = s.count;
   }
-  if (tid < cnt) {
-    const K v = s.b[tid];
+  if (tid < 4) s.b[cnt + tid] = 0;  // what rank_of reads past the list
+  row_barrier();
+  for (int q = tid; q < cnt; q += kRowThreads) {
+    const K v = s.b[q];
     const int r = rank_of(s.b, cnt, v);
     if (r < k) out[r] = v;
   }
-  __syncthreads();
+  row_barrier();
 }
 
 // ------------------------------------------------------------------ forward
@@ -125,188 +172,360 @@ struct LpArgs {
   int n_ids, k;
 };
 
-// The search key of a piece or an element: value key above position, so that
-// the lower position wins a tie.  32 bits for 16-bit formats, 64 for fp32.
+// The search key of a piece or an element: its value's order above its place,
+// so that the lower place wins a tie.  32 bits for 16-bit formats, 64 for fp32.
 template <class V>
-struct Composite;
+struct PlaceKey;
 template <>
-struct Composite<uint16_t> {
+struct PlaceKey<uint16_t> {
   using K = uint32_t;
-  __device__ static K make(uint16_t v, int pos) { return v ? (static_cast<K>(v) << 16) | (0xffffu - pos) : 0u; }
-  __device__ static int pos(K k) { return static_cast<int>(0xffffu - (k & 0xffffu)); }
-  __device__ static uint16_t value(K k) { return static_cast<uint16_t>(k >> 16); }
+  __device__ static K make(uint16_t v, int at) { return v ? (static_cast<K>(v) << 16) | (0xffffu - at) : 0u; }
+  __device__ static int at(K k) { return static_cast<int>(0xffffu - (k & 0xffffu)); }
+  __device__ static uint32_t value(K k) { return k >> 16; }
 };
 template <>
-struct Composite<uint32_t> {
+struct PlaceKey<uint32_t> {
   using K = unsigned long long;
-  __device__ static K make(uint32_t v, int pos) {
-    return v ? (static_cast<K>(v) << 32) | (0xffffffffu - static_cast<uint32_t>(pos)) : 0ull;
+  __device__ static K make(uint32_t v, int at) {
+    return v ? (static_cast<K>(v) << 32) | (0xffffffffu - static_cast<uint32_t>(at)) : 0ull;
   }
-  __device__ static int pos(K k) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(k)); }
+  __device__ static int at(K k) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(k)); }
   __device__ static uint32_t value(K k) { return static_cast<uint32_t>(k >> 32); }
 };
+// Across CTAs: the value's order above the element's place in the row.
+using ElemKey = unsigned long long;
+
+constexpr int kChunk = kRowThreads * kPieceBytes;  // one piece per consumer thread
+constexpr int kSlots = 4;
+constexpr int kMaxCluster = 8;
+constexpr int kLpThreads = kRowThreads + 32;  // consumers and the producer warp
+constexpr int kLpCtas = 4;                    // CTAs a SM holds, registers permitting
+constexpr int kSmemPerSm = 228 * 1024;
 
 template <int DT>
 struct LpSmem {
   using F = Fmt<DT>;
-  using C = Composite<typename F::Key>;
-  alignas(16) typename F::Key keys[kMaxPieces];  // piece maxima, then the chosen pieces' elements
-  SelSmem<typename C::K> sel;
-  typename C::K top[kMaxK];
-  int slots[kMaxK];
+  using C = PlaceKey<typename F::Key>;
+  Ring<kSlots, kChunk> ring;
+  union {  // one search at a time
+    SelSmem<typename C::K> sel;
+    SelSmem<ElemKey> join_sel;
+  };
+  alignas(16) typename C::K top[kMaxK];
+  alignas(16) int slots[kMaxK];  // the k pieces with the largest maxima, in the row's order
   RowStats part[kRowWarps];
+  RowStats join_part[kMaxCluster];  // clusters: every slice's statistics, in rank 0's memory
+  unsigned long long arrived, freed;  // rank 0: every slice is in; the others: rank 0 has taken the row
+  int abort;
 };
 
-__device__ __forceinline__ RowStats merge_parts(const RowStats* part, float c) {
-  RowStats s = part[0];
-#pragma unroll
-  for (int w = 1; w < kRowWarps; ++w) s = merge_row(s, part[w], c);
-  return s;
+// After it, as much as the launch needs: with clusters and alternatives, what
+// every CTA of the row found (in rank 0's memory) and the row's choice of it;
+// then the keys: piece maxima, then the chosen pieces' elements.
+constexpr int kJoinKeys = (kMaxCluster + 1) * kMaxK;
+constexpr int kAllElems = 4096;  // slices of at most this many elements search them without choosing pieces
+template <class F>
+__host__ __device__ constexpr bool takes_all(int per, int k) {
+  return per <= k || per * F::kPiece <= kAllElems;
+}
+template <class F>
+__host__ __device__ constexpr int key_places(int per, int k) {
+  const int elems = (takes_all<F>(per, k) ? per : k) * F::kPiece;
+  return k == 0 ? 0 : per > elems ? per : elems;
 }
 
-// A row whose maximum is at most kExact: its statistics without the floor, -inf elements skipped.
-// Rare, so it reads the row again.  m = -inf: no element is finite.
+// The statistics of a row that needs_exact names, by differences to its
+// maximum, -inf elements skipped.  Rare, so it reads the row again.  m = -inf:
+// no element is finite.  All consumer threads.
 template <class F>
 __device__ __noinline__ RowStats exact_row(const unsigned char* row, int V, float c, RowStats* part, int tid) {
+  const int n_vecs = (V + F::kVec - 1) / F::kVec;
+  auto each = [&](auto f) {
+#pragma unroll 4
+    for (int v = tid; v < n_vecs; v += kRowThreads) {
+      float z[F::kVec];
+      F::unpack(*reinterpret_cast<const uint4*>(row + static_cast<long long>(v) * 16), z);
+#pragma unroll
+      for (int i = 0; i < F::kVec; ++i)
+        if (v * F::kVec + i < V) f(z[i]);
+    }
+  };
   float m = -INFINITY;
-  for (int i = tid; i < V; i += kRowThreads) m = max_nan(m, F::load(row, i));
+  each([&](float z) { m = max_nan(m, z); });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  __syncthreads();
+  row_barrier();
   if ((tid & 31) == 0) part[tid >> 5].m = m;
-  __syncthreads();
+  row_barrier();
   for (int w = 0; w < kRowWarps; ++w) m = max_nan(m, part[w].m);
-  __syncthreads();
+  row_barrier();
   float s = 0.f, t = 0.f;
   if (m > -INFINITY)
-    for (int i = tid; i < V; i += kRowThreads) {
-      const float x = (F::load(row, i) - m) * c;
+    each([&](float z) {
+      const float x = (z - m) * c;
       const float e = ex2_approx(x);
       s += e;
       if (e > 0.f) t = fmaf(e, x, t);
-    }
+    });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     s += __shfl_xor_sync(0xffffffffu, s, o);
     t += __shfl_xor_sync(0xffffffffu, t, o);
   }
   if ((tid & 31) == 0) part[tid >> 5] = RowStats{m, s, t};
-  __syncthreads();
+  row_barrier();
   s = t = 0.f;
   for (int w = 0; w < kRowWarps; ++w) {
     s += part[w].r;
     t += part[w].t;
   }
+  if (m != m) s = t = m;
   return RowStats{m, s - 1.f, t};
 }
 
+// The rows first, first + stride, ... of a CTA, with their mask bits: one
+// ballot for 32 of them.  Whole warp.
+struct RowBits {
+  uint32_t bits;
+  __device__ __forceinline__ bool valid(const LpArgs& a, long long first, long long stride, int i, int lane) {
+    if (!a.mask) return true;
+    if ((i & 31) == 0) {
+      const long long r = first + (i + lane) * stride;
+      bits = __ballot_sync(0xffffffffu, r < a.R && a.mask[r] != 0);
+    }
+    return (bits >> (i & 31)) & 1u;
+  }
+};
+
+// A CTA (or, for few rows, a cluster of up to 8, each with a slice of the
+// row's pieces) takes a row at a time.  The producer warp streams the valid
+// rows' chunks through the ring; the consumers keep one key per piece (its
+// maximum) and the running statistics, then search the keys for the
+// alternatives while the producer fills the ring with the next row.
 template <int DT, bool kEntropy>
-__global__ void __launch_bounds__(kRowThreads) token_logprobs_kernel(const LpArgs a) {
+__global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(const LpArgs a) {
   using F = Fmt<DT>;
-  using Key = typename F::Key;
-  using C = Composite<Key>;
+  using C = PlaceKey<typename F::Key>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   LpSmem<DT>& sm = *reinterpret_cast<LpSmem<DT>*>(smem_raw);
+  volatile int* abort = &sm.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  static_assert(sizeof(LpSmem<DT>) % 16 == 0, "the key arrays follow");
+  const int csize = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  const long long first = blockIdx.x / csize, stride = gridDim.x / csize;
   const int V = static_cast<int>(a.V);
   const int n_pieces = (V + F::kPiece - 1) / F::kPiece;
-  const int k = a.k, n_ids = a.n_ids;
-  unsigned int err = 0;
+  const int per = (n_pieces + csize - 1) / csize;
+  const int g0 = min(n_pieces, rank * per), g1 = min(n_pieces, g0 + per);  // this CTA's pieces
+  const long long row_bytes16 = (static_cast<long long>(V) * F::kBytes + 15) & ~15LL;
+  const long long b0 = static_cast<long long>(g0) * kPieceBytes;
+  const long long n_bytes = min(row_bytes16, static_cast<long long>(g1) * kPieceBytes) - b0;
+  const int n_chunks = static_cast<int>((n_bytes + kChunk - 1) / kChunk);
+  ElemKey* const join_keys = reinterpret_cast<ElemKey*>(smem_raw + sizeof(LpSmem<DT>));
+  ElemKey* const join_top = join_keys + kMaxCluster * kMaxK;
+  typename F::Key* const keys = reinterpret_cast<typename F::Key*>(csize > 1 && a.k ? join_keys + kJoinKeys : join_keys);
 
-  for (long long row = blockIdx.x; row < a.R; row += gridDim.x) {
-    if (a.mask && a.mask[row] == 0) {
-      if (tid < n_ids) a.logp[row * n_ids + tid] = 0.f;
-      if (tid < k) {
-        a.topk_ids[row * k + tid] = -1;
-        a.topk_logp[row * k + tid] = 0.f;
-      }
-      if (tid == 0 && a.entropy) a.entropy[row] = 0.f;
-      if (tid == 0 && a.lse) a.lse[row] = 0.f;
-      continue;
-    }
-    const unsigned char* src = a.logits + row * a.row_bytes;
-    long long y = -1;
-    float zy = 0.f;
-    if (tid < n_ids) {
-      y = a.ids[row * n_ids + tid];
-      if (y >= 0 && y < V) zy = F::load(src, y);
-    }
-    WarpStats st;
-    warp_stats_init(st, F::kFloor, lane);
-    for (int p0 = 0; p0 < n_pieces; p0 += kRowThreads) {
-      const int p = p0 + tid;
-      uint32_t w[16];
-      const long long row_bytes16 = (static_cast<long long>(V) * F::kBytes + 15) & ~15LL;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const long long off = static_cast<long long>(p) * kPieceBytes + j * 16;
-        uint4 v = make_uint4(F::kNegInf2, F::kNegInf2, F::kNegInf2, F::kNegInf2);
-        if (off < row_bytes16) v = __ldg(reinterpret_cast<const uint4*>(src + off));
-        w[4 * j] = v.x;
-        w[4 * j + 1] = v.y;
-        w[4 * j + 2] = v.z;
-        w[4 * j + 3] = v.w;
-      }
-      if ((p + 1) * F::kPiece > V) F::cut(w, max(0, V - p * F::kPiece));
-      const uint32_t rm = F::raw_max(w);
-      if (k && p < n_pieces) sm.keys[p] = F::raw_key(rm);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = F::clamp(w[i]);
-      add_piece<F, kEntropy>(st, w, max_nan(F::raw_value(rm), F::kFloor), a.c, lane);
-    }
-    const RowStats ws = warp_stats_sum(st);
-    if (lane == 0) sm.part[warp] = ws;
-    __syncthreads();
-    RowStats rs = merge_parts(sm.part, a.c);
-    if (!(rs.m > F::kExact)) rs = exact_row<F>(src, V, a.c, sm.part, tid);
-    const float log_s = log1pf(rs.r);
-    if (tid < n_ids) {
-      const bool ok = y >= 0 && y < V;
-      if (!ok) err |= RL_DEVERR_ID_RANGE;
-      a.logp[row * n_ids + tid] = ok ? fmaf(zy - rs.m, a.inv_temp, -log_s) : __int_as_float(0x7fc00000);
-    }
-    if (tid == 0) {
-      if (a.lse) a.lse[row] = fmaf(rs.m, a.inv_temp, log_s);
-      if (kEntropy && a.entropy)
-        a.entropy[row] = rs.m > -INFINITY ? fmaf(-kLn2, rs.t / (1.f + rs.r), log_s) : __int_as_float(0x7fc00000);
-    }
-    if (k) {
-      // the k pieces with the largest maxima hold the k largest elements
-      int n_slots = n_pieces;
-      const bool direct = n_pieces <= kMaxPieces / F::kPiece;  // every element fits the key array
-      __syncthreads();
-      if (!direct) {
-        block_select<typename C::K>([&](int i) { return C::make(sm.keys[i], i); }, n_pieces, k, sm.top, sm.sel, tid);
-        n_slots = k;
-        if (tid < k) {  // back into the row's order
-          const int g = C::pos(sm.top[tid]);
-          int r = 0;
-          for (int j = 0; j < k; ++j) r += C::pos(sm.top[j]) < g;
-          sm.slots[r] = g;
-        }
-        __syncthreads();
-      }
-      for (int i = tid; i < n_slots * F::kPiece; i += kRowThreads) {
-        const int e = (direct ? i / F::kPiece : sm.slots[i / F::kPiece]) * F::kPiece + i % F::kPiece;
-        sm.keys[i] = e < V ? F::load_key(src, e) : Key(0);
-      }
-      __syncthreads();
-      block_select<typename C::K>([&](int i) { return C::make(sm.keys[i], i); }, n_slots * F::kPiece, k, sm.top,
-                                  sm.sel, tid);
-      if (tid < k) {
-        const typename C::K key = sm.top[tid];
-        const int i = C::pos(key);
-        const int e = (direct ? i / F::kPiece : sm.slots[i / F::kPiece]) * F::kPiece + i % F::kPiece;
-        a.topk_ids[row * k + tid] = e;
-        a.topk_logp[row * k + tid] = fmaf(F::key_value(C::value(key)) - rs.m, a.inv_temp, -log_s);
-      }
-    }
-    __syncthreads();
+  if (tid == 0) {
+    sm.ring.init(kRowWarps);
+    mbar_init(smem_addr(&sm.arrived), csize);
+    mbar_init(smem_addr(&sm.freed), 1);
+    sm.abort = 0;
+    fence_mbar_init();
   }
-  if (err && a.status) atomicOr(a.status, err);
+  __syncthreads();
+  if (csize > 1) cluster_sync_all();
+
+  if (warp == kRowWarps) {
+    // ---------------------------------------------------------------- producer
+    const uint64_t pol = policy_normal();
+    uint32_t it = 0;
+    bool ok = true;
+    RowBits rows;
+    int i = 0;
+    for (long long row = first; row < a.R && ok; row += stride, ++i) {
+      if (!rows.valid(a, first, stride, i, lane)) continue;
+      if (lane == 0) {
+        const unsigned char* src = a.logits + row * a.row_bytes + b0;
+        for (int q = 0; q < n_chunks && ok; ++q) {
+          const long long off = static_cast<long long>(q) * kChunk;
+          ok = sm.ring.issue(it, src + off, static_cast<uint32_t>(min(static_cast<long long>(kChunk), n_bytes - off)),
+                             pol, abort);
+          it += ok;
+        }
+        if (!ok) sm.ring.drain(it);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+  } else {
+    // ---------------------------------------------------------------- consumers
+    const int k = a.k, n_ids = a.n_ids, n_mine = g1 - g0;
+    unsigned int err = 0;
+    uint32_t it = 0, done = 0;  // chunks taken, rows done
+    RowBits rows;
+    WarpStats st;
+    st.low = false;
+    int row_i = 0;
+    for (long long row = first; row < a.R; row += stride, ++row_i) {
+      if (!rows.valid(a, first, stride, row_i, lane)) {
+        if (rank == 0) {
+          for (int q = tid; q < n_ids; q += kRowThreads) a.logp[row * n_ids + q] = 0.f;
+          for (int q = tid; q < k; q += kRowThreads) {
+            a.topk_ids[row * k + q] = -1;
+            a.topk_logp[row * k + q] = 0.f;
+          }
+          if (tid == 0 && a.entropy) a.entropy[row] = 0.f;
+          if (tid == 0 && a.lse) a.lse[row] = 0.f;
+        }
+        continue;
+      }
+      const unsigned char* src = a.logits + row * a.row_bytes;
+      long long y = -1;
+      float zy = 0.f;
+      if (rank == 0 && tid < n_ids) {
+        y = a.ids[row * n_ids + tid];
+        if (y >= 0 && y < V) zy = F::load(src, y);
+      }
+      warp_stats_init<F>(st, a.c);
+      for (int i = 0; i < n_chunks; ++i, ++it) {
+        const uint32_t buf = sm.ring.wait(it, abort);
+        const int w0 = i * kRowThreads + warp * 32;  // the warp's first piece in the slice
+        const int here = n_mine - w0;                // pieces from there to its end
+        if (here > 0) {
+          uint32_t w[16];
+          // a warp that reaches the row's end takes the elements in order
+          const bool ragged = (g0 + w0 + 32) * F::kPiece > V;
+          load_piece(w, 0, buf + tid * kPieceBytes, ragged ? 0 : lane >> 1);
+          sm.ring.release(it, lane);
+          const bool part = here < 32 || ragged;
+          if (part) F::cut(w, 0, lane < here ? min(F::kPiece, V - (g0 + w0 + lane) * F::kPiece) : 0);
+          const uint32_t rm = F::raw_max(w, 0);
+          if (k && lane < here) keys[w0 + lane] = F::raw_key(rm);
+          if (part) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = F::clamp(w[j]);
+          }
+          add_piece<F, kEntropy>(st, w, max_nan(F::raw_value(rm), F::kFloor), a.c, lane, row_i == 0);
+        } else {
+          sm.ring.release(it, lane);
+        }
+      }
+      const RowStats ws = warp_stats_sum<F>(st, a.c);
+      if (lane == 0) sm.part[warp] = ws;
+      row_barrier();
+      RowStats rs = sm.part[0];
+#pragma unroll
+      for (int w = 1; w < kRowWarps; ++w) rs = merge_row(rs, sm.part[w], a.c);
+      // a NaN in t is a NaN logit or a first -inf: clamp from the next row on
+      if (kEntropy) st.low = st.low || rs.t != rs.t;
+      // this CTA's k largest: the k pieces with the largest maxima hold them
+      int n_slots = n_mine;
+      const bool all = takes_all<F>(per, k);
+      auto element = [&](int i) {  // the row's element at place i of the key array
+        return (g0 + (all ? i / F::kPiece : sm.slots[i / F::kPiece])) * F::kPiece + i % F::kPiece;
+      };
+      auto key_at = [&](int i) { return C::make(keys[i], i); };
+      if (k) {
+        if (!all) {
+          block_select<typename C::K>(key_at, n_mine, k, sm.top, sm.sel, tid);
+          n_slots = min(k, n_mine);
+          if (tid < n_slots) {  // back into the row's order
+            const int g = C::at(sm.top[tid]);
+            int r = 0;
+            for (int j = 0; j < n_slots; ++j) r += C::at(sm.top[j]) < g;
+            sm.slots[r] = g;
+          }
+          row_barrier();
+        }
+        const int n_elems = n_slots * F::kPiece;
+        for (int base = tid; base < n_elems; base += 8 * kRowThreads) {
+          typename F::Key v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int i = base + j * kRowThreads;
+            v[j] = 0;
+            if (i < n_elems) {
+              const int e = element(i);
+              if (e < V) v[j] = static_cast<typename F::Key>(F::load_order(src, e));
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (base + j * kRowThreads < n_elems) keys[base + j * kRowThreads] = v[j];
+        }
+        row_barrier();
+        block_select<typename C::K>(key_at, n_elems, k, sm.top, sm.sel, tid);
+      }
+      if (csize > 1) {
+        // every CTA's findings into rank 0's memory
+        if (done > 0 && rank != 0) wait_bounded<true>(smem_addr(&sm.freed), (done - 1) & 1, abort);
+        if (tid < k) {
+          const typename C::K key = sm.top[tid];
+          ElemKey u = 0;
+          if (key)
+            u = (static_cast<ElemKey>(C::value(key)) << 32) | (0xffffffffu - static_cast<uint32_t>(element(C::at(key))));
+          st_cluster_u64(map_to_rank(smem_addr(&join_keys[rank * kMaxK + tid]), 0), u);
+        }
+        if (tid == 0) {
+          const uint32_t to = map_to_rank(smem_addr(&sm.join_part[rank]), 0);
+          st_cluster_f32(to, rs.m);
+          st_cluster_f32(to + 4, rs.r);
+          st_cluster_f32(to + 8, rs.t);
+        }
+        fence_cluster();
+        row_barrier();
+        if (tid == 0) mbar_arrive_remote(map_to_rank(smem_addr(&sm.arrived), 0));
+        if (rank == 0) {
+          wait_bounded<true>(smem_addr(&sm.arrived), done & 1, abort);
+          rs = sm.join_part[0];
+          for (int q = 1; q < csize; ++q) rs = merge_row(rs, sm.join_part[q], a.c);
+          if (k)
+            block_select<ElemKey>([&](int i) { return i % kMaxK < k ? join_keys[i] : 0ull; }, csize * kMaxK, k,
+                                  join_top, sm.join_sel, tid);
+          row_barrier();  // everything has been read: the others may send the next row
+          if (tid > 0 && tid < csize) mbar_arrive_remote(map_to_rank(smem_addr(&sm.freed), tid));
+        }
+        ++done;
+        if (rank != 0) continue;
+      }
+      if (needs_exact<F>(rs.m, a.c) || (kEntropy && rs.t != rs.t)) rs = exact_row<F>(src, V, a.c, sm.part, tid);
+      const float log_s = log1pf(rs.r);
+      if (tid < n_ids) {
+        const bool ok = y >= 0 && y < V;
+        if (!ok) err |= RL_DEVERR_ID_RANGE;
+        a.logp[row * n_ids + tid] = ok ? fmaf(zy - rs.m, a.inv_temp, -log_s) : __int_as_float(0x7fc00000);
+      }
+      if (tid == 0) {
+        if (a.lse) a.lse[row] = fmaf(rs.m, a.inv_temp, log_s);
+        if (kEntropy && a.entropy)
+          a.entropy[row] = rs.m > -INFINITY ? fmaf(-kLn2, rs.t / (1.f + rs.r), log_s) : __int_as_float(0x7fc00000);
+      }
+      if (tid < k) {
+        long long id;
+        uint32_t order;
+        if (csize > 1) {
+          const ElemKey key = join_top[tid];
+          id = 0xffffffffu - static_cast<uint32_t>(key);
+          order = static_cast<uint32_t>(key >> 32);
+        } else {
+          const typename C::K key = sm.top[tid];
+          id = element(C::at(key));
+          order = C::value(key);
+        }
+        a.topk_ids[row * k + tid] = id;
+        a.topk_logp[row * k + tid] = fmaf(F::order_value(order) - rs.m, a.inv_temp, -log_s);
+      }
+      row_barrier();  // the shared arrays are free for the next row
+    }
+    if (err && a.status) atomicOr(a.status, err);
+  }
+  if (csize > 1) cluster_sync_all();  // no CTA leaves while another may still write its memory
+  __syncthreads();
+  if (tid == 0 && *abort && a.status) atomicOr(a.status, RL_DEVERR_TIMEOUT);
 }
 
 // ------------------------------------------------------------------ backward
+constexpr int kBwdThreads = 256;
+
 struct LpBwdArgs {
   const unsigned char* logits;
   const long long* ids;
@@ -328,7 +547,7 @@ struct LpBwdArgs {
 // x = (z_v / T - lse) log2(e); the given ids' elements are computed once
 // more and written after the segment's own stores.
 template <int DT, bool kEntropy>
-__global__ void __launch_bounds__(kRowThreads) token_logprobs_bwd_kernel(const LpBwdArgs a) {
+__global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const LpBwdArgs a) {
   using F = Fmt<DT>;
   constexpr int kVec = F::kVec;
   __shared__ long long s_id[kMaxK];
@@ -377,7 +596,7 @@ __global__ void __launch_bounds__(kRowThreads) token_logprobs_bwd_kernel(const L
       x = fmaxf(x, -1024.f);  // p is 0 there; 0 * -inf would not be
       return p * fmaf(a1, x, a0);
     };
-    for (int v = v0 + tid; v < v1; v += kRowThreads) {
+    for (int v = v0 + tid; v < v1; v += kBwdThreads) {
       float d[kVec];
       if (on) {
         F::unpack(*reinterpret_cast<const uint4*>(src + static_cast<long long>(v) * 16), d);
@@ -433,26 +652,55 @@ rl_status allow_smem(const void* fn, int dev, int smem) {
   return RL_OK;
 }
 
+// CTAs that share a row.  One while there are rows for every CTA the GPU
+// holds; for fewer rows the row's slices spread over up to 8 CTAs, as long as
+// each gets a few chunks, or as many as its pieces need.
+int cluster_for(long long R, long long n_pieces, int sms) {
+  int c = 1;
+  while (c < kMaxCluster && R * c <= 2LL * sms && n_pieces >= static_cast<long long>(c) * 4 * kRowThreads) c *= 2;
+  return c;
+}
+
 template <int DT, bool kEntropy>
 rl_status launch_fwd(const LpArgs& a, int dev, int sms, cudaStream_t stream) {
+  using F = Fmt<DT>;
   const void* fn = reinterpret_cast<const void*>(&token_logprobs_kernel<DT, kEntropy>);
-  const int smem = static_cast<int>(sizeof(LpSmem<DT>));
-  const rl_status st = allow_smem(fn, dev, smem);
+  const long long n_pieces = (a.V + F::kPiece - 1) / F::kPiece;
+  int c = cluster_for(a.R, n_pieces, sms);
+  while (a.k > 0 && c < kMaxCluster && (n_pieces + c - 1) / c > kMaxPieces) c *= 2;
+  const int places = key_places<F>(static_cast<int>((n_pieces + c - 1) / c), a.k);
+  constexpr int join_bytes = kJoinKeys * static_cast<int>(sizeof(ElemKey));
+  const int smem = static_cast<int>(sizeof(LpSmem<DT>) + places * sizeof(typename F::Key)) + (c > 1 && a.k ? join_bytes : 0);
+  constexpr int most_smem = static_cast<int>(sizeof(LpSmem<DT>) + kMaxPieces * sizeof(typename F::Key)) + join_bytes;
+  const rl_status st = allow_smem(fn, dev, most_smem);
   if (st != RL_OK) return st;
-  const long long want = 4LL * sms;
-  token_logprobs_kernel<DT, kEntropy><<<static_cast<unsigned>(a.R < want ? a.R : want), kRowThreads, smem, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? RL_OK : RL_ERR_CUDA;
+  int held = kSmemPerSm / (smem + 1024);  // CTAs a SM holds at once (1 KB each is the system's)
+  if (held > kLpCtas) held = kLpCtas;
+  const long long most = static_cast<long long>(held) * sms / c;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(c);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(c * (a.R < most ? a.R : most)));
+  cfg.blockDim = dim3(kLpThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<DT, kEntropy>, a) == cudaSuccess ? RL_OK : RL_ERR_CUDA;
 }
 
 template <int DT, bool kEntropy>
 rl_status launch_bwd(const LpBwdArgs& a, int sms, cudaStream_t stream) {
   const long long units = a.R * a.n_seg, want = 8LL * sms;
-  token_logprobs_bwd_kernel<DT, kEntropy><<<static_cast<unsigned>(units < want ? units : want), kRowThreads, 0, stream>>>(a);
+  token_logprobs_bwd_kernel<DT, kEntropy><<<static_cast<unsigned>(units < want ? units : want), kBwdThreads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? RL_OK : RL_ERR_CUDA;
 }
 
 bool shape_ok(long long R, long long V, long long ld) {
-  return R >= 0 && R < (1LL << 31) && V >= 1 && V <= (1LL << 30) && ld >= V && ld <= (1LL << 31);
+  return R >= 0 && R < (1LL << 31) && V >= 1 && V <= kMaxVocab && ld >= V && ld <= (1LL << 31);
 }
 
 }  // namespace
@@ -469,7 +717,7 @@ extern "C" rl_status rl_token_logprobs(const void* logits, rl_dtype dtype, long 
   if (!shape_ok(R, V, ld)) return RL_ERR_SHAPE;
   if (n_ids < 0 || n_ids > RL_TOKEN_MAX_K || k < 0 || k > RL_TOKEN_MAX_K || !temperature_ok(temperature))
     return RL_ERR_ARG;
-  if (k > V || (k > 0 && V * es > static_cast<long long>(kMaxPieces) * kPieceBytes)) return RL_ERR_SHAPE;
+  if (k > V || (k > 0 && V * es > static_cast<long long>(kMaxPieces) * kPieceBytes * kMaxCluster)) return RL_ERR_SHAPE;
   if (R == 0) return RL_OK;
   if (!logits || (n_ids > 0 && (!ids || !logp_out)) || (k > 0 && (!topk_ids || !topk_logp))) return RL_ERR_NULL;
   if ((reinterpret_cast<uintptr_t>(logits) & 15) || ((ld * es) & 15)) return RL_ERR_ALIGN;
@@ -545,7 +793,7 @@ extern "C" rl_status rl_token_logprobs_bwd(const void* logits, rl_dtype dtype, l
   a.n_ids = n_ids;
   const long long n_vecs = (V * es + 15) / 16;
   long long seg = (16LL * sms + R - 1) / R;  // enough units for every CTA
-  const long long most = (n_vecs + 2 * kRowThreads - 1) / (2 * kRowThreads);
+  const long long most = (n_vecs + 2 * kBwdThreads - 1) / (2 * kBwdThreads);
   if (seg > most) seg = most;
   a.seg_vecs = (n_vecs + seg - 1) / seg;
   a.n_seg = static_cast<int>((n_vecs + a.seg_vecs - 1) / a.seg_vecs);

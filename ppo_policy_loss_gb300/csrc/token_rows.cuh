@@ -22,13 +22,13 @@ namespace {
 // top-k search; from shared memory lane l takes its vectors in the order
 // (j + l / 2) mod 4, which touches every bank once per 8 lanes.
 constexpr int kPieceBytes = 64;
-constexpr int kRowThreads = 256;  // threads that work on a row
+constexpr long long kMaxVocab = 1LL << 26;
 
 // Every logit counts as at least the format's floor when it enters a sum, so
 // that -inf gives 2^x = 0 and 0 * x = 0 instead of NaN.  That is exact while
 // the row's maximum is far above the floor; a row whose maximum is at most
 // kExact (all -inf, or masked with the type's lowest value) is taken again
-// without the floor (exact_row).  With temperature <= 100 the floor's term
+// without the floor (needs_exact).  With temperature <= 100 the floor's term
 // of any other row is 2^-x, x >= (65504 - 32768) log2(e) / 100 > 470: 0.
 constexpr float kRowFloor = -0x1p100f;
 constexpr float kMinTemperature = 0.01f, kMaxTemperature = 100.f;
@@ -62,7 +62,8 @@ __device__ __forceinline__ float unorder32(uint32_t k) {
 }
 
 // Per format: elements per piece, the piece's raw maximum as a key and as a
-// float, clamping at the floor, widening, and single elements.
+// float, taking elements out of it, clamping a word at the floor, widening,
+// and single elements.
 template <int DT>
 struct Fmt;
 
@@ -72,36 +73,53 @@ struct Fmt<RL_F32> {
   static constexpr int kBytes = 4, kPiece = 16, kVec = 4;
   static constexpr float kFloor = kRowFloor, kExact = -0x1p99f;
   static constexpr uint32_t kNegInf2 = 0xff800000u;
-  __device__ static uint32_t raw_max(const uint32_t (&w)[16]) {
-    float m = __uint_as_float(w[0]);
+  // of the piece at w[b .. b + 15]
+  template <int N>
+  __device__ static uint32_t raw_max(const uint32_t (&w)[N], int b) {
+    float m = __uint_as_float(w[b]);
 #pragma unroll
-    for (int i = 1; i < 16; ++i) m = max_nan(m, __uint_as_float(w[i]));
+    for (int i = 1; i < 16; ++i) m = max_nan(m, __uint_as_float(w[b + i]));
     return __float_as_uint(m);
   }
   __device__ static float raw_value(uint32_t r) { return __uint_as_float(r); }
   __device__ static Key raw_key(uint32_t r) { return order32(r); }
   __device__ static uint32_t clamp(uint32_t w) { return __float_as_uint(max_nan(__uint_as_float(w), kFloor)); }
-  // elements e .. 15 of the piece become -inf
-  __device__ static void cut(uint32_t (&w)[16], int e) {
+  // elements e .. 15 of the piece at w[b ..] become -inf
+  template <int N>
+  __device__ static void cut(uint32_t (&w)[N], int b, int e) {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (i >= e) w[i] = kNegInf2;
+      if (i >= e) w[b + i] = kNegInf2;
   }
-  // element e becomes -inf
-  __device__ static void drop(uint32_t (&w)[16], int e) {
+  // element e of the piece becomes the floor
+  template <int N>
+  __device__ static void drop(uint32_t (&w)[N], int b, int e) {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (i == e) w[i] = kNegInf2;
+      if (i == e) w[b + i] = __float_as_uint(kFloor);
   }
-  __device__ static void pair(const uint32_t (&w)[16], int i, float& a, float& b) {
+  // if `take`, the elements of value v become the floor; how many there were
+  template <int N>
+  __device__ static int drop_value(uint32_t (&w)[N], float v, bool take) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool hit = take && __uint_as_float(w[i]) == v;
+      w[i] = hit ? __float_as_uint(kFloor) : w[i];
+      n += hit;
+    }
+    return n;
+  }
+  template <int N>
+  __device__ static void pair(const uint32_t (&w)[N], int i, float& a, float& b) {
     a = __uint_as_float(w[2 * i]);
     b = __uint_as_float(w[2 * i + 1]);
   }
   __device__ static float load(const unsigned char* row, long long i) { return reinterpret_cast<const float*>(row)[i]; }
-  __device__ static Key load_key(const unsigned char* row, long long i) {
+  __device__ static uint32_t load_order(const unsigned char* row, long long i) {
     return order32(reinterpret_cast<const uint32_t*>(row)[i]);
   }
-  __device__ static float key_value(Key k) { return unorder32(k); }
+  __device__ static float order_value(uint32_t k) { return unorder32(k); }
   __device__ static void store(unsigned char* row, long long i, float v) { reinterpret_cast<float*>(row)[i] = v; }
   __device__ static void unpack(const uint4& w, float (&z)[kVec]) {
     z[0] = __uint_as_float(w.x);
@@ -120,42 +138,59 @@ struct Fmt<RL_BF16> {
   static constexpr int kBytes = 2, kPiece = 32, kVec = 8;
   static constexpr float kFloor = kRowFloor, kExact = -0x1p99f;
   static constexpr uint32_t kFloor2 = 0xF180F180u, kNegInf2 = 0xFF80FF80u;
-  __device__ static uint32_t raw_max(const uint32_t (&w)[16]) {
-    uint32_t m = w[0];
+  template <int N>
+  __device__ static uint32_t raw_max(const uint32_t (&w)[N], int b) {
+    uint32_t m = w[b];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) m = pmax_bf16x2(m, w[i]);
+    for (int i = 1; i < 16; ++i) m = pmax_bf16x2(m, w[b + i]);
     return pmax_bf16x2(m, (m >> 16) | (m << 16)) & 0xffffu;
   }
   __device__ static float raw_value(uint32_t r) { return __uint_as_float(r << 16); }
   __device__ static Key raw_key(uint32_t r) { return static_cast<Key>(order16(r, 0x7f80u)); }
   __device__ static uint32_t clamp(uint32_t w) { return pmax_bf16x2(w, kFloor2); }
-  __device__ static void cut(uint32_t (&w)[16], int e) {
+  template <int N>
+  __device__ static void cut(uint32_t (&w)[N], int b, int e) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       if (2 * i >= e)
-        w[i] = kNegInf2;
+        w[b + i] = kNegInf2;
       else if (2 * i + 1 >= e)
-        w[i] = (w[i] & 0xffffu) | (kNegInf2 & 0xffff0000u);
+        w[b + i] = (w[b + i] & 0xffffu) | (kNegInf2 & 0xffff0000u);
     }
   }
-  __device__ static void drop(uint32_t (&w)[16], int e) {
+  template <int N>
+  __device__ static void drop(uint32_t (&w)[N], int b, int e) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      if (2 * i == e) w[i] = (w[i] & 0xffff0000u) | (kNegInf2 & 0xffffu);
-      if (2 * i + 1 == e) w[i] = (w[i] & 0xffffu) | (kNegInf2 & 0xffff0000u);
+      if (2 * i == e) w[b + i] = (w[b + i] & 0xffff0000u) | (kFloor2 & 0xffffu);
+      if (2 * i + 1 == e) w[b + i] = (w[b + i] & 0xffffu) | (kFloor2 & 0xffff0000u);
     }
   }
-  __device__ static void pair(const uint32_t (&w)[16], int i, float& a, float& b) {
+  template <int N>
+  __device__ static int drop_value(uint32_t (&w)[N], float v, bool take) {
+    const uint32_t on = take ? ~0u : 0u;
+    const __nv_bfloat162 v2 = __float2bfloat162_rn(v);
+    uint32_t n2 = 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t hit = __heq2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), v2) & on;
+      w[i] = (w[i] & ~hit) | (kFloor2 & hit);
+      n2 += hit & 0x00010001u;
+    }
+    return static_cast<int>((n2 & 0xffffu) + (n2 >> 16));
+  }
+  template <int N>
+  __device__ static void pair(const uint32_t (&w)[N], int i, float& a, float& b) {
     a = __uint_as_float(w[i] << 16);
     b = __uint_as_float(w[i] & 0xffff0000u);
   }
   __device__ static float load(const unsigned char* row, long long i) {
     return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[i]) << 16);
   }
-  __device__ static Key load_key(const unsigned char* row, long long i) {
-    return static_cast<Key>(order16(reinterpret_cast<const uint16_t*>(row)[i], 0x7f80u));
+  __device__ static uint32_t load_order(const unsigned char* row, long long i) {
+    return order16(reinterpret_cast<const uint16_t*>(row)[i], 0x7f80u);
   }
-  __device__ static float key_value(Key k) { return __uint_as_float(unorder16(k) << 16); }
+  __device__ static float order_value(uint32_t k) { return __uint_as_float(unorder16(k) << 16); }
   __device__ static void store(unsigned char* row, long long i, float v) {
     reinterpret_cast<__nv_bfloat16*>(row)[i] = __float2bfloat16_rn(v);
   }
@@ -184,33 +219,50 @@ struct Fmt<RL_F16> {
   static constexpr int kBytes = 2, kPiece = 32, kVec = 8;
   static constexpr float kFloor = -65504.f, kExact = -32768.f;
   static constexpr uint32_t kFloor2 = 0xFBFFFBFFu, kNegInf2 = 0xFC00FC00u;
-  __device__ static uint32_t raw_max(const uint32_t (&w)[16]) {
-    uint32_t m = w[0];
+  template <int N>
+  __device__ static uint32_t raw_max(const uint32_t (&w)[N], int b) {
+    uint32_t m = w[b];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) m = pmax_f16x2(m, w[i]);
+    for (int i = 1; i < 16; ++i) m = pmax_f16x2(m, w[b + i]);
     return pmax_f16x2(m, (m >> 16) | (m << 16)) & 0xffffu;
   }
   __device__ static float half_bits(uint32_t r) { return __half2float(__ushort_as_half(static_cast<unsigned short>(r))); }
   __device__ static float raw_value(uint32_t r) { return half_bits(r); }
   __device__ static Key raw_key(uint32_t r) { return static_cast<Key>(order16(r, 0x7c00u)); }
   __device__ static uint32_t clamp(uint32_t w) { return pmax_f16x2(w, kFloor2); }
-  __device__ static void cut(uint32_t (&w)[16], int e) {
+  template <int N>
+  __device__ static void cut(uint32_t (&w)[N], int b, int e) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       if (2 * i >= e)
-        w[i] = kNegInf2;
+        w[b + i] = kNegInf2;
       else if (2 * i + 1 >= e)
-        w[i] = (w[i] & 0xffffu) | (kNegInf2 & 0xffff0000u);
+        w[b + i] = (w[b + i] & 0xffffu) | (kNegInf2 & 0xffff0000u);
     }
   }
-  __device__ static void drop(uint32_t (&w)[16], int e) {
+  template <int N>
+  __device__ static void drop(uint32_t (&w)[N], int b, int e) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      if (2 * i == e) w[i] = (w[i] & 0xffff0000u) | (kNegInf2 & 0xffffu);
-      if (2 * i + 1 == e) w[i] = (w[i] & 0xffffu) | (kNegInf2 & 0xffff0000u);
+      if (2 * i == e) w[b + i] = (w[b + i] & 0xffff0000u) | (kFloor2 & 0xffffu);
+      if (2 * i + 1 == e) w[b + i] = (w[b + i] & 0xffffu) | (kFloor2 & 0xffff0000u);
     }
   }
-  __device__ static void pair(const uint32_t (&w)[16], int i, float& a, float& b) {
+  template <int N>
+  __device__ static int drop_value(uint32_t (&w)[N], float v, bool take) {
+    const uint32_t on = take ? ~0u : 0u;
+    const __half2 v2 = __float2half2_rn(v);
+    uint32_t n2 = 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t hit = __heq2_mask(*reinterpret_cast<const __half2*>(&w[i]), v2) & on;
+      w[i] = (w[i] & ~hit) | (kFloor2 & hit);
+      n2 += hit & 0x00010001u;
+    }
+    return static_cast<int>((n2 & 0xffffu) + (n2 >> 16));
+  }
+  template <int N>
+  __device__ static void pair(const uint32_t (&w)[N], int i, float& a, float& b) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
     a = f.x;
     b = f.y;
@@ -218,10 +270,10 @@ struct Fmt<RL_F16> {
   __device__ static float load(const unsigned char* row, long long i) {
     return half_bits(reinterpret_cast<const uint16_t*>(row)[i]);
   }
-  __device__ static Key load_key(const unsigned char* row, long long i) {
-    return static_cast<Key>(order16(reinterpret_cast<const uint16_t*>(row)[i], 0x7c00u));
+  __device__ static uint32_t load_order(const unsigned char* row, long long i) {
+    return order16(reinterpret_cast<const uint16_t*>(row)[i], 0x7c00u);
   }
-  __device__ static float key_value(Key k) { return half_bits(unorder16(k)); }
+  __device__ static float order_value(uint32_t k) { return half_bits(unorder16(k)); }
   __device__ static void store(unsigned char* row, long long i, float v) {
     reinterpret_cast<__half*>(row)[i] = __float2half_rn(v);
   }
@@ -272,64 +324,119 @@ __device__ __forceinline__ RowStats merge_row(RowStats a, RowStats b, float c) {
 }
 
 // A warp's running statistics: m is the warp's, r and t are spread over its
-// lanes (their sums are the warp's r and t).
+// lanes.  The terms are taken in the frame x' = z c + nm, nm = -m c rounded
+// to fp32: one FMA an element, and the rounding that all terms of a frame
+// share (2^rho, rho = -m c - nm) is put right once, when the frame ends.
+// That holds for |m c| <= kFrame, where |rho| <= 2^-4; a row outside it, or
+// with a maximum of at most kExact, is taken again by differences to m.
+constexpr float kFrame = 0x1p20f;
+template <class F>
+__device__ __forceinline__ bool needs_exact(float m, float c) {
+  return !(m > F::kExact) || !(fabsf(m) * c <= kFrame);
+}
 struct WarpStats {
-  float m;
+  float m, nm;
   float2 r, t;
+  float own;  // lane 0: the maximum itself, where the set is not empty (else 0)
+  bool low;   // -inf has been met: clamp what comes
 };
 
-__device__ __forceinline__ void warp_stats_init(WarpStats& a, float floor, int lane) {
-  a.m = floor;
-  a.r = make_float2(lane == 0 ? -1.f : 0.f, 0.f);
+template <class F>
+__device__ __forceinline__ void warp_stats_init(WarpStats& a, float c) {
+  a.m = F::kFloor;
+  a.nm = -F::kFloor * c;
+  a.r = make_float2(0.f, 0.f);
   a.t = make_float2(0.f, 0.f);
+  a.own = 0.f;
 }
 
-// This lane's piece, raw and clamped as warp-wide call: `pm` is the clamped
-// maximum of the lane's piece.  A piece of nothing (all -inf) adds 0.
+// This lane's sums brought from the frame nm to the exact frame of m.
+__device__ __forceinline__ void end_frame(const WarpStats& a, float c, float& r, float& t) {
+  const float rho = fmaf(-a.m, c, -a.nm);  // exact: the product's rounding error
+  const float g = ex2_approx(rho);
+  r = a.r.x + a.r.y;
+  t = fmaf(rho, r, a.t.x + a.t.y) * g;
+  r *= g;
+}
+
+// One step: this lane's piece (raw words), of clamped maximum pm.  Warp-wide.
+// -inf words add 0 to r; their NaN in t (0 * inf) is looked for where `check`
+// says so, and from then on the words are clamped at the floor first.
 template <class F, bool kEntropy>
-__device__ __forceinline__ void add_piece(WarpStats& a, uint32_t (&w)[16], float pm, float c, int lane) {
+__device__ __forceinline__ void add_piece(WarpStats& a, uint32_t (&w)[16], float pm, float c, int lane, bool check) {
   float wm;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(wm) : "f"(pm));
-  const float2 c2 = make_float2(c, c);
-  if (wm > a.m) {  // the warp's maximum rises: rescale, and leave one new maximum out
+  if (wm > a.m) {
+    // the warp's maximum rises: the old frame ends, lane 0 takes the old
+    // maximum back in, and the first lane that holds the new one drops it
+    // (its other elements of that value are terms of exactly 1)
+    float r, t;
+    end_frame(a, c, r, t);
     const float d = (wm - a.m) * c;
     const float f = ex2_approx(-d);
-    const float one = lane == 0 ? 1.f : 0.f;
-    const float s = a.r.x + a.r.y + one;  // lane 0 takes the old maximum back in
-    if (kEntropy) a.t = make_float2(f * fmaf(-d, s, a.t.x + a.t.y), 0.f);
+    const float s = r + a.own;
+    if (kEntropy) a.t = make_float2(f * fmaf(-d, s, t), 0.f);
     a.r = make_float2(f * s, 0.f);
     a.m = wm;
+    a.nm = -wm * c;
+    a.own = lane == 0 ? 1.f : 0.f;
     const uint32_t holders = __ballot_sync(0xffffffffu, pm == wm);
-    bool out = lane == __ffs(holders) - 1;
-    const float2 nm = make_float2(-wm, -wm);
+    const bool take = lane == __ffs(holders) - 1;
+    const int n = F::template drop_value<16>(w, wm, take);
+    a.r.y = take ? static_cast<float>(n - 1) : 0.f;
+  }
+  const float2 c2 = make_float2(c, c), nm2 = make_float2(a.nm, a.nm);
+  const float2 r0 = a.r, t0 = a.t;
+  while (true) {
+    if (kEntropy && a.low) {
 #pragma unroll
-    for (int i = 0; i < F::kPiece / 2; ++i) {
-      float2 z;
-      F::pair(w, i, z.x, z.y);
-      const float2 x = __fmul2_rn(__fadd2_rn(z, nm), c2);
-      float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-      if (out && z.x == wm) {
-        e.x = 0.f;
-        out = false;
-      }
-      if (out && z.y == wm) {
-        e.y = 0.f;
-        out = false;
-      }
-      a.r = __fadd2_rn(a.r, e);
-      if (kEntropy) a.t = __ffma2_rn(e, x, a.t);
+      for (int i = 0; i < 16; ++i) w[i] = F::clamp(w[i]);
     }
-  } else {
-    const float2 nm = make_float2(-a.m, -a.m);
 #pragma unroll
     for (int i = 0; i < F::kPiece / 2; ++i) {
       float2 z;
-      F::pair(w, i, z.x, z.y);
-      const float2 x = __fmul2_rn(__fadd2_rn(z, nm), c2);
+      F::template pair<16>(w, i, z.x, z.y);
+      const float2 x = __ffma2_rn(z, c2, nm2);
       const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
       a.r = __fadd2_rn(a.r, e);
       if (kEntropy) a.t = __ffma2_rn(e, x, a.t);
     }
+    if (!kEntropy || a.low || !check) break;
+    const float t = a.t.x + a.t.y;
+    if (!__any_sync(0xffffffffu, t != t)) break;
+    a.low = true;
+    a.r = r0;
+    a.t = t0;
+  }
+}
+
+// The warp's statistics in every lane.
+template <class F>
+__device__ __forceinline__ RowStats warp_stats_sum(const WarpStats& a, float c) {
+  float r, t;
+  end_frame(a, c, r, t);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    r += __shfl_xor_sync(0xffffffffu, r, o);
+    t += __shfl_xor_sync(0xffffffffu, t, o);
+  }
+  // nothing rose above the floor: no term was left out
+  if (!(a.m > F::kFloor)) r -= 1.f;
+  return RowStats{a.m, r, t};
+}
+
+// A lane's piece from shared memory.  Lanes take their four vectors in the
+// order (j + sh) mod 4; sh = lane / 2 touches every bank once per 8 lanes, sh
+// = 0 keeps the elements in order (a row's last, partly filled piece).
+template <int N>
+__device__ __forceinline__ void load_piece(uint32_t (&w)[N], int b, uint32_t at, int sh) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 v = ld_shared_v4(at + ((j + sh) & 3) * 16);
+    w[b + 4 * j] = v.x;
+    w[b + 4 * j + 1] = v.y;
+    w[b + 4 * j + 2] = v.z;
+    w[b + 4 * j + 3] = v.w;
   }
 }
 
@@ -341,6 +448,62 @@ __device__ __forceinline__ RowStats warp_stats_sum(const WarpStats& a) {
     t += __shfl_xor_sync(0xffffffffu, t, o);
   }
   return RowStats{a.m, r, t};
+}
+
+// ------------------------------------------------------------------ chunk ring
+// Chunks of a row arrive by bulk copies in a ring of shared-memory slots: the
+// producer (one lane) waits for a slot's release and issues the copy, the
+// consumers wait for its arrival, in the same order of chunks.
+template <int kSlots, int kChunk>
+struct Ring {
+  alignas(128) unsigned char data[kSlots][kChunk];
+  unsigned long long full[kSlots], empty[kSlots];
+
+  __device__ void init(int consumer_warps) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(smem_addr(&full[s]), 1);
+      mbar_init(smem_addr(&empty[s]), consumer_warps);
+    }
+  }
+  // producer: chunk number `it` of this CTA; false once a wait has given up
+  __device__ __forceinline__ bool issue(uint32_t it, const unsigned char* src, uint32_t bytes, uint64_t policy,
+                                        volatile int* abort) {
+    const uint32_t slot = it % kSlots, round = it / kSlots;
+    if (round > 0 && !wait_bounded<false>(smem_addr(&empty[slot]), (round - 1) & 1, abort)) return false;
+    const uint32_t fb = smem_addr(&full[slot]);
+    mbar_arrive_expect_tx(fb, bytes);
+    bulk_load(smem_addr(data[slot]), src, bytes, fb, policy);
+    return true;
+  }
+  // producer: the `it` chunks issued so far have landed (before the CTA may exit)
+  __device__ void drain(uint32_t it) {
+    for (uint32_t k = it > kSlots ? it - kSlots : 0; k < it; ++k) {
+      const uint64_t t0 = global_ns();
+      while (!mbar_try_wait(smem_addr(&full[k % kSlots]), (k / kSlots) & 1) && global_ns() - t0 <= kWaitLimitNs) {
+      }
+    }
+  }
+  __device__ __forceinline__ uint32_t wait(uint32_t it, volatile int* abort) {
+    const uint32_t slot = it % kSlots;
+    wait_bounded<false>(smem_addr(&full[slot]), (it / kSlots) & 1, abort);
+    return smem_addr(data[slot]);
+  }
+  // whole warp: the slot's bytes have been read
+  __device__ __forceinline__ void release(uint32_t it, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&empty[it % kSlots]));
+  }
+};
+
+__device__ __forceinline__ uint64_t policy_keep() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+__device__ __forceinline__ uint64_t policy_normal() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
 }
 
 }  // namespace

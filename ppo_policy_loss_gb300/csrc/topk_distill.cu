@@ -17,6 +17,7 @@
 namespace rl {
 namespace {
 
+constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kMaxEntries = RL_TOKEN_MAX_K;
 constexpr int kPerLane = kMaxEntries / 32;
@@ -311,7 +312,8 @@ __global__ void __launch_bounds__(kRowThreads) topk_distill_kernel(const Distill
     const bool has_tail = n_given < V;
     // pass 1: the statistics of every token that is not given
     WarpStats st;
-    warp_stats_init(st, F::kFloor, lane);
+    st.low = false;
+    warp_stats_init<F>(st, a.c);
     for (int p0 = 0; p0 < n_pieces; p0 += kRowThreads) {
       const int p = p0 + tid;
       uint32_t w[16];
@@ -326,28 +328,26 @@ __global__ void __launch_bounds__(kRowThreads) topk_distill_kernel(const Distill
         w[4 * j + 2] = v.z;
         w[4 * j + 3] = v.w;
       }
-      if ((p + 1) * F::kPiece > V) F::cut(w, max(0, V - p * F::kPiece));
+      if ((p + 1) * F::kPiece > V) F::cut(w, 0, max(0, V - p * F::kPiece));
       if (p < n_pieces) {
         for (int j = sm.head[p & (kTable - 1)]; j; j = sm.next[j - 1]) {
           const int e = sm.id[j - 1] - p * F::kPiece;
           if (e >= 0 && e < F::kPiece) {
             sm.z[j - 1] = F::load(src, sm.id[j - 1]);
-            F::drop(w, e);
+            F::drop(w, 0, e);
           }
         }
       }
-      const uint32_t rm = F::raw_max(w);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = F::clamp(w[i]);
-      add_piece<F, false>(st, w, max_nan(F::raw_value(rm), F::kFloor), a.c, lane);
+      const uint32_t rm = F::raw_max(w, 0);
+      add_piece<F, false>(st, w, max_nan(F::raw_value(rm), F::kFloor), a.c, lane, false);
     }
-    const RowStats wst = warp_stats_sum(st);
+    const RowStats wst = warp_stats_sum<F>(st, a.c);
     if (lane == 0) sm.part[warp] = wst;
     __syncthreads();
     RowStats tail = sm.part[0];
 #pragma unroll
     for (int w = 1; w < kRowWarps; ++w) tail = merge_row(tail, sm.part[w], a.c);
-    if (!(tail.m > F::kExact)) tail = exact_tail<F>(src, V, a.c, sm, tid);
+    if (needs_exact<F>(tail.m, a.c)) tail = exact_tail<F>(src, V, a.c, sm, tid);
     if (warp == 0) {
       float lq[kPerLane];
 #pragma unroll
@@ -461,7 +461,7 @@ extern "C" rl_status rl_topk_distill_fwd_bwd(const rl_topk_distill_desc* d, void
   const int es = d->dtype == RL_F32 ? 4 : d->dtype == RL_BF16 || d->dtype == RL_F16 ? 2 : 0;
   if (es == 0 || (d->tail != RL_DISTILL_TAIL_BUCKET && d->tail != RL_DISTILL_TAIL_RENORM)) return RL_ERR_DTYPE;
   const long long R = d->R, V = d->V, ld = d->ld;
-  if (R < 0 || R >= (1LL << 31) || V < 1 || V > (1LL << 30) || ld < V || ld > (1LL << 31)) return RL_ERR_SHAPE;
+  if (R < 0 || R >= (1LL << 31) || V < 1 || V > kMaxVocab || ld < V || ld > (1LL << 31)) return RL_ERR_SHAPE;
   if (d->K < 1 || d->K > RL_TOKEN_MAX_K || !(d->reverse >= 0.f && d->reverse <= 1.f) ||
       !(d->temperature >= kMinTemperature && d->temperature <= kMaxTemperature) || !std::isfinite(d->grad_scale) ||
       !(d->norm >= 0.0) || !std::isfinite(d->norm) || (d->reverse != 0.f && d->tail == RL_DISTILL_TAIL_RENORM))

@@ -55,6 +55,13 @@ CASES = [
     (2, 151936, "f16", 0, 128, 0.5),
     (700, 500, "f32", 3, 1, 1.0),         # more rows than CTAs
     (2, 262144, "bf16", 128, 1, 1.0),
+    (2, 300007, "bf16", 50, 1, 1.0),
+    (1, 1 << 20, "f32", 20, 1, 1.0),      # the longest row that can be searched
+    (160, 300000, "bf16", 20, 1, 1.0),    # rows that need two CTAs, more of them than clusters
+    (70, 40000, "f16", 9, 2, 1.0),        # clusters of 4
+    (39, 20000, "f32", 100, 2, 1.0),
+    (20, 9000, "bf16", 30, 1, 1.0),       # fewer chunks than CTAs of the largest cluster
+    (310, 70000, "bf16", 0, 1, 1.0),
 ]
 
 

@@ -60,10 +60,10 @@ def call_fwd(lib, **over):
     (dict(R=-1), rl.RL_ERR_SHAPE),
     (dict(R=1 << 31), rl.RL_ERR_SHAPE),
     (dict(V=0), rl.RL_ERR_SHAPE),
-    (dict(V=(1 << 30) + 1, ld=(1 << 30) + 8, k=0), rl.RL_ERR_SHAPE),
+    (dict(V=(1 << 26) + 1, ld=(1 << 26) + 8, k=0), rl.RL_ERR_SHAPE),
     (dict(ld=992), rl.RL_ERR_SHAPE),
     (dict(V=3, k=4), rl.RL_ERR_SHAPE),                       # fewer tokens than alternatives
-    (dict(V=(1 << 18) + 8, ld=(1 << 18) + 8), rl.RL_ERR_SHAPE),          # row too long to search
+    (dict(V=(1 << 21) + 8, ld=(1 << 21) + 8), rl.RL_ERR_SHAPE),          # row too long to search
     (dict(k=-1), rl.RL_ERR_ARG),
     (dict(k=129), rl.RL_ERR_ARG),
     (dict(n_ids=-1), rl.RL_ERR_ARG),
