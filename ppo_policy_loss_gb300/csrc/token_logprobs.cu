@@ -211,8 +211,11 @@ struct LpSmem {
     SelSmem<typename C::K> sel;
     SelSmem<ElemKey> join_sel;
   };
+  int pieces[kList];             // fast search: pieces that reach its bound
+  int n_pieces, n_elems;
   alignas(16) typename C::K top[kMaxK];
-  alignas(16) int slots[kMaxK];  // the k pieces with the largest maxima, in the row's order
+  alignas(16) int slots[kMaxK];  // slow search: the k pieces with the largest maxima, in the row's order
+  alignas(16) ElemKey found[kMaxK];  // the CTA's k largest elements, largest first, 0 where there are fewer
   RowStats part[kRowWarps];
   RowStats join_part[kMaxCluster];  // clusters: every slice's statistics, in rank 0's memory
   unsigned long long arrived, freed;  // rank 0: every slice is in; the others: rank 0 has taken the row
@@ -232,6 +235,180 @@ template <class F>
 __host__ __device__ constexpr int key_places(int per, int k) {
   const int elems = (takes_all<F>(per, k) ? per : k) * F::kPiece;
   return k == 0 ? 0 : per > elems ? per : elems;
+}
+
+__device__ __forceinline__ ElemKey elem_key(uint32_t order, int e) {
+  return (static_cast<ElemKey>(order) << 32) | (0xffffffffu - static_cast<uint32_t>(e));
+}
+
+// How many of the threads' two maxima reach `bound` (all consumer threads).
+__device__ __forceinline__ int count_reaching(const uint32_t (&best)[2], uint32_t bound, bool both) {
+  int n;
+  const uint32_t top = best[0] > best[1] ? best[0] : best[1];
+  const uint32_t first = both ? best[0] : top;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ge.u32 p, %1, %2;\n\tbar.red.popc.u32 %0, 1, %3, p;\n\t}"
+      : "=r"(n)
+      : "r"(first), "r"(bound), "n"(kRowThreads)
+      : "memory");
+  if (both) {
+    int n1;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ge.u32 p, %1, %2;\n\tbar.red.popc.u32 %0, 1, %3, p;\n\t}"
+        : "=r"(n1)
+        : "r"(best[1]), "r"(bound), "n"(kRowThreads)
+        : "memory");
+    n += n1;
+  }
+  return n;
+}
+
+// The k largest elements of the CTA's pieces into sm.found.  `best`: the
+// largest piece orders this thread met in its even and odd steps.  A bound
+// that at least k of these maxima reach, and not many more, is found from the
+// row's maximum downwards in widening steps; at least k elements reach it
+// then, nearly all of them in pieces of their own, so the pieces that reach
+// it are listed, their elements read again (from L2), and those that reach it
+// ranked by counting.  False if a list overflows (many equal values, or a
+// large k of few pieces): search_slow then.
+template <int DT>
+__device__ __forceinline__ bool search_fast(LpSmem<DT>& sm, const typename Fmt<DT>::Key* keys, const unsigned char* src,
+                                            int g0, int n_mine, int V, int k, const uint32_t (&best)[2], uint32_t top,
+                                            int tid) {
+  using F = Fmt<DT>;
+  const int lane = tid & 31, warp = tid >> 5;
+  const bool both = k > 32;
+  const int enough = k + k / 8 + 4;
+  if (tid == 0) sm.n_pieces = sm.n_elems = 0;
+  if (tid < k) sm.found[tid] = 0;
+  uint32_t hi = top + 1, lo = 1;  // fewer than k reach hi, unless NaN does
+  int n = 0;
+  for (uint32_t step = F::kOrderStep;; step *= 4) {
+    const uint32_t mid = hi > step && step < 0x40000000u ? hi - step : 1u;
+    n = count_reaching(best, mid, both);
+    if (n >= k || mid == 1u) {
+      lo = mid;
+      break;
+    }
+    hi = mid;
+  }
+  while (n > enough && hi - lo > 1) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    const int m = count_reaching(best, mid, both);
+    if (m >= k) {
+      lo = mid;
+      n = m;
+    } else {
+      hi = mid;
+    }
+  }
+  // loads first, eight in flight, then one counter update a thread and batch
+  if (best[0] >= lo || best[1] >= lo) {
+    for (int p0 = tid; p0 < n_mine; p0 += 8 * kRowThreads) {
+      uint32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int p = p0 + j * kRowThreads;
+        v[j] = keys[min(p, n_mine - 1)];
+        if (p >= n_mine) v[j] = 0;
+      }
+      int hits = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) hits += v[j] >= lo;
+      if (hits) {
+        int at = atomicAdd(&sm.n_pieces, hits);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (v[j] >= lo) {
+            if (at < kList) sm.pieces[at] = g0 + p0 + j * kRowThreads;
+            ++at;
+          }
+      }
+    }
+  }
+  row_barrier();
+  const int n_pieces = sm.n_pieces;
+  if (n_pieces > kList) return false;
+  // a piece's elements in consecutive lanes
+  constexpr int kPer = 32 / F::kPiece;  // pieces a warp reads at once
+  for (int q0 = warp * kPer + lane / F::kPiece; q0 < n_pieces; q0 += 8 * kRowWarps * kPer) {
+    typename F::Raw raw[8];
+    int e[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int q = q0 + j * kRowWarps * kPer;
+      e[j] = sm.pieces[min(q, n_pieces - 1)] * F::kPiece + lane % F::kPiece;
+      raw[j] = F::load_raw(src, min(e[j], V - 1));
+      if (q >= n_pieces) e[j] = V;
+    }
+    uint32_t v[8];
+    int hits = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = e[j] < V ? F::raw_order(raw[j]) : 0u;
+      hits += v[j] >= lo;
+    }
+    if (hits) {
+      int at = atomicAdd(&sm.n_elems, hits);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (v[j] >= lo) {
+          if (at < kList) sm.join_sel.b[at] = elem_key(v[j], e[j]);
+          ++at;
+        }
+    }
+  }
+  row_barrier();
+  const int n_elems = sm.n_elems;
+  if (n_elems > kList) return false;
+  if (tid < 2) sm.join_sel.b[n_elems + tid] = 0;  // what rank_of reads past the list
+  row_barrier();
+  for (int q = tid; q < n_elems; q += kRowThreads) {
+    const ElemKey key = sm.join_sel.b[q];
+    const int r = rank_of(sm.join_sel.b, n_elems, key);
+    if (r < k) sm.found[r] = key;
+  }
+  row_barrier();
+  return true;
+}
+
+// The same by two exact searches: the k pieces with the largest maxima (the
+// lower piece first among equals) hold the k largest elements.
+template <int DT>
+__device__ __noinline__ void search_slow(LpSmem<DT>& sm, typename Fmt<DT>::Key* keys, const unsigned char* src, int g0,
+                                         int n_mine, int V, int per, int k, int tid) {
+  using F = Fmt<DT>;
+  using C = PlaceKey<typename F::Key>;
+  int n_slots = n_mine;
+  const bool all = takes_all<F>(per, k);
+  auto element = [&](int i) {  // the row's element at place i of the key array
+    return (g0 + (all ? i / F::kPiece : sm.slots[i / F::kPiece])) * F::kPiece + i % F::kPiece;
+  };
+  auto key_at = [&](int i) { return C::make(keys[i], i); };
+  row_barrier();
+  if (!all) {
+    block_select<typename C::K>(key_at, n_mine, k, sm.top, sm.sel, tid);
+    n_slots = min(k, n_mine);
+    if (tid < n_slots) {  // back into the row's order
+      const int g = C::at(sm.top[tid]);
+      int r = 0;
+      for (int j = 0; j < n_slots; ++j) r += C::at(sm.top[j]) < g;
+      sm.slots[r] = g;
+    }
+    row_barrier();
+  }
+  const int n_elems = n_slots * F::kPiece;
+  for (int i = tid; i < n_elems; i += kRowThreads) {
+    const int e = element(i);
+    keys[i] = e < V ? static_cast<typename F::Key>(F::load_order(src, e)) : typename F::Key(0);
+  }
+  row_barrier();
+  block_select<typename C::K>(key_at, n_elems, k, sm.top, sm.sel, tid);
+  if (tid < k) {
+    const typename C::K key = sm.top[tid];
+    sm.found[tid] = key ? elem_key(C::value(key), element(C::at(key))) : 0;
+  }
+  row_barrier();
 }
 
 // The statistics of a row that needs_exact names, by differences to its
@@ -359,14 +536,17 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
   } else {
     // ---------------------------------------------------------------- consumers
     const int k = a.k, n_ids = a.n_ids, n_mine = g1 - g0;
+    const int n_full = min(n_mine, V / F::kPiece - g0) / kRowThreads;  // steps whose every piece is a full one
     unsigned int err = 0;
     uint32_t it = 0, done = 0;  // chunks taken, rows done
     RowBits rows;
     WarpStats st;
     st.low = false;
     int row_i = 0;
+    long long y_next = rank == 0 && tid < n_ids && first < a.R ? a.ids[first * n_ids + tid] : -1;
     for (long long row = first; row < a.R; row += stride, ++row_i) {
       if (!rows.valid(a, first, stride, row_i, lane)) {
+        if (rank == 0 && tid < n_ids && row + stride < a.R) y_next = a.ids[(row + stride) * n_ids + tid];
         if (rank == 0) {
           for (int q = tid; q < n_ids; q += kRowThreads) a.logp[row * n_ids + q] = 0.f;
           for (int q = tid; q < k; q += kRowThreads) {
@@ -379,35 +559,34 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
         continue;
       }
       const unsigned char* src = a.logits + row * a.row_bytes;
-      long long y = -1;
+      const long long y = y_next;
       float zy = 0.f;
       if (rank == 0 && tid < n_ids) {
-        y = a.ids[row * n_ids + tid];
         if (y >= 0 && y < V) zy = F::load(src, y);
+        if (row + stride < a.R) y_next = a.ids[(row + stride) * n_ids + tid];  // in flight during this row
       }
+      uint32_t best[2] = {0u, 0u};
       warp_stats_init<F>(st, a.c);
       for (int i = 0; i < n_chunks; ++i, ++it) {
         const uint32_t buf = sm.ring.wait(it, abort);
-        const int w0 = i * kRowThreads + warp * 32;  // the warp's first piece in the slice
-        const int here = n_mine - w0;                // pieces from there to its end
-        if (here > 0) {
-          uint32_t w[16];
-          // a warp that reaches the row's end takes the elements in order
-          const bool ragged = (g0 + w0 + 32) * F::kPiece > V;
-          load_piece(w, 0, buf + tid * kPieceBytes, ragged ? 0 : lane >> 1);
-          sm.ring.release(it, lane);
-          const bool part = here < 32 || ragged;
-          if (part) F::cut(w, 0, lane < here ? min(F::kPiece, V - (g0 + w0 + lane) * F::kPiece) : 0);
-          const uint32_t rm = F::raw_max(w, 0);
-          if (k && lane < here) keys[w0 + lane] = F::raw_key(rm);
-          if (part) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = F::clamp(w[j]);
-          }
-          add_piece<F, kEntropy>(st, w, max_nan(F::raw_value(rm), F::kFloor), a.c, lane, row_i == 0);
-        } else {
-          sm.ring.release(it, lane);
+        const int at = i * kRowThreads + tid;  // this lane's piece in the slice
+        const bool last = i >= n_full;         // a step that reaches the slice's or the row's end
+        uint32_t w[16];
+        load_piece(w, 0, buf + tid * kPieceBytes, last ? 0 : lane >> 1);
+        sm.ring.release(it, lane);
+        if (last) F::cut(w, 0, at < n_mine ? min(F::kPiece, V - (g0 + at) * F::kPiece) : 0);
+        const uint32_t rm = F::raw_max(w, 0);
+        if (k && at < n_mine) {
+          const typename F::Key key = F::raw_key(rm);
+          keys[at] = key;
+          best[0] = max(best[0], i & 1 ? 0u : static_cast<uint32_t>(key));
+          best[1] = max(best[1], i & 1 ? static_cast<uint32_t>(key) : 0u);
         }
+        if (last) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) w[j] = F::clamp(w[j]);
+        }
+        add_piece<F, kEntropy>(st, w, max_nan(F::raw_value(rm), F::kFloor), a.c, lane, row_i == 0);
       }
       const RowStats ws = warp_stats_sum<F>(st, a.c);
       if (lane == 0) sm.part[warp] = ws;
@@ -417,54 +596,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
       for (int w = 1; w < kRowWarps; ++w) rs = merge_row(rs, sm.part[w], a.c);
       // a NaN in t is a NaN logit or a first -inf: clamp from the next row on
       if (kEntropy) st.low = st.low || rs.t != rs.t;
-      // this CTA's k largest: the k pieces with the largest maxima hold them
-      int n_slots = n_mine;
-      const bool all = takes_all<F>(per, k);
-      auto element = [&](int i) {  // the row's element at place i of the key array
-        return (g0 + (all ? i / F::kPiece : sm.slots[i / F::kPiece])) * F::kPiece + i % F::kPiece;
-      };
-      auto key_at = [&](int i) { return C::make(keys[i], i); };
-      if (k) {
-        if (!all) {
-          block_select<typename C::K>(key_at, n_mine, k, sm.top, sm.sel, tid);
-          n_slots = min(k, n_mine);
-          if (tid < n_slots) {  // back into the row's order
-            const int g = C::at(sm.top[tid]);
-            int r = 0;
-            for (int j = 0; j < n_slots; ++j) r += C::at(sm.top[j]) < g;
-            sm.slots[r] = g;
-          }
-          row_barrier();
-        }
-        const int n_elems = n_slots * F::kPiece;
-        for (int base = tid; base < n_elems; base += 8 * kRowThreads) {
-          typename F::Key v[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int i = base + j * kRowThreads;
-            v[j] = 0;
-            if (i < n_elems) {
-              const int e = element(i);
-              if (e < V) v[j] = static_cast<typename F::Key>(F::load_order(src, e));
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (base + j * kRowThreads < n_elems) keys[base + j * kRowThreads] = v[j];
-        }
-        row_barrier();
-        block_select<typename C::K>(key_at, n_elems, k, sm.top, sm.sel, tid);
-      }
+      if (k && !search_fast<DT>(sm, keys, src, g0, n_mine, V, k, best, F::order_of(rs.m), tid))
+        search_slow<DT>(sm, keys, src, g0, n_mine, V, per, k, tid);
       if (csize > 1) {
         // every CTA's findings into rank 0's memory
         if (done > 0 && rank != 0) wait_bounded<true>(smem_addr(&sm.freed), (done - 1) & 1, abort);
-        if (tid < k) {
-          const typename C::K key = sm.top[tid];
-          ElemKey u = 0;
-          if (key)
-            u = (static_cast<ElemKey>(C::value(key)) << 32) | (0xffffffffu - static_cast<uint32_t>(element(C::at(key))));
-          st_cluster_u64(map_to_rank(smem_addr(&join_keys[rank * kMaxK + tid]), 0), u);
-        }
+        if (tid < k) st_cluster_u64(map_to_rank(smem_addr(&join_keys[rank * kMaxK + tid]), 0), sm.found[tid]);
         if (tid == 0) {
           const uint32_t to = map_to_rank(smem_addr(&sm.join_part[rank]), 0);
           st_cluster_f32(to, rs.m);
@@ -500,19 +637,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
           a.entropy[row] = rs.m > -INFINITY ? fmaf(-kLn2, rs.t / (1.f + rs.r), log_s) : __int_as_float(0x7fc00000);
       }
       if (tid < k) {
-        long long id;
-        uint32_t order;
-        if (csize > 1) {
-          const ElemKey key = join_top[tid];
-          id = 0xffffffffu - static_cast<uint32_t>(key);
-          order = static_cast<uint32_t>(key >> 32);
-        } else {
-          const typename C::K key = sm.top[tid];
-          id = element(C::at(key));
-          order = C::value(key);
-        }
-        a.topk_ids[row * k + tid] = id;
-        a.topk_logp[row * k + tid] = fmaf(F::order_value(order) - rs.m, a.inv_temp, -log_s);
+        const ElemKey key = csize > 1 ? join_top[tid] : sm.found[tid];
+        a.topk_ids[row * k + tid] = 0xffffffffu - static_cast<uint32_t>(key);
+        a.topk_logp[row * k + tid] = fmaf(F::order_value(static_cast<uint32_t>(key >> 32)) - rs.m, a.inv_temp, -log_s);
       }
       row_barrier();  // the shared arrays are free for the next row
     }

@@ -76,10 +76,12 @@ struct Fmt<RL_F32> {
   // of the piece at w[b .. b + 15]
   template <int N>
   __device__ static uint32_t raw_max(const uint32_t (&w)[N], int b) {
-    float m = __uint_as_float(w[b]);
+    float m[4];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) m = max_nan(m, __uint_as_float(w[b + i]));
-    return __float_as_uint(m);
+    for (int j = 0; j < 4; ++j)  // four chains
+      m[j] = max_nan(max_nan(__uint_as_float(w[b + j]), __uint_as_float(w[b + 4 + j])),
+                     max_nan(__uint_as_float(w[b + 8 + j]), __uint_as_float(w[b + 12 + j])));
+    return __float_as_uint(max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3])));
   }
   __device__ static float raw_value(uint32_t r) { return __uint_as_float(r); }
   __device__ static Key raw_key(uint32_t r) { return order32(r); }
@@ -116,10 +118,13 @@ struct Fmt<RL_F32> {
     b = __uint_as_float(w[2 * i + 1]);
   }
   __device__ static float load(const unsigned char* row, long long i) { return reinterpret_cast<const float*>(row)[i]; }
-  __device__ static uint32_t load_order(const unsigned char* row, long long i) {
-    return order32(reinterpret_cast<const uint32_t*>(row)[i]);
-  }
+  using Raw = uint32_t;
+  __device__ static Raw load_raw(const unsigned char* row, long long i) { return reinterpret_cast<const Raw*>(row)[i]; }
+  __device__ static uint32_t raw_order(Raw r) { return order32(r); }
+  __device__ static uint32_t load_order(const unsigned char* row, long long i) { return raw_order(load_raw(row, i)); }
   __device__ static float order_value(uint32_t k) { return unorder32(k); }
+  __device__ static uint32_t order_of(float v) { return order32(__float_as_uint(v)); }
+  static constexpr uint32_t kOrderStep = 8u << 16;  // a few bf16 steps
   __device__ static void store(unsigned char* row, long long i, float v) { reinterpret_cast<float*>(row)[i] = v; }
   __device__ static void unpack(const uint4& w, float (&z)[kVec]) {
     z[0] = __uint_as_float(w.x);
@@ -140,9 +145,11 @@ struct Fmt<RL_BF16> {
   static constexpr uint32_t kFloor2 = 0xF180F180u, kNegInf2 = 0xFF80FF80u;
   template <int N>
   __device__ static uint32_t raw_max(const uint32_t (&w)[N], int b) {
-    uint32_t m = w[b];
+    uint32_t c[4];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) m = pmax_bf16x2(m, w[b + i]);
+    for (int j = 0; j < 4; ++j)  // four chains
+      c[j] = pmax_bf16x2(pmax_bf16x2(w[b + j], w[b + 4 + j]), pmax_bf16x2(w[b + 8 + j], w[b + 12 + j]));
+    const uint32_t m = pmax_bf16x2(pmax_bf16x2(c[0], c[1]), pmax_bf16x2(c[2], c[3]));
     return pmax_bf16x2(m, (m >> 16) | (m << 16)) & 0xffffu;
   }
   __device__ static float raw_value(uint32_t r) { return __uint_as_float(r << 16); }
@@ -187,10 +194,13 @@ struct Fmt<RL_BF16> {
   __device__ static float load(const unsigned char* row, long long i) {
     return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[i]) << 16);
   }
-  __device__ static uint32_t load_order(const unsigned char* row, long long i) {
-    return order16(reinterpret_cast<const uint16_t*>(row)[i], 0x7f80u);
-  }
+  using Raw = uint16_t;
+  __device__ static Raw load_raw(const unsigned char* row, long long i) { return reinterpret_cast<const Raw*>(row)[i]; }
+  __device__ static uint32_t raw_order(Raw r) { return order16(r, 0x7f80u); }
+  __device__ static uint32_t load_order(const unsigned char* row, long long i) { return raw_order(load_raw(row, i)); }
   __device__ static float order_value(uint32_t k) { return __uint_as_float(unorder16(k) << 16); }
+  __device__ static uint32_t order_of(float v) { return order16(__float_as_uint(v) >> 16, 0x7f80u); }
+  static constexpr uint32_t kOrderStep = 8u;
   __device__ static void store(unsigned char* row, long long i, float v) {
     reinterpret_cast<__nv_bfloat16*>(row)[i] = __float2bfloat16_rn(v);
   }
@@ -221,9 +231,11 @@ struct Fmt<RL_F16> {
   static constexpr uint32_t kFloor2 = 0xFBFFFBFFu, kNegInf2 = 0xFC00FC00u;
   template <int N>
   __device__ static uint32_t raw_max(const uint32_t (&w)[N], int b) {
-    uint32_t m = w[b];
+    uint32_t c[4];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) m = pmax_f16x2(m, w[b + i]);
+    for (int j = 0; j < 4; ++j)  // four chains
+      c[j] = pmax_f16x2(pmax_f16x2(w[b + j], w[b + 4 + j]), pmax_f16x2(w[b + 8 + j], w[b + 12 + j]));
+    const uint32_t m = pmax_f16x2(pmax_f16x2(c[0], c[1]), pmax_f16x2(c[2], c[3]));
     return pmax_f16x2(m, (m >> 16) | (m << 16)) & 0xffffu;
   }
   __device__ static float half_bits(uint32_t r) { return __half2float(__ushort_as_half(static_cast<unsigned short>(r))); }
@@ -270,10 +282,13 @@ struct Fmt<RL_F16> {
   __device__ static float load(const unsigned char* row, long long i) {
     return half_bits(reinterpret_cast<const uint16_t*>(row)[i]);
   }
-  __device__ static uint32_t load_order(const unsigned char* row, long long i) {
-    return order16(reinterpret_cast<const uint16_t*>(row)[i], 0x7c00u);
-  }
+  using Raw = uint16_t;
+  __device__ static Raw load_raw(const unsigned char* row, long long i) { return reinterpret_cast<const Raw*>(row)[i]; }
+  __device__ static uint32_t raw_order(Raw r) { return order16(r, 0x7c00u); }
+  __device__ static uint32_t load_order(const unsigned char* row, long long i) { return raw_order(load_raw(row, i)); }
   __device__ static float order_value(uint32_t k) { return half_bits(unorder16(k)); }
+  __device__ static uint32_t order_of(float v) { return order16(__half_as_ushort(__float2half_rn(v)), 0x7c00u); }
+  static constexpr uint32_t kOrderStep = 32u;
   __device__ static void store(unsigned char* row, long long i, float v) {
     reinterpret_cast<__half*>(row)[i] = __float2half_rn(v);
   }
@@ -336,7 +351,7 @@ __device__ __forceinline__ bool needs_exact(float m, float c) {
 }
 struct WarpStats {
   float m, nm;
-  float2 r, t;
+  float2 r[2], t[2];  // independent chains
   float own;  // lane 0: the maximum itself, where the set is not empty (else 0)
   bool low;   // -inf has been met: clamp what comes
 };
@@ -345,8 +360,8 @@ template <class F>
 __device__ __forceinline__ void warp_stats_init(WarpStats& a, float c) {
   a.m = F::kFloor;
   a.nm = -F::kFloor * c;
-  a.r = make_float2(0.f, 0.f);
-  a.t = make_float2(0.f, 0.f);
+  a.r[0] = a.r[1] = make_float2(0.f, 0.f);
+  a.t[0] = a.t[1] = make_float2(0.f, 0.f);
   a.own = 0.f;
 }
 
@@ -354,8 +369,8 @@ __device__ __forceinline__ void warp_stats_init(WarpStats& a, float c) {
 __device__ __forceinline__ void end_frame(const WarpStats& a, float c, float& r, float& t) {
   const float rho = fmaf(-a.m, c, -a.nm);  // exact: the product's rounding error
   const float g = ex2_approx(rho);
-  r = a.r.x + a.r.y;
-  t = fmaf(rho, r, a.t.x + a.t.y) * g;
+  r = (a.r[0].x + a.r[0].y) + (a.r[1].x + a.r[1].y);
+  t = fmaf(rho, r, (a.t[0].x + a.t[0].y) + (a.t[1].x + a.t[1].y)) * g;
   r *= g;
 }
 
@@ -375,38 +390,43 @@ __device__ __forceinline__ void add_piece(WarpStats& a, uint32_t (&w)[16], float
     const float d = (wm - a.m) * c;
     const float f = ex2_approx(-d);
     const float s = r + a.own;
-    if (kEntropy) a.t = make_float2(f * fmaf(-d, s, t), 0.f);
-    a.r = make_float2(f * s, 0.f);
+    a.t[0] = make_float2(kEntropy ? f * fmaf(-d, s, t) : 0.f, 0.f);
+    a.t[1] = make_float2(0.f, 0.f);
+    a.r[1] = make_float2(0.f, 0.f);
     a.m = wm;
     a.nm = -wm * c;
     a.own = lane == 0 ? 1.f : 0.f;
     const uint32_t holders = __ballot_sync(0xffffffffu, pm == wm);
     const bool take = lane == __ffs(holders) - 1;
     const int n = F::template drop_value<16>(w, wm, take);
-    a.r.y = take ? static_cast<float>(n - 1) : 0.f;
+    a.r[0] = make_float2(f * s, take ? static_cast<float>(n - 1) : 0.f);
   }
   const float2 c2 = make_float2(c, c), nm2 = make_float2(a.nm, a.nm);
-  const float2 r0 = a.r, t0 = a.t;
-  while (true) {
-    if (kEntropy && a.low) {
+  if (kEntropy && a.low) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = F::clamp(w[i]);
-    }
+    for (int i = 0; i < 16; ++i) w[i] = F::clamp(w[i]);
+  }
+  const float2 r0 = a.r[0], r1 = a.r[1], t0 = a.t[0], t1 = a.t[1];
+  while (true) {
 #pragma unroll
     for (int i = 0; i < F::kPiece / 2; ++i) {
       float2 z;
       F::template pair<16>(w, i, z.x, z.y);
       const float2 x = __ffma2_rn(z, c2, nm2);
       const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-      a.r = __fadd2_rn(a.r, e);
-      if (kEntropy) a.t = __ffma2_rn(e, x, a.t);
+      a.r[i & 1] = __fadd2_rn(a.r[i & 1], e);
+      if (kEntropy) a.t[i & 1] = __ffma2_rn(e, x, a.t[i & 1]);
     }
-    if (!kEntropy || a.low || !check) break;
-    const float t = a.t.x + a.t.y;
+    if (!kEntropy || !check || a.low) break;
+    const float t = (a.t[0].x + a.t[0].y) + (a.t[1].x + a.t[1].y);
     if (!__any_sync(0xffffffffu, t != t)) break;
     a.low = true;
-    a.r = r0;
-    a.t = t0;
+    a.r[0] = r0;
+    a.r[1] = r1;
+    a.t[0] = t0;
+    a.t[1] = t1;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = F::clamp(w[i]);
   }
 }
 
@@ -438,16 +458,6 @@ __device__ __forceinline__ void load_piece(uint32_t (&w)[N], int b, uint32_t at,
     w[b + 4 * j + 2] = v.z;
     w[b + 4 * j + 3] = v.w;
   }
-}
-
-__device__ __forceinline__ RowStats warp_stats_sum(const WarpStats& a) {
-  float r = a.r.x + a.r.y, t = a.t.x + a.t.y;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    r += __shfl_xor_sync(0xffffffffu, r, o);
-    t += __shfl_xor_sync(0xffffffffu, t, o);
-  }
-  return RowStats{a.m, r, t};
 }
 
 // ------------------------------------------------------------------ chunk ring
