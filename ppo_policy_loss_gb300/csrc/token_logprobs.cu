@@ -207,6 +207,7 @@ struct LpSmem {
   using F = Fmt<DT>;
   using C = PlaceKey<typename F::Key>;
   Ring<kSlots, kChunk> ring;
+  long long row_of[kSlots];  // the row a chunk belongs to
   union {  // one search at a time
     SelSmem<typename C::K> sel;
     SelSmem<ElemKey> join_sel;
@@ -302,60 +303,45 @@ __device__ __forceinline__ bool search_fast(LpSmem<DT>& sm, const typename Fmt<D
       hi = mid;
     }
   }
-  // loads first, eight in flight, then one counter update a thread and batch
-  if (best[0] >= lo || best[1] >= lo) {
-    for (int p0 = tid; p0 < n_mine; p0 += 8 * kRowThreads) {
-      uint32_t v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int p = p0 + j * kRowThreads;
-        v[j] = keys[min(p, n_mine - 1)];
-        if (p >= n_mine) v[j] = 0;
-      }
-      int hits = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) hits += v[j] >= lo;
-      if (hits) {
-        int at = atomicAdd(&sm.n_pieces, hits);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (v[j] >= lo) {
-            if (at < kList) sm.pieces[at] = g0 + p0 + j * kRowThreads;
-            ++at;
-          }
+  // a vector of keys, or of a piece's elements, a lane at a time; hits are few
+  const float thr = F::order_value(lo);  // of lo = 1 a NaN: everything passes
+  const uint4* kv = reinterpret_cast<const uint4*>(keys);
+  for (int q = tid; q * F::kVec < n_mine; q += kRowThreads) {
+    uint32_t hits = F::hits(kv[q], thr);
+    while (hits) {
+      const int p = q * F::kVec + F::hit_elem(__ffs(hits) - 1);
+      hits &= hits - 1;
+      if (p < n_mine) {
+        const int at = atomicAdd(&sm.n_pieces, 1);
+        if (at < kList) sm.pieces[at] = g0 + p;
       }
     }
   }
   row_barrier();
   const int n_pieces = sm.n_pieces;
   if (n_pieces > kList) return false;
-  // a piece's elements in consecutive lanes
-  constexpr int kPer = 32 / F::kPiece;  // pieces a warp reads at once
-  for (int q0 = warp * kPer + lane / F::kPiece; q0 < n_pieces; q0 += 8 * kRowWarps * kPer) {
-    typename F::Raw raw[8];
-    int e[8];
+  const long long row_vecs = (static_cast<long long>(V) * F::kBytes + 15) / 16;
+  for (int q0 = tid; q0 < n_pieces * 4; q0 += 4 * kRowThreads) {
+    uint4 v[4];
+    int e[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int q = q0 + j * kRowWarps * kPer;
-      e[j] = sm.pieces[min(q, n_pieces - 1)] * F::kPiece + lane % F::kPiece;
-      raw[j] = F::load_raw(src, min(e[j], V - 1));
-      if (q >= n_pieces) e[j] = V;
+    for (int j = 0; j < 4; ++j) {
+      const int q = q0 + j * kRowThreads;
+      const int vec = sm.pieces[min(q >> 2, n_pieces - 1)] * 4 + (q & 3);
+      e[j] = q < n_pieces * 4 ? vec * F::kVec : V;
+      v[j] = *reinterpret_cast<const uint4*>(src + min(static_cast<long long>(vec), row_vecs - 1) * 16);
     }
-    uint32_t v[8];
-    int hits = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = e[j] < V ? F::raw_order(raw[j]) : 0u;
-      hits += v[j] >= lo;
-    }
-    if (hits) {
-      int at = atomicAdd(&sm.n_elems, hits);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (v[j] >= lo) {
-          if (at < kList) sm.join_sel.b[at] = elem_key(v[j], e[j]);
-          ++at;
+    for (int j = 0; j < 4; ++j) {
+      uint32_t hits = e[j] < V ? F::hits(v[j], thr) : 0u;
+      while (hits) {
+        const int i = F::hit_elem(__ffs(hits) - 1);
+        hits &= hits - 1;
+        if (e[j] + i < V) {
+          const int at = atomicAdd(&sm.n_elems, 1);
+          if (at < kList) sm.join_sel.b[at] = elem_key(F::raw_order(static_cast<typename F::Raw>(F::pick(v[j], i))), e[j] + i);
         }
+      }
     }
   }
   row_barrier();
@@ -385,6 +371,8 @@ __device__ __noinline__ void search_slow(LpSmem<DT>& sm, typename Fmt<DT>::Key* 
     return (g0 + (all ? i / F::kPiece : sm.slots[i / F::kPiece])) * F::kPiece + i % F::kPiece;
   };
   auto key_at = [&](int i) { return C::make(keys[i], i); };
+  row_barrier();
+  for (int i = tid; i < n_mine; i += kRowThreads) keys[i] = static_cast<typename F::Key>(F::raw_order(keys[i]));
   row_barrier();
   if (!all) {
     block_select<typename C::K>(key_at, n_mine, k, sm.top, sm.sel, tid);
@@ -460,17 +448,63 @@ __device__ __noinline__ RowStats exact_row(const unsigned char* row, int V, floa
   return RowStats{m, s - 1.f, t};
 }
 
-// The rows first, first + stride, ... of a CTA, with their mask bits: one
-// ballot for 32 of them.  Whole warp.
-struct RowBits {
-  uint32_t bits;
-  __device__ __forceinline__ bool valid(const LpArgs& a, long long first, long long stride, int i, int lane) {
-    if (!a.mask) return true;
-    if ((i & 31) == 0) {
-      const long long r = first + (i + lane) * stride;
-      bits = __ballot_sync(0xffffffffu, r < a.R && a.mask[r] != 0);
+// The valid rows number first, first + stride, ... of the batch, so that every
+// CTA gets the same share of them wherever the masked rows lie.  The mask is
+// read 512 rows at a time.  Whole warp.
+struct ValidRows {
+  long long want;           // number of the next row among the valid ones
+  long long base, before;   // first row of the window, valid rows before it
+  uint32_t bits, prefix;    // this lane's 16 rows, valid rows of the window before them
+  int total;                // valid rows of the window
+  __device__ ValidRows(const LpArgs& a, long long first, int lane) : want(first), base(0), before(0) {
+    if (a.mask) load(a, lane);
+  }
+  __device__ __forceinline__ void load(const LpArgs& a, int lane) {
+    const long long r = base + lane * 16;
+    bits = 0u;
+    if (r + 16 <= a.R && ((reinterpret_cast<uintptr_t>(a.mask) + r) & 15) == 0) {
+      const uint4 v = *reinterpret_cast<const uint4*>(a.mask + r);
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) bits |= ((u[j] >> (8 * q)) & 0xffu) ? 1u << (4 * j + q) : 0u;
+    } else {
+      for (int q = 0; q < 16; ++q)
+        if (r + q < a.R && a.mask[r + q]) bits |= 1u << q;
     }
-    return (bits >> (i & 31)) & 1u;
+    uint32_t n = __popc(bits);
+    prefix = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, prefix, o);
+      if (lane >= o) prefix += up;
+    }
+    total = __shfl_sync(0xffffffffu, prefix, 31);
+    prefix -= n;
+  }
+  // the next row, -1 after the last
+  __device__ __forceinline__ long long next(const LpArgs& a, long long stride, int lane) {
+    long long row = -1;
+    if (!a.mask) {
+      if (want < a.R) row = want;
+    } else {
+      while (want >= before + total && base + 512 < a.R) {
+        before += total;
+        base += 512;
+        load(a, lane);
+      }
+      if (want < before + total) {
+        const uint32_t at = static_cast<uint32_t>(want - before);
+        const bool here = at >= prefix && at < prefix + __popc(bits);
+        const uint32_t who = __ballot_sync(0xffffffffu, here);
+        const uint32_t bit = here ? __fns(bits, 0, static_cast<int>(at - prefix) + 1) : 0u;
+        const int l = __ffs(who) - 1;
+        row = base + l * 16 + __shfl_sync(0xffffffffu, bit, l);
+      }
+    }
+    want += stride;
+    return row;
   }
 };
 
@@ -514,58 +548,63 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
 
   if (warp == kRowWarps) {
     // ---------------------------------------------------------------- producer
+    // The row of a chunk goes with it; a chunk of no bytes and row -1 is the end.
     const uint64_t pol = policy_normal();
     uint32_t it = 0;
     bool ok = true;
-    RowBits rows;
-    int i = 0;
-    for (long long row = first; row < a.R && ok; row += stride, ++i) {
-      if (!rows.valid(a, first, stride, i, lane)) continue;
+    ValidRows rows(a, first, lane);
+    while (ok) {
+      const long long row = rows.next(a, stride, lane);
       if (lane == 0) {
         const unsigned char* src = a.logits + row * a.row_bytes + b0;
-        for (int q = 0; q < n_chunks && ok; ++q) {
+        const int n = row < 0 ? 1 : n_chunks;
+        for (int q = 0; q < n && ok; ++q) {
           const long long off = static_cast<long long>(q) * kChunk;
-          ok = sm.ring.issue(it, src + off, static_cast<uint32_t>(min(static_cast<long long>(kChunk), n_bytes - off)),
-                             pol, abort);
-          it += ok;
+          const uint32_t slot = it % kSlots;
+          ok = sm.ring.reserve(it, abort);
+          if (!ok) break;
+          sm.row_of[slot] = row;
+          if (row < 0)
+            mbar_arrive(smem_addr(&sm.ring.full[slot]));
+          else
+            sm.ring.fill(it, src + off, static_cast<uint32_t>(min(static_cast<long long>(kChunk), n_bytes - off)), pol);
+          ++it;
         }
         if (!ok) sm.ring.drain(it);
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ok = __shfl_sync(0xffffffffu, ok, 0) && row >= 0;
     }
   } else {
     // ---------------------------------------------------------------- consumers
     const int k = a.k, n_ids = a.n_ids, n_mine = g1 - g0;
     const int n_full = min(n_mine, V / F::kPiece - g0) / kRowThreads;  // steps whose every piece is a full one
+    if (a.mask && rank == 0) {  // masked rows
+      for (long long row = first + tid * stride; row < a.R; row += kRowThreads * stride) {
+        if (a.mask[row]) continue;
+        for (int q = 0; q < n_ids; ++q) a.logp[row * n_ids + q] = 0.f;
+        for (int q = 0; q < k; ++q) {
+          a.topk_ids[row * k + q] = -1;
+          a.topk_logp[row * k + q] = 0.f;
+        }
+        if (a.entropy) a.entropy[row] = 0.f;
+        if (a.lse) a.lse[row] = 0.f;
+      }
+    }
     unsigned int err = 0;
-    uint32_t it = 0, done = 0;  // chunks taken, rows done
-    RowBits rows;
+    uint32_t it = 0;  // chunks taken
     WarpStats st;
     st.low = false;
-    int row_i = 0;
-    long long y_next = rank == 0 && tid < n_ids && first < a.R ? a.ids[first * n_ids + tid] : -1;
-    for (long long row = first; row < a.R; row += stride, ++row_i) {
-      if (!rows.valid(a, first, stride, row_i, lane)) {
-        if (rank == 0 && tid < n_ids && row + stride < a.R) y_next = a.ids[(row + stride) * n_ids + tid];
-        if (rank == 0) {
-          for (int q = tid; q < n_ids; q += kRowThreads) a.logp[row * n_ids + q] = 0.f;
-          for (int q = tid; q < k; q += kRowThreads) {
-            a.topk_ids[row * k + q] = -1;
-            a.topk_logp[row * k + q] = 0.f;
-          }
-          if (tid == 0 && a.entropy) a.entropy[row] = 0.f;
-          if (tid == 0 && a.lse) a.lse[row] = 0.f;
-        }
-        continue;
-      }
+    for (uint32_t done = 0;; ++done) {  // rows done
+      // the row's first chunk brings its number; the barrier also frees the
+      // shared arrays of the row before.  After a timeout every thread stops here.
+      sm.ring.wait(it, abort);
+      const long long row = sm.row_of[it % kSlots];
+      if (named_barrier_or(1, kRowThreads, row < 0 || *abort)) break;
       const unsigned char* src = a.logits + row * a.row_bytes;
-      const long long y = y_next;
+      const long long y = rank == 0 && tid < n_ids ? a.ids[row * n_ids + tid] : -1;
+      const bool y_ok = y >= 0 && y < V;
       float zy = 0.f;
-      if (rank == 0 && tid < n_ids) {
-        if (y >= 0 && y < V) zy = F::load(src, y);
-        if (row + stride < a.R) y_next = a.ids[(row + stride) * n_ids + tid];  // in flight during this row
-      }
-      uint32_t best[2] = {0u, 0u};
+      float best[2] = {-INFINITY, -INFINITY};
       warp_stats_init<F>(st, a.c);
       for (int i = 0; i < n_chunks; ++i, ++it) {
         const uint32_t buf = sm.ring.wait(it, abort);
@@ -577,17 +616,19 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
         if (last) F::cut(w, 0, at < n_mine ? min(F::kPiece, V - (g0 + at) * F::kPiece) : 0);
         const uint32_t rm = F::raw_max(w, 0);
         if (k && at < n_mine) {
-          const typename F::Key key = F::raw_key(rm);
-          keys[at] = key;
-          best[0] = max(best[0], i & 1 ? 0u : static_cast<uint32_t>(key));
-          best[1] = max(best[1], i & 1 ? static_cast<uint32_t>(key) : 0u);
+          keys[at] = static_cast<typename F::Key>(rm);
+          const float v = max_nan(i & 1 ? best[1] : best[0], F::raw_value(rm));
+          best[0] = i & 1 ? best[0] : v;
+          best[1] = i & 1 ? v : best[1];
         }
+        if (i == 1 && y_ok) zy = F::load(src, y);  // its id has arrived by now
         if (last) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) w[j] = F::clamp(w[j]);
         }
-        add_piece<F, kEntropy>(st, w, max_nan(F::raw_value(rm), F::kFloor), a.c, lane, row_i == 0);
+        add_piece<F, kEntropy>(st, w, max_nan(F::raw_value(rm), F::kFloor), a.c, lane, done == 0);
       }
+      if (n_chunks < 2 && y_ok) zy = F::load(src, y);
       const RowStats ws = warp_stats_sum<F>(st, a.c);
       if (lane == 0) sm.part[warp] = ws;
       row_barrier();
@@ -596,8 +637,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
       for (int w = 1; w < kRowWarps; ++w) rs = merge_row(rs, sm.part[w], a.c);
       // a NaN in t is a NaN logit or a first -inf: clamp from the next row on
       if (kEntropy) st.low = st.low || rs.t != rs.t;
-      if (k && !search_fast<DT>(sm, keys, src, g0, n_mine, V, k, best, F::order_of(rs.m), tid))
-        search_slow<DT>(sm, keys, src, g0, n_mine, V, per, k, tid);
+      if (k) {
+        const uint32_t order[2] = {tid < n_mine ? F::order_of(best[0]) : 0u,
+                                   tid + kRowThreads < n_mine ? F::order_of(best[1]) : 0u};
+        if (!search_fast<DT>(sm, keys, src, g0, n_mine, V, k, order, F::order_of(rs.m), tid))
+          search_slow<DT>(sm, keys, src, g0, n_mine, V, per, k, tid);
+      }
       if (csize > 1) {
         // every CTA's findings into rank 0's memory
         if (done > 0 && rank != 0) wait_bounded<true>(smem_addr(&sm.freed), (done - 1) & 1, abort);
@@ -621,15 +666,13 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
           row_barrier();  // everything has been read: the others may send the next row
           if (tid > 0 && tid < csize) mbar_arrive_remote(map_to_rank(smem_addr(&sm.freed), tid));
         }
-        ++done;
         if (rank != 0) continue;
       }
       if (needs_exact<F>(rs.m, a.c) || (kEntropy && rs.t != rs.t)) rs = exact_row<F>(src, V, a.c, sm.part, tid);
       const float log_s = log1pf(rs.r);
       if (tid < n_ids) {
-        const bool ok = y >= 0 && y < V;
-        if (!ok) err |= RL_DEVERR_ID_RANGE;
-        a.logp[row * n_ids + tid] = ok ? fmaf(zy - rs.m, a.inv_temp, -log_s) : __int_as_float(0x7fc00000);
+        if (!y_ok) err |= RL_DEVERR_ID_RANGE;
+        a.logp[row * n_ids + tid] = y_ok ? fmaf(zy - rs.m, a.inv_temp, -log_s) : __int_as_float(0x7fc00000);
       }
       if (tid == 0) {
         if (a.lse) a.lse[row] = fmaf(rs.m, a.inv_temp, log_s);
@@ -641,7 +684,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
         a.topk_ids[row * k + tid] = 0xffffffffu - static_cast<uint32_t>(key);
         a.topk_logp[row * k + tid] = fmaf(F::order_value(static_cast<uint32_t>(key >> 32)) - rs.m, a.inv_temp, -log_s);
       }
-      row_barrier();  // the shared arrays are free for the next row
     }
     if (err && a.status) atomicOr(a.status, err);
   }
@@ -797,8 +839,9 @@ rl_status launch_fwd(const LpArgs& a, int dev, int sms, cudaStream_t stream) {
   while (a.k > 0 && c < kMaxCluster && (n_pieces + c - 1) / c > kMaxPieces) c *= 2;
   const int places = key_places<F>(static_cast<int>((n_pieces + c - 1) / c), a.k);
   constexpr int join_bytes = kJoinKeys * static_cast<int>(sizeof(ElemKey));
-  const int smem = static_cast<int>(sizeof(LpSmem<DT>) + places * sizeof(typename F::Key)) + (c > 1 && a.k ? join_bytes : 0);
-  constexpr int most_smem = static_cast<int>(sizeof(LpSmem<DT>) + kMaxPieces * sizeof(typename F::Key)) + join_bytes;
+  // (keys are read a vector at a time: 16 bytes past the last)
+  const int smem = static_cast<int>(sizeof(LpSmem<DT>) + places * sizeof(typename F::Key)) + 16 + (c > 1 && a.k ? join_bytes : 0);
+  constexpr int most_smem = static_cast<int>(sizeof(LpSmem<DT>) + kMaxPieces * sizeof(typename F::Key)) + 16 + join_bytes;
   const rl_status st = allow_smem(fn, dev, most_smem);
   if (st != RL_OK) return st;
   int held = kSmemPerSm / (smem + 1024);  // CTAs a SM holds at once (1 KB each is the system's)

@@ -118,6 +118,13 @@ struct Fmt<RL_F32> {
     b = __uint_as_float(w[2 * i + 1]);
   }
   __device__ static float load(const unsigned char* row, long long i) { return reinterpret_cast<const float*>(row)[i]; }
+  // elements of a vector that are not below thr (NaN is not), as bits; hit_elem: which element a bit is
+  __device__ static uint32_t hits(const uint4& v, float thr) {
+    return (!(__uint_as_float(v.x) < thr) ? 1u : 0u) | (!(__uint_as_float(v.y) < thr) ? 2u : 0u) |
+           (!(__uint_as_float(v.z) < thr) ? 4u : 0u) | (!(__uint_as_float(v.w) < thr) ? 8u : 0u);
+  }
+  __device__ static int hit_elem(int bit) { return bit; }
+  __device__ static uint32_t pick(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
   using Raw = uint32_t;
   __device__ static Raw load_raw(const unsigned char* row, long long i) { return reinterpret_cast<const Raw*>(row)[i]; }
   __device__ static uint32_t raw_order(Raw r) { return order32(r); }
@@ -193,6 +200,20 @@ struct Fmt<RL_BF16> {
   }
   __device__ static float load(const unsigned char* row, long long i) {
     return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[i]) << 16);
+  }
+  __device__ static uint32_t hits(const uint4& v, float thr) {
+    const __nv_bfloat162 t2 = __float2bfloat162_rn(thr);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    uint32_t b = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      b |= (__hgeu2_mask(*reinterpret_cast<const __nv_bfloat162*>(&u[j]), t2) & 0x00010001u) << j;
+    return b;
+  }
+  __device__ static int hit_elem(int bit) { return 2 * (bit & 15) + (bit >> 4); }
+  __device__ static uint32_t pick(const uint4& v, int i) {
+    const uint32_t w = i < 4 ? (i < 2 ? v.x : v.y) : (i < 6 ? v.z : v.w);
+    return (i & 1) ? w >> 16 : w & 0xffffu;
   }
   using Raw = uint16_t;
   __device__ static Raw load_raw(const unsigned char* row, long long i) { return reinterpret_cast<const Raw*>(row)[i]; }
@@ -281,6 +302,20 @@ struct Fmt<RL_F16> {
   }
   __device__ static float load(const unsigned char* row, long long i) {
     return half_bits(reinterpret_cast<const uint16_t*>(row)[i]);
+  }
+  __device__ static uint32_t hits(const uint4& v, float thr) {
+    const __half2 t2 = __float2half2_rn(thr);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    uint32_t b = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      b |= (__hgeu2_mask(*reinterpret_cast<const __half2*>(&u[j]), t2) & 0x00010001u) << j;
+    return b;
+  }
+  __device__ static int hit_elem(int bit) { return 2 * (bit & 15) + (bit >> 4); }
+  __device__ static uint32_t pick(const uint4& v, int i) {
+    const uint32_t w = i < 4 ? (i < 2 ? v.x : v.y) : (i < 6 ? v.z : v.w);
+    return (i & 1) ? w >> 16 : w & 0xffffu;
   }
   using Raw = uint16_t;
   __device__ static Raw load_raw(const unsigned char* row, long long i) { return reinterpret_cast<const Raw*>(row)[i]; }
@@ -475,15 +510,15 @@ struct Ring {
       mbar_init(smem_addr(&empty[s]), consumer_warps);
     }
   }
-  // producer: chunk number `it` of this CTA; false once a wait has given up
-  __device__ __forceinline__ bool issue(uint32_t it, const unsigned char* src, uint32_t bytes, uint64_t policy,
-                                        volatile int* abort) {
+  // producer: chunk number `it` of this CTA has a free slot; false once a wait has given up
+  __device__ __forceinline__ bool reserve(uint32_t it, volatile int* abort) {
     const uint32_t slot = it % kSlots, round = it / kSlots;
-    if (round > 0 && !wait_bounded<false>(smem_addr(&empty[slot]), (round - 1) & 1, abort)) return false;
-    const uint32_t fb = smem_addr(&full[slot]);
+    return round == 0 || wait_bounded<false>(smem_addr(&empty[slot]), (round - 1) & 1, abort);
+  }
+  __device__ __forceinline__ void fill(uint32_t it, const unsigned char* src, uint32_t bytes, uint64_t policy) {
+    const uint32_t fb = smem_addr(&full[it % kSlots]);
     mbar_arrive_expect_tx(fb, bytes);
-    bulk_load(smem_addr(data[slot]), src, bytes, fb, policy);
-    return true;
+    bulk_load(smem_addr(data[it % kSlots]), src, bytes, fb, policy);
   }
   // producer: the `it` chunks issued so far have landed (before the CTA may exit)
   __device__ void drain(uint32_t it) {
