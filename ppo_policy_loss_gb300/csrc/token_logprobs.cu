@@ -448,66 +448,6 @@ __device__ __noinline__ RowStats exact_row(const unsigned char* row, int V, floa
   return RowStats{m, s - 1.f, t};
 }
 
-// The valid rows number first, first + stride, ... of the batch, so that every
-// CTA gets the same share of them wherever the masked rows lie.  The mask is
-// read 512 rows at a time.  Whole warp.
-struct ValidRows {
-  long long want;           // number of the next row among the valid ones
-  long long base, before;   // first row of the window, valid rows before it
-  uint32_t bits, prefix;    // this lane's 16 rows, valid rows of the window before them
-  int total;                // valid rows of the window
-  __device__ ValidRows(const LpArgs& a, long long first, int lane) : want(first), base(0), before(0) {
-    if (a.mask) load(a, lane);
-  }
-  __device__ __forceinline__ void load(const LpArgs& a, int lane) {
-    const long long r = base + lane * 16;
-    bits = 0u;
-    if (r + 16 <= a.R && ((reinterpret_cast<uintptr_t>(a.mask) + r) & 15) == 0) {
-      const uint4 v = *reinterpret_cast<const uint4*>(a.mask + r);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) bits |= ((u[j] >> (8 * q)) & 0xffu) ? 1u << (4 * j + q) : 0u;
-    } else {
-      for (int q = 0; q < 16; ++q)
-        if (r + q < a.R && a.mask[r + q]) bits |= 1u << q;
-    }
-    uint32_t n = __popc(bits);
-    prefix = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t up = __shfl_up_sync(0xffffffffu, prefix, o);
-      if (lane >= o) prefix += up;
-    }
-    total = __shfl_sync(0xffffffffu, prefix, 31);
-    prefix -= n;
-  }
-  // the next row, -1 after the last
-  __device__ __forceinline__ long long next(const LpArgs& a, long long stride, int lane) {
-    long long row = -1;
-    if (!a.mask) {
-      if (want < a.R) row = want;
-    } else {
-      while (want >= before + total && base + 512 < a.R) {
-        before += total;
-        base += 512;
-        load(a, lane);
-      }
-      if (want < before + total) {
-        const uint32_t at = static_cast<uint32_t>(want - before);
-        const bool here = at >= prefix && at < prefix + __popc(bits);
-        const uint32_t who = __ballot_sync(0xffffffffu, here);
-        const uint32_t bit = here ? __fns(bits, 0, static_cast<int>(at - prefix) + 1) : 0u;
-        const int l = __ffs(who) - 1;
-        row = base + l * 16 + __shfl_sync(0xffffffffu, bit, l);
-      }
-    }
-    want += stride;
-    return row;
-  }
-};
-
 // A CTA (or, for few rows, a cluster of up to 8, each with a slice of the
 // row's pieces) takes a row at a time.  The producer warp streams the valid
 // rows' chunks through the ring; the consumers keep one key per piece (its
@@ -552,9 +492,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
     const uint64_t pol = policy_normal();
     uint32_t it = 0;
     bool ok = true;
-    ValidRows rows(a, first, lane);
+    RowsOf<true> rows(a.mask, a.R, first, lane);
     while (ok) {
-      const long long row = rows.next(a, stride, lane);
+      const long long row = rows.next(stride, lane);
       if (lane == 0) {
         const unsigned char* src = a.logits + row * a.row_bytes + b0;
         const int n = row < 0 ? 1 : n_chunks;

@@ -24,13 +24,13 @@ namespace {
 constexpr int kPieceBytes = 64;
 constexpr long long kMaxVocab = 1LL << 26;
 
-// Every logit counts as at least the format's floor when it enters a sum, so
-// that -inf gives 2^x = 0 and 0 * x = 0 instead of NaN.  That is exact while
-// the row's maximum is far above the floor; a row whose maximum is at most
-// kExact (all -inf, or masked with the type's lowest value) is taken again
-// without the floor (needs_exact).  With temperature <= 100 the floor's term
-// of any other row is 2^-x, x >= (65504 - 32768) log2(e) / 100 > 470: 0.
-constexpr float kRowFloor = -0x1p100f;
+// Every logit counts as at least the format's floor where a maximum or an
+// entropy is formed, so that -inf, and the large negative numbers that masks
+// write, give 2^x = 0 and 0 * x = 0 instead of NaN.  That is exact while the
+// row's maximum is far above the floor; a row whose maximum is at most kExact
+// is taken again without the floor (needs_exact).  In any other row a floor
+// element's term is 2^-x with x >= min(32768 - 16384, 65504 - 32768)
+// log2(e) / 100 > 236: 0 in fp32.
 constexpr float kMinTemperature = 0.01f, kMaxTemperature = 100.f;
 
 __device__ __forceinline__ uint32_t pmax_bf16x2(uint32_t a, uint32_t b) {
@@ -71,7 +71,7 @@ template <>
 struct Fmt<RL_F32> {
   using Key = uint32_t;
   static constexpr int kBytes = 4, kPiece = 16, kVec = 4;
-  static constexpr float kFloor = kRowFloor, kExact = -0x1p99f;
+  static constexpr float kFloor = -32768.f, kExact = -16384.f;
   static constexpr uint32_t kNegInf2 = 0xff800000u;
   // of the piece at w[b .. b + 15]
   template <int N>
@@ -132,6 +132,7 @@ struct Fmt<RL_F32> {
   __device__ static float order_value(uint32_t k) { return unorder32(k); }
   __device__ static uint32_t order_of(float v) { return order32(__float_as_uint(v)); }
   static constexpr uint32_t kOrderStep = 8u << 16;  // a few bf16 steps
+  __device__ static float load_shared(const unsigned char* piece, int e) { return reinterpret_cast<const float*>(piece)[e]; }
   __device__ static void store(unsigned char* row, long long i, float v) { reinterpret_cast<float*>(row)[i] = v; }
   __device__ static void unpack(const uint4& w, float (&z)[kVec]) {
     z[0] = __uint_as_float(w.x);
@@ -148,8 +149,8 @@ template <>
 struct Fmt<RL_BF16> {
   using Key = uint16_t;
   static constexpr int kBytes = 2, kPiece = 32, kVec = 8;
-  static constexpr float kFloor = kRowFloor, kExact = -0x1p99f;
-  static constexpr uint32_t kFloor2 = 0xF180F180u, kNegInf2 = 0xFF80FF80u;
+  static constexpr float kFloor = -32768.f, kExact = -16384.f;
+  static constexpr uint32_t kFloor2 = 0xC700C700u, kNegInf2 = 0xFF80FF80u;
   template <int N>
   __device__ static uint32_t raw_max(const uint32_t (&w)[N], int b) {
     uint32_t c[4];
@@ -222,6 +223,7 @@ struct Fmt<RL_BF16> {
   __device__ static float order_value(uint32_t k) { return __uint_as_float(unorder16(k) << 16); }
   __device__ static uint32_t order_of(float v) { return order16(__float_as_uint(v) >> 16, 0x7f80u); }
   static constexpr uint32_t kOrderStep = 8u;
+  __device__ static float load_shared(const unsigned char* piece, int e) { return load(piece, e); }
   __device__ static void store(unsigned char* row, long long i, float v) {
     reinterpret_cast<__nv_bfloat16*>(row)[i] = __float2bfloat16_rn(v);
   }
@@ -324,6 +326,7 @@ struct Fmt<RL_F16> {
   __device__ static float order_value(uint32_t k) { return half_bits(unorder16(k)); }
   __device__ static uint32_t order_of(float v) { return order16(__half_as_ushort(__float2half_rn(v)), 0x7c00u); }
   static constexpr uint32_t kOrderStep = 32u;
+  __device__ static float load_shared(const unsigned char* piece, int e) { return load(piece, e); }
   __device__ static void store(unsigned char* row, long long i, float v) {
     reinterpret_cast<__half*>(row)[i] = __float2half_rn(v);
   }
@@ -377,9 +380,11 @@ __device__ __forceinline__ RowStats merge_row(RowStats a, RowStats b, float c) {
 // lanes.  The terms are taken in the frame x' = z c + nm, nm = -m c rounded
 // to fp32: one FMA an element, and the rounding that all terms of a frame
 // share (2^rho, rho = -m c - nm) is put right once, when the frame ends.
-// That holds for |m c| <= kFrame, where |rho| <= 2^-4; a row outside it, or
-// with a maximum of at most kExact, is taken again by differences to m.
-constexpr float kFrame = 0x1p20f;
+// That holds for |m c| <= kFrame, where |rho| <= 1/2: every frame between the
+// floor (65504 * 144.3 < kFrame at the lowest temperature) and such a maximum.
+// A row with a larger maximum, or one of at most kExact, is taken again by
+// differences to m.
+constexpr float kFrame = 0x1p24f;
 template <class F>
 __device__ __forceinline__ bool needs_exact(float m, float c) {
   return !(m > F::kExact) || !(fabsf(m) * c <= kFrame);
@@ -425,16 +430,19 @@ __device__ __forceinline__ void add_piece(WarpStats& a, uint32_t (&w)[16], float
     const float d = (wm - a.m) * c;
     const float f = ex2_approx(-d);
     const float s = r + a.own;
-    a.t[0] = make_float2(kEntropy ? f * fmaf(-d, s, t) : 0.f, 0.f);
-    a.t[1] = make_float2(0.f, 0.f);
-    a.r[1] = make_float2(0.f, 0.f);
     a.m = wm;
     a.nm = -wm * c;
     a.own = lane == 0 ? 1.f : 0.f;
     const uint32_t holders = __ballot_sync(0xffffffffu, pm == wm);
     const bool take = lane == __ffs(holders) - 1;
     const int n = F::template drop_value<16>(w, wm, take);
-    a.r[0] = make_float2(f * s, take ? static_cast<float>(n - 1) : 0.f);
+    // what goes on into the new frame: 2^-rho of it, x' = x - rho
+    const float rho = fmaf(-wm, c, -a.nm), h = ex2_approx(-rho);
+    const float kept = fmaf(f, s, take ? static_cast<float>(n - 1) : 0.f);
+    a.r[0] = make_float2(h * kept, 0.f);
+    a.r[1] = make_float2(0.f, 0.f);
+    a.t[0] = make_float2(kEntropy ? h * fmaf(-rho, kept, f * fmaf(-d, s, t)) : 0.f, 0.f);
+    a.t[1] = make_float2(0.f, 0.f);
   }
   const float2 c2 = make_float2(c, c), nm2 = make_float2(a.nm, a.nm);
   if (kEntropy && a.low) {
@@ -494,6 +502,73 @@ __device__ __forceinline__ void load_piece(uint32_t (&w)[N], int b, uint32_t at,
     w[b + 4 * j + 3] = v.w;
   }
 }
+
+// ------------------------------------------------------------------ rows
+// The valid (kValid) or the masked rows number first, first + stride, ... of the
+// batch, so that every CTA gets the same share of them wherever the masked rows
+// lie.  The mask is read 512 rows at a time; no mask: every row is valid.
+// Whole warp.
+template <bool kValid>
+struct RowsOf {
+  const unsigned char* mask;
+  long long R;
+  long long want;           // number of the next row among those
+  long long base, before;   // first row of the window, such rows before it
+  uint32_t bits, prefix;    // this lane's 16 rows, such rows of the window before them
+  int total;                // such rows of the window
+  __device__ RowsOf(const unsigned char* mask_, long long R_, long long first, int lane)
+      : mask(mask_), R(R_), want(first), base(0), before(0), bits(0u), prefix(0u), total(0) {
+    if (mask) load(lane);
+  }
+  __device__ __forceinline__ void load(int lane) {
+    const long long r = base + lane * 16;
+    bits = 0u;
+    if (r + 16 <= R && ((reinterpret_cast<uintptr_t>(mask) + r) & 15) == 0) {
+      const uint4 v = *reinterpret_cast<const uint4*>(mask + r);
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) bits |= ((u[j] >> (8 * q)) & 0xffu) ? 1u << (4 * j + q) : 0u;
+    } else {
+      for (int q = 0; q < 16; ++q)
+        if (r + q < R && mask[r + q]) bits |= 1u << q;
+    }
+    if (!kValid) bits = ~bits & (r + 16 <= R ? 0xffffu : r < R ? (1u << (R - r)) - 1u : 0u);
+    const uint32_t n = __popc(bits);
+    prefix = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, prefix, o);
+      if (lane >= o) prefix += up;
+    }
+    total = __shfl_sync(0xffffffffu, prefix, 31);
+    prefix -= n;
+  }
+  // the next row, -1 after the last
+  __device__ __forceinline__ long long next(long long stride, int lane) {
+    long long row = -1;
+    if (!mask) {
+      if (kValid && want < R) row = want;
+    } else {
+      while (want >= before + total && base + 512 < R) {
+        before += total;
+        base += 512;
+        load(lane);
+      }
+      if (want < before + total) {
+        const uint32_t at = static_cast<uint32_t>(want - before);
+        const bool here = at >= prefix && at < prefix + __popc(bits);
+        const uint32_t who = __ballot_sync(0xffffffffu, here);
+        const uint32_t bit = here ? __fns(bits, 0, static_cast<int>(at - prefix) + 1) : 0u;
+        const int l = __ffs(who) - 1;
+        row = base + l * 16 + __shfl_sync(0xffffffffu, bit, l);
+      }
+    }
+    want += stride;
+    return row;
+  }
+};
 
 // ------------------------------------------------------------------ chunk ring
 // Chunks of a row arrive by bulk copies in a ring of shared-memory slots: the

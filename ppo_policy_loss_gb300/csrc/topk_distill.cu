@@ -9,16 +9,29 @@
 // equal numbers.  The K logits and the tail then give the loss, one factor for
 // every token of the tail and one value for each given token; pass 2 writes
 // p_v times the factor, and the given tokens' values are stored over it.
+//
+//   * A CTA takes a row at a time.  The producer warp streams its chunks
+//     through a ring of shared-memory slots twice: the first load keeps its L2
+//     lines (evict-last), the second takes them from L2 (evict-first), so the
+//     logits cross the HBM bus once.
+//   * The consumer warps run pass 1 (one 64-byte piece a thread and chunk) and
+//     pass 2 (16-byte vectors, streaming stores) without a barrier of their
+//     own.
+//   * The row warp fills the table with the next row's entries, turns the
+//     consumers' partial statistics into the row's loss and gradient values,
+//     and stores the given tokens' gradients once the consumers have written
+//     the row.
 #include <cmath>
 #include <cstring>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "token_rows.cuh"
 
 namespace rl {
 namespace {
 
-constexpr int kRowThreads = 256;
-constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kMaxEntries = RL_TOKEN_MAX_K;
 constexpr int kPerLane = kMaxEntries / 32;
 constexpr int kTable = 4096;  // pieces that share a place of the table differ by a multiple of this
@@ -44,49 +57,59 @@ struct DistillArgs {
   int K, renorm;
 };
 
+// kThreads consumers; a chunk is one piece of each.
+template <int kThreads>
 struct DistillSmem {
+  static constexpr int kWarps = kThreads / 32, kChunk = kThreads * kPieceBytes;
+  static constexpr int kSlots = kThreads >= 512 ? 6 : 4;
+  Ring<kSlots, kChunk> ring;
+  long long row_of[kSlots];    // the row a chunk belongs to
   int head[kTable];            // 1 + the last entry whose piece falls on this place, 0 none
   int next[kMaxEntries];       // the entry before it there
   int id[kMaxEntries];         // -1: empty
   float z[kMaxEntries];        // the entry's logit
-  float d[kMaxEntries];        // the entry's gradient
-  RowStats part[kRowWarps];
-  long long wcount[kRowWarps];
+  RowStats part[kWarps];
+  float nan[kWarps];           // not 0: the warp met a NaN
+  long long wcount[kWarps + 2];
+  unsigned long long table, sums, values, written;  // once a row: table filled, sums in, values out, row written
   float m, factor;             // pass 2: dz = 2^((z - m) c) factor
-  int bad, is_last;
+  int plain;                   // pass 2 by differences to m
+  int abort;
 };
 
 // The entry at element e, or -1.
-__device__ __forceinline__ int entry_at(const DistillSmem& sm, int e, int piece) {
+template <class S>
+__device__ __forceinline__ int entry_at(const S& sm, int e, int piece) {
   for (int j = sm.head[piece & (kTable - 1)]; j; j = sm.next[j - 1])
     if (sm.id[j - 1] == e) return j - 1;
   return -1;
 }
 
-// A row whose maximum is at most kExact (all -inf, or at the type's lowest):
-// the tail's statistics without the floor.  Rare, so it reads the row again.
-template <class F>
-__device__ __noinline__ RowStats exact_tail(const unsigned char* row, int V, float c, DistillSmem& sm, int tid) {
+// The tail's statistics by differences to its maximum (needs_exact).  Rare, so
+// one warp reads the row again.
+template <class F, class S>
+__device__ __noinline__ RowStats exact_tail(const unsigned char* row, int V, float c, const S& sm, int lane) {
+  const int n_vecs = (V + F::kVec - 1) / F::kVec;
+  auto each = [&](auto f) {
+#pragma unroll 4
+    for (int v = lane; v < n_vecs; v += 32) {
+      float z[F::kVec];
+      F::unpack(*reinterpret_cast<const uint4*>(row + static_cast<long long>(v) * 16), z);
+#pragma unroll
+      for (int i = 0; i < F::kVec; ++i) {
+        const int e = v * F::kVec + i;
+        if (e < V && entry_at(sm, e, e / F::kPiece) < 0) f(z[i]);
+      }
+    }
+  };
   float m = -INFINITY;
-  for (int i = tid; i < V; i += kRowThreads)
-    if (entry_at(sm, i, i / F::kPiece) < 0) m = max_nan(m, F::load(row, i));
+  each([&](float z) { m = max_nan(m, z); });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  __syncthreads();
-  if ((tid & 31) == 0) sm.part[tid >> 5].m = m;
-  __syncthreads();
-  for (int w = 0; w < kRowWarps; ++w) m = max_nan(m, sm.part[w].m);
-  __syncthreads();
   float s = 0.f;
-  if (m > -INFINITY)
-    for (int i = tid; i < V; i += kRowThreads)
-      if (entry_at(sm, i, i / F::kPiece) < 0) s += ex2_approx((F::load(row, i) - m) * c);
+  if (m > -INFINITY) each([&](float z) { s += ex2_approx((z - m) * c); });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if ((tid & 31) == 0) sm.part[tid >> 5].r = s;
-  __syncthreads();
-  s = 0.f;
-  for (int w = 0; w < kRowWarps; ++w) s += sm.part[w].r;
   return RowStats{m, s - 1.f, 0.f};
 }
 
@@ -106,23 +129,31 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// A row's teacher entries, four a lane.
+struct Entries {
+  int id[kPerLane];      // -1: none
+  float lq[kPerLane];
+  float d[kPerLane];     // the given tokens' gradients, once known
+  bool bad;              // an id out of range or named twice
+};
+
 struct RowSums {
   double loss, fwd, rev, qt, pt;
+  float m, factor;
 };
 
 // One warp: a row's loss terms and gradient values from the entries' logits
-// (sm.z), the teacher's entries and the tail's statistics.
-__device__ __forceinline__ RowSums row_values(const DistillArgs& a, DistillSmem& sm, RowStats tail, bool has_tail,
-                                              const float (&lq_in)[kPerLane], float w, float s, int lane) {
+// (z), the teacher's entries and the tail's statistics.
+__device__ __forceinline__ RowSums row_values(const DistillArgs& a, Entries& en, const float* z_of, RowStats tail,
+                                              bool has_tail, bool nan, float w, float s, int lane) {
   float lq[kPerLane], q[kPerLane], z[kPerLane];
   bool given[kPerLane];
   int n = 0;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
-    const int j = lane + 32 * i;
-    given[i] = j < a.K && sm.id[j] >= 0;
-    z[i] = given[i] ? sm.z[j] : -INFINITY;
-    lq[i] = given[i] ? lq_in[i] : -INFINITY;
+    given[i] = en.id[i] >= 0;
+    z[i] = given[i] ? z_of[lane + 32 * i] : -INFINITY;
+    lq[i] = given[i] ? en.lq[i] : -INFINITY;
     n += given[i];
   }
   n = __reduce_add_sync(0xffffffffu, n);
@@ -220,142 +251,177 @@ __device__ __forceinline__ RowSums row_values(const DistillArgs& a, DistillSmem&
     ct += v * (lpt - lqt - G);
   }
   bool nothing = a.renorm && n == 0;
-  if (sm.bad) L = __int_as_float(0x7fc00000);
+  if (en.bad || nan) L = __int_as_float(0x7fc00000);
   if (!(M > -INFINITY)) L = __int_as_float(0x7fc00000);  // no distribution
   if (L != L) ct = L;
   if (nothing && L == L) L = ct = 0.f;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
-    const int j = lane + 32 * i;
-    if (given[i]) {
-      float d = u * (p[i] * Q - q[i]);
-      if (v != 0.f && p[i] > 0.f) d += v * p[i] * (gap[i] - G);
-      sm.d[j] = L != L ? L : s * d;
-    }
+    float d = u * (p[i] * Q - q[i]);
+    if (v != 0.f && p[i] > 0.f) d += v * p[i] * (gap[i] - G);
+    en.d[i] = L != L ? L : s * d;
   }
-  if (lane == 0) {
-    sm.m = M;
-    sm.factor = nothing ? 0.f : fmaxf(fminf(s * ct, 3.0e38f), -3.0e38f) * inv_s;
-    if (L != L) sm.factor = L;
-  }
+  float factor = nothing ? 0.f : fmaxf(fminf(s * ct, 3.0e38f), -3.0e38f) * inv_s;
+  if (L != L) factor = L;
   if (nothing) F = 0.f;
-  return RowSums{static_cast<double>(w) * L, F, G, qt, a.renorm ? 0.f : pt};
+  return RowSums{static_cast<double>(w) * L, F, G, qt, a.renorm ? 0.f : pt, M, factor};
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kRowThreads) topk_distill_kernel(const DistillArgs a) {
+// Takes row `row`'s entries (loaded into en) into the table and looks for ids
+// named twice.  Whole warp; the table holds no other row's entries.
+template <class F, class S>
+__device__ __forceinline__ int table_row(const DistillArgs& a, S& sm, Entries& en, const long long (&id_in)[kPerLane],
+                                         int lane, unsigned int& err) {
+  const int V = static_cast<int>(a.V);
+  bool bad = false;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    const int j = lane + 32 * i;
+    const long long id = id_in[i];
+    const bool out = id < -1 || id >= V;
+    if (out) err |= RL_DEVERR_ID_RANGE;
+    bad = bad || out;
+    en.id[i] = id >= 0 && !out ? static_cast<int>(id) : -1;
+    if (j < a.K) sm.id[j] = en.id[i];
+    if (en.id[i] >= 0) {
+      ++n;
+      sm.next[j] = atomicExch(&sm.head[(en.id[i] / F::kPiece) & (kTable - 1)], j + 1);
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    if (en.id[i] < 0) continue;
+    int same = 0;
+    for (int j = sm.head[(en.id[i] / F::kPiece) & (kTable - 1)]; j; j = sm.next[j - 1]) same += sm.id[j - 1] == en.id[i];
+    if (same > 1) {
+      err |= RL_DEVERR_ID_REPEAT;
+      bad = true;
+    }
+  }
+  en.bad = __any_sync(0xffffffffu, bad);
+  return __reduce_add_sync(0xffffffffu, n);
+}
+
+// kThreads consumers, the producer warp and the row warp.
+template <int DT, int kThreads, int kCtas>
+__global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(const DistillArgs a) {
   using F = Fmt<DT>;
+  using S = DistillSmem<kThreads>;
+  constexpr int kWarps = S::kWarps, kChunk = S::kChunk;
+  constexpr int kVecs = kChunk / 16, kVecsPerThread = kVecs / kThreads;
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  DistillSmem& sm = *reinterpret_cast<DistillSmem*>(smem_raw);
+  S& sm = *reinterpret_cast<S*>(smem_raw);
+  volatile int* abort = &sm.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int V = static_cast<int>(a.V), K = a.K;
+  const long long first = blockIdx.x, stride = gridDim.x;
   const int n_pieces = (V + F::kPiece - 1) / F::kPiece;
   const int n_vecs = (V + F::kVec - 1) / F::kVec;
-  unsigned int err = 0;
-  double acc[5] = {0.0, 0.0, 0.0, 0.0, 0.0};
+  const long long row_bytes16 = (static_cast<long long>(V) * F::kBytes + 15) & ~15LL;
+  const int n_chunks = static_cast<int>((row_bytes16 + kChunk - 1) / kChunk);
 
-  for (int i = tid; i < kTable; i += kRowThreads) sm.head[i] = 0;
+  if (tid == 0) {
+    sm.ring.init(kWarps);
+    mbar_init(smem_addr(&sm.table), 1);
+    mbar_init(smem_addr(&sm.sums), kWarps);
+    mbar_init(smem_addr(&sm.values), 1);
+    mbar_init(smem_addr(&sm.written), kWarps);
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  for (int i = tid; i < kTable; i += kThreads + 64) sm.head[i] = 0;
   // N: every CTA counts the mask
   long long N = a.R;
   if (a.mask) {
     int cnt = 0;
-    for (long long i = tid; i < a.R; i += kRowThreads) cnt += a.mask[i] != 0;
+    for (long long i = tid; i < a.R; i += kThreads + 64) cnt += a.mask[i] != 0;
     cnt = __reduce_add_sync(0xffffffffu, cnt);
     if (lane == 0) sm.wcount[warp] = cnt;
     __syncthreads();
     N = 0;
-    for (int w = 0; w < kRowWarps; ++w) N += sm.wcount[w];
+    for (int w = 0; w < kWarps + 2; ++w) N += sm.wcount[w];
   }
-  const double norm = a.norm > 0.0 ? a.norm : static_cast<double>(N);
   __syncthreads();
+  const double norm = a.norm > 0.0 ? a.norm : static_cast<double>(N);
 
-  for (long long row = blockIdx.x; row < a.R; row += gridDim.x) {
-    const unsigned char* src = a.logits + row * a.row_bytes;
-    unsigned char* dst = a.dlogits ? a.dlogits + row * a.row_bytes : nullptr;
-    if (a.mask && a.mask[row] == 0) {
-      if (dst)
-        for (int v = tid; v < n_vecs; v += kRowThreads) {
-          if ((v + 1) * F::kVec <= V)
-            st_global_cs_v4(dst + static_cast<long long>(v) * 16, make_uint4(0u, 0u, 0u, 0u));
-          else
-            for (int i = v * F::kVec; i < V; ++i) F::store(dst, i, 0.f);
-        }
-      if (tid == 0 && a.row_loss) a.row_loss[row] = 0.f;
-      continue;
-    }
-    // the row's entries into the table
-    if (tid == 0) sm.bad = 0;
-    __syncthreads();
-    if (tid < K) {
-      const long long id = a.ids[row * K + tid];
-      sm.id[tid] = id >= 0 && id < V ? static_cast<int>(id) : -1;
-      if (id < -1 || id >= V) {
-        err |= RL_DEVERR_ID_RANGE;
-        sm.bad = 1;
-      }
-      if (id >= 0 && id < V)
-        sm.next[tid] = atomicExch(&sm.head[(static_cast<int>(id) / F::kPiece) & (kTable - 1)], tid + 1);
-    }
-    __syncthreads();
-    int n_given = 0;
-    if (tid < K && sm.id[tid] >= 0) {
-      n_given = 1;
-      const int id = sm.id[tid];
-      int same = 0;
-      for (int j = sm.head[(id / F::kPiece) & (kTable - 1)]; j; j = sm.next[j - 1]) same += sm.id[j - 1] == id;
-      if (same > 1) {
-        err |= RL_DEVERR_ID_REPEAT;
-        sm.bad = 1;
-      }
-    }
-    n_given = __syncthreads_count(n_given);
-    const bool has_tail = n_given < V;
-    // pass 1: the statistics of every token that is not given
-    WarpStats st;
-    st.low = false;
-    warp_stats_init<F>(st, a.c);
-    for (int p0 = 0; p0 < n_pieces; p0 += kRowThreads) {
-      const int p = p0 + tid;
-      uint32_t w[16];
-      const long long row_bytes16 = (static_cast<long long>(V) * F::kBytes + 15) & ~15LL;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const long long off = static_cast<long long>(p) * kPieceBytes + j * 16;
-        uint4 v = make_uint4(F::kNegInf2, F::kNegInf2, F::kNegInf2, F::kNegInf2);
-        if (off < row_bytes16) v = *reinterpret_cast<const uint4*>(src + off);
-        w[4 * j] = v.x;
-        w[4 * j + 1] = v.y;
-        w[4 * j + 2] = v.z;
-        w[4 * j + 3] = v.w;
-      }
-      if ((p + 1) * F::kPiece > V) F::cut(w, 0, max(0, V - p * F::kPiece));
-      if (p < n_pieces) {
-        for (int j = sm.head[p & (kTable - 1)]; j; j = sm.next[j - 1]) {
-          const int e = sm.id[j - 1] - p * F::kPiece;
-          if (e >= 0 && e < F::kPiece) {
-            sm.z[j - 1] = F::load(src, sm.id[j - 1]);
-            F::drop(w, 0, e);
+  if (warp == kWarps) {
+    // ---------------------------------------------------------------- producer
+    // The row of a chunk goes with it; a chunk of no bytes and row -1 is the end.
+    const uint64_t keep = policy_keep(), once = policy_evict_first();
+    uint32_t it = 0;
+    bool ok = true;
+    RowsOf<true> rows(a.mask, a.R, first, lane);
+    const int passes = a.dlogits ? 2 : 1;
+    while (ok) {
+      const long long row = rows.next(stride, lane);
+      if (lane == 0) {
+        const unsigned char* src = a.logits + row * a.row_bytes;
+        const int n = row < 0 ? 1 : n_chunks * passes;
+        for (int q = 0; q < n; ++q) {
+          ok = sm.ring.reserve(it, abort);
+          if (!ok) break;
+          const uint32_t slot = it % S::kSlots;
+          sm.row_of[slot] = row;
+          if (row < 0) {
+            mbar_arrive(smem_addr(&sm.ring.full[slot]));
+          } else {
+            const long long off = static_cast<long long>(q < n_chunks ? q : q - n_chunks) * kChunk;
+            sm.ring.fill(it, src + off, static_cast<uint32_t>(min(static_cast<long long>(kChunk), row_bytes16 - off)),
+                         q < n_chunks && passes == 2 ? keep : once);
           }
+          ++it;
         }
+        if (!ok) sm.ring.drain(it);
       }
-      const uint32_t rm = F::raw_max(w, 0);
-      add_piece<F, false>(st, w, max_nan(F::raw_value(rm), F::kFloor), a.c, lane, false);
+      ok = __shfl_sync(0xffffffffu, ok, 0) && row >= 0;
     }
-    const RowStats wst = warp_stats_sum<F>(st, a.c);
-    if (lane == 0) sm.part[warp] = wst;
-    __syncthreads();
-    RowStats tail = sm.part[0];
+  } else if (warp == kWarps + 1) {
+    // ---------------------------------------------------------------- row warp
+    unsigned int err = 0;
+    double acc[5] = {0.0, 0.0, 0.0, 0.0, 0.0};
+    RowsOf<true> rows(a.mask, a.R, first, lane);
+    Entries en;
+    long long id_in[kPerLane];
+    auto load_row = [&](long long row) {
 #pragma unroll
-    for (int w = 1; w < kRowWarps; ++w) tail = merge_row(tail, sm.part[w], a.c);
-    if (needs_exact<F>(tail.m, a.c)) tail = exact_tail<F>(src, V, a.c, sm, tid);
-    if (warp == 0) {
-      float lq[kPerLane];
-#pragma unroll
-      for (int i = 0; i < kPerLane; ++i) lq[i] = lane + 32 * i < K ? a.lq[row * K + lane + 32 * i] : 0.f;
+      for (int i = 0; i < kPerLane; ++i) {
+        const int j = lane + 32 * i;
+        id_in[i] = row >= 0 && j < K ? a.ids[row * K + j] : -1;
+        en.lq[i] = row >= 0 && j < K ? a.lq[row * K + j] : 0.f;
+      }
+    };
+    long long row = rows.next(stride, lane);
+    load_row(row);
+    int n_given = row >= 0 ? table_row<F>(a, sm, en, id_in, lane, err) : 0;
+    __syncwarp();
+    if (row >= 0 && lane == 0) mbar_arrive(smem_addr(&sm.table));
+    for (uint32_t done = 0; row >= 0; ++done) {
       const float w = a.weight ? a.weight[row] : 1.f;
       const float s = static_cast<float>(static_cast<double>(a.grad_scale) * w / norm) * a.inv_temp;
-      const RowSums t = row_values(a, sm, tail, has_tail, lq, w, s, lane);
+      const unsigned char* src = a.logits + row * a.row_bytes;
+      if (!__all_sync(0xffffffffu, wait_bounded<false>(smem_addr(&sm.sums), done & 1, abort))) break;
+      RowStats tail = sm.part[0];
+      bool nan = sm.nan[0] != 0.f;
+#pragma unroll
+      for (int q = 1; q < kWarps; ++q) {
+        tail = merge_row(tail, sm.part[q], a.c);
+        nan = nan || sm.nan[q] != 0.f;
+      }
+      float zm = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kPerLane; ++i)
+        if (en.id[i] >= 0) zm = fmaxf(zm, sm.z[lane + 32 * i]);
+      const float M = fmaxf(warp_max(zm), tail.m);
+      const bool plain = needs_exact<F>(M, a.c);
+      if (plain) tail = exact_tail<F>(src, V, a.c, sm, lane);
+      const RowSums t = row_values(a, en, sm.z, tail, n_given < V, nan, w, s, lane);
       if (lane == 0) {
+        sm.m = t.m;
+        sm.factor = t.factor;
+        sm.plain = plain;
+        mbar_arrive(smem_addr(&sm.values));
         acc[0] += t.loss;
         acc[1] += t.fwd;
         acc[2] += t.rev;
@@ -363,82 +429,209 @@ __global__ void __launch_bounds__(kRowThreads) topk_distill_kernel(const Distill
         acc[4] += t.pt;
         if (a.row_loss) a.row_loss[row] = static_cast<float>(t.loss);
       }
+      // the table for the next row (every consumer is past the first pass)
+      int old_id[kPerLane];
+      float d[kPerLane];
+#pragma unroll
+      for (int i = 0; i < kPerLane; ++i) {
+        old_id[i] = en.id[i];
+        d[i] = en.d[i];
+        if (old_id[i] >= 0) sm.head[(old_id[i] / F::kPiece) & (kTable - 1)] = 0;
+      }
+      __syncwarp();
+      const long long prev = row;
+      row = rows.next(stride, lane);
+      load_row(row);
+      if (row >= 0) {
+        n_given = table_row<F>(a, sm, en, id_in, lane, err);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.table));
+      }
+      // the given tokens' gradients over what the consumers have written there
+      if (a.dlogits) {
+        if (!__all_sync(0xffffffffu, wait_bounded<false>(smem_addr(&sm.written), done & 1, abort))) break;
+        unsigned char* dst = a.dlogits + prev * a.row_bytes;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i)
+          if (old_id[i] >= 0) F::store(dst, old_id[i], d[i]);
+      }
     }
-    __syncthreads();
-    // pass 2
-    if (dst) {
-      const float2 nm = make_float2(-sm.m, -sm.m), c2 = make_float2(a.c, a.c);
-      const float2 f2 = make_float2(sm.factor, sm.factor);
-      for (int v = tid; v < n_vecs; v += kRowThreads) {
-        float z[F::kVec];
-        F::unpack(*reinterpret_cast<const uint4*>(src + static_cast<long long>(v) * 16), z);
-#pragma unroll
-        for (int i = 0; i < F::kVec; i += 2) {
-          const float2 x = __fmul2_rn(__fadd2_rn(make_float2(z[i], z[i + 1]), nm), c2);
-          const float2 d = __fmul2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), f2);
-          z[i] = d.x;
-          z[i + 1] = d.y;
-        }
-        if ((v + 1) * F::kVec <= V) {
-          st_global_cs_v4(dst + static_cast<long long>(v) * 16, F::pack(z));
-        } else {
-#pragma unroll
-          for (int i = 0; i < F::kVec; ++i)
-            if (v * F::kVec + i < V) F::store(dst, v * F::kVec + i, z[i]);
+    // this CTA's sums, then the last CTA adds all of them in CTA order
+    err = __reduce_or_sync(0xffffffffu, err);
+    bool last = false;
+    if (lane == 0) {
+      if (*abort) err |= RL_DEVERR_TIMEOUT;
+      if (err) atomicOr(&a.ws->status, err);
+      WsPartial& P = a.partials[blockIdx.x];
+      for (int i = 0; i < 5; ++i) P.v[i] = acc[i];
+      __threadfence();
+      last = atomicInc(&a.ws->ticket, gridDim.x - 1) == gridDim.x - 1;
+    }
+    if (__shfl_sync(0xffffffffu, last, 0)) {
+      __threadfence();
+      double v[5] = {0.0, 0.0, 0.0, 0.0, 0.0};
+      for (int i = lane; i < static_cast<int>(gridDim.x); i += 32)
+        for (int q = 0; q < 5; ++q) v[q] += __ldcg(&a.partials[i].v[q]);
+      for (int q = 0; q < 5; ++q) v[q] = warp_sum_d(v[q]);
+      if (lane == 0) {
+        const unsigned int stw = atomicExch(&a.ws->status, 0u);
+        a.ws->last_status = stw;
+        const double inv = N > 0 ? 1.0 / static_cast<double>(N) : 0.0;
+        rl_distill_stats o;
+        o.loss = norm > 0.0 ? v[0] / norm : 0.0;
+        o.forward_kl = v[1] * inv;
+        o.reverse_kl = v[2] * inv;
+        o.teacher_tail = v[3] * inv;
+        o.student_tail = v[4] * inv;
+        o.n_rows = N;
+        o.device_error = static_cast<int>(stw);
+        o.reserved = 0;
+        *a.stats = o;
+        if (a.loss_out) *a.loss_out = static_cast<float>(o.loss);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- consumers
+    // masked rows: an all-zero gradient, shared out evenly
+    if (a.mask) {
+      RowsOf<false> masked(a.mask, a.R, first, lane);
+      for (long long row = masked.next(stride, lane); row >= 0; row = masked.next(stride, lane)) {
+        if (tid == 0 && a.row_loss) a.row_loss[row] = 0.f;
+        if (!a.dlogits) continue;
+        unsigned char* dst = a.dlogits + row * a.row_bytes;
+        for (int v = tid; v < n_vecs; v += kThreads) {
+          if ((v + 1) * F::kVec <= V)
+            st_global_cs_v4(dst + static_cast<long long>(v) * 16, make_uint4(0u, 0u, 0u, 0u));
+          else
+            for (int i = v * F::kVec; i < V; ++i) F::store(dst, i, 0.f);
         }
       }
     }
-    __syncthreads();
-    if (tid < K && sm.id[tid] >= 0) {
-      if (dst) F::store(dst, sm.id[tid], sm.d[tid]);
-      sm.head[(sm.id[tid] / F::kPiece) & (kTable - 1)] = 0;
-    }
-    __syncthreads();
-  }
-
-  // this CTA's sums, then the last CTA adds all of them in CTA order
-  if (err) atomicOr(&a.ws->status, err);
-  __syncthreads();
-  if (tid == 0) {
-    WsPartial& P = a.partials[blockIdx.x];
-    for (int i = 0; i < 5; ++i) P.v[i] = acc[i];
-    __threadfence();
-    sm.is_last = atomicInc(&a.ws->ticket, gridDim.x - 1) == gridDim.x - 1;
-  }
-  __syncthreads();
-  if (sm.is_last && warp == 0) {
-    __threadfence();
-    double v[5] = {0.0, 0.0, 0.0, 0.0, 0.0};
-    for (int i = lane; i < static_cast<int>(gridDim.x); i += 32)
-      for (int q = 0; q < 5; ++q) v[q] += __ldcg(&a.partials[i].v[q]);
-    for (int q = 0; q < 5; ++q) v[q] = warp_sum_d(v[q]);
-    if (lane == 0) {
-      const unsigned int stw = atomicExch(&a.ws->status, 0u);
-      a.ws->last_status = stw;
-      const double inv = N > 0 ? 1.0 / static_cast<double>(N) : 0.0;
-      rl_distill_stats o;
-      o.loss = norm > 0.0 ? v[0] / norm : 0.0;
-      o.forward_kl = v[1] * inv;
-      o.reverse_kl = v[2] * inv;
-      o.teacher_tail = v[3] * inv;
-      o.student_tail = v[4] * inv;
-      o.n_rows = N;
-      o.device_error = static_cast<int>(stw);
-      o.reserved = 0;
-      *a.stats = o;
-      if (a.loss_out) *a.loss_out = static_cast<float>(o.loss);
+    const int n_full = V / F::kPiece / kThreads;  // chunks whose every piece is a full one
+    WarpStats st;
+    st.low = false;
+    uint32_t it = 0;
+    for (uint32_t done = 0;; ++done) {
+      sm.ring.wait(it, abort);
+      const long long row = sm.row_of[it % S::kSlots];
+      // (after a timeout the whole warp stops; nothing here meets another warp)
+      if (__any_sync(0xffffffffu, row < 0 || *abort)) break;
+      const unsigned char* src = a.logits + row * a.row_bytes;
+      unsigned char* dst = a.dlogits + row * a.row_bytes;
+      wait_bounded<false>(smem_addr(&sm.table), done & 1, abort);
+      // pass 1: the statistics of every token that is not given
+      warp_stats_init<F>(st, a.c);
+      bool nan = false;
+      for (int i = 0; i < n_chunks; ++i, ++it) {
+        const uint32_t buf = sm.ring.wait(it, abort);
+        const int p = i * kThreads + tid;
+        const bool last = i >= n_full;
+        uint32_t w[16];
+        const int sh = last ? 0 : lane >> 1;
+        load_piece(w, 0, buf + tid * kPieceBytes, sh);
+        int j = p < n_pieces ? sm.head[p & (kTable - 1)] : 0;
+        while (j) {
+          const int e = sm.id[j - 1] - p * F::kPiece;
+          if (e >= 0 && e < F::kPiece) {
+            sm.z[j - 1] = F::load_shared(sm.ring.data[it % S::kSlots] + tid * kPieceBytes, e);
+            F::drop(w, 0, (((e / F::kVec) - sh) & 3) * F::kVec + e % F::kVec);
+          }
+          j = sm.next[j - 1];
+        }
+        sm.ring.release(it, lane);
+        if (last) F::cut(w, 0, p < n_pieces ? min(F::kPiece, V - p * F::kPiece) : 0);
+        const float pm = F::raw_value(F::raw_max(w, 0));
+        nan = nan || pm != pm;
+        add_piece<F, false>(st, w, max_nan(pm, F::kFloor), a.c, lane, false);
+      }
+      const RowStats ws = warp_stats_sum<F>(st, a.c);
+      nan = __any_sync(0xffffffffu, nan);
+      if (lane == 0) {
+        sm.part[warp] = ws;
+        sm.nan[warp] = nan ? 1.f : 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sm.sums));
+      wait_bounded<false>(smem_addr(&sm.values), done & 1, abort);
+      if (!a.dlogits) continue;
+      // pass 2
+      const float m = sm.m;
+      const bool plain = sm.plain != 0;
+      const float nm = -m * a.c, rho = fmaf(-m, a.c, -nm);
+      const float factor = plain ? sm.factor : sm.factor * ex2_approx(rho);
+      const float2 c2 = make_float2(a.c, a.c), f2 = make_float2(factor, factor);
+      const float2 nm2 = make_float2(nm, nm), dm2 = make_float2(-m, -m);
+      for (int i = 0; i < n_chunks; ++i, ++it) {
+        const uint32_t buf = sm.ring.wait(it, abort);
+        uint4 w[kVecsPerThread];
+#pragma unroll
+        for (int q = 0; q < kVecsPerThread; ++q) w[q] = ld_shared_v4(buf + (tid + q * kThreads) * 16);
+        sm.ring.release(it, lane);
+        const int v0 = i * kVecs + tid;
+        unsigned char* out = dst + static_cast<long long>(v0) * 16;
+#pragma unroll
+        for (int q = 0; q < kVecsPerThread; ++q) {
+          float z[F::kVec];
+          F::unpack(w[q], z);
+#pragma unroll
+          for (int j = 0; j < F::kVec; j += 2) {
+            const float2 zz = make_float2(z[j], z[j + 1]);
+            const float2 x = plain ? __fmul2_rn(__fadd2_rn(zz, dm2), c2) : __ffma2_rn(zz, c2, nm2);
+            const float2 d = __fmul2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), f2);
+            z[j] = d.x;
+            z[j + 1] = d.y;
+          }
+          const int v = v0 + q * kThreads;
+          if ((v + 1) * F::kVec <= V) {
+            st_global_cs_v4(out + q * kThreads * 16, F::pack(z));
+          } else if (v < n_vecs) {
+#pragma unroll
+            for (int j = 0; j < F::kVec; ++j)
+              if (v * F::kVec + j < V) F::store(dst, v * F::kVec + j, z[j]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sm.written));
     }
   }
 }
 
 // ------------------------------------------------------------------ host side
-template <int DT>
-rl_status launch(const DistillArgs& a, int sms, cudaStream_t stream) {
-  long long grid = 4LL * sms;
+rl_status allow_smem(const void* fn, int dev, int smem) {
+  static std::mutex mu;
+  static std::map<std::pair<const void*, int>, bool> done;
+  std::lock_guard<std::mutex> lock(mu);
+  bool& d = done[std::make_pair(fn, dev)];
+  if (!d) {
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return RL_ERR_CUDA;
+    d = true;
+  }
+  return RL_OK;
+}
+
+template <int DT, int kThreads, int kCtas>
+rl_status launch(const DistillArgs& a, int dev, int sms, cudaStream_t stream) {
+  const void* fn = reinterpret_cast<const void*>(&topk_distill_kernel<DT, kThreads, kCtas>);
+  const int smem = static_cast<int>(sizeof(DistillSmem<kThreads>));
+  const rl_status st = allow_smem(fn, dev, smem);
+  if (st != RL_OK) return st;
+  long long grid = static_cast<long long>(kCtas) * sms;
   if (grid > kMaxGrid) grid = kMaxGrid;
   if (grid > a.R) grid = a.R > 0 ? a.R : 1;
-  topk_distill_kernel<DT><<<static_cast<unsigned>(grid), kRowThreads, sizeof(DistillSmem), stream>>>(a);
+  topk_distill_kernel<DT, kThreads, kCtas><<<static_cast<unsigned>(grid), kThreads + 64, smem, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? RL_OK : RL_ERR_CUDA;
+}
+
+// Rows of more than kLongRow bytes go one to a SM, on 512 consumer threads: the
+// second pass finds them in L2 then.  Shorter rows go four to a SM, on 128
+// each, so that one row's serial part overlaps the others' passes.
+constexpr long long kLongRow = 100 * 1024;
+
+template <int DT>
+rl_status launch_any(const DistillArgs& a, int dev, int sms, cudaStream_t stream) {
+  return a.V * Fmt<DT>::kBytes > kLongRow ? launch<DT, 512, 1>(a, dev, sms, stream)
+                                          : launch<DT, 128, 4>(a, dev, sms, stream);
 }
 
 }  // namespace
@@ -506,9 +699,9 @@ extern "C" rl_status rl_topk_distill_fwd_bwd(const rl_topk_distill_desc* d, void
   a.renorm = d->tail == RL_DISTILL_TAIL_RENORM;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (d->dtype) {
-    case RL_F32: return launch<RL_F32>(a, sms, s);
-    case RL_BF16: return launch<RL_BF16>(a, sms, s);
-    case RL_F16: return launch<RL_F16>(a, sms, s);
+    case RL_F32: return launch_any<RL_F32>(a, dev, sms, s);
+    case RL_BF16: return launch_any<RL_BF16>(a, dev, sms, s);
+    case RL_F16: return launch_any<RL_F16>(a, dev, sms, s);
   }
   return RL_ERR_DTYPE;
 }

@@ -376,3 +376,36 @@ def test_wrapper_refusals():
             torch_api.token_logprobs_backward(**{**dict(logits=z, ids=ids, dlogp=lse, lse=lse), **b})
     with pytest.raises(rl.RlLossError):
         torch_api.token_logprobs_backward(z, ids, lse, lse, entropy=lse)
+
+
+@pytest.mark.parametrize("dtype,low", [("bf16", -1e30), ("f32", -1e9), ("bf16", -1e4), ("f32", -20000.0), ("f16", -60000.0)])
+@pytest.mark.parametrize("entropy", [True, False])
+def test_masks_of_large_negative_numbers(dtype, low, entropy):
+    """Tokens ruled out by a large finite number: in whole pieces at the start,
+    scattered, everywhere but one token, everywhere."""
+    V, k = 6000, 9
+    z = logits(5, V, dtype, 51, sure=False)
+    z[0, :3000] = low
+    z[1, ::3] = low
+    z[2, :] = low
+    z[2, 4567] = -3.0
+    z[3, :] = low
+    z[4, 100:] = low
+    ids = torch.tensor([[5, 5000], [0, 1], [4567, 1], [0, 1], [0, 5999]])
+    for temp in (1.0, 0.01, 100.0):
+        _, out, st = run(z, ids, None, k, temp, want_entropy=entropy)
+        assert st == 0
+        check_logprobs(out, ref_of(z, dtype, ids, None, k, temp), V, temp)
+
+
+def test_logits_of_large_size():
+    """Maxima up to the type's largest: log-probabilities are differences."""
+    z = logits(6, 3000, "f32", 52, sure=False)
+    for r, c in enumerate((1e4, -1e5, 1e7, -1e8, 1e30, 3e38)):
+        z[r] = c + torch.zeros(3000)
+        z[r, 11] = c * (1 - 2 ** -20) if c > 0 else c * (1 + 2 ** -20)
+        z[r, 1000:1010] = torch.nextafter(torch.tensor(c), torch.tensor(-3e38))
+    ids = torch.tensor([[11, 1000]] * 6)
+    _, out, st = run(z, ids, None, 5)
+    assert st == 0
+    check_logprobs(out, ref_of(z, "f32", ids, None, 5), 3000)

@@ -321,3 +321,39 @@ def test_wrapper_refusals_and_empty():
             torch_api.topk_distill(z, ids, lq, **b)
     out = torch_api.topk_distill(z[:0], ids[:0], lq[:0])
     assert torch_api.read_distill_stats(out["stats"])["loss"] == 0 and out["loss"].item() == 0
+
+
+@pytest.mark.parametrize("dtype,low", [("bf16", -1e30), ("f32", -1e9), ("f32", -20000.0), ("f16", -60000.0)])
+def test_masks_of_large_negative_numbers(dtype, low):
+    """Student tokens ruled out by a large finite number: half of the tail, all
+    of it, the whole row."""
+    V = 4000
+    z = logits(4, V, dtype, 15, sd=1.0, sure=False)
+    ids, lq = teacher(z, 8, 3)
+    z[0, :2000] = low
+    z[1, :] = low
+    z[1, ids[1]] = torch.arange(8).to(z.dtype)
+    z[2, :] = low
+    z[3, ids[3, :4]] = low
+    check(z, dtype, ids, lq, reverse=1.0)
+    check(z[:3], dtype, ids[:3], lq[:3], tail="renormalise")
+
+
+def test_more_rows_than_one_round_of_ctas_long_rows():
+    """Long rows (one a SM), masked in runs, more of them than SMs."""
+    R, V = 400, 60001
+    z = logits(R, V, "bf16", 16, sd=2.0)
+    ids, lq = teacher(z, 20, 3)
+    mask = ((torch.arange(R) // 37) % 3 != 1).to(torch.uint8)
+    zd = to_dev(z)
+    out = torch_api.topk_distill(zd, ids.to(DEV), lq.to(DEV), mask=mask.to(DEV), norm=1.0)
+    rows = torch.tensor([0, 36, 37, 73, 74, 152, 153, 304, 399])
+    ref = oracle.topk_distill(storage(z[rows]), "bf16", V, ids[rows].numpy(), lq[rows].numpy(), mask=mask[rows].numpy(), norm=1.0)
+    row_tol, grad_tol = tolerances(ref, "bf16", V)
+    check_close("row_loss", out["row_loss"].cpu()[rows], ref["row_loss"], row_tol)
+    check_close("dlogits", oracle.decode(storage(out["dlogits"].cpu()[rows]), "bf16"), ref["dlogits"], grad_tol)
+    masked = mask == 0
+    assert (out["dlogits"].cpu()[masked] == 0).all() and (out["row_loss"].cpu()[masked] == 0).all()
+    st = torch_api.read_distill_stats(out["stats"])
+    assert st["n_rows"] == int(mask.sum()) and st["device_error"] == 0
+    assert abs(st["loss"] - out["row_loss"].double().sum().item()) < 1e-6 * R
