@@ -129,88 +129,88 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// A row's teacher entries, four a lane.
-struct Entries {
+// What a row's loss needs of the teacher, four entries a lane: known before
+// the student's row has streamed.
+struct Teacher {
   int id[kPerLane];      // -1: none
-  float lq[kPerLane];
-  float d[kPerLane];     // the given tokens' gradients, once known
+  float lq[kPerLane], q[kPerLane];
+  float qt, lqt, Q;      // the tail's probability and its logarithm; all probabilities
+  int n;                 // entries
   bool bad;              // an id out of range or named twice
+  float w, s;            // the row's weight, its gradient's scale
 };
+
+__device__ __forceinline__ void teacher_values(const DistillArgs& a, Teacher& t, double norm, long long row) {
+  // 1 - sum q in fp64, where it is a difference of near numbers
+  double sum = 0.0;
+  t.qt = t.lqt = 0.f;
+  if (a.renorm) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) mx = t.id[i] >= 0 ? fmaxf(mx, t.lq[i]) : mx;
+    mx = warp_max(mx);
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i)
+      if (t.id[i] >= 0) sum += exp(static_cast<double>(t.lq[i]) - static_cast<double>(mx));
+    sum = warp_sum_d(sum);
+    const float ls = static_cast<float>(static_cast<double>(mx) + log(sum));
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+      t.lq[i] = t.id[i] >= 0 ? t.lq[i] - ls : -INFINITY;
+      t.q[i] = t.id[i] >= 0 ? expf(t.lq[i]) : 0.f;
+    }
+    t.Q = 1.f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+      t.q[i] = 0.f;
+      if (t.id[i] >= 0) {
+        const double e = exp(static_cast<double>(t.lq[i]));
+        sum += e;
+        t.q[i] = static_cast<float>(e);
+      } else {
+        t.lq[i] = -INFINITY;
+      }
+    }
+    sum = warp_sum_d(sum);
+    if (t.n < a.V) {
+      const double u = 1.0 - sum;
+      t.qt = static_cast<float>(u < 0x1p-24 ? 0x1p-24 : u);  // a NaN stays one
+      t.lqt = logf(t.qt);
+    }
+    t.Q = static_cast<float>(sum) + t.qt;
+  }
+  t.w = a.weight ? a.weight[row] : 1.f;
+  t.s = static_cast<float>(static_cast<double>(a.grad_scale) * t.w / norm) * a.inv_temp;
+}
 
 struct RowSums {
   double loss, fwd, rev, qt, pt;
   float m, factor;
 };
 
-// One warp: a row's loss terms and gradient values from the entries' logits
-// (z), the teacher's entries and the tail's statistics.
-__device__ __forceinline__ RowSums row_values(const DistillArgs& a, Entries& en, const float* z_of, RowStats tail,
-                                              bool has_tail, bool nan, float w, float s, int lane) {
-  float lq[kPerLane], q[kPerLane], z[kPerLane];
-  bool given[kPerLane];
-  int n = 0;
-#pragma unroll
-  for (int i = 0; i < kPerLane; ++i) {
-    given[i] = en.id[i] >= 0;
-    z[i] = given[i] ? z_of[lane + 32 * i] : -INFINITY;
-    lq[i] = given[i] ? en.lq[i] : -INFINITY;
-    n += given[i];
-  }
-  n = __reduce_add_sync(0xffffffffu, n);
-  // the teacher: 1 - sum q in fp64, where it is a difference of near numbers
-  double sum = 0.0;
-  float qt = 0.f, lqt = 0.f;
-  if (a.renorm) {
-    float mx = lq[0];
-#pragma unroll
-    for (int i = 1; i < kPerLane; ++i) mx = fmaxf(mx, lq[i]);
-    mx = warp_max(mx);
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) sum += given[i] ? exp(static_cast<double>(lq[i]) - static_cast<double>(mx)) : 0.0;
-    sum = warp_sum_d(sum);
-    const float ls = static_cast<float>(static_cast<double>(mx) + log(sum));
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      lq[i] = given[i] ? lq[i] - ls : -INFINITY;
-      q[i] = given[i] ? expf(lq[i]) : 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      const double e = given[i] ? exp(static_cast<double>(lq[i])) : 0.0;
-      sum += e;
-      q[i] = static_cast<float>(e);
-    }
-    sum = warp_sum_d(sum);
-    if (has_tail) {
-      const double t = 1.0 - sum;
-      qt = static_cast<float>(t < 0x1p-24 ? 0x1p-24 : t);  // a NaN stays one
-      lqt = logf(qt);
-    }
-  }
-  const float Q = a.renorm ? 1.f : static_cast<float>(sum) + qt;
+// One warp: a row's loss terms and gradient values from the teacher's side,
+// the entries' logits z and the tail's statistics; d: the given tokens'
+// gradients.
+__device__ __forceinline__ RowSums row_values(const DistillArgs& a, const Teacher& t, const float (&z)[kPerLane],
+                                              RowStats tail, bool nan, float M, float (&d)[kPerLane], int lane) {
+  const bool has_tail = t.n < a.V;
   // the student: the entries joined to the tail
-  float zm = z[0];
-#pragma unroll
-  for (int i = 1; i < kPerLane; ++i) zm = max_nan(zm, z[i]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) zm = max_nan(zm, __shfl_xor_sync(0xffffffffu, zm, o));
   const bool tail_any = has_tail && tail.m > -INFINITY;
-  const bool top_in = !tail_any || zm >= tail.m;  // the row's maximum is an entry
-  const float M = top_in ? zm : tail.m;
+  const bool top_in = !tail_any || M > tail.m || !(tail.m >= M);  // the row's maximum is an entry
   float e[kPerLane], in = 0.f;
   bool holder = false;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
-    e[i] = given[i] ? ex2_approx((z[i] - M) * a.c) : 0.f;
-    holder = holder || (given[i] && z[i] == M);
+    e[i] = t.id[i] >= 0 ? ex2_approx((z[i] - M) * a.c) : 0.f;
+    holder = holder || (t.id[i] >= 0 && z[i] == M);
   }
   // one maximum stays out of the sum of the others (r)
   const uint32_t holders = __ballot_sync(0xffffffffu, holder);
   bool out = top_in && lane == __ffs(holders) - 1;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
-    if (out && given[i] && z[i] == M)
+    if (out && t.id[i] >= 0 && z[i] == M)
       out = false;
     else
       in += e[i];
@@ -220,58 +220,73 @@ __device__ __forceinline__ RowSums row_values(const DistillArgs& a, Entries& en,
   const float f_t = tail_any ? ex2_approx((tail.m - M) * a.c) : 0.f;
   const float s_t = tail_any ? f_t * (1.f + tail.r) : 0.f;
   const float r = top_in ? in + s_t : tail.r + in;
-  const float log_s = log1pf(r), inv_s = 1.f / (1.f + r);
+  const float log_s = log1pf(r), inv_s = __frcp_rn(1.f + r);
   float pt = 0.f, lpt = 0.f;
   if (has_tail) {
     pt = fmaxf(s_t * inv_s, kTiny);
     lpt = fmaxf(s_t > 0.f ? -log1pf(s_in / s_t) : -INFINITY, kLnTiny);
   }
-  float F = 0.f, G = 0.f, lp[kPerLane], p[kPerLane], gap[kPerLane];
+  float F = 0.f, G = 0.f, p[kPerLane], gap[kPerLane];
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
-    lp[i] = fmaf(z[i] - M, a.inv_temp, -log_s);
+    const float lp = fmaf(z[i] - M, a.inv_temp, -log_s);
     p[i] = e[i] * inv_s;
-    gap[i] = lp[i] - fmaxf(lq[i], kLnTiny);
-    if (q[i] > 0.f || q[i] != q[i]) F += q[i] * (lq[i] - lp[i]);
+    gap[i] = lp - fmaxf(t.lq[i], kLnTiny);
+    if (t.q[i] > 0.f || t.q[i] != t.q[i]) F += t.q[i] * (t.lq[i] - lp);
     if (p[i] > 0.f || p[i] != p[i]) G += p[i] * gap[i];
   }
-  F = warp_sum(F);
-  G = warp_sum(G);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    F += __shfl_xor_sync(0xffffffffu, F, o);
+    G += __shfl_xor_sync(0xffffffffu, G, o);
+  }
   if (a.renorm) {
     G = 0.f;
   } else if (has_tail) {
-    F += qt * (lqt - lpt);
-    G += pt * (lpt - lqt);
+    F += t.qt * (t.lqt - lpt);
+    G += pt * (lpt - t.lqt);
   }
   const float v = a.reverse, u = 1.f - v;
   float L = u != 0.f ? u * F : 0.f;  // F may be infinite
-  float ct = u * (Q - (has_tail && !a.renorm ? qt / pt : 0.f));
+  float ct = u * (t.Q - (has_tail && !a.renorm ? t.qt / pt : 0.f));
   if (v != 0.f) {
     L += v * G;
-    ct += v * (lpt - lqt - G);
+    ct += v * (lpt - t.lqt - G);
   }
-  bool nothing = a.renorm && n == 0;
-  if (en.bad || nan) L = __int_as_float(0x7fc00000);
+  const bool nothing = a.renorm && t.n == 0;
+  if (t.bad || nan || r != r) L = __int_as_float(0x7fc00000);
   if (!(M > -INFINITY)) L = __int_as_float(0x7fc00000);  // no distribution
-  if (L != L) ct = L;
-  if (nothing && L == L) L = ct = 0.f;
+  if (nothing && L == L) L = F = ct = 0.f;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
-    float d = u * (p[i] * Q - q[i]);
-    if (v != 0.f && p[i] > 0.f) d += v * p[i] * (gap[i] - G);
-    en.d[i] = L != L ? L : s * d;
+    float g = u * (p[i] * t.Q - t.q[i]);
+    if (v != 0.f && p[i] > 0.f) g += v * p[i] * (gap[i] - G);
+    d[i] = L != L ? L : t.s * g;
   }
-  float factor = nothing ? 0.f : fmaxf(fminf(s * ct, 3.0e38f), -3.0e38f) * inv_s;
+  float factor = fmaxf(fminf(t.s * ct, 3.0e38f), -3.0e38f) * inv_s;
   if (L != L) factor = L;
-  if (nothing) F = 0.f;
-  return RowSums{static_cast<double>(w) * L, F, G, qt, a.renorm ? 0.f : pt, M, factor};
+  return RowSums{static_cast<double>(t.w) * L, F, G, t.qt, a.renorm ? 0.f : pt, M, factor};
 }
 
-// Takes row `row`'s entries (loaded into en) into the table and looks for ids
+// The consumer warps' partial statistics joined, one a lane (kWarps <= 32):
+// the maximum first, then the sums in its frame.  The first warp that holds the
+// maximum leaves its term out, the others' maxima come back in.
+template <int kWarps>
+__device__ __forceinline__ RowStats join_parts(const RowStats* part, float floor, float c, int lane) {
+  RowStats p = lane < kWarps ? part[lane] : RowStats{floor, -1.f, 0.f};
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(p.m));
+  const uint32_t holders = __ballot_sync(0xffffffffu, p.m == m && lane < kWarps);
+  const float f = ex2_approx((p.m - m) * c);
+  const float r = lane == __ffs(holders) - 1 ? p.r : f * (1.f + p.r);
+  return RowStats{m, warp_sum(r), 0.f};
+}
+
+// Takes a row's entries (loaded into en) into the table and looks for ids
 // named twice.  Whole warp; the table holds no other row's entries.
 template <class F, class S>
-__device__ __forceinline__ int table_row(const DistillArgs& a, S& sm, Entries& en, const long long (&id_in)[kPerLane],
-                                         int lane, unsigned int& err) {
+__device__ __forceinline__ void table_row(const DistillArgs& a, S& sm, Teacher& en, const long long (&id_in)[kPerLane],
+                                          int lane, unsigned int& err) {
   const int V = static_cast<int>(a.V);
   bool bad = false;
   int n = 0;
@@ -301,7 +316,7 @@ __device__ __forceinline__ int table_row(const DistillArgs& a, S& sm, Entries& e
     }
   }
   en.bad = __any_sync(0xffffffffu, bad);
-  return __reduce_add_sync(0xffffffffu, n);
+  en.n = __reduce_add_sync(0xffffffffu, n);
 }
 
 // kThreads consumers, the producer warp and the row warp.
@@ -382,7 +397,7 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
     unsigned int err = 0;
     double acc[5] = {0.0, 0.0, 0.0, 0.0, 0.0};
     RowsOf<true> rows(a.mask, a.R, first, lane);
-    Entries en;
+    Teacher en;
     long long id_in[kPerLane];
     auto load_row = [&](long long row) {
 #pragma unroll
@@ -394,29 +409,37 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
     };
     long long row = rows.next(stride, lane);
     load_row(row);
-    int n_given = row >= 0 ? table_row<F>(a, sm, en, id_in, lane, err) : 0;
-    __syncwarp();
-    if (row >= 0 && lane == 0) mbar_arrive(smem_addr(&sm.table));
+    auto prepare = [&] {
+      table_row<F>(a, sm, en, id_in, lane, err);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sm.table));
+      teacher_values(a, en, norm, row);  // while the row streams
+    };
+    if (row >= 0) prepare();
     for (uint32_t done = 0; row >= 0; ++done) {
-      const float w = a.weight ? a.weight[row] : 1.f;
-      const float s = static_cast<float>(static_cast<double>(a.grad_scale) * w / norm) * a.inv_temp;
       const unsigned char* src = a.logits + row * a.row_bytes;
       if (!__all_sync(0xffffffffu, wait_bounded<false>(smem_addr(&sm.sums), done & 1, abort))) break;
-      RowStats tail = sm.part[0];
-      bool nan = sm.nan[0] != 0.f;
+      RowStats tail = join_parts<kWarps>(sm.part, F::kFloor, a.c, lane);
+      const bool nan = __any_sync(0xffffffffu, lane < kWarps && sm.nan[lane < kWarps ? lane : 0] != 0.f);
+      float z[kPerLane], M = tail.m;
 #pragma unroll
-      for (int q = 1; q < kWarps; ++q) {
-        tail = merge_row(tail, sm.part[q], a.c);
-        nan = nan || sm.nan[q] != 0.f;
+      for (int i = 0; i < kPerLane; ++i) {
+        z[i] = en.id[i] >= 0 ? sm.z[lane + 32 * i] : -INFINITY;
+        M = max_nan(M, z[i]);
       }
-      float zm = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < kPerLane; ++i)
-        if (en.id[i] >= 0) zm = fmaxf(zm, sm.z[lane + 32 * i]);
-      const float M = fmaxf(warp_max(zm), tail.m);
+      for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
       const bool plain = needs_exact<F>(M, a.c);
-      if (plain) tail = exact_tail<F>(src, V, a.c, sm, lane);
-      const RowSums t = row_values(a, en, sm.z, tail, n_given < V, nan, w, s, lane);
+      if (plain) {
+        tail = exact_tail<F>(src, V, a.c, sm, lane);
+        M = tail.m;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) M = max_nan(M, z[i]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
+      }
+      float d[kPerLane];
+      const RowSums t = row_values(a, en, z, tail, nan, M, d, lane);
       if (lane == 0) {
         sm.m = t.m;
         sm.factor = t.factor;
@@ -431,22 +454,16 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
       }
       // the table for the next row (every consumer is past the first pass)
       int old_id[kPerLane];
-      float d[kPerLane];
 #pragma unroll
       for (int i = 0; i < kPerLane; ++i) {
         old_id[i] = en.id[i];
-        d[i] = en.d[i];
         if (old_id[i] >= 0) sm.head[(old_id[i] / F::kPiece) & (kTable - 1)] = 0;
       }
       __syncwarp();
       const long long prev = row;
       row = rows.next(stride, lane);
       load_row(row);
-      if (row >= 0) {
-        n_given = table_row<F>(a, sm, en, id_in, lane, err);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sm.table));
-      }
+      if (row >= 0) prepare();
       // the given tokens' gradients over what the consumers have written there
       if (a.dlogits) {
         if (!__all_sync(0xffffffffu, wait_bounded<false>(smem_addr(&sm.written), done & 1, abort))) break;
