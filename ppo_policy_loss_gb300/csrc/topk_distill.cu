@@ -34,7 +34,8 @@ namespace {
 
 constexpr int kMaxEntries = RL_TOKEN_MAX_K;
 constexpr int kPerLane = kMaxEntries / 32;
-constexpr int kTable = 4096;  // pieces that share a place of the table differ by a multiple of this
+constexpr int kTable = 2048;  // pieces that share a place of the table differ by a multiple of this
+constexpr int kLead = 2;      // chunks of the next row's first pass before a row's second
 constexpr float kLnTiny = -87.33654475f;  // ln 2^-126
 constexpr float kTiny = 0x1p-126f;
 
@@ -57,38 +58,48 @@ struct DistillArgs {
   int K, renorm;
 };
 
+// A row's entries by the piece that holds them.
+struct EntryTable {
+  int head[kTable];            // 1 + the last entry whose piece falls on this place, 0 none
+  int next[kMaxEntries];       // the entry before it there
+  int id[kMaxEntries];         // -1: empty
+  float z[kMaxEntries];        // the entry's logit (from the consumers)
+  // the teacher's side, known before the student's row has streamed
+  float lq[kMaxEntries], q[kMaxEntries];
+  float qt, lqt, Q;            // the tail's probability and its logarithm; all probabilities
+  float w, s;                  // the row's weight, its gradient's scale
+  int n, bad;                  // entries; an id is out of range or named twice
+};
+
 // kThreads consumers; a chunk is one piece of each.
 template <int kThreads>
 struct DistillSmem {
   static constexpr int kWarps = kThreads / 32, kChunk = kThreads * kPieceBytes;
-  static constexpr int kSlots = kThreads >= 512 ? 6 : 4;
+  static constexpr int kSlots = kThreads >= 512 ? 6 : kThreads >= 256 ? 5 : 4;
   Ring<kSlots, kChunk> ring;
   long long row_of[kSlots];    // the row a chunk belongs to
-  int head[kTable];            // 1 + the last entry whose piece falls on this place, 0 none
-  int next[kMaxEntries];       // the entry before it there
-  int id[kMaxEntries];         // -1: empty
-  float z[kMaxEntries];        // the entry's logit
+  EntryTable tab[2];           // of the even and the odd rows of this CTA
   RowStats part[kWarps];
   float nan[kWarps];           // not 0: the warp met a NaN
   long long wcount[kWarps + 2];
-  unsigned long long table, sums, values, written;  // once a row: table filled, sums in, values out, row written
+  unsigned long long table[2];  // a row's entries are in tab[k & 1]
+  unsigned long long sums, values, written;  // once a row: sums in, values out, row written
   float m, factor;             // pass 2: dz = 2^((z - m) c) factor
   int plain;                   // pass 2 by differences to m
   int abort;
 };
 
 // The entry at element e, or -1.
-template <class S>
-__device__ __forceinline__ int entry_at(const S& sm, int e, int piece) {
-  for (int j = sm.head[piece & (kTable - 1)]; j; j = sm.next[j - 1])
-    if (sm.id[j - 1] == e) return j - 1;
+__device__ __forceinline__ int entry_at(const EntryTable& tab, int e, int piece) {
+  for (int j = tab.head[piece & (kTable - 1)]; j; j = tab.next[j - 1])
+    if (tab.id[j - 1] == e) return j - 1;
   return -1;
 }
 
 // The tail's statistics by differences to its maximum (needs_exact).  Rare, so
 // one warp reads the row again.
-template <class F, class S>
-__device__ __noinline__ RowStats exact_tail(const unsigned char* row, int V, float c, const S& sm, int lane) {
+template <class F>
+__device__ __noinline__ RowStats exact_tail(const unsigned char* row, int V, float c, const EntryTable& tab, int lane) {
   const int n_vecs = (V + F::kVec - 1) / F::kVec;
   auto each = [&](auto f) {
 #pragma unroll 4
@@ -98,7 +109,7 @@ __device__ __noinline__ RowStats exact_tail(const unsigned char* row, int V, flo
 #pragma unroll
       for (int i = 0; i < F::kVec; ++i) {
         const int e = v * F::kVec + i;
-        if (e < V && entry_at(sm, e, e / F::kPiece) < 0) f(z[i]);
+        if (e < V && entry_at(tab, e, e / F::kPiece) < 0) f(z[i]);
       }
     }
   };
@@ -129,59 +140,64 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// What a row's loss needs of the teacher, four entries a lane: known before
-// the student's row has streamed.
-struct Teacher {
-  int id[kPerLane];      // -1: none
-  float lq[kPerLane], q[kPerLane];
-  float qt, lqt, Q;      // the tail's probability and its logarithm; all probabilities
-  int n;                 // entries
-  bool bad;              // an id out of range or named twice
-  float w, s;            // the row's weight, its gradient's scale
-};
-
-__device__ __forceinline__ void teacher_values(const DistillArgs& a, Teacher& t, double norm, long long row) {
+// The teacher's side of a row into its table, by one warp, from the entries'
+// ids (-1: none) and log-probabilities, four a lane.
+__device__ __forceinline__ void teacher_values(const DistillArgs& a, EntryTable& tab, const int (&id)[kPerLane],
+                                               float (&lq)[kPerLane], int n, bool bad, double norm, long long row,
+                                               int lane) {
   // 1 - sum q in fp64, where it is a difference of near numbers
   double sum = 0.0;
-  t.qt = t.lqt = 0.f;
+  float q[kPerLane], qt = 0.f, lqt = 0.f, Q = 1.f;
   if (a.renorm) {
     float mx = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) mx = t.id[i] >= 0 ? fmaxf(mx, t.lq[i]) : mx;
+    for (int i = 0; i < kPerLane; ++i) mx = id[i] >= 0 ? fmaxf(mx, lq[i]) : mx;
     mx = warp_max(mx);
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i)
-      if (t.id[i] >= 0) sum += exp(static_cast<double>(t.lq[i]) - static_cast<double>(mx));
+      if (id[i] >= 0) sum += exp(static_cast<double>(lq[i]) - static_cast<double>(mx));
     sum = warp_sum_d(sum);
     const float ls = static_cast<float>(static_cast<double>(mx) + log(sum));
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
-      t.lq[i] = t.id[i] >= 0 ? t.lq[i] - ls : -INFINITY;
-      t.q[i] = t.id[i] >= 0 ? expf(t.lq[i]) : 0.f;
+      lq[i] = id[i] >= 0 ? lq[i] - ls : -INFINITY;
+      q[i] = id[i] >= 0 ? expf(lq[i]) : 0.f;
     }
-    t.Q = 1.f;
   } else {
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
-      t.q[i] = 0.f;
-      if (t.id[i] >= 0) {
-        const double e = exp(static_cast<double>(t.lq[i]));
+      q[i] = 0.f;
+      if (id[i] >= 0) {
+        const double e = exp(static_cast<double>(lq[i]));
         sum += e;
-        t.q[i] = static_cast<float>(e);
+        q[i] = static_cast<float>(e);
       } else {
-        t.lq[i] = -INFINITY;
+        lq[i] = -INFINITY;
       }
     }
     sum = warp_sum_d(sum);
-    if (t.n < a.V) {
+    if (n < a.V) {
       const double u = 1.0 - sum;
-      t.qt = static_cast<float>(u < 0x1p-24 ? 0x1p-24 : u);  // a NaN stays one
-      t.lqt = logf(t.qt);
+      qt = static_cast<float>(u < 0x1p-24 ? 0x1p-24 : u);  // a NaN stays one
+      lqt = logf(qt);
     }
-    t.Q = static_cast<float>(sum) + t.qt;
+    Q = static_cast<float>(sum) + qt;
   }
-  t.w = a.weight ? a.weight[row] : 1.f;
-  t.s = static_cast<float>(static_cast<double>(a.grad_scale) * t.w / norm) * a.inv_temp;
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    tab.lq[lane + 32 * i] = lq[i];
+    tab.q[lane + 32 * i] = q[i];
+  }
+  if (lane == 0) {
+    const float w = a.weight ? a.weight[row] : 1.f;
+    tab.qt = qt;
+    tab.lqt = lqt;
+    tab.Q = Q;
+    tab.w = w;
+    tab.s = static_cast<float>(static_cast<double>(a.grad_scale) * w / norm) * a.inv_temp;
+    tab.n = n;
+    tab.bad = bad;
+  }
 }
 
 struct RowSums {
@@ -192,8 +208,8 @@ struct RowSums {
 // One warp: a row's loss terms and gradient values from the teacher's side,
 // the entries' logits z and the tail's statistics; d: the given tokens'
 // gradients.
-__device__ __forceinline__ RowSums row_values(const DistillArgs& a, const Teacher& t, const float (&z)[kPerLane],
-                                              RowStats tail, bool nan, float M, float (&d)[kPerLane], int lane) {
+__device__ __forceinline__ RowSums row_values(const DistillArgs& a, const EntryTable& t, const int (&id)[kPerLane],
+                                              const float (&z)[kPerLane], RowStats tail, bool nan, float M, float (&d)[kPerLane], int lane) {
   const bool has_tail = t.n < a.V;
   // the student: the entries joined to the tail
   const bool tail_any = has_tail && tail.m > -INFINITY;
@@ -202,15 +218,15 @@ __device__ __forceinline__ RowSums row_values(const DistillArgs& a, const Teache
   bool holder = false;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
-    e[i] = t.id[i] >= 0 ? ex2_approx((z[i] - M) * a.c) : 0.f;
-    holder = holder || (t.id[i] >= 0 && z[i] == M);
+    e[i] = id[i] >= 0 ? ex2_approx((z[i] - M) * a.c) : 0.f;
+    holder = holder || (id[i] >= 0 && z[i] == M);
   }
   // one maximum stays out of the sum of the others (r)
   const uint32_t holders = __ballot_sync(0xffffffffu, holder);
   bool out = top_in && lane == __ffs(holders) - 1;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
-    if (out && t.id[i] >= 0 && z[i] == M)
+    if (out && id[i] >= 0 && z[i] == M)
       out = false;
     else
       in += e[i];
@@ -226,13 +242,15 @@ __device__ __forceinline__ RowSums row_values(const DistillArgs& a, const Teache
     pt = fmaxf(s_t * inv_s, kTiny);
     lpt = fmaxf(s_t > 0.f ? -log1pf(s_in / s_t) : -INFINITY, kLnTiny);
   }
-  float F = 0.f, G = 0.f, p[kPerLane], gap[kPerLane];
+  float F = 0.f, G = 0.f, p[kPerLane], q[kPerLane], gap[kPerLane];
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
     const float lp = fmaf(z[i] - M, a.inv_temp, -log_s);
     p[i] = e[i] * inv_s;
-    gap[i] = lp - fmaxf(t.lq[i], kLnTiny);
-    if (t.q[i] > 0.f || t.q[i] != t.q[i]) F += t.q[i] * (t.lq[i] - lp);
+    const float lq = t.lq[lane + 32 * i];
+    q[i] = t.q[lane + 32 * i];
+    gap[i] = lp - fmaxf(lq, kLnTiny);
+    if (q[i] > 0.f || q[i] != q[i]) F += q[i] * (lq - lp);
     if (p[i] > 0.f || p[i] != p[i]) G += p[i] * gap[i];
   }
 #pragma unroll
@@ -259,7 +277,7 @@ __device__ __forceinline__ RowSums row_values(const DistillArgs& a, const Teache
   if (nothing && L == L) L = F = ct = 0.f;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
-    float g = u * (p[i] * t.Q - t.q[i]);
+    float g = u * (p[i] * t.Q - q[i]);
     if (v != 0.f && p[i] > 0.f) g += v * p[i] * (gap[i] - G);
     d[i] = L != L ? L : t.s * g;
   }
@@ -282,41 +300,40 @@ __device__ __forceinline__ RowStats join_parts(const RowStats* part, float floor
   return RowStats{m, warp_sum(r), 0.f};
 }
 
-// Takes a row's entries (loaded into en) into the table and looks for ids
-// named twice.  Whole warp; the table holds no other row's entries.
-template <class F, class S>
-__device__ __forceinline__ void table_row(const DistillArgs& a, S& sm, Teacher& en, const long long (&id_in)[kPerLane],
-                                          int lane, unsigned int& err) {
+// Takes a row's entries into the table (which holds no other row's) and looks
+// for ids out of range (-1 in `id` then) and named twice.  Whole warp.
+template <class F>
+__device__ __forceinline__ void table_row(const DistillArgs& a, EntryTable& tab, const long long (&id_in)[kPerLane],
+                                          int (&id)[kPerLane], int& n, bool& bad, int lane, unsigned int& err) {
   const int V = static_cast<int>(a.V);
-  bool bad = false;
-  int n = 0;
+  bad = false;
+  n = 0;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
     const int j = lane + 32 * i;
-    const long long id = id_in[i];
-    const bool out = id < -1 || id >= V;
+    const bool out = id_in[i] < -1 || id_in[i] >= V;
     if (out) err |= RL_DEVERR_ID_RANGE;
     bad = bad || out;
-    en.id[i] = id >= 0 && !out ? static_cast<int>(id) : -1;
-    if (j < a.K) sm.id[j] = en.id[i];
-    if (en.id[i] >= 0) {
+    id[i] = id_in[i] >= 0 && !out ? static_cast<int>(id_in[i]) : -1;
+    tab.id[j] = id[i];
+    if (id[i] >= 0) {
       ++n;
-      sm.next[j] = atomicExch(&sm.head[(en.id[i] / F::kPiece) & (kTable - 1)], j + 1);
+      tab.next[j] = atomicExch(&tab.head[(id[i] / F::kPiece) & (kTable - 1)], j + 1);
     }
   }
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
-    if (en.id[i] < 0) continue;
+    if (id[i] < 0) continue;
     int same = 0;
-    for (int j = sm.head[(en.id[i] / F::kPiece) & (kTable - 1)]; j; j = sm.next[j - 1]) same += sm.id[j - 1] == en.id[i];
+    for (int j = tab.head[(id[i] / F::kPiece) & (kTable - 1)]; j; j = tab.next[j - 1]) same += tab.id[j - 1] == id[i];
     if (same > 1) {
       err |= RL_DEVERR_ID_REPEAT;
       bad = true;
     }
   }
-  en.bad = __any_sync(0xffffffffu, bad);
-  en.n = __reduce_add_sync(0xffffffffu, n);
+  bad = __any_sync(0xffffffffu, bad);
+  n = __reduce_add_sync(0xffffffffu, n);
 }
 
 // kThreads consumers, the producer warp and the row warp.
@@ -336,17 +353,19 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
   const int n_vecs = (V + F::kVec - 1) / F::kVec;
   const long long row_bytes16 = (static_cast<long long>(V) * F::kBytes + 15) & ~15LL;
   const int n_chunks = static_cast<int>((row_bytes16 + kChunk - 1) / kChunk);
+  const int lead = min(n_chunks, kLead);
 
   if (tid == 0) {
     sm.ring.init(kWarps);
-    mbar_init(smem_addr(&sm.table), 1);
+    mbar_init(smem_addr(&sm.table[0]), 1);
+    mbar_init(smem_addr(&sm.table[1]), 1);
     mbar_init(smem_addr(&sm.sums), kWarps);
     mbar_init(smem_addr(&sm.values), 1);
     mbar_init(smem_addr(&sm.written), kWarps);
     sm.abort = 0;
     fence_mbar_init();
   }
-  for (int i = tid; i < kTable; i += kThreads + 64) sm.head[i] = 0;
+  for (int i = tid; i < 2 * kTable; i += kThreads + 64) sm.tab[i / kTable].head[i % kTable] = 0;
   // N: every CTA counts the mask
   long long N = a.R;
   if (a.mask) {
@@ -369,27 +388,35 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
     bool ok = true;
     RowsOf<true> rows(a.mask, a.R, first, lane);
     const int passes = a.dlogits ? 2 : 1;
+    // chunks [q0, q1) of a row, lane 0; none of row -1
+    auto issue = [&](long long row, int q0, int q1, uint64_t pol) {
+      const unsigned char* src = a.logits + row * a.row_bytes;
+      for (int q = q0; q < q1 && ok; ++q) {
+        ok = sm.ring.reserve(it, abort);
+        if (!ok) break;
+        sm.row_of[it % S::kSlots] = row;
+        const long long off = static_cast<long long>(q) * kChunk;
+        sm.ring.fill(it, src + off, static_cast<uint32_t>(min(static_cast<long long>(kChunk), row_bytes16 - off)), pol);
+        ++it;
+      }
+    };
+    long long prev = -1;  // the row whose second pass is still to be issued
     while (ok) {
       const long long row = rows.next(stride, lane);
       if (lane == 0) {
-        const unsigned char* src = a.logits + row * a.row_bytes;
-        const int n = row < 0 ? 1 : n_chunks * passes;
-        for (int q = 0; q < n; ++q) {
-          ok = sm.ring.reserve(it, abort);
-          if (!ok) break;
-          const uint32_t slot = it % S::kSlots;
-          sm.row_of[slot] = row;
-          if (row < 0) {
-            mbar_arrive(smem_addr(&sm.ring.full[slot]));
-          } else {
-            const long long off = static_cast<long long>(q < n_chunks ? q : q - n_chunks) * kChunk;
-            sm.ring.fill(it, src + off, static_cast<uint32_t>(min(static_cast<long long>(kChunk), row_bytes16 - off)),
-                         q < n_chunks && passes == 2 ? keep : once);
-          }
+        const int first_q = prev >= 0 ? lead : n_chunks;
+        if (row >= 0) {
+          issue(row, 0, first_q, passes == 2 ? keep : once);
+        } else if (ok && (ok = sm.ring.reserve(it, abort))) {
+          sm.row_of[it % S::kSlots] = -1;
+          mbar_arrive(smem_addr(&sm.ring.full[it % S::kSlots]));
           ++it;
         }
+        if (prev >= 0 && passes == 2) issue(prev, 0, n_chunks, once);
+        if (row >= 0) issue(row, first_q, n_chunks, passes == 2 ? keep : once);
         if (!ok) sm.ring.drain(it);
       }
+      prev = row;
       ok = __shfl_sync(0xffffffffu, ok, 0) && row >= 0;
     }
   } else if (warp == kWarps + 1) {
@@ -397,41 +424,45 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
     unsigned int err = 0;
     double acc[5] = {0.0, 0.0, 0.0, 0.0, 0.0};
     RowsOf<true> rows(a.mask, a.R, first, lane);
-    Teacher en;
-    long long id_in[kPerLane];
-    auto load_row = [&](long long row) {
+    // the table and the teacher's side of this CTA's k-th row
+    auto prepare = [&](long long row, uint32_t k) {
+      long long id_in[kPerLane];
+      float lq[kPerLane];
+      int id[kPerLane], n;
+      bool bad;
 #pragma unroll
       for (int i = 0; i < kPerLane; ++i) {
         const int j = lane + 32 * i;
-        id_in[i] = row >= 0 && j < K ? a.ids[row * K + j] : -1;
-        en.lq[i] = row >= 0 && j < K ? a.lq[row * K + j] : 0.f;
+        id_in[i] = j < K ? a.ids[row * K + j] : -1;
+        lq[i] = j < K ? a.lq[row * K + j] : 0.f;
       }
-    };
-    long long row = rows.next(stride, lane);
-    load_row(row);
-    auto prepare = [&] {
-      table_row<F>(a, sm, en, id_in, lane, err);
+      table_row<F>(a, sm.tab[k & 1], id_in, id, n, bad, lane, err);
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&sm.table));
-      teacher_values(a, en, norm, row);  // while the row streams
+      if (lane == 0) mbar_arrive(smem_addr(&sm.table[k & 1]));
+      teacher_values(a, sm.tab[k & 1], id, lq, n, bad, norm, row, lane);
+      __syncwarp();
     };
-    if (row >= 0) prepare();
-    for (uint32_t done = 0; row >= 0; ++done) {
-      const unsigned char* src = a.logits + row * a.row_bytes;
-      if (!__all_sync(0xffffffffu, wait_bounded<false>(smem_addr(&sm.sums), done & 1, abort))) break;
+    long long row = rows.next(stride, lane), row_nxt = row >= 0 ? rows.next(stride, lane) : -1;
+    if (row >= 0) prepare(row, 0);
+    if (row_nxt >= 0) prepare(row_nxt, 1);
+    for (uint32_t k = 0; row >= 0; ++k) {
+      EntryTable& tab = sm.tab[k & 1];
+      if (!__all_sync(0xffffffffu, wait_bounded<false>(smem_addr(&sm.sums), k & 1, abort))) break;
       RowStats tail = join_parts<kWarps>(sm.part, F::kFloor, a.c, lane);
       const bool nan = __any_sync(0xffffffffu, lane < kWarps && sm.nan[lane < kWarps ? lane : 0] != 0.f);
+      int id[kPerLane];
       float z[kPerLane], M = tail.m;
 #pragma unroll
       for (int i = 0; i < kPerLane; ++i) {
-        z[i] = en.id[i] >= 0 ? sm.z[lane + 32 * i] : -INFINITY;
+        id[i] = tab.id[lane + 32 * i];
+        z[i] = id[i] >= 0 ? tab.z[lane + 32 * i] : -INFINITY;
         M = max_nan(M, z[i]);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
       const bool plain = needs_exact<F>(M, a.c);
       if (plain) {
-        tail = exact_tail<F>(src, V, a.c, sm, lane);
+        tail = exact_tail<F>(a.logits + row * a.row_bytes, V, a.c, tab, lane);
         M = tail.m;
 #pragma unroll
         for (int i = 0; i < kPerLane; ++i) M = max_nan(M, z[i]);
@@ -439,7 +470,7 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
         for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
       }
       float d[kPerLane];
-      const RowSums t = row_values(a, en, z, tail, nan, M, d, lane);
+      const RowSums t = row_values(a, tab, id, z, tail, nan, M, d, lane);
       if (lane == 0) {
         sm.m = t.m;
         sm.factor = t.factor;
@@ -452,25 +483,23 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
         acc[4] += t.pt;
         if (a.row_loss) a.row_loss[row] = static_cast<float>(t.loss);
       }
-      // the table for the next row (every consumer is past the first pass)
-      int old_id[kPerLane];
-#pragma unroll
-      for (int i = 0; i < kPerLane; ++i) {
-        old_id[i] = en.id[i];
-        if (old_id[i] >= 0) sm.head[(old_id[i] / F::kPiece) & (kTable - 1)] = 0;
-      }
+      // this row's table for the row after next (every consumer is past its first pass)
       __syncwarp();
-      const long long prev = row;
-      row = rows.next(stride, lane);
-      load_row(row);
-      if (row >= 0) prepare();
+#pragma unroll
+      for (int i = 0; i < kPerLane; ++i)
+        if (id[i] >= 0) tab.head[(id[i] / F::kPiece) & (kTable - 1)] = 0;
+      __syncwarp();
+      const long long done_row = row;
+      row = row_nxt;
+      row_nxt = row >= 0 ? rows.next(stride, lane) : -1;
+      if (row_nxt >= 0) prepare(row_nxt, k);
       // the given tokens' gradients over what the consumers have written there
       if (a.dlogits) {
-        if (!__all_sync(0xffffffffu, wait_bounded<false>(smem_addr(&sm.written), done & 1, abort))) break;
-        unsigned char* dst = a.dlogits + prev * a.row_bytes;
+        if (!__all_sync(0xffffffffu, wait_bounded<false>(smem_addr(&sm.written), k & 1, abort))) break;
+        unsigned char* dst = a.dlogits + done_row * a.row_bytes;
 #pragma unroll
         for (int i = 0; i < kPerLane; ++i)
-          if (old_id[i] >= 0) F::store(dst, old_id[i], d[i]);
+          if (id[i] >= 0) F::store(dst, id[i], d[i]);
       }
     }
     // this CTA's sums, then the last CTA adds all of them in CTA order
@@ -525,35 +554,28 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
       }
     }
     const int n_full = V / F::kPiece / kThreads;  // chunks whose every piece is a full one
-    WarpStats st;
-    st.low = false;
     uint32_t it = 0;
-    for (uint32_t done = 0;; ++done) {
-      sm.ring.wait(it, abort);
-      const long long row = sm.row_of[it % S::kSlots];
-      // (after a timeout the whole warp stops; nothing here meets another warp)
-      if (__any_sync(0xffffffffu, row < 0 || *abort)) break;
-      const unsigned char* src = a.logits + row * a.row_bytes;
-      unsigned char* dst = a.dlogits + row * a.row_bytes;
-      wait_bounded<false>(smem_addr(&sm.table), done & 1, abort);
-      // pass 1: the statistics of every token that is not given
-      warp_stats_init<F>(st, a.c);
-      bool nan = false;
-      for (int i = 0; i < n_chunks; ++i, ++it) {
+    WarpStats st;  // of the row whose first pass is under way
+    st.low = false;
+    bool nan = false;
+    // pass 1 over chunks [i0, i1) of the k-th row: every token that is not given
+    auto pass1 = [&](uint32_t k, int i0, int i1) {
+      EntryTable& tab = sm.tab[k & 1];
+      for (int i = i0; i < i1; ++i, ++it) {
         const uint32_t buf = sm.ring.wait(it, abort);
         const int p = i * kThreads + tid;
         const bool last = i >= n_full;
         uint32_t w[16];
         const int sh = last ? 0 : lane >> 1;
         load_piece(w, 0, buf + tid * kPieceBytes, sh);
-        int j = p < n_pieces ? sm.head[p & (kTable - 1)] : 0;
+        int j = p < n_pieces ? tab.head[p & (kTable - 1)] : 0;
         while (j) {
-          const int e = sm.id[j - 1] - p * F::kPiece;
+          const int e = tab.id[j - 1] - p * F::kPiece;
           if (e >= 0 && e < F::kPiece) {
-            sm.z[j - 1] = F::load_shared(sm.ring.data[it % S::kSlots] + tid * kPieceBytes, e);
+            tab.z[j - 1] = F::load_shared(sm.ring.data[it % S::kSlots] + tid * kPieceBytes, e);
             F::drop(w, 0, (((e / F::kVec) - sh) & 3) * F::kVec + e % F::kVec);
           }
-          j = sm.next[j - 1];
+          j = tab.next[j - 1];
         }
         sm.ring.release(it, lane);
         if (last) F::cut(w, 0, p < n_pieces ? min(F::kPiece, V - p * F::kPiece) : 0);
@@ -561,17 +583,9 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
         nan = nan || pm != pm;
         add_piece<F, false>(st, w, max_nan(pm, F::kFloor), a.c, lane, false);
       }
-      const RowStats ws = warp_stats_sum<F>(st, a.c);
-      nan = __any_sync(0xffffffffu, nan);
-      if (lane == 0) {
-        sm.part[warp] = ws;
-        sm.nan[warp] = nan ? 1.f : 0.f;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&sm.sums));
-      wait_bounded<false>(smem_addr(&sm.values), done & 1, abort);
-      if (!a.dlogits) continue;
-      // pass 2
+    };
+    auto pass2 = [&](long long row) {
+      unsigned char* dst = a.dlogits + row * a.row_bytes;
       const float m = sm.m;
       const bool plain = sm.plain != 0;
       const float nm = -m * a.c, rho = fmaf(-m, a.c, -nm);
@@ -610,6 +624,42 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sm.written));
+    };
+    // Each step: the first `lead` chunks of the next row's first pass (the time
+    // the row warp has for the row before), that row's second pass, then the
+    // rest of the first pass.  The first step has no row before, the last no
+    // next one.  After a timeout the whole warp stops; nothing meets another warp.
+    long long prev = -1;
+    for (uint32_t k = 0;; ++k) {
+      sm.ring.wait(it, abort);
+      const long long row = sm.row_of[it % S::kSlots];
+      if (__any_sync(0xffffffffu, *abort)) break;
+      const int lead_q = prev >= 0 ? lead : n_chunks;
+      if (row >= 0) {
+        wait_bounded<false>(smem_addr(&sm.table[k & 1]), (k >> 1) & 1, abort);
+        warp_stats_init<F>(st, a.c);
+        nan = false;
+      } else {
+        sm.ring.release(it++, lane);  // the end's empty chunk
+      }
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+        if (row >= 0) pass1(k, part ? lead_q : 0, part ? n_chunks : lead_q);
+        if (part == 0 && prev >= 0) {
+          wait_bounded<false>(smem_addr(&sm.values), (k - 1) & 1, abort);
+          if (a.dlogits) pass2(prev);
+        }
+      }
+      if (row < 0) break;
+      const RowStats ws = warp_stats_sum<F>(st, a.c);
+      nan = __any_sync(0xffffffffu, nan);
+      if (lane == 0) {
+        sm.part[warp] = ws;
+        sm.nan[warp] = nan ? 1.f : 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sm.sums));
+      prev = row;
     }
   }
 }
