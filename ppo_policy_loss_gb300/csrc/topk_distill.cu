@@ -53,7 +53,7 @@ struct DistillArgs {
   WsPartial* partials;
   long long R, V, row_bytes;
   float inv_temp, c;  // 1 / temperature, log2(e) / temperature
-  float reverse, grad_scale;
+  float temperature, reverse, grad_scale;
   double norm;
   int K, renorm;
 };
@@ -140,35 +140,60 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// e^y for y <= 88 as the sum of two floats (in fp64), relative error below
+// 2^-26: y - n ln 2 is exact (the head of ln 2 has 16 bits), and of 1 + f +
+// f^2 / 2 + ... only the terms from f^2 on are rounded to fp32.  A fraction of
+// the fp64 exponential's time on a GPU with few fp64 units.
+__device__ __forceinline__ double exp_sum(float y) {
+  constexpr float kLn2Head = 45426.0f / 65536.0f;
+  constexpr float kLn2Rest = static_cast<float>(0.69314718055994530942 - 45426.0 / 65536.0);
+  if (!(y > -87.f)) return y != y ? static_cast<double>(y) : 0.0;  // (2^-126 and less)
+  const float n = fminf(rintf(y * kLog2e), 128.f);
+  const float f = fmaf(n, -kLn2Head, y);
+  float p = 1.f / 40320.f;
+  p = fmaf(p, f, 1.f / 5040.f);
+  p = fmaf(p, f, 1.f / 720.f);
+  p = fmaf(p, f, 1.f / 120.f);
+  p = fmaf(p, f, 1.f / 24.f);
+  p = fmaf(p, f, 1.f / 6.f);
+  p = fmaf(p, f, 0.5f);
+  p *= f * f;  // e^f - 1 - f
+  const float g = -n * kLn2Rest;  // e^(f + g) = e^f (1 + g + g^2 / 2 ...), |g| < 2e-4
+  const float hi = 1.f + f, lo = (f - (hi - 1.f)) + fmaf(g * (hi + p), fmaf(0.5f, g, 1.f), p);
+  const float scale = __int_as_float((static_cast<int>(n) + 127) << 23);
+  return static_cast<double>(hi * scale) + static_cast<double>(lo * scale);
+}
+
 // The teacher's side of a row into its table, by one warp, from the entries'
 // ids (-1: none) and log-probabilities, four a lane.
 __device__ __forceinline__ void teacher_values(const DistillArgs& a, EntryTable& tab, const int (&id)[kPerLane],
-                                               float (&lq)[kPerLane], int n, bool bad, double norm, long long row,
+                                               float (&lq)[kPerLane], float w, int n, bool bad, double scale,
                                                int lane) {
-  // 1 - sum q in fp64, where it is a difference of near numbers
-  double sum = 0.0;
+  double sum = 0.0;  // 1 - sum q is a difference of near numbers
   float q[kPerLane], qt = 0.f, lqt = 0.f, Q = 1.f;
   if (a.renorm) {
-    float mx = -INFINITY;
+    float mx = -INFINITY, e = 0.f;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) mx = id[i] >= 0 ? fmaxf(mx, lq[i]) : mx;
     mx = warp_max(mx);
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i)
-      if (id[i] >= 0) sum += exp(static_cast<double>(lq[i]) - static_cast<double>(mx));
-    sum = warp_sum_d(sum);
-    const float ls = static_cast<float>(static_cast<double>(mx) + log(sum));
+    for (int i = 0; i < kPerLane; ++i) {
+      q[i] = id[i] >= 0 ? expf(lq[i] - mx) : 0.f;
+      e += q[i];
+    }
+    e = warp_sum(e);
+    const float inv = 1.f / e, ls = logf(e);
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
-      lq[i] = id[i] >= 0 ? lq[i] - ls : -INFINITY;
-      q[i] = id[i] >= 0 ? expf(lq[i]) : 0.f;
+      lq[i] = id[i] >= 0 ? (lq[i] - mx) - ls : -INFINITY;
+      q[i] = id[i] >= 0 ? q[i] * inv : 0.f;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
       q[i] = 0.f;
       if (id[i] >= 0) {
-        const double e = exp(static_cast<double>(lq[i]));
+        const double e = exp_sum(lq[i]);
         sum += e;
         q[i] = static_cast<float>(e);
       } else {
@@ -189,12 +214,11 @@ __device__ __forceinline__ void teacher_values(const DistillArgs& a, EntryTable&
     tab.q[lane + 32 * i] = q[i];
   }
   if (lane == 0) {
-    const float w = a.weight ? a.weight[row] : 1.f;
     tab.qt = qt;
     tab.lqt = lqt;
     tab.Q = Q;
     tab.w = w;
-    tab.s = static_cast<float>(static_cast<double>(a.grad_scale) * w / norm) * a.inv_temp;
+    tab.s = static_cast<float>(scale * w);
     tab.n = n;
     tab.bad = bad;
   }
@@ -424,27 +448,38 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
     unsigned int err = 0;
     double acc[5] = {0.0, 0.0, 0.0, 0.0, 0.0};
     RowsOf<true> rows(a.mask, a.R, first, lane);
-    // the table and the teacher's side of this CTA's k-th row
-    auto prepare = [&](long long row, uint32_t k) {
-      long long id_in[kPerLane];
-      float lq[kPerLane];
-      int id[kPerLane], n;
-      bool bad;
+    // the table and the teacher's side of this CTA's k-th row, from what was
+    // fetched a row ahead
+    const double scale = static_cast<double>(a.grad_scale) / (norm * static_cast<double>(a.temperature));
+    long long id_in[kPerLane];
+    float lq_in[kPerLane], w_in = 1.f;
+    auto fetch = [&](long long row) {
+      if (row < 0) return;
 #pragma unroll
       for (int i = 0; i < kPerLane; ++i) {
         const int j = lane + 32 * i;
         id_in[i] = j < K ? a.ids[row * K + j] : -1;
-        lq[i] = j < K ? a.lq[row * K + j] : 0.f;
+        lq_in[i] = j < K ? a.lq[row * K + j] : 0.f;
       }
+      if (a.weight) w_in = a.weight[row];
+    };
+    auto prepare = [&](uint32_t k) {
+      int id[kPerLane], n;
+      bool bad;
       table_row<F>(a, sm.tab[k & 1], id_in, id, n, bad, lane, err);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sm.table[k & 1]));
-      teacher_values(a, sm.tab[k & 1], id, lq, n, bad, norm, row, lane);
+      teacher_values(a, sm.tab[k & 1], id, lq_in, w_in, n, bad, scale, lane);
       __syncwarp();
     };
-    long long row = rows.next(stride, lane), row_nxt = row >= 0 ? rows.next(stride, lane) : -1;
-    if (row >= 0) prepare(row, 0);
-    if (row_nxt >= 0) prepare(row_nxt, 1);
+    long long row = rows.next(stride, lane);
+    fetch(row);
+    long long row_1 = row >= 0 ? rows.next(stride, lane) : -1;
+    if (row >= 0) prepare(0);
+    fetch(row_1);
+    long long row_2 = row_1 >= 0 ? rows.next(stride, lane) : -1;
+    if (row_1 >= 0) prepare(1);
+    fetch(row_2);
     for (uint32_t k = 0; row >= 0; ++k) {
       EntryTable& tab = sm.tab[k & 1];
       if (!__all_sync(0xffffffffu, wait_bounded<false>(smem_addr(&sm.sums), k & 1, abort))) break;
@@ -490,9 +525,11 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
         if (id[i] >= 0) tab.head[(id[i] / F::kPiece) & (kTable - 1)] = 0;
       __syncwarp();
       const long long done_row = row;
-      row = row_nxt;
-      row_nxt = row >= 0 ? rows.next(stride, lane) : -1;
-      if (row_nxt >= 0) prepare(row_nxt, k);
+      row = row_1;
+      row_1 = row_2;
+      row_2 = row_1 >= 0 ? rows.next(stride, lane) : -1;
+      if (row_1 >= 0) prepare(k);
+      fetch(row_2);
       // the given tokens' gradients over what the consumers have written there
       if (a.dlogits) {
         if (!__all_sync(0xffffffffu, wait_bounded<false>(smem_addr(&sm.written), k & 1, abort))) break;
@@ -759,6 +796,7 @@ extern "C" rl_status rl_topk_distill_fwd_bwd(const rl_topk_distill_desc* d, void
   a.row_bytes = row_bytes;
   a.inv_temp = 1.f / d->temperature;
   a.c = static_cast<float>(1.4426950408889634 / static_cast<double>(d->temperature));
+  a.temperature = d->temperature;
   a.reverse = d->reverse;
   a.grad_scale = d->grad_scale;
   a.norm = d->norm;
