@@ -199,7 +199,7 @@ constexpr int kChunk = kRowThreads * kPieceBytes;  // one piece per consumer thr
 constexpr int kSlots = 4;
 constexpr int kMaxCluster = 8;
 constexpr int kLpThreads = kRowThreads + 32;  // consumers and the producer warp
-constexpr int kLpCtas = 4;                    // CTAs a SM holds, registers permitting
+constexpr int kLpCtas = 5;                    // CTAs a SM holds, registers permitting
 constexpr int kSmemPerSm = 228 * 1024;
 
 template <int DT>
@@ -273,11 +273,10 @@ __device__ __forceinline__ int count_reaching(const uint32_t (&best)[2], uint32_
 // ranked by counting.  False if a list overflows (many equal values, or a
 // large k of few pieces): search_slow then.
 template <int DT>
-__device__ __forceinline__ bool search_fast(LpSmem<DT>& sm, const typename Fmt<DT>::Key* keys, const unsigned char* src,
+__device__ __noinline__ bool search_fast(LpSmem<DT>& sm, const typename Fmt<DT>::Key* keys, const unsigned char* src,
                                             int g0, int n_mine, int V, int k, const uint32_t (&best)[2], uint32_t top,
                                             int tid) {
   using F = Fmt<DT>;
-  const int lane = tid & 31, warp = tid >> 5;
   const bool both = k > 32;
   const int enough = k + k / 8 + 4;
   if (tid == 0) sm.n_pieces = sm.n_elems = 0;
@@ -586,7 +585,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
       if (csize > 1) {
         // every CTA's findings into rank 0's memory
         if (done > 0 && rank != 0) wait_bounded<true>(smem_addr(&sm.freed), (done - 1) & 1, abort);
-        if (tid < k) st_cluster_u64(map_to_rank(smem_addr(&join_keys[rank * kMaxK + tid]), 0), sm.found[tid]);
+        if (tid < k) st_cluster_u64(map_to_rank(smem_addr(&join_keys[rank * k + tid]), 0), sm.found[tid]);
         if (tid == 0) {
           const uint32_t to = map_to_rank(smem_addr(&sm.join_part[rank]), 0);
           st_cluster_f32(to, rs.m);
@@ -600,9 +599,16 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
           wait_bounded<true>(smem_addr(&sm.arrived), done & 1, abort);
           rs = sm.join_part[0];
           for (int q = 1; q < csize; ++q) rs = merge_row(rs, sm.join_part[q], a.c);
-          if (k)
-            block_select<ElemKey>([&](int i) { return i % kMaxK < k ? join_keys[i] : 0ull; }, csize * kMaxK, k,
-                                  join_top, sm.join_sel, tid);
+          const int n = csize * k;
+          if (n > kList) {
+            block_select<ElemKey>([&](int i) { return join_keys[i]; }, n, k, join_top, sm.join_sel, tid);
+          } else {
+            for (int q = tid; q < n; q += kRowThreads) {
+              const ElemKey key = join_keys[q];
+              const int r = rank_of(join_keys, n, key);
+              if (key && r < k) join_top[r] = key;
+            }
+          }
           row_barrier();  // everything has been read: the others may send the next row
           if (tid > 0 && tid < csize) mbar_arrive_remote(map_to_rank(smem_addr(&sm.freed), tid));
         }
@@ -798,7 +804,7 @@ rl_status launch_fwd(const LpArgs& a, int dev, int sms, cudaStream_t stream) {
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = c > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<DT, kEntropy>, a) == cudaSuccess ? RL_OK : RL_ERR_CUDA;
 }
 

@@ -415,8 +415,8 @@ __device__ __forceinline__ void end_frame(const WarpStats& a, float c, float& r,
 }
 
 // One step: this lane's piece (raw words), of clamped maximum pm.  Warp-wide.
-// -inf words add 0 to r; their NaN in t (0 * inf) is looked for where `check`
-// says so, and from then on the words are clamped at the floor first.
+// -inf words add 0 to r, but NaN to t (0 * inf): they are looked for where
+// `check` says so, and from then on the words are clamped at the floor first.
 template <class F, bool kEntropy>
 __device__ __forceinline__ void add_piece(WarpStats& a, uint32_t (&w)[16], float pm, float c, int lane, bool check) {
   float wm;
@@ -444,33 +444,83 @@ __device__ __forceinline__ void add_piece(WarpStats& a, uint32_t (&w)[16], float
     a.t[0] = make_float2(kEntropy ? h * fmaf(-rho, kept, f * fmaf(-d, s, t)) : 0.f, 0.f);
     a.t[1] = make_float2(0.f, 0.f);
   }
-  const float2 c2 = make_float2(c, c), nm2 = make_float2(a.nm, a.nm);
+  if (kEntropy && check && !a.low) {
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) any = any || F::clamp(w[i]) != w[i];
+    a.low = __any_sync(0xffffffffu, any);
+  }
   if (kEntropy && a.low) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = F::clamp(w[i]);
   }
-  const float2 r0 = a.r[0], r1 = a.r[1], t0 = a.t[0], t1 = a.t[1];
+  const float2 c2 = make_float2(c, c), nm2 = make_float2(a.nm, a.nm);
+#pragma unroll
+  for (int i = 0; i < F::kPiece / 2; ++i) {
+    float2 z;
+    F::template pair<16>(w, i, z.x, z.y);
+    const float2 x = __ffma2_rn(z, c2, nm2);
+    const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+    a.r[i & 1] = __fadd2_rn(a.r[i & 1], e);
+    if (kEntropy) a.t[i & 1] = __ffma2_rn(e, x, a.t[i & 1]);
+  }
+}
+
+// The sum of 2^x alone, over sets whose maximum need not be known: the frame
+// is that of the maximum of the warp's first piece, and moves up only when a
+// lane's sum passes kSumLimit.
+constexpr float kSumLimit = 0x1p24f;
+struct WarpSum {
+  float m, nm;
+  float2 r[2];  // independent chains
+};
+template <class F>
+__device__ __forceinline__ float clamped_max(const uint32_t (&w)[16]) {
+  float wm;
+  const float pm = max_nan(F::raw_value(F::raw_max(w, 0)), F::kFloor);
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(wm) : "f"(pm));
+  return wm;
+}
+template <class F>
+__device__ __forceinline__ void sum_init(WarpSum& a, const uint32_t (&w)[16], float c) {
+  a.m = clamped_max<F>(w);
+  if (!(a.m >= F::kFloor)) a.m = F::kFloor;  // nothing but NaN
+  a.nm = -a.m * c;
+  a.r[0] = a.r[1] = make_float2(0.f, 0.f);
+}
+template <class F>
+__device__ __forceinline__ void sum_piece(WarpSum& a, const uint32_t (&w)[16], float c) {
+  const float2 r0 = a.r[0], r1 = a.r[1];
+  const float2 c2 = make_float2(c, c);
+  bool again = false;
+#pragma unroll 1
   while (true) {
+    const float2 nm2 = make_float2(a.nm, a.nm);
 #pragma unroll
     for (int i = 0; i < F::kPiece / 2; ++i) {
       float2 z;
       F::template pair<16>(w, i, z.x, z.y);
       const float2 x = __ffma2_rn(z, c2, nm2);
-      const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-      a.r[i & 1] = __fadd2_rn(a.r[i & 1], e);
-      if (kEntropy) a.t[i & 1] = __ffma2_rn(e, x, a.t[i & 1]);
+      a.r[i & 1] = __fadd2_rn(a.r[i & 1], make_float2(ex2_approx(x.x), ex2_approx(x.y)));
     }
-    if (!kEntropy || !check || a.low) break;
-    const float t = (a.t[0].x + a.t[0].y) + (a.t[1].x + a.t[1].y);
-    if (!__any_sync(0xffffffffu, t != t)) break;
-    a.low = true;
-    a.r[0] = r0;
-    a.r[1] = r1;
-    a.t[0] = t0;
-    a.t[1] = t1;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = F::clamp(w[i]);
+    const float s = (a.r[0].x + a.r[0].y) + (a.r[1].x + a.r[1].y);
+    if (again || !__any_sync(0xffffffffu, !(s < kSumLimit))) break;
+    const float m = fmaxf(a.m, clamped_max<F>(w));
+    const float f = ex2_approx((a.m - m) * c);
+    a.m = m;
+    a.nm = -m * c;
+    a.r[0] = make_float2(f * ((r0.x + r0.y) + (r1.x + r1.y)), 0.f);
+    a.r[1] = make_float2(0.f, 0.f);
+    again = true;  // (a NaN passes)
   }
+}
+template <class F>
+__device__ __forceinline__ RowStats warp_sum_stats(const WarpSum& a, float c) {
+  float r = (a.r[0].x + a.r[0].y) + (a.r[1].x + a.r[1].y);
+  r *= ex2_approx(fmaf(-a.m, c, -a.nm));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+  return RowStats{a.m, r - 1.f, 0.f};
 }
 
 // The warp's statistics in every lane.

@@ -80,7 +80,6 @@ struct DistillSmem {
   long long row_of[kSlots];    // the row a chunk belongs to
   EntryTable tab[2];           // of the even and the odd rows of this CTA
   RowStats part[kWarps];
-  float nan[kWarps];           // not 0: the warp met a NaN
   long long wcount[kWarps + 2];
   unsigned long long table[2];  // a row's entries are in tab[k & 1]
   unsigned long long sums, values, written;  // once a row: sums in, values out, row written
@@ -233,11 +232,12 @@ struct RowSums {
 // the entries' logits z and the tail's statistics; d: the given tokens'
 // gradients.
 __device__ __forceinline__ RowSums row_values(const DistillArgs& a, const EntryTable& t, const int (&id)[kPerLane],
-                                              const float (&z)[kPerLane], RowStats tail, bool nan, float M, float (&d)[kPerLane], int lane) {
+                                              const float (&z)[kPerLane], RowStats tail, float M, float (&d)[kPerLane], int lane) {
   const bool has_tail = t.n < a.V;
-  // the student: the entries joined to the tail
+  // the student: the entries joined to the tail, in the frame of M, the larger
+  // of the entries' maximum and the tail's reference
   const bool tail_any = has_tail && tail.m > -INFINITY;
-  const bool top_in = !tail_any || M > tail.m || !(tail.m >= M);  // the row's maximum is an entry
+  const bool top_in = !tail_any || M > tail.m || !(tail.m >= M);  // M is an entry's
   float e[kPerLane], in = 0.f;
   bool holder = false;
 #pragma unroll
@@ -296,7 +296,7 @@ __device__ __forceinline__ RowSums row_values(const DistillArgs& a, const EntryT
     ct += v * (lpt - t.lqt - G);
   }
   const bool nothing = a.renorm && t.n == 0;
-  if (t.bad || nan || r != r) L = __int_as_float(0x7fc00000);
+  if (t.bad || r != r) L = __int_as_float(0x7fc00000);
   if (!(M > -INFINITY)) L = __int_as_float(0x7fc00000);  // no distribution
   if (nothing && L == L) L = F = ct = 0.f;
 #pragma unroll
@@ -484,7 +484,6 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
       EntryTable& tab = sm.tab[k & 1];
       if (!__all_sync(0xffffffffu, wait_bounded<false>(smem_addr(&sm.sums), k & 1, abort))) break;
       RowStats tail = join_parts<kWarps>(sm.part, F::kFloor, a.c, lane);
-      const bool nan = __any_sync(0xffffffffu, lane < kWarps && sm.nan[lane < kWarps ? lane : 0] != 0.f);
       int id[kPerLane];
       float z[kPerLane], M = tail.m;
 #pragma unroll
@@ -505,7 +504,7 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
         for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
       }
       float d[kPerLane];
-      const RowSums t = row_values(a, tab, id, z, tail, nan, M, d, lane);
+      const RowSums t = row_values(a, tab, id, z, tail, M, d, lane);
       if (lane == 0) {
         sm.m = t.m;
         sm.factor = t.factor;
@@ -592,9 +591,7 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
     }
     const int n_full = V / F::kPiece / kThreads;  // chunks whose every piece is a full one
     uint32_t it = 0;
-    WarpStats st;  // of the row whose first pass is under way
-    st.low = false;
-    bool nan = false;
+    WarpSum st;  // of the row whose first pass is under way
     // pass 1 over chunks [i0, i1) of the k-th row: every token that is not given
     auto pass1 = [&](uint32_t k, int i0, int i1) {
       EntryTable& tab = sm.tab[k & 1];
@@ -616,19 +613,49 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
         }
         sm.ring.release(it, lane);
         if (last) F::cut(w, 0, p < n_pieces ? min(F::kPiece, V - p * F::kPiece) : 0);
-        const float pm = F::raw_value(F::raw_max(w, 0));
-        nan = nan || pm != pm;
-        add_piece<F, false>(st, w, max_nan(pm, F::kFloor), a.c, lane, false);
+        __syncwarp();
+        if (i == 0) sum_init<F>(st, w, a.c);
+        sum_piece<F>(st, w, a.c);
       }
     };
+    // pass 2: 2^((z - m) c) factor.  16-bit outputs take |factor| into the
+    // exponent (one rounding of at most 2^-15 for |m c| <= 1024, far below
+    // theirs) and the sign on the packed result; fp32 outputs multiply.
+    const int n_full2 = n_vecs / kVecs - (V % F::kVec && n_vecs % kVecs == 0 ? 1 : 0);  // chunks of full vectors only
     auto pass2 = [&](long long row) {
       unsigned char* dst = a.dlogits + row * a.row_bytes;
-      const float m = sm.m;
-      const bool plain = sm.plain != 0;
+      const float m = sm.m, factor = sm.factor;
+      constexpr bool kFold = F::kBytes == 2;
       const float nm = -m * a.c, rho = fmaf(-m, a.c, -nm);
-      const float factor = plain ? sm.factor : sm.factor * ex2_approx(rho);
-      const float2 c2 = make_float2(a.c, a.c), f2 = make_float2(factor, factor);
-      const float2 nm2 = make_float2(nm, nm), dm2 = make_float2(-m, -m);
+      const bool plain = sm.plain != 0 || (kFold && !(fabsf(nm) <= 1024.f));  // by differences to m
+      const float add = kFold ? log2f(fabsf(factor)) : 0.f;
+      const float mul = kFold ? 1.f : plain ? factor : factor * ex2_approx(rho);
+      const uint32_t sign = kFold && factor < 0.f ? 0x80008000u : 0u;
+      const float2 c2 = make_float2(a.c, a.c), m2 = make_float2(mul, mul);
+      const float b = kFold ? nm + (rho + add) : nm;
+      const float2 b2 = make_float2(b, b);
+      auto vec = [&](const uint4& w) {
+        float z[F::kVec];
+        F::unpack(w, z);
+#pragma unroll
+        for (int j = 0; j < F::kVec; j += 2) {
+          const float2 x = __ffma2_rn(make_float2(z[j], z[j + 1]), c2, b2);
+          float2 d = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+          if (!kFold) d = __fmul2_rn(d, m2);
+          z[j] = d.x;
+          z[j + 1] = d.y;
+        }
+        uint4 u = F::pack(z);
+        if (kFold) u = make_uint4(u.x ^ sign, u.y ^ sign, u.z ^ sign, u.w ^ sign);
+        return u;
+      };
+      auto vec_plain = [&](const uint4& w) {
+        float z[F::kVec];
+        F::unpack(w, z);
+#pragma unroll
+        for (int j = 0; j < F::kVec; ++j) z[j] = ex2_approx((z[j] - m) * a.c) * factor;
+        return F::pack(z);
+      };
       for (int i = 0; i < n_chunks; ++i, ++it) {
         const uint32_t buf = sm.ring.wait(it, abort);
         uint4 w[kVecsPerThread];
@@ -637,25 +664,26 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
         sm.ring.release(it, lane);
         const int v0 = i * kVecs + tid;
         unsigned char* out = dst + static_cast<long long>(v0) * 16;
+        if (i < n_full2 && !plain) {
 #pragma unroll
-        for (int q = 0; q < kVecsPerThread; ++q) {
-          float z[F::kVec];
-          F::unpack(w[q], z);
+          for (int q = 0; q < kVecsPerThread; ++q) st_global_cs_v4(out + q * kThreads * 16, vec(w[q]));
+        } else {
+#pragma unroll 1
+          for (int q = 0; q < kVecsPerThread; ++q) {
+            const int v = v0 + q * kThreads;
+            uint4 wq = w[0];
 #pragma unroll
-          for (int j = 0; j < F::kVec; j += 2) {
-            const float2 zz = make_float2(z[j], z[j + 1]);
-            const float2 x = plain ? __fmul2_rn(__fadd2_rn(zz, dm2), c2) : __ffma2_rn(zz, c2, nm2);
-            const float2 d = __fmul2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), f2);
-            z[j] = d.x;
-            z[j + 1] = d.y;
-          }
-          const int v = v0 + q * kThreads;
-          if ((v + 1) * F::kVec <= V) {
-            st_global_cs_v4(out + q * kThreads * 16, F::pack(z));
-          } else if (v < n_vecs) {
+            for (int j = 1; j < kVecsPerThread; ++j) wq = j == q ? w[j] : wq;
+            const uint4 u = plain ? vec_plain(wq) : vec(wq);
+            if ((v + 1) * F::kVec <= V) {
+              st_global_cs_v4(out + q * kThreads * 16, u);
+            } else if (v < n_vecs) {
+              float z[F::kVec];
+              F::unpack(u, z);
 #pragma unroll
-            for (int j = 0; j < F::kVec; ++j)
-              if (v * F::kVec + j < V) F::store(dst, v * F::kVec + j, z[j]);
+              for (int j = 0; j < F::kVec; ++j)
+                if (v * F::kVec + j < V) F::store(dst, v * F::kVec + j, z[j]);
+            }
           }
         }
       }
@@ -674,8 +702,6 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
       const int lead_q = prev >= 0 ? lead : n_chunks;
       if (row >= 0) {
         wait_bounded<false>(smem_addr(&sm.table[k & 1]), (k >> 1) & 1, abort);
-        warp_stats_init<F>(st, a.c);
-        nan = false;
       } else {
         sm.ring.release(it++, lane);  // the end's empty chunk
       }
@@ -688,12 +714,8 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
         }
       }
       if (row < 0) break;
-      const RowStats ws = warp_stats_sum<F>(st, a.c);
-      nan = __any_sync(0xffffffffu, nan);
-      if (lane == 0) {
-        sm.part[warp] = ws;
-        sm.nan[warp] = nan ? 1.f : 0.f;
-      }
+      const RowStats ws = warp_sum_stats<F>(st, a.c);
+      if (lane == 0) sm.part[warp] = ws;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sm.sums));
       prev = row;

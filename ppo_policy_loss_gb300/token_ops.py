@@ -17,11 +17,11 @@ import contextlib
 
 import torch
 
-from . import (DISTILL_STATS_BYTES, DISTILL_TAILS, DTYPES, distill_stats_from_bytes, rl_token_logprobs,
-               rl_token_logprobs_bwd, rl_topk_distill_desc_init, rl_topk_distill_fwd_bwd,
-               rl_topk_distill_workspace_size)
+from . import (DISTILL_STATS_BYTES, DISTILL_TAILS, DTYPES, _check, distill_stats_from_bytes, load,
+               rl_topk_distill_desc, rl_topk_distill_workspace_size)
 
 _DT = {torch.float32: DTYPES["f32"], torch.bfloat16: DTYPES["bf16"], torch.float16: DTYPES["f16"]}
+_F32, _I64 = torch.float32, torch.int64
 _HERE = contextlib.nullcontext()
 
 
@@ -30,9 +30,18 @@ def _on(device: torch.device, stream):
     and, if one is given, the caller's stream."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    if device.index is not None and device.index != torch.cuda.current_device():
+    if device.index != torch._C._cuda_getDevice():
         return torch.cuda.device(device)
     return _HERE
+
+
+def _raw_stream(device: torch.device) -> int:
+    # a decode step's call is host-bound: the raw handle, without a Stream object
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
 
 
 def _logits(logits: torch.Tensor):
@@ -89,14 +98,15 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, mask: 
         _given("ids", ids, torch.int64, (R,) if ids.dim() == 1 else (R, n), dev)
     mask = _mask(mask, R, dev)
     with _on(dev, stream):
-        f32 = dict(dtype=torch.float32, device=dev)
-        logp = torch.empty(ids.shape, **f32) if ids is not None else None
-        ent = torch.empty(R, **f32) if want_entropy else None
-        lse = torch.empty(R, **f32) if want_lse else None
-        top = torch.empty((R, k), dtype=torch.int64, device=dev) if k > 0 else None
-        top_lp = torch.empty((R, k), **f32) if k > 0 else None
-        rl_token_logprobs(logits, dt, R, V, ld, ids if n else None, n, mask, temperature, k, logp if n else None, ent,
-                          lse, top, top_lp, status)
+        logp = torch.empty(ids.shape, dtype=_F32, device=dev) if ids is not None else None
+        ent = torch.empty(R, dtype=_F32, device=dev) if want_entropy else None
+        lse = torch.empty(R, dtype=_F32, device=dev) if want_lse else None
+        top = torch.empty((R, k), dtype=_I64, device=dev) if k > 0 else None
+        top_lp = torch.empty((R, k), dtype=_F32, device=dev) if k > 0 else None
+        _check(load().rl_token_logprobs(
+            logits.data_ptr(), dt, R, V, ld, _p(ids) if n else None, n, _p(mask), temperature, k,
+            _p(logp) if n else None, _p(ent), _p(lse), _p(top), _p(top_lp), _p(status), _raw_stream(dev)),
+            "rl_token_logprobs")
     return dict(logp=logp, entropy=ent, lse=lse, topk_ids=top, topk_logp=top_lp)
 
 
@@ -126,8 +136,10 @@ def token_logprobs_backward(logits: torch.Tensor, ids: torch.Tensor | None, dlog
     mask = _mask(mask, R, dev)
     with _on(dev, stream):
         dlogits = _dlogits_like(logits, dlogits, ld)
-        rl_token_logprobs_bwd(logits, dt, R, V, ld, ids if n else None, n, mask, temperature, lse, entropy,
-                              dlogp if n else None, dentropy, dlogits, status)
+        _check(load().rl_token_logprobs_bwd(
+            logits.data_ptr(), dt, R, V, ld, _p(ids) if n else None, n, _p(mask), temperature, _p(lse), _p(entropy),
+            _p(dlogp) if n else None, _p(dentropy), _p(dlogits), _p(status), _raw_stream(dev)),
+            "rl_token_logprobs_bwd")
     return dlogits
 
 
@@ -227,16 +239,13 @@ def topk_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logp: 
         loss = torch.empty((), dtype=torch.float32, device=dev)
         workspace = new_distill_workspace(dev) if workspace is None else workspace
         stats = torch.empty(DISTILL_STATS_BYTES, dtype=torch.uint8, device=dev) if stats is None else stats
-        d = rl_topk_distill_desc_init()
-        p = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
-        d.logits, d.dtype, d.R, d.V, d.ld = p(logits), dt, R, V, ld
-        d.teacher_ids, d.teacher_logp, d.K = p(teacher_ids), p(teacher_logp), K
-        d.mask, d.weight, d.tail = p(mask), p(weight), DISTILL_TAILS[tail]
-        d.reverse, d.temperature, d.grad_scale, d.norm = reverse, temperature, grad_scale, norm
-        d.dlogits, d.row_loss_out, d.loss_out = p(dlogits), p(row_loss), p(loss)
-        d.stats_dev, d.workspace = p(stats), p(workspace)
-        d.workspace_bytes = workspace.numel() * workspace.element_size()
-        rl_topk_distill_fwd_bwd(d)
+        d = rl_topk_distill_desc(
+            logits=logits.data_ptr(), dtype=dt, R=R, V=V, ld=ld, teacher_ids=teacher_ids.data_ptr(),
+            teacher_logp=teacher_logp.data_ptr(), K=K, mask=_p(mask), weight=_p(weight), tail=DISTILL_TAILS[tail],
+            reverse=reverse, temperature=temperature, grad_scale=grad_scale, norm=norm, dlogits=_p(dlogits),
+            row_loss_out=_p(row_loss), loss_out=loss.data_ptr(), stats_dev=stats.data_ptr(),
+            workspace=workspace.data_ptr(), workspace_bytes=workspace.numel() * workspace.element_size())
+        _check(load().rl_topk_distill_fwd_bwd(d, _raw_stream(dev)), "rl_topk_distill_fwd_bwd")
     return dict(loss=loss, row_loss=row_loss, dlogits=dlogits, stats=stats, workspace=workspace)
 
 
