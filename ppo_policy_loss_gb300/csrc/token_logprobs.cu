@@ -639,7 +639,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
 }
 
 // ------------------------------------------------------------------ backward
-constexpr int kBwdThreads = 256;
+constexpr int kBwdThreads = 256;  // at most; fewer where a row is short
+constexpr int kBwdVecs = 4;       // vectors a thread has in flight
+constexpr int kIdsPerThread = kMaxK / 32;
 
 struct LpBwdArgs {
   const unsigned char* logits;
@@ -654,89 +656,165 @@ struct LpBwdArgs {
   long long R, V, row_bytes;
   float inv_temp;
   int n_ids;
-  int n_seg;  // segments of a row
-  long long seg_vecs;
+  long long n_seg;  // units of a row
 };
 
-// One unit is a segment of a row.  dz_v = 2^x (a0 + a1 x) with
-// x = (z_v / T - lse) log2(e); the given ids' elements are computed once
-// more and written after the segment's own stores.
-template <int DT, bool kEntropy>
-__global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(const LpBwdArgs a) {
+// dz_v = 2^x (a0 + a1 x) with x = (z_v / T - lse) log2(e), a0 = -(sum_j g_j + h H) / T
+// and a1 = -h ln(2) / T: one read and one write of the row, which is all that
+// bounds it.  One CTA takes a unit of up to 16 KB of a row and the hardware deals
+// the units out, so that none waits for the slowest of a static share.  All of a
+// thread's loads, the row's scalars and ids among them, are in flight at once,
+// and six CTAs a SM cover that one latency.  The given ids' elements are
+// computed once more and written after the unit's own stores.  Measured at
+// 4096 x 151,936 bf16: 360 us with the entropy's term, 6.9 TB/s (five CTAs 394;
+// two vectors a thread 376, eight 419; 512 threads 437); a persistent grid of
+// whole rows took 409.  Rows shorter than a unit get a CTA of just their length:
+// 23 us against 105 at 30,000 x 1000.
+// kList: several ids a row, in shared memory; else one id, or none, that every
+// thread reads itself, and a barrier only in the id's own unit.
+template <int DT, bool kEntropy, bool kList>
+__global__ void __launch_bounds__(kBwdThreads, 6) token_logprobs_bwd_kernel(const LpBwdArgs a) {
   using F = Fmt<DT>;
   constexpr int kVec = F::kVec;
-  __shared__ long long s_id[kMaxK];
-  __shared__ float s_g[kMaxK];
-  const int tid = threadIdx.x;
+  __shared__ long long s_id[kList ? kMaxK : 1];
+  __shared__ float s_g[kList ? kMaxK : 1];
+  const int tid = threadIdx.x, n_threads = blockDim.x, unit = n_threads * kBwdVecs;
   const int V = static_cast<int>(a.V), n_ids = a.n_ids;
   const int n_vecs = (V + kVec - 1) / kVec;
   unsigned int err = 0;
   for (long long u = blockIdx.x; u < a.R * a.n_seg; u += gridDim.x) {
     const long long row = u / a.n_seg;
-    const int v0 = static_cast<int>((u - row * a.n_seg) * a.seg_vecs);
-    const int v1 = static_cast<int>(min(static_cast<long long>(n_vecs), v0 + a.seg_vecs));
+    const int v0 = static_cast<int>(u - row * a.n_seg) * unit;
+    const int v1 = min(n_vecs, v0 + unit);
     const unsigned char* src = a.logits + row * a.row_bytes;
     unsigned char* dst = a.dlogits + row * a.row_bytes;
-    const bool on = !a.mask || a.mask[row] != 0;
-    float a0 = 0.f, a1 = 0.f, lse = 0.f, zj = 0.f;
-    long long idj = -1;
+    const bool full = (v0 + unit) * static_cast<long long>(kVec) <= V;
+    if (a.mask && a.mask[row] == 0) {
+      for (int v = v0 + tid; v < v1; v += n_threads) {
+        if ((v + 1) * kVec <= V)
+          st_global_cs_v4(dst + static_cast<long long>(v) * 16, make_uint4(0u, 0u, 0u, 0u));
+        else
+          for (int i = v * kVec; i < V; ++i) F::store(dst, i, 0.f);
+      }
+      continue;
+    }
+    auto in_unit = [&](long long id) {
+      return id >= static_cast<long long>(v0) * kVec && id < min(static_cast<long long>(V), static_cast<long long>(v1) * kVec);
+    };
+    uint4 w[kBwdVecs];
+#pragma unroll
+    for (int q = 0; q < kBwdVecs; ++q) {
+      const int v = v0 + tid + q * n_threads;
+      w[q] = *reinterpret_cast<const uint4*>(src + static_cast<long long>(min(v, n_vecs - 1)) * 16);
+    }
+    const float lse = a.lse[row];
+    float a0 = 0.f, a1 = 0.f, h = 0.f, H = 0.f;
+    if (kEntropy) {
+      h = a.dentropy[row];
+      H = a.entropy[row];
+    }
+    float zj[kList ? kIdsPerThread : 1], g0 = 0.f;
+    long long id0 = -1;
     bool mine = false;
-    if (on) {
-      lse = a.lse[row];
-      if (tid < n_ids) {
-        idj = a.ids[row * n_ids + tid];
-        s_id[tid] = idj;
-        s_g[tid] = a.dlogp[row * n_ids + tid];
-        if (idj < 0 || idj >= V) err |= RL_DEVERR_ID_RANGE;
-        mine = idj >= static_cast<long long>(v0) * kVec && idj < min(static_cast<long long>(V), static_cast<long long>(v1) * kVec);
-        if (mine) zj = F::load(src, idj);
+    if (!kList && n_ids) {
+      id0 = a.ids[row];
+      g0 = a.dlogp[row];
+      if (id0 < 0 || id0 >= V) {
+        err |= RL_DEVERR_ID_RANGE;
+        g0 = __int_as_float(0x7fc00000);
+      }
+      mine = in_unit(id0);
+      if (mine) zj[0] = F::load(src, id0);  // before the unit is overwritten in place
+      a0 = -g0 * a.inv_temp;
+    }
+    if constexpr (kList) {
+      long long id[kIdsPerThread];
+#pragma unroll
+      for (int i = 0; i < kIdsPerThread; ++i) {
+        const int j = tid + i * n_threads;
+        id[i] = -1;
+        if (j < n_ids) {
+          id[i] = a.ids[row * n_ids + j];
+          s_id[j] = id[i];
+          s_g[j] = a.dlogp[row * n_ids + j];
+          if (id[i] < 0 || id[i] >= V) err |= RL_DEVERR_ID_RANGE;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kIdsPerThread; ++i) {
+        const bool here = in_unit(id[i]);
+        mine = mine || here;
+        zj[i] = here ? F::load(src, id[i]) : 0.f;  // before the unit is overwritten in place
       }
       __syncthreads();
       float g = 0.f;
-      for (int j = 0; j < n_ids; ++j) {
-        g += s_g[j];
-        if (s_id[j] < 0 || s_id[j] >= V) g = __int_as_float(0x7fc00000);
-      }
+      for (int j = tid & 31; j < n_ids; j += 32)
+        g += s_id[j] < 0 || s_id[j] >= V ? __int_as_float(0x7fc00000) : s_g[j];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) g += __shfl_xor_sync(0xffffffffu, g, o);
       a0 = -g * a.inv_temp;
-      if (kEntropy) {
-        const float h = a.dentropy[row] * a.inv_temp;
-        a0 = fmaf(-h, a.entropy[row], a0);
-        a1 = -h * kLn2;
-      }
     }
-    auto grad = [&](float z) {
-      float x = fmaf(z, a.inv_temp, -lse) * kLog2e;
-      const float p = ex2_approx(x);
-      if (!kEntropy) return p * a0;
-      x = fmaxf(x, -1024.f);  // p is 0 there; 0 * -inf would not be
-      return p * fmaf(a1, x, a0);
+    if (kEntropy) {
+      h *= a.inv_temp;
+      a0 = fmaf(-h, H, a0);
+      a1 = -h * kLn2;
+    }
+    const float2 T2 = make_float2(a.inv_temp, a.inv_temp), nl2 = make_float2(-lse, -lse);
+    const float2 L2 = make_float2(kLog2e, kLog2e), A0 = make_float2(a0, a0), A1 = make_float2(a1, a1);
+    auto grad = [&](float2 z) {
+      float2 x = __fmul2_rn(__ffma2_rn(z, T2, nl2), L2);
+      const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+      if (!kEntropy) return __fmul2_rn(p, A0);
+      x = make_float2(fmaxf(x.x, -1024.f), fmaxf(x.y, -1024.f));  // p is 0 there; 0 * -inf would not be
+      return __fmul2_rn(p, __ffma2_rn(A1, x, A0));
     };
-    for (int v = v0 + tid; v < v1; v += kBwdThreads) {
+#pragma unroll
+    for (int q = 0; q < kBwdVecs; ++q) {
       float d[kVec];
-      if (on) {
-        F::unpack(*reinterpret_cast<const uint4*>(src + static_cast<long long>(v) * 16), d);
+      F::unpack(w[q], d);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) d[i] = grad(d[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) d[i] = 0.f;
+      for (int i = 0; i < kVec; i += 2) {
+        const float2 g = grad(make_float2(d[i], d[i + 1]));
+        d[i] = g.x;
+        d[i + 1] = g.y;
       }
-      if ((v + 1) * kVec <= V) {
-        st_global_cs_v4(dst + static_cast<long long>(v) * 16, F::pack(d));
-      } else {
+      w[q] = F::pack(d);
+    }
+    // the CTA stores at once: 7% faster than each warp when it is done (fewer
+    // turns between reads and writes in DRAM)
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kBwdVecs; ++q) {
+      const int v = v0 + tid + q * n_threads;
+      if (full || (v + 1) * kVec <= V) {
+        st_global_cs_v4(dst + static_cast<long long>(v) * 16, w[q]);
+      } else if (v < n_vecs) {
+        float d[kVec];
+        F::unpack(w[q], d);
+#pragma unroll
         for (int i = 0; i < kVec; ++i)
           if (v * kVec + i < V) F::store(dst, v * kVec + i, d[i]);
       }
     }
-    if (on && n_ids) {
-      __syncthreads();  // the segment's stores come first
+    if constexpr (!kList) {
       if (mine) {
-        float g = 0.f;
-        for (int j = 0; j < n_ids; ++j)
-          if (s_id[j] == idj) g += s_g[j];
-        F::store(dst, idj, fmaf(g, a.inv_temp, grad(zj)));
+        __syncthreads();  // the unit's stores come first
+        if (tid == 0) F::store(dst, id0, fmaf(g0, a.inv_temp, grad(make_float2(zj[0], zj[0])).x));
       }
-      __syncthreads();
+    } else {
+      if (__syncthreads_or(mine) && mine) {
+#pragma unroll
+        for (int i = 0; i < kIdsPerThread; ++i) {
+          const int j = tid + i * n_threads;
+          const long long id = j < n_ids ? s_id[j] : -1;
+          if (!in_unit(id)) continue;
+          float g = 0.f;
+#pragma unroll 8
+          for (int q = 0; q < n_ids; ++q) g += s_id[q] == id ? s_g[q] : 0.f;
+          F::store(dst, id, fmaf(g, a.inv_temp, grad(make_float2(zj[i], zj[i])).x));
+        }
+      }
+      if (u + gridDim.x < a.R * a.n_seg) __syncthreads();  // the lists are free for the next unit
     }
   }
   if (err && a.status) atomicOr(a.status, err);
@@ -809,9 +887,13 @@ rl_status launch_fwd(const LpArgs& a, int dev, int sms, cudaStream_t stream) {
 }
 
 template <int DT, bool kEntropy>
-rl_status launch_bwd(const LpBwdArgs& a, int sms, cudaStream_t stream) {
-  const long long units = a.R * a.n_seg, want = 8LL * sms;
-  token_logprobs_bwd_kernel<DT, kEntropy><<<static_cast<unsigned>(units < want ? units : want), kBwdThreads, 0, stream>>>(a);
+rl_status launch_bwd(const LpBwdArgs& a, int threads, cudaStream_t stream) {
+  const long long units = a.R * a.n_seg, most = 1LL << 30;
+  const unsigned grid = static_cast<unsigned>(units < most ? units : most);
+  if (a.n_ids > 1)
+    token_logprobs_bwd_kernel<DT, kEntropy, true><<<grid, threads, 0, stream>>>(a);
+  else
+    token_logprobs_bwd_kernel<DT, kEntropy, false><<<grid, threads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? RL_OK : RL_ERR_CUDA;
 }
 
@@ -889,9 +971,6 @@ extern "C" rl_status rl_token_logprobs_bwd(const void* logits, rl_dtype dtype, l
     const uintptr_t n = static_cast<uintptr_t>(R) * static_cast<uintptr_t>(row_bytes);
     if (l0 < d0 + n && d0 < l0 + n) return RL_ERR_ALIAS;
   }
-  int dev = 0, sms = 0;
-  const rl_status st = device_sms(&dev, &sms);
-  if (st != RL_OK) return st;
   LpBwdArgs a;
   a.logits = static_cast<const unsigned char*>(logits);
   a.ids = ids;
@@ -908,17 +987,15 @@ extern "C" rl_status rl_token_logprobs_bwd(const void* logits, rl_dtype dtype, l
   a.inv_temp = 1.f / temperature;
   a.n_ids = n_ids;
   const long long n_vecs = (V * es + 15) / 16;
-  long long seg = (16LL * sms + R - 1) / R;  // enough units for every CTA
-  const long long most = (n_vecs + 2 * kBwdThreads - 1) / (2 * kBwdThreads);
-  if (seg > most) seg = most;
-  a.seg_vecs = (n_vecs + seg - 1) / seg;
-  a.n_seg = static_cast<int>((n_vecs + a.seg_vecs - 1) / a.seg_vecs);
+  const int threads = static_cast<int>(n_vecs >= kBwdThreads * kBwdVecs ? kBwdThreads
+                                                                        : ((n_vecs + 32 * kBwdVecs - 1) / (32 * kBwdVecs)) * 32);
+  a.n_seg = (n_vecs + threads * kBwdVecs - 1) / (threads * kBwdVecs);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool ent = dentropy != nullptr;
   switch (dtype) {
-    case RL_F32: return ent ? launch_bwd<RL_F32, true>(a, sms, s) : launch_bwd<RL_F32, false>(a, sms, s);
-    case RL_BF16: return ent ? launch_bwd<RL_BF16, true>(a, sms, s) : launch_bwd<RL_BF16, false>(a, sms, s);
-    case RL_F16: return ent ? launch_bwd<RL_F16, true>(a, sms, s) : launch_bwd<RL_F16, false>(a, sms, s);
+    case RL_F32: return ent ? launch_bwd<RL_F32, true>(a, threads, s) : launch_bwd<RL_F32, false>(a, threads, s);
+    case RL_BF16: return ent ? launch_bwd<RL_BF16, true>(a, threads, s) : launch_bwd<RL_BF16, false>(a, threads, s);
+    case RL_F16: return ent ? launch_bwd<RL_F16, true>(a, threads, s) : launch_bwd<RL_F16, false>(a, threads, s);
   }
   return RL_ERR_DTYPE;
 }
