@@ -11,23 +11,21 @@
 namespace rl {
 namespace {
 
-constexpr int kRowThreads = 128;  // threads that work on a row
-constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kMaxPieces = 8192;  // pieces of a row one CTA can search for alternatives
 constexpr int kMaxK = RL_TOKEN_MAX_K;
 constexpr int kList = 256;        // survivors a search ranks directly
 
 // ------------------------------------------------------------------ top-k search
-// The k largest of n unique keys (0 = none) by kRowThreads threads, sorted.
+// The k largest of n unique keys (0 = none) by kT threads, sorted.
 // Each thread takes the maxima of the even and the odd blocks of its keys; the
 // k-th largest of nb >= 2 k bucket maxima is a bound that at least k keys
 // reach and few others do; those that reach it are listed and ranked by
 // counting.  If more than kList reach it (an order of the keys that puts the
 // large ones on few threads), the bound is raised by bisection until exactly k
 // do.
-template <class K>
+template <class K, int kT>
 struct SelSmem {
-  alignas(16) K a[2 * kRowThreads];
+  alignas(16) K a[2 * kT];
   alignas(16) K b[kList + 4];
   K bound;
   int count;
@@ -42,7 +40,11 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
 }
 __device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
-__device__ __forceinline__ void row_barrier() { named_barrier(1, kRowThreads); }
+// kT: threads that work on a row.
+template <int kT>
+__device__ __forceinline__ void row_barrier() {
+  named_barrier(1, kT);
+}
 
 // Keys of list[0 .. n-1] above `key`; n up to a multiple of 16 bytes is read,
 // the places past n hold 0.
@@ -65,32 +67,32 @@ __device__ __forceinline__ int rank_of(const unsigned long long* list, int n, un
   return r;
 }
 
-// f(key) for this thread's keys get(tid), get(tid + kRowThreads), ... below n,
+// f(key) for this thread's keys get(tid), get(tid + kT), ... below n,
 // eight loads at a time; f also gets the block's parity.
-template <class K, class Get, class Fn>
+template <class K, int kT, class Get, class Fn>
 __device__ __forceinline__ void each_key(Get get, int n, int tid, Fn f) {
-  for (int base = tid; base < n; base += 8 * kRowThreads) {
+  for (int base = tid; base < n; base += 8 * kT) {
     K v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = base + j * kRowThreads < n ? get(base + j * kRowThreads) : 0;
+    for (int j = 0; j < 8; ++j) v[j] = base + j * kT < n ? get(base + j * kT) : 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) f(v[j], j & 1);
   }
 }
 
 // get(i): key i, i < n.  out[0 .. k-1]: the largest first, 0 where there are
-// fewer.  All kRowThreads threads, after a barrier; ends with a barrier.
-template <class K, class Get>
-__device__ __forceinline__ void block_select(Get get, int n, int k, K* out, SelSmem<K>& s, int tid) {
+// fewer.  All kT threads, after a barrier; ends with a barrier.
+template <class K, int kT, class Get>
+__device__ __forceinline__ void block_select(Get get, int n, int k, K* out, SelSmem<K, kT>& s, int tid) {
   K best[2] = {0, 0};
-  each_key<K>(get, n, tid, [&](K v, int odd) { best[odd] = v > best[odd] ? v : best[odd]; });
+  each_key<K, kT>(get, n, tid, [&](K v, int odd) { best[odd] = v > best[odd] ? v : best[odd]; });
   const int nb = k <= 16 ? 32 : k <= 32 ? 64 : k <= 64 ? 128 : 256;
   const K most = best[0] > best[1] ? best[0] : best[1];
-  if (nb == 2 * kRowThreads) {
+  if (nb == 2 * kT) {
     s.a[2 * tid] = best[0];
     s.a[2 * tid + 1] = best[1];
   } else {
-    const int per = kRowThreads / nb;  // neighbouring lanes that share a bucket
+    const int per = kT / nb;  // neighbouring lanes that share a bucket
     K top = most;
     for (int o = 1; o < per; o <<= 1) {
       const K v = __shfl_xor_sync(0xffffffffu, top, o);
@@ -104,21 +106,21 @@ __device__ __forceinline__ void block_select(Get get, int n, int k, K* out, SelS
     s.sums[0] = s.sums[1] = 0;
   }
   if (tid < k) out[tid] = 0;
-  row_barrier();
-  for (int q = tid; q < nb; q += kRowThreads) {
+  row_barrier<kT>();
+  for (int q = tid; q < nb; q += kT) {
     const K v = s.a[q];
     if (v != 0 && rank_of(s.a, nb, v) == k - 1) s.bound = v;
   }
-  row_barrier();
+  row_barrier<kT>();
   const K bound = s.bound;
   if (most >= bound)
-    each_key<K>(get, n, tid, [&](K v, int) {
+    each_key<K, kT>(get, n, tid, [&](K v, int) {
       if (v >= bound) {
         const int p = atomicAdd(&s.count, 1);
         if (p < kList) s.b[p] = v;
       }
     });
-  row_barrier();
+  row_barrier<kT>();
   int cnt = s.count;
   if (cnt > kList) {
     // bisection over the key's bits: the largest bound that k keys still reach
@@ -126,34 +128,34 @@ __device__ __forceinline__ void block_select(Get get, int n, int k, K* out, SelS
     for (int round = 0; lo < hi; ++round) {
       const K mid = lo + (hi - lo) / 2 + 1;
       int c = 0;
-      if (most >= mid) each_key<K>(get, n, tid, [&](K v, int) { c += v >= mid; });
+      if (most >= mid) each_key<K, kT>(get, n, tid, [&](K v, int) { c += v >= mid; });
       c = __reduce_add_sync(0xffffffffu, c);
       if ((tid & 31) == 0 && c) atomicAdd(&s.sums[round & 1], c);
-      row_barrier();
+      row_barrier<kT>();
       const int total = s.sums[round & 1];
       if (tid == 0) s.sums[(round + 1) & 1] = 0;
-      row_barrier();
+      row_barrier<kT>();
       if (total >= k)
         lo = mid;
       else
         hi = mid - 1;
     }
     if (tid == 0) s.count = 0;
-    row_barrier();
-    each_key<K>(get, n, tid, [&](K v, int) {
+    row_barrier<kT>();
+    each_key<K, kT>(get, n, tid, [&](K v, int) {
       if (v >= lo) s.b[atomicAdd(&s.count, 1)] = v;  // keys are unique: exactly k reach it
     });
-    row_barrier();
+    row_barrier<kT>();
     cnt = s.count;
   }
   if (tid < 4) s.b[cnt + tid] = 0;  // what rank_of reads past the list
-  row_barrier();
-  for (int q = tid; q < cnt; q += kRowThreads) {
+  row_barrier<kT>();
+  for (int q = tid; q < cnt; q += kT) {
     const K v = s.b[q];
     const int r = rank_of(s.b, cnt, v);
     if (r < k) out[r] = v;
   }
-  row_barrier();
+  row_barrier<kT>();
 }
 
 // ------------------------------------------------------------------ forward
@@ -195,29 +197,32 @@ struct PlaceKey<uint32_t> {
 // Across CTAs: the value's order above the element's place in the row.
 using ElemKey = unsigned long long;
 
-constexpr int kChunk = kRowThreads * kPieceBytes;  // one piece per consumer thread
-constexpr int kSlots = 4;
 constexpr int kMaxCluster = 8;
-constexpr int kLpThreads = kRowThreads + 32;  // consumers and the producer warp
-constexpr int kLpCtas = 5;                    // CTAs a SM holds, registers permitting
+constexpr int kSlots = 4;
+// CTAs a SM holds, registers permitting, for kT threads (shared memory may allow
+// fewer).  4096 x 151,936 bf16: six CTAs of three slots take 208 and 254 us at
+// k = 0 and 64, five of four 214 and 265; at 8192 rows and k = 64 four slots are
+// 1% faster than three, and at few rows 5%.
+template <int kT>
+constexpr int kLpCtas = kT == 128 ? 6 : 8;
 constexpr int kSmemPerSm = 228 * 1024;
 
-template <int DT>
+template <int DT, int kT>
 struct LpSmem {
   using F = Fmt<DT>;
   using C = PlaceKey<typename F::Key>;
-  Ring<kSlots, kChunk> ring;
+  Ring<kSlots, kT * kPieceBytes> ring;  // a chunk has one piece per consumer thread
   long long row_of[kSlots];  // the row a chunk belongs to
   union {  // one search at a time
-    SelSmem<typename C::K> sel;
-    SelSmem<ElemKey> join_sel;
+    SelSmem<typename C::K, kT> sel;
+    SelSmem<ElemKey, kT> join_sel;
   };
   int pieces[kList];             // fast search: pieces that reach its bound
   int n_pieces, n_elems;
   alignas(16) typename C::K top[kMaxK];
   alignas(16) int slots[kMaxK];  // slow search: the k pieces with the largest maxima, in the row's order
   alignas(16) ElemKey found[kMaxK];  // the CTA's k largest elements, largest first, 0 where there are fewer
-  RowStats part[kRowWarps];
+  RowStats part[kT / 32];
   RowStats join_part[kMaxCluster];  // clusters: every slice's statistics, in rank 0's memory
   unsigned long long arrived, freed;  // rank 0: every slice is in; the others: rank 0 has taken the row
   int abort;
@@ -243,6 +248,7 @@ __device__ __forceinline__ ElemKey elem_key(uint32_t order, int e) {
 }
 
 // How many of the threads' two maxima reach `bound` (all consumer threads).
+template <int kT>
 __device__ __forceinline__ int count_reaching(const uint32_t (&best)[2], uint32_t bound, bool both) {
   int n;
   const uint32_t top = best[0] > best[1] ? best[0] : best[1];
@@ -250,14 +256,14 @@ __device__ __forceinline__ int count_reaching(const uint32_t (&best)[2], uint32_
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ge.u32 p, %1, %2;\n\tbar.red.popc.u32 %0, 1, %3, p;\n\t}"
       : "=r"(n)
-      : "r"(first), "r"(bound), "n"(kRowThreads)
+      : "r"(first), "r"(bound), "n"(kT)
       : "memory");
   if (both) {
     int n1;
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ge.u32 p, %1, %2;\n\tbar.red.popc.u32 %0, 1, %3, p;\n\t}"
         : "=r"(n1)
-        : "r"(best[1]), "r"(bound), "n"(kRowThreads)
+        : "r"(best[1]), "r"(bound), "n"(kT)
         : "memory");
     n += n1;
   }
@@ -272,12 +278,12 @@ __device__ __forceinline__ int count_reaching(const uint32_t (&best)[2], uint32_
 // it are listed, their elements read again (from L2), and those that reach it
 // ranked by counting.  False if a list overflows (many equal values, or a
 // large k of few pieces): search_slow then.
-template <int DT>
-__device__ __noinline__ bool search_fast(LpSmem<DT>& sm, const typename Fmt<DT>::Key* keys, const unsigned char* src,
+template <int DT, int kT>
+__device__ __noinline__ bool search_fast(LpSmem<DT, kT>& sm, const typename Fmt<DT>::Key* keys, const unsigned char* src,
                                             int g0, int n_mine, int V, int k, const uint32_t (&best)[2], uint32_t top,
                                             int tid) {
   using F = Fmt<DT>;
-  const bool both = k > 32;
+  const bool both = k > kT / 4;
   const int enough = k + k / 8 + 4;
   if (tid == 0) sm.n_pieces = sm.n_elems = 0;
   if (tid < k) sm.found[tid] = 0;
@@ -285,7 +291,7 @@ __device__ __noinline__ bool search_fast(LpSmem<DT>& sm, const typename Fmt<DT>:
   int n = 0;
   for (uint32_t step = F::kOrderStep;; step *= 4) {
     const uint32_t mid = hi > step && step < 0x40000000u ? hi - step : 1u;
-    n = count_reaching(best, mid, both);
+    n = count_reaching<kT>(best, mid, both);
     if (n >= k || mid == 1u) {
       lo = mid;
       break;
@@ -294,7 +300,7 @@ __device__ __noinline__ bool search_fast(LpSmem<DT>& sm, const typename Fmt<DT>:
   }
   while (n > enough && hi - lo > 1) {
     const uint32_t mid = lo + (hi - lo) / 2;
-    const int m = count_reaching(best, mid, both);
+    const int m = count_reaching<kT>(best, mid, both);
     if (m >= k) {
       lo = mid;
       n = m;
@@ -305,7 +311,7 @@ __device__ __noinline__ bool search_fast(LpSmem<DT>& sm, const typename Fmt<DT>:
   // a vector of keys, or of a piece's elements, a lane at a time; hits are few
   const float thr = F::order_value(lo);  // of lo = 1 a NaN: everything passes
   const uint4* kv = reinterpret_cast<const uint4*>(keys);
-  for (int q = tid; q * F::kVec < n_mine; q += kRowThreads) {
+  for (int q = tid; q * F::kVec < n_mine; q += kT) {
     uint32_t hits = F::hits(kv[q], thr);
     while (hits) {
       const int p = q * F::kVec + F::hit_elem(__ffs(hits) - 1);
@@ -316,16 +322,16 @@ __device__ __noinline__ bool search_fast(LpSmem<DT>& sm, const typename Fmt<DT>:
       }
     }
   }
-  row_barrier();
+  row_barrier<kT>();
   const int n_pieces = sm.n_pieces;
   if (n_pieces > kList) return false;
   const long long row_vecs = (static_cast<long long>(V) * F::kBytes + 15) / 16;
-  for (int q0 = tid; q0 < n_pieces * 4; q0 += 4 * kRowThreads) {
+  for (int q0 = tid; q0 < n_pieces * 4; q0 += 4 * kT) {
     uint4 v[4];
     int e[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int q = q0 + j * kRowThreads;
+      const int q = q0 + j * kT;
       const int vec = sm.pieces[min(q >> 2, n_pieces - 1)] * 4 + (q & 3);
       e[j] = q < n_pieces * 4 ? vec * F::kVec : V;
       v[j] = *reinterpret_cast<const uint4*>(src + min(static_cast<long long>(vec), row_vecs - 1) * 16);
@@ -343,24 +349,24 @@ __device__ __noinline__ bool search_fast(LpSmem<DT>& sm, const typename Fmt<DT>:
       }
     }
   }
-  row_barrier();
+  row_barrier<kT>();
   const int n_elems = sm.n_elems;
   if (n_elems > kList) return false;
   if (tid < 2) sm.join_sel.b[n_elems + tid] = 0;  // what rank_of reads past the list
-  row_barrier();
-  for (int q = tid; q < n_elems; q += kRowThreads) {
+  row_barrier<kT>();
+  for (int q = tid; q < n_elems; q += kT) {
     const ElemKey key = sm.join_sel.b[q];
     const int r = rank_of(sm.join_sel.b, n_elems, key);
     if (r < k) sm.found[r] = key;
   }
-  row_barrier();
+  row_barrier<kT>();
   return true;
 }
 
 // The same by two exact searches: the k pieces with the largest maxima (the
 // lower piece first among equals) hold the k largest elements.
-template <int DT>
-__device__ __noinline__ void search_slow(LpSmem<DT>& sm, typename Fmt<DT>::Key* keys, const unsigned char* src, int g0,
+template <int DT, int kT>
+__device__ __noinline__ void search_slow(LpSmem<DT, kT>& sm, typename Fmt<DT>::Key* keys, const unsigned char* src, int g0,
                                          int n_mine, int V, int per, int k, int tid) {
   using F = Fmt<DT>;
   using C = PlaceKey<typename F::Key>;
@@ -370,11 +376,11 @@ __device__ __noinline__ void search_slow(LpSmem<DT>& sm, typename Fmt<DT>::Key* 
     return (g0 + (all ? i / F::kPiece : sm.slots[i / F::kPiece])) * F::kPiece + i % F::kPiece;
   };
   auto key_at = [&](int i) { return C::make(keys[i], i); };
-  row_barrier();
-  for (int i = tid; i < n_mine; i += kRowThreads) keys[i] = static_cast<typename F::Key>(F::raw_order(keys[i]));
-  row_barrier();
+  row_barrier<kT>();
+  for (int i = tid; i < n_mine; i += kT) keys[i] = static_cast<typename F::Key>(F::raw_order(keys[i]));
+  row_barrier<kT>();
   if (!all) {
-    block_select<typename C::K>(key_at, n_mine, k, sm.top, sm.sel, tid);
+    block_select<typename C::K, kT>(key_at, n_mine, k, sm.top, sm.sel, tid);
     n_slots = min(k, n_mine);
     if (tid < n_slots) {  // back into the row's order
       const int g = C::at(sm.top[tid]);
@@ -382,31 +388,31 @@ __device__ __noinline__ void search_slow(LpSmem<DT>& sm, typename Fmt<DT>::Key* 
       for (int j = 0; j < n_slots; ++j) r += C::at(sm.top[j]) < g;
       sm.slots[r] = g;
     }
-    row_barrier();
+    row_barrier<kT>();
   }
   const int n_elems = n_slots * F::kPiece;
-  for (int i = tid; i < n_elems; i += kRowThreads) {
+  for (int i = tid; i < n_elems; i += kT) {
     const int e = element(i);
     keys[i] = e < V ? static_cast<typename F::Key>(F::load_order(src, e)) : typename F::Key(0);
   }
-  row_barrier();
-  block_select<typename C::K>(key_at, n_elems, k, sm.top, sm.sel, tid);
+  row_barrier<kT>();
+  block_select<typename C::K, kT>(key_at, n_elems, k, sm.top, sm.sel, tid);
   if (tid < k) {
     const typename C::K key = sm.top[tid];
     sm.found[tid] = key ? elem_key(C::value(key), element(C::at(key))) : 0;
   }
-  row_barrier();
+  row_barrier<kT>();
 }
 
 // The statistics of a row that needs_exact names, by differences to its
 // maximum, -inf elements skipped.  Rare, so it reads the row again.  m = -inf:
 // no element is finite.  All consumer threads.
-template <class F>
+template <class F, int kT>
 __device__ __noinline__ RowStats exact_row(const unsigned char* row, int V, float c, RowStats* part, int tid) {
   const int n_vecs = (V + F::kVec - 1) / F::kVec;
   auto each = [&](auto f) {
 #pragma unroll 4
-    for (int v = tid; v < n_vecs; v += kRowThreads) {
+    for (int v = tid; v < n_vecs; v += kT) {
       float z[F::kVec];
       F::unpack(*reinterpret_cast<const uint4*>(row + static_cast<long long>(v) * 16), z);
 #pragma unroll
@@ -418,11 +424,11 @@ __device__ __noinline__ RowStats exact_row(const unsigned char* row, int V, floa
   each([&](float z) { m = max_nan(m, z); });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  row_barrier();
+  row_barrier<kT>();
   if ((tid & 31) == 0) part[tid >> 5].m = m;
-  row_barrier();
-  for (int w = 0; w < kRowWarps; ++w) m = max_nan(m, part[w].m);
-  row_barrier();
+  row_barrier<kT>();
+  for (int w = 0; w < kT / 32; ++w) m = max_nan(m, part[w].m);
+  row_barrier<kT>();
   float s = 0.f, t = 0.f;
   if (m > -INFINITY)
     each([&](float z) {
@@ -437,9 +443,9 @@ __device__ __noinline__ RowStats exact_row(const unsigned char* row, int V, floa
     t += __shfl_xor_sync(0xffffffffu, t, o);
   }
   if ((tid & 31) == 0) part[tid >> 5] = RowStats{m, s, t};
-  row_barrier();
+  row_barrier<kT>();
   s = t = 0.f;
-  for (int w = 0; w < kRowWarps; ++w) {
+  for (int w = 0; w < kT / 32; ++w) {
     s += part[w].r;
     t += part[w].t;
   }
@@ -452,15 +458,16 @@ __device__ __noinline__ RowStats exact_row(const unsigned char* row, int V, floa
 // rows' chunks through the ring; the consumers keep one key per piece (its
 // maximum) and the running statistics, then search the keys for the
 // alternatives while the producer fills the ring with the next row.
-template <int DT, bool kEntropy>
-__global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(const LpArgs a) {
+template <int DT, bool kEntropy, int kT>
+__global__ void __launch_bounds__(kT + 32, kLpCtas<kT>) token_logprobs_kernel(const LpArgs a) {
   using F = Fmt<DT>;
   using C = PlaceKey<typename F::Key>;
+  constexpr int kWarps = kT / 32, kChunk = kT * kPieceBytes;
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  LpSmem<DT>& sm = *reinterpret_cast<LpSmem<DT>*>(smem_raw);
+  LpSmem<DT, kT>& sm = *reinterpret_cast<LpSmem<DT, kT>*>(smem_raw);
   volatile int* abort = &sm.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  static_assert(sizeof(LpSmem<DT>) % 16 == 0, "the key arrays follow");
+  static_assert(sizeof(LpSmem<DT, kT>) % 16 == 0, "the key arrays follow");
   const int csize = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const long long first = blockIdx.x / csize, stride = gridDim.x / csize;
   const int V = static_cast<int>(a.V);
@@ -471,12 +478,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
   const long long b0 = static_cast<long long>(g0) * kPieceBytes;
   const long long n_bytes = min(row_bytes16, static_cast<long long>(g1) * kPieceBytes) - b0;
   const int n_chunks = static_cast<int>((n_bytes + kChunk - 1) / kChunk);
-  ElemKey* const join_keys = reinterpret_cast<ElemKey*>(smem_raw + sizeof(LpSmem<DT>));
+  ElemKey* const join_keys = reinterpret_cast<ElemKey*>(smem_raw + sizeof(LpSmem<DT, kT>));
   ElemKey* const join_top = join_keys + kMaxCluster * kMaxK;
   typename F::Key* const keys = reinterpret_cast<typename F::Key*>(csize > 1 && a.k ? join_keys + kJoinKeys : join_keys);
 
   if (tid == 0) {
-    sm.ring.init(kRowWarps);
+    sm.ring.init(kWarps);
     mbar_init(smem_addr(&sm.arrived), csize);
     mbar_init(smem_addr(&sm.freed), 1);
     sm.abort = 0;
@@ -485,7 +492,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
   __syncthreads();
   if (csize > 1) cluster_sync_all();
 
-  if (warp == kRowWarps) {
+  if (warp == kWarps) {
     // ---------------------------------------------------------------- producer
     // The row of a chunk goes with it; a chunk of no bytes and row -1 is the end.
     const uint64_t pol = policy_normal();
@@ -516,9 +523,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
   } else {
     // ---------------------------------------------------------------- consumers
     const int k = a.k, n_ids = a.n_ids, n_mine = g1 - g0;
-    const int n_full = min(n_mine, V / F::kPiece - g0) / kRowThreads;  // steps whose every piece is a full one
+    const int n_full = min(n_mine, V / F::kPiece - g0) / kT;  // steps whose every piece is a full one
     if (a.mask && rank == 0) {  // masked rows
-      for (long long row = first + tid * stride; row < a.R; row += kRowThreads * stride) {
+      for (long long row = first + tid * stride; row < a.R; row += kT * stride) {
         if (a.mask[row]) continue;
         for (int q = 0; q < n_ids; ++q) a.logp[row * n_ids + q] = 0.f;
         for (int q = 0; q < k; ++q) {
@@ -538,7 +545,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
       // shared arrays of the row before.  After a timeout every thread stops here.
       sm.ring.wait(it, abort);
       const long long row = sm.row_of[it % kSlots];
-      if (named_barrier_or(1, kRowThreads, row < 0 || *abort)) break;
+      if (named_barrier_or(1, kT, row < 0 || *abort)) break;
       const unsigned char* src = a.logits + row * a.row_bytes;
       const long long y = rank == 0 && tid < n_ids ? a.ids[row * n_ids + tid] : -1;
       const bool y_ok = y >= 0 && y < V;
@@ -547,7 +554,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
       warp_stats_init<F>(st, a.c);
       for (int i = 0; i < n_chunks; ++i, ++it) {
         const uint32_t buf = sm.ring.wait(it, abort);
-        const int at = i * kRowThreads + tid;  // this lane's piece in the slice
+        const int at = i * kT + tid;  // this lane's piece in the slice
         const bool last = i >= n_full;         // a step that reaches the slice's or the row's end
         uint32_t w[16];
         load_piece(w, 0, buf + tid * kPieceBytes, last ? 0 : lane >> 1);
@@ -570,17 +577,17 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
       if (n_chunks < 2 && y_ok) zy = F::load(src, y);
       const RowStats ws = warp_stats_sum<F>(st, a.c);
       if (lane == 0) sm.part[warp] = ws;
-      row_barrier();
+      row_barrier<kT>();
       RowStats rs = sm.part[0];
 #pragma unroll
-      for (int w = 1; w < kRowWarps; ++w) rs = merge_row(rs, sm.part[w], a.c);
+      for (int w = 1; w < kWarps; ++w) rs = merge_row(rs, sm.part[w], a.c);
       // a NaN in t is a NaN logit or a first -inf: clamp from the next row on
       if (kEntropy) st.low = st.low || rs.t != rs.t;
       if (k) {
         const uint32_t order[2] = {tid < n_mine ? F::order_of(best[0]) : 0u,
-                                   tid + kRowThreads < n_mine ? F::order_of(best[1]) : 0u};
-        if (!search_fast<DT>(sm, keys, src, g0, n_mine, V, k, order, F::order_of(rs.m), tid))
-          search_slow<DT>(sm, keys, src, g0, n_mine, V, per, k, tid);
+                                   tid + kT < n_mine ? F::order_of(best[1]) : 0u};
+        if (!search_fast<DT, kT>(sm, keys, src, g0, n_mine, V, k, order, F::order_of(rs.m), tid))
+          search_slow<DT, kT>(sm, keys, src, g0, n_mine, V, per, k, tid);
       }
       if (csize > 1) {
         // every CTA's findings into rank 0's memory
@@ -593,7 +600,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
           st_cluster_f32(to + 8, rs.t);
         }
         fence_cluster();
-        row_barrier();
+        row_barrier<kT>();
         if (tid == 0) mbar_arrive_remote(map_to_rank(smem_addr(&sm.arrived), 0));
         if (rank == 0) {
           wait_bounded<true>(smem_addr(&sm.arrived), done & 1, abort);
@@ -601,20 +608,20 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
           for (int q = 1; q < csize; ++q) rs = merge_row(rs, sm.join_part[q], a.c);
           const int n = csize * k;
           if (n > kList) {
-            block_select<ElemKey>([&](int i) { return join_keys[i]; }, n, k, join_top, sm.join_sel, tid);
+            block_select<ElemKey, kT>([&](int i) { return join_keys[i]; }, n, k, join_top, sm.join_sel, tid);
           } else {
-            for (int q = tid; q < n; q += kRowThreads) {
+            for (int q = tid; q < n; q += kT) {
               const ElemKey key = join_keys[q];
               const int r = rank_of(join_keys, n, key);
               if (key && r < k) join_top[r] = key;
             }
           }
-          row_barrier();  // everything has been read: the others may send the next row
+          row_barrier<kT>();  // everything has been read: the others may send the next row
           if (tid > 0 && tid < csize) mbar_arrive_remote(map_to_rank(smem_addr(&sm.freed), tid));
         }
         if (rank != 0) continue;
       }
-      if (needs_exact<F>(rs.m, a.c) || (kEntropy && rs.t != rs.t)) rs = exact_row<F>(src, V, a.c, sm.part, tid);
+      if (needs_exact<F>(rs.m, a.c) || (kEntropy && rs.t != rs.t)) rs = exact_row<F, kT>(src, V, a.c, sm.part, tid);
       const float log_s = log1pf(rs.r);
       if (tid < n_ids) {
         if (!y_ok) err |= RL_DEVERR_ID_RANGE;
@@ -850,26 +857,26 @@ rl_status allow_smem(const void* fn, int dev, int smem) {
 // each gets a few chunks, or as many as its pieces need.
 int cluster_for(long long R, long long n_pieces, int sms) {
   int c = 1;
-  while (c < kMaxCluster && R * c <= 2LL * sms && n_pieces >= static_cast<long long>(c) * 4 * kRowThreads) c *= 2;
+  while (c < kMaxCluster && R * c <= 2LL * sms && n_pieces >= static_cast<long long>(c) * 4 * 128) c *= 2;
   return c;
 }
 
-template <int DT, bool kEntropy>
+template <int DT, bool kEntropy, int kT>
 rl_status launch_fwd(const LpArgs& a, int dev, int sms, cudaStream_t stream) {
   using F = Fmt<DT>;
-  const void* fn = reinterpret_cast<const void*>(&token_logprobs_kernel<DT, kEntropy>);
+  const void* fn = reinterpret_cast<const void*>(&token_logprobs_kernel<DT, kEntropy, kT>);
   const long long n_pieces = (a.V + F::kPiece - 1) / F::kPiece;
-  int c = cluster_for(a.R, n_pieces, sms);
+  int c = kT < 128 ? 1 : cluster_for(a.R, n_pieces, sms);
   while (a.k > 0 && c < kMaxCluster && (n_pieces + c - 1) / c > kMaxPieces) c *= 2;
   const int places = key_places<F>(static_cast<int>((n_pieces + c - 1) / c), a.k);
   constexpr int join_bytes = kJoinKeys * static_cast<int>(sizeof(ElemKey));
   // (keys are read a vector at a time: 16 bytes past the last)
-  const int smem = static_cast<int>(sizeof(LpSmem<DT>) + places * sizeof(typename F::Key)) + 16 + (c > 1 && a.k ? join_bytes : 0);
-  constexpr int most_smem = static_cast<int>(sizeof(LpSmem<DT>) + kMaxPieces * sizeof(typename F::Key)) + 16 + join_bytes;
+  const int smem = static_cast<int>(sizeof(LpSmem<DT, kT>) + places * sizeof(typename F::Key)) + 16 + (c > 1 && a.k ? join_bytes : 0);
+  constexpr int most_smem = static_cast<int>(sizeof(LpSmem<DT, kT>) + kMaxPieces * sizeof(typename F::Key)) + 16 + join_bytes;
   const rl_status st = allow_smem(fn, dev, most_smem);
   if (st != RL_OK) return st;
   int held = kSmemPerSm / (smem + 1024);  // CTAs a SM holds at once (1 KB each is the system's)
-  if (held > kLpCtas) held = kLpCtas;
+  if (held > kLpCtas<kT>) held = kLpCtas<kT>;
   const long long most = static_cast<long long>(held) * sms / c;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -878,12 +885,26 @@ rl_status launch_fwd(const LpArgs& a, int dev, int sms, cudaStream_t stream) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(c * (a.R < most ? a.R : most)));
-  cfg.blockDim = dim3(kLpThreads);
+  cfg.blockDim = dim3(kT + 32);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = c > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<DT, kEntropy>, a) == cudaSuccess ? RL_OK : RL_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<DT, kEntropy, kT>, a) == cudaSuccess ? RL_OK : RL_ERR_CUDA;
+}
+
+// Rows of at most kShortRow bytes, where there are enough of them, go to CTAs of
+// half the size: what a row costs at its end (joining the warps, the search's
+// chain of barriers) then stalls a smaller part of the SM.  128 against 64
+// threads, us: 30,000 x 1000 bf16, k = 16: 233, 156; 16,384 x 32,000: 285, 259;
+// 8192 x 50,000: 201, 186; 8192 x 64,000, k = 0: 193, 194, k = 64: 254, 260;
+// 4096 x 151,936: 243, 284.
+constexpr long long kShortRow = 100 * 1024;
+template <int DT, bool kEntropy>
+rl_status launch_fwd(const LpArgs& a, int dev, int sms, cudaStream_t stream) {
+  if (a.V * Fmt<DT>::kBytes <= kShortRow && a.R >= 8LL * sms && a.k <= 64 && a.n_ids <= 64)
+    return launch_fwd<DT, kEntropy, 64>(a, dev, sms, stream);
+  return launch_fwd<DT, kEntropy, 128>(a, dev, sms, stream);
 }
 
 template <int DT, bool kEntropy>

@@ -409,3 +409,42 @@ def test_logits_of_large_size():
     _, out, st = run(z, ids, None, 5)
     assert st == 0
     check_logprobs(out, ref_of(z, "f32", ids, None, 5), 3000)
+
+
+@pytest.mark.parametrize("V,dtype,k,n", [
+    (1, "bf16", 1, 1), (9, "f32", 9, 1), (31, "f16", 16, 64), (1000, "bf16", 17, 1), (2047, "f16", 64, 2),
+    (2049, "f32", 33, 1), (4100, "bf16", 1, 1), (20000, "f16", 16, 1), (20001, "bf16", 0, 3),
+    (2500, "bf16", 65, 1), (2500, "bf16", 8, 65)])
+def test_many_short_rows(V, dtype, k, n):
+    """Enough short rows for the smaller CTAs, on both sides of their limits on
+    alternatives and ids (64 threads: V / 256 terms a chain, within sum_steps
+    up to V = 24,000)."""
+    R = 1300
+    z = logits(R, V, dtype, 9 * V + k)
+    g = np.random.default_rng(V)
+    ids = torch.from_numpy(g.integers(0, V, (R, n)))
+    mask = torch.from_numpy((g.random(R) < 0.8).astype(np.uint8))
+    z[mask == 0] = float("nan")
+    if V > 100:
+        z[5, 3:] = -torch.inf  # fewer tokens than alternatives
+        z[6] = 0.5             # ties everywhere
+    mask[5] = mask[6] = 1
+    z[mask == 0] = float("nan")
+    _, out, st = run(z, ids, mask, k)
+    assert st == 0
+    ref = ref_of(z, dtype, ids, mask, k)
+    ref = {key: None if v is None else np.asarray(v) for key, v in ref.items()}
+    check_logprobs({key: v.reshape(R, n) if key == "logp" else v for key, v in out.items()}, ref, V)
+
+
+def test_a_minus_infinity_after_rows_without():
+    """The first -inf a CTA meets is in its second row or later, in one warp's
+    share of it."""
+    V = 9000
+    for R in (1300, 4000):  # CTAs of 64 threads; rows of several rounds
+        z = logits(R, V, "bf16", 11, sure=False)
+        z[R // 2::3, 4000] = -torch.inf
+        z[-1, ::2] = -torch.inf
+        _, out, st = run(z, None, None, 3)
+        assert st == 0
+        check_logprobs(out, ref_of(z, "bf16", None, None, 3), V)
