@@ -360,6 +360,36 @@ __device__ __forceinline__ void table_row(const DistillArgs& a, EntryTable& tab,
   n = __reduce_add_sync(0xffffffffu, n);
 }
 
+// N, the number of valid rows: every CTA counts the mask, its consumers and
+// its row warp together while the producer starts.  `at`: the consumer's
+// number; the row warp counts nothing, it takes the sum.
+template <int kWarps>
+__device__ __forceinline__ long long count_rows(const DistillArgs& a, long long (&wcount)[kWarps], int at) {
+  constexpr int kCounting = (kWarps - 2) * 32;
+  if (!a.mask) return a.R;
+  if (at < kCounting) {
+    int cnt = 0;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.mask) & 15) == 0;
+    const long long n16 = wide ? a.R / 16 : 0;
+    auto add = [&](uint32_t w) { cnt += __popc(__vcmpne4(w, 0u)) >> 3; };
+#pragma unroll 2
+    for (long long i = at; i < n16; i += kCounting) {
+      const uint4 v = reinterpret_cast<const uint4*>(a.mask)[i];
+      add(v.x);
+      add(v.y);
+      add(v.z);
+      add(v.w);
+    }
+    for (long long i = n16 * 16 + at; i < a.R; i += kCounting) cnt += a.mask[i] != 0;
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    if ((at & 31) == 0) wcount[at / 32] = cnt;
+  }
+  named_barrier(2, kCounting + 32);
+  long long N = 0;
+  for (int w = 0; w < kWarps - 2; ++w) N += wcount[w];
+  return N;
+}
+
 // kThreads consumers, the producer warp and the row warp.
 template <int DT, int kThreads, int kCtas>
 __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(const DistillArgs a) {
@@ -390,19 +420,7 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
     fence_mbar_init();
   }
   for (int i = tid; i < 2 * kTable; i += kThreads + 64) sm.tab[i / kTable].head[i % kTable] = 0;
-  // N: every CTA counts the mask
-  long long N = a.R;
-  if (a.mask) {
-    int cnt = 0;
-    for (long long i = tid; i < a.R; i += kThreads + 64) cnt += a.mask[i] != 0;
-    cnt = __reduce_add_sync(0xffffffffu, cnt);
-    if (lane == 0) sm.wcount[warp] = cnt;
-    __syncthreads();
-    N = 0;
-    for (int w = 0; w < kWarps + 2; ++w) N += sm.wcount[w];
-  }
   __syncthreads();
-  const double norm = a.norm > 0.0 ? a.norm : static_cast<double>(N);
 
   if (warp == kWarps) {
     // ---------------------------------------------------------------- producer
@@ -445,6 +463,8 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
     }
   } else if (warp == kWarps + 1) {
     // ---------------------------------------------------------------- row warp
+    const long long N = count_rows(a, sm.wcount, kThreads);
+    const double norm = a.norm > 0.0 ? a.norm : static_cast<double>(N);
     unsigned int err = 0;
     double acc[5] = {0.0, 0.0, 0.0, 0.0, 0.0};
     RowsOf<true> rows(a.mask, a.R, first, lane);
@@ -552,8 +572,18 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
     if (__shfl_sync(0xffffffffu, last, 0)) {
       __threadfence();
       double v[5] = {0.0, 0.0, 0.0, 0.0, 0.0};
-      for (int i = lane; i < static_cast<int>(gridDim.x); i += 32)
-        for (int q = 0; q < 5; ++q) v[q] += __ldcg(&a.partials[i].v[q]);
+      const int n = static_cast<int>(gridDim.x);
+      for (int i0 = lane; i0 < n; i0 += 128) {  // four CTAs' loads in flight
+        double p[4][5];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int q = 0; q < 5; ++q) p[j][q] = i0 + 32 * j < n ? __ldcg(&a.partials[i0 + 32 * j].v[q]) : 0.0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int q = 0; q < 5; ++q) v[q] += p[j][q];
+      }
       for (int q = 0; q < 5; ++q) v[q] = warp_sum_d(v[q]);
       if (lane == 0) {
         const unsigned int stw = atomicExch(&a.ws->status, 0u);
@@ -574,6 +604,7 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
     }
   } else {
     // ---------------------------------------------------------------- consumers
+    count_rows(a, sm.wcount, tid);
     // masked rows: an all-zero gradient, shared out evenly
     if (a.mask) {
       RowsOf<false> masked(a.mask, a.R, first, lane);
