@@ -179,7 +179,8 @@ size_t rl_topk_distill_workspace_size(void);
 /*
  * Errors: RL_ERR_NULL (desc, stats_dev, logits or teacher), RL_ERR_DTYPE
  * (dtype, tail), RL_ERR_SHAPE, RL_ERR_ARG (K, reverse, temperature,
- * grad_scale, norm out of range; reverse != 0 with RENORM), RL_ERR_ALIGN,
+ * grad_scale, norm out of range; reverse != 0 with RENORM), RL_ERR_ALIGN (as
+ * above; workspace on 16, stats_dev on 8 bytes),
  * RL_ERR_ALIAS (dlogits partially overlaps logits), RL_ERR_WORKSPACE,
  * RL_ERR_CUDA.
  */

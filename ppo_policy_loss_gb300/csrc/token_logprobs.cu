@@ -2,9 +2,6 @@
 // log-probabilities of given tokens with entropy and top alternatives, and
 // their gradient, over logits in memory (sm_103a).
 #include <cmath>
-#include <map>
-#include <mutex>
-#include <utility>
 
 #include "token_rows.cuh"
 
@@ -839,19 +836,6 @@ rl_status device_sms(int* dev, int* sms) {
   return RL_OK;
 }
 
-// The kernel's dynamic shared memory allowed once per device.
-rl_status allow_smem(const void* fn, int dev, int smem) {
-  static std::mutex mu;
-  static std::map<std::pair<const void*, int>, bool> done;
-  std::lock_guard<std::mutex> lock(mu);
-  bool& d = done[std::make_pair(fn, dev)];
-  if (!d) {
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return RL_ERR_CUDA;
-    d = true;
-  }
-  return RL_OK;
-}
-
 // CTAs that share a row.  One while there are rows for every CTA the GPU
 // holds; for fewer rows the row's slices spread over up to 8 CTAs, as long as
 // each gets a few chunks, or as many as its pieces need.
@@ -873,7 +857,8 @@ rl_status launch_fwd(const LpArgs& a, int dev, int sms, cudaStream_t stream) {
   // (keys are read a vector at a time: 16 bytes past the last)
   const int smem = static_cast<int>(sizeof(LpSmem<DT, kT>) + places * sizeof(typename F::Key)) + 16 + (c > 1 && a.k ? join_bytes : 0);
   constexpr int most_smem = static_cast<int>(sizeof(LpSmem<DT, kT>) + kMaxPieces * sizeof(typename F::Key)) + 16 + join_bytes;
-  const rl_status st = allow_smem(fn, dev, most_smem);
+  static std::atomic<unsigned long long> allowed{0};
+  const rl_status st = allow_smem(fn, dev, most_smem, allowed);
   if (st != RL_OK) return st;
   int held = kSmemPerSm / (smem + 1024);  // CTAs a SM holds at once (1 KB each is the system's)
   if (held > kLpCtas<kT>) held = kLpCtas<kT>;

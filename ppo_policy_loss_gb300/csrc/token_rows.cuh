@@ -8,6 +8,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -84,7 +85,6 @@ struct Fmt<RL_F32> {
     return __float_as_uint(max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3])));
   }
   __device__ static float raw_value(uint32_t r) { return __uint_as_float(r); }
-  __device__ static Key raw_key(uint32_t r) { return order32(r); }
   __device__ static uint32_t clamp(uint32_t w) { return __float_as_uint(max_nan(__uint_as_float(w), kFloor)); }
   // elements e .. 15 of the piece at w[b ..] become -inf
   template <int N>
@@ -161,7 +161,6 @@ struct Fmt<RL_BF16> {
     return pmax_bf16x2(m, (m >> 16) | (m << 16)) & 0xffffu;
   }
   __device__ static float raw_value(uint32_t r) { return __uint_as_float(r << 16); }
-  __device__ static Key raw_key(uint32_t r) { return static_cast<Key>(order16(r, 0x7f80u)); }
   __device__ static uint32_t clamp(uint32_t w) { return pmax_bf16x2(w, kFloor2); }
   template <int N>
   __device__ static void cut(uint32_t (&w)[N], int b, int e) {
@@ -263,7 +262,6 @@ struct Fmt<RL_F16> {
   }
   __device__ static float half_bits(uint32_t r) { return __half2float(__ushort_as_half(static_cast<unsigned short>(r))); }
   __device__ static float raw_value(uint32_t r) { return half_bits(r); }
-  __device__ static Key raw_key(uint32_t r) { return static_cast<Key>(order16(r, 0x7c00u)); }
   __device__ static uint32_t clamp(uint32_t w) { return pmax_f16x2(w, kFloor2); }
   template <int N>
   __device__ static void cut(uint32_t (&w)[N], int b, int e) {
@@ -674,6 +672,16 @@ __device__ __forceinline__ uint64_t policy_normal() {
   uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
   return pol;
+}
+
+// Host: the kernel's dynamic shared memory allowed, once per device (a bit of
+// `allowed` each; nothing that can throw, for this runs below a C entry).
+inline rl_status allow_smem(const void* fn, int dev, int smem, std::atomic<unsigned long long>& allowed) {
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (allowed.load(std::memory_order_acquire) & bit) return RL_OK;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return RL_ERR_CUDA;
+  allowed.fetch_or(bit, std::memory_order_release);
+  return RL_OK;
 }
 
 }  // namespace

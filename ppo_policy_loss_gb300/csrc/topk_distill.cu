@@ -23,9 +23,6 @@
 //     the row.
 #include <cmath>
 #include <cstring>
-#include <map>
-#include <mutex>
-#include <utility>
 
 #include "token_rows.cuh"
 
@@ -755,23 +752,12 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
 }
 
 // ------------------------------------------------------------------ host side
-rl_status allow_smem(const void* fn, int dev, int smem) {
-  static std::mutex mu;
-  static std::map<std::pair<const void*, int>, bool> done;
-  std::lock_guard<std::mutex> lock(mu);
-  bool& d = done[std::make_pair(fn, dev)];
-  if (!d) {
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return RL_ERR_CUDA;
-    d = true;
-  }
-  return RL_OK;
-}
-
 template <int DT, int kThreads, int kCtas>
 rl_status launch(const DistillArgs& a, int dev, int sms, cudaStream_t stream) {
   const void* fn = reinterpret_cast<const void*>(&topk_distill_kernel<DT, kThreads, kCtas>);
   const int smem = static_cast<int>(sizeof(DistillSmem<kThreads>));
-  const rl_status st = allow_smem(fn, dev, smem);
+  static std::atomic<unsigned long long> allowed{0};
+  const rl_status st = allow_smem(fn, dev, smem, allowed);
   if (st != RL_OK) return st;
   long long grid = static_cast<long long>(kCtas) * sms;
   if (grid > kMaxGrid) grid = kMaxGrid;
@@ -821,7 +807,7 @@ extern "C" rl_status rl_topk_distill_fwd_bwd(const rl_topk_distill_desc* d, void
   if (R > 0 && (!d->logits || !d->teacher_ids || !d->teacher_logp)) return RL_ERR_NULL;
   const long long row_bytes = ld * es;
   if ((reinterpret_cast<uintptr_t>(d->logits) & 15) || (reinterpret_cast<uintptr_t>(d->dlogits) & 15) || (row_bytes & 15) ||
-      (reinterpret_cast<uintptr_t>(d->workspace) & 15))
+      (reinterpret_cast<uintptr_t>(d->workspace) & 15) || (reinterpret_cast<uintptr_t>(d->stats_dev) & 7))
     return RL_ERR_ALIGN;
   if (d->dlogits && d->dlogits != d->logits && R > 0) {
     const uintptr_t l0 = reinterpret_cast<uintptr_t>(d->logits), d0 = reinterpret_cast<uintptr_t>(d->dlogits);

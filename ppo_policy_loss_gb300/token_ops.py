@@ -25,10 +25,17 @@ _F32, _I64 = torch.float32, torch.int64
 _HERE = contextlib.nullcontext()
 
 
-def _on(device: torch.device, stream):
+def _on(device: torch.device, stream, inputs):
     """The context in which a call allocates and launches: the logits' device
-    and, if one is given, the caller's stream."""
+    and, if one is given, the caller's stream.  Memory of the inputs is not
+    reused before that stream has read them."""
     if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the logits are on {device}")
+        if stream != torch.cuda.current_stream(device):
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(stream)
         return torch.cuda.stream(stream)
     if device.index != torch._C._cuda_getDevice():
         return torch.cuda.device(device)
@@ -72,6 +79,13 @@ def _mask(mask, R, device):
     return _given("mask", mask.view(-1) if mask.is_contiguous() else mask, torch.uint8, (R,), device)
 
 
+def _status(status, device):
+    if status is not None and (status.dtype not in (torch.int32, torch.uint32) or status.device != device or
+                               status.numel() != 1):
+        raise ValueError(f"status must be an int32 tensor of one element on {device}")
+    return _p(status)
+
+
 def _n_ids(ids, R):
     if ids is None:
         return 0
@@ -97,7 +111,8 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, mask: 
     if ids is not None:
         _given("ids", ids, torch.int64, (R,) if ids.dim() == 1 else (R, n), dev)
     mask = _mask(mask, R, dev)
-    with _on(dev, stream):
+    status_p = _status(status, dev)
+    with _on(dev, stream, (logits, ids, mask, status)):
         logp = torch.empty(ids.shape, dtype=_F32, device=dev) if ids is not None else None
         ent = torch.empty(R, dtype=_F32, device=dev) if want_entropy else None
         lse = torch.empty(R, dtype=_F32, device=dev) if want_lse else None
@@ -105,7 +120,7 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, mask: 
         top_lp = torch.empty((R, k), dtype=_F32, device=dev) if k > 0 else None
         _check(load().rl_token_logprobs(
             logits.data_ptr(), dt, R, V, ld, _p(ids) if n else None, n, _p(mask), temperature, k,
-            _p(logp) if n else None, _p(ent), _p(lse), _p(top), _p(top_lp), _p(status), _raw_stream(dev)),
+            _p(logp) if n else None, _p(ent), _p(lse), _p(top), _p(top_lp), status_p, _raw_stream(dev)),
             "rl_token_logprobs")
     return dict(logp=logp, entropy=ent, lse=lse, topk_ids=top, topk_logp=top_lp)
 
@@ -129,16 +144,20 @@ def token_logprobs_backward(logits: torch.Tensor, ids: torch.Tensor | None, dlog
         if dlogp is None:
             raise ValueError("dlogp must be given with ids")
         _given("dlogp", dlogp, torch.float32, shape, dev)
+    elif dlogp is not None:
+        raise ValueError("ids must be given with dlogp")
     _given("lse", lse, torch.float32, (R,), dev)
     for name, t in (("entropy", entropy), ("dentropy", dentropy)):
         if t is not None:
             _given(name, t, torch.float32, (R,), dev)
     mask = _mask(mask, R, dev)
-    with _on(dev, stream):
+    status_p = _status(status, dev)
+    given = None if isinstance(dlogits, str) else dlogits
+    with _on(dev, stream, (logits, ids, dlogp, lse, entropy, dentropy, mask, status, given)):
         dlogits = _dlogits_like(logits, dlogits, ld)
         _check(load().rl_token_logprobs_bwd(
             logits.data_ptr(), dt, R, V, ld, _p(ids) if n else None, n, _p(mask), temperature, _p(lse), _p(entropy),
-            _p(dlogp) if n else None, _p(dentropy), _p(dlogits), _p(status), _raw_stream(dev)),
+            _p(dlogp) if n else None, _p(dentropy), _p(dlogits), status_p, _raw_stream(dev)),
             "rl_token_logprobs_bwd")
     return dlogits
 
@@ -160,7 +179,10 @@ class TokenLogprobs(torch.autograd.Function):
     """Autograd wrapper: logp, entropy = TokenLogprobs.apply(logits, ids, mask, temperature).
 
     The backward pass is one launch of rl_token_logprobs_bwd on the incoming
-    gradients; it reads no value on the host, so it can be captured."""
+    gradients; it reads no value on the host, so it can be captured.  Capture it
+    with torch.autograd.grad, or while no eager graph of the same leaves is
+    alive: torch's accumulation into a leaf's .grad belongs to the stream of the
+    leaf's first graph, which a capture must not wait for."""
 
     @staticmethod
     def forward(ctx, logits, ids, mask=None, temperature=1.0):
@@ -209,7 +231,9 @@ def topk_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logp: 
     student).  ``mask`` uint8 or bool [R]; ``weight`` float32 [R]; ``norm``: what
     the sum over rows is divided by (0: the number of valid rows).
     ``dlogits`` / ``row_loss``: "new" allocates, None skips, a tensor is written
-    (``dlogits=logits`` overwrites the logits).
+    (``dlogits=logits`` overwrites the logits).  ``workspace``: one call at a
+    time may use it; calls on two streams, or graphs replayed at once, take one
+    each (None: a new one).
 
     Returns dict(loss: float32 scalar, row_loss: [R], dlogits, stats: the device
     record for read_distill_stats, workspace)."""
@@ -227,9 +251,11 @@ def topk_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logp: 
         raise ValueError(f"tail must be one of {sorted(DISTILL_TAILS)}")
     if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous and on the logits' device")
-    if stats is not None and (stats.dtype != torch.uint8 or stats.device != dev or stats.numel() < DISTILL_STATS_BYTES):
-        raise ValueError(f"stats must be a uint8 tensor of {DISTILL_STATS_BYTES} bytes on the logits' device")
-    with _on(dev, stream):
+    if stats is not None and (stats.dtype != torch.uint8 or stats.device != dev or
+                              stats.numel() < DISTILL_STATS_BYTES or not stats.is_contiguous()):
+        raise ValueError(f"stats must be a contiguous uint8 tensor of {DISTILL_STATS_BYTES} bytes on the logits' device")
+    given = [None if isinstance(t, str) else t for t in (dlogits, row_loss)]
+    with _on(dev, stream, (logits, teacher_ids, teacher_logp, mask, weight, workspace, stats, *given)):
         if dlogits is not None:
             dlogits = _dlogits_like(logits, dlogits, ld)
         if isinstance(row_loss, str):
@@ -252,17 +278,20 @@ def topk_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logp: 
 class FusedTopkDistill(torch.autograd.Function):
     """Autograd wrapper: loss = FusedTopkDistill.apply(logits, teacher_ids,
     teacher_logp, mask, options), ``options`` a dict of topk_distill's keyword
-    arguments.
+    arguments (not dlogits: every call keeps its own).
 
     The forward pass runs the fused kernel and keeps its gradient; the backward
     pass hands it back times the incoming gradient.  That product is skipped
     where the incoming gradient is 1, which is read on the host, except while
     a CUDA graph is being captured, where nothing is read and the product is
-    always taken."""
+    always taken (captured as TokenLogprobs' backward is)."""
 
     @staticmethod
     def forward(ctx, logits, teacher_ids, teacher_logp, mask=None, options=None):
-        out = topk_distill(logits.detach(), teacher_ids, teacher_logp, mask=mask, **dict(options or {}))
+        options = dict(options or {})
+        if "dlogits" in options:
+            raise ValueError("the wrapper keeps a gradient of its own: options must not name dlogits")
+        out = topk_distill(logits.detach(), teacher_ids, teacher_logp, mask=mask, **options)
         ctx.save_for_backward(out["dlogits"])
         return out["loss"]
 

@@ -264,3 +264,9 @@ def test_oracle_gradient_against_differences():
             a[r, v] += h
             b[r, v] -= h
             assert abs((f(a) - f(b)) / (2 * h) - d[r, v]) < 1e-7
+
+
+@needs_nvcc
+def test_distill_refuses_a_record_off_its_boundary(lib):
+    import ctypes
+    assert lib.rl_topk_distill_fwd_bwd(ctypes.byref(distill_desc(stats_dev=at(4) + 4)), None) == rl.RL_ERR_ALIGN
