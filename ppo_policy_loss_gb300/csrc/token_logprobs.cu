@@ -454,7 +454,20 @@ __device__ __noinline__ RowStats exact_row(const unsigned char* row, int V, floa
 // row's pieces) takes a row at a time.  The producer warp streams the valid
 // rows' chunks through the ring; the consumers keep one key per piece (its
 // maximum) and the running statistics, then search the keys for the
-// alternatives while the producer fills the ring with the next row.
+// alternatives while the producer fills the ring with the next row.  One pass
+// over the logits; nothing else of their size is read or written.
+//
+// What bounds it: with the entropy, the exponentials and the instructions
+// around them, not the memory.  A 64-byte piece of 16-bit logits takes 32
+// exponentials a lane, so a SM's 16 a clock pass 32 bytes a clock, 1.4 times what
+// its share of HBM delivers; a packed add, two packed FMAs and the unpacking of
+// each pair come beside them (issue slots 65-70% busy).  4096 x 151,936 bf16:
+// 208 us (6.0 TB/s), without the entropy 181 us (6.9 TB/s).  The search waits on
+// barriers and on L2: 20 alternatives add 36 us there, 64 add 46 us, and 16 add
+// 50 us to 210 us at 16,384 x 32,000; many small CTAs cover that for one
+// another.  One warp that searched a row behind the consumers took 234 us there,
+// but 440 us against 331 at 16,384 x 32,000 and k = 64, and 27 us against 19 for
+// a single row.
 template <int DT, bool kEntropy, int kT>
 __global__ void __launch_bounds__(kT + 32, kLpCtas<kT>) token_logprobs_kernel(const LpArgs a) {
   using F = Fmt<DT>;
@@ -838,10 +851,16 @@ rl_status device_sms(int* dev, int* sms) {
 
 // CTAs that share a row.  One while there are rows for every CTA the GPU
 // holds; for fewer rows the row's slices spread over up to 8 CTAs, as long as
-// each gets a few chunks, or as many as its pieces need.
+// each gets a few chunks, or as many as its pieces need.  Rows x 151,936 bf16,
+// 20 alternatives, us on 1, 2, 4, 8 CTAs: 1 row 27.0 18.4 14.2 13.2; 38 rows
+// 28.0 19.3 15.3 15.5 (none: 24.8 15.7 12.0 10.0); 64 rows 27.9 19.2 15.5 17.5;
+// 110 rows on 2 and 4: 20.7 17.6; 150 rows 20.9 30.9 (clusters of 4 wait for a
+// second round); 300 rows on 1 and 2: 32.0 29.3.  Hence at most 4, 3 and 2 CTAs
+// a SM in clusters of 2, 4 and 8.
 int cluster_for(long long R, long long n_pieces, int sms) {
   int c = 1;
-  while (c < kMaxCluster && R * c <= 2LL * sms && n_pieces >= static_cast<long long>(c) * 4 * 128) c *= 2;
+  for (int most = 4; c < kMaxCluster; c *= 2, --most)
+    if (R * 2 * c > static_cast<long long>(most) * sms || n_pieces < static_cast<long long>(c) * 4 * 128) break;
   return c;
 }
 
