@@ -169,6 +169,7 @@ struct LpArgs {
   long long R, V, row_bytes;
   float inv_temp, c;  // 1 / temperature, log2(e) / temperature
   int n_ids, k;
+  int resident;  // CTAs the GPU holds at once
 };
 
 // The search key of a piece or an element: its value's order above its place,
@@ -221,6 +222,8 @@ struct LpSmem {
   alignas(16) ElemKey found[kMaxK];  // the CTA's k largest elements, largest first, 0 where there are fewer
   RowStats part[kT / 32];
   RowStats join_part[kMaxCluster];  // clusters: every slice's statistics, in rank 0's memory
+  alignas(16) uint4 dealt;            // the answer to the producer's request for another row
+  unsigned long long deal;            // it has come
   unsigned long long arrived, freed;  // rank 0: every slice is in; the others: rank 0 has taken the row
   int abort;
 };
@@ -242,6 +245,29 @@ __host__ __device__ constexpr int key_places(int per, int k) {
 
 __device__ __forceinline__ ElemKey elem_key(uint32_t order, int e) {
   return (static_cast<ElemKey>(order) << 32) | (0xffffffffu - static_cast<uint32_t>(e));
+}
+
+// Asks the hardware for the number of a CTA that has not been started, which
+// this CTA then does the work of; the answer arrives at `deal`.  One thread.
+__device__ __forceinline__ void ask_for_cta(uint32_t answer, uint32_t deal) {
+  fence_proxy_async_shared();
+  mbar_arrive_expect_tx(deal, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+      "r"(deal)
+      : "memory");
+}
+// The answer: a CTA's number, or -1 when all have been started (ask no more).
+__device__ __forceinline__ long long cta_dealt(uint32_t answer) {
+  uint32_t given, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\tld.shared.b128 h, [%2];\n\tmov.u32 %1, 0;\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(given), "=r"(x)
+      : "r"(answer)
+      : "memory");
+  return given ? static_cast<long long>(x) : -1;
 }
 
 // How many of the threads' two maxima reach `bound` (all consumer threads).
@@ -480,6 +506,7 @@ __global__ void __launch_bounds__(kT + 32, kLpCtas<kT>) token_logprobs_kernel(co
   static_assert(sizeof(LpSmem<DT, kT>) % 16 == 0, "the key arrays follow");
   const int csize = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const long long first = blockIdx.x / csize, stride = gridDim.x / csize;
+  const bool dealt = kT == 128 && csize == 1 && gridDim.x > static_cast<unsigned>(a.resident);
   const int V = static_cast<int>(a.V);
   const int n_pieces = (V + F::kPiece - 1) / F::kPiece;
   const int per = (n_pieces + csize - 1) / csize;
@@ -494,6 +521,7 @@ __global__ void __launch_bounds__(kT + 32, kLpCtas<kT>) token_logprobs_kernel(co
 
   if (tid == 0) {
     sm.ring.init(kWarps);
+    mbar_init(smem_addr(&sm.deal), 1);
     mbar_init(smem_addr(&sm.arrived), csize);
     mbar_init(smem_addr(&sm.freed), 1);
     sm.abort = 0;
@@ -509,8 +537,36 @@ __global__ void __launch_bounds__(kT + 32, kLpCtas<kT>) token_logprobs_kernel(co
     uint32_t it = 0;
     bool ok = true;
     RowsOf<true> rows(a.mask, a.R, first, lane);
+    // a row a CTA of the grid: the next one is asked for while a row streams
+    uint32_t asked = 0;
+    auto ask = [&]() {
+      if (lane == 0) ask_for_cta(smem_addr(&sm.dealt), smem_addr(&sm.deal));
+      ++asked;
+    };
+    auto answer = [&]() {  // a.R: no more; then nothing is asked again
+      long long n = -1;
+      if (lane == 0) {
+        ok = wait_bounded<false>(smem_addr(&sm.deal), (asked - 1) & 1, abort) && ok;
+        if (ok) n = cta_dealt(smem_addr(&sm.dealt));
+      }
+      n = __shfl_sync(0xffffffffu, n, 0);
+      return n < 0 ? a.R : n;
+    };
+    // each number dealt also stands for the row of that number, if it is masked
+    auto masked_row = [&](long long row) {
+      if (!a.mask || row >= a.R || a.mask[row]) return;
+      for (int q = lane; q < a.n_ids; q += 32) a.logp[row * a.n_ids + q] = 0.f;
+      for (int q = lane; q < a.k; q += 32) {
+        a.topk_ids[row * a.k + q] = -1;
+        a.topk_logp[row * a.k + q] = 0.f;
+      }
+      if (lane == 0 && a.entropy) a.entropy[row] = 0.f;
+      if (lane == 0 && a.lse) a.lse[row] = 0.f;
+    };
+    long long want = first;
     while (ok) {
-      const long long row = rows.next(stride, lane);
+      const long long row = rows.at(want, lane);
+      if (dealt && row >= 0) ask();
       if (lane == 0) {
         const unsigned char* src = a.logits + row * a.row_bytes + b0;
         const int n = row < 0 ? 1 : n_chunks;
@@ -528,13 +584,28 @@ __global__ void __launch_bounds__(kT + 32, kLpCtas<kT>) token_logprobs_kernel(co
         }
         if (!ok) sm.ring.drain(it);
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0) && row >= 0;
+      if (dealt) masked_row(want);
+      if (row >= 0) want = dealt ? answer() : want + stride;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (row < 0) break;
+    }
+    // no valid row is left: the CTAs not started yet have masked rows at most
+    while (dealt && ok && want < a.R) {
+      ask();
+      want = answer();
+      masked_row(want);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (!ok && asked && lane == 0) {  // an answer on its way lands before the CTA may exit
+      const uint64_t t0 = global_ns();
+      while (!mbar_try_wait(smem_addr(&sm.deal), (asked - 1) & 1) && global_ns() - t0 <= kWaitLimitNs) {
+      }
     }
   } else {
     // ---------------------------------------------------------------- consumers
     const int k = a.k, n_ids = a.n_ids, n_mine = g1 - g0;
     const int n_full = min(n_mine, V / F::kPiece - g0) / kT;  // steps whose every piece is a full one
-    if (a.mask && rank == 0) {  // masked rows
+    if (a.mask && rank == 0 && !dealt) {  // masked rows
       for (long long row = first + tid * stride; row < a.R; row += kT * stride) {
         if (a.mask[row]) continue;
         for (int q = 0; q < n_ids; ++q) a.logp[row * n_ids + q] = 0.f;
@@ -864,8 +935,17 @@ int cluster_for(long long R, long long n_pieces, int sms) {
   return c;
 }
 
+// Long rows in at least this many rounds are dealt out one by one (the grid has
+// a CTA a row, and running CTAs take over those not started): CTAs of one SM do
+// not run at the same speed, and a fixed share leaves the slowest behind.  Fixed
+// against dealt, us: 4096 x 151,936 bf16, k = 0 and 64: 213, 204 and 264, 254;
+// 70% of its rows valid: 164, 154; 8192 x 64,000: 200, 186.  Fewer rounds have
+// nothing to even out: 777 x 50,257 fp32: 42, 47; 1300: 59, 60; 2000: 81, 80.
+// Nor are short rows: the request's answer and the masked rows that it stands
+// for come on top (16,384 x 32,000 fp16, k = 16, 57% valid: 167, 186).
+constexpr int kDealtRounds = 3;
 template <int DT, bool kEntropy, int kT>
-rl_status launch_fwd(const LpArgs& a, int dev, int sms, cudaStream_t stream) {
+rl_status launch_fwd(LpArgs a, int dev, int sms, cudaStream_t stream) {
   using F = Fmt<DT>;
   const void* fn = reinterpret_cast<const void*>(&token_logprobs_kernel<DT, kEntropy, kT>);
   const long long n_pieces = (a.V + F::kPiece - 1) / F::kPiece;
@@ -882,13 +962,15 @@ rl_status launch_fwd(const LpArgs& a, int dev, int sms, cudaStream_t stream) {
   int held = kSmemPerSm / (smem + 1024);  // CTAs a SM holds at once (1 KB each is the system's)
   if (held > kLpCtas<kT>) held = kLpCtas<kT>;
   const long long most = static_cast<long long>(held) * sms / c;
+  a.resident = static_cast<int>(most);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(c);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(c * (a.R < most ? a.R : most)));
+  const bool dealt = kT == 128 && c == 1 && a.R >= kDealtRounds * most;
+  cfg.gridDim = dim3(static_cast<unsigned>(dealt ? a.R : c * (a.R < most ? a.R : most)));
   cfg.blockDim = dim3(kT + 32);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;

@@ -616,6 +616,16 @@ struct RowsOf {
     want += stride;
     return row;
   }
+  // row number n of them (in any order; forwards costs least)
+  __device__ __forceinline__ long long at(long long n, int lane) {
+    if (n >= R) return -1;
+    if (mask && n < before) {
+      base = before = 0;
+      load(lane);
+    }
+    want = n;
+    return next(0, lane);
+  }
 };
 
 // ------------------------------------------------------------------ chunk ring

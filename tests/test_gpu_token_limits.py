@@ -164,3 +164,29 @@ def test_refusals_of_what_the_kernels_would_write_or_read_wrongly():
         with pytest.raises(ValueError, match="dlogits"):
             torch_api.FusedTopkDistill.apply(leaf, tid, tlq, None, dict(dlogits=d))
     assert torch_api.token_logprobs(z, torch.empty((4, 0), dtype=torch.int64, device=DEV))["logp"].shape == (4, 0)
+
+
+@pytest.mark.parametrize("pattern", ["none", "random", "first", "last", "all"])
+def test_rows_dealt_out_one_by_one(pattern):
+    """Many rounds of long rows give the bits of the same rows in few rounds,
+    wherever the masked rows lie; every masked row is written, none twice as
+    something else."""
+    R, V, k = 4000, 60000, 7
+    gen = torch.Generator(device=DEV).manual_seed(9)
+    z = torch.empty((R, V), dtype=torch.bfloat16, device=DEV).normal_(0.0, 3.0, generator=gen)
+    ids = torch.randint(0, V, (R, 40), device=DEV, generator=gen)
+    keep = {"none": torch.ones(R), "random": (torch.rand(R, generator=torch.Generator().manual_seed(1)) < 0.6),
+            "first": torch.arange(R) < 1, "last": torch.arange(R) >= R - 900, "all": torch.zeros(R)}[pattern]
+    mask = keep.to(torch.uint8).to(DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for m in ([None, mask] if pattern == "none" else [mask]):
+        out = torch_api.token_logprobs(z, ids, mask=m, k=k, want_lse=True, status=st)
+        for a in range(0, R, 800):
+            part = torch_api.token_logprobs(z[a:a + 800], ids[a:a + 800], mask=None if m is None else m[a:a + 800], k=k,
+                                            want_lse=True)
+            for n, t in part.items():
+                assert torch.equal(out[n][a:a + 800], t), (n, a)
+        off = mask == 0
+        assert (out["topk_ids"][off] == -1).all()
+        assert all((out[n][off] == 0).all() for n in ("logp", "entropy", "lse", "topk_logp"))
+    assert int(st.item()) == 0
