@@ -483,13 +483,11 @@ __device__ __noinline__ RowStats exact_row(const unsigned char* row, int V, floa
 // alternatives while the producer fills the ring with the next row.  One pass
 // over the logits; nothing else of their size is read or written.
 //
-// What bounds it: with the entropy, the exponentials and the instructions
-// around them, not the memory.  A 64-byte piece of 16-bit logits takes 32
-// exponentials a lane, so a SM's 16 a clock pass 32 bytes a clock, 1.4 times what
-// its share of HBM delivers; a packed add, two packed FMAs and the unpacking of
-// each pair come beside them (issue slots 65-70% busy).  4096 x 151,936 bf16:
-// 208 us (6.0 TB/s), without the entropy 181 us (6.9 TB/s).  The search waits on
-// barriers and on L2: 20 alternatives add 36 us there, 64 add 46 us, and 16 add
+// What bounds it: with the entropy, the instructions around the exponentials
+// (an element's unpacking, two packed FMAs and a packed add a pair): the issue
+// slots are 65-70% busy and the rest is their latency.  4096 x 151,936 bf16:
+// 204 us (6.1 TB/s), without the entropy 184 us (6.8 TB/s).  The search waits on
+// barriers and on L2: 16 alternatives add 35 us there, 64 add 50 us, and 16 add
 // 50 us to 210 us at 16,384 x 32,000; many small CTAs cover that for one
 // another.  One warp that searched a row behind the consumers took 234 us there,
 // but 440 us against 331 at 16,384 x 32,000 and k = 64, and 27 us against 19 for
