@@ -21,6 +21,8 @@
 //     consumers' partial statistics into the row's loss and gradient values,
 //     and stores the given tokens' gradients once the consumers have written
 //     the row.  The teacher's side is formed a row ahead.
+//   * A few long rows get a cluster each: its CTAs exchange their slices'
+//     statistics and given logits, and every one of them forms the same values.
 //
 // What bounds it: a row read once and written once, 734 us at 8192 x 151,936
 // bf16; measured 820 us (6.1 TB/s).  The two passes take about the same time,
@@ -40,6 +42,7 @@ constexpr int kMaxEntries = RL_TOKEN_MAX_K;
 constexpr int kPerLane = kMaxEntries / 32;
 constexpr int kTable = 2048;  // pieces that share a place of the table differ by a multiple of this
 constexpr int kLead = 2;      // chunks of the next row's first pass before a row's second
+constexpr int kMaxCluster = 8;
 constexpr float kLnTiny = -87.33654475f;  // ln 2^-126
 constexpr float kTiny = 0x1p-126f;
 
@@ -87,6 +90,10 @@ struct DistillSmem {
   long long wcount[kWarps + 2];
   unsigned long long table[2];  // a row's entries are in tab[k & 1]
   unsigned long long sums, values, written;  // once a row: sums in, values out, row written
+  // clusters (of one row): what every CTA found in its slice, in every CTA's memory
+  float slice_z[kMaxEntries];
+  float2 slice_tail[kMaxCluster];               // m, r
+  unsigned long long slices, read_again;        // all are in; a row taken again has been read
   float m, factor;             // pass 2: dz = 2^((z - m) c) factor
   int plain;                   // pass 2 by differences to m
   int abort;
@@ -394,8 +401,9 @@ __device__ __forceinline__ long long count_rows(const DistillArgs& a, long long 
   return N;
 }
 
-// kThreads consumers, the producer warp and the row warp.
-template <int DT, int kThreads, int kCtas>
+// kThreads consumers, the producer warp and the row warp.  kCluster: the CTAs
+// of a cluster share its one row.
+template <int DT, int kThreads, int kCtas, bool kCluster>
 __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(const DistillArgs a) {
   using F = Fmt<DT>;
   using S = DistillSmem<kThreads>;
@@ -406,11 +414,16 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
   volatile int* abort = &sm.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int V = static_cast<int>(a.V), K = a.K;
-  const long long first = blockIdx.x, stride = gridDim.x;
-  const int n_pieces = (V + F::kPiece - 1) / F::kPiece;
-  const int n_vecs = (V + F::kVec - 1) / F::kVec;
-  const long long row_bytes16 = (static_cast<long long>(V) * F::kBytes + 15) & ~15LL;
-  const int n_chunks = static_cast<int>((row_bytes16 + kChunk - 1) / kChunk);
+  // this CTA's pieces are g0 .. g0 + n_mine - 1: n_elems elements from byte b0 on
+  const int csize = kCluster ? static_cast<int>(cluster_size()) : 1, rank = kCluster ? static_cast<int>(cluster_rank()) : 0;
+  const long long first = blockIdx.x / csize, stride = gridDim.x / csize;
+  const int n_pieces = (V + F::kPiece - 1) / F::kPiece, per = (n_pieces + csize - 1) / csize;
+  const int g0 = kCluster ? min(n_pieces, rank * per) : 0, n_mine = kCluster ? min(n_pieces, g0 + per) - g0 : n_pieces;
+  const int e0 = g0 * F::kPiece, n_elems = kCluster ? min(V - e0, n_mine * F::kPiece) : V;
+  const long long b0 = static_cast<long long>(g0) * kPieceBytes;
+  const int n_vecs = (n_elems + F::kVec - 1) / F::kVec;
+  const long long n_bytes = static_cast<long long>(n_vecs) * 16;
+  const int n_chunks = static_cast<int>((n_bytes + kChunk - 1) / kChunk);
   const int lead = min(n_chunks, kLead);
 
   if (tid == 0) {
@@ -420,11 +433,14 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
     mbar_init(smem_addr(&sm.sums), kWarps);
     mbar_init(smem_addr(&sm.values), 1);
     mbar_init(smem_addr(&sm.written), kWarps);
+    mbar_init(smem_addr(&sm.slices), csize);
+    mbar_init(smem_addr(&sm.read_again), csize);
     sm.abort = 0;
     fence_mbar_init();
   }
   for (int i = tid; i < 2 * kTable; i += kThreads + 64) sm.tab[i / kTable].head[i % kTable] = 0;
   __syncthreads();
+  if (kCluster) cluster_sync_all();
 
   if (warp == kWarps) {
     // ---------------------------------------------------------------- producer
@@ -436,13 +452,13 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
     const int passes = a.dlogits ? 2 : 1;
     // chunks [q0, q1) of a row, lane 0; none of row -1
     auto issue = [&](long long row, int q0, int q1, uint64_t pol) {
-      const unsigned char* src = a.logits + row * a.row_bytes;
+      const unsigned char* src = a.logits + row * a.row_bytes + b0;
       for (int q = q0; q < q1 && ok; ++q) {
         ok = sm.ring.reserve(it, abort);
         if (!ok) break;
         sm.row_of[it % S::kSlots] = row;
         const long long off = static_cast<long long>(q) * kChunk;
-        sm.ring.fill(it, src + off, static_cast<uint32_t>(min(static_cast<long long>(kChunk), row_bytes16 - off)), pol);
+        sm.ring.fill(it, src + off, static_cast<uint32_t>(min(static_cast<long long>(kChunk), n_bytes - off)), pol);
         ++it;
       }
     };
@@ -509,18 +525,49 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
       if (!__all_sync(0xffffffffu, wait_bounded<false>(smem_addr(&sm.sums), k & 1, abort))) break;
       RowStats tail = join_parts<kWarps>(sm.part, F::kFloor, a.c, lane);
       int id[kPerLane];
-      float z[kPerLane], M = tail.m;
+      float z[kPerLane];
+      bool mine[kPerLane];  // in this CTA's slice
 #pragma unroll
       for (int i = 0; i < kPerLane; ++i) {
         id[i] = tab.id[lane + 32 * i];
-        z[i] = id[i] >= 0 ? tab.z[lane + 32 * i] : -INFINITY;
-        M = max_nan(M, z[i]);
+        mine[i] = kCluster ? id[i] >= e0 && id[i] < e0 + n_elems : id[i] >= 0;
+        z[i] = mine[i] ? tab.z[lane + 32 * i] : -INFINITY;
       }
+      if (kCluster) {
+        // everything to everyone; the same values follow in every CTA
+        for (int q = 0; q < csize; ++q) {
+#pragma unroll
+          for (int i = 0; i < kPerLane; ++i)
+            if (mine[i]) st_cluster_f32(map_to_rank(smem_addr(&sm.slice_z[lane + 32 * i]), q), z[i]);
+          if (lane == 0) {
+            const uint32_t to = map_to_rank(smem_addr(&sm.slice_tail[rank]), q);
+            st_cluster_f32(to, tail.m);
+            st_cluster_f32(to + 4, tail.r);
+          }
+        }
+        fence_cluster();
+        __syncwarp();
+        if (lane < csize) mbar_arrive_remote(map_to_rank(smem_addr(&sm.slices), lane));
+        if (!__all_sync(0xffffffffu, wait_bounded<true>(smem_addr(&sm.slices), 0, abort))) break;
+        tail = RowStats{sm.slice_tail[0].x, sm.slice_tail[0].y, 0.f};
+        for (int q = 1; q < csize; ++q)
+          tail = merge_row(tail, RowStats{sm.slice_tail[q].x, sm.slice_tail[q].y, 0.f}, a.c);
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) z[i] = id[i] >= 0 ? sm.slice_z[lane + 32 * i] : -INFINITY;
+      }
+      float M = tail.m;
+#pragma unroll
+      for (int i = 0; i < kPerLane; ++i) M = max_nan(M, z[i]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
       const bool plain = needs_exact<F>(M, a.c);
       if (plain) {
         tail = exact_tail<F>(a.logits + row * a.row_bytes, V, a.c, tab, lane);
+        if (kCluster) {  // no CTA may write its slice (of logits in place) before all have read the row
+          __syncwarp();
+          if (lane < csize) mbar_arrive_remote(map_to_rank(smem_addr(&sm.read_again), lane));
+          if (!__all_sync(0xffffffffu, wait_bounded<true>(smem_addr(&sm.read_again), 0, abort))) break;
+        }
         M = tail.m;
 #pragma unroll
         for (int i = 0; i < kPerLane; ++i) M = max_nan(M, z[i]);
@@ -534,12 +581,14 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
         sm.factor = t.factor;
         sm.plain = plain;
         mbar_arrive(smem_addr(&sm.values));
-        acc[0] += t.loss;
-        acc[1] += t.fwd;
-        acc[2] += t.rev;
-        acc[3] += t.qt;
-        acc[4] += t.pt;
-        if (a.row_loss) a.row_loss[row] = static_cast<float>(t.loss);
+        if (rank == 0) {
+          acc[0] += t.loss;
+          acc[1] += t.fwd;
+          acc[2] += t.rev;
+          acc[3] += t.qt;
+          acc[4] += t.pt;
+          if (a.row_loss) a.row_loss[row] = static_cast<float>(t.loss);
+        }
       }
       // this row's table for the row after next (every consumer is past its first pass)
       __syncwarp();
@@ -559,7 +608,7 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
         unsigned char* dst = a.dlogits + done_row * a.row_bytes;
 #pragma unroll
         for (int i = 0; i < kPerLane; ++i)
-          if (id[i] >= 0) F::store(dst, id[i], d[i]);
+          if (mine[i]) F::store(dst, id[i], d[i]);
       }
     }
     // this CTA's sums, then the last CTA adds all of them in CTA order
@@ -613,18 +662,18 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
     if (a.mask) {
       RowsOf<false> masked(a.mask, a.R, first, lane);
       for (long long row = masked.next(stride, lane); row >= 0; row = masked.next(stride, lane)) {
-        if (tid == 0 && a.row_loss) a.row_loss[row] = 0.f;
+        if (tid == 0 && rank == 0 && a.row_loss) a.row_loss[row] = 0.f;
         if (!a.dlogits) continue;
-        unsigned char* dst = a.dlogits + row * a.row_bytes;
+        unsigned char* dst = a.dlogits + row * a.row_bytes + b0;
         for (int v = tid; v < n_vecs; v += kThreads) {
-          if ((v + 1) * F::kVec <= V)
+          if ((v + 1) * F::kVec <= n_elems)
             st_global_cs_v4(dst + static_cast<long long>(v) * 16, make_uint4(0u, 0u, 0u, 0u));
           else
-            for (int i = v * F::kVec; i < V; ++i) F::store(dst, i, 0.f);
+            for (int i = v * F::kVec; i < n_elems; ++i) F::store(dst, i, 0.f);
         }
       }
     }
-    const int n_full = V / F::kPiece / kThreads;  // chunks whose every piece is a full one
+    const int n_full = n_elems / F::kPiece / kThreads;  // chunks whose every piece is a full one
     uint32_t it = 0;
     WarpSum st;  // of the row whose first pass is under way
     // pass 1 over chunks [i0, i1) of the k-th row: every token that is not given
@@ -637,9 +686,9 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
         uint32_t w[16];
         const int sh = last ? 0 : lane >> 1;
         load_piece(w, 0, buf + tid * kPieceBytes, sh);
-        int j = p < n_pieces ? tab.head[p & (kTable - 1)] : 0;
+        int j = p < n_mine ? tab.head[(g0 + p) & (kTable - 1)] : 0;
         while (j) {
-          const int e = tab.id[j - 1] - p * F::kPiece;
+          const int e = tab.id[j - 1] - (g0 + p) * F::kPiece;
           if (e >= 0 && e < F::kPiece) {
             tab.z[j - 1] = F::load_shared(sm.ring.data[it % S::kSlots] + tid * kPieceBytes, e);
             F::drop(w, 0, (((e / F::kVec) - sh) & 3) * F::kVec + e % F::kVec);
@@ -647,7 +696,7 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
           j = tab.next[j - 1];
         }
         sm.ring.release(it, lane);
-        if (last) F::cut(w, 0, p < n_pieces ? min(F::kPiece, V - p * F::kPiece) : 0);
+        if (last) F::cut(w, 0, p < n_mine ? min(F::kPiece, n_elems - p * F::kPiece) : 0);
         __syncwarp();
         if (i == 0) sum_init<F>(st, w, a.c);
         sum_piece<F>(st, w, a.c);
@@ -656,9 +705,9 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
     // pass 2: 2^((z - m) c) factor.  16-bit outputs take |factor| into the
     // exponent (one rounding of at most 2^-15 for |m c| <= 1024, far below
     // theirs) and the sign on the packed result; fp32 outputs multiply.
-    const int n_full2 = n_vecs / kVecs - (V % F::kVec && n_vecs % kVecs == 0 ? 1 : 0);  // chunks of full vectors only
+    const int n_full2 = n_vecs / kVecs - (n_elems % F::kVec && n_vecs % kVecs == 0 ? 1 : 0);  // chunks of full vectors only
     auto pass2 = [&](long long row) {
-      unsigned char* dst = a.dlogits + row * a.row_bytes;
+      unsigned char* dst = a.dlogits + row * a.row_bytes + b0;
       const float m = sm.m, factor = sm.factor;
       constexpr bool kFold = F::kBytes == 2;
       const float nm = -m * a.c, rho = fmaf(-m, a.c, -nm);
@@ -710,14 +759,14 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
 #pragma unroll
             for (int j = 1; j < kVecsPerThread; ++j) wq = j == q ? w[j] : wq;
             const uint4 u = plain ? vec_plain(wq) : vec(wq);
-            if ((v + 1) * F::kVec <= V) {
+            if ((v + 1) * F::kVec <= n_elems) {
               st_global_cs_v4(out + q * kThreads * 16, u);
             } else if (v < n_vecs) {
               float z[F::kVec];
               F::unpack(u, z);
 #pragma unroll
               for (int j = 0; j < F::kVec; ++j)
-                if (v * F::kVec + j < V) F::store(dst, v * F::kVec + j, z[j]);
+                if (v * F::kVec + j < n_elems) F::store(dst, v * F::kVec + j, z[j]);
             }
           }
         }
@@ -756,21 +805,45 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
       prev = row;
     }
   }
+  if (kCluster) cluster_sync_all();  // no CTA leaves while another may still write its memory
 }
 
 // ------------------------------------------------------------------ host side
-template <int DT, int kThreads, int kCtas>
-rl_status launch(const DistillArgs& a, int dev, int sms, cudaStream_t stream) {
-  const void* fn = reinterpret_cast<const void*>(&topk_distill_kernel<DT, kThreads, kCtas>);
+template <int DT, int kThreads, int kCtas, bool kCluster>
+rl_status launch(const DistillArgs& a, int cluster, int dev, int sms, cudaStream_t stream) {
+  const void* fn = reinterpret_cast<const void*>(&topk_distill_kernel<DT, kThreads, kCtas, kCluster>);
   const int smem = static_cast<int>(sizeof(DistillSmem<kThreads>));
   static std::atomic<unsigned long long> allowed{0};
   const rl_status st = allow_smem(fn, dev, smem, allowed);
   if (st != RL_OK) return st;
   long long grid = static_cast<long long>(kCtas) * sms;
   if (grid > kMaxGrid) grid = kMaxGrid;
-  if (grid > a.R) grid = a.R > 0 ? a.R : 1;
-  topk_distill_kernel<DT, kThreads, kCtas><<<static_cast<unsigned>(grid), kThreads + 64, smem, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? RL_OK : RL_ERR_CUDA;
+  if (kCluster || grid > a.R) grid = a.R > 0 ? a.R * cluster : 1;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads + 64);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = kCluster ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, topk_distill_kernel<DT, kThreads, kCtas, kCluster>, a) == cudaSuccess ? RL_OK : RL_ERR_CUDA;
+}
+
+// CTAs of 128 threads that share a row: up to 8, each with a few chunks, where
+// that leaves two a SM at most.  Rows x 151,936 bf16, 64 entries, us on 8 CTAs
+// and on one of 512 threads: 1 row 16.4, 22.2; 38 rows 20.8, 22.4; 64 rows 22.6,
+// 23.0; 76 rows 26.5, 23.0.  A row costs the entries' table, the exchange and the
+// values once in any case.
+int cluster_for(long long R, long long n_pieces, int sms) {
+  int c = 1;
+  if (R > 0 && R * kMaxCluster <= 2LL * sms && R * kMaxCluster <= kMaxGrid)
+    while (c < kMaxCluster && n_pieces >= static_cast<long long>(c) * 4 * 128) c *= 2;
+  return c;
 }
 
 // Rows of more than kLongRow bytes go one to a SM, on 512 consumer threads: the
@@ -782,8 +855,10 @@ constexpr long long kLongRow = 100 * 1024;
 
 template <int DT>
 rl_status launch_any(const DistillArgs& a, int dev, int sms, cudaStream_t stream) {
-  return a.V * Fmt<DT>::kBytes > kLongRow ? launch<DT, 512, 1>(a, dev, sms, stream)
-                                          : launch<DT, 128, 4>(a, dev, sms, stream);
+  const int c = cluster_for(a.R, (a.V + Fmt<DT>::kPiece - 1) / Fmt<DT>::kPiece, sms);
+  if (c > 1) return launch<DT, 128, 4, true>(a, c, dev, sms, stream);
+  return a.V * Fmt<DT>::kBytes > kLongRow ? launch<DT, 512, 1, false>(a, 1, dev, sms, stream)
+                                          : launch<DT, 128, 4, false>(a, 1, dev, sms, stream);
 }
 
 }  // namespace

@@ -190,3 +190,27 @@ def test_rows_dealt_out_one_by_one(pattern):
         assert (out["topk_ids"][off] == -1).all()
         assert all((out[n][off] == 0).all() for n in ("logp", "entropy", "lse", "topk_logp"))
     assert int(st.item()) == 0
+
+
+def test_dealt_rows_beside_another_call_and_replayed():
+    """Two calls whose rows are dealt out run on two streams at once, and one is
+    captured and replayed: the bits of a call alone."""
+    R, V = 3000, 60000
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    z = [torch.empty((R, V), dtype=torch.bfloat16, device=DEV).normal_(0.0, 3.0, generator=gen) for _ in range(2)]
+    mask = (torch.rand(R, device=DEV, generator=gen) < 0.7)
+    call = lambda i, s=None: torch_api.token_logprobs(z[i], mask=mask, k=5, want_lse=True, stream=s)  # noqa: E731
+    ref = [call(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(DEV) for _ in range(2)]
+    outs = [[call(i, streams[i]) for i in range(2)] for _ in range(5)]
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        got = call(0)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    for o in outs + [[got]]:
+        for i, out in enumerate(o):
+            assert all(torch.equal(out[n], ref[i][n]) for n in ("entropy", "lse", "topk_ids", "topk_logp"))

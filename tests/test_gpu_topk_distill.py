@@ -357,3 +357,44 @@ def test_more_rows_than_one_round_of_ctas_long_rows():
     st = torch_api.read_distill_stats(out["stats"])
     assert st["n_rows"] == int(mask.sum()) and st["device_error"] == 0
     assert abs(st["loss"] - out["row_loss"].double().sum().item()) < 1e-6 * R
+
+
+@pytest.mark.parametrize("R,V,dtype,K,reverse,inplace", [
+    (1, 151936, "bf16", 64, 0.0, False), (3, 70001, "f16", 16, 0.5, True), (17, 40000, "f32", 128, 1.0, True),
+    (38, 65537, "bf16", 33, 0.5, False), (75, 33000, "f16", 5, 0.0, True), (130, 20000, "f32", 9, 0.5, False),
+    (304, 16400, "bf16", 12, 0.5, True)])
+def test_few_rows_share_their_ctas(R, V, dtype, K, reverse, inplace):
+    """Clusters of up to 8 CTAs a row, and numbers of rows on both sides of what
+    gets clusters; entries at the slices' edges."""
+    z = logits(R, V, dtype, R + V)
+    ids, lq = teacher(z, K, 3)
+    per = 16 if dtype == "f32" else 32
+    pieces = -(-V // per)
+    edges = [0, V - 1] + [min(V - 1, e) for c in (2, 4, 8) for e in (-(-pieces // c) * per - 1, -(-pieces // c) * per)]
+    edges = [e for e in dict.fromkeys(edges) if e not in ids[0].tolist()][:K]
+    ids[0, K - len(edges):] = torch.tensor(edges)
+    mask = (torch.arange(R) % 6 != 4).to(torch.uint8) if R > 4 else None
+    check(z, dtype, ids, lq, inplace=inplace, mask=mask, reverse=reverse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_few_rows_taken_again(dtype):
+    """Rows whose statistics are taken by differences (all tokens at or below
+    the floor, or far above the frame) with their gradient written in place of
+    the logits, in clusters, between rows that are not."""
+    V, R = 40003, 12
+    z = logits(R, V, dtype, 8, sure=False)
+    low = torch.finfo(TORCH[dtype]).min
+    z[1] = low
+    z[2, 100:] = -torch.inf
+    z[4, :] = -60000.0 if dtype == "f16" else -1e30
+    z[4, 39000] = low if dtype == "f16" else -0.99e30
+    z[5, :30000] = -torch.inf          # whole slices with nothing
+    z[7, 1:] = low
+    ids, lq = teacher(z, 6, 3)
+    ids[4], ids[1] = torch.arange(6) * 7000, torch.arange(6) * 6000 + 5
+    lq = torch.log_softmax(torch.randn(R, 6, generator=torch.Generator().manual_seed(4)), 1) - 0.3
+    ids[7], ids[2] = torch.arange(6), torch.arange(6) + 90
+    a, _, _ = check(z, dtype, ids, lq)
+    b, _, _ = check(z, dtype, ids, lq, inplace=True)
+    assert np.array_equal(storage(a["dlogits"]), storage(b["dlogits"]))
