@@ -851,14 +851,19 @@ int cluster_for(long long R, long long n_pieces, int sms) {
 // each, so that one row's serial part overlaps the others' passes.  512 x 1
 // against 128 x 4, us, bf16: 4096 x 151,936: 427, 585; 4096 x 60,000: 208, 208;
 // 4096 x 50,000: 205, 177; 16,384 x 32,000: 561, 465; 16,384 x 8000: 522, 205.
-constexpr long long kLongRow = 100 * 1024;
+// Many rows of at most kTinyRow bytes, which are bound by the row warp's serial
+// steps, go seven to a SM, on 32 consumer threads each: 32,768 x 1000 bf16, 16
+// entries: 271 against 176; x 2000: 268, 209; x 4000: 271, 285; 1100 x 1000: 24, 26.
+constexpr long long kLongRow = 100 * 1024, kTinyRow = 4 * 1024;
 
 template <int DT>
 rl_status launch_any(const DistillArgs& a, int dev, int sms, cudaStream_t stream) {
   const int c = cluster_for(a.R, (a.V + Fmt<DT>::kPiece - 1) / Fmt<DT>::kPiece, sms);
   if (c > 1) return launch<DT, 128, 4, true>(a, c, dev, sms, stream);
-  return a.V * Fmt<DT>::kBytes > kLongRow ? launch<DT, 512, 1, false>(a, 1, dev, sms, stream)
-                                          : launch<DT, 128, 4, false>(a, 1, dev, sms, stream);
+  const long long bytes = a.V * Fmt<DT>::kBytes;
+  if (bytes > kLongRow) return launch<DT, 512, 1, false>(a, 1, dev, sms, stream);
+  if (bytes <= kTinyRow && a.R >= 14LL * sms) return launch<DT, 32, 7, false>(a, 1, dev, sms, stream);
+  return launch<DT, 128, 4, false>(a, 1, dev, sms, stream);
 }
 
 }  // namespace

@@ -398,3 +398,13 @@ def test_few_rows_taken_again(dtype):
     a, _, _ = check(z, dtype, ids, lq)
     b, _, _ = check(z, dtype, ids, lq, inplace=True)
     assert np.array_equal(storage(a["dlogits"]), storage(b["dlogits"]))
+
+
+@pytest.mark.parametrize("R,V,dtype,K,reverse", [
+    (2300, 1, "bf16", 1, 0.0), (2300, 37, "f32", 8, 0.5), (2200, 1000, "bf16", 128, 0.5), (4000, 2048, "f16", 16, 0.0),
+    (2200, 1024, "f32", 5, 1.0), (2200, 2049, "bf16", 16, 0.0)])
+def test_many_tiny_rows(R, V, dtype, K, reverse):
+    """Many rows of at most 4 KB, and one element more."""
+    z = logits(R, V, dtype, V)
+    ids, lq = teacher(z, K, 3)
+    check(z, dtype, ids, lq, mask=(torch.arange(R) % 5 != 2).to(torch.uint8), reverse=reverse)
