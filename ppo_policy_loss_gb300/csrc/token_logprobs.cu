@@ -302,6 +302,9 @@ __device__ __noinline__ bool search_fast(LpSmem<DT, kT>& sm, const typename Fmt<
   const int enough = k + k / 8 + 4;
   if (tid == 0) sm.n_pieces = sm.n_elems = 0;
   if (tid < k) sm.found[tid] = 0;
+  // no more pieces than alternatives: no bound between them, every element
+  // would be listed (32,768 x 1000, k = 32: 400 us with the attempt, 298 without)
+  if (n_mine <= k && n_mine * F::kPiece > kList) return false;
   uint32_t hi = top + 1, lo = 1;  // fewer than k reach hi, unless NaN does
   int n = 0;
   for (uint32_t step = F::kOrderStep;; step *= 4) {
