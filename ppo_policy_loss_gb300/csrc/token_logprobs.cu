@@ -291,8 +291,8 @@ __device__ __forceinline__ int count_reaching(const uint32_t (&best)[2], uint32_
 // row's maximum downwards in widening steps; at least k elements reach it
 // then, nearly all of them in pieces of their own, so the pieces that reach
 // it are listed, their elements read again (from L2), and those that reach it
-// ranked by counting.  False if a list overflows (many equal values, or a
-// large k of few pieces): search_slow then.
+// ranked by counting.  False if a list overflows, or would (many
+// equal values, or a large k of few pieces): search_slow then.
 template <int DT, int kT>
 __device__ __noinline__ bool search_fast(LpSmem<DT, kT>& sm, const typename Fmt<DT>::Key* keys, const unsigned char* src,
                                             int g0, int n_mine, int V, int k, const uint32_t (&best)[2], uint32_t top,
@@ -300,7 +300,7 @@ __device__ __noinline__ bool search_fast(LpSmem<DT, kT>& sm, const typename Fmt<
   using F = Fmt<DT>;
   const bool both = k > kT / 4;
   const int enough = k + k / 8 + 4;
-  if (tid == 0) sm.n_pieces = sm.n_elems = 0;
+  if (tid == 0) sm.n_pieces = sm.n_elems = 0;  // the counts below are the barrier before the lists' first entries
   if (tid < k) sm.found[tid] = 0;
   // no more pieces than alternatives: no bound between them, every element
   // would be listed (32,768 x 1000, k = 32: 400 us with the attempt, 298 without)
