@@ -70,15 +70,6 @@ constexpr uint32_t kMnBlock = kGK * 128;      // one 64-element M/N block of an 
 #ifndef RLG_STORE
 #define RLG_STORE 0
 #endif
-// RLG_CLUSTER CTAs per cluster (1 or 2).  With 2, the CTAs of a pair take
-// row tiles 2p and 2p + 1 of the same column tile: each TMA-loads half of the
-// B tile and multicasts it to both, so each CTA reads 32 KB per K block from
-// L2 instead of 48 KB, and each MMA commit frees the stage in both CTAs.
-#ifndef RLG_CLUSTER
-#define RLG_CLUSTER 1
-#endif
-constexpr int kCl = RLG_CLUSTER;
-static_assert(kCl == 1 || kCl == 2, "one CTA or a pair per cluster");
 constexpr int kEpiWarps = RLG_EPI_WARPS;
 constexpr int kEpiGroups = kEpiWarps / 4;          // warpgroups, each on kGN / kEpiGroups columns
 constexpr int kStageBufs = RLG_STAGE_BUFS;
@@ -186,19 +177,15 @@ lmhead_grad_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
   GSmem& sm = *reinterpret_cast<GSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abort_flag = &sm.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // units are (row tile, or pair of row tiles with clusters of two CTAs;
-  // slice of column tiles), the slice's tiles taken in order
+  // units are (row tile, slice of column tiles), the slice's tiles taken in order
   const int n_nt = a.n_nt, n_kb = a.n_kb, n_sl = a.n_sl;
-  const int n_mt = (a.n_mt + kCl - 1) / kCl, n_units = n_mt * n_sl;
-  const uint32_t crank = kCl > 1 ? cluster_rank() : 0;
-  const int cid = kCl > 1 ? static_cast<int>(cluster_id()) : static_cast<int>(blockIdx.x);
-  const int ncl = kCl > 1 ? static_cast<int>(cluster_count()) : static_cast<int>(gridDim.x);
-  constexpr uint16_t kMask = static_cast<uint16_t>((1u << kCl) - 1);
+  const int n_mt = a.n_mt, n_units = n_mt * n_sl;
+  const int cta = static_cast<int>(blockIdx.x), n_ctas = static_cast<int>(gridDim.x);
 
   if (tid == 0) {
     for (int s = 0; s < kGStages; ++s) {
       mbar_init(smem_addr(&sm.full[s]), 1);
-      mbar_init(smem_addr(&sm.empty[s]), kCl);  // freed by the MMA commits of every CTA that writes it
+      mbar_init(smem_addr(&sm.empty[s]), 1);  // freed by the MMA commit
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_addr(&sm.acc_full[s]), 1);
@@ -218,7 +205,6 @@ lmhead_grad_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
   }
   tc_fence_before();
   __syncthreads();
-  if (kCl > 1) cluster_sync_all();  // the peer's barriers exist before any multicast reaches them
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
@@ -227,10 +213,9 @@ lmhead_grad_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
     if (lane == 0) {
       uint32_t it = 0;
       bool stop = false;
-      for (int u = cid; u < n_units && !stop; u += ncl) {
+      for (int u = cta; u < n_units && !stop; u += n_ctas) {
         int mt, vs;
         unit_tile(u, n_mt, n_sl, a.group, mt, vs);
-        mt = mt * kCl + static_cast<int>(crank);
         for (int nt = slice_first(vs, n_nt, n_sl); nt < slice_first(vs + 1, n_nt, n_sl) && !stop; ++nt)
         for (int kb = 0; kb < n_kb; ++kb, ++it) {
           const uint32_t s = it % kGStages, round = it / kGStages;
@@ -247,22 +232,12 @@ lmhead_grad_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
           } else {
             tma_load_2d(smem_addr(sm.a[s]), &tmap_a, kb * kGK, mt * kGM, fb);
           }
-          // this CTA's share of the B tile (all of it without a cluster)
           if (kBMN) {
 #pragma unroll
-            for (int j = 0; j < kGN / 64 / kCl; ++j) {
-              const int jj = static_cast<int>(crank) * (kGN / 64 / kCl) + j;
-              if (kCl > 1)
-                tma_load_2d_mc(smem_addr(sm.b[s]) + jj * kMnBlock, &tmap_b, nt * kGN + jj * 64, kb * kGK, fb, kMask);
-              else
-                tma_load_2d(smem_addr(sm.b[s]) + jj * kMnBlock, &tmap_b, nt * kGN + jj * 64, kb * kGK, fb);
-            }
+            for (int j = 0; j < kGN / 64; ++j)
+              tma_load_2d(smem_addr(sm.b[s]) + j * kMnBlock, &tmap_b, nt * kGN + j * 64, kb * kGK, fb);
           } else {
-            const int r0 = static_cast<int>(crank) * (kGN / kCl);
-            if (kCl > 1)
-              tma_load_2d_mc(smem_addr(sm.b[s]) + r0 * 128, &tmap_b, kb * kGK, nt * kGN + r0, fb, kMask);
-            else
-              tma_load_2d(smem_addr(sm.b[s]), &tmap_b, kb * kGK, nt * kGN, fb);
+            tma_load_2d(smem_addr(sm.b[s]), &tmap_b, kb * kGK, nt * kGN, fb);
           }
         }
       }
@@ -275,10 +250,10 @@ lmhead_grad_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
     if (lane == 0) {
       uint32_t it = 0, acc_it = 0;
       bool stop = false, issued = false;
-      int mt_u = 0, vs = 0, nt = 0, nt_end = 0, u = cid - ncl;
+      int mt_u = 0, vs = 0, nt = 0, nt_end = 0, u = cta - n_ctas;
       while (!stop) {
         if (nt == nt_end) {  // next unit: its slice's column tiles
-          u += ncl;
+          u += n_ctas;
           if (u >= n_units) break;
           unit_tile(u, n_mt, n_sl, a.group, mt_u, vs);
           nt = slice_first(vs, n_nt, n_sl);
@@ -313,11 +288,7 @@ lmhead_grad_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
             umma_f16(d_tmem, ad, bd, a.idesc, (kb | k) != 0);
           }
           issued = true;
-          // the stage is free once these MMAs have read it (in every CTA that loads into it)
-          if (kCl > 1)
-            umma_commit_mc(smem_addr(&sm.empty[s]), kMask);
-          else
-            umma_commit(smem_addr(&sm.empty[s]));
+          umma_commit(smem_addr(&sm.empty[s]));  // the stage is free once these MMAs have read it
         }
         if (stop) break;
         umma_commit(smem_addr(&sm.acc_full[buf]));  // accumulator ready for the epilogue
@@ -339,10 +310,9 @@ lmhead_grad_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
     const uint64_t store_pol = policy_evict_first();
 #endif
     bool stop = false;
-    for (int u = cid; u < n_units && !stop; u += ncl) {
+    for (int u = cta; u < n_units && !stop; u += n_ctas) {
       int mt, vs;
       unit_tile(u, n_mt, n_sl, a.group, mt, vs);
-      mt = mt * kCl + static_cast<int>(crank);
       for (int nt = slice_first(vs, n_nt, n_sl); nt < slice_first(vs + 1, n_nt, n_sl); ++nt, ++acc_it) {
       const long long row = static_cast<long long>(mt) * kGM + r_in_tile;
       const bool row_ok = row < a.M;
@@ -500,7 +470,6 @@ lmhead_grad_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
     tc_fence_after();
     tmem_dealloc(tmem, kGTmemCols);
   }
-  if (kCl > 1) cluster_sync_all();  // no CTA leaves while its peer may still multicast into it
 }
 
 // ------------------------------------------------------------------ host side
@@ -512,37 +481,22 @@ rl_status launch_grad(const CUtensorMap& ma, const CUtensorMap& mb, const CUtens
   const int smem = static_cast<int>(sizeof(GSmem)) + 1024;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || tc_device_sms(&sms) != RL_OK) return RL_ERR_CUDA;
-  static int max_clusters = 0;
   auto fn = lmhead_grad_kernel<kAMN, kBMN, kEpi>;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCl;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
   cfg.blockDim = dim3(kGThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   {
     std::lock_guard<std::mutex> lock(mu);
     if (attr_dev != dev) {
       if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return RL_ERR_CUDA;
-      int n = sms;
-      if (kCl > 1) {
-        cfg.gridDim = dim3(kCl);
-        if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) return RL_ERR_CUDA;
-      }
-      max_clusters = n;
       attr_dev = dev;
     }
   }
-  const long long units = static_cast<long long>((args.n_mt + kCl - 1) / kCl) * args.n_sl;
+  const long long units = static_cast<long long>(args.n_mt) * args.n_sl;
   if (units == 0) return RL_OK;
-  const long long n_clusters = units < max_clusters ? units : max_clusters;
-  cfg.gridDim = dim3(static_cast<unsigned>(n_clusters * kCl));
+  cfg.gridDim = dim3(static_cast<unsigned>(units < sms ? units : sms));
   return cudaLaunchKernelEx(&cfg, fn, ma, mb, mo, args) == cudaSuccess ? RL_OK : RL_ERR_CUDA;
 }
 
@@ -596,12 +550,12 @@ extern "C" rl_status rl_lmhead_dlogits(const void* hidden, long long ld_h, const
   if (tc_encode_fn(&enc) != RL_OK) return RL_ERR_CUDA;
   CUtensorMap ma, mb, mo;
   if (!tc_make_map(enc, &ma, tmap_type(dtype), hidden, R, D, ld_h, kGK, kGM) ||
-      !tc_make_map(enc, &mb, tmap_type(dtype), weight, V, D, ld_w, kGK, kGN / kCl) ||
+      !tc_make_map(enc, &mb, tmap_type(dtype), weight, V, D, ld_w, kGK, kGN) ||
       !tc_make_map(enc, &mo, tmap_type(dtype), dlogits, R, V, ld_dz, 64, kStageRows))
     return RL_ERR_CUDA;
   GArgs g = base_args(R, V, D, dtype == RL_BF16, false, false);
   const long long tile_bytes = static_cast<long long>(kGM) * g.n_kb * kGK * 2;
-  const long long grp = kHiddenL2Bytes / tile_bytes / kCl;  // groups of row-tile pairs
+  const long long grp = kHiddenL2Bytes / tile_bytes;
   g.group = static_cast<int>(grp < 1 ? 1 : (grp > g.n_mt ? g.n_mt : grp));
   g.out = dlogits;
   g.ld_out = ld_dz;
