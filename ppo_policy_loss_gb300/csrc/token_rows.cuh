@@ -466,7 +466,9 @@ __device__ __forceinline__ void add_piece(WarpStats& a, uint32_t (&w)[16], float
 
 // The sum of 2^x alone, over sets whose maximum need not be known: the frame
 // is that of the maximum of the warp's first piece, and moves up only when a
-// lane's sum passes kSumLimit.
+// lane's sum passes kSumLimit.  The sum so far then goes along by 2^(nm' - nm),
+// which its terms 2^(z c + nm) need to the bit; the last frame's rounding is
+// put right at the end, as above.
 constexpr float kSumLimit = 0x1p24f;
 struct WarpSum {
   float m, nm;
@@ -504,9 +506,10 @@ __device__ __forceinline__ void sum_piece(WarpSum& a, const uint32_t (&w)[16], f
     const float s = (a.r[0].x + a.r[0].y) + (a.r[1].x + a.r[1].y);
     if (again || !__any_sync(0xffffffffu, !(s < kSumLimit))) break;
     const float m = fmaxf(a.m, clamped_max<F>(w));
-    const float f = ex2_approx((a.m - m) * c);
+    const float nm = __fmul_rn(-m, c);  // rounded here, not fused into the difference
+    const float f = ex2_approx(nm - a.nm);
     a.m = m;
-    a.nm = -m * c;
+    a.nm = nm;
     a.r[0] = make_float2(f * ((r0.x + r0.y) + (r1.x + r1.y)), 0.f);
     a.r[1] = make_float2(0.f, 0.f);
     again = true;  // (a NaN passes)

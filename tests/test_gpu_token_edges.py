@@ -1,0 +1,53 @@
+"""The token operators on rows and in calls where one of their steps had gone
+wrong or was run by no other test.
+
+Bounds.  u = 2^-24 is half a step of fp32.  A term is 2^x with x = z c + nm, one
+fused multiply-add (|x| ln 2 u), or x = (z - m) c where a row is taken by
+differences (c, the difference and the product: 3 |x| ln 2 u); the hardware
+exponential adds 4 u.  A CTA's T threads each add V / T terms in at most four
+chains, then join lanes (5 steps), warps (4) and CTAs (7).  steps(V, T) counts
+V / T + 64 roundings, which is what T = 128 threads with one chain need, and
+more than four chains of T = 64 do."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import ppo_policy_loss_gb300 as rl
+from ppo_policy_loss_gb300 import torch_api
+from _tokens import TORCH, U, check_close, logits, storage
+from test_gpu_topk_distill import check, teacher, to_dev
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    rl.build()
+    rl.load()
+
+
+def steps(V, threads=128):
+    return V / threads + 64
+
+
+@pytest.mark.parametrize("R,V", [(40, 60001), (40, 20000), (3, 151936), (2200, 1024)])  # 512, 128, 8 x 128 and 32 threads
+@pytest.mark.parametrize("base,temp", [(1e3, 1.0), (1e4, 1.0), (1e3, 0.1), (1e4, 0.1), (1e3, 0.01), (1e4, 0.01), (6e4, 0.01)])
+def test_tail_sum_whose_frame_moves(R, V, base, temp):
+    """Rows of large logits whose first chunk lies 12 to 14 nats below the
+    rest: each warp's sum of the tail passes 2^24 after a few chunks and goes on
+    in the frame of a larger maximum, which rounds m c to another number."""
+    gen = torch.Generator().manual_seed(int(base) + V)
+    first = 16 * (512 if V == 60001 else 32 if V == 1024 else 128)
+    per = -(-(-(-V // 16)) // 8) * 16 if R == 3 else V  # a slice of the row
+    low = (torch.arange(V) % per) < first
+    rows = 11 if R > 1000 else R
+    down = 12.0 + 0.25 * (torch.arange(rows) % 9).float()
+    z = base + temp * (0.1 * torch.randn((rows, V), generator=gen) - low * down[:, None])
+    z = z.float().repeat(-(-R // rows), 1)[:R]
+    z = torch.nn.functional.pad(z, (0, -V % 4), value=float("nan"))[:, :V]
+    ids, lq = teacher(z[:rows], 8, 3, noise=temp, temperature=temp)
+    ids, lq = (t.repeat(-(-R // rows), 1)[:R].contiguous() for t in (ids, lq))
+    check(z, "f32", ids, lq, temperature=temp, reverse=0.5)
+    check(z, "f32", ids, lq, temperature=temp, tail="renormalise")
