@@ -308,7 +308,9 @@ __device__ __forceinline__ RowSums row_values(const DistillArgs& a, const EntryT
   }
   const bool nothing = a.renorm && t.n == 0;
   if (t.bad || r != r) L = __int_as_float(0x7fc00000);
-  if (!(M > -INFINITY)) L = __int_as_float(0x7fc00000);  // no distribution
+  // a maximum of -inf: no distribution; +inf (left out of r, or of teacher
+  // probability 0, it is in no other term) and NaN: none either
+  if (!(fabsf(M) < INFINITY)) L = __int_as_float(0x7fc00000);
   if (nothing && L == L) L = F = ct = 0.f;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {

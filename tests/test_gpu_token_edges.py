@@ -51,3 +51,30 @@ def test_tail_sum_whose_frame_moves(R, V, base, temp):
     ids, lq = (t.repeat(-(-R // rows), 1)[:R].contiguous() for t in (ids, lq))
     check(z, "f32", ids, lq, temperature=temp, reverse=0.5)
     check(z, "f32", ids, lq, temperature=temp, tail="renormalise")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("R,V", [(9, 704), (9, 50000), (60, 60000), (2200, 1000)])
+def test_nan_and_infinity_make_their_row_nan_in_the_distillation(dtype, R, V):
+    """NaN or +inf at a given token, also one of teacher probability 0, or in
+    the tail: that row's loss and gradient are NaN, the others keep their bits."""
+    z = to_dev(logits(R, V, dtype, 3 + V))
+    ids, lq = (t.to(DEV) for t in teacher(z.cpu(), 6, 3))
+    lq[:, 2] = -torch.inf
+    lq[:, 3] = -90.0
+    bad = z.clone()
+    where = {1: ids[1, 0], 2: ids[2, 2], 3: ids[3, 3], 5: (ids[5].max() + 1) % V, 6: ids[6, 2], 7: ids[7, 0]}
+    while int(where[5]) in ids[5].tolist():
+        where[5] = (where[5] + 1) % V
+    for r, e in where.items():
+        bad[r, e] = torch.nan if r > 5 else torch.inf
+    for kw in (dict(), dict(reverse=1.0), dict(reverse=0.5, temperature=0.7), dict(tail="renormalise")):
+        ref, out = (torch_api.topk_distill(x, ids, lq, **kw) for x in (z, bad))
+        rows = torch.tensor(sorted(where), device=DEV)
+        assert torch.isnan(out["row_loss"][rows]).all() and torch.isnan(out["dlogits"][rows]).all(), kw
+        assert torch.isnan(out["loss"])
+        rest = torch.ones(R, dtype=torch.bool, device=DEV)
+        rest[rows] = False
+        assert torch.equal(out["row_loss"][rest], ref["row_loss"][rest])
+        assert torch.equal(out["dlogits"][rest], ref["dlogits"][rest])
+        assert torch.isfinite(ref["dlogits"].float()).all()
