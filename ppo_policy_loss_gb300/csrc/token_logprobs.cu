@@ -423,8 +423,9 @@ __device__ __noinline__ void search_slow(LpSmem<DT, kT>& sm, typename Fmt<DT>::K
 }
 
 // The statistics of a row that needs_exact names, by differences to its
-// maximum, -inf elements skipped.  Rare, so it reads the row again.  m = -inf:
-// no element is finite.  All consumer threads.
+// maximum, -inf elements skipped.  Rare, so it reads the row again.  The maxima
+// are counted, not summed, and one of them stays out, so that r is a sum of
+// small terms here too.  m = -inf: no element is finite.  All consumer threads.
 template <class F, int kT>
 __device__ __noinline__ RowStats exact_row(const unsigned char* row, int V, float c, RowStats* part, int tid) {
   const int n_vecs = (V + F::kVec - 1) / F::kVec;
@@ -448,11 +449,13 @@ __device__ __noinline__ RowStats exact_row(const unsigned char* row, int V, floa
   for (int w = 0; w < kT / 32; ++w) m = max_nan(m, part[w].m);
   row_barrier<kT>();
   float s = 0.f, t = 0.f;
+  int top = 0;
   if (m > -INFINITY)
     each([&](float z) {
       const float x = (z - m) * c;
       const float e = ex2_approx(x);
-      s += e;
+      top += z == m;
+      s += z == m ? 0.f : e;
       if (e > 0.f) t = fmaf(e, x, t);
     });
 #pragma unroll
@@ -460,15 +463,19 @@ __device__ __noinline__ RowStats exact_row(const unsigned char* row, int V, floa
     s += __shfl_xor_sync(0xffffffffu, s, o);
     t += __shfl_xor_sync(0xffffffffu, t, o);
   }
-  if ((tid & 31) == 0) part[tid >> 5] = RowStats{m, s, t};
+  top = __reduce_add_sync(0xffffffffu, top);
+  if ((tid & 31) == 0) part[tid >> 5] = RowStats{static_cast<float>(top), s, t};  // exact: at most 2^24 in a warp's share
   row_barrier<kT>();
   s = t = 0.f;
+  float others = -1.f;
   for (int w = 0; w < kT / 32; ++w) {
+    others += part[w].m;
     s += part[w].r;
     t += part[w].t;
   }
-  if (m != m) s = t = m;
-  return RowStats{m, s - 1.f, t};
+  s += others;
+  if (!(m < INFINITY)) s = t = __int_as_float(0x7fc00000);  // NaN, +inf
+  return RowStats{m, s, t};
 }
 
 // A CTA (or, for few rows, a cluster of up to 8, each with a slice of the

@@ -78,3 +78,27 @@ def test_nan_and_infinity_make_their_row_nan_in_the_distillation(dtype, R, V):
         assert torch.equal(out["row_loss"][rest], ref["row_loss"][rest])
         assert torch.equal(out["dlogits"][rest], ref["dlogits"][rest])
         assert torch.isfinite(ref["dlogits"].float()).all()
+
+
+@pytest.mark.parametrize("R", [33, 700, 1300])  # clusters, CTAs of 128 threads, of 64
+@pytest.mark.parametrize("base,step", [(-20000.0, 2.0 ** -8), (2.0e7, 2.0)])
+def test_certain_rows_taken_by_differences_keep_relative_precision(R, base, step):
+    """Log-probabilities next to 0 in rows so far down, or of such large
+    logits, that their statistics are taken by differences to the maximum.  The
+    terms are at least e^-70: 3 x 70 u each, and the sum's steps."""
+    V, rows = 20000, 33
+    gen = torch.Generator().manual_seed(3)
+    z = torch.round(torch.randn((rows, V), generator=gen) / step) * step
+    top = torch.randint(0, V, (rows,), generator=gen)
+    z[torch.arange(rows), top] = torch.round((torch.arange(rows).float() + 16.0) / step) * step
+    z = (z + base).repeat(-(-R // rows), 1)[:R]
+    top = top.repeat(-(-R // rows))[:R]
+    out = torch_api.token_logprobs(z.to(DEV), top.to(DEV), want_lse=True)
+    ref = oracle.token_logprobs(z[:rows].numpy(), "f32", V, top[:rows, None].numpy())
+    bound = (steps(V, 64) + 3 * 70) * U
+    rel = np.abs(out["logp"].cpu().numpy()[:rows] / ref["logp"][:, 0] - 1)
+    assert rel.max() < bound, rel.max()
+    rel = np.abs(out["entropy"].cpu().numpy()[:rows] / ref["entropy"] - 1)
+    assert rel.max() < 3 * bound, rel.max()
+    for n in ("logp", "entropy", "lse"):
+        assert torch.equal(out[n][rows:2 * rows], out[n][:rows][:max(0, R - rows)]), n
