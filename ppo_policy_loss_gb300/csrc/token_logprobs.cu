@@ -422,6 +422,55 @@ __device__ __noinline__ void search_slow(LpSmem<DT, kT>& sm, typename Fmt<DT>::K
   row_barrier<kT>();
 }
 
+// The row's statistics where an -inf has made t NaN: the warps that met one take
+// their pieces once more, from memory and with every word clamped.  The pieces,
+// lanes, order and steps are the stream's, so a warp gets the bits that it would
+// have got by clamping while the row streamed, and a row's results are the same
+// whether an earlier row had made the CTA clamp or not.  All consumer threads.
+template <int DT, int kT>
+__device__ __noinline__ RowStats clamped_row(RowStats* part, const unsigned char* src, int V, int g0, int n_mine, int n_full,
+                                             float c, int tid) {
+  using F = Fmt<DT>;
+  const int lane = tid & 31, row_vecs = (V + F::kVec - 1) / F::kVec;
+  row_barrier<kT>();
+  if (part[tid >> 5].t != part[tid >> 5].t) {
+    WarpStats st;
+    warp_stats_init<F>(st, c);
+    st.low = true;
+#pragma unroll 1
+    for (int i = 0; i * kT < n_mine; ++i) {
+      const int at = i * kT + tid;
+      const bool last = i >= n_full;
+      const int sh = last ? 0 : lane >> 1;
+      uint32_t w[16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int vec = (g0 + at) * 4 + ((j + sh) & 3);
+        const uint4 v = at < n_mine && vec < row_vecs ? *reinterpret_cast<const uint4*>(src + static_cast<long long>(vec) * 16)
+                                                      : make_uint4(0u, 0u, 0u, 0u);
+        w[4 * j] = v.x;
+        w[4 * j + 1] = v.y;
+        w[4 * j + 2] = v.z;
+        w[4 * j + 3] = v.w;
+      }
+      if (last) F::cut(w, 0, at < n_mine ? min(F::kPiece, V - (g0 + at) * F::kPiece) : 0);
+      const float pm = max_nan(F::raw_value(F::raw_max(w, 0)), F::kFloor);
+      if (last) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) w[j] = F::clamp(w[j]);
+      }
+      add_piece<F, true>(st, w, pm, c, lane, false);
+    }
+    const RowStats ws = warp_stats_sum<F>(st, c);
+    if (lane == 0) part[tid >> 5] = ws;
+  }
+  row_barrier<kT>();
+  RowStats rs = part[0];
+#pragma unroll
+  for (int w = 1; w < kT / 32; ++w) rs = merge_row(rs, part[w], c);
+  return rs;
+}
+
 // The statistics of a row that needs_exact names, by differences to its
 // maximum, -inf elements skipped.  Rare, so it reads the row again.  The maxima
 // are counted, not summed, and one of them stays out, so that r is a sum of
@@ -662,13 +711,15 @@ __global__ void __launch_bounds__(kT + 32, kLpCtas<kT>) token_logprobs_kernel(co
       RowStats rs = sm.part[0];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) rs = merge_row(rs, sm.part[w], a.c);
-      // a NaN in t is a NaN logit or a first -inf: clamp from the next row on
-      if (kEntropy) st.low = st.low || rs.t != rs.t;
       if (k) {
         const uint32_t order[2] = {tid < n_mine ? F::order_of(best[0]) : 0u,
                                    tid + kT < n_mine ? F::order_of(best[1]) : 0u};
         if (!search_fast<DT, kT>(sm, keys, src, g0, n_mine, V, k, order, F::order_of(rs.m), tid))
           search_slow<DT, kT>(sm, keys, src, g0, n_mine, V, per, k, tid);
+      }
+      if (kEntropy && rs.t != rs.t) {  // a first -inf, or NaN: clamp from now on, and this row again
+        st.low = true;
+        rs = clamped_row<DT, kT>(sm.part, src, V, g0, n_mine, n_full, a.c, tid);
       }
       if (csize > 1) {
         // every CTA's findings into rank 0's memory
@@ -702,7 +753,7 @@ __global__ void __launch_bounds__(kT + 32, kLpCtas<kT>) token_logprobs_kernel(co
         }
         if (rank != 0) continue;
       }
-      if (needs_exact<F>(rs.m, a.c) || (kEntropy && rs.t != rs.t)) rs = exact_row<F, kT>(src, V, a.c, sm.part, tid);
+      if (needs_exact<F>(rs.m, a.c)) rs = exact_row<F, kT>(src, V, a.c, sm.part, tid);
       const float log_s = log1pf(rs.r);
       if (tid < n_ids) {
         if (!y_ok) err |= RL_DEVERR_ID_RANGE;

@@ -403,18 +403,21 @@ __device__ __forceinline__ void warp_stats_init(WarpStats& a, float c) {
   a.own = 0.f;
 }
 
-// This lane's sums brought from the frame nm to the exact frame of m.
+// This lane's sums brought from the frame nm to the exact frame of m.  (Products
+// that a sum takes are rounded: two builds of a caller give the same bits.)
 __device__ __forceinline__ void end_frame(const WarpStats& a, float c, float& r, float& t) {
   const float rho = fmaf(-a.m, c, -a.nm);  // exact: the product's rounding error
   const float g = ex2_approx(rho);
   r = (a.r[0].x + a.r[0].y) + (a.r[1].x + a.r[1].y);
-  t = fmaf(rho, r, (a.t[0].x + a.t[0].y) + (a.t[1].x + a.t[1].y)) * g;
-  r *= g;
+  t = __fmul_rn(fmaf(rho, r, (a.t[0].x + a.t[0].y) + (a.t[1].x + a.t[1].y)), g);
+  r = __fmul_rn(r, g);
 }
 
 // One step: this lane's piece (raw words), of clamped maximum pm.  Warp-wide.
 // -inf words add 0 to r, but NaN to t (0 * inf): they are looked for where
 // `check` says so, and from then on the words are clamped at the floor first.
+// A set without -inf gives the same bits either way: what the clamp changes is
+// a term of 0 in the end (a row that needs_exact aside).
 template <class F, bool kEntropy>
 __device__ __forceinline__ void add_piece(WarpStats& a, uint32_t (&w)[16], float pm, float c, int lane, bool check) {
   float wm;

@@ -102,3 +102,56 @@ def test_certain_rows_taken_by_differences_keep_relative_precision(R, base, step
     assert rel.max() < 3 * bound, rel.max()
     for n in ("logp", "entropy", "lse"):
         assert torch.equal(out[n][rows:2 * rows], out[n][:rows][:max(0, R - rows)]), n
+
+
+@pytest.mark.parametrize("R,V,dtype", [
+    (4000, 60000, "bf16"),   # rows dealt out, against CTAs of a fixed share
+    (3000, 9000, "f16"),     # CTAs of 64 threads
+    (700, 30000, "f32"),
+    (74, 40000, "bf16")])    # clusters
+def test_rows_with_banned_tokens_keep_their_bits_wherever_they_stand(R, V, dtype):
+    """A row with -inf gives the same bits first or last in the batch, after
+    rows with -inf or without, in every call."""
+    gen = torch.Generator(device=DEV).manual_seed(R)
+    z = torch.empty((R, V), dtype=torch.float32, device=DEV).normal_(0.0, 2.0, generator=gen).to(TORCH[dtype])
+    some = torch.rand(R, device=DEV, generator=gen)
+    at = torch.randint(0, V, (R,), device=DEV, generator=gen)
+    one = (some < 0.2).nonzero()[:, 0]
+    z[one, at[one]] = -torch.inf
+    z[(some > 0.9).nonzero()[:, 0], V // 3:] = -torch.inf
+    z[((some > 0.5) & (some < 0.52)).nonzero()[:, 0], 1::2] = -torch.inf
+    z[(some > 0.97).nonzero()[:, 0], 7] = torch.nan
+    ids = torch.randint(0, V // 3, (R,), device=DEV, generator=gen)
+    ref = torch_api.token_logprobs(z, ids, k=5, want_lse=True)
+    bits = lambda t: t.view(torch.int32) if t.dtype == torch.float32 else t  # noqa: E731
+    for _ in range(3):
+        out = torch_api.token_logprobs(z, ids, k=5, want_lse=True)
+        for n in ref:
+            assert torch.equal(bits(out[n]), bits(ref[n])), n
+    back = torch_api.token_logprobs(z.flip(0).contiguous(), ids.flip(0).contiguous(), k=5, want_lse=True)
+    for n in ref:
+        assert torch.equal(bits(back[n].flip(0)), bits(ref[n])), n
+    cut = {4000: 800, 3000: 1500, 700: 350, 74: 74}[R]
+    for a in range(0, R, cut):
+        part = torch_api.token_logprobs(z[a:a + cut], ids[a:a + cut], k=5, want_lse=True)
+        for n in ref:
+            assert torch.equal(bits(part[n]), bits(ref[n][a:a + cut])), (n, a)
+
+
+@pytest.mark.parametrize("R", [20, 700, 1300])
+def test_certain_rows_with_banned_tokens_keep_relative_precision(R):
+    """One token far above the others, and tokens that cannot occur, in rows
+    after rows without.  Terms of at least e^-60."""
+    V, rows = 20000, 20
+    gen = torch.Generator().manual_seed(3)
+    z = torch.randn((rows, V), generator=gen)
+    top = torch.randint(0, V // 2, (rows,), generator=gen)
+    z[torch.arange(rows), top] = torch.arange(rows).float() + 16.0
+    z = z.repeat(-(-R // rows), 1)[:R]
+    top = top.repeat(-(-R // rows))[:R]
+    z[R - rows:, V - 1 - 700 * (torch.arange(rows) % 3)] = -torch.inf
+    out = torch_api.token_logprobs(z.to(DEV), top.to(DEV))
+    ref = oracle.token_logprobs(z[R - rows:].numpy(), "f32", V, top[R - rows:, None].numpy())
+    bound = (steps(V, 64) + 60) * U
+    assert np.abs(out["logp"].cpu().numpy()[R - rows:] / ref["logp"][:, 0] - 1).max() < bound
+    assert np.abs(out["entropy"].cpu().numpy()[R - rows:] / ref["entropy"] - 1).max() < 3 * bound
