@@ -3,6 +3,7 @@
 // their gradient, over logits in memory (sm_103a).
 #include <cmath>
 
+#include "dealt_rows.h"
 #include "token_rows.cuh"
 
 namespace rl {
@@ -592,16 +593,14 @@ __global__ void __launch_bounds__(kT + 32, kLpCtas<kT>) token_logprobs_kernel(co
       if (lane == 0) ask_for_cta(smem_addr(&sm.dealt), smem_addr(&sm.deal));
       ++asked;
     };
-    auto answer = [&]() {  // a.R: no more; then nothing is asked again
+    auto answer = [&]() {  // -1: no more; then nothing is asked again
       long long n = -1;
       if (lane == 0) {
         ok = wait_bounded<false>(smem_addr(&sm.deal), (asked - 1) & 1, abort) && ok;
         if (ok) n = cta_dealt(smem_addr(&sm.dealt));
       }
-      n = __shfl_sync(0xffffffffu, n, 0);
-      return n < 0 ? a.R : n;
+      return __shfl_sync(0xffffffffu, n, 0);
     };
-    // each number dealt also stands for the row of that number, if it is masked
     auto masked_row = [&](long long row) {
       if (!a.mask || row >= a.R || a.mask[row]) return;
       for (int q = lane; q < a.n_ids; q += 32) a.logp[row * a.n_ids + q] = 0.f;
@@ -612,10 +611,7 @@ __global__ void __launch_bounds__(kT + 32, kLpCtas<kT>) token_logprobs_kernel(co
       if (lane == 0 && a.entropy) a.entropy[row] = 0.f;
       if (lane == 0 && a.lse) a.lse[row] = 0.f;
     };
-    long long want = first;
-    while (ok) {
-      const long long row = rows.at(want, lane);
-      if (dealt && row >= 0) ask();
+    auto stream = [&](long long row) {  // its chunks; of row -1 the end's
       if (lane == 0) {
         const unsigned char* src = a.logits + row * a.row_bytes + b0;
         const int n = row < 0 ? 1 : n_chunks;
@@ -633,18 +629,10 @@ __global__ void __launch_bounds__(kT + 32, kLpCtas<kT>) token_logprobs_kernel(co
         }
         if (!ok) sm.ring.drain(it);
       }
-      if (dealt) masked_row(want);
-      if (row >= 0) want = dealt ? answer() : want + stride;
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (row < 0) break;
-    }
-    // no valid row is left: the CTAs not started yet have masked rows at most
-    while (dealt && ok && want < a.R) {
-      ask();
-      want = answer();
-      masked_row(want);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-    }
+      return ok;
+    };
+    take_rows(first, stride, dealt, ask, answer, [&](long long n) { return rows.at(n, lane); }, stream, masked_row);
     if (!ok && asked && lane == 0) {  // an answer on its way lands before the CTA may exit
       const uint64_t t0 = global_ns();
       while (!mbar_try_wait(smem_addr(&sm.deal), (asked - 1) & 1) && global_ns() - t0 <= kWaitLimitNs) {
