@@ -278,7 +278,9 @@ def topk_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logp: 
 class FusedTopkDistill(torch.autograd.Function):
     """Autograd wrapper: loss = FusedTopkDistill.apply(logits, teacher_ids,
     teacher_logp, mask, options), ``options`` a dict of topk_distill's keyword
-    arguments (not dlogits: every call keeps its own).
+    arguments: not dlogits, for every call keeps its own, and not stream, for the
+    backward pass runs on the stream that is current here (call it under
+    ``torch.cuda.stream`` for another one).
 
     The forward pass runs the fused kernel and keeps its gradient; the backward
     pass hands it back times the incoming gradient.  That product is skipped
@@ -291,6 +293,8 @@ class FusedTopkDistill(torch.autograd.Function):
         options = dict(options or {})
         if "dlogits" in options:
             raise ValueError("the wrapper keeps a gradient of its own: options must not name dlogits")
+        if "stream" in options:
+            raise ValueError("the backward pass runs on the current stream: options must not name stream")
         out = topk_distill(logits.detach(), teacher_ids, teacher_logp, mask=mask, **options)
         ctx.save_for_backward(out["dlogits"])
         return out["loss"]

@@ -155,3 +155,19 @@ def test_certain_rows_with_banned_tokens_keep_relative_precision(R):
     bound = (steps(V, 64) + 60) * U
     assert np.abs(out["logp"].cpu().numpy()[R - rows:] / ref["logp"][:, 0] - 1).max() < bound
     assert np.abs(out["entropy"].cpu().numpy()[R - rows:] / ref["entropy"] - 1).max() < 3 * bound
+
+
+def test_distill_wrapper_under_another_stream():
+    """Forward and backward under a busy side stream: the bits of the current
+    stream's gradient, read there after the side stream has been waited for."""
+    z = logits(64, 32000, "bf16", 12, sure=False).to(DEV).contiguous()
+    ids, lq = (t.to(DEV) for t in teacher(z.cpu(), 8, 3))
+    ref = torch_api.topk_distill(z, ids, lq)["dlogits"]
+    side = torch.cuda.Stream(DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        leaf = z.clone().requires_grad_()
+        torch.cuda._sleep(20_000_000)
+        grad = torch.autograd.grad(torch_api.FusedTopkDistill.apply(leaf, ids, lq), leaf)[0]
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(grad, ref)
