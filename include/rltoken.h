@@ -15,7 +15,9 @@
  * caller on the current device, nothing is allocated, calls are stream-ordered
  * and capturable, argument errors are found on the host before anything is
  * launched, device-detected errors set RL_DEVERR_* bits, make the affected
- * outputs NaN and never trap.
+ * outputs NaN and never trap.  A bounded wait that gives up (RL_DEVERR_TIMEOUT)
+ * may affect any row: the call's loss and every row that is not known to be
+ * right become NaN, right ones among them.
  *
  * Common arguments:
  *   logits      : [R, ld] of `dtype` (RL_F32, RL_BF16, RL_F16), row-major,

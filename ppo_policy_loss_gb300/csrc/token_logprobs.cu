@@ -4,6 +4,7 @@
 #include <cmath>
 
 #include "dealt_rows.h"
+#include "lost_rows.h"
 #include "token_rows.cuh"
 
 namespace rl {
@@ -762,7 +763,12 @@ __global__ void __launch_bounds__(kT + 32, kLpCtas<kT>) token_logprobs_kernel(co
   }
   if (csize > 1) cluster_sync_all();  // no CTA leaves while another may still write its memory
   __syncthreads();
-  if (tid == 0 && *abort && a.status) atomicOr(a.status, RL_DEVERR_TIMEOUT);
+  // a wait has given up: which rows this CTA would still have been given is not
+  // known, so every row's outputs become NaN (other CTAs may write theirs after)
+  if (*abort) {
+    if (tid == 0 && a.status) atomicOr(a.status, RL_DEVERR_TIMEOUT);
+    for (long long row = warp; row < a.R; row += kWarps + 1) lose_logprobs(a, row, lane, 32);
+  }
 }
 
 // ------------------------------------------------------------------ backward

@@ -33,6 +33,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "lost_rows.h"
 #include "token_rows.cuh"
 
 namespace rl {
@@ -653,6 +654,7 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
         o.n_rows = N;
         o.device_error = static_cast<int>(stw);
         o.reserved = 0;
+        if (stw & RL_DEVERR_TIMEOUT) lose_record(o);
         *a.stats = o;
         if (a.loss_out) *a.loss_out = static_cast<float>(o.loss);
       }
@@ -807,7 +809,18 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
       prev = row;
     }
   }
-  if (kCluster) cluster_sync_all();  // no CTA leaves while another may still write its memory
+  if (kCluster)
+    cluster_sync_all();  // no CTA leaves while another may still write its memory
+  else
+    __syncthreads();
+  // a wait has given up: every row's outputs become NaN (other CTAs may write theirs after)
+  if (*abort) {
+    for (long long row = warp; row < a.R; row += kWarps + 2) {
+      if (lane == 0 && a.row_loss) a.row_loss[row] = __int_as_float(0x7fc00000);
+      if (a.dlogits)
+        for (int v = lane; v < V; v += 32) F::store(a.dlogits + row * a.row_bytes, v, __int_as_float(0x7fc00000));
+    }
+  }
 }
 
 // ------------------------------------------------------------------ host side
