@@ -707,20 +707,22 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
       }
     };
     // pass 2: 2^((z - m) c) factor.  16-bit outputs take |factor| into the
-    // exponent (one rounding of at most 2^-15 for |m c| <= 1024, far below
-    // theirs) and the sign on the packed result; fp32 outputs multiply.
+    // exponent and the sign on the packed result: the offset b = log2|factor| -
+    // m c is rounded by at most 2^-15 for |b| <= 1024, 2.1e-5 of the result, a
+    // twelfth to a 23rd of fp16's own half step.  Beyond, and where a row is taken by
+    // differences, they multiply, as fp32 outputs do.
     const int n_full2 = n_vecs / kVecs - (n_elems % F::kVec && n_vecs % kVecs == 0 ? 1 : 0);  // chunks of full vectors only
     auto pass2 = [&](long long row) {
       unsigned char* dst = a.dlogits + row * a.row_bytes + b0;
       const float m = sm.m, factor = sm.factor;
       constexpr bool kFold = F::kBytes == 2;
-      const float nm = -m * a.c, rho = fmaf(-m, a.c, -nm);
-      const bool plain = sm.plain != 0 || (kFold && !(fabsf(nm) <= 1024.f));  // by differences to m
+      const float nm = __fmul_rn(-m, a.c), rho = fmaf(-m, a.c, -nm);
       const float add = kFold ? log2f(fabsf(factor)) : 0.f;
+      const float b = kFold ? nm + (rho + add) : nm;
+      const bool plain = sm.plain != 0 || (kFold && factor != 0.f && !(fabsf(b) <= 1024.f));  // by differences to m
       const float mul = kFold ? 1.f : plain ? factor : factor * ex2_approx(rho);
       const uint32_t sign = kFold && factor < 0.f ? 0x80008000u : 0u;
       const float2 c2 = make_float2(a.c, a.c), m2 = make_float2(mul, mul);
-      const float b = kFold ? nm + (rho + add) : nm;
       const float2 b2 = make_float2(b, b);
       auto vec = [&](const uint4& w) {
         float z[F::kVec];

@@ -171,3 +171,31 @@ def test_distill_wrapper_under_another_stream():
         grad = torch.autograd.grad(torch_api.FusedTopkDistill.apply(leaf, ids, lq), leaf)[0]
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(grad, ref)
+
+
+def half_step(x, dtype):
+    """Half a step of the 16-bit type at x (normal numbers)."""
+    e = np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -14)))
+    return 2.0 ** (e - (11 if dtype == "f16" else 8))
+
+
+def test_gradient_factor_in_the_exponent_at_its_limit():
+    """Logits near -706 and tail gradients up to 2^15: the exponent's offset passes
+    1024, where it would keep 13 bits after the point.  Beside the output's own
+    rounding, p_v's error: at most 20 u for x and its exponential, the offset's
+    rounding (2^-15 ln 2 = 363 u) and the row's sum."""
+    R, V = 1500, 504  # 13 values a row
+    gen = torch.Generator().manual_seed(5)
+    z = (-708.5 + 0.5 * torch.randint(-6, 7, (R, V), generator=gen)).half()
+    ids = teacher(z, 4, 3)[0]
+    lq = torch.log(torch.tensor([0.3, 0.25, 0.25, 0.16])).repeat(R, 1)   # q_t / p_t is small: no cancellation
+    weight = torch.rand(R, generator=gen) * 0.5 + 0.5
+    kw = dict(grad_scale=2.0 ** 21, norm=1.0)
+    out = torch_api.topk_distill(to_dev(z), ids.to(DEV), lq.to(DEV), weight=weight.to(DEV), **kw)
+    ref = oracle.topk_distill(storage(z), "f16", V, ids.numpy(), lq.numpy(), weight=weight.numpy(), **kw)
+    tail = np.ones((R, V), bool)
+    np.put_along_axis(tail, ids.numpy(), False, 1)   # the given tokens' gradients do not fit fp16
+    d, size = ref["dlogits"][tail], ref["size"][tail]
+    assert 2.0 ** 8 < np.median(np.abs(d)) and 2.0 ** 14 < np.abs(d).max() < 60000
+    tol = half_step(d, "f16") * (1 + 2.0 ** -9) + (363 + 20 + 3 * steps(V)) * U * size
+    check_close("dlogits", out["dlogits"].cpu().numpy()[tail], d, tol)
