@@ -237,7 +237,7 @@ __device__ __forceinline__ void teacher_values(const DistillArgs& a, EntryTable&
 
 struct RowSums {
   double loss, fwd, rev, qt, pt;
-  float m, factor;
+  float m, factor;  // of the tail's gradient
 };
 
 // One warp: a row's loss terms and gradient values from the teacher's side,
@@ -269,8 +269,10 @@ __device__ __forceinline__ RowSums row_values(const DistillArgs& a, const EntryT
   }
   in = warp_sum(in);                          // entries without the left-out one
   const float s_in = top_in ? 1.f + in : in;  // all entries
-  const float f_t = tail_any ? ex2_approx((tail.m - M) * a.c) : 0.f;
-  const float s_t = tail_any ? f_t * (1.f + tail.r) : 0.f;
+  // 2^((tail.m - M) c) in two halves: far below M it has no place in fp32, while
+  // its product with the sum of many tokens, or with q_t / p_t, has
+  const float half = tail_any ? ex2_approx(0.5f * ((tail.m - M) * a.c)) : 0.f;
+  const float s_t = (half * (1.f + tail.r)) * half;
   const float r = top_in ? in + s_t : tail.r + in;
   const float log_s = log1pf(r), inv_s = __frcp_rn(1.f + r);
   float pt = 0.f, lpt = 0.f;
@@ -319,9 +321,14 @@ __device__ __forceinline__ RowSums row_values(const DistillArgs& a, const EntryT
     if (v != 0.f && p[i] > 0.f) g += v * p[i] * (gap[i] - G);
     d[i] = L != L ? L : t.s * g;
   }
-  float factor = fmaxf(fminf(t.s * ct, 3.0e38f), -3.0e38f) * inv_s;
+  // The tail's gradient s ct p_v as 2^((z_v - m) c) factor, m the tail's own
+  // reference: of a tail far below M, ct holds q_t / p_t of up to 2^126, and p_v as
+  // little, and s ct would overflow.
+  const bool in_tail = tail_any && tail.r > -1.f;
+  const float m = in_tail ? tail.m : M;
+  float factor = t.s * ((in_tail ? (ct * half) * half : ct) * inv_s);
   if (L != L) factor = L;
-  return RowSums{static_cast<double>(t.w) * L, F, G, t.qt, a.renorm ? 0.f : pt, M, factor};
+  return RowSums{static_cast<double>(t.w) * L, F, G, t.qt, a.renorm ? 0.f : pt, m, factor};
 }
 
 // The consumer warps' partial statistics joined, one a lane (kWarps <= 32):

@@ -199,3 +199,32 @@ def test_gradient_factor_in_the_exponent_at_its_limit():
     assert 2.0 ** 8 < np.median(np.abs(d)) and 2.0 ** 14 < np.abs(d).max() < 60000
     tol = half_step(d, "f16") * (1 + 2.0 ** -9) + (363 + 20 + 3 * steps(V)) * U * size
     check_close("dlogits", out["dlogits"].cpu().numpy()[tail], d, tol)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("R,V", [(5, 100), (45, 70000), (3, 140000), (2200, 1000)])
+def test_tails_of_almost_no_mass_under_a_large_loss_scale(dtype, R, V):
+    """The student's tail holds e^-60 to e^-100 of its mass, the gradient is
+    scaled by 65536: s q_t / p_t passes what fp32 holds, the tail's gradients s
+    q_t p_v / max(p_t, 2^-126) do not.  Relative errors: x = (z - m) c of up to
+    160 ln 2, three roundings, two exponentials, and the row's sum."""
+    z = torch.zeros((R, V))
+    gap = torch.tensor([60.0, 85.0, 87.5, 90.0, 100.0]).repeat(-(-R // 5))[:R]
+    given = torch.arange(R) % V
+    z[torch.arange(R), given] = gap + float(np.log(V))
+    z = z + torch.randint(-2, 3, (R, V), generator=torch.Generator().manual_seed(1)) * 0.25
+    z = z.to(TORCH[dtype])
+    ids = torch.stack([given, (given + 3) % V], 1)
+    lq = torch.log(torch.tensor([[0.5, 0.2]])).repeat(R, 1)
+    kw = dict(grad_scale=65536.0, norm=1.0)
+    out = torch_api.topk_distill(to_dev(torch.nn.functional.pad(z, (0, -V % 8))[:, :V]), ids.to(DEV), lq.to(DEV), **kw)
+    ref = oracle.topk_distill(storage(z), dtype, V, ids.numpy(), lq.numpy(), **kw)
+    d, got = ref["dlogits"], oracle.decode(storage(out["dlogits"]), dtype)
+    tail = np.ones((R, V), bool)
+    np.put_along_axis(tail, ids.numpy(), False, 1)
+    assert np.abs(d[tail]).max() < 60000
+    half = {"f32": 1.0, "bf16": 2.0 ** 16, "f16": 2.0 ** 13}[dtype] * U
+    rel = half + (3 * 160 + 16 + 3 * steps(V)) * U
+    tol = rel * np.abs(d[tail]) + {"f32": 2.0 ** -126, "bf16": 2.0 ** -126, "f16": 2.0 ** -25}[dtype]
+    check_close("tail", got[tail], d[tail], tol)
+    check_close("row_loss", out["row_loss"].cpu(), ref["row_loss"], (3 * 160 + 16 + 3 * steps(V)) * U * ref["size_row"])
