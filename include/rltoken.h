@@ -91,7 +91,8 @@ rl_status rl_token_logprobs(const void* logits, rl_dtype dtype, long long R, lon
  *              [0, V) makes the row NaN and sets RL_DEVERR_ID_RANGE.
  *   entropy, dentropy : float [R] each, or both NULL (no entropy gradient).
  *   dlogits  : [R, ld] of `dtype`, written (columns >= V untouched); may be
- *              the same pointer as logits, any other overlap is RL_ERR_ALIAS.
+ *              the same pointer as logits; sharing other elements with it is
+ *              RL_ERR_ALIAS (columns beside the logits' own are none of theirs).
  * One launch.  Errors as rl_token_logprobs, and RL_ERR_NULL when neither
  * dlogp nor dentropy is given.
  */
@@ -183,8 +184,8 @@ size_t rl_topk_distill_workspace_size(void);
  * (dtype, tail), RL_ERR_SHAPE, RL_ERR_ARG (K, reverse, temperature,
  * grad_scale, norm out of range; reverse != 0 with RENORM), RL_ERR_ALIGN (as
  * above; workspace on 16, stats_dev on 8 bytes),
- * RL_ERR_ALIAS (dlogits partially overlaps logits), RL_ERR_WORKSPACE,
- * RL_ERR_CUDA.
+ * RL_ERR_ALIAS (dlogits shares elements with logits and is not logits),
+ * RL_ERR_WORKSPACE, RL_ERR_CUDA.
  */
 rl_status rl_topk_distill_fwd_bwd(const rl_topk_distill_desc* desc, void* stream);
 

@@ -1118,11 +1118,7 @@ extern "C" rl_status rl_token_logprobs_bwd(const void* logits, rl_dtype dtype, l
   const long long row_bytes = ld * es;
   if ((reinterpret_cast<uintptr_t>(logits) & 15) || (reinterpret_cast<uintptr_t>(dlogits) & 15) || (row_bytes & 15))
     return RL_ERR_ALIGN;
-  if (dlogits != logits) {
-    const uintptr_t l0 = reinterpret_cast<uintptr_t>(logits), d0 = reinterpret_cast<uintptr_t>(dlogits);
-    const uintptr_t n = static_cast<uintptr_t>(R) * static_cast<uintptr_t>(row_bytes);
-    if (l0 < d0 + n && d0 < l0 + n) return RL_ERR_ALIAS;
-  }
+  if (dlogits != logits && rows_overlap(logits, dlogits, R, row_bytes, V * es)) return RL_ERR_ALIAS;
   LpBwdArgs a;
   a.logits = static_cast<const unsigned char*>(logits);
   a.ids = ids;

@@ -708,5 +708,15 @@ inline rl_status allow_smem(const void* fn, int dev, int smem, std::atomic<unsig
   return RL_OK;
 }
 
+// Host: whether two matrices of R rows of `width` bytes, both with rows
+// `row_bytes` apart, share any of them.
+inline bool rows_overlap(const void* a, const void* b, long long R, long long row_bytes, long long width) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t d = x < y ? y - x : x - y, step = static_cast<uintptr_t>(row_bytes);
+  const uintptr_t rows = static_cast<uintptr_t>(R), w = static_cast<uintptr_t>(width);
+  // row j of the later one begins d % step past row j + d / step of the earlier one
+  return (d / step < rows && d % step < w) || (d / step + 1 < rows && step - d % step < w);
+}
+
 }  // namespace
 }  // namespace rl

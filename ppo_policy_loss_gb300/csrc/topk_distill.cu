@@ -922,11 +922,7 @@ extern "C" rl_status rl_topk_distill_fwd_bwd(const rl_topk_distill_desc* d, void
   if ((reinterpret_cast<uintptr_t>(d->logits) & 15) || (reinterpret_cast<uintptr_t>(d->dlogits) & 15) || (row_bytes & 15) ||
       (reinterpret_cast<uintptr_t>(d->workspace) & 15) || (reinterpret_cast<uintptr_t>(d->stats_dev) & 7))
     return RL_ERR_ALIGN;
-  if (d->dlogits && d->dlogits != d->logits && R > 0) {
-    const uintptr_t l0 = reinterpret_cast<uintptr_t>(d->logits), d0 = reinterpret_cast<uintptr_t>(d->dlogits);
-    const uintptr_t n = static_cast<uintptr_t>(R) * static_cast<uintptr_t>(row_bytes);
-    if (l0 < d0 + n && d0 < l0 + n) return RL_ERR_ALIAS;
-  }
+  if (d->dlogits && d->dlogits != d->logits && rows_overlap(d->logits, d->dlogits, R, row_bytes, V * es)) return RL_ERR_ALIAS;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)

@@ -228,3 +228,41 @@ def test_tails_of_almost_no_mass_under_a_large_loss_scale(dtype, R, V):
     tol = rel * np.abs(d[tail]) + {"f32": 2.0 ** -126, "bf16": 2.0 ** -126, "f16": 2.0 ** -25}[dtype]
     check_close("tail", got[tail], d[tail], tol)
     check_close("row_loss", out["row_loss"].cpu(), ref["row_loss"], (3 * 160 + 16 + 3 * steps(V)) * U * ref["size_row"])
+
+
+def test_gradients_beside_the_logits_in_one_buffer():
+    """dlogits may begin where the logits' last row ends, and may lie in the
+    columns beside them; tensors that share elements are refused."""
+    R, V, ld = 6, 992, 1000
+    buf = torch.randn(2 * R * ld, device=DEV).bfloat16()
+    z = torch.as_strided(buf, (R, V), (ld, 1), 8)
+    after = torch.as_strided(buf, (R, V), (ld, 1), R * ld)
+    before = torch.as_strided(buf, (R, V), (ld, 1), R * ld + 8)  # z0 follows it
+    ids = torch.randint(0, V, (R,), device=DEV)
+    one = torch.ones(R, device=DEV)
+    tid, tlq = (t.to(DEV) for t in teacher(z.cpu(), 4, 3))
+    wide = torch.empty((R, 2 * 1024), dtype=torch.bfloat16, device=DEV)
+    wide[:, :V] = z
+
+    def both(x, d):
+        lse = torch_api.token_logprobs(x, ids, want_lse=True)["lse"]
+        a = torch_api.token_logprobs_backward(x, ids, one, lse, dlogits=d).clone()
+        return a, torch_api.topk_distill(x, tid, tlq, dlogits=d)["dlogits"].clone()
+
+    ref = both(z, "new")
+    for x, d in ((z, after), (wide[:, :V], wide[:, 1024:1024 + V])):
+        for a, b in zip(both(x, d), ref):
+            assert torch.equal(a, b)
+    wide[:, 1024:1024 + V] = z
+    for a, b in zip(both(wide[:, 1024:1024 + V], wide[:, :V]), ref):
+        assert torch.equal(a, b)
+    lse = torch_api.token_logprobs(z, want_lse=True)["lse"]
+    for off in (0, 16, 16 + ld, 8 + 2 * ld, R * ld - 8):
+        d = torch.as_strided(buf, (R, V), (ld, 1), off)
+        with pytest.raises(rl.RlLossError):
+            torch_api.token_logprobs_backward(z, ids, one, lse, dlogits=d)
+        with pytest.raises(rl.RlLossError):
+            torch_api.topk_distill(z, tid, tlq, dlogits=d)
+    d = torch.as_strided(buf, (R, V), (ld, 1), 0)
+    with pytest.raises(rl.RlLossError):
+        torch_api.topk_distill(before, tid, tlq, dlogits=torch.as_strided(buf, (R, V), (ld, 1), R * ld))
