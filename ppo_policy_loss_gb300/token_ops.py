@@ -134,7 +134,8 @@ def token_logprobs_backward(logits: torch.Tensor, ids: torch.Tensor | None, dlog
     like ``ids``) and, with ``entropy`` and ``dentropy`` [R], the entropies that
     token_logprobs gave; ``lse`` [R] is its log-sum-exp.  ``dlogits``: "new"
     allocates it with the logits' row stride, a tensor of that stride is written
-    in place (``dlogits=logits`` overwrites the logits)."""
+    in place (``dlogits=logits`` overwrites the logits).  ids of shape [R, 0]
+    without ``dentropy`` give a gradient of zeros."""
     dt, R, V, ld = _logits(logits)
     dev = logits.device
     n = _n_ids(ids, R)
@@ -155,6 +156,8 @@ def token_logprobs_backward(logits: torch.Tensor, ids: torch.Tensor | None, dlog
     given = None if isinstance(dlogits, str) else dlogits
     with _on(dev, stream, (logits, ids, dlogp, lse, entropy, dentropy, mask, status, given)):
         dlogits = _dlogits_like(logits, dlogits, ld)
+        if ids is not None and n == 0 and entropy is None and dentropy is None:
+            return dlogits.zero_()
         _check(load().rl_token_logprobs_bwd(
             logits.data_ptr(), dt, R, V, ld, _p(ids) if n else None, n, _p(mask), temperature, _p(lse), _p(entropy),
             _p(dlogp) if n else None, _p(dentropy), _p(dlogits), status_p, _raw_stream(dev)),

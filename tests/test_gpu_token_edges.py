@@ -266,3 +266,25 @@ def test_gradients_beside_the_logits_in_one_buffer():
     d = torch.as_strided(buf, (R, V), (ld, 1), 0)
     with pytest.raises(rl.RlLossError):
         torch_api.topk_distill(before, tid, tlq, dlogits=torch.as_strided(buf, (R, V), (ld, 1), R * ld))
+
+
+def test_gradient_of_no_given_tokens():
+    """ids of shape [R, 0] have log-probabilities of shape [R, 0], whose
+    gradient is zero; the entropy's stays."""
+    z = logits(5, 512, "bf16", 33, sure=False).to(DEV).contiguous()
+    none = torch.empty((5, 0), dtype=torch.int64, device=DEV)
+    leaf = z.clone().requires_grad_()
+    logp, ent = torch_api.TokenLogprobs.apply(leaf, none)
+    assert logp.shape == (5, 0)
+    logp.sum().backward()
+    assert leaf.grad is not None and (leaf.grad == 0).all()
+    leaf.grad = None
+    logp, ent = torch_api.TokenLogprobs.apply(leaf, none)
+    (logp.sum() + ent.sum()).backward()
+    out = torch_api.token_logprobs(z, want_lse=True)
+    one = torch.ones(5, device=DEV)
+    assert torch.equal(leaf.grad, torch_api.token_logprobs_backward(z, None, None, out["lse"], out["entropy"], one))
+    got = torch_api.token_logprobs_backward(z, none, torch.empty((5, 0), device=DEV), out["lse"], dlogits=z)
+    assert got.data_ptr() == z.data_ptr() and (z == 0).all()
+    with pytest.raises(rl.RlLossError):
+        torch_api.token_logprobs_backward(z, None, None, out["lse"])
