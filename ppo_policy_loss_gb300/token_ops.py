@@ -47,6 +47,14 @@ def _raw_stream(device: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _written(*tensors):
+    """Count a kernel's writes into the caller's tensors as changes in place, so
+    that autograd refuses to use what it has kept of them."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
@@ -162,6 +170,7 @@ def token_logprobs_backward(logits: torch.Tensor, ids: torch.Tensor | None, dlog
             logits.data_ptr(), dt, R, V, ld, _p(ids) if n else None, n, _p(mask), temperature, _p(lse), _p(entropy),
             _p(dlogp) if n else None, _p(dentropy), _p(dlogits), status_p, _raw_stream(dev)),
             "rl_token_logprobs_bwd")
+        _written(given)
     return dlogits
 
 
@@ -275,6 +284,7 @@ def topk_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logp: 
             row_loss_out=_p(row_loss), loss_out=loss.data_ptr(), stats_dev=stats.data_ptr(),
             workspace=workspace.data_ptr(), workspace_bytes=workspace.numel() * workspace.element_size())
         _check(load().rl_topk_distill_fwd_bwd(d, _raw_stream(dev)), "rl_topk_distill_fwd_bwd")
+        _written(*given)
     return dict(loss=loss, row_loss=row_loss, dlogits=dlogits, stats=stats, workspace=workspace)
 
 

@@ -288,3 +288,23 @@ def test_gradient_of_no_given_tokens():
     assert got.data_ptr() == z.data_ptr() and (z == 0).all()
     with pytest.raises(rl.RlLossError):
         torch_api.token_logprobs_backward(z, None, None, out["lse"])
+
+
+def test_overwritten_logits_are_not_used_by_an_earlier_backward():
+    """A gradient written over the logits counts as a change in place: an
+    autograd graph that has kept them refuses its backward pass."""
+    z = logits(6, 512, "bf16", 33, sure=False).to(DEV).contiguous()
+    ids = torch.randint(0, 512, (6,), device=DEV)
+    tid, tlq = (t.to(DEV) for t in teacher(z.cpu(), 4, 3))
+    one = torch.ones(6, device=DEV)
+    lse = torch_api.token_logprobs(z, want_lse=True)["lse"]
+    for over in (lambda x: torch_api.topk_distill(x, tid, tlq, dlogits=x),
+                 lambda x: torch_api.token_logprobs_backward(x, ids, one, lse, dlogits=x)):
+        leaf = z.clone().requires_grad_()
+        logp, _ = torch_api.TokenLogprobs.apply(leaf, ids)
+        over(leaf.detach())
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            logp.sum().backward()
+    with torch.inference_mode():
+        x = z.clone()
+        assert torch.equal(torch_api.topk_distill(x, tid, tlq, dlogits=x)["dlogits"], torch_api.topk_distill(z, tid, tlq)["dlogits"])
