@@ -26,6 +26,9 @@
  *   V           : 1 <= V <= 2^26.
  *   mask        : uint8[R], nonzero = valid row; NULL = every row is valid.
  *                 The logits, ids and teacher of a masked row are not read.
+ *                 With a mask the forward pass and the distillation take R <=
+ *                 2^28 (the way to the next valid row stays far below the
+ *                 limit of their waits).
  *   temperature : z = logits / temperature enters every formula;
  *                 0.01 <= temperature <= 100.
  *   status_dev  : one unsigned int or NULL; RL_DEVERR_* bits are ORed into it.
@@ -69,8 +72,8 @@ extern "C" {
  * fp32 arithmetic on the exact differences to the row's maximum; the maximum
  * itself stays out of the running sum, so that a log-probability next to 0
  * keeps its relative precision.  Deterministic.  One launch.
- * Errors: RL_ERR_DTYPE, RL_ERR_SHAPE (R < 0, R >= 2^31, V or ld out of range,
- * k > V, a row too long for k > 0), RL_ERR_ARG (n_ids or k out of range,
+ * Errors: RL_ERR_DTYPE, RL_ERR_SHAPE (R < 0, R >= 2^31, R > 2^28 with a mask, V
+ * or ld out of range, k > V, a row too long for k > 0), RL_ERR_ARG (n_ids or k out of range,
  * temperature), RL_ERR_NULL, RL_ERR_ALIGN, RL_ERR_CUDA.  R = 0 launches
  * nothing.
  */

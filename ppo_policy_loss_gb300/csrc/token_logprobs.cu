@@ -1067,6 +1067,7 @@ extern "C" rl_status rl_token_logprobs(const void* logits, rl_dtype dtype, long 
   if (!shape_ok(R, V, ld)) return RL_ERR_SHAPE;
   if (n_ids < 0 || n_ids > RL_TOKEN_MAX_K || k < 0 || k > RL_TOKEN_MAX_K || !temperature_ok(temperature))
     return RL_ERR_ARG;
+  if (mask && R > kMaxMaskedRows) return RL_ERR_SHAPE;
   if (k > V || (k > 0 && V * es > static_cast<long long>(kMaxPieces) * kPieceBytes * kMaxCluster)) return RL_ERR_SHAPE;
   if (R == 0) return RL_OK;
   if (!logits || (n_ids > 0 && (!ids || !logp_out)) || (k > 0 && (!topk_ids || !topk_logp))) return RL_ERR_NULL;

@@ -24,6 +24,11 @@ namespace {
 // (j + l / 2) mod 4, which touches every bank once per 8 lanes.
 constexpr int kPieceBytes = 64;
 constexpr long long kMaxVocab = 1LL << 26;
+// Rows of a masked batch.  A warp looks through the mask at 512 rows in 0.4 us, so
+// 2^28 masked rows before a valid one take 0.2 s (the distillation, which also
+// counts them, 0.5 s) while the consumers' wait for its first chunk runs: half
+// of the wait's limit.
+constexpr long long kMaxMaskedRows = 1LL << 28;
 
 // Every logit counts as at least the format's floor where a maximum or an
 // entropy is formed, so that -inf, and the large negative numbers that masks

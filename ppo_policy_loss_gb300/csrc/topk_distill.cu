@@ -911,6 +911,7 @@ extern "C" rl_status rl_topk_distill_fwd_bwd(const rl_topk_distill_desc* d, void
   if (es == 0 || (d->tail != RL_DISTILL_TAIL_BUCKET && d->tail != RL_DISTILL_TAIL_RENORM)) return RL_ERR_DTYPE;
   const long long R = d->R, V = d->V, ld = d->ld;
   if (R < 0 || R >= (1LL << 31) || V < 1 || V > kMaxVocab || ld < V || ld > (1LL << 31)) return RL_ERR_SHAPE;
+  if (d->mask && R > kMaxMaskedRows) return RL_ERR_SHAPE;
   if (d->K < 1 || d->K > RL_TOKEN_MAX_K || !(d->reverse >= 0.f && d->reverse <= 1.f) ||
       !(d->temperature >= kMinTemperature && d->temperature <= kMaxTemperature) || !std::isfinite(d->grad_scale) ||
       !(d->norm >= 0.0) || !std::isfinite(d->norm) || (d->reverse != 0.f && d->tail == RL_DISTILL_TAIL_RENORM))
