@@ -308,3 +308,31 @@ def test_overwritten_logits_are_not_used_by_an_earlier_backward():
     with torch.inference_mode():
         x = z.clone()
         assert torch.equal(torch_api.topk_distill(x, tid, tlq, dlogits=x)["dlogits"], torch_api.topk_distill(z, tid, tlq)["dlogits"])
+
+
+@pytest.mark.parametrize("R,V,dtype,K", [
+    (1, 1, "f32", 1), (40, 60001, "bf16", 20), (70, 20000, "f32", 9), (5, 100000, "f16", 64), (2300, 1000, "bf16", 16),
+    (700, 300, "f16", 8)])
+@pytest.mark.parametrize("kw", [dict(reverse=0.5, temperature=0.8), dict(tail="renormalise")], ids=["bucket", "renormalise"])
+def test_loss_without_gradient(R, V, dtype, K, kw):
+    """dlogits=None: the same losses and record, bit for bit, as with the
+    gradient, within the oracle's bounds; row_loss=None leaves them as well."""
+    z = logits(R, V, dtype, R + V)
+    ids, lq = teacher(z, K, 3)
+    gen = torch.Generator().manual_seed(9)
+    if R > 4:
+        kw = dict(kw, mask=(torch.arange(R) % 5 != 3).to(torch.uint8), weight=torch.rand(R, generator=gen) + 0.5)
+    with_grad, _, _ = check(z, dtype, ids, lq, grad_scale=float(R) if dtype == "f16" else 1.0, **kw)
+    kw = {n: t.to(DEV) if torch.is_tensor(t) else t for n, t in kw.items()}
+    zd = to_dev(z)
+    keep = zd.clone()
+    ws = torch_api.new_distill_workspace(DEV)
+    for row in ("new", None):
+        out = torch_api.topk_distill(zd, ids.to(DEV), lq.to(DEV), dlogits=None, row_loss=row, workspace=ws, **kw)
+        assert out["dlogits"] is None and torch.equal(out["loss"], with_grad["loss"])
+        assert torch.equal(out["stats"], with_grad["stats"])
+        if row:
+            assert torch.equal(out["row_loss"], with_grad["row_loss"])
+        else:
+            assert out["row_loss"] is None
+    assert torch.equal(zd.nan_to_num(7.0), keep.nan_to_num(7.0))
