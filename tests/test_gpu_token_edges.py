@@ -336,3 +336,74 @@ def test_loss_without_gradient(R, V, dtype, K, kw):
         else:
             assert out["row_loss"] is None
     assert torch.equal(zd.nan_to_num(7.0), keep.nan_to_num(7.0))
+
+
+def reach(keys, k, threads):
+    """How many keys (unique, larger wins) reach the bound of the exact search:
+    the k-th largest of its buckets' maxima.  Key i is thread i % threads', in
+    its even or odd block; below 2 threads buckets, neighbouring lanes share one."""
+    nb = 32 if k <= 16 else 64 if k <= 32 else 128 if k <= 64 else 256
+    i = np.arange(keys.size)
+    thread, odd = i % threads, (i // threads) & 1
+    bucket = 2 * thread + odd if nb == 2 * threads else thread // (threads // nb)
+    best = np.full(nb, -1, np.int64)
+    np.maximum.at(best, bucket, keys)
+    bound = np.sort(best)[-k]
+    return int((keys >= max(bound, 0)).sum())
+
+
+def place_keys(values):
+    """Unique keys in the order of (value, lower place first)."""
+    order = np.lexsort((-np.arange(values.size), values))
+    keys = np.empty(values.size, np.int64)
+    keys[order] = np.arange(values.size)
+    return keys
+
+
+@pytest.mark.parametrize("dtype,R,V,k,threads,lanes", [
+    ("bf16", 20, 1000, 32, 128, 48), ("f16", 20, 1000, 64, 128, 40), ("f32", 20, 1000, 64, 128, 40),
+    ("bf16", 20, 4000, 128, 128, 50), ("f32", 20, 2040, 128, 128, 50),
+    ("bf16", 1300, 1000, 32, 64, 24), ("f32", 1300, 1000, 64, 64, 20), ("f16", 1300, 2000, 64, 64, 20)])
+def test_exact_search_over_elements_that_raises_its_bound(dtype, R, V, k, threads, lanes):
+    """No more pieces than alternatives, the large values on few threads: more
+    than 256 elements reach the search's first bound."""
+    assert -(-V // (16 if dtype == "f32" else 32)) <= k
+    at = torch.arange(V)
+    z = logits(8, V, dtype, V + k, sure=False)
+    z += torch.where(at % threads < lanes, 20.0, 0.0).to(z.dtype)
+    z[1] = torch.where(at % threads < lanes, 1.0, 0.0)    # all of them tied
+    z[2, V // 2:] = -torch.inf
+    for r in (0, 1, 3, 7):
+        assert reach(place_keys(z[r].double().numpy()), k, threads) > 256
+    rows = torch.arange(R) % 8
+    out = torch_api.token_logprobs(to_dev(torch.nn.functional.pad(z, (0, -V % 8))[:, :V])[rows.to(DEV)].contiguous(), k=k)
+    ref = oracle.token_logprobs(storage(z), dtype, V, None, None, k)
+    ids, lp = out["topk_ids"].cpu().numpy(), out["topk_logp"].cpu().numpy()
+    assert np.array_equal(ids, ref["topk_ids"][rows.numpy()])
+    want = ref["topk_logp"][rows.numpy()]
+    check_close("topk_logp", lp, want, (steps(V, 64) + 3 * 40) * U * (1 + np.abs(np.where(np.isfinite(want), want, 0))))
+
+
+@pytest.mark.parametrize("dtype,V,k", [("bf16", 200000, 60), ("f16", 150000, 16), ("f32", 100000, 100)])
+def test_exact_search_over_pieces_that_raises_its_bound(dtype, V, k):
+    """Long rows, one CTA each, with hundreds of tied pieces on 10 threads: the
+    lists of the fast search overflow, and so does the exact search's first."""
+    R, per = 320, 16 if dtype == "f32" else 32
+    piece = torch.arange(V) // per
+    z = logits(4, V, dtype, 77, sure=False).clamp_(-9.0, 9.0)
+    z = torch.where(piece % 128 < 10, torch.full((), 10.0, dtype=z.dtype), z)
+    z[1] = torch.where(piece % 128 < 10, 1.0, 0.0).to(z.dtype)
+    z[2] = torch.where(piece % 128 < 10, z[2] + at_random(V, z.dtype), z[2])
+    tops = torch.nn.functional.pad(z.float(), (0, -V % per), value=-99.0).view(4, -1, per).amax(2)
+    for r in (0, 1):
+        assert reach(place_keys(tops[r].double().numpy()), k, 128) > 256
+    rows = torch.arange(R) % 4
+    out = torch_api.token_logprobs(to_dev(z)[rows.to(DEV)].contiguous(), k=k)
+    ref = oracle.token_logprobs(storage(z), dtype, V, None, None, k)
+    assert np.array_equal(out["topk_ids"].cpu().numpy(), ref["topk_ids"][rows.numpy()])
+    want = ref["topk_logp"][rows.numpy()]
+    check_close("topk_logp", out["topk_logp"].cpu(), want, (steps(V) + 3 * 40) * U * (1 + np.abs(want)))
+
+
+def at_random(V, dtype):
+    return (torch.rand(V, generator=torch.Generator().manual_seed(2)) * 8.0).to(dtype)
