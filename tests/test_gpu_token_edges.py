@@ -407,3 +407,36 @@ def test_exact_search_over_pieces_that_raises_its_bound(dtype, V, k):
 
 def at_random(V, dtype):
     return (torch.rand(V, generator=torch.Generator().manual_seed(2)) * 8.0).to(dtype)
+
+
+def test_bindings_of_the_c_entry_points():
+    """The functions that forward to the C entry points, with tensors and with
+    addresses, give the bits of the torch layer."""
+    R, V, k = 7, 1000, 5
+    z = logits(R, V, "bf16", 3, sure=False).to(DEV).contiguous()
+    ids = torch.randint(0, V, (R, 2), device=DEV)
+    mask = (torch.arange(R, device=DEV) != 3).to(torch.uint8)
+    ref = torch_api.token_logprobs(z, ids, mask=mask, k=k, temperature=0.9, want_lse=True)
+    f32 = lambda *s: torch.empty(s, device=DEV)  # noqa: E731
+    logp, ent, lse, top, top_lp = f32(R, 2), f32(R), f32(R), torch.empty((R, k), dtype=torch.int64, device=DEV), f32(R, k)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    rl.rl_token_logprobs(z, "bf16", R, V, V, ids, 2, mask, 0.9, k, logp, ent, lse.data_ptr(), top, top_lp, st)
+    for n, t in dict(logp=logp, entropy=ent, lse=lse, topk_ids=top, topk_logp=top_lp).items():
+        assert torch.equal(t, ref[n]), n
+    g, h, dz = torch.randn((R, 2), device=DEV), torch.randn(R, device=DEV), torch.empty_like(z)
+    rl.rl_token_logprobs_bwd(z, rl.RL_BF16, R, V, V, ids, 2, mask, 0.9, lse, ent, g, h, dz, st, torch.cuda.current_stream())
+    assert torch.equal(dz, torch_api.token_logprobs_backward(z, ids, g, lse, ent, h, mask, 0.9))
+    tid, tlq = (t.to(DEV) for t in teacher(z.cpu(), 4, 3))
+    out = torch_api.topk_distill(z, tid, tlq, mask=mask)
+    d = rl.rl_topk_distill_desc_init()
+    ws, stats = torch_api.new_distill_workspace(DEV), torch.empty(rl.DISTILL_STATS_BYTES, dtype=torch.uint8, device=DEV)
+    d.logits, d.R, d.V, d.ld, d.K = z.data_ptr(), R, V, V, 4
+    d.teacher_ids, d.teacher_logp, d.mask = tid.data_ptr(), tlq.data_ptr(), mask.data_ptr()
+    d.dlogits, d.stats_dev, d.workspace, d.workspace_bytes = dz.data_ptr(), stats.data_ptr(), ws.data_ptr(), ws.numel()
+    rl.rl_topk_distill_fwd_bwd(d)
+    assert torch.equal(dz, out["dlogits"]) and torch.equal(stats, out["stats"])
+    assert rl.distill_stats_from_bytes(stats.cpu().numpy().tobytes())["n_rows"] == R - 1 and int(st.item()) == 0
+    for call in (lambda: rl.rl_token_logprobs(z, "bf16", R, V, V, None, 1, None, 1.0, 0, None, ent, None, None, None),
+                 lambda: rl.rl_token_logprobs_bwd(z, "bf16", R, V, V, None, 0, None, 1.0, lse, None, None, None, dz)):
+        with pytest.raises(rl.RlLossError):
+            call()
