@@ -818,13 +818,13 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
       prev = row;
     }
   }
-  if (kCluster)
-    cluster_sync_all();  // no CTA leaves while another may still write its memory
-  else
-    __syncthreads();
-  // a wait has given up: every row's outputs become NaN (other CTAs may write theirs after)
+  if (kCluster) cluster_sync_all();  // no CTA leaves while another may still write its memory
+  // A wait has given up: every row's outputs become NaN.  Each warp writes all of
+  // them once it is done: whatever a warp wrote from then on it sees `abort` after,
+  // and what other warps and CTAs write later is right.  (A barrier before it cost
+  // the 32-thread build 8%: registers.)
   if (*abort) {
-    for (long long row = warp; row < a.R; row += kWarps + 2) {
+    for (long long row = 0; row < a.R; ++row) {
       if (lane == 0 && a.row_loss) a.row_loss[row] = __int_as_float(0x7fc00000);
       if (a.dlogits)
         for (int v = lane; v < V; v += 32) F::store(a.dlogits + row * a.row_bytes, v, __int_as_float(0x7fc00000));
