@@ -191,12 +191,13 @@ using ElemKey = unsigned long long;
 
 constexpr int kMaxCluster = 8;
 constexpr int kSlots = 4;
-// CTAs a SM holds, registers permitting, for kT threads (shared memory may allow
-// fewer).  4096 x 151,936 bf16: six CTAs of three slots take 208 and 254 us at
-// k = 0 and 64, five of four 214 and 265; at 8192 rows and k = 64 four slots are
-// 1% faster than three, and at few rows 5%.
+// CTAs a SM holds, for kT threads: what their registers have to allow.  Shared
+// memory lets in five of 128 threads without alternatives; with them four (151,936
+// 16-bit or 50,257 fp32 logits) down to two (151,936 fp32).  Against a bound of
+// six, which takes them to 64 registers and spills: 4096 x 151,936 bf16, us, k = 0
+// and 64: 209.5, 217.7 and 256.7, 258.7; 8192 rows at k = 64: 479, 477.
 template <int kT>
-constexpr int kLpCtas = kT == 128 ? 6 : 8;
+constexpr int kLpCtas = kT == 128 ? 5 : 8;
 constexpr int kSmemPerSm = 228 * 1024;
 
 template <int DT, int kT>
