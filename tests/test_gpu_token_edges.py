@@ -440,3 +440,55 @@ def test_bindings_of_the_c_entry_points():
                  lambda: rl.rl_token_logprobs_bwd(z, "bf16", R, V, V, None, 0, None, 1.0, lse, None, None, None, dz)):
         with pytest.raises(rl.RlLossError):
             call()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_longest_rows(dtype):
+    """Rows of 2^26 - 3 logits, in clusters: log-probabilities, entropy, their
+    gradient, and the distillation, against fp64 sums.  An element's term is
+    added in one of 8 x 512 chains (8 x 128 x 4), 2^14 roundings, and a given
+    token's log-probability carries the sum's error."""
+    V, R, K = 2 ** 26 - 3, 2, 6
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    full = torch.empty((R, 2 ** 26), dtype=torch.float32, device=DEV).normal_(0.0, 2.0, generator=gen).to(TORCH[dtype])
+    z = full[:, :V]
+    ids = torch.tensor([[0, V - 1, 12345678], [V - 1, 1, 40000000]], device=DEV)
+    out = torch_api.token_logprobs(z, ids, want_lse=True)
+    x = z.double()
+    m = x.amax(1, keepdim=True)
+    lse = m[:, 0] + (x - m).exp_().sum(1).log()
+    lp = x.sub_(lse[:, None])
+    p = lp.exp()
+    H = -(p * lp).sum(1)
+    bound = (2 ** 14 + 64 + 3 * 40) * U
+    check_close("lse", out["lse"].cpu(), lse.cpu(), bound + 2 * U * np.abs(lse.cpu().numpy()))
+    check_close("logp", out["logp"].cpu(), lp.gather(1, ids).cpu(), bound + 4 * U * 40)
+    check_close("entropy", out["entropy"].cpu(), H.cpu(), 3 * bound * (1 + H.cpu().numpy()))
+    g, h = torch.randn((R, 3), device=DEV, generator=gen), torch.randn(R, device=DEV, generator=gen)
+    got = torch_api.token_logprobs_backward(z, ids, g, out["lse"], out["entropy"], h)
+    off = (out["lse"].double() - lse)[:, None]            # the gradient is formed with the rounded lse and entropy
+    want = -(p * torch.exp(-off)) * (g.double().sum(1, keepdim=True) + h.double()[:, None] * (lp - off + out["entropy"].double()[:, None]))
+    size = (p * (g.abs().double().sum(1, keepdim=True) + h.abs().double()[:, None] * (lp.abs() + 40))).scatter_add_(1, ids, g.abs().double())
+    want.scatter_add_(1, ids, g.double())
+    half = 2.0 ** -8 if dtype == "bf16" else U
+    err = (got.double() - want).abs()
+    assert bool((err <= half * want.abs() * 1.001 + (4 * 40 + 144) * U * size + 2.0 ** -126).all())
+    del got, want, size, err
+    tid = torch.tensor([[5, V - 1, 77, 1 << 20, 1 << 25, -1], [0, 31, 32, 33, V - 2, V - 1]], device=DEV)
+    tlq = torch.log_softmax(torch.randn((R, K + 1), device=DEV, generator=gen), 1)[:, :K].contiguous()
+    q = torch.where(tid >= 0, tlq.double().exp(), 0.0)
+    at = tid.clamp(min=0)
+    pt = 1.0 - torch.where(tid >= 0, p.gather(1, at), 0.0).sum(1)
+    qt = 1.0 - q.sum(1)
+    F = torch.where(tid >= 0, q * (tlq.double() - lp.gather(1, at)), 0.0).sum(1) + qt * (qt.log() - pt.log())
+    d = torch_api.topk_distill(z, tid, tlq, norm=1.0)
+    check_close("row_loss", d["row_loss"].cpu(), F.cpu(), 3 * bound * (1 + 40))
+    slope = (1.0 - qt / pt)[:, None]
+    want = p * slope
+    for r in range(R):
+        for j in range(K):
+            if tid[r, j] >= 0:
+                want[r, tid[r, j]] = p[r, tid[r, j]] - q[r, j]
+    size = (p * (1.0 + qt / pt)[:, None]).scatter_add_(1, at, q)
+    err = (d["dlogits"].double() - want).abs_()
+    assert bool((err <= half * want.abs() * 1.001 + 3 * bound * size + 2.0 ** -126).all())
