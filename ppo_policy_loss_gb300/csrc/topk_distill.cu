@@ -152,27 +152,38 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // e^y for y <= 88 as the sum of two floats (in fp64), relative error below
-// 2^-26: y - n ln 2 is exact (the head of ln 2 has 16 bits), and of 1 + f +
-// f^2 / 2 + ... only the terms from f^2 on are rounded to fp32.  A fraction of
-// the fp64 exponential's time on a GPU with few fp64 units.
+// 2^-34, and 2^-35.5 from y = -20 on: 1 - sum q keeps 2^-12 of a tail of 2^-24, and
+// 20 bits from 2^-15 on.  Cody and Waite's reduction: y - n ln 2 is exact (the head
+// of ln 2 has 16 bits).  Then Horner's scheme for the Taylor series, its last five
+// steps on an unevaluated sum h + l (Dekker's product and sum: p + e = f h exactly,
+// s + rounding = c + p exactly).  A fraction of the fp64 exponential's time on a
+// GPU with few fp64 units.
+__device__ __forceinline__ void horner_pair(float c, float c_low, float f, float& h, float& l) {
+  const float p = __fmul_rn(f, h), e = fmaf(f, l, fmaf(f, h, -p));
+  h = c + p;
+  l = (p - (h - c)) + (e + c_low);
+}
 __device__ __forceinline__ double exp_sum(float y) {
   constexpr float kLn2Head = 45426.0f / 65536.0f;
   constexpr float kLn2Rest = static_cast<float>(0.69314718055994530942 - 45426.0 / 65536.0);
   if (!(y > -87.f)) return y != y ? static_cast<double>(y) : 0.0;  // (2^-126 and less)
   const float n = fminf(rintf(y * kLog2e), 128.f);
   const float f = fmaf(n, -kLn2Head, y);
-  float p = 1.f / 40320.f;
-  p = fmaf(p, f, 1.f / 5040.f);
-  p = fmaf(p, f, 1.f / 720.f);
-  p = fmaf(p, f, 1.f / 120.f);
-  p = fmaf(p, f, 1.f / 24.f);
-  p = fmaf(p, f, 1.f / 6.f);
-  p = fmaf(p, f, 0.5f);
-  p *= f * f;  // e^f - 1 - f
-  const float g = -n * kLn2Rest;  // e^(f + g) = e^f (1 + g + g^2 / 2 ...), |g| < 2e-4
-  const float hi = 1.f + f, lo = (f - (hi - 1.f)) + fmaf(g * (hi + p), fmaf(0.5f, g, 1.f), p);
+  float h = 1.f / 362880.f, l = 0.f;
+  h = fmaf(h, f, 1.f / 40320.f);
+  h = fmaf(h, f, 1.f / 5040.f);
+  h = fmaf(h, f, 1.f / 720.f);
+  h = fmaf(h, f, 1.f / 120.f);
+  constexpr float k24 = static_cast<float>(1.0 / 24.0), k6 = static_cast<float>(1.0 / 6.0);
+  horner_pair(k24, static_cast<float>(1.0 / 24.0 - k24), f, h, l);
+  horner_pair(k6, static_cast<float>(1.0 / 6.0 - k6), f, h, l);
+  horner_pair(0.5f, 0.f, f, h, l);
+  horner_pair(1.f, 0.f, f, h, l);
+  horner_pair(1.f, 0.f, f, h, l);
+  const float g = -n * kLn2Rest;  // e^(f + g) = e^f (1 + g + g^2 / 2 ...), |g| < 1e-3
+  l = fmaf(h, g * fmaf(0.5f, g, 1.f), l);
   const float scale = __int_as_float((static_cast<int>(n) + 127) << 23);
-  return static_cast<double>(hi * scale) + static_cast<double>(lo * scale);
+  return static_cast<double>(h * scale) + static_cast<double>(l * scale);
 }
 
 // The teacher's side of a row into its table, by one warp, from the entries'

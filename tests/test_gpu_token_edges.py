@@ -157,6 +157,32 @@ def test_certain_rows_with_banned_tokens_keep_relative_precision(R):
     assert np.abs(out["entropy"].cpu().numpy()[R - rows:] / ref["entropy"] - 1).max() < 3 * bound
 
 
+@pytest.mark.parametrize("R,V,K", [(60, 1000, 2), (60, 1000, 5), (48, 70000, 64), (3, 140000, 128), (2200, 700, 33)])
+def test_teacher_whose_tail_is_the_rest_of_a_sum_next_to_one(R, V, K):
+    """Given probabilities of ordinary size that leave a tail of 2^-22 to 2^-12,
+    under a student who gives the tail half: ln q_t, in the reverse divergence
+    and its gradient, has the relative error of 1 - sum q.  Each q is formed to
+    2^-34 of itself and the sum in fp64, so that error is 2^-34 / q_t."""
+    g = np.random.default_rng(R + K)
+    tail = 2.0 ** -(12.0 + np.arange(R) % 11)
+    q = g.dirichlet(np.full(K, 2.0), R) * (1.0 - tail[:, None])
+    lq = torch.from_numpy(np.log(q).astype(np.float32))
+    ids = torch.from_numpy(np.stack([g.permutation(V)[:K] for _ in range(R)]))
+    z = torch.from_numpy(g.normal(0, 1, (R, V)).astype(np.float32))
+    z.scatter_add_(1, ids, torch.full((R, K), float(np.log(V / K))))
+    qt = 1.0 - np.exp(lq.double().numpy()).sum(1)
+    assert 2.0 ** -24 < qt.min() and qt.max() < 2.0 ** -11
+    zd = torch.nn.functional.pad(z, (0, -V % 4)).to(DEV)[:, :V]
+    for reverse in (1.0, 0.5):
+        out = torch_api.topk_distill(zd, ids.to(DEV), lq.to(DEV), reverse=reverse, norm=1.0)
+        ref = oracle.topk_distill(z.numpy(), "f32", V, ids.numpy(), lq.numpy(), reverse=reverse, norm=1.0)
+        n = 3 * (steps(V) + 64) * U
+        check_close("row_loss", out["row_loss"].cpu(), ref["row_loss"], 2.0 ** -34 / qt + n * ref["size_row"])
+        lp = np.abs(ref["lp"])
+        check_close("dlogits", out["dlogits"].cpu(), ref["dlogits"],
+                    2 * 2.0 ** -34 / qt[:, None] * np.exp(-lp) + (n + 4 * lp * U) * ref["size"])
+
+
 def test_distill_wrapper_under_another_stream():
     """Forward and backward under a busy side stream: the bits of the current
     stream's gradient, read there after the side stream has been waited for."""
