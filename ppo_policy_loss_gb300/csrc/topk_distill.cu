@@ -25,7 +25,7 @@
 //     statistics and given logits, and every one of them forms the same values.
 //
 // What bounds it: a row read once and written once, 734 us at 8192 x 151,936
-// bf16; measured 820 us (6.1 TB/s).  The two passes take about the same time,
+// bf16; measured 812 us (6.1 TB/s).  The two passes take about the same time,
 // and the consumers wait for data in an eighth of it: the rest is their own
 // instructions, two exponentials an element.  Chunks of the next row's first
 // pass run before a row's second (kLead), so that the row warp's serial part
@@ -420,6 +420,16 @@ __device__ __forceinline__ long long count_rows(const DistillArgs& a, long long 
   long long N = 0;
   for (int w = 0; w < kWarps - 2; ++w) N += wcount[w];
   return N;
+}
+
+// One warp: NaN to every row's loss and gradient.
+template <class F>
+__device__ __noinline__ void lose_rows(float* row_loss, unsigned char* dlogits, long long R, long long row_bytes, int V, int lane) {
+  for (long long row = 0; row < R; ++row) {
+    if (lane == 0 && row_loss) row_loss[row] = __int_as_float(0x7fc00000);
+    if (dlogits)
+      for (int v = lane; v < V; v += 32) F::store(dlogits + row * row_bytes, v, __int_as_float(0x7fc00000));
+  }
 }
 
 // kThreads consumers, the producer warp and the row warp.  kCluster: the CTAs
@@ -835,11 +845,7 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
   // and what other warps and CTAs write later is right.  (A barrier before it cost
   // the 32-thread build 8%: registers.)
   if (*abort) {
-    for (long long row = 0; row < a.R; ++row) {
-      if (lane == 0 && a.row_loss) a.row_loss[row] = __int_as_float(0x7fc00000);
-      if (a.dlogits)
-        for (int v = lane; v < V; v += 32) F::store(a.dlogits + row * a.row_bytes, v, __int_as_float(0x7fc00000));
-    }
+    lose_rows<F>(a.row_loss, a.dlogits, a.R, a.row_bytes, V, lane);
   }
 }
 
