@@ -35,7 +35,8 @@
  * A logit of -inf is a token that cannot occur (probability 0, log-probability
  * -inf, nothing in the entropy).  A valid row whose logits are all -inf has no
  * distribution: its log-probabilities and entropy are NaN.  NaN or +inf in a
- * valid row makes that row's results NaN.
+ * valid row makes that row's results NaN.  A log-probability below fp32's range
+ * is -inf, a probability below 2^-126 counts as 0.
  */
 #ifndef RLTOKEN_H
 #define RLTOKEN_H
@@ -71,7 +72,10 @@ extern "C" {
  *   most 4 MB (2^21 16-bit or 2^20 fp32 logits).
  * fp32 arithmetic on the exact differences to the row's maximum; the maximum
  * itself stays out of the running sum, so that a log-probability next to 0
- * keeps its relative precision.  Deterministic.  One launch.
+ * keeps its relative precision.  A row's sum is rounded at most V / 256 + 64
+ * times (V / 64 + 64 where the row's maximum is at or below -16384, fp16 -32768,
+ * or above 2^24 temperature ln 2).  Deterministic: a row's results depend on its
+ * logits and on the launch's shape, not on other rows.  One launch.
  * Errors: RL_ERR_DTYPE, RL_ERR_SHAPE (R < 0, R >= 2^31, R > 2^28 with a mask, V
  * or ld out of range, k > V, a row too long for k > 0), RL_ERR_ARG (n_ids or k out of range,
  * temperature), RL_ERR_NULL, RL_ERR_ALIGN, RL_ERR_CUDA.  R = 0 launches
@@ -88,7 +92,9 @@ rl_status rl_token_logprobs(const void* logits, rl_dtype dtype, long long R, lon
  *   dlogits_v = (1 / temperature) [ sum_j dlogp_j ([v = ids_j] - p_v)
  *                                   - dentropy p_v (z_v - lse + entropy) ]
  * rounded once to `dtype`; masked rows get an all-zero row.
- *   lse      : float [R], as rl_token_logprobs wrote it.
+ *   lse      : float [R], as rl_token_logprobs wrote it.  Its rounding is a
+ *              relative error of up to |lse| 2^-24 in every p_v, which counts
+ *              for logits of many thousands, and for those alone.
  *   dlogp    : float [R, n_ids]; NULL iff n_ids = 0.  An id that a row names
  *              several times collects the sum of its gradients; an id outside
  *              [0, V) makes the row NaN and sets RL_DEVERR_ID_RANGE.

@@ -540,7 +540,7 @@ __device__ __noinline__ RowStats exact_row(const unsigned char* row, int V, floa
 // What bounds it: with the entropy, the instructions around the exponentials
 // (an element's unpacking, two packed FMAs and a packed add a pair): the issue
 // slots are 65-70% busy and the rest is their latency.  4096 x 151,936 bf16:
-// 204 us (6.1 TB/s), without the entropy 184 us (6.8 TB/s).  The search waits on
+// 205 us (6.1 TB/s), without the entropy 184 us (6.8 TB/s).  The search waits on
 // barriers and on L2: 16 alternatives add 35 us there, 64 add 50 us, and 16 add
 // 50 us to 210 us at 16,384 x 32,000; many small CTAs cover that for one
 // another.  One warp that searched a row behind the consumers took 234 us there,
