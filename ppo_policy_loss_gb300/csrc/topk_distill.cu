@@ -841,12 +841,10 @@ __global__ void __launch_bounds__(kThreads + 64, kCtas) topk_distill_kernel(cons
   }
   if (kCluster) cluster_sync_all();  // no CTA leaves while another may still write its memory
   // A wait has given up: every row's outputs become NaN.  Each warp writes all of
-  // them once it is done: whatever a warp wrote from then on it sees `abort` after,
-  // and what other warps and CTAs write later is right.  (A barrier before it cost
-  // the 32-thread build 8%: registers.)
-  if (*abort) {
-    lose_rows<F>(a.row_loss, a.dlogits, a.R, a.row_bytes, V, lane);
-  }
+  // them once it is done, for a warp that wrote wrong values finds `abort` set, and
+  // what other warps and CTAs write later is right.  (A barrier before it cost the
+  // 32-thread build 8%: registers.)
+  if (*abort) lose_rows<F>(a.row_loss, a.dlogits, a.R, a.row_bytes, V, lane);
 }
 
 // ------------------------------------------------------------------ host side
