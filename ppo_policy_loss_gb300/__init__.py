@@ -1,8 +1,8 @@
 """Python binding of librlloss, the GB300-native fused RL policy-loss library.
 
 Argument marshalling only: every function forwards to the C entry point of
-the same name declared in include/rlloss.h or include/rltoken.h, with the same arguments in the
-same order.  Array arguments may be torch CUDA tensors (their data_ptr() is
+the same name declared in include/rlloss.h, include/rltoken.h or include/rlrollout.h, with the same
+arguments in the same order.  Array arguments may be torch CUDA tensors (their data_ptr() is
 passed), plain integer device addresses, or None for NULL.  ``stream`` may be
 a torch.cuda.Stream, an integer cudaStream_t, or None for torch's current
 stream.  A status other than RL_OK raises RlLossError.
@@ -27,6 +27,8 @@ AGGREGATIONS = {"token_mean": 0, "seq_mean_token_mean": 1, "seq_mean_token_sum":
                 "token_sum_norm": 3}
 RL_DEVERR_ID_RANGE, RL_DEVERR_TIMEOUT, RL_DEVERR_ID_REPEAT = 1, 2, 4
 RL_TOKEN_MAX_K = 128
+RL_INT8_MAX_D = 131071
+RL_VERIFY_MAX_DRAFT = 128
 RL_DISTILL_TAIL_BUCKET, RL_DISTILL_TAIL_RENORM = 0, 1
 DISTILL_TAILS = {"bucket": 0, "renormalise": 1}
 
@@ -42,6 +44,8 @@ __all__ = [
     "rl_token_logprobs", "rl_token_logprobs_bwd", "rl_topk_distill_fwd_bwd",
     "rl_topk_distill_desc", "rl_topk_distill_desc_init", "rl_topk_distill_workspace_size",
     "rl_distill_stats", "distill_stats_from_bytes",
+    "rl_quantize_rows_int8", "rl_lmhead_logits_int8", "rl_lmhead_int8_workspace_size", "rl_verify_drafts",
+    "rl_verify_drafts_desc", "rl_verify_drafts_desc_init",
     "rl_status_string", "rl_loss_stats", "RlLossError", "build", "load", "stats_from_bytes",
 ]
 
@@ -102,6 +106,16 @@ class rl_topk_distill_desc(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class rl_verify_drafts_desc(ctypes.Structure):
+    _fields_ = [("target_logits", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("B", ctypes.c_longlong), ("G", ctypes.c_longlong), ("V", ctypes.c_longlong),
+                ("ld", ctypes.c_longlong), ("draft_logits", ctypes.c_void_p), ("ld_draft", ctypes.c_longlong),
+                ("draft_lse", ctypes.c_void_p), ("draft_ids", ctypes.c_void_p), ("n_draft", ctypes.c_void_p),
+                ("uniforms", ctypes.c_void_p), ("temperature", ctypes.c_double), ("tokens", ctypes.c_void_p),
+                ("n_accepted", ctypes.c_void_p), ("logp_out", ctypes.c_void_p), ("lse_out", ctypes.c_void_p),
+                ("status_dev", ctypes.c_void_p)]
+
+
 STATS_BYTES = ctypes.sizeof(rl_loss_stats)
 DISTILL_STATS_BYTES = ctypes.sizeof(rl_distill_stats)
 VALUE_STATS_BYTES = ctypes.sizeof(rl_value_stats)
@@ -153,7 +167,15 @@ def load(path: str | None = None):
     lib.rl_topk_distill_workspace_size.argtypes = []
     lib.rl_topk_distill_workspace_size.restype = SZ
     lib.rl_topk_distill_fwd_bwd.argtypes = [ctypes.POINTER(rl_topk_distill_desc), P]
-    for fn in ("rl_token_logprobs", "rl_token_logprobs_bwd", "rl_topk_distill_fwd_bwd"):
+    lib.rl_quantize_rows_int8.argtypes = [P, I, LL, LL, LL, P, LL, P, P]
+    lib.rl_lmhead_logits_int8.argtypes = [P, LL, P, P, LL, P, LL, LL, LL, I, P, LL, P, P, SZ, P]
+    lib.rl_lmhead_int8_workspace_size.argtypes = [LL, LL]
+    lib.rl_lmhead_int8_workspace_size.restype = SZ
+    lib.rl_verify_drafts_desc_init.argtypes = [ctypes.POINTER(rl_verify_drafts_desc)]
+    lib.rl_verify_drafts_desc_init.restype = None
+    lib.rl_verify_drafts.argtypes = [ctypes.POINTER(rl_verify_drafts_desc), P]
+    for fn in ("rl_token_logprobs", "rl_token_logprobs_bwd", "rl_topk_distill_fwd_bwd", "rl_quantize_rows_int8",
+               "rl_lmhead_logits_int8", "rl_verify_drafts"):
         getattr(lib, fn).restype = I
     for fn in ("rl_lmhead_row_partials", "rl_lmhead_dlogits", "rl_lmhead_dhidden",
                "rl_lmhead_dweight"):
@@ -363,6 +385,36 @@ def rl_topk_distill_workspace_size() -> int:
 
 def rl_topk_distill_fwd_bwd(desc: rl_topk_distill_desc, stream=None):
     _check(load().rl_topk_distill_fwd_bwd(ctypes.byref(desc), _stream(stream)), "rl_topk_distill_fwd_bwd")
+
+
+def rl_quantize_rows_int8(x, dtype, R, D, ld_x, codes, ld_c, scale, stream=None):
+    _check(load().rl_quantize_rows_int8(_ptr(x), _dtype(dtype), R, D, ld_x, _ptr(codes), ld_c, _ptr(scale),
+                                        _stream(stream)), "rl_quantize_rows_int8")
+
+
+def rl_lmhead_int8_workspace_size(R, D) -> int:
+    return int(load().rl_lmhead_int8_workspace_size(R, D))
+
+
+def rl_lmhead_logits_int8(hidden, ld_h, scale_h, weight, ld_w, scale_w, R, D, V, dtype, logits, ld,
+                          status_dev=None, workspace=None, workspace_bytes=0, stream=None):
+    if workspace is not None and hasattr(workspace, "numel") and not workspace_bytes:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(load().rl_lmhead_logits_int8(_ptr(hidden), ld_h, _ptr(scale_h), _ptr(weight), ld_w, _ptr(scale_w),
+                                        R, D, V, _dtype(dtype), _ptr(logits), ld, _ptr(status_dev),
+                                        _ptr(workspace), workspace_bytes, _stream(stream)),
+           "rl_lmhead_logits_int8")
+
+
+def rl_verify_drafts_desc_init() -> rl_verify_drafts_desc:
+    """A descriptor holding the library's defaults (see rl_verify_drafts_desc_init)."""
+    d = rl_verify_drafts_desc()
+    load().rl_verify_drafts_desc_init(ctypes.byref(d))
+    return d
+
+
+def rl_verify_drafts(desc: rl_verify_drafts_desc, stream=None):
+    _check(load().rl_verify_drafts(ctypes.byref(desc), _stream(stream)), "rl_verify_drafts")
 
 
 def distill_stats_from_bytes(raw: bytes) -> dict:

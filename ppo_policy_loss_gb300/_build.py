@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "librlloss.so")
 SOURCES = ["policy_loss.cu", "advantages.cu", "critic.cu", "status.cu", "lmhead.cu", "lmhead_grad.cu",
-           "token_logprobs.cu", "topk_distill.cu"]
+           "token_logprobs.cu", "topk_distill.cu", "quantize_rows.cu", "int8_logits.cu", "verify_drafts.cu"]
 # (object, source, extra flags): policy_loss.cu builds a second time with the
 # short-row configuration of the loss kernel.
 UNITS = [(src.replace(".cu", ".o"), src, []) for src in SOURCES] + [

@@ -59,15 +59,15 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _logits(logits: torch.Tensor):
+def _logits(logits: torch.Tensor, name: str = "logits"):
     """(dtype code, rows, columns, row stride) of a [R, V] matrix of logits."""
     dt = _DT.get(logits.dtype)
     if dt is None or logits.dim() != 2 or not logits.is_cuda:
-        raise ValueError("logits must be a 2-D float32, bfloat16 or float16 CUDA tensor")
+        raise ValueError(f"{name} must be a 2-D float32, bfloat16 or float16 CUDA tensor")
     R, V = logits.shape
     ld = logits.stride(0) if R > 1 else max(V, logits.stride(0))
     if V > 1 and logits.stride(1) != 1:
-        raise ValueError("logits must have unit column stride")
+        raise ValueError(f"{name} must have unit column stride")
     return dt, R, V, ld
 
 

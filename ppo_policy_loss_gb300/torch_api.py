@@ -262,3 +262,6 @@ def lmhead_logprobs(hidden: torch.Tensor, weight: torch.Tensor, ids: torch.Tenso
 # they live in a module of their own.
 from .token_ops import (FusedTopkDistill, TokenLogprobs, new_distill_workspace,  # noqa: E402,F401
                         read_distill_stats, token_logprobs, token_logprobs_backward, topk_distill)
+# So are the rollout's operators.
+from .rollout_ops import (lmhead_logits_int8, new_int8_workspace, quantize_rows, sample_tokens,  # noqa: E402,F401
+                          verify_drafts)
