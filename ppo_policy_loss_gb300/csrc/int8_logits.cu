@@ -1,20 +1,155 @@
 // int8_logits.cu — rl_lmhead_logits_int8: the logits of an 8-bit LM head
-// (include/rlrollout.h).
+// (include/rlrollout.h) on the 5th-generation tensor cores (sm_103a).
 //
-// Simple form: a CTA takes 64 tokens x 64 channels, 64 columns at a time in
-// shared memory, and sums products of four codes at a time in 32-bit integers.
+// The tensor cores take 8-bit integers at a fraction of their 16-bit rate
+// here, and fp16 holds every code exactly, every product of two codes has 15 bits,
+// and a sum of 1024 such products is at most 2^24: fp32 accumulation is exact over
+// 1024 columns.  So the codes are widened to fp16 on their way to the tensor
+// cores, and sums over more columns are taken 1024 at a time and added in
+// 32-bit integers.  HBM sees 8-bit weights only.
+//
+//   logits^T tile [128 channels x N tokens] = W[128 x D] . hidden[N x D]^T
+//
+//   * widen_kernel writes the tokens' codes as fp16 into the workspace (R D
+//     elements, 1 to 2 us beside a product that reads V D bytes).
+//   * warp 0 (one lane): TMA producer of two rings: 8-bit weight tiles (128
+//     channels x 128 columns, 16 KB) and fp16 token tiles (N x 64 columns).
+//     Where all columns of a single token tile fit (small batches), they are loaded once and stay.
+//   * warps 4-7: one channel a thread.  A 128-byte row of codes from shared memory, widened
+//     in registers (4 codes: one XOR, two byte permutes to 1024 + code + 128,
+//     two fp16 subtractions), and stored to tensor memory: the A operand of
+//     tcgen05.mma comes from there, so that widened weights cost no
+//     shared-memory traffic, which the token tiles already keep busy.
+//   * warp 1 (one lane): tcgen05.mma.kind::f16, M = 128, K = 16, into one of two
+//     accumulators of N columns.
+//   * warps 8-11: epilogue, a channel a lane: scales, rounding, and stores of
+//     32 neighbouring channels of a token at a time.
+//   * N is a multiple of 16 up to 192 (2 accumulators of 192 columns and two A tiles
+//     of 64 fill the 512 columns of tensor memory); 128 where sums stay in the epilogue's registers (D > 1024).
+//   * Every mbarrier wait is bounded; on timeout the kernel raises an error
+//     flag, waits for its own copies and tensor-core work, writes NaN for what it has
+//     not finished, frees its tensor memory and exits.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "rlrollout.h"
+#include "tc_device.cuh"
 
 namespace rl {
 namespace {
 
-constexpr int kT = 64;       // tokens and channels of a tile, bytes of a step
+constexpr int kM = 128;                   // channels of a tile
+constexpr int kStepK = 128;               // columns of a weight tile
+constexpr int kBlockK = 64;               // columns of a token tile (fp16: 128 bytes)
+constexpr int kExactK = 1024;             // columns that fp32 sums exactly
+constexpr int kChunkSteps = kExactK / kStepK;
+constexpr int kMaxN = 192, kMaxNDeep = 128;
+constexpr uint32_t kTileA = kM * kStepK;  // 16 KB
+constexpr int kThreadsI = 384;
+constexpr uint32_t kTmemAll = 512, kTmemA = 2 * kMaxN;  // columns: two accumulators, then two A tiles of 64
+constexpr int kMaxA = 12, kMaxB = 96;     // ring slots
+constexpr uint32_t kRingBytes = 224 * 1024;
+constexpr int kWidenThreads = 256;
+
+struct Bars {
+  unsigned long long full_a[kMaxA], empty_a[kMaxA];
+  unsigned long long full_b[kMaxB], empty_b[kMaxB];
+  unsigned long long wide_full[2], wide_empty[2];
+  unsigned long long acc_full[2], acc_empty[2];
+  unsigned long long drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+static_assert(kRingBytes + 1024 + sizeof(Bars) <= 232448, "rings and barriers fit the 227 KB a CTA may use");
+
+struct IArgs {
+  long long R, V, ld;
+  int n_tt, n_vt, group;  // token tiles, channel tiles, token tiles of a unit group
+  int N;                  // tokens of a tile
+  int steps, blocks;      // weight and token tiles along D
+  int slots_a, slots_b;
+  int resident;           // the token tile's blocks are loaded once
+  uint32_t idesc;
+  const float* scale_h;
+  const float* scale_w;
+  void* out;
+  unsigned int* status;
+};
+
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 16 consecutive columns of this thread's TMEM lane; wait_ld() before they are used.
+__device__ __forceinline__ void tmem_ld16_issue(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// 32 consecutive columns of this thread's TMEM lane, written.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Four 8-bit codes as fp16 numbers, exactly: 0x6400 | u is 1024 + u.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;  // code + 128
+  const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1024 + 128
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off), y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// The tokens' codes as fp16, rows ld_f elements apart: 16 codes a thread.
+__global__ void __launch_bounds__(kWidenThreads)
+widen_kernel(const signed char* __restrict__ h, long long ld_h, long long R, long long D, unsigned char* __restrict__ f,
+             long long ld_f) {
+  allow_dependents();
+  const long long per_row = (D + 15) / 16;
+  const long long i = static_cast<long long>(blockIdx.x) * kWidenThreads + threadIdx.x;
+  if (i >= R * per_row) return;
+  const long long r = i / per_row, c = (i - r * per_row) * 16;
+  // (the stride is a multiple of 16: the columns behind D are the caller's, and multiplied by nothing)
+  uint32_t w[4], o[8];
+  if (c + 16 <= D) {
+    const uint4 v = *reinterpret_cast<const uint4*>(h + r * ld_h + c);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[j] = 0u;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (c + 4 * j + q < D) w[j] |= (static_cast<uint32_t>(h[r * ld_h + c + 4 * j + q]) & 0xffu) << (8 * q);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) widen4(w[j], o[2 * j], o[2 * j + 1]);
+  uint4* p = reinterpret_cast<uint4*>(f + (r * ld_f + c) * 2);
+  p[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
 
 template <class T>
 __device__ __forceinline__ T rounded(float v);
@@ -25,58 +160,339 @@ __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { retur
 template <>
 __device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
 
-template <class T>
-__global__ void __launch_bounds__(256)
-logits_int8_kernel(const signed char* __restrict__ h, long long ld_h, const float* __restrict__ sh,
-                   const signed char* __restrict__ w, long long ld_w, const float* __restrict__ sw, long long R,
-                   long long D, long long V, T* __restrict__ out, long long ld) {
-  __shared__ int a[kT][kT / 4 + 1], b[kT][kT / 4 + 1];
-  const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
-  const long long v0 = static_cast<long long>(blockIdx.x) * kT, r0 = static_cast<long long>(blockIdx.y) * kT;
-  int acc[4][4] = {};
-  for (long long k = 0; k < D; k += kT) {
-    for (int i = t; i < kT * kT / 4; i += 256) {
-      const int row = i / (kT / 4), col = i % (kT / 4);
-      int x = 0, y = 0;
-      for (int j = 0; j < 4; ++j) {
-        const long long d = k + col * 4 + j;
-        if (d < D && r0 + row < R) x |= (h[(r0 + row) * ld_h + d] & 0xff) << (8 * j);
-        if (d < D && v0 + row < V) y |= (w[(v0 + row) * ld_w + d] & 0xff) << (8 * j);
+template <class T, bool kDeep>
+__global__ void __launch_bounds__(kThreadsI, 1)
+logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h, const IArgs a) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ Bars sm;
+  const uint32_t ring_a = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t ring_b = ring_a + a.slots_a * kTileA, tile_b = static_cast<uint32_t>(a.N) * 128u;
+  volatile int* abort_flag = &sm.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n_units = a.n_tt * a.n_vt;
+
+  if (tid == 0) {
+    for (int s = 0; s < a.slots_a; ++s) {
+      mbar_init(smem_addr(&sm.full_a[s]), 1);
+      mbar_init(smem_addr(&sm.empty_a[s]), 4);
+    }
+    for (int s = 0; s < a.slots_b; ++s) {
+      mbar_init(smem_addr(&sm.full_b[s]), 1);
+      mbar_init(smem_addr(&sm.empty_b[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_addr(&sm.wide_full[s]), 4);
+      mbar_init(smem_addr(&sm.wide_empty[s]), 1);
+      mbar_init(smem_addr(&sm.acc_full[s]), 1);
+      mbar_init(smem_addr(&sm.acc_empty[s]), 4);
+    }
+    mbar_init(smem_addr(&sm.drain), 1);
+    sm.abort = 0;
+    fence_mbar_init();
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_h)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_w)) : "memory");
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(&sm.tmem_base), kTmemAll);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      uint32_t ia = 0, ib = 0;
+      bool stop = false, waited = false;
+      for (int u = blockIdx.x; u < n_units && !stop; u += gridDim.x) {
+        int tt, vt;
+        unit_tile(u, a.n_tt, a.n_vt, a.group, tt, vt);
+        for (int k = 0; k < a.steps && !stop; ++k) {
+          const uint32_t s = ia % a.slots_a, round = ia / a.slots_a;
+          if (round > 0 && !tc_wait<false>(smem_addr(&sm.empty_a[s]), (round - 1) & 1, abort_flag)) {
+            stop = true;
+            break;
+          }
+          const uint32_t fa = smem_addr(&sm.full_a[s]);
+          mbar_arrive_expect_tx(fa, kTileA);
+          tma_load_2d(ring_a + s * kTileA, &map_w, k * kStepK, vt * kM, fa);
+          ++ia;
+          if (a.resident && u != blockIdx.x) continue;
+          for (int j = 2 * k; j < min(2 * k + 2, a.blocks); ++j, ++ib) {
+            const uint32_t t = ib % a.slots_b, turn = ib / a.slots_b;
+            if (turn > 0 && !tc_wait<false>(smem_addr(&sm.empty_b[t]), (turn - 1) & 1, abort_flag)) {
+              stop = true;
+              break;
+            }
+            if (!waited) {  // the workspace is written by the launch before this one
+              grid_dependency_wait();
+              waited = true;
+            }
+            const uint32_t fb = smem_addr(&sm.full_b[t]);
+            mbar_arrive_expect_tx(fb, tile_b);
+            tma_load_2d(ring_b + t * tile_b, &map_h, j * kBlockK, tt * a.N, fb);
+          }
+        }
       }
-      a[row][col] = x;
-      b[row][col] = y;
+      if (stop) {  // copies already issued land before the CTA can exit
+        for (uint32_t k = ia > a.slots_a ? ia - a.slots_a : 0; k < ia; ++k)
+          tc_wait<true>(smem_addr(&sm.full_a[k % a.slots_a]), (k / a.slots_a) & 1, abort_flag);
+        for (uint32_t k = ib > a.slots_b ? ib - a.slots_b : 0; k < ib; ++k)
+          tc_wait<true>(smem_addr(&sm.full_b[k % a.slots_b]), (k / a.slots_b) & 1, abort_flag);
+      }
     }
-    __syncthreads();
-    for (int c = 0; c < kT / 4; ++c)
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(a[ty * 4 + i][c], b[tx + 16 * j][c], acc[i][j]);
-    __syncthreads();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      uint32_t iw = 0, ib = 0, acc = 0;
+      bool stop = false, issued = false;
+      for (int u = blockIdx.x; u < n_units && !stop; u += gridDim.x) {
+        for (int k = 0; k < a.steps && !stop; ++k, ++iw) {
+          const uint32_t buf = acc & 1, use = acc >> 1;
+          const uint32_t d_tmem = tmem + buf * kMaxN;
+          const bool first = k % kChunkSteps == 0;
+          if (first) {
+            if (use > 0 && !tc_wait<false>(smem_addr(&sm.acc_empty[buf]), (use - 1) & 1, abort_flag)) {
+              stop = true;
+              break;
+            }
+          }
+          const uint32_t wb = iw & 1;
+          if (!tc_wait<false>(smem_addr(&sm.wide_full[wb]), (iw >> 1) & 1, abort_flag)) {
+            stop = true;
+            break;
+          }
+          const uint32_t a_tmem = tmem + kTmemA + wb * (kStepK / 2);
+          for (int j = 0; j < 2 && 2 * k + j < a.blocks; ++j) {
+            const uint32_t t = a.resident ? 2 * k + j : ib % a.slots_b;
+            if (!tc_wait<false>(smem_addr(&sm.full_b[t]), a.resident ? 0 : (ib / a.slots_b) & 1, abort_flag)) {
+              stop = true;
+              break;
+            }
+            ++ib;
+            tc_fence_after();
+            const uint32_t b_base = ring_b + t * tile_b;
+#pragma unroll
+            for (int q = 0; q < kBlockK / 16; ++q)
+              umma_f16_ts(d_tmem, a_tmem + j * (kBlockK / 2) + q * 8, smem_desc_sw128(b_base + q * 32), a.idesc,
+                          !(first && j == 0 && q == 0));
+            issued = true;
+            if (!a.resident) umma_commit(smem_addr(&sm.empty_b[t]));
+          }
+          if (stop) break;
+          umma_commit(smem_addr(&sm.wide_empty[wb]));
+          if (k % kChunkSteps == kChunkSteps - 1 || k == a.steps - 1) {
+            umma_commit(smem_addr(&sm.acc_full[buf]));
+            ++acc;
+          }
+        }
+      }
+      if (stop && issued) {  // every MMA already issued completes before the memory is freed
+        umma_commit(smem_addr(&sm.drain));
+        tc_wait<true>(smem_addr(&sm.drain), 0, abort_flag);
+      }
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ---------------------------------------------------------------- widening
+    const int q = warp & 3, row = q * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
+    uint32_t it = 0;
+    bool stop = false;
+    for (int u = blockIdx.x; u < n_units && !stop; u += gridDim.x) {
+      for (int k = 0; k < a.steps; ++k, ++it) {
+        const uint32_t s = it % a.slots_a, wb = it & 1;
+        // warp-uniform outcome: the tensor-memory stores below are warp-collective
+        bool ok = tc_wait<false>(smem_addr(&sm.full_a[s]), (it / a.slots_a) & 1, abort_flag);
+        if (it >= 2) ok = ok && tc_wait<false>(smem_addr(&sm.wide_empty[wb]), ((it >> 1) - 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) {
+          stop = true;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t base = ring_a + s * kTileA + row * 128;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t o[32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4 v = ld_shared_v4(base + (((half * 4 + c) ^ (row & 7)) << 4));
+            widen4(v.x, o[8 * c], o[8 * c + 1]);
+            widen4(v.y, o[8 * c + 2], o[8 * c + 3]);
+            widen4(v.z, o[8 * c + 4], o[8 * c + 5]);
+            widen4(v.w, o[8 * c + 6], o[8 * c + 7]);
+          }
+          tmem_st32(tmem + kTmemA + wb * (kStepK / 2) + half * 32 + lane_addr, o);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_addr(&sm.empty_a[s]));
+          mbar_arrive(smem_addr(&sm.wide_full[wb]));
+        }
+      }
+    }
+  } else if (warp >= 8) {
+    // ---------------------------------------------------------------- epilogue
+    const int q = warp & 3, row = q * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
+    uint32_t acc = 0;
+    bool stop = false;
+    const int n_chunks = (a.steps + kChunkSteps - 1) / kChunkSteps;
+    for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
+      int tt, vt;
+      unit_tile(u, a.n_tt, a.n_vt, a.group, tt, vt);
+      const long long v = static_cast<long long>(vt) * kM + row, r0 = static_cast<long long>(tt) * a.N;
+      const int n = static_cast<int>(min(static_cast<long long>(a.N), a.R - r0));
+      const bool here = v < a.V;
+      const float sw = here ? a.scale_w[v] : 0.f;
+      T* out = static_cast<T*>(a.out) + r0 * a.ld + v;
+      int sum[kDeep ? kMaxNDeep : 1];
+      for (int ch = 0; ch < n_chunks; ++ch, ++acc) {
+        const uint32_t buf = acc & 1, use = acc >> 1;
+        stop = stop || !__all_sync(0xffffffffu, tc_wait<false>(smem_addr(&sm.acc_full[buf]), use & 1, abort_flag));
+        if (stop) break;
+        tc_fence_after();
+        const uint32_t from = tmem + lane_addr + buf * kMaxN;
+        if (kDeep) {
+#pragma unroll
+          for (int c = 0; c < kMaxNDeep / 16; ++c) {
+            if (c * 16 < a.N) {
+              uint32_t x[16];
+              tmem_ld16_issue(from + c * 16, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                sum[c * 16 + i] = __float2int_rn(__uint_as_float(x[i])) + (ch > 0 ? sum[c * 16 + i] : 0);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < a.N; c += 16) {
+            uint32_t x[16];
+            tmem_ld16_issue(from + c, x);
+            float sh[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sh[i] = c + i < n ? __ldg(a.scale_h + r0 + c + i) : 0.f;
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (here && c + i < n)
+                out[(c + i) * a.ld] = rounded<T>(__fmul_rn(__fmul_rn(__uint_as_float(x[i]), sh[i]), sw));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.acc_empty[buf]));
+      }
+      if (stop) {  // not known to be right
+        for (int t = 0; t < n; ++t)
+          if (here) out[t * a.ld] = rounded<T>(__int_as_float(0x7fc00000));
+      } else if (kDeep) {
+#pragma unroll
+        for (int i = 0; i < kMaxNDeep; ++i)
+          if (here && i < n)
+            out[i * a.ld] = rounded<T>(__fmul_rn(__fmul_rn(static_cast<float>(sum[i]), __ldg(a.scale_h + r0 + i)), sw));
+      }
+    }
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const long long r = r0 + ty * 4 + i, v = v0 + tx + 16 * j;
-      if (r < R && v < V)
-        out[r * ld + v] = rounded<T>(__fmul_rn(__fmul_rn(static_cast<float>(acc[i][j]), sh[r]), sw[v]));
-    }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag && tid == 0 && a.status) atomicOr(a.status, RL_DEVERR_TIMEOUT);
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemAll);
+  }
 }
 
-template <class T>
-void launch(const signed char* h, long long ld_h, const float* sh, const signed char* w, long long ld_w, const float* sw,
-            long long R, long long D, long long V, void* out, long long ld, cudaStream_t s) {
-  for (long long r = 0; r < R; r += 65535LL * kT) {
-    const long long n = R - r < 65535LL * kT ? R - r : 65535LL * kT;
-    const dim3 grid(static_cast<unsigned>((V + kT - 1) / kT), static_cast<unsigned>((n + kT - 1) / kT));
-    logits_int8_kernel<T><<<grid, 256, 0, s>>>(h + r * ld_h, ld_h, sh + r, w, ld_w, sw, n, D, V,
-                                               static_cast<T*>(out) + r * ld, ld);
-  }
-}
-
+// ------------------------------------------------------------------ host side
 bool shape_ok(long long R, long long D) { return R >= 0 && R < (1LL << 31) && D >= 1 && D <= RL_INT8_MAX_D; }
+
+// Row stride of the widened codes, in elements.
+long long wide_ld(long long D) { return (D + kBlockK - 1) / kBlockK * kBlockK; }
 
 // Whether [x, x + nx) and [y, y + ny) share a byte.
 bool overlap(const void* x, long long nx, const void* y, long long ny) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
   return a < b + static_cast<uintptr_t>(ny) && b < a + static_cast<uintptr_t>(nx);
+}
+
+// Token tiles that the CTAs working at one time may touch: about 40 MB of L2.
+constexpr long long kTokenL2Bytes = 40LL << 20;
+
+struct IPlan {
+  int n_tt, n_vt, group, N, steps, blocks, slots_a, slots_b, resident;
+};
+
+IPlan int8_plan(long long R, long long D, long long V) {
+  IPlan p;
+  const int most = D > kExactK ? kMaxNDeep : kMaxN;
+  p.n_tt = static_cast<int>((R + most - 1) / most);
+  const long long each = (R + p.n_tt - 1) / p.n_tt;
+  p.N = static_cast<int>((each + 15) / 16 * 16);
+  p.n_tt = static_cast<int>((R + p.N - 1) / p.N);
+  p.n_vt = static_cast<int>((V + kM - 1) / kM);
+  p.steps = static_cast<int>((D + kStepK - 1) / kStepK);
+  p.blocks = static_cast<int>((D + kBlockK - 1) / kBlockK);
+  const long long tile_b = static_cast<long long>(p.N) * 128, budget = kRingBytes;
+  // weights in flight are what a small batch waits for: at least 80 KB of them beside resident tokens
+  p.resident = p.n_tt == 1 && p.blocks <= kMaxB && p.blocks * tile_b + 5 * static_cast<long long>(kTileA) <= budget;
+  if (p.resident) {
+    p.slots_b = p.blocks;
+    const long long room = (budget - p.blocks * tile_b) / kTileA;
+    p.slots_a = static_cast<int>(room < kMaxA ? room : kMaxA);
+  } else {
+    p.slots_a = 6;
+    const long long room = (budget - 6 * static_cast<long long>(kTileA)) / tile_b;
+    p.slots_b = static_cast<int>(room < kMaxB ? room : kMaxB);
+  }
+  const long long g = kTokenL2Bytes / (static_cast<long long>(p.N) * wide_ld(D) * 2);
+  p.group = static_cast<int>(g < 1 ? 1 : (g > p.n_tt ? p.n_tt : g));
+  return p;
+}
+
+// 2-D tensor map of bytes over [rows, cols], box 128 x 128, 128-byte swizzle, zeros outside.
+bool byte_map(EncodeTiled enc, CUtensorMap* map, const void* base, long long rows, long long cols, long long ld) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+  const cuuint32_t box[2] = {kStepK, kM};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The kernel's dynamic shared memory allowed, once per device (a bit each).
+template <class T, bool kDeep>
+rl_status launch(const CUtensorMap& map_w, const CUtensorMap& map_h, const IArgs& a, int grid, int dev, cudaStream_t s) {
+  constexpr int smem = kRingBytes + 1024;
+  static std::atomic<unsigned long long> allowed{0};
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(allowed.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(logits_int8_kernel<T, kDeep>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return RL_ERR_CUDA;
+    allowed.fetch_or(bit, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreadsI);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the weight's first tiles load while the codes are widened
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, logits_int8_kernel<T, kDeep>, map_w, map_h, a) == cudaSuccess ? RL_OK : RL_ERR_CUDA;
+}
+
+template <class T>
+rl_status launch_any(const CUtensorMap& map_w, const CUtensorMap& map_h, const IArgs& a, int grid, int dev, cudaStream_t s) {
+  return a.steps > kChunkSteps ? launch<T, true>(map_w, map_h, a, grid, dev, s) : launch<T, false>(map_w, map_h, a, grid, dev, s);
 }
 
 }  // namespace
@@ -85,7 +501,7 @@ bool overlap(const void* x, long long nx, const void* y, long long ny) {
 extern "C" size_t rl_lmhead_int8_workspace_size(long long R, long long D) {
   using namespace rl;
   if (!shape_ok(R, D)) return 0;
-  return (static_cast<size_t>(R) * static_cast<size_t>((D + 127) / 128 * 128) * 2 + 255) & ~size_t(255);
+  return (static_cast<size_t>(R) * static_cast<size_t>(wide_ld(D)) * 2 + 255) & ~size_t(255);
 }
 
 extern "C" rl_status rl_lmhead_logits_int8(const signed char* hidden, long long ld_h, const float* scale_h,
@@ -110,13 +526,42 @@ extern "C" rl_status rl_lmhead_logits_int8(const signed char* hidden, long long 
   if (overlap(logits, out_bytes, hidden, (R - 1) * ld_h + D) || overlap(logits, out_bytes, weight, (V - 1) * ld_w + D))
     return RL_ERR_ALIAS;
   if (!workspace || workspace_bytes < rl_lmhead_int8_workspace_size(R, D)) return RL_ERR_WORKSPACE;
-  (void)status_dev;
+  EncodeTiled enc = nullptr;
+  int dev = 0, sms = 0;
+  if (tc_encode_fn(&enc) != RL_OK || cudaGetDevice(&dev) != cudaSuccess || tc_device_sms(&sms) != RL_OK) return RL_ERR_CUDA;
+  const IPlan p = int8_plan(R, D, V);
+  const long long ldw = wide_ld(D);
+  CUtensorMap map_w, map_h;
+  if (!byte_map(enc, &map_w, weight, V, D, ld_w) ||
+      !tc_make_map(enc, &map_h, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, workspace, R, D, ldw, kBlockK, p.N))
+    return RL_ERR_CUDA;
+  IArgs a;
+  a.R = R;
+  a.V = V;
+  a.ld = ld;
+  a.n_tt = p.n_tt;
+  a.n_vt = p.n_vt;
+  a.group = p.group;
+  a.N = p.N;
+  a.steps = p.steps;
+  a.blocks = p.blocks;
+  a.slots_a = p.slots_a;
+  a.slots_b = p.slots_b;
+  a.resident = p.resident;
+  a.idesc = make_idesc_f16(false, kM, p.N, false, false);
+  a.scale_h = scale_h;
+  a.scale_w = scale_w;
+  a.out = logits;
+  a.status = status_dev;
+  const long long units = static_cast<long long>(p.n_tt) * p.n_vt;
+  if (units > (1LL << 30)) return RL_ERR_SHAPE;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == RL_F32)
-    launch<float>(hidden, ld_h, scale_h, weight, ld_w, scale_w, R, D, V, logits, ld, s);
-  else if (dtype == RL_BF16)
-    launch<__nv_bfloat16>(hidden, ld_h, scale_h, weight, ld_w, scale_w, R, D, V, logits, ld, s);
-  else
-    launch<__half>(hidden, ld_h, scale_h, weight, ld_w, scale_w, R, D, V, logits, ld, s);
-  return cudaGetLastError() == cudaSuccess ? RL_OK : RL_ERR_CUDA;
+  const long long pieces = R * ((D + 15) / 16);
+  widen_kernel<<<static_cast<unsigned>((pieces + kWidenThreads - 1) / kWidenThreads), kWidenThreads, 0, s>>>(
+      hidden, ld_h, R, D, static_cast<unsigned char*>(workspace), ldw);
+  if (cudaGetLastError() != cudaSuccess) return RL_ERR_CUDA;
+  const int grid = static_cast<int>(units < sms ? units : sms);
+  if (dtype == RL_F32) return launch_any<float>(map_w, map_h, a, grid, dev, s);
+  if (dtype == RL_BF16) return launch_any<__nv_bfloat16>(map_w, map_h, a, grid, dev, s);
+  return launch_any<__half>(map_w, map_h, a, grid, dev, s);
 }
