@@ -12,7 +12,7 @@
 //
 //   * widen_kernel writes the tokens' codes as fp16 into the workspace (R D
 //     elements, 1 to 2 us beside a product that reads V D bytes).
-//   * warp 0 (one lane): TMA producer of two rings: 8-bit weight tiles (128
+//   * warps 0 and 2 (one lane each): TMA producers of two rings: 8-bit weight tiles (128
 //     channels x 128 columns, 16 KB) and fp16 token tiles (N x 64 columns).
 //     Where all columns of a single token tile fit (small batches), they are loaded once and stay.
 //   * warps 4-7: one channel a thread.  A 128-byte row of codes from shared memory, widened
@@ -20,11 +20,11 @@
 //     two fp16 subtractions), and stored to tensor memory: the A operand of
 //     tcgen05.mma comes from there, so that widened weights cost no
 //     shared-memory traffic, which the token tiles already keep busy.
-//   * warp 1 (one lane): tcgen05.mma.kind::f16, M = 128, K = 16, into one of two
+//   * warp 1: tcgen05.mma.kind::f16, M = 128, K = 16, into one of two
 //     accumulators of N columns.
 //   * warps 8-11: epilogue, a channel a lane: scales, rounding, and stores of
 //     32 neighbouring channels of a token at a time.
-//   * N is a multiple of 16 up to 192 (2 accumulators of 192 columns and two A tiles
+//   * N is a multiple of 16 up to 192 (2 accumulators of 192 columns and two widened tiles
 //     of 64 fill the 512 columns of tensor memory); 128 where sums stay in the epilogue's registers (D > 1024).
 //   * Every mbarrier wait is bounded; on timeout the kernel raises an error
 //     flag, waits for its own copies and tensor-core work, writes NaN for what it has
@@ -51,15 +51,16 @@ constexpr int kChunkSteps = kExactK / kStepK;
 constexpr int kMaxN = 192, kMaxNDeep = 128;
 constexpr uint32_t kTileA = kM * kStepK;  // 16 KB
 constexpr int kThreadsI = 384;
-constexpr uint32_t kTmemAll = 512, kTmemA = 2 * kMaxN;  // columns: two accumulators, then two A tiles of 64
-constexpr int kMaxA = 12, kMaxB = 96;     // ring slots
+constexpr uint32_t kTmemAll = 512;        // columns: two accumulators of N, then widened tiles of 64
+constexpr int kWideCols = kStepK / 2;
+constexpr int kMaxA = 12, kMaxB = 96, kMaxWide = 4;  // ring slots, widened tiles
 constexpr uint32_t kRingBytes = 224 * 1024;
 constexpr int kWidenThreads = 256;
 
 struct Bars {
   unsigned long long full_a[kMaxA], empty_a[kMaxA];
   unsigned long long full_b[kMaxB], empty_b[kMaxB];
-  unsigned long long wide_full[2], wide_empty[2];
+  unsigned long long wide_full[kMaxWide], wide_empty[kMaxWide];
   unsigned long long acc_full[2], acc_empty[2];
   unsigned long long drain;
   uint32_t tmem_base;
@@ -73,7 +74,7 @@ struct IArgs {
   int n_tt, n_vt, group;  // token tiles, channel tiles, token tiles of a unit group
   int N;                  // tokens of a tile
   int steps, blocks;      // weight and token tiles along D
-  int slots_a, slots_b;
+  int slots_a, slots_b, slots_w;
   int resident;           // the token tile's blocks are loaded once
   uint32_t idesc;
   const float* scale_h;
@@ -82,12 +83,40 @@ struct IArgs {
   unsigned int* status;
 };
 
+// A place in a ring of n slots, and the parity of its present round.  (Counted, not
+// divided: a division by n is a hundred cycles of the one lane that feeds the tensor cores.)
+struct Place {
+  uint32_t i = 0, parity = 0;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++i == n) {
+      i = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+// A whole warp's wait; the outcome is warp-uniform.  (Every lane looks: a lane that
+// waits by itself, with the others held at the next warp-wide instruction or at the end of
+// its role, makes the scheduler change between the two: a tile took 5.4 us, not 3.4.)
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, tc_wait<false>(bar, parity, abort));
+}
+
+// One lane of the warp issues.  (The whole warp runs the loop around it, so that the
+// compiler sees warp-uniform operands: from a single lane's registers each operand takes a
+// move to the uniform ones, and an instruction 110 cycles instead of 46.)
 __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_elect(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
 // 16 consecutive columns of this thread's TMEM lane; wait_ld() before they are used.
@@ -160,6 +189,8 @@ __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { retur
 template <>
 __device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
 
+// (Loops stay rolled: an unrolled role is a kilobyte of instructions that each call fetches
+// from HBM, 1200 cycles a line, for the weights before it have swept them out of L2.)
 template <class T, bool kDeep>
 __global__ void __launch_bounds__(kThreadsI, 1)
 logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h, const IArgs a) {
@@ -168,7 +199,7 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
   const uint32_t ring_a = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t ring_b = ring_a + a.slots_a * kTileA, tile_b = static_cast<uint32_t>(a.N) * 128u;
   volatile int* abort_flag = &sm.abort;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int n_units = a.n_tt * a.n_vt;
 
   if (tid == 0) {
@@ -180,9 +211,11 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
       mbar_init(smem_addr(&sm.full_b[s]), 1);
       mbar_init(smem_addr(&sm.empty_b[s]), 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < a.slots_w; ++s) {
       mbar_init(smem_addr(&sm.wide_full[s]), 4);
       mbar_init(smem_addr(&sm.wide_empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(smem_addr(&sm.acc_full[s]), 1);
       mbar_init(smem_addr(&sm.acc_empty[s]), 4);
     }
@@ -199,119 +232,137 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem_base, 0), wide = tmem + 2 * a.N;
 
   if (warp == 0) {
-    // ---------------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      uint32_t ia = 0, ib = 0;
-      bool stop = false, waited = false;
-      for (int u = blockIdx.x; u < n_units && !stop; u += gridDim.x) {
-        int tt, vt;
-        unit_tile(u, a.n_tt, a.n_vt, a.group, tt, vt);
-        for (int k = 0; k < a.steps && !stop; ++k) {
-          const uint32_t s = ia % a.slots_a, round = ia / a.slots_a;
-          if (round > 0 && !tc_wait<false>(smem_addr(&sm.empty_a[s]), (round - 1) & 1, abort_flag)) {
-            stop = true;
-            break;
-          }
-          const uint32_t fa = smem_addr(&sm.full_a[s]);
-          mbar_arrive_expect_tx(fa, kTileA);
-          tma_load_2d(ring_a + s * kTileA, &map_w, k * kStepK, vt * kM, fa);
-          ++ia;
-          if (a.resident && u != blockIdx.x) continue;
-          for (int j = 2 * k; j < min(2 * k + 2, a.blocks); ++j, ++ib) {
-            const uint32_t t = ib % a.slots_b, turn = ib / a.slots_b;
-            if (turn > 0 && !tc_wait<false>(smem_addr(&sm.empty_b[t]), (turn - 1) & 1, abort_flag)) {
-              stop = true;
-              break;
-            }
-            if (!waited) {  // the workspace is written by the launch before this one
-              grid_dependency_wait();
-              waited = true;
-            }
-            const uint32_t fb = smem_addr(&sm.full_b[t]);
-            mbar_arrive_expect_tx(fb, tile_b);
-            tma_load_2d(ring_b + t * tile_b, &map_h, j * kBlockK, tt * a.N, fb);
-          }
+    // ---------------------------------------------------------------- TMA producer: weight tiles (whole warp)
+    Place pa;
+    uint32_t issued = 0;
+    bool stop = false;
+#pragma unroll 1
+    for (int u = blockIdx.x; u < n_units && !stop; u += gridDim.x) {
+      int tt, vt;
+      unit_tile(u, a.n_tt, a.n_vt, a.group, tt, vt);
+#pragma unroll 1
+      for (int k = 0; k < a.steps; ++k, ++issued) {
+        // (a barrier that has completed no phase passes a wait for the one before its first)
+        if (!warp_wait(smem_addr(&sm.empty_a[pa.i]), pa.parity ^ 1, abort_flag)) {
+          stop = true;
+          break;
         }
-      }
-      if (stop) {  // copies already issued land before the CTA can exit
-        for (uint32_t k = ia > a.slots_a ? ia - a.slots_a : 0; k < ia; ++k)
-          tc_wait<true>(smem_addr(&sm.full_a[k % a.slots_a]), (k / a.slots_a) & 1, abort_flag);
-        for (uint32_t k = ib > a.slots_b ? ib - a.slots_b : 0; k < ib; ++k)
-          tc_wait<true>(smem_addr(&sm.full_b[k % a.slots_b]), (k / a.slots_b) & 1, abort_flag);
+        if (lane == 0) {
+          const uint32_t fa = smem_addr(&sm.full_a[pa.i]);
+          mbar_arrive_expect_tx(fa, kTileA);
+          tma_load_2d(ring_a + pa.i * kTileA, &map_w, k * kStepK, vt * kM, fa);
+        }
+        __syncwarp();
+        pa.next(a.slots_a);
       }
     }
+    if (stop)  // copies already issued land before the CTA can exit
+      for (uint32_t k = issued > a.slots_a ? issued - a.slots_a : 0; k < issued; ++k)
+        tc_wait<true>(smem_addr(&sm.full_a[k % a.slots_a]), (k / a.slots_a) & 1, abort_flag);
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- TMA producer: token tiles (whole warp)
+    Place pb;
+    uint32_t issued = 0;
+    bool stop = false;
+    grid_dependency_wait();  // the workspace is written by the launch before this one
+#pragma unroll 1
+    for (int u = blockIdx.x; u < n_units && !stop; u += gridDim.x) {
+      int tt, vt;
+      unit_tile(u, a.n_tt, a.n_vt, a.group, tt, vt);
+#pragma unroll 1
+      for (int j = 0; j < a.blocks; ++j, ++issued) {
+        if (!warp_wait(smem_addr(&sm.empty_b[pb.i]), pb.parity ^ 1, abort_flag)) {
+          stop = true;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t fb = smem_addr(&sm.full_b[pb.i]);
+          mbar_arrive_expect_tx(fb, tile_b);
+          tma_load_2d(ring_b + pb.i * tile_b, &map_h, j * kBlockK, tt * a.N, fb);
+        }
+        __syncwarp();
+        pb.next(a.slots_b);
+      }
+      if (a.resident) break;
+    }
+    if (stop)
+      for (uint32_t k = issued > a.slots_b ? issued - a.slots_b : 0; k < issued; ++k)
+        tc_wait<true>(smem_addr(&sm.full_b[k % a.slots_b]), (k / a.slots_b) & 1, abort_flag);
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      uint32_t iw = 0, ib = 0, acc = 0;
-      bool stop = false, issued = false;
-      for (int u = blockIdx.x; u < n_units && !stop; u += gridDim.x) {
-        for (int k = 0; k < a.steps && !stop; ++k, ++iw) {
-          const uint32_t buf = acc & 1, use = acc >> 1;
-          const uint32_t d_tmem = tmem + buf * kMaxN;
-          const bool first = k % kChunkSteps == 0;
-          if (first) {
-            if (use > 0 && !tc_wait<false>(smem_addr(&sm.acc_empty[buf]), (use - 1) & 1, abort_flag)) {
-              stop = true;
-              break;
-            }
-          }
-          const uint32_t wb = iw & 1;
-          if (!tc_wait<false>(smem_addr(&sm.wide_full[wb]), (iw >> 1) & 1, abort_flag)) {
+    // ---------------------------------------------------------------- MMA issuer (whole warp)
+    Place pw, pb, pc;
+    bool stop = false, issued = false;
+#pragma unroll 1
+    for (int u = blockIdx.x; u < n_units && !stop; u += gridDim.x) {
+      const bool loaded = a.resident && u != static_cast<int>(blockIdx.x);
+      uint32_t accumulate = 0;
+#pragma unroll 1
+      for (int k = 0; k < a.steps; ++k) {
+        if (k % kChunkSteps == 0) {
+          accumulate = 0;
+          if (!warp_wait(smem_addr(&sm.acc_empty[pc.i]), pc.parity ^ 1, abort_flag)) {
             stop = true;
             break;
           }
-          const uint32_t a_tmem = tmem + kTmemA + wb * (kStepK / 2);
-          for (int j = 0; j < 2 && 2 * k + j < a.blocks; ++j) {
-            const uint32_t t = a.resident ? 2 * k + j : ib % a.slots_b;
-            if (!tc_wait<false>(smem_addr(&sm.full_b[t]), a.resident ? 0 : (ib / a.slots_b) & 1, abort_flag)) {
-              stop = true;
-              break;
-            }
-            ++ib;
-            tc_fence_after();
-            const uint32_t b_base = ring_b + t * tile_b;
+        }
+        const uint32_t d_tmem = tmem + pc.i * a.N, a_tmem = wide + pw.i * kWideCols;
+        if (!warp_wait(smem_addr(&sm.wide_full[pw.i]), pw.parity, abort_flag)) {
+          stop = true;
+          break;
+        }
 #pragma unroll
-            for (int q = 0; q < kBlockK / 16; ++q)
-              umma_f16_ts(d_tmem, a_tmem + j * (kBlockK / 2) + q * 8, smem_desc_sw128(b_base + q * 32), a.idesc,
-                          !(first && j == 0 && q == 0));
-            issued = true;
-            if (!a.resident) umma_commit(smem_addr(&sm.empty_b[t]));
-          }
-          if (stop) break;
-          umma_commit(smem_addr(&sm.wide_empty[wb]));
-          if (k % kChunkSteps == kChunkSteps - 1 || k == a.steps - 1) {
-            umma_commit(smem_addr(&sm.acc_full[buf]));
-            ++acc;
+        for (int j = 0; j < 2; ++j) {
+          if (2 * k + j < a.blocks && !stop) {
+            if (!loaded && !warp_wait(smem_addr(&sm.full_b[pb.i]), pb.parity, abort_flag)) {
+              stop = true;
+            } else {
+              tc_fence_after();
+              const uint64_t desc = smem_desc_sw128(ring_b + pb.i * tile_b);
+#pragma unroll
+              for (int q = 0; q < kBlockK / 16; ++q) {
+                umma_f16_ts(d_tmem, a_tmem + j * (kBlockK / 2) + q * 8, desc + q * 2, a.idesc, accumulate);
+                accumulate = 1;
+              }
+              issued = true;
+              if (!a.resident) umma_commit_elect(smem_addr(&sm.empty_b[pb.i]));
+              pb.next(a.slots_b);
+            }
           }
         }
+        if (stop) break;
+        umma_commit_elect(smem_addr(&sm.wide_empty[pw.i]));
+        pw.next(a.slots_w);
+        if (k % kChunkSteps == kChunkSteps - 1 || k == a.steps - 1) {
+          umma_commit_elect(smem_addr(&sm.acc_full[pc.i]));
+          pc.next(2);
+        }
       }
-      if (stop && issued) {  // every MMA already issued completes before the memory is freed
-        umma_commit(smem_addr(&sm.drain));
-        tc_wait<true>(smem_addr(&sm.drain), 0, abort_flag);
-      }
+    }
+    if (stop && issued) {  // every MMA already issued completes before the memory is freed
+      umma_commit_elect(smem_addr(&sm.drain));
+      tc_wait<true>(smem_addr(&sm.drain), 0, abort_flag);
     }
   } else if (warp >= 4 && warp < 8) {
     // ---------------------------------------------------------------- widening
     const int q = warp & 3, row = q * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
-    uint32_t it = 0;
+    Place pa, pw;
     bool stop = false;
+#pragma unroll 1
     for (int u = blockIdx.x; u < n_units && !stop; u += gridDim.x) {
-      for (int k = 0; k < a.steps; ++k, ++it) {
-        const uint32_t s = it % a.slots_a, wb = it & 1;
-        // warp-uniform outcome: the tensor-memory stores below are warp-collective
-        bool ok = tc_wait<false>(smem_addr(&sm.full_a[s]), (it / a.slots_a) & 1, abort_flag);
-        if (it >= 2) ok = ok && tc_wait<false>(smem_addr(&sm.wide_empty[wb]), ((it >> 1) - 1) & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) {
+#pragma unroll 1
+      for (int k = 0; k < a.steps; ++k) {
+        const bool ok = warp_wait(smem_addr(&sm.full_a[pa.i]), pa.parity, abort_flag) &&
+                        warp_wait(smem_addr(&sm.wide_empty[pw.i]), pw.parity ^ 1, abort_flag);
+        if (!ok) {
           stop = true;
           break;
         }
         tc_fence_after();
-        const uint32_t base = ring_a + s * kTileA + row * 128;
+        const uint32_t base = ring_a + pa.i * kTileA + row * 128, to = wide + pw.i * kWideCols + lane_addr;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t o[32];
@@ -323,24 +374,27 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             widen4(v.z, o[8 * c + 4], o[8 * c + 5]);
             widen4(v.w, o[8 * c + 6], o[8 * c + 7]);
           }
-          tmem_st32(tmem + kTmemA + wb * (kStepK / 2) + half * 32 + lane_addr, o);
+          tmem_st32(to + half * 32, o);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_addr(&sm.empty_a[s]));
-          mbar_arrive(smem_addr(&sm.wide_full[wb]));
+          mbar_arrive(smem_addr(&sm.empty_a[pa.i]));
+          mbar_arrive(smem_addr(&sm.wide_full[pw.i]));
         }
+        pa.next(a.slots_a);
+        pw.next(a.slots_w);
       }
     }
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3, row = q * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
-    uint32_t acc = 0;
+    Place pc;
     bool stop = false;
     const int n_chunks = (a.steps + kChunkSteps - 1) / kChunkSteps;
+#pragma unroll 1
     for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
       int tt, vt;
       unit_tile(u, a.n_tt, a.n_vt, a.group, tt, vt);
@@ -349,13 +403,15 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
       const bool here = v < a.V;
       const float sw = here ? a.scale_w[v] : 0.f;
       T* out = static_cast<T*>(a.out) + r0 * a.ld + v;
+      T* to = out;
+      float sh = lane < n ? __ldg(a.scale_h + r0 + lane) : 0.f;
       int sum[kDeep ? kMaxNDeep : 1];
-      for (int ch = 0; ch < n_chunks; ++ch, ++acc) {
-        const uint32_t buf = acc & 1, use = acc >> 1;
-        stop = stop || !__all_sync(0xffffffffu, tc_wait<false>(smem_addr(&sm.acc_full[buf]), use & 1, abort_flag));
+#pragma unroll 1
+      for (int ch = 0; ch < n_chunks; ++ch) {
+        stop = stop || !warp_wait(smem_addr(&sm.acc_full[pc.i]), pc.parity, abort_flag);
         if (stop) break;
         tc_fence_after();
-        const uint32_t from = tmem + lane_addr + buf * kMaxN;
+        const uint32_t from = tmem + lane_addr + pc.i * a.N;
         if (kDeep) {
 #pragma unroll
           for (int c = 0; c < kMaxNDeep / 16; ++c) {
@@ -370,22 +426,25 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
           }
         } else {
 #pragma unroll 1
-          for (int c = 0; c < a.N; c += 16) {
-            uint32_t x[16];
-            tmem_ld16_issue(from + c, x);
-            float sh[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sh[i] = c + i < n ? __ldg(a.scale_h + r0 + c + i) : 0.f;
+          for (int c = 0; c < a.N; c += 32) {
+            const float mine = sh;  // of token c + lane; the next 32 are on their way
+            sh = c + 32 + lane < n ? __ldg(a.scale_h + r0 + c + 32 + lane) : 0.f;
+            uint32_t x[2][16];
+            tmem_ld16_issue(from + c, x[0]);
+            if (c + 16 < a.N) tmem_ld16_issue(from + c + 16, x[1]);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (here && c + i < n)
-                out[(c + i) * a.ld] = rounded<T>(__fmul_rn(__fmul_rn(__uint_as_float(x[i]), sh[i]), sw));
+            for (int i = 0; i < 32; ++i) {
+              const float s = __shfl_sync(0xffffffffu, mine, i);
+              if (here && c + i < n) *to = rounded<T>(__fmul_rn(__fmul_rn(__uint_as_float(x[i / 16][i % 16]), s), sw));
+              to += a.ld;
+            }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sm.acc_empty[buf]));
+        if (lane == 0) mbar_arrive(smem_addr(&sm.acc_empty[pc.i]));
+        pc.next(2);
       }
       if (stop) {  // not known to be right
         for (int t = 0; t < n; ++t)
@@ -425,7 +484,7 @@ bool overlap(const void* x, long long nx, const void* y, long long ny) {
 constexpr long long kTokenL2Bytes = 40LL << 20;
 
 struct IPlan {
-  int n_tt, n_vt, group, N, steps, blocks, slots_a, slots_b, resident;
+  int n_tt, n_vt, group, N, steps, blocks, slots_a, slots_b, slots_w, resident;
 };
 
 IPlan int8_plan(long long R, long long D, long long V) {
@@ -446,10 +505,12 @@ IPlan int8_plan(long long R, long long D, long long V) {
     const long long room = (budget - p.blocks * tile_b) / kTileA;
     p.slots_a = static_cast<int>(room < kMaxA ? room : kMaxA);
   } else {
-    p.slots_a = 6;
-    const long long room = (budget - 6 * static_cast<long long>(kTileA)) / tile_b;
+    p.slots_a = 5;
+    const long long room = (budget - p.slots_a * static_cast<long long>(kTileA)) / tile_b;
     p.slots_b = static_cast<int>(room < kMaxB ? room : kMaxB);
   }
+  const int wide = (static_cast<int>(kTmemAll) - 2 * p.N) / kWideCols;
+  p.slots_w = wide < kMaxWide ? wide : kMaxWide;
   const long long g = kTokenL2Bytes / (static_cast<long long>(p.N) * wide_ld(D) * 2);
   p.group = static_cast<int>(g < 1 ? 1 : (g > p.n_tt ? p.n_tt : g));
   return p;
@@ -547,6 +608,7 @@ extern "C" rl_status rl_lmhead_logits_int8(const signed char* hidden, long long 
   a.blocks = p.blocks;
   a.slots_a = p.slots_a;
   a.slots_b = p.slots_b;
+  a.slots_w = p.slots_w;
   a.resident = p.resident;
   a.idesc = make_idesc_f16(false, kM, p.N, false, false);
   a.scale_h = scale_h;
