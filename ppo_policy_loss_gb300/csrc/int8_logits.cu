@@ -13,7 +13,7 @@
 //   * widen_kernel writes the tokens' codes as fp16 into the workspace (R D
 //     elements, 1 to 2 us beside a product that reads V D bytes).
 //   * warps 0 and 2 (one lane each): TMA producers of two rings: 8-bit weight tiles (128
-//     channels x 128 columns, 16 KB) and fp16 token tiles (N x 64 columns).
+//     channels x 128 columns, 16 KB) and fp16 token tiles (N x 128 columns).
 //     Where all columns of a single token tile fit (small batches), they are loaded once and stay.
 //   * warps 4-7: one channel a thread.  A 128-byte row of codes from shared memory, widened
 //     in registers (4 codes: one XOR, two byte permutes to 1024 + code + 128,
@@ -22,7 +22,7 @@
 //     shared-memory traffic, which the token tiles already keep busy.
 //   * warp 1: tcgen05.mma.kind::f16, M = 128, K = 16, into one of two
 //     accumulators of N columns.
-//   * warps 8-11: epilogue, a channel a lane: scales, rounding, and stores of
+//   * warps 8-11 and 12-15: epilogue, a channel a lane: scales, rounding, and stores of
 //     32 neighbouring channels of a token at a time.
 //   * N is a multiple of 16 up to 192 (2 accumulators of 192 columns and two widened tiles
 //     of 64 fill the 512 columns of tensor memory); 128 where sums stay in the epilogue's registers (D > 1024).
@@ -50,21 +50,23 @@ constexpr int kExactK = 1024;             // columns that fp32 sums exactly
 constexpr int kChunkSteps = kExactK / kStepK;
 constexpr int kMaxN = 192, kMaxNDeep = 128;
 constexpr uint32_t kTileA = kM * kStepK;  // 16 KB
-constexpr int kThreadsI = 384;
 constexpr uint32_t kTmemAll = 512;        // columns: two accumulators of N, then widened tiles of 64
 constexpr int kWideCols = kStepK / 2;
-constexpr int kMaxA = 12, kMaxB = 96, kMaxWide = 4;  // ring slots, widened tiles
-constexpr uint32_t kRingBytes = 224 * 1024;
+constexpr int kMaxA = 12, kMaxB = 48, kMaxWide = 4;  // ring slots, widened tiles
+constexpr int kMaxDone = 8;
+constexpr uint32_t kRingBytes = 222 * 1024;
 constexpr int kWidenThreads = 256;
 
 struct Bars {
   unsigned long long full_a[kMaxA], empty_a[kMaxA];
-  unsigned long long full_b[kMaxB], empty_b[kMaxB];
-  unsigned long long wide_full[kMaxWide], wide_empty[kMaxWide];
+  unsigned long long full_b[kMaxB];
+  unsigned long long wide_full[kMaxWide];
+  unsigned long long done[kMaxDone];
   unsigned long long acc_full[2], acc_empty[2];
   unsigned long long drain;
   uint32_t tmem_base;
   int abort;
+  alignas(16) float scale[2][kMaxN + 32];  // of the tokens of the epilogue's unit
 };
 
 static_assert(kRingBytes + 1024 + sizeof(Bars) <= 232448, "rings and barriers fit the 227 KB a CTA may use");
@@ -73,9 +75,9 @@ struct IArgs {
   long long R, V, ld;
   int n_tt, n_vt, group;  // token tiles, channel tiles, token tiles of a unit group
   int N;                  // tokens of a tile
-  int steps, blocks;      // weight and token tiles along D
-  int slots_a, slots_b, slots_w;
-  int resident;           // the token tile's blocks are loaded once
+  int steps;              // tiles along D
+  int slots_a, slots_b, slots_w, slots_d;
+  int resident;           // the token tiles are loaded once
   uint32_t idesc;
   const float* scale_h;
   const float* scale_w;
@@ -95,11 +97,15 @@ struct Place {
   }
 };
 
+__device__ __noinline__ bool warp_wait_on(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, tc_wait<false>(bar, parity, abort));
+}
 // A whole warp's wait; the outcome is warp-uniform.  (Every lane looks: a lane that
 // waits by itself, with the others held at the next warp-wide instruction or at the end of
 // its role, makes the scheduler change between the two: a tile took 5.4 us, not 3.4.)
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, tc_wait<false>(bar, parity, abort));
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return warp_wait_on(bar, parity, abort);
 }
 
 // One lane of the warp issues.  (The whole warp runs the loop around it, so that the
@@ -124,6 +130,14 @@ __device__ __forceinline__ void tmem_ld16_issue(uint32_t taddr, uint32_t (&r)[16
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// 32 of them.
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
 }
@@ -189,35 +203,120 @@ __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { retur
 template <>
 __device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
 
+// Where a lane writes what it holds of 32 tokens.  Neighbouring lanes hold neighbouring
+// channels: of 16-bit logits, lanes 2i and 2i + 1 exchange halves, so that the even one
+// writes both channels of the even tokens and the odd one those of the odd tokens.
+template <class T>
+struct Rows {
+  T* p;
+  long long ld;
+  int odd;
+  int width;  // channels that this lane writes of a token
+  __device__ __forceinline__ Rows(T* out, long long v, long long V, long long ld_, int lane) : ld(ld_) {
+    if (sizeof(T) == 2) {
+      odd = lane & 1;
+      const long long v0 = v - odd;
+      width = v0 + 1 < V ? 2 : v0 < V ? 1 : 0;
+      p = out + odd * ld + v0;
+    } else {
+      odd = 0;
+      width = v < V;
+      p = out + v;
+    }
+  }
+  __device__ __forceinline__ void next(int tokens) { p += tokens * ld; }
+};
+
+__device__ __forceinline__ uint32_t pack2(float x, float y, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float x, float y, __half) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The scaled sums of 32 tokens (of which there are n), rounded and stored.  All words are
+// formed before the first store, and those of whole tiles are stored without a branch.
+__device__ __forceinline__ void store32(const uint32_t (&x)[32], const float* scale, float sw, int n, const Rows<float>& to) {
+  float w[32];
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float4 s = *reinterpret_cast<const float4*>(scale + i);
+    w[i] = __fmul_rn(__fmul_rn(__uint_as_float(x[i]), s.x), sw);
+    w[i + 1] = __fmul_rn(__fmul_rn(__uint_as_float(x[i + 1]), s.y), sw);
+    w[i + 2] = __fmul_rn(__fmul_rn(__uint_as_float(x[i + 2]), s.z), sw);
+    w[i + 3] = __fmul_rn(__fmul_rn(__uint_as_float(x[i + 3]), s.w), sw);
+  }
+  float* p = to.p;
+  if (__all_sync(0xffffffffu, to.width == 1) && n >= 32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i, p += to.ld) *p = w[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i, p += to.ld)
+      if (to.width && i < n) *p = w[i];
+  }
+}
+template <class T>
+__device__ __forceinline__ void store32(const uint32_t (&x)[32], const float* scale, float sw, int n, const Rows<T>& to) {
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float4 s = *reinterpret_cast<const float4*>(scale + i);
+    w[i / 2] = pack2(__fmul_rn(__fmul_rn(__uint_as_float(x[i]), s.x), sw), __fmul_rn(__fmul_rn(__uint_as_float(x[i + 1]), s.y), sw), T());
+    w[i / 2 + 1] = pack2(__fmul_rn(__fmul_rn(__uint_as_float(x[i + 2]), s.z), sw), __fmul_rn(__fmul_rn(__uint_as_float(x[i + 3]), s.w), sw), T());
+  }
+  const uint32_t pick = to.odd ? 0x3276u : 0x5410u;  // own word, then the neighbour's: even the low halves, odd the high ones
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = __byte_perm(w[i], __shfl_xor_sync(0xffffffffu, w[i], 1), pick);
+  T* p = to.p;
+  if (__all_sync(0xffffffffu, to.width == 2) && n >= 32) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i, p += 2 * to.ld) *reinterpret_cast<uint32_t*>(p) = w[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i, p += 2 * to.ld)
+      if (2 * i + to.odd < n) {
+        if (to.width == 2)
+          *reinterpret_cast<uint32_t*>(p) = w[i];
+        else if (to.width == 1)
+          *reinterpret_cast<unsigned short*>(p) = static_cast<unsigned short>(w[i]);
+      }
+  }
+}
+
 // (Loops stay rolled: an unrolled role is a kilobyte of instructions that each call fetches
 // from HBM, 1200 cycles a line, for the weights before it have swept them out of L2.)
+// Threads of a CTA: sums over many columns stay in the epilogue's registers, which
+// leaves room for one group of four epilogue warps instead of two.
+__host__ __device__ constexpr int int8_threads(bool deep) { return deep ? 384 : 512; }
+constexpr int kChunkN = 32;  // columns of an accumulator that an epilogue warp takes at a time
+
 template <class T, bool kDeep>
-__global__ void __launch_bounds__(kThreadsI, 1)
+__global__ void __launch_bounds__(int8_threads(kDeep), 1)
 logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h, const IArgs a) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ Bars sm;
   const uint32_t ring_a = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t ring_b = ring_a + a.slots_a * kTileA, tile_b = static_cast<uint32_t>(a.N) * 128u;
+  const uint32_t ring_b = ring_a + a.slots_a * kTileA, block_b = static_cast<uint32_t>(a.N) * 128u, tile_b = 2 * block_b;
   volatile int* abort_flag = &sm.abort;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int n_units = a.n_tt * a.n_vt;
+  const int n_units = a.n_tt * a.n_vt, steps = a.steps, N = a.N;
+  const uint32_t slots_a = a.slots_a, slots_b = a.slots_b, slots_w = a.slots_w, slots_d = a.slots_d;
+  constexpr int kEpilogue = kDeep ? 4 : 8;  // epilogue warps
 
   if (tid == 0) {
     for (int s = 0; s < a.slots_a; ++s) {
       mbar_init(smem_addr(&sm.full_a[s]), 1);
       mbar_init(smem_addr(&sm.empty_a[s]), 4);
     }
-    for (int s = 0; s < a.slots_b; ++s) {
-      mbar_init(smem_addr(&sm.full_b[s]), 1);
-      mbar_init(smem_addr(&sm.empty_b[s]), 1);
-    }
-    for (int s = 0; s < a.slots_w; ++s) {
-      mbar_init(smem_addr(&sm.wide_full[s]), 4);
-      mbar_init(smem_addr(&sm.wide_empty[s]), 1);
-    }
+    for (int s = 0; s < a.slots_b; ++s) mbar_init(smem_addr(&sm.full_b[s]), 1);
+    for (int s = 0; s < a.slots_w; ++s) mbar_init(smem_addr(&sm.wide_full[s]), 4);
+    for (int s = 0; s < a.slots_d; ++s) mbar_init(smem_addr(&sm.done[s]), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_addr(&sm.acc_full[s]), 1);
-      mbar_init(smem_addr(&sm.acc_empty[s]), 4);
+      mbar_init(smem_addr(&sm.acc_empty[s]), kEpilogue);
     }
     mbar_init(smem_addr(&sm.drain), 1);
     sm.abort = 0;
@@ -244,7 +343,7 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
       int tt, vt;
       unit_tile(u, a.n_tt, a.n_vt, a.group, tt, vt);
 #pragma unroll 1
-      for (int k = 0; k < a.steps; ++k, ++issued) {
+      for (int k = 0; k < steps; ++k, ++issued) {
         // (a barrier that has completed no phase passes a wait for the one before its first)
         if (!warp_wait(smem_addr(&sm.empty_a[pa.i]), pa.parity ^ 1, abort_flag)) {
           stop = true;
@@ -256,15 +355,15 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
           tma_load_2d(ring_a + pa.i * kTileA, &map_w, k * kStepK, vt * kM, fa);
         }
         __syncwarp();
-        pa.next(a.slots_a);
+        pa.next(slots_a);
       }
     }
     if (stop)  // copies already issued land before the CTA can exit
-      for (uint32_t k = issued > a.slots_a ? issued - a.slots_a : 0; k < issued; ++k)
-        tc_wait<true>(smem_addr(&sm.full_a[k % a.slots_a]), (k / a.slots_a) & 1, abort_flag);
+      for (uint32_t k = issued > slots_a ? issued - slots_a : 0; k < issued; ++k)
+        tc_wait<true>(smem_addr(&sm.full_a[k % slots_a]), (k / slots_a) & 1, abort_flag);
   } else if (warp == 2) {
     // ---------------------------------------------------------------- TMA producer: token tiles (whole warp)
-    Place pb;
+    Place pb, pd;
     uint32_t issued = 0;
     bool stop = false;
     grid_dependency_wait();  // the workspace is written by the launch before this one
@@ -273,73 +372,66 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
       int tt, vt;
       unit_tile(u, a.n_tt, a.n_vt, a.group, tt, vt);
 #pragma unroll 1
-      for (int j = 0; j < a.blocks; ++j, ++issued) {
-        if (!warp_wait(smem_addr(&sm.empty_b[pb.i]), pb.parity ^ 1, abort_flag)) {
-          stop = true;
-          break;
+      for (int k = 0; k < steps; ++k, ++issued) {
+        if (issued >= slots_b) {  // the step that used the slot last
+          if (!warp_wait(smem_addr(&sm.done[pd.i]), pd.parity, abort_flag)) {
+            stop = true;
+            break;
+          }
+          pd.next(slots_d);
         }
         if (lane == 0) {
-          const uint32_t fb = smem_addr(&sm.full_b[pb.i]);
+          const uint32_t fb = smem_addr(&sm.full_b[pb.i]), to = ring_b + pb.i * tile_b;
           mbar_arrive_expect_tx(fb, tile_b);
-          tma_load_2d(ring_b + pb.i * tile_b, &map_h, j * kBlockK, tt * a.N, fb);
+          tma_load_2d(to, &map_h, k * kStepK, tt * N, fb);
+          tma_load_2d(to + block_b, &map_h, k * kStepK + kBlockK, tt * N, fb);
         }
         __syncwarp();
-        pb.next(a.slots_b);
+        pb.next(slots_b);
       }
       if (a.resident) break;
     }
     if (stop)
-      for (uint32_t k = issued > a.slots_b ? issued - a.slots_b : 0; k < issued; ++k)
-        tc_wait<true>(smem_addr(&sm.full_b[k % a.slots_b]), (k / a.slots_b) & 1, abort_flag);
+      for (uint32_t k = issued > slots_b ? issued - slots_b : 0; k < issued; ++k)
+        tc_wait<true>(smem_addr(&sm.full_b[k % slots_b]), (k / slots_b) & 1, abort_flag);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (whole warp)
-    Place pw, pb, pc;
-    bool stop = false, issued = false;
+    Place pw, pb, pc, pd;
+    const uint32_t idesc = a.idesc;
+    bool stop = false, issued = false, loaded = false;
 #pragma unroll 1
     for (int u = blockIdx.x; u < n_units && !stop; u += gridDim.x) {
-      const bool loaded = a.resident && u != static_cast<int>(blockIdx.x);
-      uint32_t accumulate = 0;
+      int in_sum = 0;  // steps in the accumulator
 #pragma unroll 1
-      for (int k = 0; k < a.steps; ++k) {
-        if (k % kChunkSteps == 0) {
-          accumulate = 0;
-          if (!warp_wait(smem_addr(&sm.acc_empty[pc.i]), pc.parity ^ 1, abort_flag)) {
-            stop = true;
-            break;
-          }
-        }
-        const uint32_t d_tmem = tmem + pc.i * a.N, a_tmem = wide + pw.i * kWideCols;
-        if (!warp_wait(smem_addr(&sm.wide_full[pw.i]), pw.parity, abort_flag)) {
+      for (int k = 0; k < steps; ++k) {
+        if (in_sum == 0 && !warp_wait(smem_addr(&sm.acc_empty[pc.i]), pc.parity ^ 1, abort_flag)) {
           stop = true;
           break;
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (2 * k + j < a.blocks && !stop) {
-            if (!loaded && !warp_wait(smem_addr(&sm.full_b[pb.i]), pb.parity, abort_flag)) {
-              stop = true;
-            } else {
-              tc_fence_after();
-              const uint64_t desc = smem_desc_sw128(ring_b + pb.i * tile_b);
-#pragma unroll
-              for (int q = 0; q < kBlockK / 16; ++q) {
-                umma_f16_ts(d_tmem, a_tmem + j * (kBlockK / 2) + q * 8, desc + q * 2, a.idesc, accumulate);
-                accumulate = 1;
-              }
-              issued = true;
-              if (!a.resident) umma_commit_elect(smem_addr(&sm.empty_b[pb.i]));
-              pb.next(a.slots_b);
-            }
-          }
+        if (!warp_wait(smem_addr(&sm.wide_full[pw.i]), pw.parity, abort_flag) ||
+            (!loaded && !warp_wait(smem_addr(&sm.full_b[pb.i]), pb.parity, abort_flag))) {
+          stop = true;
+          break;
         }
-        if (stop) break;
-        umma_commit_elect(smem_addr(&sm.wide_empty[pw.i]));
-        pw.next(a.slots_w);
-        if (k % kChunkSteps == kChunkSteps - 1 || k == a.steps - 1) {
+        tc_fence_after();
+        const uint32_t d_tmem = tmem + pc.i * N, a_tmem = wide + pw.i * kWideCols;
+        const uint64_t desc = smem_desc_sw128(ring_b + pb.i * tile_b), desc1 = desc + (block_b >> 4);
+#pragma unroll
+        for (int q = 0; q < kBlockK / 16; ++q) umma_f16_ts(d_tmem, a_tmem + q * 8, desc + q * 2, idesc, q | in_sum);
+#pragma unroll
+        for (int q = 0; q < kBlockK / 16; ++q) umma_f16_ts(d_tmem, a_tmem + kBlockK / 2 + q * 8, desc1 + q * 2, idesc, 1);
+        issued = true;
+        umma_commit_elect(smem_addr(&sm.done[pd.i]));  // frees the widened tile and the token tile
+        pw.next(slots_w);
+        pb.next(slots_b);
+        pd.next(slots_d);
+        if (++in_sum == kChunkSteps || k == steps - 1) {
           umma_commit_elect(smem_addr(&sm.acc_full[pc.i]));
           pc.next(2);
+          in_sum = 0;
         }
       }
+      loaded = a.resident;
     }
     if (stop && issued) {  // every MMA already issued completes before the memory is freed
       umma_commit_elect(smem_addr(&sm.drain));
@@ -349,14 +441,20 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     // ---------------------------------------------------------------- widening
     const int q = warp & 3, row = q * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
-    Place pa, pw;
+    Place pa, pw, pd;
+    uint32_t ahead = slots_w;  // tiles that no step has to free
     bool stop = false;
 #pragma unroll 1
     for (int u = blockIdx.x; u < n_units && !stop; u += gridDim.x) {
 #pragma unroll 1
-      for (int k = 0; k < a.steps; ++k) {
-        const bool ok = warp_wait(smem_addr(&sm.full_a[pa.i]), pa.parity, abort_flag) &&
-                        warp_wait(smem_addr(&sm.wide_empty[pw.i]), pw.parity ^ 1, abort_flag);
+      for (int k = 0; k < steps; ++k) {
+        bool ok = warp_wait(smem_addr(&sm.full_a[pa.i]), pa.parity, abort_flag);
+        if (ahead > 0) {
+          --ahead;
+        } else {
+          ok = ok && warp_wait(smem_addr(&sm.done[pd.i]), pd.parity, abort_flag);
+          pd.next(slots_d);
+        }
         if (!ok) {
           stop = true;
           break;
@@ -380,11 +478,11 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_addr(&sm.empty_a[pa.i]));
           mbar_arrive(smem_addr(&sm.wide_full[pw.i]));
+          mbar_arrive(smem_addr(&sm.empty_a[pa.i]));
         }
-        pa.next(a.slots_a);
-        pw.next(a.slots_w);
+        pa.next(slots_a);
+        pw.next(slots_w);
       }
     }
   } else if (warp >= 8) {
@@ -392,10 +490,19 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     const int q = warp & 3, row = q * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
     Place pc;
+    const int group = (warp - 8) >> 2, me = tid - 8 * 32;
+    uint32_t parity = 0;
     bool stop = false;
     const int n_chunks = (a.steps + kChunkSteps - 1) / kChunkSteps;
+    float mine = 0.f;  // a token's scale
+    if (static_cast<int>(blockIdx.x) < n_units) {
+      int tt, vt;
+      unit_tile(blockIdx.x, a.n_tt, a.n_vt, a.group, tt, vt);
+      const long long r = static_cast<long long>(tt) * a.N + me;
+      mine = me < a.N && r < a.R ? __ldg(a.scale_h + r) : 0.f;
+    }
 #pragma unroll 1
-    for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
+    for (int u = blockIdx.x; u < n_units; u += gridDim.x, parity ^= 1) {
       int tt, vt;
       unit_tile(u, a.n_tt, a.n_vt, a.group, tt, vt);
       const long long v = static_cast<long long>(vt) * kM + row, r0 = static_cast<long long>(tt) * a.N;
@@ -403,8 +510,17 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
       const bool here = v < a.V;
       const float sw = here ? a.scale_w[v] : 0.f;
       T* out = static_cast<T*>(a.out) + r0 * a.ld + v;
-      T* to = out;
-      float sh = lane < n ? __ldg(a.scale_h + r0 + lane) : 0.f;
+      // the tokens' scales, in turn in two places: the barrier keeps the warps within a unit of
+      // one another.  The next unit's are on their way while this one's are used.
+      if (me < a.N) sm.scale[parity][me] = mine;
+      named_barrier(1, kEpilogue * 32);
+      if (u + static_cast<int>(gridDim.x) < n_units) {
+        int tn, vn;
+        unit_tile(u + gridDim.x, a.n_tt, a.n_vt, a.group, tn, vn);
+        const long long r = static_cast<long long>(tn) * a.N + me;
+        mine = me < a.N && r < a.R ? __ldg(a.scale_h + r) : 0.f;
+      }
+      Rows<T> to(static_cast<T*>(a.out) + (r0 + group * kChunkN) * a.ld, v, a.V, a.ld, lane);
       int sum[kDeep ? kMaxNDeep : 1];
 #pragma unroll 1
       for (int ch = 0; ch < n_chunks; ++ch) {
@@ -425,20 +541,14 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             }
           }
         } else {
+          const float* scale = sm.scale[parity];
 #pragma unroll 1
-          for (int c = 0; c < a.N; c += 32) {
-            const float mine = sh;  // of token c + lane; the next 32 are on their way
-            sh = c + 32 + lane < n ? __ldg(a.scale_h + r0 + c + 32 + lane) : 0.f;
-            uint32_t x[2][16];
-            tmem_ld16_issue(from + c, x[0]);
-            if (c + 16 < a.N) tmem_ld16_issue(from + c + 16, x[1]);
+          for (int c = group * kChunkN; c < a.N; c += kEpilogue / 4 * kChunkN) {
+            uint32_t x[32];
+            tmem_ld32_issue(from + c, x);  // (behind N: what lies there, and goes nowhere)
             tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float s = __shfl_sync(0xffffffffu, mine, i);
-              if (here && c + i < n) *to = rounded<T>(__fmul_rn(__fmul_rn(__uint_as_float(x[i / 16][i % 16]), s), sw));
-              to += a.ld;
-            }
+            store32(x, scale + c, sw, n - c, to);
+            to.next(kEpilogue / 4 * kChunkN);
           }
         }
         tc_fence_before();
@@ -453,7 +563,7 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
 #pragma unroll
         for (int i = 0; i < kMaxNDeep; ++i)
           if (here && i < n)
-            out[i * a.ld] = rounded<T>(__fmul_rn(__fmul_rn(static_cast<float>(sum[i]), __ldg(a.scale_h + r0 + i)), sw));
+            out[i * a.ld] = rounded<T>(__fmul_rn(__fmul_rn(static_cast<float>(sum[i]), sm.scale[parity][i]), sw));
       }
     }
   }
@@ -484,7 +594,7 @@ bool overlap(const void* x, long long nx, const void* y, long long ny) {
 constexpr long long kTokenL2Bytes = 40LL << 20;
 
 struct IPlan {
-  int n_tt, n_vt, group, N, steps, blocks, slots_a, slots_b, slots_w, resident;
+  int n_tt, n_vt, group, N, steps, slots_a, slots_b, slots_w, slots_d, resident;
 };
 
 IPlan int8_plan(long long R, long long D, long long V) {
@@ -496,21 +606,21 @@ IPlan int8_plan(long long R, long long D, long long V) {
   p.n_tt = static_cast<int>((R + p.N - 1) / p.N);
   p.n_vt = static_cast<int>((V + kM - 1) / kM);
   p.steps = static_cast<int>((D + kStepK - 1) / kStepK);
-  p.blocks = static_cast<int>((D + kBlockK - 1) / kBlockK);
-  const long long tile_b = static_cast<long long>(p.N) * 128, budget = kRingBytes;
+  const long long tile_b = static_cast<long long>(p.N) * 256, budget = kRingBytes;
   // weights in flight are what a small batch waits for: at least 80 KB of them beside resident tokens
-  p.resident = p.n_tt == 1 && p.blocks <= kMaxB && p.blocks * tile_b + 5 * static_cast<long long>(kTileA) <= budget;
+  p.resident = p.n_tt == 1 && p.steps <= kMaxB && p.steps * tile_b + 5 * static_cast<long long>(kTileA) <= budget;
   if (p.resident) {
-    p.slots_b = p.blocks;
-    const long long room = (budget - p.blocks * tile_b) / kTileA;
+    p.slots_b = p.steps;
+    const long long room = (budget - p.steps * tile_b) / kTileA;
     p.slots_a = static_cast<int>(room < kMaxA ? room : kMaxA);
   } else {
-    p.slots_a = 5;
+    p.slots_a = 4;
     const long long room = (budget - p.slots_a * static_cast<long long>(kTileA)) / tile_b;
-    p.slots_b = static_cast<int>(room < kMaxB ? room : kMaxB);
+    p.slots_b = static_cast<int>(room < kMaxDone ? room : kMaxDone);
   }
   const int wide = (static_cast<int>(kTmemAll) - 2 * p.N) / kWideCols;
   p.slots_w = wide < kMaxWide ? wide : kMaxWide;
+  p.slots_d = p.resident || p.slots_w > p.slots_b ? p.slots_w : p.slots_b;
   const long long g = kTokenL2Bytes / (static_cast<long long>(p.N) * wide_ld(D) * 2);
   p.group = static_cast<int>(g < 1 ? 1 : (g > p.n_tt ? p.n_tt : g));
   return p;
@@ -540,7 +650,7 @@ rl_status launch(const CUtensorMap& map_w, const CUtensorMap& map_h, const IArgs
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreadsI);
+  cfg.blockDim = dim3(int8_threads(kDeep));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -605,10 +715,10 @@ extern "C" rl_status rl_lmhead_logits_int8(const signed char* hidden, long long 
   a.group = p.group;
   a.N = p.N;
   a.steps = p.steps;
-  a.blocks = p.blocks;
   a.slots_a = p.slots_a;
   a.slots_b = p.slots_b;
   a.slots_w = p.slots_w;
+  a.slots_d = p.slots_d;
   a.resident = p.resident;
   a.idesc = make_idesc_f16(false, kM, p.N, false, false);
   a.scale_h = scale_h;
