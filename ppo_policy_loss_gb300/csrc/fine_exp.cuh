@@ -55,20 +55,24 @@ __device__ __forceinline__ float quick_two_sum(float x, float y, float& err) {
   return s;
 }
 
-// 2^((z - m) c - kappa), c = c_hi + c_lo.  0 below 2^-120; above 2 the value is
-// not to be used (but exceeds 2).  z = -inf gives 0.
+// 2^((z - m) c - kappa), c = c_hi + c_lo.  z - m counts as at least dmin, so that what is
+// below 2^-124 (and -inf) gives 2^-124, which no sum notices (is_zero() tells it from a
+// weight), and as at most dmax, so that what is above 4 gives about 4.
 struct FineExp {
-  float m, c_hi, c_lo, kappa;
+  float m, c_hi, c_lo, kappa, dmin, dmax;
 
-  // c: log2(e) / temperature.  The frame: the terms are 2^(z c - k).
+  // c: log2(e) / temperature.  The frame: the terms are 2^(z c - k), kappa = k - m c.
   __device__ __forceinline__ void init(double c, float m_, double kappa_) {
     c_hi = static_cast<float>(c);
     c_lo = static_cast<float>(c - static_cast<double>(c_hi));
     m = m_;
     kappa = static_cast<float>(kappa_);
+    const float unit = 1.f / c_hi;
+    dmin = -124.f * unit;
+    dmax = 2.f * unit;
   }
-  // kWide: z has 24 significant bits (16-bit numbers have 8 or 11).
-  template <bool kWide>
+  // kWide: z has 24 significant bits (16-bit numbers have 8 or 11).  kTop: z - m may be above dmax.
+  template <bool kWide, bool kTop>
   __device__ __forceinline__ Term at(float z, const float* T, const float* delta) const {
     // the difference and its error r; of 16-bit numbers that is 0 unless |z| is far below |m|
     float r, d;
@@ -76,11 +80,17 @@ struct FineExp {
       d = two_sum(z, -m, r);
     else
       d = quick_two_sum(-m, z, r);
+    r = d > dmin ? r : 0.f;
+    d = fmaxf(d, dmin);
+    if (kTop) {
+      r = d < dmax ? r : 0.f;
+      d = fminf(d, dmax);
+    }
     const float x = __fmul_rn(d, c_hi);
     float gl = fmaf(r, c_hi, -kappa);
     gl = __fadd_rn(fmaf(d, c_hi, -x), fmaf(d, c_lo, gl));
     constexpr float kMagic = 393216.f;  // 1.5 2^18: its last place is 1 / 32
-    const float t = __fadd_rn(fminf(fmaxf(x, -125.f), 2.f), kMagic);
+    const float t = __fadd_rn(x, kMagic);
     const int jn = __float_as_int(t) - __float_as_int(kMagic);
     const int j = jn & (kPow - 1);
     const float gh = __fsub_rn(x, __fsub_rn(t, kMagic));
@@ -96,10 +106,9 @@ struct FineExp {
     p.a = __int_as_float(__float_as_int(T[j]) + ((jn >> 5) << 23));
     p.b = __fmul_rn(p.a, u);
     p.c = fmaf(p.a, v, fmaf(p.a, u, -p.b));
-    if (!(x > -120.f)) p.a = p.b = p.c = 0.f;
-    if (x > 1.5f) p.b = p.c = 0.f;
     return p;
   }
+  __device__ __forceinline__ bool is_zero(float z) const { return !(__fsub_rn(z, m) > dmin); }
 };
 
 // The difference of two terms; its sign is that of a + b + c.

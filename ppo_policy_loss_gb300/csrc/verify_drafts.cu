@@ -1,16 +1,28 @@
 // verify_drafts.cu — rl_verify_drafts: which drafted tokens a sequence keeps,
 // and the token drawn after them (include/rlrollout.h).
 //
-// A CTA takes a sequence.
-//  1. Its target rows in order, until a draft does not stay: maximum and sum of
-//     e^((z - m) / T) of the row in one pass, fp32, online.  The maxima, whose
-//     terms are exactly 1, are counted beside the sum, so that log S keeps its
-//     relative precision where one token holds nearly all the mass.
-//  2. The weights of the row that the token is drawn from, in fine arithmetic (fine_exp.cuh),
-//     summed for each warp's part of the row: the row's own softmax, and where a
-//     draft with a distribution was refused, in a second pass max(p S - q S, 0).
-//  3. The part in which the running sum passes the border is split again among
-//     the warps, until one warp walks through what is left.
+// A cluster of 1 to 16 CTAs takes a sequence; each warp has a part of every row.
+//  1. The sequence's target rows in order, until a draft does not stay: maximum
+//     and sum of e^((z - m) / T) of the row in one pass, fp32, online, with the warp's
+//     maximum as the frame (one FMA an element: x = z c + nm; the rounding of nm = -m c, common
+//     to a frame's terms, is put right when the frame ends).  The maxima, whose terms are exactly 1,
+//     are counted beside the sum, so that log S keeps its relative precision
+//     where one token holds nearly all the mass.  Rows behind a refused draft
+//     are not read.
+//  2. The token.  The sums of the warps' parts, then of parts of that part, lead to the
+//     one in which the running sum passes the border u S.  These fp32 sums are good to
+//     kCoarse of S (below): where the border is nearer than that to either side of the
+//     token's own weight, everything is summed again in fine arithmetic (fine_exp.cuh).
+//  3. Where a draft with a distribution was refused, the weights max(p - q, 0)
+//     are sums of differences, and always taken in fine arithmetic, in one pass over
+//     the target's and the draft's row: with S known to 2^-19 from step 1, the set of tokens
+//     with p > q is right but for tokens with p = q to 2^-19, whose weight is below 2^-19 of
+//     p there, and W - S Q of the sums over that set takes the S of the same pass.
+//
+// fp32 sums, in units of 2^-24: a term 2^x carries 4 of the hardware exponential and 2 ln 2 |x|
+// of its argument (the FMA's rounding and c's), |x| weighted by p at most log2 V < 18 for 2^18
+// tokens; 32 terms are added in chains of 10, the chains' sums with their errors kept; then
+// 5 joins in the warp and 13 for the frames of lanes and warps: 57, and the same for S.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -24,8 +36,12 @@
 namespace rl {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 3;
+constexpr int kMaxCluster = 16, kMaxParts = kMaxCluster * kWarps;
 constexpr double kLog2eD = 1.4426950408889634074;
+constexpr double kCoarse = 0x1p-17;   // two sums of 57 2^-24 each, rounded up
+constexpr double kNothing = 0x1p-90;  // sums of weights that are 0 (2^-124 each) stay below
 
 struct Args {
   const unsigned char* target;
@@ -45,8 +61,8 @@ struct Args {
   unsigned int* status;
 };
 
-// Which weights a token is drawn from.
-enum Mode { kSoftmax, kWithout, kRest };  // p; p without the drafted token; max(p - q, 0)
+// Which weights a token is drawn from: p; p without the drafted token; max(p - q, 0).
+enum Mode { kSoftmax, kWithout, kRest };
 
 // Maximum, how many hold it, and the sum of 2^((z - m) c) of the rest.
 struct Stats {
@@ -69,41 +85,162 @@ __device__ __forceinline__ Stats merged(Stats a, Stats b, float c) {
   return a;
 }
 
-struct Smem {
-  float T[kPow], delta[kPow];
-  Stats part[kWarps];
-  double sums[kWarps];
-  double log2_total;
-  long long found;
-  int verdict;  // of a row's draft
-};
-
 enum Verdict { kStays, kRefused, kNoDistribution };
 
-// log p of logit z of a row.
-__device__ __forceinline__ float log_prob(float z, const Stats& st, double inv_t) {
-  return static_cast<float>((static_cast<double>(z) - static_cast<double>(st.m)) * inv_t - log1pf((st.n - 1.f) + st.s));
-}
+// What the CTAs of a cluster tell one another, in turn in two places: whoever writes the
+// one has passed the barrier behind which everybody had read the other.
+struct Exchange {
+  Stats stats[kMaxParts];
+  double sum[kMaxParts], plus[kMaxParts], minus[kMaxParts];
+  long long token;
+  int bad, unsure;
+};
+struct Smem {
+  float T[kPow], delta[kPow];
+  Exchange ex[2];
+  double sums[kWarps];   // of the search
+  double log2_total, gap;
+  long long found;
+  int verdict;
+};
 
-template <int DT>
-__device__ __forceinline__ void load_elems(float (&z)[Fmt<DT>::kVec], const unsigned char* row, long long i, long long end) {
-  using F = Fmt<DT>;
-  // (16 bytes at a time: the stride is a multiple of that, what lies behind the row is dropped)
-  F::unpack(__ldg(reinterpret_cast<const uint4*>(row + i * F::kBytes)), z);
-  if (i + F::kVec > end) {
-#pragma unroll
-    for (int j = 0; j < F::kVec; ++j)
-      if (i + j >= end) z[j] = -INFINITY;
+// ------------------------------------------------------------------ the cluster
+struct Group {
+  int size, rank;  // CTAs of the cluster
+  uint32_t turn;
+  __device__ __forceinline__ void sync() const {
+    if (size > 1)
+      cluster_sync_all();
+    else
+      __syncthreads();
   }
+};
+
+template <class T>
+__device__ __forceinline__ void put(uint32_t addr, const T& v) {
+  static_assert(sizeof(T) % 4 == 0, "words");
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 4); ++i)
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr + 4 * i), "r"(w[i]) : "memory");
+}
+// v at `place` of this CTA, written in every CTA of the cluster by the lanes of a warp.
+template <class T>
+__device__ __forceinline__ void tell(const Group& g, T* place, const T& v, int lane) {
+  if (lane < g.size) put(map_to_rank(smem_addr(place), lane), v);
 }
 
+// ------------------------------------------------------------------ rows
+// elements behind `end` become -inf in a vector that begins at i
 template <int DT>
-__device__ __forceinline__ Stats row_stats(const unsigned char* row, long long V, float c, Smem& sm) {
+__device__ __forceinline__ void cut_vec(uint4& v, long long i, long long end) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const int n = static_cast<int>(end - i);  // of those, valid
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (DT == RL_F32) {
+      if (j >= n) w[j] = 0xff800000u;
+    } else {
+      if (2 * j >= n)
+        w[j] = Fmt<DT>::kNegInf2;
+      else if (2 * j + 1 >= n)
+        w[j] = (w[j] & 0xffffu) | (Fmt<DT>::kNegInf2 & 0xffff0000u);
+    }
+  }
+  v = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 16 bytes of a row from element i on (the stride is a multiple of that); -inf behind `end`.
+template <int DT>
+__device__ __forceinline__ uint4 load_vec(const unsigned char* row, long long i, long long end) {
+  uint4 v = make_uint4(Fmt<DT>::kNegInf2, Fmt<DT>::kNegInf2, Fmt<DT>::kNegInf2, Fmt<DT>::kNegInf2);
+  if (i < end) {
+    v = __ldg(reinterpret_cast<const uint4*>(row + i * Fmt<DT>::kBytes));
+    if (i + Fmt<DT>::kVec > end) cut_vec<DT>(v, i, end);
+  }
+  return v;
+}
+
+// Where part p of n of [begin, end) begins, parts being multiples of a warp's vectors.
+__device__ __forceinline__ long long part_size(long long length, int n, int step) {
+  return ((length + n - 1) / n + step - 1) / step * step;
+}
+
+// A warp's statistics of elements [lo, hi) of a row, in every lane.
+template <int DT>
+__device__ __forceinline__ Stats part_stats(const unsigned char* row, long long lo, long long hi, float c, int lane) {
+  using F = Fmt<DT>;
+  constexpr int kStep = 32 * F::kVec;
+  float m = F::kFloor, nm = -F::kFloor * c;
+  float n = 0.f, s = 0.f, err = 0.f;
+  uint4 next[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) next[j] = load_vec<DT>(row, lo + j * kStep + lane * F::kVec, hi);
+#pragma unroll 1
+  for (long long base = lo; base < hi; base += 4 * kStep) {
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[4 * j] = next[j].x;
+      w[4 * j + 1] = next[j].y;
+      w[4 * j + 2] = next[j].z;
+      w[4 * j + 3] = next[j].w;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) next[j] = load_vec<DT>(row, base + (4 + j) * kStep + lane * F::kVec, hi);
+    float wm;
+    {
+      const float pm = max_nan(F::raw_value(F::raw_max(w, 0)), F::kFloor);
+      asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(wm) : "f"(pm));
+    }
+    if (!(wm < m)) {
+      if (!(wm == m)) {  // the frame ends: its sum goes along, and so do the old maxima
+        const float rho = fmaf(-m, c, -nm);
+        s = fmaf(s + err, ex2_approx(rho), n) * ex2_approx((m - wm) * c);
+        err = 0.f;
+        n = 0.f;
+        m = wm;
+        nm = -m * c;
+        // what the new frame's terms are off by, s is now off by too
+        s *= ex2_approx(-fmaf(-m, c, -nm));
+      }
+      n += static_cast<float>(F::template drop_value<16>(w, m, true));
+    }
+    const float2 c2 = make_float2(c, c), nm2 = make_float2(nm, nm);
+    float2 t0 = make_float2(0.f, 0.f), t1 = t0;
+#pragma unroll
+    for (int i = 0; i < F::kPiece / 2; ++i) {
+      float2 z;
+      F::template pair<16>(w, i, z.x, z.y);
+      const float2 x = __ffma2_rn(z, c2, nm2);
+      const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+      if (i & 1)
+        t1 = __fadd2_rn(t1, e);
+      else
+        t0 = __fadd2_rn(t0, e);
+    }
+    float lost;
+    s = two_sum(s, (t0.x + t0.y) + (t1.x + t1.y), lost);
+    err += lost;
+  }
+  s = (s + err) * ex2_approx(fmaf(-m, c, -nm));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+  }
+  return Stats{m, n, s};
+}
+
+// The same by differences to the maximum, without a floor: rows of very large
+// or very small numbers.
+template <int DT>
+__device__ __noinline__ Stats part_stats_exact(const unsigned char* row, long long lo, long long hi, float c, int lane) {
   using F = Fmt<DT>;
   Stats a{-FLT_MAX, 0.f, 0.f};
-  for (long long i = static_cast<long long>(threadIdx.x) * F::kVec; i < V; i += static_cast<long long>(kThreads) * F::kVec) {
+  for (long long i = lo + lane * F::kVec; i < hi; i += 32 * F::kVec) {
     float z[F::kVec];
-    load_elems<DT>(z, row, i, V);
+    F::unpack(load_vec<DT>(row, i, hi), z);
     float vm = z[0];
 #pragma unroll
     for (int j = 1; j < F::kVec; ++j) vm = max_nan(vm, z[j]);
@@ -127,47 +264,64 @@ __device__ __forceinline__ Stats row_stats(const unsigned char* row, long long V
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     a = merged(a, Stats{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.n, o), __shfl_xor_sync(0xffffffffu, a.s, o)}, c);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sm.part[threadIdx.x >> 5] = a;
-  __syncthreads();
-  a = sm.part[0];
-  for (int w = 1; w < kWarps; ++w) a = merged(a, sm.part[w], c);
   return a;
 }
 
-// The weights of one row.
-template <int DT, int MODE>
+// ------------------------------------------------------------------ weights
+// log p of logit z of a row.
+__device__ __forceinline__ float log_prob(float z, const Stats& st, double inv_t) {
+  return static_cast<float>((static_cast<double>(z) - static_cast<double>(st.m)) * inv_t - log1pf((st.n - 1.f) + st.s));
+}
+
+template <int DT, int MODE, bool kFine>
 struct Weights {
   const unsigned char* row;
   const unsigned char* draft_row;
-  long long V, without;
+  long long without;
+  float c, nm;      // coarse: 2^(z c + nm)
   FineExp p, q;
   const float* T;
   const float* delta;
   bool bad;
 
-  // weights of elements i .. i + kVec - 1
-  __device__ __forceinline__ void at(long long i, long long end, Term (&w)[Fmt<DT>::kVec]) {
-    using F = Fmt<DT>;
-    constexpr bool wide = DT == RL_F32;
-    float z[F::kVec];
-    load_elems<DT>(z, row, i, end);
-    if (MODE == kWithout && without >= i && without < i + F::kVec) {
+  __device__ __forceinline__ Term fine(float z) const { return p.template at<DT == RL_F32, false>(z, T, delta); }
+  __device__ __forceinline__ Term drafted(float z) const { return q.template at<DT == RL_F32, true>(z, T, delta); }
+
+  // a vector's logits, -inf behind `end` and at the token that is left out
+  __device__ __forceinline__ void logits(long long i, long long end, float (&z)[Fmt<DT>::kVec]) const {
+    Fmt<DT>::unpack(load_vec<DT>(row, i, end), z);
+    if (MODE == kWithout && without >= i && without < i + Fmt<DT>::kVec) {
 #pragma unroll
-      for (int j = 0; j < F::kVec; ++j)
+      for (int j = 0; j < Fmt<DT>::kVec; ++j)
         if (i + j == without) z[j] = -INFINITY;
     }
+  }
+  // weights of elements i .. i + kVec - 1, as terms
+  __device__ __forceinline__ void at(long long i, long long end, Term (&w)[Fmt<DT>::kVec]) {
+    using F = Fmt<DT>;
+    float z[F::kVec], y[F::kVec];
+    logits(i, end, z);
+    if (MODE == kRest) F::unpack(load_vec<DT>(draft_row, i, end), y);
 #pragma unroll
-    for (int j = 0; j < F::kVec; ++j) w[j] = p.template at<wide>(z[j], T, delta);
-    if (MODE == kRest) {
-      load_elems<DT>(z, draft_row, i, end);
-#pragma unroll
-      for (int j = 0; j < F::kVec; ++j) {
-        bad = bad || !(z[j] < INFINITY);
-        w[j] = minus(w[j], q.template at<wide>(z[j], T, delta));
-        if (!(w[j].a + w[j].b + w[j].c > 0.f)) w[j].a = w[j].b = w[j].c = 0.f;
+    for (int j = 0; j < F::kVec; ++j) {
+      if (!kFine) {
+        w[j] = Term{ex2_approx(fmaf(z[j], c, nm)), 0.f, 0.f};
+      } else {
+        w[j] = fine(z[j]);
+        if (MODE == kRest) w[j] = minus(w[j], drafted(y[j]));
+        if (MODE == kRest && !(w[j].a + w[j].b + w[j].c > 0.f)) w[j] = Term{0.f, 0.f, 0.f};
       }
     }
+  }
+  // the same, 0 where a token cannot occur
+  __device__ __forceinline__ void exactly(long long i, long long end, double (&x)[Fmt<DT>::kVec]) {
+    using F = Fmt<DT>;
+    float z[F::kVec];
+    Term w[F::kVec];
+    logits(i, end, z);
+    at(i, end, w);
+#pragma unroll
+    for (int j = 0; j < F::kVec; ++j) x[j] = kFine && p.is_zero(z[j]) ? 0.0 : w[j].value();
   }
 };
 
@@ -177,93 +331,120 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-// [lo, hi) of part w of n parts of [begin, end): multiples of `step` long
-__device__ __forceinline__ long long part_size(long long length, int n, int step) {
-  return ((length + n - 1) / n + step - 1) / step * step;
-}
-
 // The warp's sum over [lo, hi), whole vectors from lo.
-template <int DT, int MODE>
-__device__ __forceinline__ double part_sum(Weights<DT, MODE>& f, long long lo, long long hi, int lane) {
+template <int DT, int MODE, bool kFine>
+__device__ __forceinline__ double part_sum(Weights<DT, MODE, kFine>& f, long long lo, long long hi, int lane) {
   using F = Fmt<DT>;
   double total = 0.0;
+  float plain = 0.f;
   FineSum s;
   s.clear();
   int n = 0;
+#pragma unroll 1
   for (long long i = lo + lane * F::kVec; i < hi; i += 32 * F::kVec) {
     Term w[F::kVec];
     f.at(i, hi, w);
+    if (kFine) {
 #pragma unroll
-    for (int j = 0; j < F::kVec; ++j) s.add(w[j]);
-    if (++n == 128 / F::kVec) {
-      total += s.value();
-      s.clear();
-      n = 0;
+      for (int j = 0; j < F::kVec; ++j) s.add(w[j]);
+      if (++n == 64) {
+        total += s.value();
+        s.clear();
+        n = 0;
+      }
+    } else {
+#pragma unroll
+      for (int j = 1; j < F::kVec; ++j) w[0].a += w[j].a;
+      plain += w[0].a;
+      if (++n == 4) {
+        total += static_cast<double>(plain);
+        plain = 0.f;
+        n = 0;
+      }
     }
   }
-  return warp_sum(total + s.value());
+  return warp_sum(total + (kFine ? s.value() : static_cast<double>(plain)));
 }
 
-// Sums of the CTA's warps over their parts of [begin, end); the total.
-template <int DT, int MODE>
-__device__ __forceinline__ double all_parts(Weights<DT, MODE>& f, long long begin, long long end, Smem& sm) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long size = part_size(end - begin, kWarps, 32 * Fmt<DT>::kVec);
-  const long long lo = min(end, begin + warp * size), hi = min(end, lo + size);
-  const double s = part_sum<DT, MODE>(f, lo, hi, lane);
-  __syncthreads();
-  if (lane == 0) sm.sums[warp] = s;
-  __syncthreads();
-  double total = 0.0;
-  for (int w = 0; w < kWarps; ++w) total += sm.sums[w];
-  return total;
+// Of n <= kMaxParts sums: the one in which the running sum exceeds `want` and what is before it
+// (past the last weight, a rounding: the last part that has any).  Whole warp.
+template <int MODE, bool kFine>
+__device__ __forceinline__ int find_part(const double* sums, int n, double want, double& before, int lane) {
+  constexpr double none = kFine && MODE != kRest ? kNothing : 0.0;
+  double v[kMaxParts / 32], own = 0.0;
+#pragma unroll
+  for (int j = 0; j < kMaxParts / 32; ++j) {
+    const int i = lane * (kMaxParts / 32) + j;
+    v[j] = i < n ? sums[i] : 0.0;
+    own += v[j];
+  }
+  double upto = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double up = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += up;
+  }
+  double run = __shfl_up_sync(0xffffffffu, upto, 1);
+  if (lane == 0) run = 0.0;
+  int at = -1, last = -1;
+  double at_before = 0.0, last_before = 0.0;
+#pragma unroll
+  for (int j = 0; j < kMaxParts / 32; ++j) {
+    if (v[j] > none) {
+      last = lane * (kMaxParts / 32) + j;
+      last_before = run;
+      if (at < 0 && run + v[j] > want) {
+        at = last;
+        at_before = run;
+      }
+    }
+    run += v[j];
+  }
+  const uint32_t hit = __ballot_sync(0xffffffffu, at >= 0), some = __ballot_sync(0xffffffffu, last >= 0);
+  const int src = hit ? __ffs(hit) - 1 : some ? 31 - __clz(some) : 0;
+  before = __shfl_sync(0xffffffffu, hit ? at_before : last_before, src);
+  return __shfl_sync(0xffffffffu, hit ? at : last, src);
+}
+__device__ __forceinline__ double total_of(const double* sums, int n, int lane) {
+  double v = 0.0;
+  for (int i = lane; i < n; i += 32) v += sums[i];
+  return warp_sum(v);
 }
 
-// The first token at which the running sum exceeds u times the total of sm.sums, whose parts are those of [0, V).
-template <int DT, int MODE>
-__device__ __forceinline__ long long search(Weights<DT, MODE>& f, double want, Smem& sm) {
+// The first token of [begin, end) at which the running sum exceeds `want`, by one CTA; gap: how far
+// `want` is from the nearer end of its weight.  -1: no weight in it.
+template <int DT, int MODE, bool kFine>
+__device__ __forceinline__ long long search(Weights<DT, MODE, kFine>& f, long long begin, long long end, double want, double& gap,
+                                            Smem& sm) {
   using F = Fmt<DT>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  long long begin = 0, end = f.V;
-  while (true) {
-    // the part that holds the border; past the last weight (a rounding), the last part that has any
-    const long long size = part_size(end - begin, kWarps, 32 * F::kVec);
-    double before = 0.0, last_before = 0.0;
-    int at = -1, last = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      const double s = sm.sums[w];
-      if (s > 0.0) {
-        last = w;
-        last_before = before;
-        if (before + s > want) {
-          at = w;
-          break;
-        }
-      }
-      before += s;
-    }
-    if (at < 0) {
-      at = last;
-      before = last_before;
-    }
+  constexpr int kStep = 32 * F::kVec;
+  while (end - begin > 2 * kStep) {
+    const long long size = part_size(end - begin, kWarps, kStep);
+    const long long lo = min(end, begin + warp * size), hi = min(end, lo + size);
+    const double s = part_sum<DT, MODE, kFine>(f, lo, hi, lane);
+    __syncthreads();
+    if (lane == 0) sm.sums[warp] = s;
+    __syncthreads();
+    double before;
+    const int at = max(0, find_part<MODE, kFine>(sm.sums, kWarps, want, before, lane));
     want -= before;
     begin = min(end, begin + at * size);
     end = min(end, begin + size);
-    if (end - begin <= 4 * 32 * F::kVec) break;
-    all_parts<DT, MODE>(f, begin, end, sm);
   }
   __syncthreads();
   if (warp == 0) {
     long long found = -1, last = -1;
-    for (long long base = begin; base < end && found < 0; base += 32 * F::kVec) {
+    double near = 0.0, last_near = 0.0;
+    for (long long base = begin; base < end && found < 0; base += kStep) {
       const long long i = base + lane * F::kVec;
-      Term w[F::kVec];
+      double x[F::kVec];
 #pragma unroll
-      for (int j = 0; j < F::kVec; ++j) w[j].a = w[j].b = w[j].c = 0.f;
-      if (i < end) f.at(i, end, w);
+      for (int j = 0; j < F::kVec; ++j) x[j] = 0.0;
+      if (i < end) f.exactly(i, end, x);
       double sum = 0.0;
 #pragma unroll
-      for (int j = 0; j < F::kVec; ++j) sum += w[j].value();
+      for (int j = 0; j < F::kVec; ++j) sum += x[j];
       double upto = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -273,35 +454,80 @@ __device__ __forceinline__ long long search(Weights<DT, MODE>& f, double want, S
       double run = __shfl_up_sync(0xffffffffu, upto, 1);
       if (lane == 0) run = 0.0;
       long long mine = -1, mine_last = -1;
+      double mine_near = 0.0;
 #pragma unroll
       for (int j = 0; j < F::kVec; ++j) {
-        const double x = w[j].value();
-        run += x;
-        if (x > 0.0) {
+        if (x[j] > 0.0) {
           mine_last = i + j;
-          if (mine < 0 && run > want) mine = i + j;
+          if (mine < 0 && run + x[j] > want) {
+            mine = i + j;
+            mine_near = fmin(want - run, run + x[j] - want);
+          }
         }
+        run += x[j];
       }
       const uint32_t who = __ballot_sync(0xffffffffu, mine >= 0);
-      if (who) found = __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
+      if (who) {
+        found = __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
+        near = __shfl_sync(0xffffffffu, mine_near, __ffs(who) - 1);
+      }
       const uint32_t some = __ballot_sync(0xffffffffu, mine_last >= 0);
       if (some) last = __shfl_sync(0xffffffffu, mine_last, 31 - __clz(some));
       want -= __shfl_sync(0xffffffffu, upto, 31);
     }
-    if (lane == 0) sm.found = found >= 0 ? found : last;
+    if (lane == 0) {
+      sm.found = found >= 0 ? found : last;
+      sm.gap = found >= 0 ? near : last_near;
+    }
   }
   __syncthreads();
+  gap = sm.gap;
   return sm.found;
 }
 
+// The parts' sums in fine arithmetic, told to the whole cluster (behind it: g.turn's place).
+template <int DT, int MODE>
+__device__ __forceinline__ void sum_parts(Weights<DT, MODE, true>& f, long long lo, long long hi, Group& g, Smem& sm) {
+  const int lane = threadIdx.x & 31, part = g.rank * kWarps + (threadIdx.x >> 5);
+  const double s = part_sum<DT, MODE, true>(f, lo, hi, lane);
+  g.turn ^= 1;
+  tell(g, &sm.ex[g.turn].sum[part], s, lane);
+  g.sync();
+}
+
+// From the parts' sums (in `sums`, the same in every CTA) to the token; the CTA that has the part
+// looks for it there and tells the others.
+template <int DT, int MODE, bool kFine>
+__device__ __forceinline__ long long draw(Weights<DT, MODE, kFine>& f, const double* sums, double want, double unsure, long long V,
+                                          long long size, Group& g, Smem& sm, bool& sure) {
+  const int lane = threadIdx.x & 31, parts = g.size * kWarps;
+  double before;
+  const int at = max(0, find_part<MODE, kFine>(sums, parts, want, before, lane));
+  Exchange& ex = sm.ex[g.turn ^ 1];
+  if (at / kWarps == g.rank) {
+    const long long lo = min(V, at * size), hi = min(V, lo + size);
+    double gap;
+    const long long t = search<DT, MODE, kFine>(f, lo, hi, want - before, gap, sm);
+    if (threadIdx.x < 32) {
+      tell(g, &ex.token, t, lane);
+      tell(g, &ex.unsure, static_cast<int>(!(gap > unsure)), lane);
+    }
+  }
+  g.turn ^= 1;
+  g.sync();
+  sure = !ex.unsure;
+  return ex.token;
+}
+
 template <int DT>
-__global__ void __launch_bounds__(kThreads)
-verify_drafts_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+verify_drafts_kernel(const Args a, int cluster) {
   using F = Fmt<DT>;
-  constexpr bool wide = DT == RL_F32;
   __shared__ Smem sm;
-  const long long b = blockIdx.x;
-  const int tid = threadIdx.x, G = a.G;
+  Group g{cluster, cluster > 1 ? static_cast<int>(cluster_rank()) : 0, 0u};
+  const long long b = blockIdx.x / cluster;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.G;
+  const bool writes = g.rank == 0 && tid == 0;
   const long long V = a.V, rows = static_cast<long long>(G) + 1;
   long long* tokens = a.tokens + b * rows;
   float* logp = a.logp ? a.logp + b * rows : nullptr;
@@ -316,30 +542,53 @@ verify_drafts_kernel(const Args a) {
   if (!wrong)
     for (int i = tid; i < n; i += kThreads) wrong = wrong || a.ids[b * G + i] < 0 || a.ids[b * G + i] >= V;
   wrong = __syncthreads_or(wrong);
-  if (wrong || n < 0) {
-    for (int i = tid; i <= G; i += kThreads) {
-      tokens[i] = -1;
-      if (logp) logp[i] = wrong ? nan : 0.f;
-      if (lse) lse[i] = wrong ? nan : 0.f;
-    }
-    if (tid == 0) {
-      if (a.n_accepted) a.n_accepted[b] = 0;
-      if (wrong && a.status) atomicOr(a.status, RL_DEVERR_ID_RANGE);
+  if (wrong || n < 0) {  // the same in every CTA of the cluster
+    if (g.rank == 0) {
+      for (int i = tid; i <= G; i += kThreads) {
+        tokens[i] = -1;
+        if (logp) logp[i] = wrong ? nan : 0.f;
+        if (lse) lse[i] = wrong ? nan : 0.f;
+      }
+      if (tid == 0) {
+        if (a.n_accepted) a.n_accepted[b] = 0;
+        if (wrong && a.status) atomicOr(a.status, RL_DEVERR_ID_RANGE);
+      }
     }
     return;
   }
+  if (cluster > 1) cluster_sync_all();  // every CTA runs before its shared memory is written
+
+  const int parts = cluster * kWarps, part = g.rank * kWarps + warp;
+  const long long size = part_size(V, parts, 32 * F::kVec);
+  const long long lo = min(V, part * size), hi = min(V, lo + size);
 
   FineExp fp;
   int kept = 0;
   Stats st;
-  bool lost = false, bad = false;
+  bool lost = false, bad = false, exact = false;
   const unsigned char* row = nullptr;
+#pragma unroll 1
   for (int i = 0;; ++i) {
     row = a.target + (b * rows + i) * a.row_bytes;
-    st = row_stats<DT>(row, V, a.c, sm);
+    Stats mine = part_stats<DT>(row, lo, hi, a.c, lane);
+    exact = false;
+#pragma unroll 1
+    while (true) {
+      g.turn ^= 1;
+      tell(g, &sm.ex[g.turn].stats[part], mine, lane);
+      g.sync();
+      st = Stats{-FLT_MAX, 0.f, 0.f};
+      for (int k = lane; k < parts; k += 32) st = merged(st, sm.ex[g.turn].stats[k], a.c);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        st = merged(st, Stats{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.n, o), __shfl_xor_sync(0xffffffffu, st.s, o)}, a.c);
+      if (exact || !needs_exact<F>(st.m, a.c) || st.m != st.m) break;
+      exact = true;
+      mine = part_stats_exact<DT>(row, lo, hi, a.c, lane);
+    }
     bad = !(fabsf(st.m) < INFINITY) || !(st.n > 0.f);
     fp.init(a.c_d, st.m, 0.0);
-    if (tid == 0 && lse) lse[i] = bad ? nan : static_cast<float>(static_cast<double>(st.m) * a.inv_t + log1pf((st.n - 1.f) + st.s));
+    if (writes && lse) lse[i] = bad ? nan : static_cast<float>(static_cast<double>(st.m) * a.inv_t + log1pf((st.n - 1.f) + st.s));
     if (bad || i == n) break;
     if (tid == 0) {
       const long long d = a.ids[b * G + i];
@@ -351,18 +600,19 @@ verify_drafts_kernel(const Args a) {
         if (!(zq < INFINITY) || !(fabsf(lq) < INFINITY)) v = kNoDistribution;
         qd = exp(static_cast<double>(zq) * a.inv_t - static_cast<double>(lq));
       }
-      const Term w = fp.template at<wide>(zd, sm.T, sm.delta);
+      const double w = fp.is_zero(zd) ? 0.0 : fp.template at<DT == RL_F32, false>(zd, sm.T, sm.delta).value();
       const double total = static_cast<double>(st.n) + static_cast<double>(st.s);
-      if (v == kStays && !(a.u[b * rows + i] * qd * total < w.value())) v = kRefused;
-      if (v == kStays) {
+      if (v == kStays && !(a.u[b * rows + i] * qd * total < w)) v = kRefused;
+      if (v == kStays && writes) {
         tokens[i] = d;
         if (logp) logp[i] = log_prob(zd, st, a.inv_t);
       }
       sm.verdict = v;
     }
     __syncthreads();
-    lost = sm.verdict == kRefused;
-    bad = sm.verdict == kNoDistribution;
+    const int v = sm.verdict;
+    lost = v == kRefused;
+    bad = v == kNoDistribution;
     if (lost || bad) break;
     kept = i + 1;
   }
@@ -371,51 +621,186 @@ verify_drafts_kernel(const Args a) {
   if (!bad) {
     double u = a.u[b * rows + G];
     u = u > 0.0 ? fmin(u, 1.0 - 0x1p-53) : 0.0;
-    bool own = !lost;
-    if (lost && !a.draft) {
-      Weights<DT, kWithout> f{row, nullptr, V, a.ids[b * G + kept], fp, fp, sm.T, sm.delta, false};
-      const double total = all_parts(f, 0, V, sm);
-      if (total > 0.0)
-        token = search(f, u * total, sm);
-      else
-        own = true;
-    }
-    if (own || a.draft) {
-      Weights<DT, kSoftmax> f{row, nullptr, V, -1, fp, fp, sm.T, sm.delta, false};
-      double total = all_parts(f, 0, V, sm);
-      if (lost && a.draft) {
-        // S q_v = 2^(z c - k), k = lse_q log2(e) - log2 S, in the frame of a number with few digits
+    const double S = static_cast<double>(st.n) + static_cast<double>(st.s);
+    const unsigned char* draft_row = a.draft ? a.draft + (b * G + kept) * a.draft_bytes : nullptr;
+    bool done = false;
+    if (lost && a.draft) {
+      // S q_v = 2^(z c - k), k = lse_q log2(e) - log2 S, in the frame of a number with few digits
+      const double lq = static_cast<double>(a.draft_lse[b * G + kept]) * kLog2eD;
+      Weights<DT, kRest, true> f{row, draft_row, -1, 0.f, 0.f, fp, fp, sm.T, sm.delta, false};
+      double total = S;
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
         if (tid == 0) sm.log2_total = log2(total);
         __syncthreads();
-        const double k = static_cast<double>(a.draft_lse[b * G + kept]) * kLog2eD - sm.log2_total;
-        const double near = rint(k / a.c_d * 4096.0) / 4096.0;
-        const float mq = static_cast<float>(near);
-        FineExp fq;
-        fq.init(a.c_d, mq, k - static_cast<double>(mq) * a.c_d);
-        Weights<DT, kRest> r{row, a.draft + (b * G + kept) * a.draft_bytes, V, -1, fp, fq, sm.T, sm.delta, false};
-        const double rest = all_parts(r, 0, V, sm);
-        bad = __syncthreads_or(r.bad);
-        if (!bad && rest > 0.0)
-          token = search(r, u * rest, sm);
-        else
-          own = !bad;
-        if (own) total = all_parts(f, 0, V, sm);
+        const double k = lq - sm.log2_total;
+        const float mq = static_cast<float>(rint(k / a.c_d * 4096.0) / 4096.0);
+        f.q.init(a.c_d, mq, k - static_cast<double>(mq) * a.c_d);
+        if (pass == 1) break;
+        // sums over all tokens, and of both sides over those with p > q
+        double all = 0.0, plus = 0.0, neg = 0.0;
+        FineSum fa, fb, fc;
+        fa.clear();
+        fb.clear();
+        fc.clear();
+        int count = 0;
+#pragma unroll 1
+        for (long long i = lo + lane * F::kVec; i < hi; i += 32 * F::kVec) {
+          float z[F::kVec], y[F::kVec];
+          F::unpack(load_vec<DT>(row, i, hi), z);
+          F::unpack(load_vec<DT>(draft_row, i, hi), y);
+#pragma unroll
+          for (int j = 0; j < F::kVec; ++j) {
+            bad = bad || !(y[j] < INFINITY);
+            const Term w = f.fine(z[j]), q = f.drafted(y[j]), d = minus(w, q);
+            const bool more = d.a + d.b + d.c > 0.f;
+            fa.add(w);
+            if (more) {
+              fb.add(w);
+              fc.add(q);
+            }
+          }
+          if (++count == 32) {
+            all += fa.value();
+            plus += fb.value();
+            neg += fc.value();
+            fa.clear();
+            fb.clear();
+            fc.clear();
+            count = 0;
+          }
+        }
+        all = warp_sum(all + fa.value());
+        plus = warp_sum(plus + fb.value());
+        neg = warp_sum(neg + fc.value());
+        bad = __any_sync(0xffffffffu, bad);
+        g.turn ^= 1;
+        Exchange& ex = sm.ex[g.turn];
+        tell(g, &ex.sum[part], bad ? -1.0 : all, lane);
+        tell(g, &ex.plus[part], plus, lane);
+        tell(g, &ex.minus[part], neg, lane);
+        g.sync();
+        bad = false;
+        for (int k2 = lane; k2 < parts; k2 += 32) bad = bad || ex.sum[k2] < 0.0;
+        bad = __any_sync(0xffffffffu, bad);
+        total = total_of(ex.sum, parts, lane);
+        if (bad) break;
       }
-      if (own) token = search(f, u * total, sm);
+      if (!bad) {
+        Exchange& ex = sm.ex[g.turn];
+        const double ratio = total / S;  // q's terms were taken with S, and belong to `total`
+        __syncthreads();
+        if (tid < parts) ex.plus[tid] = fmax(0.0, ex.plus[tid] - ratio * ex.minus[tid]);
+        __syncthreads();
+        const double rest = total_of(ex.plus, parts, lane);
+        if (rest > 0.0) {
+          bool sure;
+          token = draw<DT, kRest, true>(f, ex.plus, u * rest, -1.0, V, size, g, sm, sure);
+          done = token >= 0;
+        }
+      }
+    } else {
+      // the parts' sums of step 1 in the row's frame, without the draft that was looked up
+      const bool without = lost;
+      const long long d = without ? a.ids[b * G + kept] : -1;
+      if (!exact) {
+        const Exchange& ex = sm.ex[g.turn];
+        const float nm = -st.m * a.c, back = ex2_approx(fmaf(-st.m, a.c, -nm));
+        __syncthreads();
+        double* sums = sm.ex[g.turn].sum;
+        if (tid < parts) {
+          const Stats s = ex.stats[tid];
+          double x = (static_cast<double>(s.n) + static_cast<double>(s.s)) * static_cast<double>(ex2_approx((s.m - st.m) * a.c));
+          // (the search's terms are in the frame nm)
+          if (without && d >= tid * size && d < (tid + 1) * size) x = fmax(0.0, x - static_cast<double>(ex2_approx(fmaf(F::load(row, d), a.c, nm)) * back));
+          sums[tid] = x / static_cast<double>(back);
+        }
+        __syncthreads();
+        const double total = total_of(sums, parts, lane);
+        bool sure;
+        long long t;
+        if (without) {
+          Weights<DT, kWithout, false> f{row, nullptr, d, a.c, nm, fp, fp, sm.T, sm.delta, false};
+          t = draw<DT, kWithout, false>(f, sums, u * total, kCoarse * S, V, size, g, sm, sure);
+        } else {
+          Weights<DT, kSoftmax, false> f{row, nullptr, -1, a.c, nm, fp, fp, sm.T, sm.delta, false};
+          t = draw<DT, kSoftmax, false>(f, sums, u * total, kCoarse * S, V, size, g, sm, sure);
+        }
+        if (sure && t >= 0) {
+          token = t;
+          done = true;
+        }
+      }
+      if (!done && without) {
+        Weights<DT, kWithout, true> f{row, nullptr, d, 0.f, 0.f, fp, fp, sm.T, sm.delta, false};
+        sum_parts(f, lo, hi, g, sm);
+        const double* sums = sm.ex[g.turn].sum;
+        const double total = total_of(sums, parts, lane);
+        if (total > kNothing) {
+          bool sure;
+          token = draw<DT, kWithout, true>(f, sums, u * total, -1.0, V, size, g, sm, sure);
+          done = token >= 0;
+        }
+      }
+    }
+    if (!done && !bad) {
+      Weights<DT, kSoftmax, true> f{row, nullptr, -1, 0.f, 0.f, fp, fp, sm.T, sm.delta, false};
+      sum_parts(f, lo, hi, g, sm);
+      const double* sums = sm.ex[g.turn].sum;
+      bool sure;
+      token = draw<DT, kSoftmax, true>(f, sums, u * total_of(sums, parts, lane), -1.0, V, size, g, sm, sure);
+    }
+    bad = bad || token < 0;
+  }
+  if (g.rank == 0) {
+    for (int i = tid; i <= G; i += kThreads) {
+      if (i > kept) {
+        tokens[i] = -1;
+        if (logp) logp[i] = 0.f;
+        if (lse) lse[i] = 0.f;
+      }
+    }
+    if (tid == 0) {
+      if (a.n_accepted) a.n_accepted[b] = kept;
+      tokens[kept] = bad ? -1 : token;
+      if (logp) logp[kept] = bad ? nan : log_prob(F::load(row, token), st, a.inv_t);
     }
   }
-  for (int i = tid; i <= G; i += kThreads) {
-    if (i > kept) {
-      tokens[i] = -1;
-      if (logp) logp[i] = 0.f;
-      if (lse) lse[i] = 0.f;
-    }
+  if (cluster > 1) cluster_sync_all();  // nobody leaves while its shared memory may be written
+}
+
+// CTAs of a cluster: as many as fit at once, at most 16 (8 without the attribute that allows
+// more), and no more than leave a warp 256 elements.
+int cluster_for(long long B, long long V, int sms) {
+  const long long slots = static_cast<long long>(sms) * kCtasPerSm;
+  const long long most = (V + 256 * kWarps - 1) / (256 * kWarps);
+  long long c = slots / B;
+  if (c > kMaxCluster) c = kMaxCluster;
+  if (c > 8) c = c >= kMaxCluster ? kMaxCluster : 8;
+  if (c > most) c = most;
+  return static_cast<int>(c < 1 ? 1 : c);
+}
+
+template <int DT>
+rl_status launch(const Args& a, long long B, int cluster, int dev, cudaStream_t stream) {
+  static std::atomic<unsigned long long> allowed{0};
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (cluster > 8 && !(allowed.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(verify_drafts_kernel<DT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return RL_ERR_CUDA;
+    allowed.fetch_or(bit, std::memory_order_release);
   }
-  if (tid == 0) {
-    if (a.n_accepted) a.n_accepted[b] = kept;
-    tokens[kept] = bad ? -1 : token;
-    if (logp) logp[kept] = bad ? nan : log_prob(F::load(row, token), st, a.inv_t);
-  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(B * cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<DT>, a, cluster) == cudaSuccess ? RL_OK : RL_ERR_CUDA;
 }
 
 }  // namespace
@@ -446,6 +831,9 @@ extern "C" rl_status rl_verify_drafts(const rl_verify_drafts_desc* desc, void* s
       off(d.uniforms, 8) || off(d.tokens, 8) || off(d.n_accepted, 8) || off(d.draft_ids, 8) || off(d.draft_lse, 4) ||
       off(d.n_draft, 4) || off(d.logp_out, 4) || off(d.lse_out, 4) || off(d.status_dev, 4))
     return RL_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return RL_ERR_CUDA;
   Args a;
   a.target = static_cast<const unsigned char*>(d.target_logits);
   a.draft = d.G > 0 ? static_cast<const unsigned char*>(d.draft_logits) : nullptr;
@@ -465,13 +853,9 @@ extern "C" rl_status rl_verify_drafts(const rl_verify_drafts_desc* desc, void* s
   a.logp = d.logp_out;
   a.lse = d.lse_out;
   a.status = d.status_dev;
-  const unsigned grid = static_cast<unsigned>(d.B);
+  const int cluster = cluster_for(d.B, d.V, sms);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d.dtype == RL_F32)
-    verify_drafts_kernel<RL_F32><<<grid, kThreads, 0, s>>>(a);
-  else if (d.dtype == RL_BF16)
-    verify_drafts_kernel<RL_BF16><<<grid, kThreads, 0, s>>>(a);
-  else
-    verify_drafts_kernel<RL_F16><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? RL_OK : RL_ERR_CUDA;
+  if (d.dtype == RL_F32) return launch<RL_F32>(a, d.B, cluster, dev, s);
+  if (d.dtype == RL_BF16) return launch<RL_BF16>(a, d.B, cluster, dev, s);
+  return launch<RL_F16>(a, d.B, cluster, dev, s);
 }
