@@ -53,7 +53,7 @@ struct Args {
   long long V, row_bytes, draft_bytes;
   int G;
   float c;       // log2(e) / temperature
-  double c_d, inv_t;
+  double c_d, inv_t, t_ln2;  // log2(e) / temperature, 1 / temperature, temperature ln 2
   long long* tokens;
   long long* n_accepted;
   float* logp;
@@ -95,7 +95,9 @@ struct Exchange {
   long long token;
   int bad, unsure;
 };
+constexpr int kSlots = 4, kChunkBytes = 2048;  // of a warp's ring
 struct Smem {
+  unsigned long long full[kWarps][kSlots];
   float T[kPow], delta[kPow];
   Exchange ex[2];
   double sums[kWarps];   // of the search
@@ -166,28 +168,91 @@ __device__ __forceinline__ long long part_size(long long length, int n, int step
   return ((length + n - 1) / n + step - 1) / step * step;
 }
 
-// A warp's statistics of elements [lo, hi) of a row, in every lane.
+// The chunks of a warp's part of the rows, in the order of the rows: bulk copies into a ring
+// of its own in shared memory.  They run ahead of the warp, into the next row too
+// before it is known whether that is needed, so that a row's end costs no waiting for memory.
 template <int DT>
-__device__ __forceinline__ Stats part_stats(const unsigned char* row, long long lo, long long hi, float c, int lane) {
-  using F = Fmt<DT>;
-  constexpr int kStep = 32 * F::kVec;
-  float m = F::kFloor, nm = -F::kFloor * c;
-  float n = 0.f, s = 0.f, err = 0.f;
-  uint4 next[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) next[j] = load_vec<DT>(row, lo + j * kStep + lane * F::kVec, hi);
-#pragma unroll 1
-  for (long long base = lo; base < hi; base += 4 * kStep) {
-    uint32_t w[16];
+struct Stream {
+  static constexpr int kElems = kChunkBytes / Fmt<DT>::kBytes;
+  const unsigned char* next;  // row of the next copy, from the part's first element on
+  long long row_bytes, length, at;  // bytes to the next row; elements of the part, and of them copied
+  int rows;                   // rows left to copy
+  uint32_t data, bars, issued, taken;
+  uint64_t policy;
+
+  __device__ __forceinline__ void init(const unsigned char* row, long long row_bytes_, int rows_, long long lo, long long hi,
+                                       uint32_t data_, uint32_t bars_, int lane) {
+    next = row + lo * Fmt<DT>::kBytes;
+    row_bytes = row_bytes_;
+    length = hi - lo;
+    at = 0;
+    rows = length > 0 ? rows_ : 0;
+    data = data_;
+    bars = bars_;
+    issued = taken = 0;
+    policy = policy_normal();
+    for (int j = 0; j < kSlots - 1; ++j) copy(lane);
+  }
+  __device__ __forceinline__ void copy(int lane) {
+    if (rows == 0) return;
+    const uint32_t slot = issued % kSlots;
+    if (lane == 0) {
+      const long long left = (length - at) * Fmt<DT>::kBytes;  // (the stride is a multiple of 16)
+      const uint32_t bytes = left >= kChunkBytes ? kChunkBytes : static_cast<uint32_t>((left + 15) & ~15LL);
+      mbar_arrive_expect_tx(bars + 8 * slot, bytes);
+      bulk_load(data + slot * kChunkBytes, next + at * Fmt<DT>::kBytes, bytes, bars + 8 * slot, policy);
+    }
+    ++issued;
+    at += kElems;
+    if (at >= length) {
+      at = 0;
+      next += row_bytes;
+      --rows;
+    }
+  }
+  // The next chunk's words of this lane; its vectors are j 32 kVec + lane kVec elements from the
+  // chunk's begin, of which `left` belong to the part.  false: a wait gave up.
+  __device__ __forceinline__ bool take(uint32_t (&w)[16], long long left, int lane, volatile int* abort) {
+    __syncwarp();  // the slot before is read
+    copy(lane);
+    const uint32_t slot = taken % kSlots;
+    const bool ok = __all_sync(0xffffffffu, wait_bounded<false>(bars + 8 * slot, (taken / kSlots) & 1, abort));
+    ++taken;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      w[4 * j] = next[j].x;
-      w[4 * j + 1] = next[j].y;
-      w[4 * j + 2] = next[j].z;
-      w[4 * j + 3] = next[j].w;
+      uint4 v = ld_shared_v4(data + slot * kChunkBytes + j * 512 + lane * 16);
+      if (left < kElems) {
+        const int i = (j * 32 + lane) * Fmt<DT>::kVec;
+        if (i + Fmt<DT>::kVec > left) cut_vec<DT>(v, i, left);
+      }
+      w[4 * j] = v.x;
+      w[4 * j + 1] = v.y;
+      w[4 * j + 2] = v.z;
+      w[4 * j + 3] = v.w;
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) next[j] = load_vec<DT>(row, base + (4 + j) * kStep + lane * F::kVec, hi);
+    return ok;
+  }
+  // copies still on their way land before the CTA can exit
+  __device__ __forceinline__ void drain(volatile int* abort) {
+    for (; taken < issued; ++taken) {
+      const uint64_t t0 = global_ns();
+      while (!mbar_try_wait(bars + 8 * (taken % kSlots), (taken / kSlots) & 1) && global_ns() - t0 <= kWaitLimitNs) {
+      }
+    }
+  }
+};
+
+// A warp's statistics of its part of the stream's next row, in every lane.
+template <int DT>
+__device__ __forceinline__ Stats part_stats(Stream<DT>& in, float c, int lane, volatile int* abort) {
+  using F = Fmt<DT>;
+  float m = F::kFloor, nm = -F::kFloor * c;
+  float n = 0.f, s = 0.f, err = 0.f;
+  bool ok = true;
+#pragma unroll 1
+  for (long long left = in.length; left > 0; left -= Stream<DT>::kElems) {
+    uint32_t w[16];
+    ok = in.take(w, left, lane, abort) && ok;
     float wm;
     {
       const float pm = max_nan(F::raw_value(F::raw_max(w, 0)), F::kFloor);
@@ -229,7 +294,7 @@ __device__ __forceinline__ Stats part_stats(const unsigned char* row, long long 
     s += __shfl_xor_sync(0xffffffffu, s, o);
     n += __shfl_xor_sync(0xffffffffu, n, o);
   }
-  return Stats{m, n, s};
+  return Stats{ok ? m : __int_as_float(0x7fc00000), n, s};  // a wait that gave up: no distribution
 }
 
 // The same by differences to the maximum, without a floor: rows of very large
@@ -271,6 +336,18 @@ __device__ __noinline__ Stats part_stats_exact(const unsigned char* row, long lo
 // log p of logit z of a row.
 __device__ __forceinline__ float log_prob(float z, const Stats& st, double inv_t) {
   return static_cast<float>((static_cast<double>(z) - static_cast<double>(st.m)) * inv_t - log1pf((st.n - 1.f) + st.s));
+}
+
+// q = e^(z / temperature - lse) (fp64's own exponential is some hundred dependent steps of a
+// unit with a 64th of fp32's rate, and everybody waits for this one number).
+template <int DT>
+__device__ __forceinline__ double draft_prob(float z, float lse, const Args& a, const float* T, const float* delta) {
+  const double k = static_cast<double>(lse) * kLog2eD, m = rint(k * a.t_ln2 * 4096.0) * (1.0 / 4096.0);
+  const double x = static_cast<double>(z) * a.c_d - k;
+  if (!(x > -120.0 && x < 1.5 && fabs(m) < 4096.0)) return exp(static_cast<double>(z) * a.inv_t - static_cast<double>(lse));
+  FineExp q;
+  q.init(a.c_d, static_cast<float>(m), k - m * a.c_d);
+  return q.template at<true, false>(z, T, delta).value();
 }
 
 template <int DT, int MODE, bool kFine>
@@ -523,7 +600,10 @@ template <int DT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 verify_drafts_kernel(const Args a, int cluster) {
   using F = Fmt<DT>;
+  extern __shared__ __align__(16) unsigned char ring[];
   __shared__ Smem sm;
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
   Group g{cluster, cluster > 1 ? static_cast<int>(cluster_rank()) : 0, 0u};
   const long long b = blockIdx.x / cluster;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.G;
@@ -537,6 +617,9 @@ verify_drafts_kernel(const Args a, int cluster) {
     sm.T[tid] = kPowT[tid];
     sm.delta[tid] = kPowD[tid];
   }
+  if (tid < kWarps * kSlots) mbar_init(smem_addr(&sm.full[0][0]) + 8 * tid, 1);
+  if (tid == 0) abort_word = 0;
+  fence_mbar_init();
   const int n = a.n_draft ? a.n_draft[b] : G;
   bool wrong = n < -1 || n > G;
   if (!wrong)
@@ -562,15 +645,32 @@ verify_drafts_kernel(const Args a, int cluster) {
   const long long size = part_size(V, parts, 32 * F::kVec);
   const long long lo = min(V, part * size), hi = min(V, lo + size);
 
+  Stream<DT> in;
+  in.init(a.target + b * rows * a.row_bytes, a.row_bytes, n + 1, lo, hi, smem_addr(ring) + warp * kSlots * kChunkBytes,
+          smem_addr(&sm.full[warp][0]), lane);
   FineExp fp;
   int kept = 0;
+  // what thread 0 needs of a row's draft, on its way while the row is summed
+  long long d = 0, d_next = tid == 0 && n > 0 ? a.ids[b * G] : 0;
   Stats st;
   bool lost = false, bad = false, exact = false;
   const unsigned char* row = nullptr;
 #pragma unroll 1
   for (int i = 0;; ++i) {
     row = a.target + (b * rows + i) * a.row_bytes;
-    Stats mine = part_stats<DT>(row, lo, hi, a.c, lane);
+    float zd = 0.f, zq = 0.f, lq = 0.f;
+    double ui = 0.0;
+    if (tid == 0 && i < n) {
+      d = d_next;
+      if (i + 1 < n) d_next = a.ids[b * G + i + 1];
+      zd = F::load(row, d);
+      ui = a.u[b * rows + i];
+      if (a.draft) {
+        zq = F::load(a.draft + (b * G + i) * a.draft_bytes, d);
+        lq = a.draft_lse[b * G + i];
+      }
+    }
+    Stats mine = part_stats<DT>(in, a.c, lane, abort_flag);
     exact = false;
 #pragma unroll 1
     while (true) {
@@ -591,18 +691,15 @@ verify_drafts_kernel(const Args a, int cluster) {
     if (writes && lse) lse[i] = bad ? nan : static_cast<float>(static_cast<double>(st.m) * a.inv_t + log1pf((st.n - 1.f) + st.s));
     if (bad || i == n) break;
     if (tid == 0) {
-      const long long d = a.ids[b * G + i];
-      const float zd = F::load(row, d);
       int v = kStays;
       double qd = 1.0;
       if (a.draft) {
-        const float zq = F::load(a.draft + (b * G + i) * a.draft_bytes, d), lq = a.draft_lse[b * G + i];
         if (!(zq < INFINITY) || !(fabsf(lq) < INFINITY)) v = kNoDistribution;
-        qd = exp(static_cast<double>(zq) * a.inv_t - static_cast<double>(lq));
+        qd = draft_prob<DT>(zq, lq, a, sm.T, sm.delta);
       }
       const double w = fp.is_zero(zd) ? 0.0 : fp.template at<DT == RL_F32, false>(zd, sm.T, sm.delta).value();
       const double total = static_cast<double>(st.n) + static_cast<double>(st.s);
-      if (v == kStays && !(a.u[b * rows + i] * qd * total < w)) v = kRefused;
+      if (v == kStays && !(ui * qd * total < w)) v = kRefused;
       if (v == kStays && writes) {
         tokens[i] = d;
         if (logp) logp[i] = log_prob(zd, st, a.inv_t);
@@ -634,7 +731,7 @@ verify_drafts_kernel(const Args a, int cluster) {
         if (tid == 0) sm.log2_total = log2(total);
         __syncthreads();
         const double k = lq - sm.log2_total;
-        const float mq = static_cast<float>(rint(k / a.c_d * 4096.0) / 4096.0);
+        const float mq = static_cast<float>(rint(k * a.t_ln2 * 4096.0) * (1.0 / 4096.0));
         f.q.init(a.c_d, mq, k - static_cast<double>(mq) * a.c_d);
         if (pass == 1) break;
         // sums over all tokens, and of both sides over those with p > q
@@ -752,6 +849,8 @@ verify_drafts_kernel(const Args a, int cluster) {
     }
     bad = bad || token < 0;
   }
+  in.drain(abort_flag);
+  if (*abort_flag && lane == 0 && a.status) atomicOr(a.status, RL_DEVERR_TIMEOUT);
   if (g.rank == 0) {
     for (int i = tid; i <= G; i += kThreads) {
       if (i > kept) {
@@ -785,14 +884,17 @@ template <int DT>
 rl_status launch(const Args& a, long long B, int cluster, int dev, cudaStream_t stream) {
   static std::atomic<unsigned long long> allowed{0};
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  if (cluster > 8 && !(allowed.load(std::memory_order_acquire) & bit)) {
-    if (cudaFuncSetAttribute(verify_drafts_kernel<DT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+  if (!(allowed.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(verify_drafts_kernel<DT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaFuncSetAttribute(verify_drafts_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * kSlots * kChunkBytes) !=
+            cudaSuccess)
       return RL_ERR_CUDA;
     allowed.fetch_or(bit, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(B * cluster));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kWarps * kSlots * kChunkBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -847,6 +949,7 @@ extern "C" rl_status rl_verify_drafts(const rl_verify_drafts_desc* desc, void* s
   a.G = static_cast<int>(d.G);
   a.inv_t = 1.0 / d.temperature;
   a.c_d = kLog2eD / d.temperature;
+  a.t_ln2 = d.temperature * 0.69314718055994530942;
   a.c = static_cast<float>(a.c_d);
   a.tokens = d.tokens;
   a.n_accepted = d.n_accepted;
