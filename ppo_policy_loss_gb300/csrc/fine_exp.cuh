@@ -61,14 +61,13 @@ __device__ __forceinline__ float quick_two_sum(float x, float y, float& err) {
 struct FineExp {
   float m, c_hi, c_lo, kappa, dmin, dmax;
 
-  // c: log2(e) / temperature.  The frame: the terms are 2^(z c - k), kappa = k - m c.
-  __device__ __forceinline__ void init(double c, float m_, double kappa_) {
-    c_hi = static_cast<float>(c);
-    c_lo = static_cast<float>(c - static_cast<double>(c_hi));
+  // c: log2(e) / temperature, as two floats.  The frame: the terms are 2^(z c - k), kappa = k - m c.
+  __device__ __forceinline__ void init(float c_hi_, float c_lo_, float unit, float m_, float kappa_) {
+    c_hi = c_hi_;
+    c_lo = c_lo_;
     m = m_;
-    kappa = static_cast<float>(kappa_);
-    const float unit = 1.f / c_hi;
-    dmin = -124.f * unit;
+    kappa = kappa_;
+    dmin = -124.f * unit;  // unit: 1 / c
     dmax = 2.f * unit;
   }
   // kWide: z has 24 significant bits (16-bit numbers have 8 or 11).  kTop: z - m may be above dmax.

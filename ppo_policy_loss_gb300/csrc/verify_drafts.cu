@@ -22,7 +22,9 @@
 // fp32 sums, in units of 2^-24: a term 2^x carries 4 of the hardware exponential and 2 ln 2 |x|
 // of its argument (the FMA's rounding and c's), |x| weighted by p at most log2 V < 18 for 2^18
 // tokens; 32 terms are added in chains of 10, the chains' sums with their errors kept; then
-// 5 joins in the warp and 13 for the frames of lanes and warps: 57, and the same for S.
+// 5 joins in the warp, 13 for the frames of lanes and warps, and 15 in the running sums of the
+// search: 72, and the same for S.  (fp64 is kept for what a single lane decides: the unit does
+// two operations a cycle and SM, and a warp that adds in fp64 holds it for 16 cycles.)
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -40,7 +42,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 3;
 constexpr int kMaxCluster = 16, kMaxParts = kMaxCluster * kWarps;
 constexpr double kLog2eD = 1.4426950408889634074;
-constexpr double kCoarse = 0x1p-17;   // two sums of 57 2^-24 each, rounded up
+constexpr float kCoarse = 0x1.4p-17f;  // two sums of 72 2^-24 each, rounded up
 constexpr double kNothing = 0x1p-90;  // sums of weights that are 0 (2^-124 each) stay below
 
 struct Args {
@@ -52,7 +54,7 @@ struct Args {
   const double* u;
   long long V, row_bytes, draft_bytes;
   int G;
-  float c;       // log2(e) / temperature
+  float c, c_lo, unit;       // log2(e) / temperature as two floats, and its reciprocal
   double c_d, inv_t, t_ln2;  // log2(e) / temperature, 1 / temperature, temperature ln 2
   long long* tokens;
   long long* n_accepted;
@@ -93,7 +95,7 @@ struct Exchange {
   Stats stats[kMaxParts];
   double sum[kMaxParts], plus[kMaxParts], minus[kMaxParts];
   long long token;
-  int bad, unsure;
+  int unsure;
 };
 constexpr int kSlots = 4, kChunkBytes = 2048;  // of a warp's ring
 struct Smem {
@@ -101,9 +103,11 @@ struct Smem {
   float T[kPow], delta[kPow];
   Exchange ex[2];
   double sums[kWarps];   // of the search
-  double log2_total, gap;
+  float coarse[kWarps];
+  double before, total;
+  float gap;
   long long found;
-  int verdict;
+  int verdict, at;
 };
 
 // ------------------------------------------------------------------ the cluster
@@ -346,7 +350,7 @@ __device__ __forceinline__ double draft_prob(float z, float lse, const Args& a, 
   const double x = static_cast<double>(z) * a.c_d - k;
   if (!(x > -120.0 && x < 1.5 && fabs(m) < 4096.0)) return exp(static_cast<double>(z) * a.inv_t - static_cast<double>(lse));
   FineExp q;
-  q.init(a.c_d, static_cast<float>(m), k - m * a.c_d);
+  q.init(a.c, a.c_lo, a.unit, static_cast<float>(m), static_cast<float>(k - m * a.c_d));
   return q.template at<true, false>(z, T, delta).value();
 }
 
@@ -390,30 +394,36 @@ struct Weights {
       }
     }
   }
-  // the same, 0 where a token cannot occur
-  __device__ __forceinline__ void exactly(long long i, long long end, double (&x)[Fmt<DT>::kVec]) {
+  // the same as numbers, 0 where a token cannot occur
+  template <class N>
+  __device__ __forceinline__ void exactly(long long i, long long end, N (&x)[Fmt<DT>::kVec]) {
     using F = Fmt<DT>;
     float z[F::kVec];
     Term w[F::kVec];
     logits(i, end, z);
     at(i, end, w);
 #pragma unroll
-    for (int j = 0; j < F::kVec; ++j) x[j] = kFine && p.is_zero(z[j]) ? 0.0 : w[j].value();
+    for (int j = 0; j < F::kVec; ++j) {
+      if constexpr (kFine)
+        x[j] = p.is_zero(z[j]) ? 0.0 : w[j].value();
+      else
+        x[j] = w[j].a;
+    }
   }
 };
 
-__device__ __forceinline__ double warp_sum(double v) {
+template <class N>
+__device__ __forceinline__ N warp_sum(N v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// The warp's sum over [lo, hi), whole vectors from lo.
-template <int DT, int MODE, bool kFine>
-__device__ __forceinline__ double part_sum(Weights<DT, MODE, kFine>& f, long long lo, long long hi, int lane) {
+// The warp's sum over [lo, hi) in fine arithmetic, whole vectors from lo.
+template <int DT, int MODE>
+__device__ __forceinline__ double part_sum(Weights<DT, MODE, true>& f, long long lo, long long hi, int lane) {
   using F = Fmt<DT>;
   double total = 0.0;
-  float plain = 0.f;
   FineSum s;
   s.clear();
   int n = 0;
@@ -421,54 +431,56 @@ __device__ __forceinline__ double part_sum(Weights<DT, MODE, kFine>& f, long lon
   for (long long i = lo + lane * F::kVec; i < hi; i += 32 * F::kVec) {
     Term w[F::kVec];
     f.at(i, hi, w);
-    if (kFine) {
 #pragma unroll
-      for (int j = 0; j < F::kVec; ++j) s.add(w[j]);
-      if (++n == 64) {
-        total += s.value();
-        s.clear();
-        n = 0;
-      }
-    } else {
-#pragma unroll
-      for (int j = 1; j < F::kVec; ++j) w[0].a += w[j].a;
-      plain += w[0].a;
-      if (++n == 4) {
-        total += static_cast<double>(plain);
-        plain = 0.f;
-        n = 0;
-      }
+    for (int j = 0; j < F::kVec; ++j) s.add(w[j]);
+    if (++n == 64) {
+      total += s.value();
+      s.clear();
+      n = 0;
     }
   }
-  return warp_sum(total + (kFine ? s.value() : static_cast<double>(plain)));
+  return warp_sum(total + s.value());
+}
+// The same in fp32.
+template <int DT, int MODE>
+__device__ __forceinline__ float part_sum(Weights<DT, MODE, false>& f, long long lo, long long hi, int lane) {
+  using F = Fmt<DT>;
+  float total = 0.f, err = 0.f;
+#pragma unroll 2
+  for (long long i = lo + lane * F::kVec; i < hi; i += 32 * F::kVec) {
+    Term w[F::kVec];
+    f.at(i, hi, w);
+#pragma unroll
+    for (int j = 1; j < F::kVec; ++j) w[0].a += w[j].a;
+    float lost;
+    total = two_sum(total, w[0].a, lost);
+    err += lost;
+  }
+  return warp_sum(total + err);
 }
 
-// Of n <= kMaxParts sums: the one in which the running sum exceeds `want` and what is before it
-// (past the last weight, a rounding: the last part that has any).  Whole warp.
-template <int MODE, bool kFine>
-__device__ __forceinline__ int find_part(const double* sums, int n, double want, double& before, int lane) {
-  constexpr double none = kFine && MODE != kRest ? kNothing : 0.0;
-  double v[kMaxParts / 32], own = 0.0;
+// Of the lanes' kPer sums each, in order: the one in which the running sum exceeds `want` and
+// what is before it (past the last weight, a rounding: the last one that has any; -1: none has).
+// `none`: what a sum of nothing stays below.  Whole warp.
+template <class N, int kPer>
+__device__ __forceinline__ int find_part(const N (&v)[kPer], N want, N none, N& before, int lane) {
+  N own = v[0];
 #pragma unroll
-  for (int j = 0; j < kMaxParts / 32; ++j) {
-    const int i = lane * (kMaxParts / 32) + j;
-    v[j] = i < n ? sums[i] : 0.0;
-    own += v[j];
-  }
-  double upto = own;
+  for (int j = 1; j < kPer; ++j) own += v[j];
+  N upto = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const double up = __shfl_up_sync(0xffffffffu, upto, o);
+    const N up = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += up;
   }
-  double run = __shfl_up_sync(0xffffffffu, upto, 1);
-  if (lane == 0) run = 0.0;
+  N run = __shfl_up_sync(0xffffffffu, upto, 1);
+  if (lane == 0) run = N(0);
   int at = -1, last = -1;
-  double at_before = 0.0, last_before = 0.0;
+  N at_before = N(0), last_before = N(0);
 #pragma unroll
-  for (int j = 0; j < kMaxParts / 32; ++j) {
+  for (int j = 0; j < kPer; ++j) {
     if (v[j] > none) {
-      last = lane * (kMaxParts / 32) + j;
+      last = lane * kPer + j;
       last_before = run;
       if (at < 0 && run + v[j] > want) {
         at = last;
@@ -482,63 +494,78 @@ __device__ __forceinline__ int find_part(const double* sums, int n, double want,
   before = __shfl_sync(0xffffffffu, hit ? at_before : last_before, src);
   return __shfl_sync(0xffffffffu, hit ? at : last, src);
 }
-__device__ __forceinline__ double total_of(const double* sums, int n, int lane) {
-  double v = 0.0;
-  for (int i = lane; i < n; i += 32) v += sums[i];
-  return warp_sum(v);
-}
 
-// The first token of [begin, end) at which the running sum exceeds `want`, by one CTA; gap: how far
-// `want` is from the nearer end of its weight.  -1: no weight in it.
-template <int DT, int MODE, bool kFine>
-__device__ __forceinline__ long long search(Weights<DT, MODE, kFine>& f, long long begin, long long end, double want, double& gap,
-                                            Smem& sm) {
+// The first token of [begin, end) at which the running sum exceeds `want`, by one CTA (sm.found; -1:
+// no weight there); sm.gap: how far `want` is from the nearer end of its weight.
+template <int DT, int MODE, bool kFine, class N>
+__device__ __forceinline__ void search(Weights<DT, MODE, kFine>& f, long long begin, long long end, N want, Smem& sm) {
   using F = Fmt<DT>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kStep = 32 * F::kVec;
+  constexpr double none = kFine && MODE != kRest ? kNothing : 0.0;
   while (end - begin > 2 * kStep) {
     const long long size = part_size(end - begin, kWarps, kStep);
     const long long lo = min(end, begin + warp * size), hi = min(end, lo + size);
-    const double s = part_sum<DT, MODE, kFine>(f, lo, hi, lane);
+    const N s = part_sum(f, lo, hi, lane);
+    N* sums;
+    if constexpr (kFine)
+      sums = sm.sums;
+    else
+      sums = sm.coarse;
     __syncthreads();
-    if (lane == 0) sm.sums[warp] = s;
+    if (lane == 0) sums[warp] = s;
     __syncthreads();
-    double before;
-    const int at = max(0, find_part<MODE, kFine>(sm.sums, kWarps, want, before, lane));
-    want -= before;
-    begin = min(end, begin + at * size);
+    if (!kFine || warp == 0) {
+      N v[1], before;
+      v[0] = lane < kWarps ? sums[lane] : N(0);
+      const int at = max(0, find_part(v, want, N(none), before, lane));
+      if (kFine) {
+        if (lane == 0) {
+          sm.at = at;
+          sm.before = before;
+        }
+      } else {
+        begin = min(end, begin + at * size);
+        want -= before;
+      }
+    }
+    if (kFine) {
+      __syncthreads();
+      begin = min(end, begin + sm.at * size);
+      want -= N(sm.before);
+    }
     end = min(end, begin + size);
   }
   __syncthreads();
   if (warp == 0) {
     long long found = -1, last = -1;
-    double near = 0.0, last_near = 0.0;
+    N near = N(0);
     for (long long base = begin; base < end && found < 0; base += kStep) {
       const long long i = base + lane * F::kVec;
-      double x[F::kVec];
+      N x[F::kVec];
 #pragma unroll
-      for (int j = 0; j < F::kVec; ++j) x[j] = 0.0;
+      for (int j = 0; j < F::kVec; ++j) x[j] = N(0);
       if (i < end) f.exactly(i, end, x);
-      double sum = 0.0;
+      N sum = N(0);
 #pragma unroll
       for (int j = 0; j < F::kVec; ++j) sum += x[j];
-      double upto = sum;
+      N upto = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const double up = __shfl_up_sync(0xffffffffu, upto, o);
+        const N up = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += up;
       }
-      double run = __shfl_up_sync(0xffffffffu, upto, 1);
-      if (lane == 0) run = 0.0;
+      N run = __shfl_up_sync(0xffffffffu, upto, 1);
+      if (lane == 0) run = N(0);
       long long mine = -1, mine_last = -1;
-      double mine_near = 0.0;
+      N mine_near = N(0);
 #pragma unroll
       for (int j = 0; j < F::kVec; ++j) {
-        if (x[j] > 0.0) {
+        if (x[j] > N(0)) {
           mine_last = i + j;
           if (mine < 0 && run + x[j] > want) {
             mine = i + j;
-            mine_near = fmin(want - run, run + x[j] - want);
+            mine_near = min(want - run, run + x[j] - want);
           }
         }
         run += x[j];
@@ -554,46 +581,66 @@ __device__ __forceinline__ long long search(Weights<DT, MODE, kFine>& f, long lo
     }
     if (lane == 0) {
       sm.found = found >= 0 ? found : last;
-      sm.gap = found >= 0 ? near : last_near;
+      sm.gap = found >= 0 ? static_cast<float>(near) : 0.f;
     }
   }
   __syncthreads();
-  gap = sm.gap;
-  return sm.found;
 }
 
-// The parts' sums in fine arithmetic, told to the whole cluster (behind it: g.turn's place).
-template <int DT, int MODE>
-__device__ __forceinline__ void sum_parts(Weights<DT, MODE, true>& f, long long lo, long long hi, Group& g, Smem& sm) {
-  const int lane = threadIdx.x & 31, part = g.rank * kWarps + (threadIdx.x >> 5);
-  const double s = part_sum<DT, MODE, true>(f, lo, hi, lane);
-  g.turn ^= 1;
-  tell(g, &sm.ex[g.turn].sum[part], s, lane);
-  g.sync();
-}
-
-// From the parts' sums (in `sums`, the same in every CTA) to the token; the CTA that has the part
-// looks for it there and tells the others.
-template <int DT, int MODE, bool kFine>
-__device__ __forceinline__ long long draw(Weights<DT, MODE, kFine>& f, const double* sums, double want, double unsure, long long V,
-                                          long long size, Group& g, Smem& sm, bool& sure) {
-  const int lane = threadIdx.x & 31, parts = g.size * kWarps;
-  double before;
-  const int at = max(0, find_part<MODE, kFine>(sums, parts, want, before, lane));
+// The CTA that has part `at` (of `size` elements) looks for the token there and tells the others.
+// The answer is sure if the border is more than `unsure` away from the ends of the token's weight.
+template <int DT, int MODE, bool kFine, class N>
+__device__ __forceinline__ long long draw(Weights<DT, MODE, kFine>& f, int at, N want, float unsure, long long V, long long size,
+                                          Group& g, Smem& sm, bool& sure) {
   Exchange& ex = sm.ex[g.turn ^ 1];
   if (at / kWarps == g.rank) {
     const long long lo = min(V, at * size), hi = min(V, lo + size);
-    double gap;
-    const long long t = search<DT, MODE, kFine>(f, lo, hi, want - before, gap, sm);
+    search<DT, MODE, kFine, N>(f, lo, hi, want, sm);
     if (threadIdx.x < 32) {
-      tell(g, &ex.token, t, lane);
-      tell(g, &ex.unsure, static_cast<int>(!(gap > unsure)), lane);
+      tell(g, &ex.token, sm.found, threadIdx.x);
+      tell(g, &ex.unsure, static_cast<int>(!(sm.gap > unsure)), threadIdx.x);
     }
   }
   g.turn ^= 1;
   g.sync();
   sure = !ex.unsure;
   return ex.token;
+}
+
+// The parts' fine sums, told to the whole cluster; then the token at u of their total.
+template <int DT, int MODE>
+__device__ __forceinline__ void tell_sum(Weights<DT, MODE, true>& f, long long lo, long long hi, Group& g, Smem& sm) {
+  const int lane = threadIdx.x & 31, part = g.rank * kWarps + (threadIdx.x >> 5);
+  const double s = part_sum(f, lo, hi, lane);
+  g.turn ^= 1;
+  tell(g, &sm.ex[g.turn].sum[part], s, lane);
+  g.sync();
+}
+template <int DT, int MODE>
+__device__ __forceinline__ long long draw_fine(Weights<DT, MODE, true>& f, const double* sums, double u, long long V, long long size,
+                                               Group& g, Smem& sm) {
+  const int lane = threadIdx.x & 31, parts = g.size * kWarps;
+  constexpr double none = MODE != kRest ? kNothing : 0.0;
+  if (threadIdx.x < 32) {
+    double v[kMaxParts / 32], own = 0.0, before;
+#pragma unroll
+    for (int j = 0; j < kMaxParts / 32; ++j) {
+      const int i = lane * (kMaxParts / 32) + j;
+      v[j] = i < parts ? sums[i] : 0.0;
+      own += v[j];
+    }
+    const double total = warp_sum(own), want = u * total;
+    const int at = total > none ? find_part(v, want, none, before, lane) : -1;
+    if (lane == 0) {
+      sm.at = at;
+      sm.before = want - before;
+    }
+  }
+  __syncthreads();
+  const int at = sm.at;  // the same in every CTA
+  if (at < 0) return -1;
+  bool sure;
+  return draw<DT, MODE, true, double>(f, at, sm.before, -1.f, V, size, g, sm, sure);
 }
 
 template <int DT>
@@ -620,11 +667,10 @@ verify_drafts_kernel(const Args a, int cluster) {
   if (tid < kWarps * kSlots) mbar_init(smem_addr(&sm.full[0][0]) + 8 * tid, 1);
   if (tid == 0) abort_word = 0;
   fence_mbar_init();
+  long long id = 0;
+  if (tid < G) id = a.ids[b * G + tid];
   const int n = a.n_draft ? a.n_draft[b] : G;
-  bool wrong = n < -1 || n > G;
-  if (!wrong)
-    for (int i = tid; i < n; i += kThreads) wrong = wrong || a.ids[b * G + i] < 0 || a.ids[b * G + i] >= V;
-  wrong = __syncthreads_or(wrong);
+  const bool wrong = __syncthreads_or(n < -1 || n > G || (tid < n && (id < 0 || id >= V)));
   if (wrong || n < 0) {  // the same in every CTA of the cluster
     if (g.rank == 0) {
       for (int i = tid; i <= G; i += kThreads) {
@@ -639,7 +685,6 @@ verify_drafts_kernel(const Args a, int cluster) {
     }
     return;
   }
-  if (cluster > 1) cluster_sync_all();  // every CTA runs before its shared memory is written
 
   const int parts = cluster * kWarps, part = g.rank * kWarps + warp;
   const long long size = part_size(V, parts, 32 * F::kVec);
@@ -648,11 +693,12 @@ verify_drafts_kernel(const Args a, int cluster) {
   Stream<DT> in;
   in.init(a.target + b * rows * a.row_bytes, a.row_bytes, n + 1, lo, hi, smem_addr(ring) + warp * kSlots * kChunkBytes,
           smem_addr(&sm.full[warp][0]), lane);
+  if (cluster > 1) cluster_sync_all();  // every CTA runs before its shared memory is written
   FineExp fp;
   int kept = 0;
   // what thread 0 needs of a row's draft, on its way while the row is summed
-  long long d = 0, d_next = tid == 0 && n > 0 ? a.ids[b * G] : 0;
-  Stats st;
+  long long d = 0, d_next = id;
+  Stats st, of_lane[kMaxParts / 32];  // of the row; of the parts that this lane looks after
   bool lost = false, bad = false, exact = false;
   const unsigned char* row = nullptr;
 #pragma unroll 1
@@ -677,37 +723,61 @@ verify_drafts_kernel(const Args a, int cluster) {
       g.turn ^= 1;
       tell(g, &sm.ex[g.turn].stats[part], mine, lane);
       g.sync();
-      st = Stats{-FLT_MAX, 0.f, 0.f};
-      for (int k = lane; k < parts; k += 32) st = merged(st, sm.ex[g.turn].stats[k], a.c);
+      // maximum, then the parts' sums in its frame
+      float m = -FLT_MAX;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        st = merged(st, Stats{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.n, o), __shfl_xor_sync(0xffffffffu, st.s, o)}, a.c);
+      for (int j = 0; j < kMaxParts / 32; ++j) {
+        const int k = lane * (kMaxParts / 32) + j;
+        of_lane[j] = k < parts ? sm.ex[g.turn].stats[k] : Stats{-FLT_MAX, 0.f, 0.f};
+        m = max_nan(m, of_lane[j].m);
+      }
+      asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(st.m) : "f"(m));
+      st.n = st.s = 0.f;
+#pragma unroll
+      for (int j = 0; j < kMaxParts / 32; ++j) {
+        const bool top = of_lane[j].m == st.m;
+        st.n += top ? of_lane[j].n : 0.f;
+        st.s += top ? of_lane[j].s : (of_lane[j].n + of_lane[j].s) * ex2_approx((of_lane[j].m - st.m) * a.c);
+      }
+      st.n = warp_sum(st.n);
+      st.s = warp_sum(st.s);
       if (exact || !needs_exact<F>(st.m, a.c) || st.m != st.m) break;
       exact = true;
       mine = part_stats_exact<DT>(row, lo, hi, a.c, lane);
     }
     bad = !(fabsf(st.m) < INFINITY) || !(st.n > 0.f);
-    fp.init(a.c_d, st.m, 0.0);
-    if (writes && lse) lse[i] = bad ? nan : static_cast<float>(static_cast<double>(st.m) * a.inv_t + log1pf((st.n - 1.f) + st.s));
-    if (bad || i == n) break;
+    fp.init(a.c, a.c_lo, a.unit, st.m, 0.f);
+    if (bad || i == n) {
+      if (writes && lse) lse[i] = bad ? nan : static_cast<float>(static_cast<double>(st.m) * a.inv_t + log1pf((st.n - 1.f) + st.s));
+      break;
+    }
     if (tid == 0) {
-      int v = kStays;
-      double qd = 1.0;
-      if (a.draft) {
-        if (!(zq < INFINITY) || !(fabsf(lq) < INFINITY)) v = kNoDistribution;
-        qd = draft_prob<DT>(zq, lq, a, sm.T, sm.delta);
-      }
-      const double w = fp.is_zero(zd) ? 0.0 : fp.template at<DT == RL_F32, false>(zd, sm.T, sm.delta).value();
-      const double total = static_cast<double>(st.n) + static_cast<double>(st.s);
-      if (v == kStays && !(ui * qd * total < w)) v = kRefused;
-      if (v == kStays && writes) {
-        tokens[i] = d;
-        if (logp) logp[i] = log_prob(zd, st, a.inv_t);
+      const Term w = fp.is_zero(zd) ? Term{0.f, 0.f, 0.f} : fp.template at<DT == RL_F32, false>(zd, sm.T, sm.delta);
+      int v;
+      if (a.draft && (!(zq < INFINITY) || !(fabsf(lq) < INFINITY))) {
+        v = kNoDistribution;
+      } else {
+        // u q S < w, where fp32 decides it (an exponent of up to 128: 2^-17 of the value)
+        const float x = a.draft ? fmaf(zq, a.c, -lq * kLog2e) : 0.f;
+        const float left = static_cast<float>(ui) * ex2_approx(x) * (st.n + st.s);
+        if (fabsf(x) < 128.f && fabsf(zq * a.c) < 1024.f && fabsf(left - w.a) > 0x1p-8f * w.a && w.a > 0x1p-100f) {
+          v = left < w.a ? kStays : kRefused;
+        } else {
+          const double qd = a.draft ? draft_prob<DT>(zq, lq, a, sm.T, sm.delta) : 1.0;
+          v = ui * qd * (static_cast<double>(st.n) + static_cast<double>(st.s)) < w.value() ? kStays : kRefused;
+        }
       }
       sm.verdict = v;
     }
     __syncthreads();
     const int v = sm.verdict;
+    if (writes) {
+      if (lse) lse[i] = static_cast<float>(static_cast<double>(st.m) * a.inv_t + log1pf((st.n - 1.f) + st.s));
+      if (v == kStays) {
+        tokens[i] = d;
+        if (logp) logp[i] = log_prob(zd, st, a.inv_t);
+      }
+    }
     lost = v == kRefused;
     bad = v == kNoDistribution;
     if (lost || bad) break;
@@ -718,21 +788,23 @@ verify_drafts_kernel(const Args a, int cluster) {
   if (!bad) {
     double u = a.u[b * rows + G];
     u = u > 0.0 ? fmin(u, 1.0 - 0x1p-53) : 0.0;
-    const double S = static_cast<double>(st.n) + static_cast<double>(st.s);
     const unsigned char* draft_row = a.draft ? a.draft + (b * G + kept) * a.draft_bytes : nullptr;
     bool done = false;
     if (lost && a.draft) {
       // S q_v = 2^(z c - k), k = lse_q log2(e) - log2 S, in the frame of a number with few digits
-      const double lq = static_cast<double>(a.draft_lse[b * G + kept]) * kLog2eD;
       Weights<DT, kRest, true> f{row, draft_row, -1, 0.f, 0.f, fp, fp, sm.T, sm.delta, false};
-      double total = S;
+      const double S = static_cast<double>(st.n) + static_cast<double>(st.s);
+      if (tid == 0) sm.total = S;
 #pragma unroll 1
       for (int pass = 0; pass < 2; ++pass) {
-        if (tid == 0) sm.log2_total = log2(total);
+        if (tid == 0) {
+          const double k = static_cast<double>(a.draft_lse[b * G + kept]) * kLog2eD - log2(sm.total);
+          const float mq = static_cast<float>(rint(k * a.t_ln2 * 4096.0) * (1.0 / 4096.0));
+          sm.coarse[0] = mq;
+          sm.coarse[1] = static_cast<float>(k - static_cast<double>(mq) * a.c_d);
+        }
         __syncthreads();
-        const double k = lq - sm.log2_total;
-        const float mq = static_cast<float>(rint(k * a.t_ln2 * 4096.0) * (1.0 / 4096.0));
-        f.q.init(a.c_d, mq, k - static_cast<double>(mq) * a.c_d);
+        f.q.init(a.c, a.c_lo, a.unit, sm.coarse[0], sm.coarse[1]);
         if (pass == 1) break;
         // sums over all tokens, and of both sides over those with p > q
         double all = 0.0, plus = 0.0, neg = 0.0;
@@ -749,8 +821,8 @@ verify_drafts_kernel(const Args a, int cluster) {
 #pragma unroll
           for (int j = 0; j < F::kVec; ++j) {
             bad = bad || !(y[j] < INFINITY);
-            const Term w = f.fine(z[j]), q = f.drafted(y[j]), d = minus(w, q);
-            const bool more = d.a + d.b + d.c > 0.f;
+            const Term w = f.fine(z[j]), q = f.drafted(y[j]), r = minus(w, q);
+            const bool more = r.a + r.b + r.c > 0.f;
             fa.add(w);
             if (more) {
               fb.add(w);
@@ -777,51 +849,54 @@ verify_drafts_kernel(const Args a, int cluster) {
         tell(g, &ex.plus[part], plus, lane);
         tell(g, &ex.minus[part], neg, lane);
         g.sync();
-        bad = false;
-        for (int k2 = lane; k2 < parts; k2 += 32) bad = bad || ex.sum[k2] < 0.0;
-        bad = __any_sync(0xffffffffu, bad);
-        total = total_of(ex.sum, parts, lane);
+        if (warp == 0) {
+          double total = 0.0;
+          bad = false;
+          for (int k = lane; k < parts; k += 32) {
+            bad = bad || ex.sum[k] < 0.0;
+            total += ex.sum[k];
+          }
+          total = warp_sum(total);
+          bad = __any_sync(0xffffffffu, bad);
+          const double ratio = total / S;  // q's terms were taken with S, and belong to `total`
+          for (int k = lane; k < parts; k += 32) ex.plus[k] = fmax(0.0, ex.plus[k] - ratio * ex.minus[k]);
+          if (lane == 0) {
+            sm.total = total;
+            sm.verdict = bad;
+          }
+        }
+        __syncthreads();
+        bad = sm.verdict;
         if (bad) break;
       }
       if (!bad) {
-        Exchange& ex = sm.ex[g.turn];
-        const double ratio = total / S;  // q's terms were taken with S, and belong to `total`
-        __syncthreads();
-        if (tid < parts) ex.plus[tid] = fmax(0.0, ex.plus[tid] - ratio * ex.minus[tid]);
-        __syncthreads();
-        const double rest = total_of(ex.plus, parts, lane);
-        if (rest > 0.0) {
-          bool sure;
-          token = draw<DT, kRest, true>(f, ex.plus, u * rest, -1.0, V, size, g, sm, sure);
-          done = token >= 0;
-        }
+        token = draw_fine(f, sm.ex[g.turn].plus, u, V, size, g, sm);
+        done = token >= 0;
       }
     } else {
-      // the parts' sums of step 1 in the row's frame, without the draft that was looked up
+      // the parts' sums of step 1 in the frame of the row, without the draft that was looked up
       const bool without = lost;
-      const long long d = without ? a.ids[b * G + kept] : -1;
+      const long long d_out = without ? a.ids[b * G + kept] : -1;
       if (!exact) {
-        const Exchange& ex = sm.ex[g.turn];
-        const float nm = -st.m * a.c, back = ex2_approx(fmaf(-st.m, a.c, -nm));
-        __syncthreads();
-        double* sums = sm.ex[g.turn].sum;
-        if (tid < parts) {
-          const Stats s = ex.stats[tid];
-          double x = (static_cast<double>(s.n) + static_cast<double>(s.s)) * static_cast<double>(ex2_approx((s.m - st.m) * a.c));
-          // (the search's terms are in the frame nm)
-          if (without && d >= tid * size && d < (tid + 1) * size) x = fmax(0.0, x - static_cast<double>(ex2_approx(fmaf(F::load(row, d), a.c, nm)) * back));
-          sums[tid] = x / static_cast<double>(back);
+        const float nm = -st.m * a.c, back = ex2_approx(fmaf(st.m, a.c, nm));  // true terms to the search's
+        float v[kMaxParts / 32], own = 0.f, before;
+#pragma unroll
+        for (int j = 0; j < kMaxParts / 32; ++j) {
+          const long long k = lane * (kMaxParts / 32) + j;
+          v[j] = (of_lane[j].n + of_lane[j].s) * ex2_approx((of_lane[j].m - st.m) * a.c) * back;
+          if (without && d_out >= k * size && d_out < (k + 1) * size) v[j] = fmaxf(0.f, v[j] - ex2_approx(fmaf(F::load(row, d_out), a.c, nm)));
+          own += v[j];
         }
-        __syncthreads();
-        const double total = total_of(sums, parts, lane);
+        const float total = warp_sum(own), want = static_cast<float>(u) * total;
+        const int at = max(0, find_part(v, want, 0.f, before, lane));
         bool sure;
         long long t;
         if (without) {
-          Weights<DT, kWithout, false> f{row, nullptr, d, a.c, nm, fp, fp, sm.T, sm.delta, false};
-          t = draw<DT, kWithout, false>(f, sums, u * total, kCoarse * S, V, size, g, sm, sure);
+          Weights<DT, kWithout, false> f{row, nullptr, d_out, a.c, nm, fp, fp, sm.T, sm.delta, false};
+          t = draw<DT, kWithout, false, float>(f, at, want - before, kCoarse * (st.n + st.s), V, size, g, sm, sure);
         } else {
           Weights<DT, kSoftmax, false> f{row, nullptr, -1, a.c, nm, fp, fp, sm.T, sm.delta, false};
-          t = draw<DT, kSoftmax, false>(f, sums, u * total, kCoarse * S, V, size, g, sm, sure);
+          t = draw<DT, kSoftmax, false, float>(f, at, want - before, kCoarse * (st.n + st.s), V, size, g, sm, sure);
         }
         if (sure && t >= 0) {
           token = t;
@@ -829,23 +904,16 @@ verify_drafts_kernel(const Args a, int cluster) {
         }
       }
       if (!done && without) {
-        Weights<DT, kWithout, true> f{row, nullptr, d, 0.f, 0.f, fp, fp, sm.T, sm.delta, false};
-        sum_parts(f, lo, hi, g, sm);
-        const double* sums = sm.ex[g.turn].sum;
-        const double total = total_of(sums, parts, lane);
-        if (total > kNothing) {
-          bool sure;
-          token = draw<DT, kWithout, true>(f, sums, u * total, -1.0, V, size, g, sm, sure);
-          done = token >= 0;
-        }
+        Weights<DT, kWithout, true> f{row, nullptr, d_out, 0.f, 0.f, fp, fp, sm.T, sm.delta, false};
+        tell_sum(f, lo, hi, g, sm);
+        token = draw_fine(f, sm.ex[g.turn].sum, u, V, size, g, sm);
+        done = token >= 0;
       }
     }
     if (!done && !bad) {
       Weights<DT, kSoftmax, true> f{row, nullptr, -1, 0.f, 0.f, fp, fp, sm.T, sm.delta, false};
-      sum_parts(f, lo, hi, g, sm);
-      const double* sums = sm.ex[g.turn].sum;
-      bool sure;
-      token = draw<DT, kSoftmax, true>(f, sums, u * total_of(sums, parts, lane), -1.0, V, size, g, sm, sure);
+      tell_sum(f, lo, hi, g, sm);
+      token = draw_fine(f, sm.ex[g.turn].sum, u, V, size, g, sm);
     }
     bad = bad || token < 0;
   }
@@ -868,16 +936,17 @@ verify_drafts_kernel(const Args a, int cluster) {
   if (cluster > 1) cluster_sync_all();  // nobody leaves while its shared memory may be written
 }
 
-// CTAs of a cluster: as many as fit at once, at most 16 (8 without the attribute that allows
-// more), and no more than leave a warp 256 elements.
+// CTAs of a cluster: the power of two with which all are at work at once, at most 16, and no
+// more than leave a warp 256 elements.  (Clusters of 8 fill a third fewer of the places, of
+// 16 half as many: parts of the chip hold no whole number of them.)  From two CTAs a place on, clusters of 2:
+// shorter last rounds.
 int cluster_for(long long B, long long V, int sms) {
   const long long slots = static_cast<long long>(sms) * kCtasPerSm;
   const long long most = (V + 256 * kWarps - 1) / (256 * kWarps);
-  long long c = slots / B;
-  if (c > kMaxCluster) c = kMaxCluster;
-  if (c > 8) c = c >= kMaxCluster ? kMaxCluster : 8;
-  if (c > most) c = most;
-  return static_cast<int>(c < 1 ? 1 : c);
+  int c = 2;
+  while (c < kMaxCluster && 2 * c * B <= (c >= 4 ? slots / 2 : slots)) c *= 2;
+  while (c > 1 && c > most) c /= 2;
+  return c;
 }
 
 template <int DT>
@@ -951,6 +1020,8 @@ extern "C" rl_status rl_verify_drafts(const rl_verify_drafts_desc* desc, void* s
   a.c_d = kLog2eD / d.temperature;
   a.t_ln2 = d.temperature * 0.69314718055994530942;
   a.c = static_cast<float>(a.c_d);
+  a.c_lo = static_cast<float>(a.c_d - static_cast<double>(a.c));
+  a.unit = 1.f / a.c;
   a.tokens = d.tokens;
   a.n_accepted = d.n_accepted;
   a.logp = d.logp_out;
