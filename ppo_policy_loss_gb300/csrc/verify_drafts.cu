@@ -43,6 +43,7 @@ constexpr int kCtasPerSm = 3;
 constexpr int kMaxCluster = 16, kMaxParts = kMaxCluster * kWarps;
 constexpr double kLog2eD = 1.4426950408889634074;
 constexpr float kCoarse = 0x1.4p-17f;  // two sums of 72 2^-24 each, rounded up
+constexpr float kFar = 0x1p20f;       // |m c| beyond which m - 124 / c is near m's own last place
 constexpr double kNothing = 0x1p-90;  // sums of weights that are 0 (2^-124 each) stay below
 
 struct Args {
@@ -93,14 +94,15 @@ enum Verdict { kStays, kRefused, kNoDistribution };
 // one has passed the barrier behind which everybody had read the other.
 struct Exchange {
   Stats stats[kMaxParts];
-  double sum[kMaxParts], plus[kMaxParts], minus[kMaxParts];
+  double sum[kMaxParts], plus[kMaxParts];
+  float drafted[kMaxParts];
   long long token;
   int unsure;
 };
 constexpr int kSlots = 4, kChunkBytes = 2048;  // of a warp's ring
 struct Smem {
   unsigned long long full[kWarps][kSlots];
-  float T[kPow], delta[kPow];
+  uint2 powers[kPow];
   Exchange ex[2];
   double sums[kWarps];   // of the search
   float coarse[kWarps];
@@ -345,13 +347,13 @@ __device__ __forceinline__ float log_prob(float z, const Stats& st, double inv_t
 // q = e^(z / temperature - lse) (fp64's own exponential is some hundred dependent steps of a
 // unit with a 64th of fp32's rate, and everybody waits for this one number).
 template <int DT>
-__device__ __forceinline__ double draft_prob(float z, float lse, const Args& a, const float* T, const float* delta) {
+__device__ __forceinline__ double draft_prob(float z, float lse, const Args& a, const uint2* powers) {
   const double k = static_cast<double>(lse) * kLog2eD, m = rint(k * a.t_ln2 * 4096.0) * (1.0 / 4096.0);
   const double x = static_cast<double>(z) * a.c_d - k;
   if (!(x > -120.0 && x < 1.5 && fabs(m) < 4096.0)) return exp(static_cast<double>(z) * a.inv_t - static_cast<double>(lse));
   FineExp q;
-  q.init(a.c, a.c_lo, a.unit, static_cast<float>(m), static_cast<float>(k - m * a.c_d));
-  return q.template at<true, false>(z, T, delta).value();
+  q.init(a.c, a.c_lo, a.unit, static_cast<float>(m), static_cast<float>(k - m * a.c_d), false);
+  return q.template at<true, false>(z, powers).value();
 }
 
 template <int DT, int MODE, bool kFine>
@@ -361,12 +363,10 @@ struct Weights {
   long long without;
   float c, nm;      // coarse: 2^(z c + nm)
   FineExp p, q;
-  const float* T;
-  const float* delta;
-  bool bad;
+  const uint2* powers;
 
-  __device__ __forceinline__ Term fine(float z) const { return p.template at<DT == RL_F32, false>(z, T, delta); }
-  __device__ __forceinline__ Term drafted(float z) const { return q.template at<DT == RL_F32, true>(z, T, delta); }
+  __device__ __forceinline__ Term2 fine(float2 z) const { return p.template at<DT == RL_F32, false>(z, powers); }
+  __device__ __forceinline__ Term2 drafted(float2 z) const { return q.template at<DT == RL_F32, true>(z, powers); }
 
   // a vector's logits, -inf behind `end` and at the token that is left out
   __device__ __forceinline__ void logits(long long i, long long end, float (&z)[Fmt<DT>::kVec]) const {
@@ -377,20 +377,23 @@ struct Weights {
         if (i + j == without) z[j] = -INFINITY;
     }
   }
-  // weights of elements i .. i + kVec - 1, as terms
-  __device__ __forceinline__ void at(long long i, long long end, Term (&w)[Fmt<DT>::kVec]) {
+  // weights of elements i .. i + kVec - 1, in pairs
+  __device__ __forceinline__ void at(long long i, long long end, Term2 (&w)[Fmt<DT>::kVec / 2]) const {
     using F = Fmt<DT>;
     float z[F::kVec], y[F::kVec];
     logits(i, end, z);
     if (MODE == kRest) F::unpack(load_vec<DT>(draft_row, i, end), y);
 #pragma unroll
-    for (int j = 0; j < F::kVec; ++j) {
+    for (int j = 0; j < F::kVec / 2; ++j) {
+      const float2 zz = make_float2(z[2 * j], z[2 * j + 1]);
       if (!kFine) {
-        w[j] = Term{ex2_approx(fmaf(z[j], c, nm)), 0.f, 0.f};
+        const float2 x = __ffma2_rn(zz, both(c), both(nm));
+        w[j].a = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+        w[j].b = w[j].c = both(0.f);
       } else {
-        w[j] = fine(z[j]);
-        if (MODE == kRest) w[j] = minus(w[j], drafted(y[j]));
-        if (MODE == kRest && !(w[j].a + w[j].b + w[j].c > 0.f)) w[j] = Term{0.f, 0.f, 0.f};
+        w[j] = fine(zz);
+        float2 more;
+        if (MODE == kRest) w[j] = above(w[j], drafted(make_float2(y[2 * j], y[2 * j + 1])), more);
       }
     }
   }
@@ -399,15 +402,16 @@ struct Weights {
   __device__ __forceinline__ void exactly(long long i, long long end, N (&x)[Fmt<DT>::kVec]) {
     using F = Fmt<DT>;
     float z[F::kVec];
-    Term w[F::kVec];
+    Term2 w[F::kVec / 2];
     logits(i, end, z);
     at(i, end, w);
 #pragma unroll
     for (int j = 0; j < F::kVec; ++j) {
+      const Term x1 = j & 1 ? w[j / 2].y() : w[j / 2].x();
       if constexpr (kFine)
-        x[j] = p.is_zero(z[j]) ? 0.0 : w[j].value();
+        x[j] = p.is_zero(z[j]) ? 0.0 : x1.value();
       else
-        x[j] = w[j].a;
+        x[j] = x1.a;
     }
   }
 };
@@ -429,10 +433,10 @@ __device__ __forceinline__ double part_sum(Weights<DT, MODE, true>& f, long long
   int n = 0;
 #pragma unroll 1
   for (long long i = lo + lane * F::kVec; i < hi; i += 32 * F::kVec) {
-    Term w[F::kVec];
+    Term2 w[F::kVec / 2];
     f.at(i, hi, w);
 #pragma unroll
-    for (int j = 0; j < F::kVec; ++j) s.add(w[j]);
+    for (int j = 0; j < F::kVec / 2; ++j) s.add(w[j]);
     if (++n == 64) {
       total += s.value();
       s.clear();
@@ -448,12 +452,12 @@ __device__ __forceinline__ float part_sum(Weights<DT, MODE, false>& f, long long
   float total = 0.f, err = 0.f;
 #pragma unroll 2
   for (long long i = lo + lane * F::kVec; i < hi; i += 32 * F::kVec) {
-    Term w[F::kVec];
+    Term2 w[F::kVec / 2];
     f.at(i, hi, w);
 #pragma unroll
-    for (int j = 1; j < F::kVec; ++j) w[0].a += w[j].a;
+    for (int j = 1; j < F::kVec / 2; ++j) w[0].a = __fadd2_rn(w[0].a, w[j].a);
     float lost;
-    total = two_sum(total, w[0].a, lost);
+    total = two_sum(total, w[0].a.x + w[0].a.y, lost);
     err += lost;
   }
   return warp_sum(total + err);
@@ -660,10 +664,8 @@ verify_drafts_kernel(const Args a, int cluster) {
   float* logp = a.logp ? a.logp + b * rows : nullptr;
   float* lse = a.lse ? a.lse + b * rows : nullptr;
   const float nan = __int_as_float(0x7fc00000);
-  if (tid < kPow) {
-    sm.T[tid] = kPowT[tid];
-    sm.delta[tid] = kPowD[tid];
-  }
+  static_assert(kPow == kThreads, "one power a thread");
+  sm.powers[tid] = kPowers[tid];
   if (tid < kWarps * kSlots) mbar_init(smem_addr(&sm.full[0][0]) + 8 * tid, 1);
   if (tid == 0) abort_word = 0;
   fence_mbar_init();
@@ -746,13 +748,13 @@ verify_drafts_kernel(const Args a, int cluster) {
       mine = part_stats_exact<DT>(row, lo, hi, a.c, lane);
     }
     bad = !(fabsf(st.m) < INFINITY) || !(st.n > 0.f);
-    fp.init(a.c, a.c_lo, a.unit, st.m, 0.f);
+    fp.init(a.c, a.c_lo, a.unit, st.m, 0.f, fabsf(st.m) * a.c > kFar);
     if (bad || i == n) {
       if (writes && lse) lse[i] = bad ? nan : static_cast<float>(static_cast<double>(st.m) * a.inv_t + log1pf((st.n - 1.f) + st.s));
       break;
     }
     if (tid == 0) {
-      const Term w = fp.is_zero(zd) ? Term{0.f, 0.f, 0.f} : fp.template at<DT == RL_F32, false>(zd, sm.T, sm.delta);
+      const Term w = fp.is_zero(zd) ? Term{0.f, 0.f, 0.f} : fp.template at<DT == RL_F32, false>(zd, sm.powers);
       int v;
       if (a.draft && (!(zq < INFINITY) || !(fabsf(lq) < INFINITY))) {
         v = kNoDistribution;
@@ -763,7 +765,7 @@ verify_drafts_kernel(const Args a, int cluster) {
         if (fabsf(x) < 128.f && fabsf(zq * a.c) < 1024.f && fabsf(left - w.a) > 0x1p-8f * w.a && w.a > 0x1p-100f) {
           v = left < w.a ? kStays : kRefused;
         } else {
-          const double qd = a.draft ? draft_prob<DT>(zq, lq, a, sm.T, sm.delta) : 1.0;
+          const double qd = a.draft ? draft_prob<DT>(zq, lq, a, sm.powers) : 1.0;
           v = ui * qd * (static_cast<double>(st.n) + static_cast<double>(st.s)) < w.value() ? kStays : kRefused;
         }
       }
@@ -792,7 +794,7 @@ verify_drafts_kernel(const Args a, int cluster) {
     bool done = false;
     if (lost && a.draft) {
       // S q_v = 2^(z c - k), k = lse_q log2(e) - log2 S, in the frame of a number with few digits
-      Weights<DT, kRest, true> f{row, draft_row, -1, 0.f, 0.f, fp, fp, sm.T, sm.delta, false};
+      Weights<DT, kRest, true> f{row, draft_row, -1, 0.f, 0.f, fp, fp, sm.powers};
       const double S = static_cast<double>(st.n) + static_cast<double>(st.s);
       if (tid == 0) sm.total = S;
 #pragma unroll 1
@@ -804,14 +806,14 @@ verify_drafts_kernel(const Args a, int cluster) {
           sm.coarse[1] = static_cast<float>(k - static_cast<double>(mq) * a.c_d);
         }
         __syncthreads();
-        f.q.init(a.c, a.c_lo, a.unit, sm.coarse[0], sm.coarse[1]);
+        f.q.init(a.c, a.c_lo, a.unit, sm.coarse[0], sm.coarse[1], fabsf(sm.coarse[0]) * a.c > kFar);
         if (pass == 1) break;
-        // sums over all tokens, and of both sides over those with p > q
-        double all = 0.0, plus = 0.0, neg = 0.0;
-        FineSum fa, fb, fc;
+        // sums of p over all tokens, and of p - q and of q over those with p > q
+        double all = 0.0, plus = 0.0;
+        FineSum fa, fb;
         fa.clear();
         fb.clear();
-        fc.clear();
+        float2 qs = both(0.f);
         int count = 0;
 #pragma unroll 1
         for (long long i = lo + lane * F::kVec; i < hi; i += 32 * F::kVec) {
@@ -819,35 +821,31 @@ verify_drafts_kernel(const Args a, int cluster) {
           F::unpack(load_vec<DT>(row, i, hi), z);
           F::unpack(load_vec<DT>(draft_row, i, hi), y);
 #pragma unroll
-          for (int j = 0; j < F::kVec; ++j) {
-            bad = bad || !(y[j] < INFINITY);
-            const Term w = f.fine(z[j]), q = f.drafted(y[j]), r = minus(w, q);
-            const bool more = r.a + r.b + r.c > 0.f;
+          for (int j = 0; j < F::kVec; j += 2) {
+            bad = bad || !(y[j] < INFINITY) || !(y[j + 1] < INFINITY);
+            const Term2 w = f.fine(make_float2(z[j], z[j + 1])), q = f.drafted(make_float2(y[j], y[j + 1]));
+            float2 more;
             fa.add(w);
-            if (more) {
-              fb.add(w);
-              fc.add(q);
-            }
+            fb.add(above(w, q, more));
+            qs = __ffma2_rn(more, q.a, qs);
           }
-          if (++count == 32) {
+          if (++count == 64) {
             all += fa.value();
             plus += fb.value();
-            neg += fc.value();
             fa.clear();
             fb.clear();
-            fc.clear();
             count = 0;
           }
         }
         all = warp_sum(all + fa.value());
         plus = warp_sum(plus + fb.value());
-        neg = warp_sum(neg + fc.value());
+        const float drafted = warp_sum(qs.x + qs.y);
         bad = __any_sync(0xffffffffu, bad);
         g.turn ^= 1;
         Exchange& ex = sm.ex[g.turn];
         tell(g, &ex.sum[part], bad ? -1.0 : all, lane);
         tell(g, &ex.plus[part], plus, lane);
-        tell(g, &ex.minus[part], neg, lane);
+        tell(g, &ex.drafted[part], drafted, lane);
         g.sync();
         if (warp == 0) {
           double total = 0.0;
@@ -858,8 +856,8 @@ verify_drafts_kernel(const Args a, int cluster) {
           }
           total = warp_sum(total);
           bad = __any_sync(0xffffffffu, bad);
-          const double ratio = total / S;  // q's terms were taken with S, and belong to `total`
-          for (int k = lane; k < parts; k += 32) ex.plus[k] = fmax(0.0, ex.plus[k] - ratio * ex.minus[k]);
+          const double more = total / S - 1.0;  // q's terms were taken with S, and belong to `total`
+          for (int k = lane; k < parts; k += 32) ex.plus[k] = fmax(0.0, ex.plus[k] - more * static_cast<double>(ex.drafted[k]));
           if (lane == 0) {
             sm.total = total;
             sm.verdict = bad;
@@ -892,10 +890,10 @@ verify_drafts_kernel(const Args a, int cluster) {
         bool sure;
         long long t;
         if (without) {
-          Weights<DT, kWithout, false> f{row, nullptr, d_out, a.c, nm, fp, fp, sm.T, sm.delta, false};
+          Weights<DT, kWithout, false> f{row, nullptr, d_out, a.c, nm, fp, fp, sm.powers};
           t = draw<DT, kWithout, false, float>(f, at, want - before, kCoarse * (st.n + st.s), V, size, g, sm, sure);
         } else {
-          Weights<DT, kSoftmax, false> f{row, nullptr, -1, a.c, nm, fp, fp, sm.T, sm.delta, false};
+          Weights<DT, kSoftmax, false> f{row, nullptr, -1, a.c, nm, fp, fp, sm.powers};
           t = draw<DT, kSoftmax, false, float>(f, at, want - before, kCoarse * (st.n + st.s), V, size, g, sm, sure);
         }
         if (sure && t >= 0) {
@@ -904,14 +902,14 @@ verify_drafts_kernel(const Args a, int cluster) {
         }
       }
       if (!done && without) {
-        Weights<DT, kWithout, true> f{row, nullptr, d_out, 0.f, 0.f, fp, fp, sm.T, sm.delta, false};
+        Weights<DT, kWithout, true> f{row, nullptr, d_out, 0.f, 0.f, fp, fp, sm.powers};
         tell_sum(f, lo, hi, g, sm);
         token = draw_fine(f, sm.ex[g.turn].sum, u, V, size, g, sm);
         done = token >= 0;
       }
     }
     if (!done && !bad) {
-      Weights<DT, kSoftmax, true> f{row, nullptr, -1, 0.f, 0.f, fp, fp, sm.T, sm.delta, false};
+      Weights<DT, kSoftmax, true> f{row, nullptr, -1, 0.f, 0.f, fp, fp, sm.powers};
       tell_sum(f, lo, hi, g, sm);
       token = draw_fine(f, sm.ex[g.turn].sum, u, V, size, g, sm);
     }
