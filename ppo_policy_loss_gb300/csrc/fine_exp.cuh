@@ -17,6 +17,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include <cuda_runtime.h>
 
 namespace rl {
@@ -90,10 +91,87 @@ __device__ const uint2 kPowers[kPow] = {
     {0x3f7e83b3u, 0xb2579081u}, {0x3f7eb194u, 0xb29826b8u}, {0x3f7edfedu, 0x331fae17u}, {0x3f7f0ec0u, 0x31c86dfdu},
     {0x3f7f3e0cu, 0x319726b5u}, {0x3f7f6dd2u, 0xb2db5dc0u}, {0x3f7f9e11u, 0x33062615u}, {0x3f7fcecbu, 0x330134d5u}};
 
+// x + y = the sum returned + err, exactly
+__device__ __forceinline__ float two_sum(float x, float y, float& err) {
+  const float s = __fadd_rn(x, y), t = __fsub_rn(s, x);
+  err = __fadd_rn(__fsub_rn(x, __fsub_rn(s, t)), __fsub_rn(y, t));
+  return s;
+}
+
+// A number of 48 bits as the sum of two floats, l at most half a last place of h.
+struct Wide {
+  float h, l;
+  __device__ __forceinline__ Wide() {}
+  __device__ __forceinline__ explicit Wide(float x) : h(x), l(0.f) {}
+  // x + y, |x| >= |y|
+  __device__ __forceinline__ Wide(float x, float y) {
+    h = __fadd_rn(x, y);
+    l = __fsub_rn(y, __fsub_rn(h, x));
+  }
+  __device__ __forceinline__ explicit operator float() const { return h; }
+  __device__ __forceinline__ Wide operator-() const {
+    Wide r;
+    r.h = -h;
+    r.l = -l;
+    return r;
+  }
+};
+__device__ __forceinline__ Wide operator+(const Wide& x, const Wide& y) {
+  float e;
+  const float s = two_sum(x.h, y.h, e);
+  return Wide(s, __fadd_rn(e, __fadd_rn(x.l, y.l)));
+}
+__device__ __forceinline__ Wide operator-(const Wide& x, const Wide& y) { return x + (-y); }
+__device__ __forceinline__ Wide& operator+=(Wide& x, const Wide& y) { return x = x + y; }
+__device__ __forceinline__ Wide& operator-=(Wide& x, const Wide& y) { return x = x - y; }
+__device__ __forceinline__ Wide operator*(const Wide& x, const Wide& y) {
+  const float p = __fmul_rn(x.h, y.h);
+  return Wide(p, __fadd_rn(fmaf(x.h, y.h, -p), fmaf(x.h, y.l, __fmul_rn(x.l, y.h))));
+}
+__device__ __forceinline__ bool operator>(const Wide& x, const Wide& y) { return x.h > y.h || (x.h == y.h && x.l > y.l); }
+template <class N>
+__device__ __forceinline__ N smaller(const N& x, const N& y) { return x > y ? y : x; }
+
+// A warp's exchanges of plain and of wide numbers.
+template <class N>
+__device__ __forceinline__ N from_xor(const N& v, int o) {
+  if constexpr (std::is_same<N, Wide>::value) {
+    N r;
+    r.h = __shfl_xor_sync(0xffffffffu, v.h, o);
+    r.l = __shfl_xor_sync(0xffffffffu, v.l, o);
+    return r;
+  } else {
+    return __shfl_xor_sync(0xffffffffu, v, o);
+  }
+}
+template <class N>
+__device__ __forceinline__ N from_below(const N& v, int o) {
+  if constexpr (std::is_same<N, Wide>::value) {
+    N r;
+    r.h = __shfl_up_sync(0xffffffffu, v.h, o);
+    r.l = __shfl_up_sync(0xffffffffu, v.l, o);
+    return r;
+  } else {
+    return __shfl_up_sync(0xffffffffu, v, o);
+  }
+}
+template <class N>
+__device__ __forceinline__ N from_lane(const N& v, int src) {
+  if constexpr (std::is_same<N, Wide>::value) {
+    N r;
+    r.h = __shfl_sync(0xffffffffu, v.h, src);
+    r.l = __shfl_sync(0xffffffffu, v.l, src);
+    return r;
+  } else {
+    return __shfl_sync(0xffffffffu, v, src);
+  }
+}
+
 struct Term {
   float a, b, c;
-  __device__ __forceinline__ double value() const {
-    return static_cast<double>(a) + (static_cast<double>(b) + static_cast<double>(c));
+  __device__ __forceinline__ Wide value() const {
+    const Wide s(a, b);
+    return Wide(s.h, __fadd_rn(s.l, c));
   }
 };
 struct Term2 {
@@ -105,18 +183,13 @@ struct Term2 {
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 sub2(float2 x, float2 y) { return __ffma2_rn(y, both(-1.f), x); }
 
-// x + y = the sum returned + err, exactly
-__device__ __forceinline__ float two_sum(float x, float y, float& err) {
-  const float s = __fadd_rn(x, y), t = __fsub_rn(s, x);
-  err = __fadd_rn(__fsub_rn(x, __fsub_rn(s, t)), __fsub_rn(y, t));
-  return s;
-}
+// the same for two numbers at a time
 __device__ __forceinline__ float2 two_sum2(float2 x, float2 y, float2& err) {
   const float2 s = __fadd2_rn(x, y), t = sub2(s, x);
   err = __fadd2_rn(sub2(x, sub2(s, t)), sub2(y, t));
   return s;
 }
-// the same for |x| >= |y|
+// and for |x| >= |y|
 __device__ __forceinline__ float2 quick_two_sum2(float2 x, float2 y, float2& err) {
   const float2 s = __fadd2_rn(x, y);
   err = sub2(y, sub2(s, x));
@@ -217,12 +290,31 @@ struct FineSum {
     mid = quick_two_sum2(mid, p.b, f);
     lo = __fadd2_rn(lo, __fadd2_rn(__fadd2_rn(e, f), p.c));
   }
-  __device__ __forceinline__ double value() const {
-    const double x = (static_cast<double>(hi.x) - 1.0) + ((static_cast<double>(mid.x) - 1.0) + static_cast<double>(lo.x));
-    const double y = (static_cast<double>(hi.y) - 1.0) + ((static_cast<double>(mid.y) - 1.0) + static_cast<double>(lo.y));
-    return x + y;
+  __device__ __forceinline__ Wide value() const {
+    float e, f;
+    const float s = two_sum(__fsub_rn(hi.x, 1.f), __fsub_rn(hi.y, 1.f), e);
+    const float t = two_sum(__fsub_rn(mid.x, 1.f), __fsub_rn(mid.y, 1.f), f);
+    float r;
+    const float h = two_sum(s, t, r);
+    return Wide(h, __fadd_rn(__fadd_rn(r, __fadd_rn(e, f)), __fadd_rn(lo.x, lo.y)));
   }
 };
+
+// log2 of a positive number, to 2^-38: the hardware's logarithm of its significand f, put right by
+// what f 2^-log2(f) is above 1.
+__device__ __forceinline__ Wide log2_wide(const Wide& s, const uint2* powers) {
+  const int bits = __float_as_int(s.h), n = (bits >> 23) - 127;
+  const float down = __int_as_float((127 - n) << 23);
+  Wide f;
+  f.h = __fmul_rn(s.h, down);
+  f.l = __fmul_rn(s.l, down);
+  const float y = __log2f(f.h);
+  FineExp e;
+  e.init(1.f, 0.f, 1.f, 0.f, 0.f, false);
+  const Wide over = f * e.at<true, false>(-y, powers).value() - Wide(1.f);
+  const float fix = __fmul_rn(over.h, fmaf(over.h, -0x1.715476p-1f, 0x1.715476p+0f));  // log2(e) (x - x^2 / 2)
+  return Wide(static_cast<float>(n)) + Wide(y) + Wide(fix);
+}
 
 }  // namespace
 }  // namespace rl

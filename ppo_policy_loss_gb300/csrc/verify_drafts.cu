@@ -44,7 +44,7 @@ constexpr int kMaxCluster = 16, kMaxParts = kMaxCluster * kWarps;
 constexpr double kLog2eD = 1.4426950408889634074;
 constexpr float kCoarse = 0x1.4p-17f;  // two sums of 72 2^-24 each, rounded up
 constexpr float kFar = 0x1p20f;       // |m c| beyond which m - 124 / c is near m's own last place
-constexpr double kNothing = 0x1p-90;  // sums of weights that are 0 (2^-124 each) stay below
+constexpr float kNothing = 0x1p-90f;  // sums of weights that are 0 (2^-124 each) stay below
 
 struct Args {
   const unsigned char* target;
@@ -94,7 +94,7 @@ enum Verdict { kStays, kRefused, kNoDistribution };
 // one has passed the barrier behind which everybody had read the other.
 struct Exchange {
   Stats stats[kMaxParts];
-  double sum[kMaxParts], plus[kMaxParts];
+  Wide sum[kMaxParts], plus[kMaxParts];
   float drafted[kMaxParts];
   long long token;
   int unsure;
@@ -104,12 +104,12 @@ struct Smem {
   unsigned long long full[kWarps][kSlots];
   uint2 powers[kPow];
   Exchange ex[2];
-  double sums[kWarps];   // of the search
+  Wide sums[kWarps];   // of the search
   float coarse[kWarps];
-  double before, total;
   float gap;
   long long found;
-  int verdict, at;
+  int verdict;
+  Wide u;              // for the draw
 };
 
 // ------------------------------------------------------------------ the cluster
@@ -353,7 +353,8 @@ __device__ __forceinline__ double draft_prob(float z, float lse, const Args& a, 
   if (!(x > -120.0 && x < 1.5 && fabs(m) < 4096.0)) return exp(static_cast<double>(z) * a.inv_t - static_cast<double>(lse));
   FineExp q;
   q.init(a.c, a.c_lo, a.unit, static_cast<float>(m), static_cast<float>(k - m * a.c_d), false);
-  return q.template at<true, false>(z, powers).value();
+  const Wide v = q.template at<true, false>(z, powers).value();
+  return static_cast<double>(v.h) + static_cast<double>(v.l);
 }
 
 template <int DT, int MODE, bool kFine>
@@ -409,7 +410,7 @@ struct Weights {
     for (int j = 0; j < F::kVec; ++j) {
       const Term x1 = j & 1 ? w[j / 2].y() : w[j / 2].x();
       if constexpr (kFine)
-        x[j] = p.is_zero(z[j]) ? 0.0 : x1.value();
+        x[j] = p.is_zero(z[j]) ? Wide(0.f) : x1.value();
       else
         x[j] = x1.a;
     }
@@ -419,15 +420,15 @@ struct Weights {
 template <class N>
 __device__ __forceinline__ N warp_sum(N v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1) v += from_xor(v, o);
   return v;
 }
 
 // The warp's sum over [lo, hi) in fine arithmetic, whole vectors from lo.
 template <int DT, int MODE>
-__device__ __forceinline__ double part_sum(Weights<DT, MODE, true>& f, long long lo, long long hi, int lane) {
+__device__ __forceinline__ Wide part_sum(Weights<DT, MODE, true>& f, long long lo, long long hi, int lane) {
   using F = Fmt<DT>;
-  double total = 0.0;
+  Wide total(0.f);
   FineSum s;
   s.clear();
   int n = 0;
@@ -467,23 +468,23 @@ __device__ __forceinline__ float part_sum(Weights<DT, MODE, false>& f, long long
 // what is before it (past the last weight, a rounding: the last one that has any; -1: none has).
 // `none`: what a sum of nothing stays below.  Whole warp.
 template <class N, int kPer>
-__device__ __forceinline__ int find_part(const N (&v)[kPer], N want, N none, N& before, int lane) {
+__device__ __forceinline__ int find_part(const N (&v)[kPer], N want, float none, N& before, int lane) {
   N own = v[0];
 #pragma unroll
   for (int j = 1; j < kPer; ++j) own += v[j];
   N upto = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const N up = __shfl_up_sync(0xffffffffu, upto, o);
+    const N up = from_below(upto, o);
     if (lane >= o) upto += up;
   }
-  N run = __shfl_up_sync(0xffffffffu, upto, 1);
-  if (lane == 0) run = N(0);
+  N run = from_below(upto, 1);
+  if (lane == 0) run = N(0.f);
   int at = -1, last = -1;
-  N at_before = N(0), last_before = N(0);
+  N at_before = N(0.f), last_before = N(0.f);
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    if (v[j] > none) {
+    if (static_cast<float>(v[j]) > none) {
       last = lane * kPer + j;
       last_before = run;
       if (at < 0 && run + v[j] > want) {
@@ -495,7 +496,7 @@ __device__ __forceinline__ int find_part(const N (&v)[kPer], N want, N none, N& 
   }
   const uint32_t hit = __ballot_sync(0xffffffffu, at >= 0), some = __ballot_sync(0xffffffffu, last >= 0);
   const int src = hit ? __ffs(hit) - 1 : some ? 31 - __clz(some) : 0;
-  before = __shfl_sync(0xffffffffu, hit ? at_before : last_before, src);
+  before = from_lane(hit ? at_before : last_before, src);
   return __shfl_sync(0xffffffffu, hit ? at : last, src);
 }
 
@@ -506,7 +507,7 @@ __device__ __forceinline__ void search(Weights<DT, MODE, kFine>& f, long long be
   using F = Fmt<DT>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kStep = 32 * F::kVec;
-  constexpr double none = kFine && MODE != kRest ? kNothing : 0.0;
+  constexpr float none = kFine && MODE != kRest ? kNothing : 0.f;
   while (end - begin > 2 * kStep) {
     const long long size = part_size(end - begin, kWarps, kStep);
     const long long lo = min(end, begin + warp * size), hi = min(end, lo + size);
@@ -519,57 +520,43 @@ __device__ __forceinline__ void search(Weights<DT, MODE, kFine>& f, long long be
     __syncthreads();
     if (lane == 0) sums[warp] = s;
     __syncthreads();
-    if (!kFine || warp == 0) {
-      N v[1], before;
-      v[0] = lane < kWarps ? sums[lane] : N(0);
-      const int at = max(0, find_part(v, want, N(none), before, lane));
-      if (kFine) {
-        if (lane == 0) {
-          sm.at = at;
-          sm.before = before;
-        }
-      } else {
-        begin = min(end, begin + at * size);
-        want -= before;
-      }
-    }
-    if (kFine) {
-      __syncthreads();
-      begin = min(end, begin + sm.at * size);
-      want -= N(sm.before);
-    }
+    N v[1], before;
+    v[0] = lane < kWarps ? sums[lane] : N(0.f);
+    const int at = max(0, find_part(v, want, none, before, lane));
+    want -= before;
+    begin = min(end, begin + at * size);
     end = min(end, begin + size);
   }
   __syncthreads();
   if (warp == 0) {
     long long found = -1, last = -1;
-    N near = N(0);
+    N near = N(0.f);
     for (long long base = begin; base < end && found < 0; base += kStep) {
       const long long i = base + lane * F::kVec;
       N x[F::kVec];
 #pragma unroll
-      for (int j = 0; j < F::kVec; ++j) x[j] = N(0);
+      for (int j = 0; j < F::kVec; ++j) x[j] = N(0.f);
       if (i < end) f.exactly(i, end, x);
-      N sum = N(0);
+      N sum = N(0.f);
 #pragma unroll
       for (int j = 0; j < F::kVec; ++j) sum += x[j];
       N upto = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const N up = __shfl_up_sync(0xffffffffu, upto, o);
+        const N up = from_below(upto, o);
         if (lane >= o) upto += up;
       }
-      N run = __shfl_up_sync(0xffffffffu, upto, 1);
-      if (lane == 0) run = N(0);
+      N run = from_below(upto, 1);
+      if (lane == 0) run = N(0.f);
       long long mine = -1, mine_last = -1;
-      N mine_near = N(0);
+      N mine_near = N(0.f);
 #pragma unroll
       for (int j = 0; j < F::kVec; ++j) {
-        if (x[j] > N(0)) {
+        if (static_cast<float>(x[j]) > 0.f) {
           mine_last = i + j;
           if (mine < 0 && run + x[j] > want) {
             mine = i + j;
-            mine_near = min(want - run, run + x[j] - want);
+            mine_near = smaller(want - run, run + x[j] - want);
           }
         }
         run += x[j];
@@ -577,11 +564,11 @@ __device__ __forceinline__ void search(Weights<DT, MODE, kFine>& f, long long be
       const uint32_t who = __ballot_sync(0xffffffffu, mine >= 0);
       if (who) {
         found = __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
-        near = __shfl_sync(0xffffffffu, mine_near, __ffs(who) - 1);
+        near = from_lane(mine_near, __ffs(who) - 1);
       }
       const uint32_t some = __ballot_sync(0xffffffffu, mine_last >= 0);
       if (some) last = __shfl_sync(0xffffffffu, mine_last, 31 - __clz(some));
-      want -= __shfl_sync(0xffffffffu, upto, 31);
+      want -= from_lane(upto, 31);
     }
     if (lane == 0) {
       sm.found = found >= 0 ? found : last;
@@ -615,36 +602,28 @@ __device__ __forceinline__ long long draw(Weights<DT, MODE, kFine>& f, int at, N
 template <int DT, int MODE>
 __device__ __forceinline__ void tell_sum(Weights<DT, MODE, true>& f, long long lo, long long hi, Group& g, Smem& sm) {
   const int lane = threadIdx.x & 31, part = g.rank * kWarps + (threadIdx.x >> 5);
-  const double s = part_sum(f, lo, hi, lane);
+  const Wide s = part_sum(f, lo, hi, lane);
   g.turn ^= 1;
   tell(g, &sm.ex[g.turn].sum[part], s, lane);
   g.sync();
 }
 template <int DT, int MODE>
-__device__ __forceinline__ long long draw_fine(Weights<DT, MODE, true>& f, const double* sums, double u, long long V, long long size,
-                                               Group& g, Smem& sm) {
+__device__ __forceinline__ long long draw_fine(Weights<DT, MODE, true>& f, const Wide* sums, long long V, long long size, Group& g,
+                                               Smem& sm) {
   const int lane = threadIdx.x & 31, parts = g.size * kWarps;
-  constexpr double none = MODE != kRest ? kNothing : 0.0;
-  if (threadIdx.x < 32) {
-    double v[kMaxParts / 32], own = 0.0, before;
+  constexpr float none = MODE != kRest ? kNothing : 0.f;
+  Wide v[kMaxParts / 32], own(0.f), before;
 #pragma unroll
-    for (int j = 0; j < kMaxParts / 32; ++j) {
-      const int i = lane * (kMaxParts / 32) + j;
-      v[j] = i < parts ? sums[i] : 0.0;
-      own += v[j];
-    }
-    const double total = warp_sum(own), want = u * total;
-    const int at = total > none ? find_part(v, want, none, before, lane) : -1;
-    if (lane == 0) {
-      sm.at = at;
-      sm.before = want - before;
-    }
+  for (int j = 0; j < kMaxParts / 32; ++j) {
+    const int i = lane * (kMaxParts / 32) + j;
+    v[j] = i < parts ? sums[i] : Wide(0.f);
+    own += v[j];
   }
-  __syncthreads();
-  const int at = sm.at;  // the same in every CTA
+  const Wide total = warp_sum(own), want = sm.u * total;
+  const int at = total.h > none ? find_part(v, want, none, before, lane) : -1;  // the same in every CTA
   if (at < 0) return -1;
   bool sure;
-  return draw<DT, MODE, true, double>(f, at, sm.before, -1.f, V, size, g, sm, sure);
+  return draw<DT, MODE, true, Wide>(f, at, want - before, -1.f, V, size, g, sm, sure);
 }
 
 template <int DT>
@@ -667,7 +646,13 @@ verify_drafts_kernel(const Args a, int cluster) {
   static_assert(kPow == kThreads, "one power a thread");
   sm.powers[tid] = kPowers[tid];
   if (tid < kWarps * kSlots) mbar_init(smem_addr(&sm.full[0][0]) + 8 * tid, 1);
-  if (tid == 0) abort_word = 0;
+  if (tid == 0) {
+    abort_word = 0;
+    double u = a.u[b * rows + G];
+    u = u > 0.0 ? fmin(u, 1.0 - 0x1p-53) : 0.0;
+    const float h = static_cast<float>(u);
+    sm.u = Wide(h, static_cast<float>(u - static_cast<double>(h)));
+  }
   fence_mbar_init();
   long long id = 0;
   if (tid < G) id = a.ids[b * G + tid];
@@ -766,7 +751,8 @@ verify_drafts_kernel(const Args a, int cluster) {
           v = left < w.a ? kStays : kRefused;
         } else {
           const double qd = a.draft ? draft_prob<DT>(zq, lq, a, sm.powers) : 1.0;
-          v = ui * qd * (static_cast<double>(st.n) + static_cast<double>(st.s)) < w.value() ? kStays : kRefused;
+          const Wide p = w.value();
+          v = ui * qd * (static_cast<double>(st.n) + static_cast<double>(st.s)) < static_cast<double>(p.h) + static_cast<double>(p.l) ? kStays : kRefused;
         }
       }
       sm.verdict = v;
@@ -788,28 +774,29 @@ verify_drafts_kernel(const Args a, int cluster) {
 
   long long token = -1;
   if (!bad) {
-    double u = a.u[b * rows + G];
-    u = u > 0.0 ? fmin(u, 1.0 - 0x1p-53) : 0.0;
     const unsigned char* draft_row = a.draft ? a.draft + (b * G + kept) * a.draft_bytes : nullptr;
     bool done = false;
     if (lost && a.draft) {
       // S q_v = 2^(z c - k), k = lse_q log2(e) - log2 S, in the frame of a number with few digits
       Weights<DT, kRest, true> f{row, draft_row, -1, 0.f, 0.f, fp, fp, sm.powers};
-      const double S = static_cast<double>(st.n) + static_cast<double>(st.s);
-      if (tid == 0) sm.total = S;
+      Wide total;
+      total.h = two_sum(st.n, st.s, total.l);
+      const Wide S = total;
+      const float lq = a.draft_lse[b * G + kept];
+      Wide log2e;
+      log2e.h = 0x1.715476p+0f;
+      log2e.l = 0x1.4ae0c0p-26f;
 #pragma unroll 1
       for (int pass = 0; pass < 2; ++pass) {
-        if (tid == 0) {
-          const double k = static_cast<double>(a.draft_lse[b * G + kept]) * kLog2eD - log2(sm.total);
-          const float mq = static_cast<float>(rint(k * a.t_ln2 * 4096.0) * (1.0 / 4096.0));
-          sm.coarse[0] = mq;
-          sm.coarse[1] = static_cast<float>(k - static_cast<double>(mq) * a.c_d);
-        }
-        __syncthreads();
-        f.q.init(a.c, a.c_lo, a.unit, sm.coarse[0], sm.coarse[1], fabsf(sm.coarse[0]) * a.c > kFar);
+        const Wide k = Wide(lq) * log2e - log2_wide(total, sm.powers);
+        const float mq = rintf(k.h * a.unit * 4096.f) * 0x1p-12f;
+        Wide c2;
+        c2.h = a.c;
+        c2.l = a.c_lo;
+        f.q.init(a.c, a.c_lo, a.unit, mq, (k - Wide(mq) * c2).h, fabsf(mq) * a.c > kFar);
         if (pass == 1) break;
         // sums of p over all tokens, and of p - q and of q over those with p > q
-        double all = 0.0, plus = 0.0;
+        Wide all(0.f), plus(0.f);
         FineSum fa, fb;
         fa.clear();
         fb.clear();
@@ -843,32 +830,31 @@ verify_drafts_kernel(const Args a, int cluster) {
         bad = __any_sync(0xffffffffu, bad);
         g.turn ^= 1;
         Exchange& ex = sm.ex[g.turn];
-        tell(g, &ex.sum[part], bad ? -1.0 : all, lane);
+        tell(g, &ex.sum[part], bad ? Wide(-1.f) : all, lane);
         tell(g, &ex.plus[part], plus, lane);
         tell(g, &ex.drafted[part], drafted, lane);
         g.sync();
-        if (warp == 0) {
-          double total = 0.0;
-          bad = false;
-          for (int k = lane; k < parts; k += 32) {
-            bad = bad || ex.sum[k] < 0.0;
-            total += ex.sum[k];
-          }
-          total = warp_sum(total);
-          bad = __any_sync(0xffffffffu, bad);
-          const double more = total / S - 1.0;  // q's terms were taken with S, and belong to `total`
-          for (int k = lane; k < parts; k += 32) ex.plus[k] = fmax(0.0, ex.plus[k] - more * static_cast<double>(ex.drafted[k]));
-          if (lane == 0) {
-            sm.total = total;
-            sm.verdict = bad;
+        total = Wide(0.f);
+        bad = false;
+        for (int j = lane; j < parts; j += 32) {
+          bad = bad || ex.sum[j].h < 0.f;
+          total += ex.sum[j];
+        }
+        total = warp_sum(total);
+        bad = __any_sync(0xffffffffu, bad);
+        if (bad) break;
+        __syncthreads();
+        if (warp == 0) {  // q's terms were taken with S, and belong to `total`
+          const float more = (total - S).h / S.h;
+          for (int j = lane; j < parts; j += 32) {
+            const Wide r = ex.plus[j] - Wide(more * ex.drafted[j]);
+            ex.plus[j] = r.h > 0.f ? r : Wide(0.f);
           }
         }
         __syncthreads();
-        bad = sm.verdict;
-        if (bad) break;
       }
       if (!bad) {
-        token = draw_fine(f, sm.ex[g.turn].plus, u, V, size, g, sm);
+        token = draw_fine(f, sm.ex[g.turn].plus, V, size, g, sm);
         done = token >= 0;
       }
     } else {
@@ -885,7 +871,7 @@ verify_drafts_kernel(const Args a, int cluster) {
           if (without && d_out >= k * size && d_out < (k + 1) * size) v[j] = fmaxf(0.f, v[j] - ex2_approx(fmaf(F::load(row, d_out), a.c, nm)));
           own += v[j];
         }
-        const float total = warp_sum(own), want = static_cast<float>(u) * total;
+        const float total = warp_sum(own), want = sm.u.h * total;
         const int at = max(0, find_part(v, want, 0.f, before, lane));
         bool sure;
         long long t;
@@ -904,14 +890,14 @@ verify_drafts_kernel(const Args a, int cluster) {
       if (!done && without) {
         Weights<DT, kWithout, true> f{row, nullptr, d_out, 0.f, 0.f, fp, fp, sm.powers};
         tell_sum(f, lo, hi, g, sm);
-        token = draw_fine(f, sm.ex[g.turn].sum, u, V, size, g, sm);
+        token = draw_fine(f, sm.ex[g.turn].sum, V, size, g, sm);
         done = token >= 0;
       }
     }
     if (!done && !bad) {
       Weights<DT, kSoftmax, true> f{row, nullptr, -1, 0.f, 0.f, fp, fp, sm.powers};
       tell_sum(f, lo, hi, g, sm);
-      token = draw_fine(f, sm.ex[g.turn].sum, u, V, size, g, sm);
+      token = draw_fine(f, sm.ex[g.turn].sum, V, size, g, sm);
     }
     bad = bad || token < 0;
   }
