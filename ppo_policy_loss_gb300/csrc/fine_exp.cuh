@@ -181,17 +181,21 @@ struct Term2 {
 };
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// Sums, differences and products of pairs, all as FMAs: the packed addition and product take
+// twice as long to give their result, which counts where an SM has few warps.
+__device__ __forceinline__ float2 add2(float2 x, float2 y) { return __ffma2_rn(x, both(1.f), y); }
 __device__ __forceinline__ float2 sub2(float2 x, float2 y) { return __ffma2_rn(y, both(-1.f), x); }
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) { return __ffma2_rn(x, y, both(-0.f)); }
 
 // the same for two numbers at a time
 __device__ __forceinline__ float2 two_sum2(float2 x, float2 y, float2& err) {
-  const float2 s = __fadd2_rn(x, y), t = sub2(s, x);
-  err = __fadd2_rn(sub2(x, sub2(s, t)), sub2(y, t));
+  const float2 s = add2(x, y), t = sub2(s, x);
+  err = add2(sub2(x, sub2(s, t)), sub2(y, t));
   return s;
 }
 // and for |x| >= |y|
 __device__ __forceinline__ float2 quick_two_sum2(float2 x, float2 y, float2& err) {
-  const float2 s = __fadd2_rn(x, y);
+  const float2 s = add2(x, y);
   err = sub2(y, sub2(s, x));
   return s;
 }
@@ -227,27 +231,27 @@ struct FineExp {
       d = two_sum2(z, both(-m), r);
     else
       d = quick_two_sum2(both(-m), z, r);
-    const float2 nx = __fmul2_rn(d, both(-c_hi));
+    const float2 nx = mul2(d, both(-c_hi));
     float2 gl = __ffma2_rn(r, both(c_hi), both(-kappa));
-    gl = __fadd2_rn(__ffma2_rn(d, both(c_hi), nx), __ffma2_rn(d, both(c_lo), gl));
+    gl = add2(__ffma2_rn(d, both(c_hi), nx), __ffma2_rn(d, both(c_lo), gl));
     constexpr float kMagic = 49152.f;  // 1.5 2^15: its last place is 1 / 256, its bits from the 20th on only
     const float2 t = __ffma2_rn(d, both(c_hi), both(kMagic));
-    const float2 gn = __fadd2_rn(nx, __fadd2_rn(t, both(-kMagic)));  // -gh
+    const float2 gn = add2(nx, add2(t, both(-kMagic)));  // -gh
     const uint32_t t0 = __float_as_uint(t.x), t1 = __float_as_uint(t.y);
     const uint2 p0 = powers[t0 & (kPow - 1)], p1 = powers[t1 & (kPow - 1)];
-    gl = __fadd2_rn(gl, make_float2(__uint_as_float(p0.y), __uint_as_float(p1.y)));
+    gl = add2(gl, make_float2(__uint_as_float(p0.y), __uint_as_float(p1.y)));
     const float2 g = sub2(gl, gn);
     constexpr float kLn2Hi = 0x1.62e430p-1f, kLn2Lo = -0x1.05c610p-29f;
-    const float2 u = __fmul2_rn(gn, both(-kLn2Hi));
+    const float2 u = mul2(gn, both(-kLn2Hi));
     float2 v = __ffma2_rn(gn, both(-kLn2Hi), make_float2(-u.x, -u.y));
     v = __ffma2_rn(gn, both(-kLn2Lo), v);
     v = __ffma2_rn(gl, both(kLn2Hi), v);
     const float2 q = __ffma2_rn(g, both(0x1.c6b08ep-5f), both(0x1.ebfbe0p-3f));  // ln^3 2 / 6, ln^2 2 / 2
-    v = __ffma2_rn(__fmul2_rn(g, g), q, v);
+    v = __ffma2_rn(mul2(g, g), q, v);
     Term2 p;
     // the exponent n: t's bits are those of the magic number + 256 n + j
     p.a = make_float2(__uint_as_float(p0.x + (t0 << 15)), __uint_as_float(p1.x + (t1 << 15)));
-    p.b = __fmul2_rn(p.a, u);
+    p.b = mul2(p.a, u);
     p.c = __ffma2_rn(p.a, v, __ffma2_rn(p.a, u, make_float2(-p.b.x, -p.b.y)));
     return p;
   }
@@ -258,7 +262,7 @@ struct FineExp {
   __device__ __forceinline__ bool is_zero(float z) const { return !((off != 0.f ? __fsub_rn(z, off) : z) > zmin); }
 };
 
-// The differences of two terms where they are positive, 0 elsewhere (more: 1 and 0).  Of positive
+// The differences of two terms, and 1 where they are positive, 0 elsewhere.  Of positive
 // differences the first number is the larger one in a, or the two are so near that
 // p.a - q.a is exact.
 __device__ __forceinline__ Term2 above(const Term2& p, const Term2& q, float2& more) {
@@ -266,12 +270,9 @@ __device__ __forceinline__ Term2 above(const Term2& p, const Term2& q, float2& m
   Term2 d;
   d.a = quick_two_sum2(p.a, make_float2(-q.a.x, -q.a.y), e);
   d.b = sub2(p.b, q.b);
-  d.c = __fadd2_rn(e, sub2(p.c, q.c));
-  const float2 s = __fadd2_rn(__fadd2_rn(d.a, d.b), d.c);
+  d.c = add2(e, sub2(p.c, q.c));
+  const float2 s = add2(add2(d.a, d.b), d.c);
   more = make_float2(s.x > 0.f ? 1.f : 0.f, s.y > 0.f ? 1.f : 0.f);
-  d.a = __fmul2_rn(d.a, more);
-  d.b = __fmul2_rn(d.b, more);
-  d.c = __fmul2_rn(d.c, more);
   return d;
 }
 
@@ -288,7 +289,15 @@ struct FineSum {
     float2 e, f;
     hi = quick_two_sum2(hi, p.a, e);
     mid = quick_two_sum2(mid, p.b, f);
-    lo = __fadd2_rn(lo, __fadd2_rn(__fadd2_rn(e, f), p.c));
+    lo = add2(lo, add2(add2(e, f), p.c));
+  }
+  // the same times 1 or 0
+  __device__ __forceinline__ void add(const Term2& p, float2 times) {
+    const float2 h = __ffma2_rn(times, p.a, hi), m = __ffma2_rn(times, p.b, mid);
+    const float2 e = __ffma2_rn(times, p.a, sub2(hi, h)), f = __ffma2_rn(times, p.b, sub2(mid, m));
+    hi = h;
+    mid = m;
+    lo = add2(__ffma2_rn(times, p.c, lo), add2(e, f));
   }
   __device__ __forceinline__ Wide value() const {
     float e, f;

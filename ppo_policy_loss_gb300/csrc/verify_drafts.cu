@@ -393,8 +393,13 @@ struct Weights {
         w[j].b = w[j].c = both(0.f);
       } else {
         w[j] = fine(zz);
-        float2 more;
-        if (MODE == kRest) w[j] = above(w[j], drafted(make_float2(y[2 * j], y[2 * j + 1])), more);
+        if (MODE == kRest) {
+          float2 more;
+          w[j] = above(w[j], drafted(make_float2(y[2 * j], y[2 * j + 1])), more);
+          w[j].a = mul2(w[j].a, more);
+          w[j].b = mul2(w[j].b, more);
+          w[j].c = mul2(w[j].c, more);
+        }
       }
     }
   }
@@ -813,7 +818,8 @@ verify_drafts_kernel(const Args a, int cluster) {
             const Term2 w = f.fine(make_float2(z[j], z[j + 1])), q = f.drafted(make_float2(y[j], y[j + 1]));
             float2 more;
             fa.add(w);
-            fb.add(above(w, q, more));
+            const Term2 r = above(w, q, more);
+            fb.add(r, more);
             qs = __ffma2_rn(more, q.a, qs);
           }
           if (++count == 64) {
