@@ -222,7 +222,7 @@ struct FineExp {
   // kWide: z has 24 significant bits (16-bit numbers have 8 or 11).  kTop: z may be above zmax.
   template <bool kWide, bool kTop>
   __device__ __forceinline__ Term2 at(float2 z, const uint2* powers) const {
-    if (off != 0.f) z = make_float2(__fsub_rn(z.x, off), __fsub_rn(z.y, off));
+    z = sub2(z, both(off));  // (a branch here would keep the pairs of a vector apart)
     z = make_float2(fmaxf(z.x, zmin), fmaxf(z.y, zmin));
     if (kTop) z = make_float2(fminf(z.x, zmax), fminf(z.y, zmax));
     // the difference and its error r; of 16-bit numbers that is 0 unless |z| is far below |m|
@@ -259,7 +259,7 @@ struct FineExp {
   __device__ __forceinline__ Term at(float z, const uint2* powers) const {
     return at<kWide, kTop>(both(z), powers).x();
   }
-  __device__ __forceinline__ bool is_zero(float z) const { return !((off != 0.f ? __fsub_rn(z, off) : z) > zmin); }
+  __device__ __forceinline__ bool is_zero(float z) const { return !(__fsub_rn(z, off) > zmin); }
 };
 
 // The differences of two terms, and 1 where they are positive, 0 elsewhere.  Of positive
