@@ -585,13 +585,13 @@ __device__ __forceinline__ void search(Weights<DT, MODE, kFine>& f, long long be
 
 // The CTA that has part `at` (of `size` elements) looks for the token there and tells the others.
 // The answer is sure if the border is more than `unsure` away from the ends of the token's weight.
-template <int DT, int MODE, bool kFine, class N>
-__device__ __forceinline__ long long draw(Weights<DT, MODE, kFine>& f, int at, N want, float unsure, long long V, long long size,
-                                          Group& g, Smem& sm, bool& sure) {
+template <int DT, int MODE>
+__device__ __forceinline__ long long draw_coarse(Weights<DT, MODE, false>& f, int at, float want, float unsure, long long V,
+                                                 long long size, Group& g, Smem& sm, bool& sure) {
   Exchange& ex = sm.ex[g.turn ^ 1];
   if (at / kWarps == g.rank) {
     const long long lo = min(V, at * size), hi = min(V, lo + size);
-    search<DT, MODE, kFine, N>(f, lo, hi, want, sm);
+    search<DT, MODE, false, float>(f, lo, hi, want, sm);
     if (threadIdx.x < 32) {
       tell(g, &ex.token, sm.found, threadIdx.x);
       tell(g, &ex.unsure, static_cast<int>(!(sm.gap > unsure)), threadIdx.x);
@@ -612,8 +612,11 @@ __device__ __forceinline__ void tell_sum(Weights<DT, MODE, true>& f, long long l
   tell(g, &sm.ex[g.turn].sum[part], s, lane);
   g.sync();
 }
+// The token, in the CTA that has it; kElsewhere in the others, which have nothing left to do;
+// kNowhere in all where no part has any weight.
+constexpr long long kElsewhere = -2, kNowhere = -3;
 template <int DT, int MODE>
-__device__ __forceinline__ long long draw_fine(Weights<DT, MODE, true>& f, const Wide* sums, long long V, long long size, Group& g,
+__device__ __forceinline__ long long draw_fine(Weights<DT, MODE, true>& f, const Wide* sums, long long V, long long size, const Group& g,
                                                Smem& sm) {
   const int lane = threadIdx.x & 31, parts = g.size * kWarps;
   constexpr float none = MODE != kRest ? kNothing : 0.f;
@@ -626,9 +629,18 @@ __device__ __forceinline__ long long draw_fine(Weights<DT, MODE, true>& f, const
   }
   const Wide total = warp_sum(own), want = sm.u * total;
   const int at = total.h > none ? find_part(v, want, none, before, lane) : -1;  // the same in every CTA
-  if (at < 0) return -1;
-  bool sure;
-  return draw<DT, MODE, true, Wide>(f, at, want - before, -1.f, V, size, g, sm, sure);
+  if (at < 0) return kNowhere;
+  if (at / kWarps != g.rank) return kElsewhere;
+  const long long lo = min(V, at * size), hi = min(V, lo + size);
+  search<DT, MODE, true, Wide>(f, lo, hi, want - before, sm);
+  long long t = sm.found;
+  if (MODE == kRest && t < 0) {  // p = q to the last digit kept in the whole part: its first token
+    for (long long i = lo; i < hi && t < 0; i += 32) {
+      const uint32_t some = __ballot_sync(0xffffffffu, i + lane < hi && !f.p.is_zero(Fmt<DT>::load(f.row, min(i + lane, hi - 1))));
+      if (some) t = i + __ffs(some) - 1;
+    }
+  }
+  return t;
 }
 
 template <int DT>
@@ -777,10 +789,9 @@ verify_drafts_kernel(const Args a, int cluster) {
     kept = i + 1;
   }
 
-  long long token = -1;
+  long long token = kNowhere;
   if (!bad) {
     const unsigned char* draft_row = a.draft ? a.draft + (b * G + kept) * a.draft_bytes : nullptr;
-    bool done = false;
     if (lost && a.draft) {
       // S q_v = 2^(z c - k), k = lse_q log2(e) - log2 S, in the frame of a number with few digits
       Weights<DT, kRest, true> f{row, draft_row, -1, 0.f, 0.f, fp, fp, sm.powers};
@@ -861,7 +872,6 @@ verify_drafts_kernel(const Args a, int cluster) {
       }
       if (!bad) {
         token = draw_fine(f, sm.ex[g.turn].plus, V, size, g, sm);
-        done = token >= 0;
       }
     } else {
       // the parts' sums of step 1 in the frame of the row, without the draft that was looked up
@@ -883,47 +893,43 @@ verify_drafts_kernel(const Args a, int cluster) {
         long long t;
         if (without) {
           Weights<DT, kWithout, false> f{row, nullptr, d_out, a.c, nm, fp, fp, sm.powers};
-          t = draw<DT, kWithout, false, float>(f, at, want - before, kCoarse * (st.n + st.s), V, size, g, sm, sure);
+          t = draw_coarse(f, at, want - before, kCoarse * (st.n + st.s), V, size, g, sm, sure);
         } else {
           Weights<DT, kSoftmax, false> f{row, nullptr, -1, a.c, nm, fp, fp, sm.powers};
-          t = draw<DT, kSoftmax, false, float>(f, at, want - before, kCoarse * (st.n + st.s), V, size, g, sm, sure);
+          t = draw_coarse(f, at, want - before, kCoarse * (st.n + st.s), V, size, g, sm, sure);
         }
-        if (sure && t >= 0) {
-          token = t;
-          done = true;
-        }
+        if (sure && t >= 0) token = g.rank == 0 ? t : kElsewhere;
       }
-      if (!done && without) {
+      if (token == kNowhere && without) {
         Weights<DT, kWithout, true> f{row, nullptr, d_out, 0.f, 0.f, fp, fp, sm.powers};
         tell_sum(f, lo, hi, g, sm);
         token = draw_fine(f, sm.ex[g.turn].sum, V, size, g, sm);
-        done = token >= 0;
       }
     }
-    if (!done && !bad) {
+    if (token == kNowhere && !bad) {
       Weights<DT, kSoftmax, true> f{row, nullptr, -1, 0.f, 0.f, fp, fp, sm.powers};
       tell_sum(f, lo, hi, g, sm);
       token = draw_fine(f, sm.ex[g.turn].sum, V, size, g, sm);
     }
-    bad = bad || token < 0;
   }
   in.drain(abort_flag);
   if (*abort_flag && lane == 0 && a.status) atomicOr(a.status, RL_DEVERR_TIMEOUT);
-  if (g.rank == 0) {
-    for (int i = tid; i <= G; i += kThreads) {
-      if (i > kept) {
-        tokens[i] = -1;
-        if (logp) logp[i] = 0.f;
-        if (lse) lse[i] = 0.f;
-      }
-    }
-    if (tid == 0) {
-      if (a.n_accepted) a.n_accepted[b] = kept;
-      tokens[kept] = bad ? -1 : token;
-      if (logp) logp[kept] = bad ? nan : log_prob(F::load(row, token), st, a.inv_t);
+  // One CTA writes: the one that found the token, or the first.  (Nobody writes another's shared
+  // memory behind the last barrier, so all may leave as they are done.)
+  if (token == kElsewhere || (token == kNowhere && g.rank != 0)) return;
+  bad = bad || token < 0;
+  for (int i = tid; i <= G; i += kThreads) {
+    if (i > kept) {
+      tokens[i] = -1;
+      if (logp) logp[i] = 0.f;
+      if (lse) lse[i] = 0.f;
     }
   }
-  if (cluster > 1) cluster_sync_all();  // nobody leaves while its shared memory may be written
+  if (tid == 0) {
+    if (a.n_accepted) a.n_accepted[b] = kept;
+    tokens[kept] = bad ? -1 : token;
+    if (logp) logp[kept] = bad ? nan : log_prob(F::load(row, token), st, a.inv_t);
+  }
 }
 
 // CTAs of a cluster: the power of two with which all are at work at once, at most 16, and no
