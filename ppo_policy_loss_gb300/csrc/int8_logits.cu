@@ -15,14 +15,14 @@
 //   * warps 0 and 2 (one lane each): TMA producers of two rings: 8-bit weight tiles (128
 //     channels x 128 columns, 16 KB) and fp16 token tiles (N x 128 columns).
 //     Where all columns of a single token tile fit (small batches), they are loaded once and stay.
-//   * warps 4-7: one channel a thread.  A 128-byte row of codes from shared memory, widened
+//   * warps 4-7 and 12-15, step by step in turn: one channel a thread.  A 128-byte row of codes from shared memory, widened
 //     in registers (4 codes: one XOR, two byte permutes to 1024 + code + 128,
 //     two fp16 subtractions), and stored to tensor memory: the A operand of
 //     tcgen05.mma comes from there, so that widened weights cost no
 //     shared-memory traffic, which the token tiles already keep busy.
 //   * warp 1: tcgen05.mma.kind::f16, M = 128, K = 16, into one of two
 //     accumulators of N columns.
-//   * warps 8-11 and 12-15: epilogue, a channel a lane: scales, rounding, and stores of
+//   * warps 8-11: epilogue, a channel a lane: scales, rounding, and stores of
 //     32 neighbouring channels of a token at a time.
 //   * N is a multiple of 16 up to 192 (2 accumulators of 192 columns and two widened tiles
 //     of 64 fill the 512 columns of tensor memory); 128 where sums stay in the epilogue's registers (D > 1024).
@@ -125,15 +125,7 @@ __device__ __forceinline__ void umma_commit_elect(uint32_t bar) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
-// 16 consecutive columns of this thread's TMEM lane; wait_ld() before they are used.
-__device__ __forceinline__ void tmem_ld16_issue(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-// 32 of them.
+// 32 consecutive columns of this thread's TMEM lane; tmem_wait_ld() before they are used.
 __device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
@@ -288,13 +280,13 @@ __device__ __forceinline__ void store32(const uint32_t (&x)[32], const float* sc
 
 // (Loops stay rolled: an unrolled role is a kilobyte of instructions that each call fetches
 // from HBM, 1200 cycles a line, for the weights before it have swept them out of L2.)
-// Threads of a CTA: sums over many columns stay in the epilogue's registers, which
-// leaves room for one group of four epilogue warps instead of two.
-__host__ __device__ constexpr int int8_threads(bool deep) { return deep ? 384 : 512; }
+// Threads of a CTA.  Warps 12-15 widen every other step, or where sums over many columns are
+// kept in registers share the epilogue.
+constexpr int kThreadsI = 512;
 constexpr int kChunkN = 32;  // columns of an accumulator that an epilogue warp takes at a time
 
 template <class T, bool kDeep>
-__global__ void __launch_bounds__(int8_threads(kDeep), 1)
+__global__ void __launch_bounds__(kThreadsI, 1)
 logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h, const IArgs a) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ Bars sm;
@@ -304,7 +296,8 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int n_units = a.n_tt * a.n_vt, steps = a.steps, N = a.N;
   const uint32_t slots_a = a.slots_a, slots_b = a.slots_b, slots_w = a.slots_w, slots_d = a.slots_d;
-  constexpr int kEpilogue = kDeep ? 4 : 8;  // epilogue warps
+  constexpr int kEpilogue = kDeep ? 8 : 4;  // epilogue warps
+  constexpr int kGroups = kDeep ? 1 : 2;  // of four widening warps, which take the steps in turn
 
   if (tid == 0) {
     for (int s = 0; s < a.slots_a; ++s) {
@@ -437,17 +430,27 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
       umma_commit_elect(smem_addr(&sm.drain));
       tc_wait<true>(smem_addr(&sm.drain), 0, abort_flag);
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if ((warp >= 4 && warp < 8) || (!kDeep && warp >= 12)) {
     // ---------------------------------------------------------------- widening
     const int q = warp & 3, row = q * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
     Place pa, pw, pd;
-    uint32_t ahead = slots_w;  // tiles that no step has to free
+    const int turn = warp >= 12 ? 1 : 0;
+    uint32_t ahead = slots_w, step = 0;  // ahead: tiles that no step has to free
     bool stop = false;
 #pragma unroll 1
     for (int u = blockIdx.x; u < n_units && !stop; u += gridDim.x) {
 #pragma unroll 1
-      for (int k = 0; k < steps; ++k) {
+      for (int k = 0; k < steps; ++k, ++step) {
+        if (kGroups == 2 && static_cast<int>(step & 1) != turn) {  // (no phase is missed: it ends behind this group's next step)
+          if (ahead > 0)
+            --ahead;
+          else
+            pd.next(slots_d);
+          pa.next(slots_a);
+          pw.next(slots_w);
+          continue;
+        }
         bool ok = warp_wait(smem_addr(&sm.full_a[pa.i]), pa.parity, abort_flag);
         if (ahead > 0) {
           --ahead;
@@ -494,61 +497,71 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     uint32_t parity = 0;
     bool stop = false;
     const int n_chunks = (a.steps + kChunkSteps - 1) / kChunkSteps;
-    float mine = 0.f;  // a token's scale
-    if (static_cast<int>(blockIdx.x) < n_units) {
+    constexpr int kMine = (kMaxN + kEpilogue * 32 - 1) / (kEpilogue * 32);
+    float mine[kMine];  // scales of the unit's tokens me, me + 32 kEpilogue
+    const auto load_scales = [&](int u) {
       int tt, vt;
-      unit_tile(blockIdx.x, a.n_tt, a.n_vt, a.group, tt, vt);
-      const long long r = static_cast<long long>(tt) * a.N + me;
-      mine = me < a.N && r < a.R ? __ldg(a.scale_h + r) : 0.f;
-    }
+      unit_tile(u, a.n_tt, a.n_vt, a.group, tt, vt);
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        const int i = me + j * kEpilogue * 32;
+        const long long r = static_cast<long long>(tt) * N + i;
+        mine[j] = i < N && r < a.R ? __ldg(a.scale_h + r) : 0.f;
+      }
+    };
+    if (static_cast<int>(blockIdx.x) < n_units) load_scales(blockIdx.x);
 #pragma unroll 1
     for (int u = blockIdx.x; u < n_units; u += gridDim.x, parity ^= 1) {
       int tt, vt;
       unit_tile(u, a.n_tt, a.n_vt, a.group, tt, vt);
-      const long long v = static_cast<long long>(vt) * kM + row, r0 = static_cast<long long>(tt) * a.N;
-      const int n = static_cast<int>(min(static_cast<long long>(a.N), a.R - r0));
+      const long long v = static_cast<long long>(vt) * kM + row, r0 = static_cast<long long>(tt) * N;
+      const int n = static_cast<int>(min(static_cast<long long>(N), a.R - r0));
       const bool here = v < a.V;
       const float sw = here ? a.scale_w[v] : 0.f;
       T* out = static_cast<T*>(a.out) + r0 * a.ld + v;
       // the tokens' scales, in turn in two places: the barrier keeps the warps within a unit of
       // one another.  The next unit's are on their way while this one's are used.
-      if (me < a.N) sm.scale[parity][me] = mine;
+#pragma unroll
+      for (int j = 0; j < kMine; ++j)
+        if (me + j * kEpilogue * 32 < N) sm.scale[parity][me + j * kEpilogue * 32] = mine[j];
       named_barrier(1, kEpilogue * 32);
-      if (u + static_cast<int>(gridDim.x) < n_units) {
-        int tn, vn;
-        unit_tile(u + gridDim.x, a.n_tt, a.n_vt, a.group, tn, vn);
-        const long long r = static_cast<long long>(tn) * a.N + me;
-        mine = me < a.N && r < a.R ? __ldg(a.scale_h + r) : 0.f;
-      }
+      if (u + static_cast<int>(gridDim.x) < n_units) load_scales(u + gridDim.x);
       Rows<T> to(static_cast<T*>(a.out) + (r0 + group * kChunkN) * a.ld, v, a.V, a.ld, lane);
-      int sum[kDeep ? kMaxNDeep : 1];
+      int sum[kDeep ? kMaxNDeep / 2 : 1];  // deep: chunks of 32 tokens go to the two groups of warps in turn
 #pragma unroll 1
       for (int ch = 0; ch < n_chunks; ++ch) {
         stop = stop || !warp_wait(smem_addr(&sm.acc_full[pc.i]), pc.parity, abort_flag);
         if (stop) break;
         tc_fence_after();
-        const uint32_t from = tmem + lane_addr + pc.i * a.N;
+        const uint32_t from = tmem + lane_addr + pc.i * N;
         if (kDeep) {
 #pragma unroll
-          for (int c = 0; c < kMaxNDeep / 16; ++c) {
-            if (c * 16 < a.N) {
-              uint32_t x[16];
-              tmem_ld16_issue(from + c * 16, x);
+          for (int c = 0; c < kMaxNDeep / 64; ++c) {
+            const int col = (2 * c + group) * kChunkN;
+            if (col < N) {
+              uint32_t x[32];
+              tmem_ld32_issue(from + col, x);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                sum[c * 16 + i] = __float2int_rn(__uint_as_float(x[i])) + (ch > 0 ? sum[c * 16 + i] : 0);
+              for (int i = 0; i < 32; ++i)
+                sum[c * 32 + i] = __float2int_rn(__uint_as_float(x[i])) + (ch > 0 ? sum[c * 32 + i] : 0);
             }
           }
         } else {
           const float* scale = sm.scale[parity];
+          uint32_t x[2][32];  // (columns behind N: what lies there, and goes nowhere)
+          tmem_ld32_issue(from, x[0]);
 #pragma unroll 1
-          for (int c = group * kChunkN; c < a.N; c += kEpilogue / 4 * kChunkN) {
-            uint32_t x[32];
-            tmem_ld32_issue(from + c, x);  // (behind N: what lies there, and goes nowhere)
+          for (int c = 0; c < N; c += 2 * kChunkN) {
             tmem_wait_ld();
-            store32(x, scale + c, sw, n - c, to);
-            to.next(kEpilogue / 4 * kChunkN);
+            if (c + kChunkN < N) tmem_ld32_issue(from + c + kChunkN, x[1]);
+            store32(x[0], scale + c, sw, n - c, to);
+            to.next(kChunkN);
+            if (c + kChunkN >= N) break;
+            tmem_wait_ld();
+            if (c + 2 * kChunkN < N) tmem_ld32_issue(from + c + 2 * kChunkN, x[0]);
+            store32(x[1], scale + c + kChunkN, sw, n - c - kChunkN, to);
+            to.next(kChunkN);
           }
         }
         tc_fence_before();
@@ -561,9 +574,16 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
           if (here) out[t * a.ld] = rounded<T>(__int_as_float(0x7fc00000));
       } else if (kDeep) {
 #pragma unroll
-        for (int i = 0; i < kMaxNDeep; ++i)
-          if (here && i < n)
-            out[i * a.ld] = rounded<T>(__fmul_rn(__fmul_rn(static_cast<float>(sum[i]), sm.scale[parity][i]), sw));
+        for (int c = 0; c < kMaxNDeep / 64; ++c) {
+          const int col = (2 * c + group) * kChunkN;
+          if (col < N) {
+            uint32_t x[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(static_cast<float>(sum[c * 32 + i]));
+            store32(x, sm.scale[parity] + col, sw, n - col, to);
+            to.next(2 * kChunkN);
+          }
+        }
       }
     }
   }
@@ -650,7 +670,7 @@ rl_status launch(const CUtensorMap& map_w, const CUtensorMap& map_h, const IArgs
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(int8_threads(kDeep));
+  cfg.blockDim = dim3(kThreadsI);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
