@@ -47,7 +47,7 @@ extern "C" {
  *           byte of it in x; columns D .. ld_c-1 are not written.
  *   scale : float [R].
  * Errors: RL_ERR_DTYPE, RL_ERR_SHAPE (R < 0, R >= 2^31, D < 1, D >= 2^31, a stride below
- * D), RL_ERR_NULL, RL_ERR_ALIGN, RL_ERR_ALIAS (codes in x), RL_ERR_CUDA.  R =
+ * D or so large that 64 bits do not address the rows), RL_ERR_NULL, RL_ERR_ALIGN, RL_ERR_ALIAS (codes in x), RL_ERR_CUDA.  R =
  * 0 launches nothing.
  */
 rl_status rl_quantize_rows_int8(const void* x, rl_dtype dtype, long long R, long long D, long long ld_x,
@@ -71,7 +71,8 @@ rl_status rl_quantize_rows_int8(const void* x, rl_dtype dtype, long long R, long
  *               need not be initialised; calls that may overlap take one each.
  *   1 <= D <= RL_INT8_MAX_D.
  * Errors: RL_ERR_DTYPE, RL_ERR_SHAPE (R < 0, R >= 2^31, V < 1, V >= 2^31, D out of
- * range, a stride too small), RL_ERR_NULL, RL_ERR_ALIGN, RL_ERR_ALIAS (logits
+ * range, a stride too small or so large that 64 bits do not address the rows, more than
+ * 2^30 tiles of 128 channels and 128 tokens), RL_ERR_NULL, RL_ERR_ALIGN, RL_ERR_ALIAS (logits
  * in hidden or weight), RL_ERR_WORKSPACE, RL_ERR_CUDA.  R = 0 launches
  * nothing.
  */
@@ -105,9 +106,10 @@ size_t rl_lmhead_int8_workspace_size(long long R, long long D);
  * So tokens are drawn as from p alone, whatever the drafts.  With G = 0 the
  * call draws one token for each row; lse_out is then what a later call takes
  * as draft_lse.  Rows behind the first draft that does not stay decide
- * nothing.  Differences between uniforms and the sums they are compared with
- * are resolved to 2^-34 of a total or better;
- * log-probabilities are fp32, with relative precision next to 0.
+ * nothing.  The drawn token's border is resolved to 2^-34 of the total (for
+ * max(p - q, 0) of p's total) or better, so that it is the same in any batch; a draft's own
+ * test to 2^-17 of p_i(d) (fp32's sum over the row).  Log-probabilities are
+ * fp32, with relative precision next to 0.
  *
  * n_draft[b] = -1 leaves a sequence out: its tokens are -1, the rest 0, nothing
  * of it is read.  A logit of -inf is a token of probability 0.  A row without a

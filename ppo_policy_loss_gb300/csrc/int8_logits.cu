@@ -108,6 +108,13 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return warp_wait_on(bar, parity, abort);
 }
 
+// Both of two.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t bar1, uint32_t parity1, volatile int* abort) {
+  const bool first = mbar_try_wait(bar, parity), second = mbar_try_wait(bar1, parity1);
+  if (__all_sync(0xffffffffu, first && second)) return true;
+  return warp_wait_on(bar, parity, abort) && warp_wait_on(bar1, parity1, abort);
+}
+
 // One lane of the warp issues.  (The whole warp runs the loop around it, so that the
 // compiler sees warp-uniform operands: from a single lane's registers each operand takes a
 // move to the uniform ones, and an instruction 110 cycles instead of 46.)
@@ -401,8 +408,8 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
           stop = true;
           break;
         }
-        if (!warp_wait(smem_addr(&sm.wide_full[pw.i]), pw.parity, abort_flag) ||
-            (!loaded && !warp_wait(smem_addr(&sm.full_b[pb.i]), pb.parity, abort_flag))) {
+        if (!(loaded ? warp_wait(smem_addr(&sm.wide_full[pw.i]), pw.parity, abort_flag)
+                     : warp_wait(smem_addr(&sm.full_b[pb.i]), pb.parity, smem_addr(&sm.wide_full[pw.i]), pw.parity, abort_flag))) {
           stop = true;
           break;
         }
@@ -451,11 +458,12 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
           pw.next(slots_w);
           continue;
         }
-        bool ok = warp_wait(smem_addr(&sm.full_a[pa.i]), pa.parity, abort_flag);
+        bool ok;
         if (ahead > 0) {
           --ahead;
+          ok = warp_wait(smem_addr(&sm.full_a[pa.i]), pa.parity, abort_flag);
         } else {
-          ok = ok && warp_wait(smem_addr(&sm.done[pd.i]), pd.parity, abort_flag);
+          ok = warp_wait(smem_addr(&sm.full_a[pa.i]), pa.parity, smem_addr(&sm.done[pd.i]), pd.parity, abort_flag);
           pd.next(slots_d);
         }
         if (!ok) {
@@ -707,12 +715,16 @@ extern "C" rl_status rl_lmhead_logits_int8(const signed char* hidden, long long 
       ld_w >= (1LL << 40) || ld >= (1LL << 40))
     return RL_ERR_SHAPE;
   if (R == 0) return RL_OK;
+  const IPlan p = int8_plan(R, D, V);
+  const long long units = static_cast<long long>(p.n_tt) * p.n_vt;
+  if (units > (1LL << 30)) return RL_ERR_SHAPE;
   if (!hidden || !weight || !scale_h || !scale_w || !logits) return RL_ERR_NULL;
   if ((reinterpret_cast<uintptr_t>(hidden) & 15) || (reinterpret_cast<uintptr_t>(weight) & 15) ||
       (reinterpret_cast<uintptr_t>(logits) & 15) || (reinterpret_cast<uintptr_t>(workspace) & 15) || (ld_h & 15) ||
       (ld_w & 15) || ((ld * es) & 15) || (reinterpret_cast<uintptr_t>(scale_h) & 3) ||
       (reinterpret_cast<uintptr_t>(scale_w) & 3))
     return RL_ERR_ALIGN;
+  if (R > (1LL << 60) / (ld * es) || R > (1LL << 60) / ld_h || V > (1LL << 60) / ld_w) return RL_ERR_SHAPE;  // more than 64 bits address
   const long long out_bytes = ((R - 1) * ld + V) * es;
   if (overlap(logits, out_bytes, hidden, (R - 1) * ld_h + D) || overlap(logits, out_bytes, weight, (V - 1) * ld_w + D))
     return RL_ERR_ALIAS;
@@ -720,7 +732,6 @@ extern "C" rl_status rl_lmhead_logits_int8(const signed char* hidden, long long 
   EncodeTiled enc = nullptr;
   int dev = 0, sms = 0;
   if (tc_encode_fn(&enc) != RL_OK || cudaGetDevice(&dev) != cudaSuccess || tc_device_sms(&sms) != RL_OK) return RL_ERR_CUDA;
-  const IPlan p = int8_plan(R, D, V);
   const long long ldw = wide_ld(D);
   CUtensorMap map_w, map_h;
   if (!byte_map(enc, &map_w, weight, V, D, ld_w) ||
@@ -745,8 +756,6 @@ extern "C" rl_status rl_lmhead_logits_int8(const signed char* hidden, long long 
   a.scale_w = scale_w;
   a.out = logits;
   a.status = status_dev;
-  const long long units = static_cast<long long>(p.n_tt) * p.n_vt;
-  if (units > (1LL << 30)) return RL_ERR_SHAPE;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const long long pieces = R * ((D + 15) / 16);
   widen_kernel<<<static_cast<unsigned>((pieces + kWidenThreads - 1) / kWidenThreads), kWidenThreads, 0, s>>>(

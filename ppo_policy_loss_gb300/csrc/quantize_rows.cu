@@ -221,6 +221,7 @@ extern "C" rl_status rl_quantize_rows_int8(const void* x, rl_dtype dtype, long l
     return RL_ERR_SHAPE;
   if (R == 0) return RL_OK;
   if (!x || !codes || !scale) return RL_ERR_NULL;
+  if (R > (1LL << 60) / (ld_x * es) || R > (1LL << 60) / ld_c) return RL_ERR_SHAPE;  // more than 64 bits address
   const uintptr_t xa = reinterpret_cast<uintptr_t>(x), ca = reinterpret_cast<uintptr_t>(codes);
   if ((xa & 15) || (ca & 15) || ((ld_x * es) & 15) || (ld_c & 15) || (reinterpret_cast<uintptr_t>(scale) & 3)) return RL_ERR_ALIGN;
   if (xa < ca + static_cast<uintptr_t>((R - 1) * ld_c + D) && ca < xa + static_cast<uintptr_t>(((R - 1) * ld_x + D) * es))

@@ -20,10 +20,10 @@
 //     p there, and W - S Q of the sums over that set takes the S of the same pass.
 //
 // fp32 sums, in units of 2^-24: a term 2^x carries 4 of the hardware exponential and 2 ln 2 |x|
-// of its argument (the FMA's rounding and c's), |x| weighted by p at most log2 V < 18 for 2^18
-// tokens; 32 terms are added in chains of 10, the chains' sums with their errors kept; then
+// of its argument (the FMA's rounding and c's), |x| weighted by p at most log2 V <= 26;
+// 32 terms are added in chains of 10, the chains' sums with their errors kept; then
 // 5 joins in the warp, 13 for the frames of lanes and warps, and 15 in the running sums of the
-// search: 72, and the same for S.  (fp64 is kept for what a single lane decides: the unit does
+// search: 83, and the same for S.  (fp64 is kept for what a single lane decides: the unit does
 // two operations a cycle and SM, and a warp that adds in fp64 holds it for 16 cycles.)
 #include <cuda_runtime.h>
 
@@ -42,7 +42,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 3;
 constexpr int kMaxCluster = 16, kMaxParts = kMaxCluster * kWarps;
 constexpr double kLog2eD = 1.4426950408889634074;
-constexpr float kCoarse = 0x1.4p-17f;  // two sums of 72 2^-24 each, rounded up
+constexpr float kCoarse = 0x1.8p-17f;  // two sums of 83 2^-24 each, rounded up
 constexpr float kFar = 0x1p20f;       // |m c| beyond which m - 124 / c is near m's own last place
 constexpr float kNothing = 0x1p-90f;  // sums of weights that are 0 (2^-124 each) stay below
 

@@ -6,6 +6,7 @@ import torch
 
 TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 U = 2.0 ** -24  # half a step of fp32
+RESOLUTION = 2.0 ** -34  # of a drawn token's border (include/rlrollout.h)
 
 
 def quantize_ref(x):
@@ -36,7 +37,7 @@ def verify_ref(target, ids, u, draft=None, draft_lse=None, n_draft=None, tempera
     B, rows, V = target.shape
     G = rows - 1
     out = dict(tokens=np.full((B, rows), -1, np.int64), n_accepted=np.zeros(B, np.int64), logp=np.zeros((B, rows)),
-               lse=np.zeros((B, rows)), status=0)
+               lse=np.zeros((B, rows)), status=0, near={})
     for b in range(B):
         n = G if n_draft is None else int(n_draft[b])
         if n < -1 or n > G or any(not 0 <= int(ids[b, i]) < V for i in range(max(n, 0))):
@@ -83,6 +84,17 @@ def verify_ref(target, ids, u, draft=None, draft_lse=None, n_draft=None, tempera
             over = np.nonzero((edges > x * edges[-1]) & (w > 0))[0]
             t = int(over[0]) if over.size else int(np.nonzero(w)[0][-1])
             out["tokens"][b, i], out["logp"][b, i] = t, (z[t] - m) - math.log1p(rest)
+            # A border of the token within RESOLUTION of the row's total (1, p being normalised): the
+            # kernel holds u and the sums in 48 bits and its terms to 2^-41, so which side of such a
+            # border u lies on is not decided, and the neighbour with a weight is as right.
+            weighty = np.nonzero(w > 0)[0]
+            k = int(np.searchsorted(weighty, t))
+            if k > 0 and x * edges[-1] - edges[weighty[k - 1]] <= RESOLUTION:
+                out["near"][b, i] = int(weighty[k - 1])
+            if k + 1 < weighty.size and edges[t] - x * edges[-1] <= RESOLUTION:
+                out["near"][b, i] = int(weighty[k + 1])
+            if (b, i) in out["near"]:
+                out["near"][b, i] = (out["near"][b, i], (z[out["near"][b, i]] - m) - math.log1p(rest))
             break
     return out
 
@@ -96,6 +108,11 @@ def sum_steps(V):
 
 
 def check_verify(out, ref, V):
+    tokens = out["tokens"].cpu().numpy()
+    ref = dict(ref, tokens=ref["tokens"].copy(), logp=ref["logp"].copy())
+    for place, (token, logp) in ref["near"].items():
+        if tokens[place] == token:
+            ref["tokens"][place], ref["logp"][place] = token, logp
     for k in ("tokens", "n_accepted"):
         got = out[k].cpu().numpy()
         assert np.array_equal(got, ref[k]), (k, np.argwhere(got != ref[k])[:4], got[got != ref[k]][:4], ref[k][got != ref[k]][:4])

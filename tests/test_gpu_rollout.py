@@ -393,6 +393,35 @@ def test_offsets_beyond_32_bits():
     assert (out["tokens"][:-3, 0] - flat).abs().max() <= 1
 
 
+@pytest.mark.parametrize("dtype,V", [("bf16", 1 << 22), ("f32", (1 << 21) + 5)])
+def test_very_long_rows(dtype, V):
+    """Rows whose parts are searched in several rounds."""
+    run_verify(**verify_inputs(2, 0, V, dtype, 61))
+    run_verify(**verify_inputs(1, 1, V, dtype, 67))
+    run_verify(**verify_inputs(1, 1, V, dtype, 71, "lookup"))
+
+
+@pytest.mark.parametrize("kind", ["model", "lookup"])
+@pytest.mark.parametrize("B", [1, 14, 15, 28, 29, 114, 115, 500])
+def test_every_size_of_cluster(B, kind):
+    """The batch decides how many CTAs share a row."""
+    run_verify(**verify_inputs(B, 1, 33000, "bf16", B, kind))
+
+
+def test_equal_logits():
+    """Rows of one value, and of two: sums of equal terms, borders at multiples of them."""
+    V = 50000
+    z = torch.full((6, 1, V), 1.5)
+    z[1] = -3.0e38
+    z[2, :, V // 2:] = 0.75
+    z[3, :, ::2] = -1.0e4
+    z[4] = 6.0e4
+    z[5] = -2.0e4
+    u = torch.tensor([0.123456789, 0.5000001, 0.77, 0.9, 0.31, 0.999999], dtype=torch.float64)[:, None]
+    run_verify(z, None, u)
+    run_verify(z.clamp(min=-6.0e4).half(), None, u)
+
+
 # ------------------------------------------------------------------ streams, graphs, a rollout's step
 def step_inputs(seed, B=12, G=3, V=1200, D=256):
     gen = torch.Generator().manual_seed(seed)

@@ -213,3 +213,17 @@ def test_verification_reference_keeps_the_targets_distribution():
         out = verify_ref(np.broadcast_to(zt, (n * n, 2, V)), np.full((n * n, 1), d), u, np.broadcast_to(zq, (n * n, 1, V)), np.full((n * n, 1), lq))
         got += q[d] * np.bincount(out["tokens"][:, 0], minlength=V) / (n * n)
     assert np.abs(got - p).max() < 3 / n
+
+
+@needs_nvcc
+def test_strides_beyond_the_address_space(lib):
+    """Row spans of more than 2^60 bytes are refused before their product is formed."""
+    big = 1 << 39
+    assert call_quantize(lib, R=(1 << 31) - 1, ld_x=big) == rl.RL_ERR_SHAPE
+    assert call_quantize(lib, R=(1 << 31) - 1, ld_c=big) == rl.RL_ERR_SHAPE
+    assert call_logits(lib, R=(1 << 31) - 1, ld=big) == rl.RL_ERR_SHAPE
+    assert call_logits(lib, R=(1 << 31) - 1, ld_h=big) == rl.RL_ERR_SHAPE
+    assert call_logits(lib, V=(1 << 31) - 1, ld=1 << 32, ld_w=big) == rl.RL_ERR_SHAPE
+    # more tiles than a launch counts
+    assert call_logits(lib, R=1 << 24, V=(1 << 31) - 8, D=64, ld_h=64, ld_w=64, ld=1 << 31, w=at(2) + (1 << 56), out=at(4) + (1 << 57),
+                       ws_bytes=1 << 50) == rl.RL_ERR_SHAPE
