@@ -43,8 +43,8 @@ constexpr int kCtasPerSm = 3;
 constexpr int kMaxCluster = 16, kMaxParts = kMaxCluster * kWarps;
 constexpr double kLog2eD = 1.4426950408889634074;
 constexpr float kCoarse = 0x1.8p-17f;  // two sums of 83 2^-24 each, rounded up
-constexpr float kFar = 0x1p20f;       // |m c| beyond which m - 124 / c is near m's own last place
-constexpr float kNothing = 0x1p-90f;  // sums of weights that are 0 (2^-124 each) stay below
+constexpr float kFar = 0x1p20f;       // |m c| beyond which m - 86 T is near m's own last place
+constexpr float kNothing = 0x1p-90f;  // sums of weights that are 0 (e^-86 each) stay below
 
 struct Args {
   const unsigned char* target;
@@ -55,8 +55,9 @@ struct Args {
   const double* u;
   long long V, row_bytes, draft_bytes;
   int G;
-  float c, c_lo, unit;       // log2(e) / temperature as two floats, and its reciprocal
-  double c_d, inv_t, t_ln2;  // log2(e) / temperature, 1 / temperature, temperature ln 2
+  float c;             // log2(e) / temperature
+  float T, r_hi, r_lo;  // temperature, and 1 / temperature as two floats
+  double inv_t;        // 1 / temperature
   long long* tokens;
   long long* n_accepted;
   float* logp;
@@ -346,18 +347,18 @@ __device__ __forceinline__ float log_prob(float z, const Stats& st, double inv_t
 
 // q = e^(z / temperature - lse) (fp64's own exponential is some hundred dependent steps of a
 // unit with a 64th of fp32's rate, and everybody waits for this one number).
-template <int DT>
+template <bool kUnit>
 __device__ __forceinline__ double draft_prob(float z, float lse, const Args& a, const uint2* powers) {
-  const double k = static_cast<double>(lse) * kLog2eD, m = rint(k * a.t_ln2 * 4096.0) * (1.0 / 4096.0);
-  const double x = static_cast<double>(z) * a.c_d - k;
-  if (!(x > -120.0 && x < 1.5 && fabs(m) < 4096.0)) return exp(static_cast<double>(z) * a.inv_t - static_cast<double>(lse));
+  const double x = static_cast<double>(z) * a.inv_t - static_cast<double>(lse);
+  const float m = rintf(lse * a.T * 4096.f) * 0x1p-12f;
+  if (!(x > -80.0 && x < 1.0 && fabsf(m) < 4096.f)) return exp(x);
   FineExp q;
-  q.init(a.c, a.c_lo, a.unit, static_cast<float>(m), static_cast<float>(k - m * a.c_d), false);
-  const Wide v = q.template at<true, false>(z, powers).value();
+  q.init(a.r_hi, a.r_lo, a.T, m, static_cast<float>(static_cast<double>(lse) - static_cast<double>(m) * a.inv_t), false);
+  const Wide v = q.template at<true, false, kUnit>(z, powers).value();
   return static_cast<double>(v.h) + static_cast<double>(v.l);
 }
 
-template <int DT, int MODE, bool kFine>
+template <int DT, int MODE, bool kFine, bool kUnit>
 struct Weights {
   const unsigned char* row;
   const unsigned char* draft_row;
@@ -366,8 +367,8 @@ struct Weights {
   FineExp p, q;
   const uint2* powers;
 
-  __device__ __forceinline__ Term2 fine(float2 z) const { return p.template at<DT == RL_F32, false>(z, powers); }
-  __device__ __forceinline__ Term2 drafted(float2 z) const { return q.template at<DT == RL_F32, true>(z, powers); }
+  __device__ __forceinline__ Term2 fine(float2 z) const { return p.template at<DT == RL_F32, false, kUnit>(z, powers); }
+  __device__ __forceinline__ Term2 drafted(float2 z) const { return q.template at<DT == RL_F32, true, kUnit>(z, powers); }
 
   // a vector's logits, -inf behind `end` and at the token that is left out
   __device__ __forceinline__ void logits(long long i, long long end, float (&z)[Fmt<DT>::kVec]) const {
@@ -430,8 +431,8 @@ __device__ __forceinline__ N warp_sum(N v) {
 }
 
 // The warp's sum over [lo, hi) in fine arithmetic, whole vectors from lo.
-template <int DT, int MODE>
-__device__ __forceinline__ Wide part_sum(Weights<DT, MODE, true>& f, long long lo, long long hi, int lane) {
+template <int DT, int MODE, bool kUnit>
+__device__ __forceinline__ Wide part_sum(Weights<DT, MODE, true, kUnit>& f, long long lo, long long hi, int lane) {
   using F = Fmt<DT>;
   Wide total(0.f);
   FineSum s;
@@ -452,8 +453,8 @@ __device__ __forceinline__ Wide part_sum(Weights<DT, MODE, true>& f, long long l
   return warp_sum(total + s.value());
 }
 // The same in fp32.
-template <int DT, int MODE>
-__device__ __forceinline__ float part_sum(Weights<DT, MODE, false>& f, long long lo, long long hi, int lane) {
+template <int DT, int MODE, bool kUnit>
+__device__ __forceinline__ float part_sum(Weights<DT, MODE, false, kUnit>& f, long long lo, long long hi, int lane) {
   using F = Fmt<DT>;
   float total = 0.f, err = 0.f;
 #pragma unroll 2
@@ -507,8 +508,8 @@ __device__ __forceinline__ int find_part(const N (&v)[kPer], N want, float none,
 
 // The first token of [begin, end) at which the running sum exceeds `want`, by one CTA (sm.found; -1:
 // no weight there); sm.gap: how far `want` is from the nearer end of its weight.
-template <int DT, int MODE, bool kFine, class N>
-__device__ __forceinline__ void search(Weights<DT, MODE, kFine>& f, long long begin, long long end, N want, Smem& sm) {
+template <int DT, int MODE, bool kFine, class N, bool kUnit>
+__device__ __forceinline__ void search(Weights<DT, MODE, kFine, kUnit>& f, long long begin, long long end, N want, Smem& sm) {
   using F = Fmt<DT>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kStep = 32 * F::kVec;
@@ -585,8 +586,8 @@ __device__ __forceinline__ void search(Weights<DT, MODE, kFine>& f, long long be
 
 // The CTA that has part `at` (of `size` elements) looks for the token there and tells the others.
 // The answer is sure if the border is more than `unsure` away from the ends of the token's weight.
-template <int DT, int MODE>
-__device__ __forceinline__ long long draw_coarse(Weights<DT, MODE, false>& f, int at, float want, float unsure, long long V,
+template <int DT, int MODE, bool kUnit>
+__device__ __forceinline__ long long draw_coarse(Weights<DT, MODE, false, kUnit>& f, int at, float want, float unsure, long long V,
                                                  long long size, Group& g, Smem& sm, bool& sure) {
   Exchange& ex = sm.ex[g.turn ^ 1];
   if (at / kWarps == g.rank) {
@@ -604,8 +605,8 @@ __device__ __forceinline__ long long draw_coarse(Weights<DT, MODE, false>& f, in
 }
 
 // The parts' fine sums, told to the whole cluster; then the token at u of their total.
-template <int DT, int MODE>
-__device__ __forceinline__ void tell_sum(Weights<DT, MODE, true>& f, long long lo, long long hi, Group& g, Smem& sm) {
+template <int DT, int MODE, bool kUnit>
+__device__ __forceinline__ void tell_sum(Weights<DT, MODE, true, kUnit>& f, long long lo, long long hi, Group& g, Smem& sm) {
   const int lane = threadIdx.x & 31, part = g.rank * kWarps + (threadIdx.x >> 5);
   const Wide s = part_sum(f, lo, hi, lane);
   g.turn ^= 1;
@@ -615,8 +616,8 @@ __device__ __forceinline__ void tell_sum(Weights<DT, MODE, true>& f, long long l
 // The token, in the CTA that has it; kElsewhere in the others, which have nothing left to do;
 // kNowhere in all where no part has any weight.
 constexpr long long kElsewhere = -2, kNowhere = -3;
-template <int DT, int MODE>
-__device__ __forceinline__ long long draw_fine(Weights<DT, MODE, true>& f, const Wide* sums, long long V, long long size, const Group& g,
+template <int DT, int MODE, bool kUnit>
+__device__ __forceinline__ long long draw_fine(Weights<DT, MODE, true, kUnit>& f, const Wide* sums, long long V, long long size, const Group& g,
                                                Smem& sm) {
   const int lane = threadIdx.x & 31, parts = g.size * kWarps;
   constexpr float none = MODE != kRest ? kNothing : 0.f;
@@ -643,7 +644,7 @@ __device__ __forceinline__ long long draw_fine(Weights<DT, MODE, true>& f, const
   return t;
 }
 
-template <int DT>
+template <int DT, bool kUnit>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 verify_drafts_kernel(const Args a, int cluster) {
   using F = Fmt<DT>;
@@ -750,13 +751,13 @@ verify_drafts_kernel(const Args a, int cluster) {
       mine = part_stats_exact<DT>(row, lo, hi, a.c, lane);
     }
     bad = !(fabsf(st.m) < INFINITY) || !(st.n > 0.f);
-    fp.init(a.c, a.c_lo, a.unit, st.m, 0.f, fabsf(st.m) * a.c > kFar);
+    fp.init(a.r_hi, a.r_lo, a.T, st.m, 0.f, fabsf(st.m) * a.c > kFar);
     if (bad || i == n) {
       if (writes && lse) lse[i] = bad ? nan : static_cast<float>(static_cast<double>(st.m) * a.inv_t + log1pf((st.n - 1.f) + st.s));
       break;
     }
     if (tid == 0) {
-      const Term w = fp.is_zero(zd) ? Term{0.f, 0.f, 0.f} : fp.template at<DT == RL_F32, false>(zd, sm.powers);
+      const Term w = fp.is_zero(zd) ? Term{0.f, 0.f, 0.f} : fp.template at<DT == RL_F32, false, kUnit>(zd, sm.powers);
       int v;
       if (a.draft && (!(zq < INFINITY) || !(fabsf(lq) < INFINITY))) {
         v = kNoDistribution;
@@ -767,7 +768,7 @@ verify_drafts_kernel(const Args a, int cluster) {
         if (fabsf(x) < 128.f && fabsf(zq * a.c) < 1024.f && fabsf(left - w.a) > 0x1p-8f * w.a && w.a > 0x1p-100f) {
           v = left < w.a ? kStays : kRefused;
         } else {
-          const double qd = a.draft ? draft_prob<DT>(zq, lq, a, sm.powers) : 1.0;
+          const double qd = a.draft ? draft_prob<kUnit>(zq, lq, a, sm.powers) : 1.0;
           const Wide p = w.value();
           v = ui * qd * (static_cast<double>(st.n) + static_cast<double>(st.s)) < static_cast<double>(p.h) + static_cast<double>(p.l) ? kStays : kRefused;
         }
@@ -793,23 +794,20 @@ verify_drafts_kernel(const Args a, int cluster) {
   if (!bad) {
     const unsigned char* draft_row = a.draft ? a.draft + (b * G + kept) * a.draft_bytes : nullptr;
     if (lost && a.draft) {
-      // S q_v = 2^(z c - k), k = lse_q log2(e) - log2 S, in the frame of a number with few digits
-      Weights<DT, kRest, true> f{row, draft_row, -1, 0.f, 0.f, fp, fp, sm.powers};
+      // S q_v = e^(z / T - k), k = lse_q - ln S, in the frame of a number with few digits
+      Weights<DT, kRest, true, kUnit> f{row, draft_row, -1, 0.f, 0.f, fp, fp, sm.powers};
       Wide total;
       total.h = two_sum(st.n, st.s, total.l);
       const Wide S = total;
       const float lq = a.draft_lse[b * G + kept];
-      Wide log2e;
-      log2e.h = 0x1.715476p+0f;
-      log2e.l = 0x1.4ae0c0p-26f;
 #pragma unroll 1
       for (int pass = 0; pass < 2; ++pass) {
-        const Wide k = Wide(lq) * log2e - log2_wide(total, sm.powers);
-        const float mq = rintf(k.h * a.unit * 4096.f) * 0x1p-12f;
-        Wide c2;
-        c2.h = a.c;
-        c2.l = a.c_lo;
-        f.q.init(a.c, a.c_lo, a.unit, mq, (k - Wide(mq) * c2).h, fabsf(mq) * a.c > kFar);
+        const Wide k = Wide(lq) - ln_wide(total, sm.powers);
+        const float mq = rintf(k.h * a.T * 4096.f) * 0x1p-12f;
+        Wide r;
+        r.h = a.r_hi;
+        r.l = a.r_lo;
+        f.q.init(a.r_hi, a.r_lo, a.T, mq, (k - Wide(mq) * r).h, fabsf(mq) * a.c > kFar);
         if (pass == 1) break;
         // sums of p over all tokens, and of p - q and of q over those with p > q
         Wide all(0.f), plus(0.f);
@@ -892,22 +890,22 @@ verify_drafts_kernel(const Args a, int cluster) {
         bool sure;
         long long t;
         if (without) {
-          Weights<DT, kWithout, false> f{row, nullptr, d_out, a.c, nm, fp, fp, sm.powers};
+          Weights<DT, kWithout, false, kUnit> f{row, nullptr, d_out, a.c, nm, fp, fp, sm.powers};
           t = draw_coarse(f, at, want - before, kCoarse * (st.n + st.s), V, size, g, sm, sure);
         } else {
-          Weights<DT, kSoftmax, false> f{row, nullptr, -1, a.c, nm, fp, fp, sm.powers};
+          Weights<DT, kSoftmax, false, kUnit> f{row, nullptr, -1, a.c, nm, fp, fp, sm.powers};
           t = draw_coarse(f, at, want - before, kCoarse * (st.n + st.s), V, size, g, sm, sure);
         }
         if (sure && t >= 0) token = g.rank == 0 ? t : kElsewhere;
       }
       if (token == kNowhere && without) {
-        Weights<DT, kWithout, true> f{row, nullptr, d_out, 0.f, 0.f, fp, fp, sm.powers};
+        Weights<DT, kWithout, true, kUnit> f{row, nullptr, d_out, 0.f, 0.f, fp, fp, sm.powers};
         tell_sum(f, lo, hi, g, sm);
         token = draw_fine(f, sm.ex[g.turn].sum, V, size, g, sm);
       }
     }
     if (token == kNowhere && !bad) {
-      Weights<DT, kSoftmax, true> f{row, nullptr, -1, 0.f, 0.f, fp, fp, sm.powers};
+      Weights<DT, kSoftmax, true, kUnit> f{row, nullptr, -1, 0.f, 0.f, fp, fp, sm.powers};
       tell_sum(f, lo, hi, g, sm);
       token = draw_fine(f, sm.ex[g.turn].sum, V, size, g, sm);
     }
@@ -945,13 +943,13 @@ int cluster_for(long long B, long long V, int sms) {
   return c;
 }
 
-template <int DT>
-rl_status launch(const Args& a, long long B, int cluster, int dev, cudaStream_t stream) {
+template <int DT, bool kUnit>
+rl_status launch_kernel(const Args& a, long long B, int cluster, int dev, cudaStream_t stream) {
   static std::atomic<unsigned long long> allowed{0};
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
   if (!(allowed.load(std::memory_order_acquire) & bit)) {
-    if (cudaFuncSetAttribute(verify_drafts_kernel<DT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-        cudaFuncSetAttribute(verify_drafts_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * kSlots * kChunkBytes) !=
+    if (cudaFuncSetAttribute(verify_drafts_kernel<DT, kUnit>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaFuncSetAttribute(verify_drafts_kernel<DT, kUnit>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * kSlots * kChunkBytes) !=
             cudaSuccess)
       return RL_ERR_CUDA;
     allowed.fetch_or(bit, std::memory_order_release);
@@ -967,7 +965,12 @@ rl_status launch(const Args& a, long long B, int cluster, int dev, cudaStream_t 
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<DT>, a, cluster) == cudaSuccess ? RL_OK : RL_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<DT, kUnit>, a, cluster) == cudaSuccess ? RL_OK : RL_ERR_CUDA;
+}
+
+template <int DT>
+rl_status launch(const Args& a, long long B, int cluster, int dev, cudaStream_t stream) {
+  return a.inv_t == 1.0 ? launch_kernel<DT, true>(a, B, cluster, dev, stream) : launch_kernel<DT, false>(a, B, cluster, dev, stream);
 }
 
 }  // namespace
@@ -1013,11 +1016,10 @@ extern "C" rl_status rl_verify_drafts(const rl_verify_drafts_desc* desc, void* s
   a.draft_bytes = d.ld_draft * es;
   a.G = static_cast<int>(d.G);
   a.inv_t = 1.0 / d.temperature;
-  a.c_d = kLog2eD / d.temperature;
-  a.t_ln2 = d.temperature * 0.69314718055994530942;
-  a.c = static_cast<float>(a.c_d);
-  a.c_lo = static_cast<float>(a.c_d - static_cast<double>(a.c));
-  a.unit = 1.f / a.c;
+  a.c = static_cast<float>(kLog2eD / d.temperature);
+  a.T = static_cast<float>(d.temperature);
+  a.r_hi = static_cast<float>(a.inv_t);
+  a.r_lo = static_cast<float>(a.inv_t - static_cast<double>(a.r_hi));
   a.tokens = d.tokens;
   a.n_accepted = d.n_accepted;
   a.logp = d.logp_out;
