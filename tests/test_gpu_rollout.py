@@ -7,7 +7,7 @@ import torch
 
 import ppo_policy_loss_gb300 as rl
 from ppo_policy_loss_gb300 import torch_api
-from tests._rollout import TORCH, check_verify, f64, logits_ref, make_logits, quantize_ref, verify_ref
+from tests._rollout import RESOLUTION, TORCH, check_verify, f64, logits_ref, make_logits, quantize_ref, verify_ref
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -315,6 +315,30 @@ def test_uniforms_next_to_a_border(dtype, V):
     whole = torch.nn.functional.pad(z, (0, -V % per)).expand(u.size, 1, -1).contiguous().to(DEV)[..., :V]
     got = torch_api.verify_drafts(whole, None, torch.from_numpy(u)[:, None].to(DEV))["tokens"].view(-1).cpu().numpy()
     assert np.array_equal(got, np.concatenate([at, at + 1]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("order", ["random", "rising", "falling", "two values"])
+@pytest.mark.parametrize("B", [200, 1000])
+def test_uniforms_some_way_from_a_border(dtype, order, B):
+    """Numbers 2^-20 to 2^-17 of the total to either side of a border: around the distance at
+    which fp32 sums are no longer asked."""
+    V = 40000
+    z = make_logits((1,), V, dtype, 39, sd=2.0, sure=False)[0]
+    if order == "two values":
+        z = torch.where(torch.arange(V) % 3 == 0, 0.0, -1.3).to(TORCH[dtype])
+    elif order != "random":
+        z = z.sort(descending=order == "falling").values
+    p = np.exp(f64(z) - f64(z).max())
+    p /= p.sum()
+    edges = np.cumsum(p)
+    gen = np.random.default_rng(B)
+    at = gen.integers(1, V - 1, B)
+    u = np.clip(edges[at] + 2.0 ** gen.uniform(-20, -17, B) * gen.choice([-1.0, 1.0], B), 0.0, 1 - 2.0 ** -53)
+    got = torch_api.verify_drafts(z.expand(B, 1, V).contiguous().to(DEV), None, torch.from_numpy(u)[:, None].to(DEV))["tokens"]
+    got = got[:, 0].cpu().numpy()
+    # u lies in the token's interval, to the resolution of its borders
+    assert (u < edges[got] + RESOLUTION).all() and (u >= edges[got] - p[got] - RESOLUTION).all()
 
 
 def test_refused_drafts_next_to_a_border():
