@@ -530,6 +530,29 @@ def test_captured_and_replayed():
             assert torch.equal(out[0], want[0]) and torch.equal(out[1]["tokens"], want[1]["tokens"]) and torch.equal(out[1]["lse"], want[1]["lse"])
 
 
+def test_the_c_names():
+    """The bindings that forward to the C entry points, with their defaults."""
+    hidden, weight, ids, u = step_inputs(7)
+    (B, G), (V, D), R = ids.shape, weight.shape, hidden.shape[0]
+    want_logits, want = rollout_step(hidden, weight, ids, u)
+    h, w = torch.empty((R, D), dtype=torch.int8, device=DEV), torch.empty((V, D), dtype=torch.int8, device=DEV)
+    sh, sw = torch.empty(R, device=DEV), torch.empty(V, device=DEV)
+    rl.rl_quantize_rows_int8(hidden, "bf16", R, D, D, h, D, sh)
+    rl.rl_quantize_rows_int8(weight, "bf16", V, D, D, w, D, sw)
+    logits = torch.empty((R, V), dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(rl.rl_lmhead_int8_workspace_size(R, D), dtype=torch.uint8, device=DEV)
+    rl.rl_lmhead_logits_int8(h, D, sh, w, D, sw, R, D, V, "bf16", logits, V, workspace=ws)
+    assert torch.equal(logits, want_logits)
+    tokens = torch.empty((B, G + 1), dtype=torch.int64, device=DEV)
+    d = rl.rl_verify_drafts_desc_init()
+    d.target_logits, d.B, d.G, d.V, d.ld = logits.data_ptr(), B, G, V, V
+    d.draft_ids, d.uniforms, d.tokens = ids.data_ptr(), u.data_ptr(), tokens.data_ptr()
+    rl.rl_verify_drafts(d)      # the other outputs are not asked for
+    assert torch.equal(tokens, want["tokens"])
+    with pytest.raises(rl.RlLossError, match="rl_lmhead_logits_int8"):
+        rl.rl_lmhead_logits_int8(h, D, sh, w, D, sw, R, D, V, "bf16", logits, V)
+
+
 def test_nothing_to_do():
     assert torch_api.quantize_rows(torch.zeros((0, 64), device=DEV))[0].shape == (0, 64)
     w, sw = torch_api.quantize_rows(torch.randn((100, 64), device=DEV))

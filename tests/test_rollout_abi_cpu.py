@@ -6,6 +6,7 @@ import os
 import re
 import shutil
 import subprocess
+import tempfile
 
 import numpy as np
 import pytest
@@ -227,3 +228,19 @@ def test_strides_beyond_the_address_space(lib):
     # more tiles than a launch counts
     assert call_logits(lib, R=1 << 24, V=(1 << 31) - 8, D=64, ld_h=64, ld_w=64, ld=1 << 31, w=at(2) + (1 << 56), out=at(4) + (1 << 57),
                        ws_bytes=1 << 50) == rl.RL_ERR_SHAPE
+
+
+@needs_nvcc
+def test_verify_record_matches_the_header(lib):
+    """The ctypes record has the C struct's size and offsets."""
+    t = rl.rl_verify_drafts_desc
+    src = "#include <stdio.h>\n#include <stddef.h>\n#include \"rlrollout.h\"\nint main(void) {\n"
+    src += 'printf("%zu", sizeof(rl_verify_drafts_desc));\n'
+    for f, _ in t._fields_:
+        src += f'printf(" %zu", offsetof(rl_verify_drafts_desc, {f}));\n'
+    src += "return 0; }\n"
+    with tempfile.TemporaryDirectory() as d:
+        open(os.path.join(d, "t.c"), "w").write(src)
+        subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), os.path.join(d, "t.c"), "-o", os.path.join(d, "t")], check=True)
+        got = subprocess.run([os.path.join(d, "t")], capture_output=True, text=True, check=True).stdout
+    assert [int(x) for x in got.split()] == [ctypes.sizeof(t)] + [getattr(t, f).offset for f, _ in t._fields_]
