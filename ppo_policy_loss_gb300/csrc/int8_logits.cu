@@ -358,9 +358,9 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         pa.next(slots_a);
       }
     }
-    if (stop)  // copies already issued land before the CTA can exit
-      for (uint32_t k = issued > slots_a ? issued - slots_a : 0; k < issued; ++k)
-        tc_wait<true>(smem_addr(&sm.full_a[k % slots_a]), (k / slots_a) & 1, abort_flag);
+    // copies already issued land before the CTA can exit, whoever gave up (else they have)
+    for (uint32_t k = issued > slots_a ? issued - slots_a : 0; k < issued; ++k)
+      tc_wait<true>(smem_addr(&sm.full_a[k % slots_a]), (k / slots_a) & 1, abort_flag);
   } else if (warp == 2) {
     // ---------------------------------------------------------------- TMA producer: token tiles (whole warp)
     Place pb, pd;
@@ -391,9 +391,8 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
       }
       if (a.resident) break;
     }
-    if (stop)
-      for (uint32_t k = issued > slots_b ? issued - slots_b : 0; k < issued; ++k)
-        tc_wait<true>(smem_addr(&sm.full_b[k % slots_b]), (k / slots_b) & 1, abort_flag);
+    for (uint32_t k = issued > slots_b ? issued - slots_b : 0; k < issued; ++k)
+      tc_wait<true>(smem_addr(&sm.full_b[k % slots_b]), (k / slots_b) & 1, abort_flag);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (whole warp)
     Place pw, pb, pc, pd;
@@ -433,7 +432,7 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
       }
       loaded = a.resident;
     }
-    if (stop && issued) {  // every MMA already issued completes before the memory is freed
+    if (issued) {  // every MMA, and every arrival that stands for one, is done before the CTA can exit
       umma_commit_elect(smem_addr(&sm.drain));
       tc_wait<true>(smem_addr(&sm.drain), 0, abort_flag);
     }
