@@ -12,7 +12,7 @@
 //
 //   * widen_kernel writes the tokens' codes as fp16 into the workspace (R D
 //     elements, 1 to 2 us beside a product that reads V D bytes).
-//   * warps 0 and 2 (one lane each): TMA producers of two rings: 8-bit weight tiles (128
+//   * warps 0 and 2: TMA producers of two rings: 8-bit weight tiles (128
 //     channels x 128 columns, 16 KB) and fp16 token tiles (N x 128 columns).
 //     Where all columns of a single token tile fit (small batches), they are loaded once and stay.
 //   * warps 4-7 and 12-15, step by step in turn: one channel a thread.  A 128-byte row of codes from shared memory, widened
@@ -69,6 +69,7 @@ struct Bars {
   alignas(16) float scale[2][kMaxN + 32];  // of the tokens of the epilogue's unit
 };
 
+static_assert((static_cast<int>(kTmemAll) - 2 * kMaxN) / kWideCols >= 2, "two widened tiles at least");
 static_assert(kRingBytes + 1024 + sizeof(Bars) <= 232448, "rings and barriers fit the 227 KB a CTA may use");
 
 struct IArgs {
@@ -108,7 +109,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return warp_wait_on(bar, parity, abort);
 }
 
-// Both of two.
+// Both of two, the second looked at after the first: no lane takes what it saw of the second
+// for an answer unless it had seen the first pass.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t bar1, uint32_t parity1, volatile int* abort) {
   const bool first = mbar_try_wait(bar, parity), second = mbar_try_wait(bar1, parity1);
   if (__all_sync(0xffffffffu, first && second)) return true;
@@ -448,7 +450,7 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     for (int u = blockIdx.x; u < n_units && !stop; u += gridDim.x) {
 #pragma unroll 1
       for (int k = 0; k < steps; ++k, ++step) {
-        if (kGroups == 2 && static_cast<int>(step & 1) != turn) {  // (no phase is missed: it ends behind this group's next step)
+        if (kGroups == 2 && static_cast<int>(step & 1) != turn) {
           if (ahead > 0)
             --ahead;
           else
@@ -457,12 +459,17 @@ logits_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
           pw.next(slots_w);
           continue;
         }
+        // done before full_a: this group has not watched the other's steps, and tiles land in
+        // any order.  A barrier whose phase before the awaited one is still open passes a wait
+        // for the one to come; that step - slots_w is done says that this step's slot, last filled
+        // at step - slots_a <= step - slots_w, has had that tile land.  (done itself is two
+        // steps behind a done that this group waited for, and slots_d >= 2.)
         bool ok;
         if (ahead > 0) {
           --ahead;
           ok = warp_wait(smem_addr(&sm.full_a[pa.i]), pa.parity, abort_flag);
         } else {
-          ok = warp_wait(smem_addr(&sm.full_a[pa.i]), pa.parity, smem_addr(&sm.done[pd.i]), pd.parity, abort_flag);
+          ok = warp_wait(smem_addr(&sm.done[pd.i]), pd.parity, smem_addr(&sm.full_a[pa.i]), pa.parity, abort_flag);
           pd.next(slots_d);
         }
         if (!ok) {
@@ -641,12 +648,12 @@ IPlan int8_plan(long long R, long long D, long long V) {
     const long long room = (budget - p.steps * tile_b) / kTileA;
     p.slots_a = static_cast<int>(room < kMaxA ? room : kMaxA);
   } else {
-    p.slots_a = 4;
+    p.slots_a = kMaxWide;
     const long long room = (budget - p.slots_a * static_cast<long long>(kTileA)) / tile_b;
     p.slots_b = static_cast<int>(room < kMaxDone ? room : kMaxDone);
   }
   const int wide = (static_cast<int>(kTmemAll) - 2 * p.N) / kWideCols;
-  p.slots_w = wide < kMaxWide ? wide : kMaxWide;
+  p.slots_w = wide < kMaxWide ? wide : kMaxWide;  // 2 to 4, and never more than slots_a: the widening warps' waits need both
   p.slots_d = p.resident || p.slots_w > p.slots_b ? p.slots_w : p.slots_b;
   const long long g = kTokenL2Bytes / (static_cast<long long>(p.N) * wide_ld(D) * 2);
   p.group = static_cast<int>(g < 1 ? 1 : (g > p.n_tt ? p.n_tt : g));

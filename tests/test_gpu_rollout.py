@@ -145,6 +145,26 @@ def test_logits_do_not_depend_on_the_batch():
         assert torch.equal(check_logits(h[lo:lo + n], sh[lo:lo + n], w, sw, "f32"), whole[lo:lo + n])
 
 
+@pytest.mark.parametrize("R", [1, 16, 50, 64, 90, 100, 128, 150, 160, 176, 192, 300])
+def test_logits_of_many_calls_on_end(R):
+    """Weights that L2 does not hold, so that tiles land late and in any order: the rings' every
+    depth, each call's every bit."""
+    D, V, calls = 1024, 151_936, 200
+    g = torch.Generator(device=DEV).manual_seed(R)
+    h = torch.randint(-128, 128, (R, D), generator=g, dtype=torch.int8, device=DEV)
+    w = torch.randint(-128, 128, (V, D), generator=g, dtype=torch.int8, device=DEV)
+    sh, sw = (torch.rand(n, generator=g, device=DEV) + 0.5 for n in (R, V))
+    want = (h.double() @ w.double().T).float().mul_(sh[:, None]).mul_(sw).bfloat16()  # (sums below 2^24: exact in both)
+    status, work = torch.zeros(1, dtype=torch.int32, device=DEV), torch_api.new_int8_workspace(R, D, device=DEV)
+    out, wrong = torch.empty_like(want), torch.zeros((), dtype=torch.int64, device=DEV)
+    for _ in range(calls):
+        for _ in range(4):
+            torch_api.lmhead_logits_int8(h, sh, w, sw, out=out, workspace=work, status=status)
+        wrong += (out.view(torch.int16) != want.view(torch.int16)).sum()
+        out.zero_()
+    assert wrong.item() == 0 and status.item() == 0
+
+
 def test_logits_scales_that_are_not_numbers():
     h, sh, w, sw = int8_inputs(20, 64, 200, 5)
     sh[3], sh[4], sw[7], sw[9] = np.nan, 0.0, np.inf, np.nan
