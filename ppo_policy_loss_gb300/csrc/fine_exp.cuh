@@ -205,20 +205,20 @@ __device__ __forceinline__ float2 quick_two_sum2(float2 x, float2 y, float2& err
 
 // e^((z - m) / T - kappa).  z counts as at least zmin, so that what is
 // below e^-86 (and -inf) gives e^-86, which no sum notices (is_zero() tells it from a
-// weight), and as at most zmax, so that what is above 4 gives about 4.
+// weight), or another `low`, and as at most zmax, so that what is above 4 gives about 4.
 // `far`: m is so large that zmin would be m itself; z - m is then formed first (exact
 // where e^((z - m) / T) is not 0: z is within a factor of two of m).
 struct FineExp {
   float r_hi, r_lo, kappa, off, m, zmin, zmax;
 
   // 1 / T as two floats; the frame: the terms are e^(z / T - k), kappa = k - m / T.
-  __device__ __forceinline__ void init(float r_hi_, float r_lo_, float T, float m_, float kappa_, bool far) {
+  __device__ __forceinline__ void init(float r_hi_, float r_lo_, float T, float m_, float kappa_, bool far, float low = -86.f) {
     r_hi = r_hi_;
     r_lo = r_lo_;
     off = far ? m_ : 0.f;
     m = far ? 0.f : m_;
     kappa = kappa_;
-    zmin = fmaf(-86.f, T, m);
+    zmin = fmaf(low, T, m);
     zmax = fmaf(1.4f, T, m);
   }
   // kWide: z has 24 significant bits (16-bit numbers have 8 or 11).  kTop: z may be above zmax.  kUnit: T = 1.

@@ -811,7 +811,8 @@ verify_drafts_kernel(const Args a, int cluster) {
         Wide r;
         r.h = a.r_hi;
         r.l = a.r_lo;
-        f.q.init(a.r_hi, a.r_lo, a.T, mq, (k - Wide(mq) * r).h, fabsf(mq) * a.c > kFar);
+        // (q's least term is above p's: a token that neither can give, -inf twice or behind the row, has no p - q)
+        f.q.init(a.r_hi, a.r_lo, a.T, mq, (k - Wide(mq) * r).h, fabsf(mq) * a.c > kFar, -84.f);
         if (pass == 1) break;
         // sums of p over all tokens, and of p - q and of q over those with p > q
         Wide all(0.f), plus(0.f);

@@ -302,6 +302,22 @@ def test_draft_that_is_never_below_the_target():
     assert 0 < ref["n_accepted"].sum() < 40
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("V", [301, 304, 5000])
+@pytest.mark.parametrize("temperature", [1.0, 0.7, 0.01])
+def test_masked_draft_that_is_never_below_the_target(dtype, V, temperature):
+    """The same with tokens that neither distribution has: their p - q is 0 as well."""
+    a = verify_inputs(40, 1, V, dtype, 24, temperature=temperature)
+    a["target"][:, :, 5:V:3] = -math.inf
+    a["target"][:, :, V - 1] = -math.inf
+    a["ids"][:] = torch.arange(40)[:, None] % 5
+    a["draft"] = torch.nn.functional.pad(a["target"][:, :1], (0, -V % 8))[..., :V]
+    a["draft_lse"] = ((a["draft"].double() / temperature).logsumexp(-1) - 1.0).float()
+    a["u"][:, 0] = 1.0 - 2.0 ** -20
+    out, ref = run_verify(**a)
+    assert ref["n_accepted"].sum() == 0
+
+
 def test_draft_logits_of_minus_infinity():
     """q = 0 at the draft: kept wherever p > 0."""
     a = verify_inputs(20, 2, 300, "f16", 29)
