@@ -935,17 +935,35 @@ verify_drafts_kernel(const Args a, int cluster) {
   }
 }
 
-// CTAs of a cluster: the power of two with which all are at work at once, at most 16, and no
-// more than leave a warp 256 elements.  (Clusters of 8 fill a third fewer of the places, of
-// 16 half as many: parts of the chip hold no whole number of them.)  From two CTAs a place on, clusters of 2:
-// shorter last rounds.
+// CTAs of a cluster, no more than leave a warp 256 elements.  Few sequences take the largest
+// clusters of which all are at work at once; 5 and 10 of them fill the chip's parts best (435 and 430 of 456
+// places; 8: 408, 16: 336).  us, V = 151,936, four drafts / a draw:
+//   B = 4    16: 27 / 14    10: 26 / 14    8: 32 / 15
+//   B = 40   10: 52 / 29     7: 53 / 33    5: 65 / 36    4: 76 / 49
+//   B = 64    7: 83 / 39     5: 72 / 42    4: 76 / 51    2: 105 / 68
+//   B = 130   5: 128 / 56    4: 130 / 57   2: 139 / 81   1: 199 / 74
+//   B = 300   5: 245 / 90    4: 237 / 88   2: 243 / 97   1: 259 / 104
+//   B = 512   4: 360 / 129   2: 338 / 125  1: 361 / 129
+// Of short rows a cluster's barriers are a larger share; V = 32,000:
+//   B = 100   5: 54 / 30     4: 38 / 23    2: 43 / 27
+//   B = 200                  4: 64 / 34    2: 61 / 35    1: 65 / 34
+//   B = 400                  4: 122 / 58   2: 97 / 48    1: 84 / 35
+constexpr long long kShortRow = 1 << 16;
 int cluster_for(long long B, long long V, int sms) {
-  const long long slots = static_cast<long long>(sms) * kCtasPerSm;
-  const long long most = (V + 256 * kWarps - 1) / (256 * kWarps);
-  int c = 2;
-  while (c < kMaxCluster && 2 * c * B <= (c >= 4 ? slots / 2 : slots)) c *= 2;
-  while (c > 1 && c > most) c /= 2;
-  return c;
+  const long long slots = static_cast<long long>(sms) * kCtasPerSm, most = (V + 256 * kWarps - 1) / (256 * kWarps);
+  const long long filled = slots - slots / 32;
+  int c;
+  if (B * kMaxCluster <= slots / 7)
+    c = kMaxCluster;
+  else if (B * 10 <= filled)
+    c = 10;
+  else if (B * 5 <= filled)
+    c = 5;
+  else if (B * 4 <= (V < kShortRow ? slots : 3 * slots))
+    c = 4;
+  else
+    c = V < kShortRow && B >= 2 * sms ? 1 : 2;
+  return static_cast<int>(c < most ? c : most);
 }
 
 template <int DT, bool kUnit>

@@ -468,6 +468,14 @@ def test_every_size_of_cluster(B, kind):
     run_verify(**verify_inputs(B, 1, 33000, "bf16", B, kind))
 
 
+@pytest.mark.parametrize("kind", ["model", "lookup"])
+@pytest.mark.parametrize("B,V", [(4, 66000), (5, 66000), (44, 66000), (45, 66000), (88, 66000), (89, 66000), (342, 66000), (343, 66000),
+                                 (114, 40000), (115, 40000), (304, 40000), (5, 20479), (5, 18433), (45, 8193), (3, 6145)])
+def test_every_share_of_a_row(B, V, kind):
+    """Shares that are no powers of two; fewer where rows are short."""
+    run_verify(**verify_inputs(B, 1, V, "bf16", B + V, kind))
+
+
 def test_equal_logits():
     """Rows of one value, and of two: sums of equal terms, borders at multiples of them."""
     V = 50000
