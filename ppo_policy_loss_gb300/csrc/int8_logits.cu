@@ -166,6 +166,9 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 __global__ void __launch_bounds__(kWidenThreads)
 widen_kernel(const signed char* __restrict__ h, long long ld_h, long long R, long long D, unsigned char* __restrict__ f,
              long long ld_f) {
+  // The launch before may still be at work; behind the wait it is not, and what depends on this one
+  // may start: its weight tiles load while the codes are widened.
+  grid_dependency_wait();
   allow_dependents();
   const long long per_row = (D + 15) / 16;
   const long long i = static_cast<long long>(blockIdx.x) * kWidenThreads + threadIdx.x;
@@ -764,9 +767,16 @@ extern "C" rl_status rl_lmhead_logits_int8(const signed char* hidden, long long 
   a.status = status_dev;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const long long pieces = R * ((D + 15) / 16);
-  widen_kernel<<<static_cast<unsigned>((pieces + kWidenThreads - 1) / kWidenThreads), kWidenThreads, 0, s>>>(
-      hidden, ld_h, R, D, static_cast<unsigned char*>(workspace), ldw);
-  if (cudaGetLastError() != cudaSuccess) return RL_ERR_CUDA;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((pieces + kWidenThreads - 1) / kWidenThreads));
+  cfg.blockDim = dim3(kWidenThreads);
+  cfg.stream = s;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, widen_kernel, hidden, ld_h, R, D, static_cast<unsigned char*>(workspace), ldw) != cudaSuccess) return RL_ERR_CUDA;
   const int grid = static_cast<int>(units < sms ? units : sms);
   if (dtype == RL_F32) return launch_any<float>(map_w, map_h, a, grid, dev, s);
   if (dtype == RL_BF16) return launch_any<__nv_bfloat16>(map_w, map_h, a, grid, dev, s);
