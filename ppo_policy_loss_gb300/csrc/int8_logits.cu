@@ -164,10 +164,10 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 
 // The tokens' codes as fp16, rows ld_f elements apart: 16 codes a thread.
 __global__ void __launch_bounds__(kWidenThreads)
-widen_kernel(const signed char* __restrict__ h, long long ld_h, long long R, long long D, unsigned char* __restrict__ f,
-             long long ld_f) {
+widen_kernel(const signed char* h, long long ld_h, long long R, long long D, unsigned char* f, long long ld_f) {
   // The launch before may still be at work; behind the wait it is not, and what depends on this one
-  // may start: its weight tiles load while the codes are widened.
+  // may start: its weight tiles load while the codes are widened.  (No __restrict__: a load that
+  // counts as one of constants might be moved before the wait.)
   grid_dependency_wait();
   allow_dependents();
   const long long per_row = (D + 15) / 16;

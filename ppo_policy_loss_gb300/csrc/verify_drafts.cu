@@ -668,8 +668,9 @@ verify_drafts_kernel(const Args a, int cluster) {
   static_assert(kPow == kThreads, "one power a thread");
   sm.powers[tid] = kPowers[tid];
   if (tid < kWarps * kSlots) mbar_init(smem_addr(&sm.full[0][0]) + 8 * tid, 1);
+  if (tid == 0) abort_word = 0;
+  grid_dependency_wait();  // the launch before this one may have ended only now
   if (tid == 0) {
-    abort_word = 0;
     double u = a.u[b * rows + G];
     u = u > 0.0 ? fmin(u, 1.0 - 0x1p-53) : 0.0;
     const float h = static_cast<float>(u);
@@ -982,12 +983,14 @@ rl_status launch_kernel(const Args& a, long long B, int cluster, int dev, cudaSt
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kWarps * kSlots * kChunkBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // starts while the launch before it ends
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<DT, kUnit>, a, cluster) == cudaSuccess ? RL_OK : RL_ERR_CUDA;
 }
 
