@@ -47,7 +47,8 @@ extern "C" {
  *           byte of it in x; columns D .. ld_c-1 are not written.
  *   scale : float [R].
  * Errors: RL_ERR_DTYPE, RL_ERR_SHAPE (R < 0, R >= 2^31, D < 1, D >= 2^31, a stride below
- * D or so large that 64 bits do not address the rows), RL_ERR_NULL, RL_ERR_ALIGN, RL_ERR_ALIAS (codes in x), RL_ERR_CUDA.  R =
+ * D or so large that 64 bits do not address the rows), RL_ERR_NULL, RL_ERR_ALIGN, RL_ERR_ALIAS (an
+ * output in x or in the other), RL_ERR_CUDA.  R =
  * 0 launches nothing.
  */
 rl_status rl_quantize_rows_int8(const void* x, rl_dtype dtype, long long R, long long D, long long ld_x,
@@ -73,8 +74,8 @@ rl_status rl_quantize_rows_int8(const void* x, rl_dtype dtype, long long R, long
  * Errors: RL_ERR_DTYPE, RL_ERR_SHAPE (R < 0, R >= 2^31, V < 1, V >= 2^31, D out of
  * range, a stride too small or so large that 64 bits do not address the rows, more than
  * 2^30 tiles of 128 channels and 128 tokens), RL_ERR_NULL, RL_ERR_ALIGN, RL_ERR_ALIAS (logits
- * in hidden or weight), RL_ERR_WORKSPACE, RL_ERR_CUDA.  R = 0 launches
- * nothing.
+ * or workspace in an input or in one another), RL_ERR_WORKSPACE, RL_ERR_CUDA.  R = 0
+ * launches nothing.
  */
 rl_status rl_lmhead_logits_int8(const signed char* hidden, long long ld_h, const float* scale_h,
                                 const signed char* weight, long long ld_w, const float* scale_w, long long R,
@@ -144,8 +145,9 @@ void rl_verify_drafts_desc_init(rl_verify_drafts_desc* desc);
 /*
  * Errors: RL_ERR_NULL (desc, target_logits, draft_ids, draft_lse beside
  * draft_logits, uniforms, tokens), RL_ERR_DTYPE, RL_ERR_SHAPE (B < 0, G, V or a
- * stride out of range, B (G + 1) >= 2^31), RL_ERR_ARG (temperature),
- * RL_ERR_ALIGN, RL_ERR_CUDA.  B = 0 launches nothing.
+ * stride out of range, B (G + 1) >= 2^31, rows that 64 bits do not address), RL_ERR_ARG
+ * (temperature), RL_ERR_ALIGN, RL_ERR_ALIAS (an output in an input or in another output),
+ * RL_ERR_CUDA.  B = 0 launches nothing.
  */
 rl_status rl_verify_drafts(const rl_verify_drafts_desc* desc, void* stream);
 

@@ -737,7 +737,13 @@ extern "C" rl_status rl_lmhead_logits_int8(const signed char* hidden, long long 
   const long long out_bytes = ((R - 1) * ld + V) * es;
   if (overlap(logits, out_bytes, hidden, (R - 1) * ld_h + D) || overlap(logits, out_bytes, weight, (V - 1) * ld_w + D))
     return RL_ERR_ALIAS;
-  if (!workspace || workspace_bytes < rl_lmhead_int8_workspace_size(R, D)) return RL_ERR_WORKSPACE;
+  const size_t scratch = rl_lmhead_int8_workspace_size(R, D);
+  if (!workspace || workspace_bytes < scratch) return RL_ERR_WORKSPACE;
+  const long long taken = static_cast<long long>(scratch);
+  if (overlap(workspace, taken, logits, out_bytes) || overlap(workspace, taken, hidden, (R - 1) * ld_h + D) ||
+      overlap(workspace, taken, weight, (V - 1) * ld_w + D) || overlap(workspace, taken, scale_h, R * 4) || overlap(workspace, taken, scale_w, V * 4) ||
+      overlap(logits, out_bytes, scale_h, R * 4) || overlap(logits, out_bytes, scale_w, V * 4))
+    return RL_ERR_ALIAS;
   EncodeTiled enc = nullptr;
   int dev = 0, sms = 0;
   if (tc_encode_fn(&enc) != RL_OK || cudaGetDevice(&dev) != cudaSuccess || tc_device_sms(&sms) != RL_OK) return RL_ERR_CUDA;

@@ -224,8 +224,9 @@ extern "C" rl_status rl_quantize_rows_int8(const void* x, rl_dtype dtype, long l
   if (R > (1LL << 60) / (ld_x * es) || R > (1LL << 60) / ld_c) return RL_ERR_SHAPE;  // more than 64 bits address
   const uintptr_t xa = reinterpret_cast<uintptr_t>(x), ca = reinterpret_cast<uintptr_t>(codes);
   if ((xa & 15) || (ca & 15) || ((ld_x * es) & 15) || (ld_c & 15) || (reinterpret_cast<uintptr_t>(scale) & 3)) return RL_ERR_ALIGN;
-  if (xa < ca + static_cast<uintptr_t>((R - 1) * ld_c + D) && ca < xa + static_cast<uintptr_t>(((R - 1) * ld_x + D) * es))
-    return RL_ERR_ALIAS;
+  const uintptr_t sa = reinterpret_cast<uintptr_t>(scale), x_end = xa + static_cast<uintptr_t>(((R - 1) * ld_x + D) * es),
+                  c_end = ca + static_cast<uintptr_t>((R - 1) * ld_c + D), s_end = sa + static_cast<uintptr_t>(R * 4);
+  if ((xa < c_end && ca < x_end) || (xa < s_end && sa < x_end) || (ca < s_end && sa < c_end)) return RL_ERR_ALIAS;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == RL_F32)
     launch_rows<RL_F32>(x, R, D, ld_x, codes, ld_c, scale, s);

@@ -1027,6 +1027,31 @@ extern "C" rl_status rl_verify_drafts(const rl_verify_drafts_desc* desc, void* s
       off(d.uniforms, 8) || off(d.tokens, 8) || off(d.n_accepted, 8) || off(d.draft_ids, 8) || off(d.draft_lse, 4) ||
       off(d.n_draft, 4) || off(d.logp_out, 4) || off(d.lse_out, 4) || off(d.status_dev, 4))
     return RL_ERR_ALIGN;
+  const long long rows = d.B * (d.G + 1), drafts = d.B * d.G;
+  if (rows > (1LL << 60) / (d.ld * es) || (d.draft_logits && drafts > 0 && drafts > (1LL << 60) / (d.ld_draft * es)))
+    return RL_ERR_SHAPE;  // more than 64 bits address
+  // what is written shares no byte with what is read, nor with what else is written
+  struct Span {
+    const void* p;
+    long long bytes;
+  };
+  const Span out[4] = {{d.tokens, rows * 8}, {d.n_accepted, d.B * 8}, {d.logp_out, rows * 4}, {d.lse_out, rows * 4}};
+  const Span in[6] = {{d.target_logits, ((rows - 1) * d.ld + d.V) * es},
+                      {drafts > 0 ? d.draft_logits : nullptr, ((drafts - 1) * d.ld_draft + d.V) * es},
+                      {drafts > 0 && d.draft_logits ? d.draft_lse : nullptr, drafts * 4},
+                      {drafts > 0 ? d.draft_ids : nullptr, drafts * 8},
+                      {d.n_draft, d.B * 4},
+                      {d.uniforms, rows * 8}};
+  const auto meet = [](const Span& x, const Span& y) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    return a && b && a < b + static_cast<uintptr_t>(y.bytes) && b < a + static_cast<uintptr_t>(x.bytes);
+  };
+  for (int i = 0; i < 4; ++i) {
+    for (const Span& s : in)
+      if (meet(out[i], s)) return RL_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return RL_ERR_ALIAS;
+  }
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     return RL_ERR_CUDA;

@@ -136,6 +136,22 @@ def test_workspace_size(lib):
     assert call_logits(lib, **call) == rl.RL_ERR_WORKSPACE
 
 
+@needs_nvcc
+@pytest.mark.parametrize("over", [
+    dict(ws=FAKE + 1024), dict(ws=at(2) + 16), dict(ws=at(4) + 16), dict(ws=at(1) + 16, sh=at(1) + 16), dict(ws=at(3), sw=at(3) + 8),
+    dict(out=at(4), sh=at(4) + 64), dict(out=at(4), sw=at(4) + 4096), dict(out=at(4) + 16 * 1000, ws=at(4)),
+])
+def test_logits_shared_memory(lib, over):
+    """Neither the logits nor the scratch may lie in what is read, nor in one another."""
+    assert call_logits(lib, **over) == rl.RL_ERR_ALIAS
+
+
+@needs_nvcc
+@pytest.mark.parametrize("over", [dict(codes=FAKE + 1024), dict(scale=FAKE + 64), dict(scale=at(1) + 1008 * 7), dict(codes=at(2), scale=at(2) + 16)])
+def test_codes_shared_memory(lib, over):
+    assert call_quantize(lib, **over) == rl.RL_ERR_ALIAS
+
+
 def verify_desc(**over):
     d = rl.rl_verify_drafts_desc_init()
     d.target_logits, d.B, d.G, d.V, d.ld = FAKE, 8, 3, 1000, 1000
@@ -186,6 +202,23 @@ def test_verify_desc_defaults(lib):
 ])
 def test_verify_refusals(lib, over, expect):
     assert lib.rl_verify_drafts(ctypes.byref(verify_desc(**over)), None) == expect
+
+
+@needs_nvcc
+@pytest.mark.parametrize("over", [
+    dict(tokens=at(3)), dict(tokens=at(3) + 8 * 23), dict(tokens=at(4) + 8), dict(tokens=FAKE + 16), dict(tokens=at(1) + 16), dict(tokens=at(2)),
+    dict(n_draft=at(6), tokens=at(6) - 8), dict(n_accepted=at(5) + 8 * 31), dict(n_accepted=at(3)), dict(logp_out=at(2) + 4), dict(lse_out=at(2)),
+    dict(logp_out=at(7), lse_out=at(7)), dict(logp_out=at(7), lse_out=at(7) + 4 * 31), dict(logp_out=at(5)), dict(lse_out=at(4)),
+])
+def test_verify_shared_memory(lib, over):
+    """No output may lie in an input or in another output."""
+    assert lib.rl_verify_drafts(ctypes.byref(verify_desc(**over)), None) == rl.RL_ERR_ALIAS
+
+
+@needs_nvcc
+def test_verify_rows_that_64_bits_do_not_address(lib):
+    assert lib.rl_verify_drafts(ctypes.byref(verify_desc(B=1 << 24, ld=1 << 39)), None) == rl.RL_ERR_SHAPE
+    assert lib.rl_verify_drafts(ctypes.byref(verify_desc(B=1 << 24, ld_draft=1 << 39)), None) == rl.RL_ERR_SHAPE
 
 
 @needs_nvcc
