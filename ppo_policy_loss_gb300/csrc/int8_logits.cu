@@ -26,6 +26,11 @@
 //     32 neighbouring channels of a token at a time.
 //   * N is a multiple of 16 up to 192 (2 accumulators of 192 columns and two widened tiles
 //     of 64 fill the 512 columns of tensor memory); 128 where sums stay in the epilogue's registers (D > 1024).
+//   * What bounds it.  Few tokens: HBM (1 token, 151,936 x 1024: 30 us, of which 6.7 us are launches, the
+//     first tiles and the last stores; what more channels add runs at 6.7 TB/s).  Many: shared memory, at 128 bytes a
+//     cycle.  A step writes the token tile (2 N cycles) and reads it (2 N), writes the weight tile (128) and
+//     reads it (128): 1024 cycles at N = 192, of which the MMA needs 768 and a step takes 1044 (4096 tokens:
+//     750 to 870 us, 1.47 to 1.7 PFLOP/s).  That is why weights are widened into tensor memory.
 //   * Every mbarrier wait is bounded; on timeout the kernel raises an error
 //     flag, waits for its own copies and tensor-core work, writes NaN for what it has
 //     not finished, frees its tensor memory and exits.
@@ -643,16 +648,16 @@ IPlan int8_plan(long long R, long long D, long long V) {
   p.n_tt = static_cast<int>((R + p.N - 1) / p.N);
   p.n_vt = static_cast<int>((V + kM - 1) / kM);
   p.steps = static_cast<int>((D + kStepK - 1) / kStepK);
-  const long long tile_b = static_cast<long long>(p.N) * 256, budget = kRingBytes;
+  const long long tile_b = static_cast<long long>(p.N) * 256, ring = kRingBytes;
   // weights in flight are what a small batch waits for: at least 80 KB of them beside resident tokens
-  p.resident = p.n_tt == 1 && p.steps <= kMaxB && p.steps * tile_b + 5 * static_cast<long long>(kTileA) <= budget;
+  p.resident = p.n_tt == 1 && p.steps <= kMaxB && p.steps * tile_b + 5 * static_cast<long long>(kTileA) <= ring;
   if (p.resident) {
     p.slots_b = p.steps;
-    const long long room = (budget - p.steps * tile_b) / kTileA;
+    const long long room = (ring - p.steps * tile_b) / kTileA;
     p.slots_a = static_cast<int>(room < kMaxA ? room : kMaxA);
   } else {
     p.slots_a = kMaxWide;
-    const long long room = (budget - p.slots_a * static_cast<long long>(kTileA)) / tile_b;
+    const long long room = (ring - p.slots_a * static_cast<long long>(kTileA)) / tile_b;
     p.slots_b = static_cast<int>(room < kMaxDone ? room : kMaxDone);
   }
   const int wide = (static_cast<int>(kTmemAll) - 2 * p.N) / kWideCols;

@@ -574,6 +574,53 @@ def test_captured_and_replayed():
             assert torch.equal(out[0], want[0]) and torch.equal(out[1]["tokens"], want[1]["tokens"]) and torch.equal(out[1]["lse"], want[1]["lse"])
 
 
+def test_behind_other_work():
+    """Calls whose inputs the launch, copy or fill right before them writes, in part on a stream that is joined there: one after
+    another, and captured.  (Each call's launch may begin before that work has ended.)"""
+    sets = [step_inputs(seed) for seed in (6, 7)]
+    wants = [rollout_step(*s) for s in sets]
+    source, here = [x.clone() for x in sets[0]], [x.clone() for x in sets[0]]
+    z, side = torch.empty_like(wants[0][0]), torch.cuda.Stream()
+    (B, G), V = here[2].shape, z.shape[1]
+
+    def step():
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            here[1].copy_(source[1])                       # a copy, joined right before the step
+        here[2].copy_(source[2])
+        here[3].zero_()
+        here[3].add_(source[3])
+        here[0].copy_(source[0])
+        torch.cuda.current_stream().wait_stream(side)
+        logits, out = rollout_step(*here)
+        z.fill_(-1.0)
+        z.copy_(logits)                                    # a copy right before a verification
+        again = torch_api.verify_drafts(z.view(B, G + 1, V), here[2], here[3])
+        here[3].zero_()                                    # a fill: every draft stays that can, the first token is drawn
+        first = torch_api.verify_drafts(z.view(B, G + 1, V), here[2], here[3])
+        return logits, out, again, first
+
+    def check(got, want):
+        assert torch.equal(got[0], want[0])
+        for k in ("tokens", "n_accepted", "logp", "lse"):
+            assert torch.equal(got[1][k], want[1][k]) and torch.equal(got[2][k], want[1][k])
+        possible = want[0].view(B, G + 1, V).gather(2, here[2].clamp(0, V - 1)[..., None].expand(B, G, 1)) > -math.inf
+        assert torch.equal(got[3]["n_accepted"], possible[..., 0].long().cumprod(1).sum(1))
+
+    for k in range(40):
+        for x, y in zip(source, sets[k % 2]):
+            x.copy_(y)
+        check(step(), wants[k % 2])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for k in range(10):
+        for x, y in zip(source, sets[k % 2]):
+            x.copy_(y)
+        g.replay()
+        check(got, wants[k % 2])
+
+
 def test_the_c_names():
     """The bindings that forward to the C entry points, with their defaults."""
     hidden, weight, ids, u = step_inputs(7)
