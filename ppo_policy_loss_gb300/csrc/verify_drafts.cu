@@ -20,9 +20,9 @@
 //     p there, and W - S Q of the sums over that set takes the S of the same pass.
 //
 // What bounds it.  One row of 151,936 bf16 logits takes 9.3 us: launch, one pass (2 us) and a
-// chain of short steps.  Few sequences are such chains of rows (64 with four drafts each: 70 us).  Many are bound by the FMA
-// pipe where drafts are refused, 62 packed operations for two tokens of both rows (512 with four drafts: 336 us; all kept:
-// 267 us), else by HBM and the last round of sequences (512 draws: 71 us, 2.2 TB/s, 125 us where some fall back).
+// chain of short steps.  Few sequences are such chains of rows (64 with four drafts each: 66 us).  Many are bound by
+// instructions and their latency where drafts are refused, 62 packed operations for two tokens of both rows (512 with four drafts:
+// 322 us, all kept 260), else by HBM and the last round of sequences (512 draws: 67 us, 2.3 TB/s; 122 where some fall back).
 //
 // fp32 sums, in units of 2^-24: a term 2^x carries 4 of the hardware exponential and 2 ln 2 |x|
 // of its argument (the FMA's rounding and c's), |x| weighted by p at most log2 V <= 26;
