@@ -264,18 +264,23 @@ struct FineExp {
   __device__ __forceinline__ bool is_zero(float z) const { return !(__fsub_rn(z, off) > zmin); }
 };
 
-// The differences of two terms, and 1 where they are positive, 0 elsewhere.  Of positive
-// differences the first number is the larger one in a, or the two are so near that
+// The differences of two terms, 1 where they are positive, 0 elsewhere, and 1 where they are within
+// `window` of q.  Of positive differences the first number is the larger one in a, or the two are so near that
 // p.a - q.a is exact.
-__device__ __forceinline__ Term2 above(const Term2& p, const Term2& q, float2& more) {
+__device__ __forceinline__ Term2 above(const Term2& p, const Term2& q, float2& more, float window, float2& beside) {
   float2 e;
   Term2 d;
   d.a = quick_two_sum2(p.a, make_float2(-q.a.x, -q.a.y), e);
   d.b = sub2(p.b, q.b);
   d.c = add2(e, sub2(p.c, q.c));
-  const float2 s = add2(add2(d.a, d.b), d.c);
+  const float2 s = add2(add2(d.a, d.b), d.c), w = mul2(q.a, both(window));
   more = make_float2(s.x > 0.f ? 1.f : 0.f, s.y > 0.f ? 1.f : 0.f);
+  beside = make_float2(fabsf(s.x) < w.x ? 1.f : 0.f, fabsf(s.y) < w.y ? 1.f : 0.f);
   return d;
+}
+__device__ __forceinline__ Term2 above(const Term2& p, const Term2& q, float2& more) {
+  float2 beside;
+  return above(p, q, more, 0.f, beside);
 }
 
 // A sum of such terms, none above 1: hi and mid start at 1, so that the error

@@ -15,13 +15,14 @@
 //     token's own weight, everything is summed again in fine arithmetic (fine_exp.cuh).
 //  3. Where a draft with a distribution was refused, the weights max(p - q, 0)
 //     are sums of differences, and always taken in fine arithmetic, in one pass over
-//     the target's and the draft's row: with S known to 2^-19 from step 1, the set of tokens
-//     with p > q is right but for tokens with p = q to 2^-19, whose weight is below 2^-19 of
-//     p there, and W - S Q of the sums over that set takes the S of the same pass.
+//     the target's and the draft's row: S is known to fp32 from step 1, and W - S Q of the sums over the set of tokens
+//     with p > q takes the S of the same pass.  The set is right but for tokens with p / q within S's error of 1; what they
+//     have of q is summed too, and where it counts (a draft's row that nearly equals the target's) the pass is made again with the
+//     new S.
 //
 // What bounds it.  One row of 151,936 bf16 logits takes 9.3 us: launch, one pass (2 us) and a
 // chain of short steps.  Few sequences are such chains of rows (64 with four drafts each: 66 us).  Many are bound by
-// instructions and their latency where drafts are refused, 62 packed operations for two tokens of both rows (512 with four drafts:
+// instructions and their latency where drafts are refused, 64 packed operations for two tokens of both rows (512 with four drafts:
 // 322 us, all kept 260), else by HBM and the last round of sequences (512 draws: 67 us, 2.3 TB/s; 122 where some fall back).
 //
 // fp32 sums, in units of 2^-24: a term 2^x carries 4 of the hardware exponential and 2 ln 2 |x|
@@ -53,6 +54,7 @@ constexpr int kMaxCluster = 16, kMaxParts = kMaxCluster * kWarps;
 constexpr double kLog2eD = 1.4426950408889634074;
 constexpr float kCoarse = 0x1p-19f;  // seven times the largest error met (above)
 constexpr float kFar = 0x1p20f;       // |m c| beyond which m - 86 T is near m's own last place
+constexpr float kWindow = 0x1p-17f;   // of p / q around 1, in which a row's fp32 sum may leave open which is larger
 constexpr float kNothing = 0x1p-90f;  // sums of weights that are 0 (e^-86 each) stay below
 
 struct Args {
@@ -103,9 +105,8 @@ enum Verdict { kStays, kRefused, kNoDistribution };
 // What the CTAs of a cluster tell one another, in turn in two places: whoever writes the
 // one has passed the barrier behind which everybody had read the other.
 struct Exchange {
-  Stats stats[kMaxParts];
+  Stats stats[kMaxParts];  // of a fine pass over two rows: (q beside p, -, q below p)
   Wide sum[kMaxParts], plus[kMaxParts];
-  float drafted[kMaxParts];
   long long token;
   int unsure;
 };
@@ -818,24 +819,24 @@ verify_drafts_kernel(const Args a, int cluster) {
       Weights<DT, kRest, true, kUnit> f{row, draft_row, -1, 0.f, 0.f, fp, fp, sm.powers};
       Wide total;
       total.h = two_sum(st.n, st.s, total.l);
-      const Wide S = total;
       const float lq = a.draft_lse[b * G + kept];
+      bool sure = false;
 #pragma unroll 1
-      for (int pass = 0; pass < 2; ++pass) {
-        const Wide k = Wide(lq) - ln_wide(total, sm.powers);
+      for (int pass = 0;; ++pass) {
+        const Wide S = total, k = Wide(lq) - ln_wide(S, sm.powers);
         const float mq = rintf(k.h * a.T * 4096.f) * 0x1p-12f;
         Wide r;
         r.h = a.r_hi;
         r.l = a.r_lo;
         // (q's least term is above p's: a token that neither can give, -inf twice or behind the row, has no p - q)
         f.q.init(a.r_hi, a.r_lo, a.T, mq, (k - Wide(mq) * r).h, fabsf(mq) * a.c > kFar, -84.f);
-        if (pass == 1) break;
-        // sums of p over all tokens, and of p - q and of q over those with p > q
+        if (sure) break;
+        // sums of p over all tokens, of p - q and of q over those with p > q, and of q over those with p next to q
         Wide all(0.f), plus(0.f);
         FineSum fa, fb;
         fa.clear();
         fb.clear();
-        float2 qs = both(0.f);
+        float2 qs = both(0.f), ns = both(0.f);
         int count = 0;
 #pragma unroll 1
         for (long long i = lo + lane * F::kVec; i < hi; i += 32 * F::kVec) {
@@ -848,11 +849,12 @@ verify_drafts_kernel(const Args a, int cluster) {
           for (int j = 0; j < F::kVec; j += 2) {
             bad = bad || !(y[j] < INFINITY) || !(y[j + 1] < INFINITY);
             const Term2 w = f.fine(make_float2(z[j], z[j + 1])), q = f.drafted(make_float2(y[j], y[j + 1]));
-            float2 more;
+            float2 more, beside;
             fa.add(w);
-            const Term2 r = above(w, q, more);
+            const Term2 r = above(w, q, more, kWindow, beside);
             fb.add(r, more);
             qs = __ffma2_rn(more, q.a, qs);
+            ns = __ffma2_rn(beside, q.a, ns);
           }
           if (++count == 64) {
             all += fa.value();
@@ -864,28 +866,36 @@ verify_drafts_kernel(const Args a, int cluster) {
         }
         all = warp_sum(all + fa.value());
         plus = warp_sum(plus + fb.value());
-        const float drafted = warp_sum(qs.x + qs.y);
+        const float drafted = warp_sum(qs.x + qs.y), next_to = warp_sum(ns.x + ns.y);
         bad = __any_sync(0xffffffffu, bad);
         g.turn ^= 1;
         Exchange& ex = sm.ex[g.turn];
         tell(g, &ex.sum[part], bad ? Wide(-1.f) : all, lane);
         tell(g, &ex.plus[part], plus, lane);
-        tell(g, &ex.drafted[part], drafted, lane);
+        tell(g, &ex.stats[part], Stats{next_to, 0.f, drafted}, lane);
         g.sync();
         total = Wide(0.f);
+        float close = 0.f;
         bad = false;
         for (int j = lane; j < parts; j += 32) {
           bad = bad || ex.sum[j].h < 0.f;
           total += ex.sum[j];
+          close += ex.stats[j].m;
         }
         total = warp_sum(total);
+        close = warp_sum(close);
         bad = __any_sync(0xffffffffu, bad);
         if (bad) break;
+        // q's terms were taken with S, and belong to `total`.  Which tokens have p > q was asked with S too: those
+        // that it decides otherwise have p / q within (total - S) / S of 1, and a weight below that much of q.  Where they may
+        // have more than 2^-36 of the total together, all is done once more with the total for S.
+        const float more = (total - S).h / S.h;
+        sure = pass == 2 || (fabsf(more) < 0.5f * kWindow && fabsf(more) * close < 0x1p-36f * total.h);
+        if (!sure) continue;
         __syncthreads();
-        if (warp == 0) {  // q's terms were taken with S, and belong to `total`
-          const float more = (total - S).h / S.h;
+        if (warp == 0) {
           for (int j = lane; j < parts; j += 32) {
-            const Wide r = ex.plus[j] - Wide(more * ex.drafted[j]);
+            const Wide r = ex.plus[j] - Wide(more * ex.stats[j].s);
             ex.plus[j] = r.h > 0.f ? r : Wide(0.f);
           }
         }

@@ -1,0 +1,78 @@
+"""Verification and sampling where rows, numbers and shares of the work lie at an edge: draft rows that nearly
+equal the target's, low temperatures, log-sum-exps of any size, tokens of almost no probability, numbers next to
+a draft's own border, maxima that rise all along a row, and the same sequences by clusters of every size."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import ppo_policy_loss_gb300 as rl
+from ppo_policy_loss_gb300 import torch_api
+from tests._rollout import RESOLUTION, f64, make_logits
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BATCHES = (3, 30, 70, 110, 250, 400)   # clusters of 16, 10, 5, 4, 2 and 1 CTAs on 152 SMs (V = 33,000)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    rl.build()
+    rl.load()
+
+
+def rows(t, B, n=1):
+    """[B, n, V] on the GPU, every row the 1-D ``t``, 16-byte aligned."""
+    V, per = t.shape[0], 16 // t.element_size()
+    return torch.nn.functional.pad(t, (0, -V % per)).to(DEV).expand(B, n, -1).contiguous()[..., :V]
+
+
+def softmax(z, T=1.0):
+    e = np.exp(z / T - (z / T).max())
+    return e / e.sum(), (z / T).max() + math.log(e.sum())
+
+
+def check_draws(tokens, w, x):
+    """The drawn tokens of weights w (of p's total of 1) with uniforms x: the border x W lies in the token's
+    interval, to the resolution of its ends, and the token has a weight."""
+    edges = np.cumsum(w)
+    at = x * edges[-1]
+    assert (tokens >= 0).all()
+    assert (w[tokens] > 0).all(), (tokens[w[tokens] <= 0][:4], w[tokens][w[tokens] <= 0][:4])
+    off = np.maximum(edges[tokens] - w[tokens] - at, at - edges[tokens])
+    assert (off <= RESOLUTION).all(), (math.log2(off.max()), tokens[off > RESOLUTION][:4])
+
+
+# ------------------------------------------------------------------ max(p - q, 0)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("beside", [-1e-7, -3e-8, -1e-8, 1e-8, 3e-8, 1e-7])
+@pytest.mark.parametrize("B", BATCHES)
+def test_draft_that_nearly_equals_the_target(dtype, beside, B):
+    """The draft's row is the target's but for a masked tail of mass 2e-7 and one token that it has 300 times as
+    often, and everywhere else p / q = 1 + beside: which tokens have p > q is known only once the row's sum is known
+    to more than fp32 gives."""
+    V = 33000
+    z = make_logits((1,), V, dtype, 3, sure=False)[0]
+    # without the one token that brings the row's log-sum-exp nearest to `beside` below a float
+    e = np.exp(f64(z))
+    lq = np.float32(math.log(e.sum()))
+    if float(lq) > math.log(e.sum()) + beside:
+        lq = np.nextafter(lq, np.float32(-np.inf))
+    z[int(np.argmin(np.abs(np.log(e.sum() - e) - (float(lq) - beside))))] = -math.inf
+    p, lse = softmax(f64(z))
+    assert abs(float(lq) - lse - beside) < 2e-9
+    order = np.argsort(p)
+    tail = order[:int(np.searchsorted(np.cumsum(p[order]), 2e-7))]
+    d = int(order[np.searchsorted(p[order], 1e-9)])
+    y = z.clone()
+    y[tail] = -math.inf
+    y[d] = z[d].float() + math.log(300.0)
+    w = np.maximum(p - np.exp(f64(y) - np.float64(lq)), 0.0)
+    assert w[d] == 0 and w.sum() > 1e-7
+    x = np.random.default_rng(B).random(B)
+    u = torch.from_numpy(np.stack([np.full(B, 0.999), x], 1)).to(DEV)
+    out = torch_api.verify_drafts(rows(z, B, 2), torch.full((B, 1), d, device=DEV), u, draft_logits=rows(y, B),
+                                  draft_lse=torch.full((B, 1), float(lq), device=DEV))
+    assert (out["n_accepted"] == 0).all()
+    check_draws(out["tokens"][:, 0].cpu().numpy(), w, x)
