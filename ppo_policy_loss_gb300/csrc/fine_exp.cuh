@@ -1,4 +1,4 @@
-// fine_exp.cuh — e^y to 2^-41 in fp32 arithmetic, and sums of such terms that
+// fine_exp.cuh — e^y to 2^-39 (2^-41 in a row's own frame) in fp32 arithmetic, and sums of such terms that
 // keep it, for the places where a sum over the vocabulary is compared with a
 // random number: between two of 10^5 tokens' borders lie 10^-5 of the total,
 // and a sum of fp32 terms, off by 10^-8, would give another token once in a
@@ -203,6 +203,8 @@ __device__ __forceinline__ float2 quick_two_sum2(float2 x, float2 y, float2& err
   return s;
 }
 
+constexpr float kFar = 0x1p20f;       // |m| / (T ln 2) beyond which m - 86 T is near m's own last place
+
 // e^((z - m) / T - kappa).  z counts as at least zmin, so that what is
 // below e^-86 (and -inf) gives e^-86, which no sum notices (is_zero() tells it from a
 // weight), or another `low`, and as at most zmax, so that what is above 4 gives about 4.
@@ -211,8 +213,8 @@ __device__ __forceinline__ float2 quick_two_sum2(float2 x, float2 y, float2& err
 struct FineExp {
   float r_hi, r_lo, kappa, off, m, zmin, zmax;
 
-  // 1 / T as two floats; the frame: the terms are e^(z / T - k), kappa = k - m / T.
-  __device__ __forceinline__ void init(float r_hi_, float r_lo_, float T, float m_, float kappa_, bool far, float low = -86.f) {
+  // 1 / T as two floats; the frame: a number of the row's type, where the terms are 1.
+  __device__ __forceinline__ void init(float r_hi_, float r_lo_, float T, float m_, bool far, float kappa_ = 0.f, float low = -86.f) {
     r_hi = r_hi_;
     r_lo = r_lo_;
     off = far ? m_ : 0.f;
@@ -220,6 +222,22 @@ struct FineExp {
     kappa = kappa_;
     zmin = fmaf(low, T, m);
     zmax = fmaf(1.4f, T, m);
+  }
+  // e^(z / T - lse + ln_s), c = log2(e) / T.  m is the multiple of 2^-16 of T's power of two next to (lse - ln_s) T, so
+  // that z - m is exact or has a float as its error, and |kappa| <= 2^-17: what is added to kappa in at()
+  // is off by 2^-41 a step, 2^-39 in all.  (A coarser m leaves more in kappa, and a term good to 2^-23 kappa and to its
+  // fourth power: steps of 2^-12 at every temperature gave 2^-35 at T = 1 and 2^-28 at 0.01.)  Where m has no such digits, beyond
+  // |m| = 2^8 T, it is the nearest float, and kappa and the error grow with |lse|: 2^-35 at |lse| = 2^11.
+  __device__ __forceinline__ void init_around(float r_hi_, float r_lo_, float T, float c, float lse, const Wide& ln_s, float low) {
+    const Wide k = Wide(lse) - ln_s;
+    const int step_bits = (__float_as_int(T) & 0x7f800000) - (16 << 23);
+    const float step = __int_as_float(step_bits), per_step = __int_as_float((254 << 23) - step_bits);
+    float x = k.h * T;
+    if (fabsf(x) < 0x1p23f * step) x = rintf(x * per_step) * step;
+    Wide r;
+    r.h = r_hi_;
+    r.l = r_lo_;
+    init(r_hi_, r_lo_, T, x, fabsf(x) * c > kFar, (k - Wide(x) * r).h, low);
   }
   // kWide: z has 24 significant bits (16-bit numbers have 8 or 11).  kTop: z may be above zmax.  kUnit: T = 1.
   template <bool kWide, bool kTop, bool kUnit>
@@ -328,7 +346,7 @@ __device__ __forceinline__ Wide ln_wide(const Wide& s, const uint2* powers) {
   ln2.l = -0x1.05c610p-29f;
   const float y = __logf(f.h);
   FineExp e;
-  e.init(1.f, 0.f, 1.f, 0.f, 0.f, false);
+  e.init(1.f, 0.f, 1.f, 0.f, false);
   const Wide over = f * e.at<true, false, true>(-y, powers).value() - Wide(1.f);
   const float fix = __fmul_rn(over.h, fmaf(over.h, -0.5f, 1.f));
   return Wide(static_cast<float>(n)) * ln2 + Wide(y) + Wide(fix);

@@ -53,7 +53,6 @@ constexpr int kCtasPerSm = 3;
 constexpr int kMaxCluster = 16, kMaxParts = kMaxCluster * kWarps;
 constexpr double kLog2eD = 1.4426950408889634074;
 constexpr float kCoarse = 0x1p-19f;  // seven times the largest error met (above)
-constexpr float kFar = 0x1p20f;       // |m c| beyond which m - 86 T is near m's own last place
 constexpr float kWindow = 0x1p-17f;   // of p / q around 1, in which a row's fp32 sum may leave open which is larger
 constexpr float kNothing = 0x1p-90f;  // sums of weights that are 0 (e^-86 each) stay below
 
@@ -369,10 +368,9 @@ __device__ __forceinline__ float log_prob(float z, const Stats& st, double inv_t
 template <bool kUnit>
 __device__ __forceinline__ double draft_prob(float z, float lse, const Args& a, const uint2* powers) {
   const double x = static_cast<double>(z) * a.inv_t - static_cast<double>(lse);
-  const float m = rintf(lse * a.T * 4096.f) * 0x1p-12f;
-  if (!(x > -80.0 && x < 1.0 && fabsf(m) < 4096.f)) return exp(x);
+  if (!(x > -80.0 && x < 1.0 && fabsf(lse) < 256.f)) return exp(x);
   FineExp q;
-  q.init(a.r_hi, a.r_lo, a.T, m, static_cast<float>(static_cast<double>(lse) - static_cast<double>(m) * a.inv_t), false);
+  q.init_around(a.r_hi, a.r_lo, a.T, a.c, lse, Wide(0.f), -86.f);
   const Wide v = q.template at<true, false, kUnit>(z, powers).value();
   return static_cast<double>(v.h) + static_cast<double>(v.l);
 }
@@ -772,7 +770,7 @@ verify_drafts_kernel(const Args a, int cluster) {
       mine = part_stats_exact<DT>(row, lo, hi, a.c, lane);
     }
     bad = !(fabsf(st.m) < INFINITY) || !(st.n > 0.f);
-    fp.init(a.r_hi, a.r_lo, a.T, st.m, 0.f, fabsf(st.m) * a.c > kFar);
+    fp.init(a.r_hi, a.r_lo, a.T, st.m, fabsf(st.m) * a.c > kFar);
     if (bad || i == n) {
       if (writes && lse) lse[i] = bad ? nan : static_cast<float>(static_cast<double>(st.m) * a.inv_t + log1pf((st.n - 1.f) + st.s));
       break;
@@ -815,7 +813,7 @@ verify_drafts_kernel(const Args a, int cluster) {
   if (!bad) {
     const unsigned char* draft_row = a.draft ? a.draft + (b * G + kept) * a.draft_bytes : nullptr;
     if (lost && a.draft) {
-      // S q_v = e^(z / T - k), k = lse_q - ln S, in the frame of a number with few digits
+      // S q_v = e^(z / T - lse_q + ln S)
       Weights<DT, kRest, true, kUnit> f{row, draft_row, -1, 0.f, 0.f, fp, fp, sm.powers};
       Wide total;
       total.h = two_sum(st.n, st.s, total.l);
@@ -823,13 +821,9 @@ verify_drafts_kernel(const Args a, int cluster) {
       bool sure = false;
 #pragma unroll 1
       for (int pass = 0;; ++pass) {
-        const Wide S = total, k = Wide(lq) - ln_wide(S, sm.powers);
-        const float mq = rintf(k.h * a.T * 4096.f) * 0x1p-12f;
-        Wide r;
-        r.h = a.r_hi;
-        r.l = a.r_lo;
+        const Wide S = total;
         // (q's least term is above p's: a token that neither can give, -inf twice or behind the row, has no p - q)
-        f.q.init(a.r_hi, a.r_lo, a.T, mq, (k - Wide(mq) * r).h, fabsf(mq) * a.c > kFar, -84.f);
+        f.q.init_around(a.r_hi, a.r_lo, a.T, a.c, lq, ln_wide(S, sm.powers), -84.f);
         if (sure) break;
         // sums of p over all tokens, of p - q and of q over those with p > q, and of q over those with p next to q
         Wide all(0.f), plus(0.f);

@@ -9,7 +9,7 @@ import torch
 
 import ppo_policy_loss_gb300 as rl
 from ppo_policy_loss_gb300 import torch_api
-from tests._rollout import RESOLUTION, f64, make_logits
+from tests._rollout import RESOLUTION, TORCH, f64, make_logits
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -76,3 +76,34 @@ def test_draft_that_nearly_equals_the_target(dtype, beside, B):
                                   draft_lse=torch.full((B, 1), float(lq), device=DEV))
     assert (out["n_accepted"] == 0).all()
     check_draws(out["tokens"][:, 0].cpu().numpy(), w, x)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("temperature,shift", [(1.0, 0.0), (0.7, 0.0), (0.7, 20.0), (0.1, 0.0), (0.1, 3.0), (0.03, 1.0), (0.01, 0.0), (0.01, 0.5), (30.0, 0.0), (100.0, 700.0)])
+def test_refused_drafts_next_to_a_border_at_any_temperature(dtype, temperature, shift):
+    """Numbers 1.1 to 4 resolutions of p's total to either side of a border of max(p - q, 0), in rows whose
+    log-sum-exps lie anywhere."""
+    V, T, n, each = 4000, temperature, 24, 20
+    gen, rng = torch.Generator().manual_seed(7), np.random.default_rng(1)
+    z = (torch.randn((n, V), generator=gen) * 3 * T + shift).to(TORCH[dtype])
+    y = (z.float() + torch.randn((n, V), generator=gen) * T).to(TORCH[dtype])
+    weights, lqs, xs, ids = [], [], [], []
+    for i in range(n):
+        p, _ = softmax(f64(z[i]), T)
+        q, lse = softmax(f64(y[i]), T)
+        lqs.append(np.float32(lse))
+        w = np.maximum(p - np.exp(f64(y[i]) / T - np.float64(lqs[-1])), 0.0)
+        edges = np.cumsum(w)
+        some = rng.choice(np.nonzero(w > 64 * RESOLUTION)[0][:-1], each, replace=False)
+        xs.append((edges[some] + rng.uniform(1.1, 4.0, each) * rng.choice([-1.0, 1.0], each) * RESOLUTION) / edges[-1])
+        weights.append(w)
+        ids.append(int(np.argmax(q - p)))
+    u = np.stack([np.full(n * each, 1 - 2.0 ** -53), np.concatenate(xs)], 1)
+    spread = lambda t: t.to(DEV)[:, None].expand(n, each, V).reshape(n * each, 1, V)  # noqa: E731
+    out = torch_api.verify_drafts(spread(z).expand(-1, 2, V).contiguous(), torch.tensor(ids, device=DEV).repeat_interleave(each)[:, None],
+                                  torch.from_numpy(u).to(DEV), draft_logits=spread(y).contiguous(),
+                                  draft_lse=torch.tensor(np.array(lqs), device=DEV).repeat_interleave(each)[:, None].contiguous(), temperature=T)
+    assert (out["n_accepted"] == 0).all()
+    tokens = out["tokens"][:, 0].cpu().numpy().reshape(n, each)
+    for i in range(n):
+        check_draws(tokens[i], weights[i], xs[i])
