@@ -205,6 +205,15 @@ __device__ __forceinline__ float2 quick_two_sum2(float2 x, float2 y, float2& err
 
 constexpr float kFar = 0x1p20f;       // |m| / (T ln 2) beyond which m - 86 T is near m's own last place
 
+// lse - ln_s - off / T as y / T + kappa, y a multiple of `step`.  (Next to a float so large that 100 is nothing, terms are 0
+// or too large anyway.  Out of line: with it in the kernel 228 refused drafts took 164 us in place of 161.)
+__device__ __noinline__ float2 beyond(float off, float T, double inv_t, float lse, float ln_h, float ln_l, float step) {
+  double left = fma(-static_cast<double>(off), inv_t, static_cast<double>(lse)) - (static_cast<double>(ln_h) + static_cast<double>(ln_l));
+  left = fmin(fmax(left, -100.0), 100.0);
+  const float y = rintf(static_cast<float>(left) * T / step) * step;
+  return make_float2(y, static_cast<float>(fma(-static_cast<double>(y), inv_t, left)));
+}
+
 // e^((z - m) / T - kappa).  z counts as at least zmin, so that what is
 // below e^-86 (and -inf) gives e^-86, which no sum notices (is_zero() tells it from a
 // weight), or another `low`, and as at most zmax, so that what is above 4 gives about 4.
@@ -223,21 +232,30 @@ struct FineExp {
     zmin = fmaf(low, T, m);
     zmax = fmaf(1.4f, T, m);
   }
-  // e^(z / T - lse + ln_s), c = log2(e) / T.  m is the multiple of 2^-16 of T's power of two next to (lse - ln_s) T, so
+  // e^(z / T - lse + ln_s).  m is the multiple of 2^-16 of T's power of two next to (lse - ln_s) T, so
   // that z - m is exact or has a float as its error, and |kappa| <= 2^-17: what is added to kappa in at()
   // is off by 2^-41 a step, 2^-39 in all.  (A coarser m leaves more in kappa, and a term good to 2^-23 kappa and to its
-  // fourth power: steps of 2^-12 at every temperature gave 2^-35 at T = 1 and 2^-28 at 0.01.)  Where m has no such digits, beyond
-  // |m| = 2^8 T, it is the nearest float, and kappa and the error grow with |lse|: 2^-35 at |lse| = 2^11.
-  __device__ __forceinline__ void init_around(float r_hi_, float r_lo_, float T, float c, float lse, const Wide& ln_s, float low) {
+  // fourth power: steps of 2^-12 at every temperature gave 2^-35 at T = 1 and 2^-28 at 0.01.)  Where a float has no such digits,
+  // from 2^8 T on, the nearest one is `off` and m what it leaves; z - off is exact where e^(z / T - lse) is above
+  // e^-60, and the error that of the subtraction of off / T, |lse| 2^-52, where that is more.
+  __device__ __forceinline__ void init_around(float r_hi_, float r_lo_, float T, double inv_t, float lse, const Wide& ln_s, float low) {
     const Wide k = Wide(lse) - ln_s;
     const int step_bits = (__float_as_int(T) & 0x7f800000) - (16 << 23);
     const float step = __int_as_float(step_bits), per_step = __int_as_float((254 << 23) - step_bits);
-    float x = k.h * T;
-    if (fabsf(x) < 0x1p23f * step) x = rintf(x * per_step) * step;
-    Wide r;
-    r.h = r_hi_;
-    r.l = r_lo_;
-    init(r_hi_, r_lo_, T, x, fabsf(x) * c > kFar, (k - Wide(x) * r).h, low);
+    float2 at = make_float2(k.h * T, 0.f);
+    float far_off = 0.f;
+    if (fabsf(at.x) < 0x1p24f * step) {
+      at.x = rintf(at.x * per_step) * step;
+      Wide r;
+      r.h = r_hi_;
+      r.l = r_lo_;
+      at.y = (k - Wide(at.x) * r).h;
+    } else {
+      far_off = fminf(fmaxf(at.x, -0x1.fffffep127f), 0x1.fffffep127f);
+      at = beyond(far_off, T, inv_t, lse, ln_s.h, ln_s.l, step);
+    }
+    init(r_hi_, r_lo_, T, at.x, false, at.y, low);
+    off = far_off;
   }
   // kWide: z has 24 significant bits (16-bit numbers have 8 or 11).  kTop: z may be above zmax.  kUnit: T = 1.
   template <bool kWide, bool kTop, bool kUnit>

@@ -370,7 +370,7 @@ __device__ __forceinline__ double draft_prob(float z, float lse, const Args& a, 
   const double x = static_cast<double>(z) * a.inv_t - static_cast<double>(lse);
   if (!(x > -80.0 && x < 1.0 && fabsf(lse) < 256.f)) return exp(x);
   FineExp q;
-  q.init_around(a.r_hi, a.r_lo, a.T, a.c, lse, Wide(0.f), -86.f);
+  q.init_around(a.r_hi, a.r_lo, a.T, a.inv_t, lse, Wide(0.f), -86.f);
   const Wide v = q.template at<true, false, kUnit>(z, powers).value();
   return static_cast<double>(v.h) + static_cast<double>(v.l);
 }
@@ -823,7 +823,7 @@ verify_drafts_kernel(const Args a, int cluster) {
       for (int pass = 0;; ++pass) {
         const Wide S = total;
         // (q's least term is above p's: a token that neither can give, -inf twice or behind the row, has no p - q)
-        f.q.init_around(a.r_hi, a.r_lo, a.T, a.c, lq, ln_wide(S, sm.powers), -84.f);
+        f.q.init_around(a.r_hi, a.r_lo, a.T, a.inv_t, lq, ln_wide(S, sm.powers), -84.f);
         if (sure) break;
         // sums of p over all tokens, of p - q and of q over those with p > q, and of q over those with p next to q
         Wide all(0.f), plus(0.f);

@@ -107,3 +107,32 @@ def test_refused_drafts_next_to_a_border_at_any_temperature(dtype, temperature, 
     tokens = out["tokens"][:, 0].cpu().numpy().reshape(n, each)
     for i in range(n):
         check_draws(tokens[i], weights[i], xs[i])
+
+
+@pytest.mark.parametrize("dtype,size,temperature", [
+    (dtype, size, T) for dtype, sizes in (("f32", (3e4, 1e6, 1e9, 1e15, 1e36, 3e38)), ("bf16", (3e4, 1e6, 1e15, 1e36)), ("f16", (6e4,))) for size in sizes
+    for T in (1.0, 0.5, 2.0 ** -6, 64.0, 0.7, 0.01) if size / T < 3.3e38 and (size < 1e5 or math.log2(T) % 1 == 0)])
+@pytest.mark.parametrize("B", [3, 250])
+def test_draft_logits_of_any_size(dtype, size, temperature, B):
+    """A draft's row of which one token has all: it is refused, and another one is drawn.  The same with every token at
+    a very low number: q is 1 everywhere, nothing is left of max(p - q, 0), and the token is drawn from p."""
+    V, T = 33000, temperature
+    z = make_logits((1,), V, dtype, 11, sure=False)[0]
+    z = (z.float() * min(T, 1.0)).to(TORCH[dtype])
+    p, _ = softmax(f64(z), T)
+    rng = np.random.default_rng(5)
+    d, x = int(np.argmax(p)), rng.random(B)
+    high, low = torch.zeros(V).to(TORCH[dtype]), torch.full((V,), -size).to(TORCH[dtype])
+    high[d] = size
+    for row in (high, low):
+        lse = np.float32(f64(row)[d] / T)
+        with np.errstate(over="ignore"):
+            q = np.exp(f64(row) / T - np.float64(lse))
+        assert (q[0] < 1e-30 or q[0] > 0.9) and q[d] > 0.9
+        w = np.maximum(p - q, 0.0)
+        w = w if w.any() else p
+        u = torch.from_numpy(np.stack([np.full(B, 1 - 2.0 ** -53), x], 1)).to(DEV)
+        out = torch_api.verify_drafts(rows(z, B, 2), torch.full((B, 1), d, device=DEV), u, draft_logits=rows(row, B),
+                                      draft_lse=torch.full((B, 1), float(lse), device=DEV), temperature=T)
+        assert (out["n_accepted"] == 0).all()
+        check_draws(out["tokens"][:, 0].cpu().numpy(), w, x)
