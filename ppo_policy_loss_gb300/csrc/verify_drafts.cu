@@ -375,6 +375,12 @@ __device__ __forceinline__ double draft_prob(float z, float lse, const Args& a, 
   return static_cast<double>(v.h) + static_cast<double>(v.l);
 }
 
+// u e^x S < e^y, for what fp32 or fp64 numbers do not hold: y below -86, or u = 0 beside a q that may be anything.
+__device__ __noinline__ bool stays_by_logs(double u, double x, double S, double y) {
+  if (!(y > -INFINITY)) return false;
+  return u <= 0.0 || log(u) + x + log(S) < y;
+}
+
 template <int DT, int MODE, bool kFine, bool kUnit>
 struct Weights {
   const unsigned char* row;
@@ -786,6 +792,10 @@ verify_drafts_kernel(const Args a, int cluster) {
         const float left = static_cast<float>(ui) * ex2_approx(x) * (st.n + st.s);
         if (fabsf(x) < 128.f && fabsf(zq * a.c) < 1024.f && fabsf(left - w.a) > 0x1p-8f * w.a && w.a > 0x1p-100f) {
           v = left < w.a ? kStays : kRefused;
+        } else if (w.a == 0.f || !(ui > 0.0)) {
+          const double xq = a.draft ? static_cast<double>(zq) * a.inv_t - static_cast<double>(lq) : 0.0;
+          v = stays_by_logs(ui, xq, static_cast<double>(st.n) + static_cast<double>(st.s),
+                            (static_cast<double>(zd) - static_cast<double>(st.m)) * a.inv_t) ? kStays : kRefused;
         } else {
           const double qd = a.draft ? draft_prob<kUnit>(zq, lq, a, sm.powers) : 1.0;
           const Wide p = w.value();

@@ -136,3 +136,36 @@ def test_draft_logits_of_any_size(dtype, size, temperature, B):
                                       draft_lse=torch.full((B, 1), float(lse), device=DEV), temperature=T)
         assert (out["n_accepted"] == 0).all()
         check_draws(out["tokens"][:, 0].cpu().numpy(), w, x)
+
+
+# ------------------------------------------------------------------ a draft's own test
+@pytest.mark.parametrize("temperature,gap", [(1.0, 100.0), (1.0, 700.0), (1.0, 2000.0), (0.1, 9.0), (0.1, 300.0), (0.01, 0.9), (0.01, 5.0), (0.01, 100.0)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("numbers", [torch.float32, torch.float64])
+def test_drafts_of_almost_no_probability(dtype, temperature, gap, numbers):
+    """A draft stays iff u q < p, however small p is: with u = 0 and with q = 0 always."""
+    V, T, B = 1000, temperature, 6
+    z = (torch.randn(V, generator=torch.Generator().manual_seed(9)) * 0.1 * T).to(TORCH[dtype])
+    z[3] = 0.5 * T
+    z[7] = 0.5 * T - gap
+    y = torch.zeros(V).to(TORCH[dtype])
+    y[7] = -math.inf
+    log_p = (f64(z)[7] - f64(z).max()) / T - math.log(softmax(f64(z), T)[0].max() ** -1)
+    ids = torch.full((B, 1), 7, device=DEV)
+    u = torch.full((B, 2), 0.5, dtype=torch.float64)
+    u[:, 0] = torch.tensor([0.0, math.exp(max(log_p - 2, -740)), math.exp(max(log_p - 0.01, -740)), math.exp(max(log_p + 0.01, -740)), 1e-3, 1 - 2.0 ** -53],
+                           dtype=numbers).clamp(max=1 - 2.0 ** -53)
+    x = u[:, 0].numpy()
+    stays = (x == 0) | (np.log(np.maximum(x, 5e-324)) < log_p)
+    out = torch_api.verify_drafts(rows(z, B, 2), ids, u.to(DEV), temperature=T)
+    assert np.array_equal(out["n_accepted"].cpu().numpy(), stays.astype(int))
+    logp = out["logp"][:, 0].cpu().numpy()
+    assert np.abs(logp[stays] / log_p - 1).max() < 2.0 ** -20
+    # q = 0 at the draft
+    out = torch_api.verify_drafts(rows(z, B, 2), ids, u.to(DEV), draft_logits=rows(y, B), draft_lse=torch.full((B, 1), math.log(V - 1.0), device=DEV), temperature=T)
+    assert (out["n_accepted"] == 1).all()
+    # p = 0: refused, whatever u and q
+    z[7] = -math.inf
+    for kw in (dict(), dict(draft_logits=rows(y, B), draft_lse=torch.full((B, 1), math.log(V - 1.0), device=DEV))):
+        out = torch_api.verify_drafts(rows(z, B, 2), ids, u.to(DEV), temperature=T, **kw)
+        assert (out["n_accepted"] == 0).all() and (out["tokens"][:, 0] != 7).all()
