@@ -108,9 +108,9 @@ size_t rl_lmhead_int8_workspace_size(long long R, long long D);
  * call draws one token for each row; lse_out is then what a later call takes
  * as draft_lse.  Rows behind the first draft that does not stay decide
  * nothing.  The drawn token's border is resolved to 2^-34 of the total (for
- * max(p - q, 0) of p's total, and to 2^-52 |draft_lse| where that is more) or better, so that
- * it is the same in any batch; a
- * draft's own test as finely as fp32 sums a row (some 2^-22 of p_i(d)).
+ * max(p - q, 0) of p's total, and to 2^-52 |draft_lse| where that is more) or better, a
+ * draft's own test to 2^-34 of p_i(d) (likewise), so that what stays and what is drawn are the same in
+ * any batch.
  * Log-probabilities are fp32, with relative precision next to 0.
  *
  * n_draft[b] = -1 leaves a sequence out: its tokens are -1, the rest 0, nothing

@@ -54,6 +54,7 @@ constexpr int kMaxCluster = 16, kMaxParts = kMaxCluster * kWarps;
 constexpr double kLog2eD = 1.4426950408889634074;
 constexpr float kCoarse = 0x1p-19f;  // seven times the largest error met (above)
 constexpr float kWindow = 0x1p-17f;   // of p / q around 1, in which a row's fp32 sum may leave open which is larger
+constexpr double kOpen = 0x1p-17;     // relative: a draft's test that is nearer asks for the row's fine sum
 constexpr float kNothing = 0x1p-90f;  // sums of weights that are 0 (e^-86 each) stay below
 
 struct Args {
@@ -99,7 +100,7 @@ __device__ __forceinline__ Stats merged(Stats a, Stats b, float c) {
   return a;
 }
 
-enum Verdict { kStays, kRefused, kNoDistribution };
+enum Verdict { kStays, kRefused, kNoDistribution, kNear };
 
 // What the CTAs of a cluster tell one another, in turn in two places: whoever writes the
 // one has passed the barrier behind which everybody had read the other.
@@ -122,6 +123,7 @@ struct Smem {
   long long found;
   int verdict;
   Wide u;              // for the draw
+  double left, right;  // of a draft's test that fp32 sums leave open: u q, and p's term
 };
 
 // ------------------------------------------------------------------ the cluster
@@ -637,6 +639,18 @@ __device__ __forceinline__ void tell_sum(Weights<DT, MODE, true, kUnit>& f, long
   tell(g, &sm.ex[g.turn].sum[part], s, lane);
   g.sync();
 }
+// The row's sum in fine arithmetic, in every thread of the cluster.  (Out of line, for one draft in 2^16 asks for it.  A draw
+// that falls back, one in twenty, has the sum in line: 64 draws take 41 us, 44 with a call.)
+template <int DT, bool kUnit>
+__device__ __noinline__ double row_sum(const unsigned char* row, long long lo, long long hi, FineExp p, Group& g, Smem& sm) {
+  Weights<DT, kSoftmax, true, kUnit> f{row, nullptr, -1, 0.f, 0.f, p, p, sm.powers};
+  tell_sum(f, lo, hi, g, sm);
+  Wide total(0.f);
+  for (int j = threadIdx.x & 31; j < g.size * kWarps; j += 32) total += sm.ex[g.turn].sum[j];
+  total = warp_sum(total);
+  return static_cast<double>(total.h) + static_cast<double>(total.l);
+}
+
 // The token, in the CTA that has it; kElsewhere in the others, which have nothing left to do;
 // kNowhere in all where no part has any weight.
 constexpr long long kElsewhere = -2, kNowhere = -3;
@@ -799,13 +813,25 @@ verify_drafts_kernel(const Args a, int cluster) {
         } else {
           const double qd = a.draft ? draft_prob<kUnit>(zq, lq, a, sm.powers) : 1.0;
           const Wide p = w.value();
-          v = ui * qd * (static_cast<double>(st.n) + static_cast<double>(st.s)) < static_cast<double>(p.h) + static_cast<double>(p.l) ? kStays : kRefused;
+          const double uq = ui * qd, right = static_cast<double>(p.h) + static_cast<double>(p.l);
+          const double over = uq * (static_cast<double>(st.n) + static_cast<double>(st.s)) - right;
+          v = over < 0.0 ? kStays : kRefused;
+          if (fabs(over) <= kOpen * right) {
+            v = kNear;
+            sm.left = uq;
+            sm.right = right;
+          }
         }
       }
       sm.verdict = v;
     }
     __syncthreads();
-    const int v = sm.verdict;
+    int v = sm.verdict;
+    if (v == kNear) {  // the same in every CTA
+      Group h = g;
+      v = sm.left * row_sum<DT, kUnit>(row, lo, hi, fp, h, sm) < sm.right ? kStays : kRefused;
+      g.turn = h.turn;
+    }
     if (writes) {
       if (lse) lse[i] = static_cast<float>(static_cast<double>(st.m) * a.inv_t + log1pf((st.n - 1.f) + st.s));
       if (v == kStays) {

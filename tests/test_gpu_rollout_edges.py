@@ -169,3 +169,27 @@ def test_drafts_of_almost_no_probability(dtype, temperature, gap, numbers):
     for kw in (dict(), dict(draft_logits=rows(y, B), draft_lse=torch.full((B, 1), math.log(V - 1.0), device=DEV))):
         out = torch_api.verify_drafts(rows(z, B, 2), ids, u.to(DEV), temperature=T, **kw)
         assert (out["n_accepted"] == 0).all() and (out["tokens"][:, 0] != 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("temperature", [1.0, 0.7, 0.05])
+@pytest.mark.parametrize("kind", ["model", "lookup"])
+@pytest.mark.parametrize("B", BATCHES)
+def test_drafts_next_to_their_own_border(dtype, temperature, kind, B):
+    """u within 2^-32 of p / q to either side, by clusters of every size: what stays does not depend on the batch."""
+    V, T = 33000, temperature
+    z = make_logits((1,), V, dtype, 13, sure=False)[0]
+    z = (z.float() * T).to(TORCH[dtype])
+    z[100] = 9.0 * T
+    p, _ = softmax(f64(z), T)
+    y = z.clone()
+    y[100] = z[100].float() + 0.75 * T
+    q, lse = softmax(f64(y), T)
+    lq = np.float32(lse)
+    border = p[100] / (math.exp(f64(y)[100] / T - float(lq)) if kind == "model" else 1.0)
+    u = np.full((B, 2), 0.3)
+    sign = np.where(np.arange(B) % 2 == 0, 1.0, -1.0)
+    u[:, 0] = border * (1 + sign * 2.0 ** -32 * (1 + np.arange(B) % 7))
+    kw = dict(draft_logits=rows(y, B), draft_lse=torch.full((B, 1), float(lq), device=DEV)) if kind == "model" else {}
+    out = torch_api.verify_drafts(rows(z, B, 2), torch.full((B, 1), 100, device=DEV), torch.from_numpy(u).to(DEV), temperature=T, **kw)
+    assert np.array_equal(out["n_accepted"].cpu().numpy(), (sign < 0).astype(int))
