@@ -291,7 +291,7 @@ __device__ __forceinline__ Stats part_stats(Stream<DT>& in, float c, int lane, v
         s = fmaf(s + err, ex2_approx(rho), n) * ex2_approx((m - wm) * c);
         err = 0.f;
         n = 0.f;
-        m = wm;
+        m = max_nan(m, wm);  // (a NaN stays)
         nm = -m * c;
         // what the new frame's terms are off by, s is now off by too
         s *= ex2_approx(-fmaf(-m, c, -nm));

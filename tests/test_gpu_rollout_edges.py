@@ -138,6 +138,33 @@ def test_draft_logits_of_any_size(dtype, size, temperature, B):
         check_draws(out["tokens"][:, 0].cpu().numpy(), w, x)
 
 
+# ------------------------------------------------------------------ numbers that are none
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("V,B", [(33000, 3), (33000, 70), (33000, 250), (33000, 400), (200000, 3)])
+def test_a_row_with_one_number_that_is_none(dtype, value, V, B):
+    """Wherever it stands in the row, and whatever stands behind it: no token, no log-probability; in a draft's row the same."""
+    z = rows(make_logits((1,), V, dtype, 31)[0], B).clone()
+    at = torch.from_numpy(np.random.default_rng(B).integers(0, V, B)).to(DEV)
+    at[0], at[1], at[2] = 0, V - 1, V // 2
+    one = torch.arange(B, device=DEV)
+    clean = z.clone()
+    z[one, 0, at] = value
+    u = torch.full((B, 1), 0.4, dtype=torch.float64, device=DEV)
+    out = torch_api.verify_drafts(z, None, u)
+    assert (out["tokens"] == -1).all() and out["logp"].isnan().all() and out["lse"].isnan().all() and (out["n_accepted"] == 0).all()
+    # a draft's row with it, where the draft is refused and its row asked
+    ids = torch.full((B, 1), 17, device=DEV)
+    at[at == 17] = 18
+    y = clean.clone()
+    y[one, 0, 17] += 9.0
+    lse = y[:, 0].double().logsumexp(-1).float()[:, None].contiguous()
+    y[one, 0, at] = value
+    u2 = torch.full((B, 2), 0.9, dtype=torch.float64, device=DEV)
+    out = torch_api.verify_drafts(rows(clean[0, 0], B, 2), ids, u2, draft_logits=y, draft_lse=lse)
+    assert (out["tokens"] == -1).all() and out["logp"][:, 0].isnan().all() and (out["n_accepted"] == 0).all()
+
+
 # ------------------------------------------------------------------ a draft's own test
 @pytest.mark.parametrize("temperature,gap", [(1.0, 100.0), (1.0, 700.0), (1.0, 2000.0), (0.1, 9.0), (0.1, 300.0), (0.01, 0.9), (0.01, 5.0), (0.01, 100.0)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
