@@ -5,7 +5,9 @@
 //  1. The sequence's target rows in order, until a draft does not stay: maximum
 //     and sum of e^((z - m) / T) of the row in one pass, fp32, online, with the warp's
 //     maximum as the frame (one FMA an element: x = z c + nm; the rounding of nm = -m c, common
-//     to a frame's terms, is put right when the frame ends).  The maxima, whose terms are exactly 1,
+//     to a frame's terms, is put right when the frame ends).  A maximum that rises by less than 2^4 keeps
+//     the frame: each change costs the sum some units of its last place, and a row may rise all along (2^26
+//     fp32 numbers from 0 to 0.01: off by 669 units with a frame for each maximum, by 3 so).  The maxima, whose terms are exactly 1,
 //     are counted beside the sum, so that log S keeps its relative precision
 //     where one token holds nearly all the mass.  Rows behind a refused draft
 //     are not read.
@@ -52,6 +54,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 3;
 constexpr int kMaxCluster = 16, kMaxParts = kMaxCluster * kWarps;
 constexpr double kLog2eD = 1.4426950408889634074;
+constexpr float kSlack = 4.f;         // a frame stays while the maximum's term is below 2^4
 constexpr float kCoarse = 0x1p-19f;  // seven times the largest error met (above)
 constexpr float kWindow = 0x1p-17f;   // of p / q around 1, in which a row's fp32 sum may leave open which is larger
 constexpr double kOpen = 0x1p-17;     // relative: a draft's test that is nearer asks for the row's fine sum
@@ -286,15 +289,19 @@ __device__ __forceinline__ Stats part_stats(Stream<DT>& in, float c, int lane, v
       asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(wm) : "f"(pm));
     }
     if (!(wm < m)) {
-      if (!(wm == m)) {  // the frame ends: its sum goes along, and so do the old maxima
-        const float rho = fmaf(-m, c, -nm);
-        s = fmaf(s + err, ex2_approx(rho), n) * ex2_approx((m - wm) * c);
-        err = 0.f;
+      if (!(wm == m)) {  // the old maxima join the sum
+        float lost;
+        s = two_sum(s, n * ex2_approx(fmaf(m, c, nm)), lost);
+        err += lost;
         n = 0.f;
         m = max_nan(m, wm);  // (a NaN stays)
-        nm = -m * c;
-        // what the new frame's terms are off by, s is now off by too
-        s *= ex2_approx(-fmaf(-m, c, -nm));
+        if (!(fmaf(m, c, nm) < kSlack)) {  // the frame ends, and its sum goes along
+          s = (s + err) * ex2_approx(-fmaf(m, c, nm));
+          err = 0.f;
+          nm = -m * c;
+          // what the new frame's terms are off by, s is now off by too
+          s *= ex2_approx(-fmaf(-m, c, -nm));
+        }
       }
       n += static_cast<float>(F::template drop_value<16>(w, m, true));
     }
@@ -330,6 +337,7 @@ template <int DT>
 __device__ __noinline__ Stats part_stats_exact(const unsigned char* row, long long lo, long long hi, float c, int lane) {
   using F = Fmt<DT>;
   Stats a{-FLT_MAX, 0.f, 0.f};
+  float frame = a.m, err = 0.f, lost;
   for (long long i = lo + lane * F::kVec; i < hi; i += 32 * F::kVec) {
     float z[F::kVec];
     F::unpack(load_vec<DT>(row, i, hi), z);
@@ -338,9 +346,15 @@ __device__ __noinline__ Stats part_stats_exact(const unsigned char* row, long lo
     for (int j = 1; j < F::kVec; ++j) vm = max_nan(vm, z[j]);
     if (!(vm < a.m)) {
       if (!(vm == a.m)) {
-        a.s = (a.n + a.s) * ex2_approx((a.m - vm) * c);
+        a.s = two_sum(a.s, a.n * ex2_approx((a.m - frame) * c), lost);
+        err += lost;
         a.n = 0.f;
         a.m = max_nan(a.m, vm);
+        if (!((a.m - frame) * c < kSlack)) {
+          a.s = (a.s + err) * ex2_approx((frame - a.m) * c);
+          err = 0.f;
+          frame = a.m;
+        }
       }
 #pragma unroll
       for (int j = 0; j < F::kVec; ++j) {
@@ -350,9 +364,13 @@ __device__ __noinline__ Stats part_stats_exact(const unsigned char* row, long lo
         }
       }
     }
+    float t = 0.f;
 #pragma unroll
-    for (int j = 0; j < F::kVec; ++j) a.s += ex2_approx((z[j] - a.m) * c);
+    for (int j = 0; j < F::kVec; ++j) t += ex2_approx((z[j] - frame) * c);
+    a.s = two_sum(a.s, t, lost);
+    err += lost;
   }
+  a.s = (a.s + err) * ex2_approx((frame - a.m) * c);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     a = merged(a, Stats{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.n, o), __shfl_xor_sync(0xffffffffu, a.s, o)}, c);

@@ -9,7 +9,7 @@ import torch
 
 import ppo_policy_loss_gb300 as rl
 from ppo_policy_loss_gb300 import torch_api
-from tests._rollout import RESOLUTION, TORCH, f64, make_logits
+from tests._rollout import RESOLUTION, TORCH, U, f64, make_logits
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -220,3 +220,80 @@ def test_drafts_next_to_their_own_border(dtype, temperature, kind, B):
     kw = dict(draft_logits=rows(y, B), draft_lse=torch.full((B, 1), float(lq), device=DEV)) if kind == "model" else {}
     out = torch_api.verify_drafts(rows(z, B, 2), torch.full((B, 1), 100, device=DEV), torch.from_numpy(u).to(DEV), temperature=T, **kw)
     assert np.array_equal(out["n_accepted"].cpu().numpy(), (sign < 0).astype(int))
+
+
+# ------------------------------------------------------------------ the row's sum
+def sum_bound(V):
+    """Of a row's fp32 sum, relative, in units of 2^-24, whatever V: a term carries 4 of the hardware exponential and
+    2 ln 2 |x| of its argument (the FMA's rounding and c's), |x| weighted by p at most log2 V; 9 additions in a chunk's
+    chains, its frame's end and the frame's correction 10 each, 5 joins of lanes, 7 of a part's frame, 9 joins of parts."""
+    return 4 + 2 * math.log(2) * math.log2(V) + 9 + 20 + 5 + 7 + 9
+
+
+def check_sums(z, T=1.0):
+    """lse of rows z [n, V] and the log-probabilities of drawn tokens."""
+    n, V = z.shape
+    per = 16 // z.element_size()
+    zd = torch.nn.functional.pad(z, (0, -V % per)).to(DEV)[:, :V]
+    out = torch_api.sample_tokens(zd, torch.full((n,), 0.37, dtype=torch.float64, device=DEV), temperature=T)
+    x = f64(z) / T
+    m = x.max(1)
+    e = np.exp(x - m[:, None])
+    top = e == 1.0
+    log_s = np.log1p(top.sum(1) - 1 + np.where(top, 0.0, e).sum(1))
+    tol = (sum_bound(V) + 4 * np.abs(log_s)) * U
+    lse, logp = (out[k].cpu().numpy().astype(np.float64) for k in ("lse", "logp"))
+    err = np.abs(lse - (m + log_s))
+    assert (err <= tol + U * np.abs(m + log_s)).all(), (err / U, sum_bound(V))
+    want = x[np.arange(n), out["tokens"].cpu().numpy()] - m - log_s
+    err = np.abs(logp - want)
+    assert (err <= tol + 2 * U * np.abs(want)).all(), (err / U, sum_bound(V))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("V,n", [(5, 3), (1000, 3), (33000, 3), (33000, 400), (151936, 4), (151936, 200), (1 << 20, 2), (1 << 22, 1)])
+def test_sums_of_long_rows(dtype, V, n):
+    check_sums(make_logits((n,), V, dtype, V + n))
+    check_sums(make_logits((n,), V, dtype, V + n, sure=False), 0.7)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V,n", [(33000, 400), (1 << 20, 2), (1 << 23, 1)])
+@pytest.mark.parametrize("rise", [1e-3, 0.01, 0.1, 1.0, 5.0])
+@pytest.mark.parametrize("way", [1, -1])
+def test_sums_of_rows_that_rise(dtype, V, n, rise, way):
+    """The maximum rises by a little from one part of the row to the next."""
+    z = torch.linspace(0, rise, V, dtype=torch.float64)
+    z = (z if way > 0 else z.flip(0)).to(TORCH[dtype])
+    check_sums(z.expand(n, V).contiguous())
+
+
+@pytest.mark.parametrize("rise", [0.01, 0.5])
+def test_sums_of_the_longest_rows_that_rise(rise):
+    check_sums(torch.linspace(0, rise, 1 << 26)[None])
+
+
+@pytest.mark.parametrize("V", [33000, 1 << 20, 1 << 25])
+@pytest.mark.parametrize("at", [3.0e7, -2.0e4, 1.0e9])
+@pytest.mark.parametrize("T", [1.0, 100.0])
+def test_sums_of_rows_taken_by_differences(V, at, T):
+    """Rows of large or very low numbers, their sums as those of any other row."""
+    step = float(np.spacing(np.float32(abs(at))))
+    k = torch.randint(0, max(1, int(8 * T / step)) + 2, (2, V), generator=torch.Generator().manual_seed(1))
+    check_sums((at - k.double() * step).float(), T)
+    k = torch.arange(V).expand(2, V) * (max(1, int(8 * T / step)) + 2) // V
+    check_sums((at + k.double() * step).float(), T)
+
+
+@pytest.mark.parametrize("dtype,V", [("f32", 1 << 20), ("bf16", 1 << 20), ("f32", 1 << 26)])
+@pytest.mark.parametrize("rise", [0.01, 0.5, 2.0])
+def test_draws_of_rows_that_rise(dtype, V, rise):
+    """Numbers some 2^-22 to 2^-16 of the total to either side of a border, in rows whose maximum rises all along."""
+    z = torch.linspace(0, rise, V, dtype=torch.float64).to(TORCH[dtype])
+    p, _ = softmax(f64(z))
+    n = 200 if V <= 1 << 20 else 12
+    edges, rng = np.cumsum(p), np.random.default_rng(3)
+    at = rng.integers(0, V - 1, n)
+    x = np.clip(edges[at] + 2.0 ** rng.uniform(-22, -16, n) * rng.choice([-1.0, 1.0], n), 0.0, 1 - 2.0 ** -53)
+    out = torch_api.verify_drafts(rows(z, n), None, torch.from_numpy(x)[:, None].to(DEV))
+    check_draws(out["tokens"][:, 0].cpu().numpy(), p, x)
