@@ -110,7 +110,9 @@ size_t rl_lmhead_int8_workspace_size(long long R, long long D);
  * nothing.  The drawn token's border is resolved to 2^-34 of the total (for
  * max(p - q, 0) of p's total, and to 2^-52 |draft_lse| where that is more) or better, a
  * draft's own test to 2^-34 of p_i(d) (likewise), so that what stays and what is drawn are the same in
- * any batch.
+ * any batch.  (fp32 sums decide what lies further than 2^-19 of the total from a border, or 2^-17 of p_i(d); that
+ * they are never off by so much rests on rows built to add up their roundings, of which none was off by
+ * more than 2^-20.3, not on a proof.)
  * Log-probabilities are fp32, with relative precision next to 0.
  *
  * n_draft[b] = -1 leaves a sequence out: its tokens are -1, the rest 0, nothing

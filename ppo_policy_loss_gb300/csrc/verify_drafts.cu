@@ -30,13 +30,15 @@
 // fp32 sums, in units of 2^-24: a term 2^x carries 4 of the hardware exponential and 2 ln 2 |x|
 // of its argument (the FMA's rounding and c's), |x| weighted by p at most log2 V <= 26;
 // 32 terms are added in chains of 10, the chains' sums with their errors kept; then
-// 5 joins in the warp, some for the frames of lanes and warps, and 15 in the running sums of the
-// search.  These are of both signs and hardly ever add up: over rows of
-// 151,936 logits in random, rising and falling order, of one, two and evenly spread values, in each type,
-// a token drawn from the fp32 sums alone was never further than 2.6e-7 (4.4 units) of S from
-// its border.  Where the border is within 32 units the fine sums decide.  (With 192 units, which cover the
-// sum of all bounds, 22% of N(0, 9) rows fell back instead of 5%.)  fp64 is kept for what a single lane
-// decides: the unit does two operations a cycle and SM, and a warp that adds in fp64 holds it for 16 cycles.
+// 12 where a frame ends, 5 joins in the warp, 10 for the frames of lanes and warps, and up to 50 roundings in the running
+// sums of the search.  What a comparison with the border takes of the terms' errors is at most half of the largest (they are in
+// the total too), 45 units if all that depends on the values adds up, and the roundings of the search are of both signs.
+// Over 6 10^5 batches of rows built to add them up (halves, blocks and cycles of few values, ramps, one value just below a
+// top, sorted ones; 2,000 to 400,000 numbers of each type, temperatures of 0.011 to 90) a token drawn from the fp32 sums
+// alone was never further than 12.3 units of S from its border.  Where the border is within 32 units the fine sums decide.
+// (64 units, more than all but the search can add up to: a draw of 24 rows in turn 11.6 us against 10.6, 64 draws 42.0 against 41.0, 512
+// 121 against 117.  192 units, the sum of all bounds: 22% of N(0, 9) rows fell back instead of 5%.)  fp64 is kept for what a
+// single lane decides: the unit does two operations a cycle and SM, and a warp that adds in fp64 holds it for 16 cycles.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -55,7 +57,7 @@ constexpr int kCtasPerSm = 3;
 constexpr int kMaxCluster = 16, kMaxParts = kMaxCluster * kWarps;
 constexpr double kLog2eD = 1.4426950408889634074;
 constexpr float kSlack = 4.f;         // a frame stays while the maximum's term is below 2^4
-constexpr float kCoarse = 0x1p-19f;  // seven times the largest error met (above)
+constexpr float kCoarse = 0x1p-19f;  // 2.6 times the largest error met (above)
 constexpr float kWindow = 0x1p-17f;   // of p / q around 1, in which a row's fp32 sum may leave open which is larger
 constexpr double kOpen = 0x1p-17;     // relative: a draft's test that is nearer asks for the row's fine sum
 constexpr float kNothing = 0x1p-90f;  // sums of weights that are 0 (e^-86 each) stay below

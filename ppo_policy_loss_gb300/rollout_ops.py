@@ -20,10 +20,6 @@ from .token_ops import _DT, _given, _logits, _on, _p, _raw_stream, _status, _wri
 _F32, _I64 = torch.float32, torch.int64
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
-
-
 def _codes(name: str, t: torch.Tensor) -> int:
     """Row stride of a [rows, D] matrix of 8-bit codes."""
     if t.dtype != torch.int8 or t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):

@@ -297,3 +297,31 @@ def test_draws_of_rows_that_rise(dtype, V, rise):
     x = np.clip(edges[at] + 2.0 ** rng.uniform(-22, -16, n) * rng.choice([-1.0, 1.0], n), 0.0, 1 - 2.0 ** -53)
     out = torch_api.verify_drafts(rows(z, n), None, torch.from_numpy(x)[:, None].to(DEV))
     check_draws(out["tokens"][:, 0].cpu().numpy(), p, x)
+
+
+# ------------------------------------------------------------------ clusters of every size
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["none", "model", "lookup"])
+def test_the_same_sequences_by_clusters_of_every_size(dtype, kind):
+    """Tokens of the same sequences in batches that clusters of 16, 10, 5, 4, 2 and 1 CTAs take, bit for bit, their
+    drawn tokens' numbers 2^-32 to 2^-17 of the total from a border of the last row."""
+    V, B, G = 33000, max(BATCHES), 0 if kind == "none" else 1
+    gen = torch.Generator().manual_seed(17)
+    z = make_logits((1,), V, dtype, 19, sure=False)[0]
+    p, _ = softmax(f64(z))
+    edges, rng = np.cumsum(p), np.random.default_rng(23)
+    u = np.random.default_rng(29).random((B, G + 1))
+    u[:, G] = np.clip(edges[rng.integers(1, V - 1, B)] + 2.0 ** rng.uniform(-32, -17, B) * rng.choice([-1.0, 1.0], B), 0, 1 - 2.0 ** -53)
+    a = dict(target_logits=rows(z, B, G + 1), draft_ids=None, uniforms=torch.from_numpy(u).to(DEV))
+    if G:
+        y = (z.float() + torch.randn(V, generator=gen) * 0.7).to(z.dtype)
+        q, lse = softmax(f64(y))
+        a["draft_ids"] = torch.from_numpy(rng.choice(V, (B, 1), p=q)).to(DEV)
+        if kind == "model":
+            a.update(draft_logits=rows(y, B), draft_lse=torch.full((B, 1), float(np.float32(lse)), device=DEV))
+    whole = torch_api.verify_drafts(**a)
+    for n in BATCHES:
+        for lo in range(0, B - n + 1, max(n, 80)):
+            part = torch_api.verify_drafts(**{k: v if v is None else v[lo:lo + n] for k, v in a.items()})
+            for k in ("tokens", "n_accepted"):
+                assert torch.equal(part[k], whole[k][lo:lo + n]), (n, lo, k)
