@@ -138,6 +138,39 @@ def test_draft_logits_of_any_size(dtype, size, temperature, B):
         check_draws(out["tokens"][:, 0].cpu().numpy(), w, x)
 
 
+@pytest.mark.parametrize("dtype,at", [("f32", 5.0e3), ("f32", -2.0e4), ("f32", 3.0e7), ("f32", 1.0e9), ("f32", -1.0e9), ("bf16", 3.0e4), ("bf16", -3.0e4), ("bf16", 1.0e9), ("f16", 6.0e4), ("f16", -6.0e4)])
+@pytest.mark.parametrize("temperature", [1.0, 64.0])
+@pytest.mark.parametrize("B", [3, 70, 400])
+def test_refused_drafts_of_rows_of_large_numbers(dtype, at, temperature, B):
+    """Both rows far from 0, their numbers some steps of the type apart (a temperature that is a power of two: the fp64 form is
+    exact); the draft's log-sum-exp is what fp32 holds of it."""
+    V, T = 33000, temperature
+    base = torch.tensor(at).to(TORCH[dtype])
+    step = abs(float(torch.nextafter(base, torch.zeros_like(base)).double() - base.double()))
+    gen = torch.Generator().manual_seed(37)
+    levels = max(2, int(8 * T / step))
+    k = torch.randint(0, levels, (V,), generator=gen)
+    far = -1.0 if at > 0 else 1.0     # towards 0 steps do not grow
+    z = (base.double() + far * k * step).to(TORCH[dtype])
+    y = (base.double() + far * ((k + torch.randint(0, max(2, levels // 6), (V,), generator=gen)) % levels) * step).to(TORCH[dtype])
+    p, _ = softmax(f64(z), T)
+    lq = np.float32(softmax(f64(y), T)[1])
+    with np.errstate(over="ignore"):
+        q = np.exp(f64(y) / T - np.float64(lq))
+    w = np.maximum(p - q, 0.0)
+    w = w if w.any() else p
+    d = int(np.argmax(q - p))
+    x = np.random.default_rng(B).random(B)
+    u = torch.from_numpy(np.stack([np.full(B, 1 - 2.0 ** -53), x], 1)).to(DEV)
+    out = torch_api.verify_drafts(rows(z, B, 2), torch.full((B, 1), d, device=DEV), u, draft_logits=rows(y, B),
+                                  draft_lse=torch.full((B, 1), float(lq), device=DEV), temperature=T)
+    if q[d] * (1 - 2.0 ** -53) < p[d]:
+        assert (out["n_accepted"] == 1).all() and (out["tokens"][:, 0] == d).all()
+    else:
+        assert (out["n_accepted"] == 0).all()
+        check_draws(out["tokens"][:, 0].cpu().numpy(), w, x)
+
+
 # ------------------------------------------------------------------ numbers that are none
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("value", [math.nan, math.inf])
