@@ -108,7 +108,7 @@ size_t rl_lmhead_int8_workspace_size(long long R, long long D);
  * call draws one token for each row; lse_out is then what a later call takes
  * as draft_lse.  Rows behind the first draft that does not stay decide
  * nothing.  The drawn token's border is resolved to 2^-34 of the total (for
- * max(p - q, 0) of p's total, and to 2^-52 |draft_lse| where that is more) or better, a
+ * max(p - q, 0) of p's total; to V 2^-52, or 2^-52 |draft_lse|, where that is more) or better, a
  * draft's own test to 2^-34 of p_i(d) (likewise), so that what stays and what is drawn are the same in
  * any batch.  (fp32 sums decide what lies further than 2^-19 of the total from a border, or 2^-17 of p_i(d); that
  * they are never off by so much rests on rows built to add up their roundings, of which none was off by

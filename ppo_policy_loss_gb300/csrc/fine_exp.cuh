@@ -319,14 +319,22 @@ __device__ __forceinline__ Term2 above(const Term2& p, const Term2& q, float2& m
   return above(p, q, more, 0.f, beside);
 }
 
-// A sum of such terms, none above 1: hi and mid start at 1, so that the error
+// A sum of such terms, none above half of `start`: hi and mid start there, so that the error
 // of each addition to them is exact (the larger one comes first), and lo, which
-// is small, takes those and the c.
+// is small, takes those and the c.  What lo is rounded by is 2^-24 of it at each addition, always to the same side where terms are equal:
+// settle(), after a few terms, leaves it 2^-24 of hi, and a start far above the terms would leave errors as large as theirs.  (One token and
+// 151,935 equal ones of 2^-17 of it, in 8 parts: off by 2^-26 with a start of 1 and no settling, by 2^-34 with both, and a
+// border by 2^-36.6; settling every other time 2^-36.1, every fourth 2^-34.2.  64 draws take 41.8 us, 40.8 without either.)
 struct FineSum {
   float2 hi, mid, lo;
-  __device__ __forceinline__ void clear() {
-    hi = mid = both(1.f);
+  __device__ __forceinline__ void clear(float start) {
+    hi = mid = both(start);
     lo = both(0.f);
+  }
+  __device__ __forceinline__ void settle() {
+    float2 e;
+    hi = quick_two_sum2(hi, lo, e);
+    lo = e;
   }
   __device__ __forceinline__ void add(const Term2& p) {
     float2 e, f;
@@ -342,10 +350,10 @@ struct FineSum {
     mid = m;
     lo = add2(__ffma2_rn(times, p.c, lo), add2(e, f));
   }
-  __device__ __forceinline__ Wide value() const {
+  __device__ __forceinline__ Wide value(float start) const {
     float e, f;
-    const float s = two_sum(__fsub_rn(hi.x, 1.f), __fsub_rn(hi.y, 1.f), e);
-    const float t = two_sum(__fsub_rn(mid.x, 1.f), __fsub_rn(mid.y, 1.f), f);
+    const float s = two_sum(__fsub_rn(hi.x, start), __fsub_rn(hi.y, start), e);
+    const float t = two_sum(__fsub_rn(mid.x, start), __fsub_rn(mid.y, start), f);
     float r;
     const float h = two_sum(s, t, r);
     return Wide(h, __fadd_rn(__fadd_rn(r, __fadd_rn(e, f)), __fadd_rn(lo.x, lo.y)));

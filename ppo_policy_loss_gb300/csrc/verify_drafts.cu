@@ -123,6 +123,7 @@ struct Smem {
   uint2 powers[kPow];
   Exchange ex[2];
   Wide sums[kWarps];   // of the search
+  float top[kWarps];   // of the row, the warps' maxima
   float coarse[kWarps];
   float gap;
   long long found;
@@ -411,6 +412,7 @@ struct Weights {
   float c, nm;      // coarse: 2^(z c + nm)
   FineExp p, q;
   const uint2* powers;
+  float start;      // fine: a power of two, twice the weights or more
 
   __device__ __forceinline__ Term2 fine(float2 z) const { return p.template at<DT == RL_F32, false, kUnit>(z, powers); }
   __device__ __forceinline__ Term2 drafted(float2 z) const { return q.template at<DT == RL_F32, true, kUnit>(z, powers); }
@@ -468,6 +470,12 @@ struct Weights {
   }
 };
 
+// Where sums of a part's terms start: four times e^((top - m) / T) at most, as a power of two.
+__device__ __forceinline__ float fine_start(float top, const FineExp& p, float c) {
+  const float x = ceilf(((top - p.off) - p.m) * c) + 1.f;
+  return __int_as_float((127 + static_cast<int>(fminf(fmaxf(x, -60.f), 1.f))) << 23);
+}
+
 template <class N>
 __device__ __forceinline__ N warp_sum(N v) {
 #pragma unroll
@@ -481,7 +489,7 @@ __device__ __forceinline__ Wide part_sum(Weights<DT, MODE, true, kUnit>& f, long
   using F = Fmt<DT>;
   Wide total(0.f);
   FineSum s;
-  s.clear();
+  s.clear(f.start);
   int n = 0;
 #pragma unroll 1
   for (long long i = lo + lane * F::kVec; i < hi; i += 32 * F::kVec) {
@@ -490,13 +498,14 @@ __device__ __forceinline__ Wide part_sum(Weights<DT, MODE, true, kUnit>& f, long
     f.at(i, hi, w);
 #pragma unroll
     for (int j = 0; j < F::kVec / 2; ++j) s.add(w[j]);
+    s.settle();
     if (++n == 64) {
-      total += s.value();
-      s.clear();
+      total += s.value(f.start);
+      s.clear(f.start);
       n = 0;
     }
   }
-  return warp_sum(total + s.value());
+  return warp_sum(total + s.value(f.start));
 }
 // The same in fp32.
 template <int DT, int MODE, bool kUnit>
@@ -662,8 +671,8 @@ __device__ __forceinline__ void tell_sum(Weights<DT, MODE, true, kUnit>& f, long
 // The row's sum in fine arithmetic, in every thread of the cluster.  (Out of line, for one draft in 2^16 asks for it.  A draw
 // that falls back, one in twenty, has the sum in line: 64 draws take 41 us, 44 with a call.)
 template <int DT, bool kUnit>
-__device__ __noinline__ double row_sum(const unsigned char* row, long long lo, long long hi, FineExp p, Group& g, Smem& sm) {
-  Weights<DT, kSoftmax, true, kUnit> f{row, nullptr, -1, 0.f, 0.f, p, p, sm.powers};
+__device__ __noinline__ double row_sum(const unsigned char* row, long long lo, long long hi, FineExp p, float c, Group& g, Smem& sm) {
+  Weights<DT, kSoftmax, true, kUnit> f{row, nullptr, -1, c, 0.f, p, p, sm.powers, fine_start(sm.top[threadIdx.x >> 5], p, c)};
   tell_sum(f, lo, hi, g, sm);
   Wide total(0.f);
   for (int j = threadIdx.x & 31; j < g.size * kWarps; j += 32) total += sm.ex[g.turn].sum[j];
@@ -691,6 +700,7 @@ __device__ __forceinline__ long long draw_fine(Weights<DT, MODE, true, kUnit>& f
   if (at < 0) return kNowhere;
   if (at / kWarps != g.rank) return kElsewhere;
   const long long lo = min(V, at * size), hi = min(V, lo + size);
+  f.start = fine_start(sm.top[at % kWarps], f.p, f.c);
   search<DT, MODE, true, Wide>(f, lo, hi, want - before, sm);
   long long t = sm.found;
   if (MODE == kRest && t < 0) {  // p = q to the last digit kept in the whole part: its first token
@@ -786,6 +796,7 @@ verify_drafts_kernel(const Args a, int cluster) {
     while (true) {
       g.turn ^= 1;
       tell(g, &sm.ex[g.turn].stats[part], mine, lane);
+      if (lane == 0) sm.top[warp] = mine.m;
       g.sync();
       // maximum, then the parts' sums in its frame
       float m = -FLT_MAX;
@@ -849,7 +860,7 @@ verify_drafts_kernel(const Args a, int cluster) {
     int v = sm.verdict;
     if (v == kNear) {  // the same in every CTA
       Group h = g;
-      v = sm.left * row_sum<DT, kUnit>(row, lo, hi, fp, h, sm) < sm.right ? kStays : kRefused;
+      v = sm.left * row_sum<DT, kUnit>(row, lo, hi, fp, a.c, h, sm) < sm.right ? kStays : kRefused;
       g.turn = h.turn;
     }
     if (writes) {
@@ -870,7 +881,7 @@ verify_drafts_kernel(const Args a, int cluster) {
     const unsigned char* draft_row = a.draft ? a.draft + (b * G + kept) * a.draft_bytes : nullptr;
     if (lost && a.draft) {
       // S q_v = e^(z / T - lse_q + ln S)
-      Weights<DT, kRest, true, kUnit> f{row, draft_row, -1, 0.f, 0.f, fp, fp, sm.powers};
+      Weights<DT, kRest, true, kUnit> f{row, draft_row, -1, a.c, 0.f, fp, fp, sm.powers, fine_start(sm.top[warp], fp, a.c)};
       Wide total;
       total.h = two_sum(st.n, st.s, total.l);
       const float lq = a.draft_lse[b * G + kept];
@@ -884,8 +895,8 @@ verify_drafts_kernel(const Args a, int cluster) {
         // sums of p over all tokens, of p - q and of q over those with p > q, and of q over those with p next to q
         Wide all(0.f), plus(0.f);
         FineSum fa, fb;
-        fa.clear();
-        fb.clear();
+        fa.clear(f.start);
+        fb.clear(f.start);
         float2 qs = both(0.f), ns = both(0.f);
         int count = 0;
 #pragma unroll 1
@@ -906,16 +917,18 @@ verify_drafts_kernel(const Args a, int cluster) {
             qs = __ffma2_rn(more, q.a, qs);
             ns = __ffma2_rn(beside, q.a, ns);
           }
+          fa.settle();
+          fb.settle();
           if (++count == 64) {
-            all += fa.value();
-            plus += fb.value();
-            fa.clear();
-            fb.clear();
+            all += fa.value(f.start);
+            plus += fb.value(f.start);
+            fa.clear(f.start);
+            fb.clear(f.start);
             count = 0;
           }
         }
-        all = warp_sum(all + fa.value());
-        plus = warp_sum(plus + fb.value());
+        all = warp_sum(all + fa.value(f.start));
+        plus = warp_sum(plus + fb.value(f.start));
         const float drafted = warp_sum(qs.x + qs.y), next_to = warp_sum(ns.x + ns.y);
         bad = __any_sync(0xffffffffu, bad);
         g.turn ^= 1;
@@ -973,22 +986,22 @@ verify_drafts_kernel(const Args a, int cluster) {
         bool sure;
         long long t;
         if (without) {
-          Weights<DT, kWithout, false, kUnit> f{row, nullptr, d_out, a.c, nm, fp, fp, sm.powers};
+          Weights<DT, kWithout, false, kUnit> f{row, nullptr, d_out, a.c, nm, fp, fp, sm.powers, 1.f};
           t = draw_coarse(f, at, want - before, kCoarse * (st.n + st.s), V, size, g, sm, sure);
         } else {
-          Weights<DT, kSoftmax, false, kUnit> f{row, nullptr, -1, a.c, nm, fp, fp, sm.powers};
+          Weights<DT, kSoftmax, false, kUnit> f{row, nullptr, -1, a.c, nm, fp, fp, sm.powers, 1.f};
           t = draw_coarse(f, at, want - before, kCoarse * (st.n + st.s), V, size, g, sm, sure);
         }
         if (sure && t >= 0) token = g.rank == 0 ? t : kElsewhere;
       }
       if (token == kNowhere && without) {
-        Weights<DT, kWithout, true, kUnit> f{row, nullptr, d_out, 0.f, 0.f, fp, fp, sm.powers};
+        Weights<DT, kWithout, true, kUnit> f{row, nullptr, d_out, a.c, 0.f, fp, fp, sm.powers, fine_start(sm.top[warp], fp, a.c)};
         tell_sum(f, lo, hi, g, sm);
         token = draw_fine(f, sm.ex[g.turn].sum, V, size, g, sm);
       }
     }
     if (token == kNowhere && !bad) {
-      Weights<DT, kSoftmax, true, kUnit> f{row, nullptr, -1, 0.f, 0.f, fp, fp, sm.powers};
+      Weights<DT, kSoftmax, true, kUnit> f{row, nullptr, -1, a.c, 0.f, fp, fp, sm.powers, fine_start(sm.top[warp], fp, a.c)};
       tell_sum(f, lo, hi, g, sm);
       token = draw_fine(f, sm.ex[g.turn].sum, V, size, g, sm);
     }

@@ -35,13 +35,14 @@ def softmax(z, T=1.0):
 
 def check_draws(tokens, w, x):
     """The drawn tokens of weights w (of p's total of 1) with uniforms x: the border x W lies in the token's
-    interval, to the resolution of its ends, and the token has a weight."""
+    interval, to the resolution of its ends (include/rlrollout.h), and the token has a weight."""
+    resolution = max(RESOLUTION, w.size * 2.0 ** -52)
     edges = np.cumsum(w)
     at = x * edges[-1]
     assert (tokens >= 0).all()
     assert (w[tokens] > 0).all(), (tokens[w[tokens] <= 0][:4], w[tokens][w[tokens] <= 0][:4])
     off = np.maximum(edges[tokens] - w[tokens] - at, at - edges[tokens])
-    assert (off <= RESOLUTION).all(), (math.log2(off.max()), tokens[off > RESOLUTION][:4])
+    assert (off <= resolution).all(), (math.log2(off.max()), tokens[off > resolution][:4])
 
 
 # ------------------------------------------------------------------ max(p - q, 0)
@@ -330,6 +331,36 @@ def test_draws_of_rows_that_rise(dtype, V, rise):
     x = np.clip(edges[at] + 2.0 ** rng.uniform(-22, -16, n) * rng.choice([-1.0, 1.0], n), 0.0, 1 - 2.0 ** -53)
     out = torch_api.verify_drafts(rows(z, n), None, torch.from_numpy(x)[:, None].to(DEV))
     check_draws(out["tokens"][:, 0].cpu().numpy(), p, x)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("V,B,low", [(V, B, low) for V, B in ((60000, 400), (60000, 70), (151936, 400), (151936, 30)) for low in (-4.7, -9.3, -11.8, -13.1)] +
+                         [(1 << 21, 100, -14.1), (1 << 24, 3, -16.3)])
+@pytest.mark.parametrize("kind", ["none", "model"])
+def test_borders_of_rows_of_equal_numbers(dtype, V, B, low, kind):
+    """One token, and all others alike: every addition to the fine sums rounds to the same side.  Numbers 1.1 to 4
+    resolutions to either side of a border."""
+    z = torch.full((V,), low).to(TORCH[dtype])
+    z[V // 3] = 0.0
+    p, _ = softmax(f64(z))
+    w = p
+    if kind == "model":
+        y = torch.full((V,), low).to(TORCH[dtype])
+        y[V // 2] = max(low + math.log(V), 0.0)     # half of the draft's mass, or more
+        lq = np.float32(softmax(f64(y))[1])
+        w = np.maximum(p - np.exp(f64(y) - np.float64(lq)), 0.0)
+    edges, rng = np.cumsum(w), np.random.default_rng(B)
+    # (where the draft has more of every token than the target, all but one: nothing but that one token is drawn)
+    some = rng.choice(np.nonzero(w > min(64 * RESOLUTION, w.max()) / 2)[0], B)
+    x = np.clip((edges[some] + rng.uniform(1.1, 4.0, B) * rng.choice([-1.0, 1.0], B) * RESOLUTION) / edges[-1], 0, 1 - 2.0 ** -53)
+    if kind == "none":
+        out = torch_api.verify_drafts(rows(z, B), None, torch.from_numpy(x)[:, None].to(DEV))
+    else:
+        u = torch.from_numpy(np.stack([np.full(B, 1 - 2.0 ** -53), x], 1)).to(DEV)
+        out = torch_api.verify_drafts(rows(z, B, 2), torch.full((B, 1), V // 2, device=DEV), u, draft_logits=rows(y, B),
+                                      draft_lse=torch.full((B, 1), float(lq), device=DEV))
+        assert (out["n_accepted"] == 0).all()
+    check_draws(out["tokens"][:, 0].cpu().numpy(), w, x)
 
 
 # ------------------------------------------------------------------ clusters of every size
