@@ -97,7 +97,7 @@ size_t rl_lmhead_int8_workspace_size(long long R, long long D);
  *       uniforms[b, i] q_i(d) < p_i(d),        d = draft_ids[b, i]
  *   a = the number that stay
  *   one more token is drawn, from p_n if a = n, else from
- *       max(p_a - q_a, 0) (from p_a where that is 0 everywhere):
+ *       max(p_a - q_a, 0) (from p_a where that is 0 everywhere, to 2^-38 of what q_a has where they are equal):
  *       the first token at which the sum of weights in token order exceeds
  *       uniforms[b, G] times their total
  *   tokens[b]     = the a drafts that stay, the drawn token, then -1

@@ -681,11 +681,11 @@ __device__ __noinline__ double row_sum(const unsigned char* row, long long lo, l
 }
 
 // The token, in the CTA that has it; kElsewhere in the others, which have nothing left to do;
-// kNowhere in all where no part has any weight.
+// kNowhere in all where the parts' weights are `nothing`.
 constexpr long long kElsewhere = -2, kNowhere = -3;
 template <int DT, int MODE, bool kUnit>
 __device__ __forceinline__ long long draw_fine(Weights<DT, MODE, true, kUnit>& f, const Wide* sums, long long V, long long size, const Group& g,
-                                               Smem& sm) {
+                                               Smem& sm, float nothing = kNothing) {
   const int lane = threadIdx.x & 31, parts = g.size * kWarps;
   constexpr float none = MODE != kRest ? kNothing : 0.f;
   Wide v[kMaxParts / 32], own(0.f), before;
@@ -696,7 +696,7 @@ __device__ __forceinline__ long long draw_fine(Weights<DT, MODE, true, kUnit>& f
     own += v[j];
   }
   const Wide total = warp_sum(own), want = sm.u * total;
-  const int at = total.h > none ? find_part(v, want, none, before, lane) : -1;  // the same in every CTA
+  const int at = total.h > nothing ? find_part(v, want, none, before, lane) : -1;  // the same in every CTA
   if (at < 0) return kNowhere;
   if (at / kWarps != g.rank) return kElsewhere;
   const long long lo = min(V, at * size), hi = min(V, lo + size);
@@ -885,6 +885,7 @@ verify_drafts_kernel(const Args a, int cluster) {
       Wide total;
       total.h = two_sum(st.n, st.s, total.l);
       const float lq = a.draft_lse[b * G + kept];
+      float close = 0.f;
       bool sure = false;
 #pragma unroll 1
       for (int pass = 0;; ++pass) {
@@ -938,7 +939,7 @@ verify_drafts_kernel(const Args a, int cluster) {
         tell(g, &ex.stats[part], Stats{next_to, 0.f, drafted}, lane);
         g.sync();
         total = Wide(0.f);
-        float close = 0.f;
+        close = 0.f;
         bad = false;
         for (int j = lane; j < parts; j += 32) {
           bad = bad || ex.sum[j].h < 0.f;
@@ -964,8 +965,8 @@ verify_drafts_kernel(const Args a, int cluster) {
         }
         __syncthreads();
       }
-      if (!bad) {
-        token = draw_fine(f, sm.ex[g.turn].plus, V, size, g, sm);
+      if (!bad) {  // (terms are good to 2^-39: of tokens with p next to q nothing below that is known to be left)
+        token = draw_fine(f, sm.ex[g.turn].plus, V, size, g, sm, 0x1p-38f * close);
       }
     } else {
       // the parts' sums of step 1 in the frame of the row, without the draft that was looked up

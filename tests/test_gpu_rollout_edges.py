@@ -172,6 +172,27 @@ def test_refused_drafts_of_rows_of_large_numbers(dtype, at, temperature, B):
         check_draws(out["tokens"][:, 0].cpu().numpy(), w, x)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("temperature", [1.0, 0.7, 0.1])
+@pytest.mark.parametrize("top", [64.0, 64.1234567, 70.0001])
+@pytest.mark.parametrize("B", BATCHES)
+def test_draft_with_nothing_but_roundings_below_the_target(dtype, temperature, top, B):
+    """One token has all but e^-60; the draft's row is the target's but for the refused token, of which it has more: p is
+    nowhere above q, but equal to it in every digit, and the token is drawn from p."""
+    V, T = 33000, temperature
+    z = (make_logits((1,), V, dtype, 51, sure=False)[0].float() * T).clamp(max=10.0 * T).to(TORCH[dtype])
+    z[V // 5] = top * T
+    y = z.clone()
+    y[17] += 0.5 * T
+    lq = f64(z)[V // 5] / T
+    if float(np.float32(lq)) != lq:
+        lq = np.nextafter(np.float32(lq), np.float32(-np.inf)) if float(np.float32(lq)) > lq else np.float32(lq)   # q > p everywhere
+    u = torch.from_numpy(np.stack([np.full(B, 0.99), np.random.default_rng(B).random(B)], 1)).to(DEV)
+    out = torch_api.verify_drafts(rows(z, B, 2), torch.full((B, 1), 17, device=DEV), u, draft_logits=rows(y, B),
+                                  draft_lse=torch.full((B, 1), float(lq), device=DEV), temperature=T)
+    assert (out["n_accepted"] == 0).all() and (out["tokens"][:, 0] == V // 5).all()
+
+
 # ------------------------------------------------------------------ numbers that are none
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("value", [math.nan, math.inf])
