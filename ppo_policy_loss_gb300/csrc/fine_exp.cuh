@@ -13,6 +13,8 @@
 //   e^g - 1 = gh + v,  v = gl + g^2 / 2 + g^3 / 6 with g = gh + gl, |g| <= ln 2 / 512 (what is left out
 //   of the series is below 2^-42);
 //   a = T_j 2^n,   b = a gh rounded,   c = its error + a v.
+// (The table-driven exponential of P. T. P. Tang, ACM TOMS 15, 1989, with a constant split as W. J. Cody and W. Waite
+// do, and the error-free sums of T. J. Dekker and D. E. Knuth; the table and the constants follow from these lines.)
 // Everything is done for two numbers at a time (the packed fp32 instructions, an issue slot for
 // two operations): 16 packed operations a pair with T = 1, 20 otherwise.  With 256 powers b is so small
 // that a difference of two b may be rounded.

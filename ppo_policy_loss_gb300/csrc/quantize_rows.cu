@@ -2,8 +2,10 @@
 // a scale for each (include/rlrollout.h).
 //
 // One pass over the data: a row stays in its threads' registers between the
-// maximum and the rounding (rows of more than kMaxThreads * kVecs vectors are read
-// a second time, from L2).  Bound by HBM: an element is 2 or 4 bytes in and 1 out.
+// maximum and the rounding.  Bound by HBM: an element is 2 or 4 bytes in and 1 out.  Rows of more than
+// kMaxThreads * kVecs vectors are read a second time, mostly from HBM again: 1.5 GB of bf16 rows of 16,384 take
+// 430 us (5.2 TB/s of in and out), of 16,640 611 us (3.7), of 262,144 693 us; of fp32 rows of 8,192 346 us (5.4), of
+// 16,384 435 us (4.3), of 262,144 640 us.
 //
 // The codes are those of the exact quotient x / s.  The candidate k, the low byte of
 // x (1 / s) + 1.5 2^23, is within one of it, and e = x - k s is exact in one FMA

@@ -22,10 +22,12 @@
 //     have of q is summed too, and where it counts (a draft's row that nearly equals the target's) the pass is made again with the
 //     new S.
 //
-// What bounds it.  One row of 151,936 bf16 logits takes 9.3 us: launch, one pass (2 us) and a
-// chain of short steps.  Few sequences are such chains of rows (64 with four drafts each: 66 us).  Many are bound by
-// instructions and their latency where drafts are refused, 64 packed operations for two tokens of both rows (512 with four drafts:
-// 322 us, all kept 260), else by HBM and the last round of sequences (512 draws: 67 us, 2.3 TB/s; 122 where some fall back).
+// What bounds it.  One row of 151,936 bf16 logits takes 9.6 us: launch, one pass (2 us) and a
+// chain of short steps; 21 where it falls back to fine sums.  Few sequences are such chains of rows (64 with four drafts each: 73 us,
+// 71 where all stay).  Many are bound by instructions and their latency where drafts are refused, 66 packed operations for two
+// tokens of both rows (512 with four drafts: 328 us, all kept 265).  Draws are bound by waiting: one CTA of a cluster searches
+// while the others stand at its barrier, the last round of clusters is nearly empty (512: 67 us, 2.3 TB/s), and where a row
+// falls back its few CTAs sum it again while the rest of the chip has nothing to do (512: 116 us; 64: 42, 20 where none does).
 //
 // fp32 sums, in units of 2^-24: a term 2^x carries 4 of the hardware exponential and 2 ln 2 |x|
 // of its argument (the FMA's rounding and c's), |x| weighted by p at most log2 V <= 26;
@@ -116,7 +118,7 @@ struct Exchange {
   int unsure;
 };
 // Of a warp's ring: one chunk on its way while one is read.  What shared memory leaves is L1, which the
-// passes behind the first read through (64 x 151,936, four drafts: 69.1 us with 4 slots, 68.4 with 3, 66.2 with 2).
+// passes behind the first read through (64 x 151,936, four drafts: with 4 slots 4% longer, with 3 3%).
 constexpr int kSlots = 2, kChunkBytes = 2048;
 struct Smem {
   unsigned long long full[kWarps][kSlots];
@@ -903,7 +905,7 @@ verify_drafts_kernel(const Args a, int cluster) {
 #pragma unroll 1
         for (long long i = lo + lane * F::kVec; i < hi; i += 32 * F::kVec) {
           float z[F::kVec], y[F::kVec];
-          fetch<DT>(row, i, hi);  // (512 sequences: 324 us, 336 without)
+          fetch<DT>(row, i, hi);  // (512 sequences take 4% longer without)
           fetch<DT>(draft_row, i, hi);
           F::unpack(load_vec<DT>(row, i, hi), z);
           F::unpack(load_vec<DT>(draft_row, i, hi), y);
@@ -1029,17 +1031,19 @@ verify_drafts_kernel(const Args a, int cluster) {
 
 // CTAs of a cluster, no more than leave a warp 256 elements.  Few sequences take the largest
 // clusters of which all are at work at once; 5 and 10 of them fill the chip's parts best (435 and 430 of 456
-// places; 8: 408, 16: 336).  us, V = 151,936, four drafts / a draw:
-//   B = 4    16: 27 / 14    10: 26 / 14    8: 32 / 15
-//   B = 40   10: 52 / 29     7: 53 / 33    5: 65 / 36    4: 76 / 49
-//   B = 64    7: 83 / 39     5: 72 / 42    4: 76 / 51    2: 105 / 68
-//   B = 130   5: 128 / 56    4: 130 / 57   2: 139 / 81   1: 199 / 74
-//   B = 300   5: 245 / 90    4: 237 / 88   2: 243 / 97   1: 259 / 104
-//   B = 512   4: 360 / 129   2: 338 / 125  1: 361 / 129
-// Of short rows a cluster's barriers are a larger share; V = 32,000:
-//   B = 100   5: 54 / 30     4: 38 / 23    2: 43 / 27
-//   B = 200                  4: 64 / 34    2: 61 / 35    1: 65 / 34
-//   B = 400                  4: 122 / 58   2: 97 / 48    1: 84 / 35
+// places; 8: 408, 16: 336).  us, V = 151,936, four drafts / a draw (2% less than with settled fine sums):
+//   B = 4    16: 30 / 16    10: 31 / 17    8: 37 / 19
+//   B = 40   10: 53 / 28     8: 60 / 32    5: 64 / 36    4: 69 / 41
+//   B = 64    8: 86 / 39     5: 77 / 39    4: 77 / 45    2: 102 / 64
+//   B = 130   5: 123 / 52    4: 124 / 55   2: 133 / 70   1: 179 / 72
+//   B = 300   5: 229 / 82    4: 221 / 81   2: 228 / 92   1: 236 / 87
+//   B = 512   4: 346 / 117   2: 327 / 117  1: 365 / 124
+// Of short rows a cluster's barriers are a larger share.  What counts is their number of elements, not of bytes:
+//   V = 32,000 bf16            V = 50,257 bf16               V = 50,257 fp32               V = 66,000 bf16
+//   4: 41 / 25   2: 46 / 31    4: 51 / 31    2: 64 / 40      4: 58 / 31    2: 70 / 40      4: 64 / 38    2: 76 / 45      B = 100
+//   2: 56 / 34   1: 66 / 29    2: 75 / 44    1: 92 / 39      2: 84 / 48    1: 114 / 44     4: 106 / 47   2: 95 / 48      B = 200
+//   2: 88 / 45   1: 83 / 33    2: 128 / 58   1: 119 / 43     2: 146 / 63   1: 141 / 51     2: 153 / 67   1: 150 / 56     B = 400
+// (At 66,000 and 100,000 elements 200 sequences with four drafts would be 4 to 10% faster by 2 CTAs, and 400 draws by one.)
 constexpr long long kShortRow = 1 << 16;
 int cluster_for(long long B, long long V, int sms) {
   const long long slots = static_cast<long long>(sms) * kCtasPerSm, most = (V + 256 * kWarps - 1) / (256 * kWarps);
